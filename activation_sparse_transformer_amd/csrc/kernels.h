@@ -263,10 +263,15 @@ bool bwd_supported(const Geometry& g, int elem_bytes);
 int64_t bwd_max_entries(const Geometry& g, int64_t dense_cap);
 // Parts of a workspace at `ws` (nullptr: sizes only, in .bytes).
 BwdWorkspace bwd_carve(const Geometry& g, int elem_bytes, int64_t dense_cap, void* ws);
+// x as rows of the storage type, or (x8 given, x unused) as an 8-bit checkpoint.
+struct BwdAct8 {
+  const int8_t* codes;
+  const float* scales;
+};
 hipError_t launch_backward(const Geometry& g, int elem_bytes, const BwdHybrid& hy, const void* x,
-                           const void* w_up_t, const void* w_down, const void* dy,
-                           const BwdWorkspace& w, void* dx, float* dw_up_t, float* db,
-                           float* dw_down, hipStream_t s);
+                           const BwdAct8* x8, const void* w_up_t, const void* w_down,
+                           const void* dy, const BwdWorkspace& w, void* dx, float* dw_up_t,
+                           float* db, float* dw_down, hipStream_t s);
 
 // The ReLU-gated FFN's up branch on a packed and routed gate: each stored
 // non-zero g (TwELL slots of the sparse rows sparse_rows[0 .. *n_sparse),
@@ -287,5 +292,15 @@ struct GateHybrid {
 bool gate_supported(const Geometry& g, int elem_bytes);
 hipError_t launch_gate_up(const Geometry& g, int elem_bytes, const GateHybrid& hy, const void* x,
                           const void* w_up_t, const float* b_up, hipStream_t s);
+
+// 8-bit activation checkpoints: int8 codes [n_rows][act8_pitch(d)] and one
+// float32 scale per row and block of kAct8Block columns.
+constexpr int kAct8Block = 128;
+inline int act8_blocks(int d) { return (d + kAct8Block - 1) / kAct8Block; }
+inline int act8_pitch(int d) { return (d + 15) / 16 * 16; }
+hipError_t launch_act8_pack(int64_t n_rows, int d, int elem_bytes, const void* x, int8_t* codes,
+                            float* scales, hipStream_t s);
+hipError_t launch_act8_unpack(int64_t n_rows, int d, int elem_bytes, const int8_t* codes,
+                              const float* scales, void* x, hipStream_t s);
 
 }  // namespace twell

@@ -570,10 +570,14 @@ TWELL_EXPORT size_t ffn_sparse_backward_workspace_size(const twell_shape* shape,
   return bwd_carve(geometry(shape), elem_bytes(shape->dtype), dense_capacity, nullptr).bytes;
 }
 
-TWELL_EXPORT int ffn_sparse_backward(const twell_shape* shape, const void* x, const void* w_up_t,
-                                     const void* w_down, const twell_hybrid* h, const void* dy,
-                                     void* dx, float* dw_up_t, float* db_up, float* dw_down,
-                                     void* workspace, size_t workspace_bytes, void* stream) {
+namespace twell {
+namespace {
+
+// ffn_sparse_backward with x as rows (x8 null) or as an 8-bit checkpoint.
+int backward_impl(const twell_shape* shape, const void* x, const twell_act8* x8,
+                  const void* w_up_t, const void* w_down, const twell_hybrid* h, const void* dy,
+                  void* dx, float* dw_up_t, float* db_up, float* dw_down, void* workspace,
+                  size_t workspace_bytes, void* stream) {
   int rc = check_shape(shape, true);
   if (rc != TWELL_OK) return rc;
   const Geometry g = geometry(shape);
@@ -581,18 +585,85 @@ TWELL_EXPORT int ffn_sparse_backward(const twell_shape* shape, const void* x, co
   if ((rc = check_backward_shape(shape, h->dense_capacity)) != TWELL_OK) return rc;
   if (dw_up_t == nullptr || db_up == nullptr || dw_down == nullptr || workspace == nullptr)
     return TWELL_ERR_INVALID_ARG;
+  const bool have_x = x8 == nullptr ? x != nullptr : x8->codes != nullptr && x8->scales != nullptr;
   if (g.n_rows > 0 &&
-      (x == nullptr || w_up_t == nullptr || w_down == nullptr || dy == nullptr || dx == nullptr))
+      (!have_x || w_up_t == nullptr || w_down == nullptr || dy == nullptr || dx == nullptr))
     return TWELL_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_up_t) || !aligned16(w_down) || !aligned16(dy) ||
       !aligned16(dx) || !aligned16(dw_up_t) || !aligned16(db_up) || !aligned16(dw_down) ||
       !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  if (x8 != nullptr && (!aligned16(x8->codes) || !aligned16(x8->scales)))
     return TWELL_ERR_INVALID_ARG;
   const int eb = elem_bytes(shape->dtype);
   const BwdWorkspace w = bwd_carve(g, eb, h->dense_capacity, workspace);
   if (workspace_bytes < w.bytes) return TWELL_ERR_WORKSPACE;
   const BwdHybrid hy{h->values,       h->indices, h->counts,         h->dense_rows,
                      h->dense_values, h->n_dense, h->dense_capacity};
-  return hip_status(launch_backward(g, eb, hy, x, w_up_t, w_down, dy, w, dx, dw_up_t, db_up,
-                                    dw_down, static_cast<hipStream_t>(stream)));
+  const BwdAct8 a8{x8 == nullptr ? nullptr : x8->codes, x8 == nullptr ? nullptr : x8->scales};
+  return hip_status(launch_backward(g, eb, hy, x, x8 == nullptr ? nullptr : &a8, w_up_t, w_down,
+                                    dy, w, dx, dw_up_t, db_up, dw_down,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT int ffn_sparse_backward(const twell_shape* shape, const void* x, const void* w_up_t,
+                                     const void* w_down, const twell_hybrid* h, const void* dy,
+                                     void* dx, float* dw_up_t, float* db_up, float* dw_down,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return backward_impl(shape, x, nullptr, w_up_t, w_down, h, dy, dx, dw_up_t, db_up, dw_down,
+                       workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ 8-bit checkpoints
+namespace twell {
+namespace {
+
+int check_act8(int64_t n_rows, int32_t d_model, int32_t dtype, const void* x,
+               const twell_act8* a) {
+  if (n_rows < 0 || n_rows > INT32_MAX || d_model <= 0 || d_model % 8 != 0 || a == nullptr)
+    return TWELL_ERR_INVALID_ARG;
+  if (dtype != TWELL_F32 && dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (n_rows > 0 && (x == nullptr || a->codes == nullptr || a->scales == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(a->codes) || !aligned16(a->scales)) return TWELL_ERR_INVALID_ARG;
+  // a launch holds fewer than 2^32 lanes, 16 columns each
+  if (n_rows * act8_blocks(d_model) >= (int64_t{1} << 29)) return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT int twell_act8_pack(int64_t n_rows, int32_t d_model, int32_t dtype, const void* x,
+                                 const twell_act8* out, void* stream) {
+  const int rc = check_act8(n_rows, d_model, dtype, x, out);
+  if (rc != TWELL_OK) return rc;
+  return hip_status(launch_act8_pack(n_rows, d_model, elem_bytes(dtype), x, out->codes,
+                                     out->scales, static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT int twell_act8_unpack(int64_t n_rows, int32_t d_model, int32_t dtype,
+                                   const twell_act8* in, void* x, void* stream) {
+  const int rc = check_act8(n_rows, d_model, dtype, x, in);
+  if (rc != TWELL_OK) return rc;
+  return hip_status(launch_act8_unpack(n_rows, d_model, elem_bytes(dtype), in->codes, in->scales,
+                                       x, static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape,
+                                                            int64_t dense_capacity) {
+  return ffn_sparse_backward_workspace_size(shape, dense_capacity);
+}
+
+TWELL_EXPORT int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8,
+                                          const void* w_up_t, const void* w_down,
+                                          const twell_hybrid* h, const void* dy, void* dx,
+                                          float* dw_up_t, float* db_up, float* dw_down,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (x8 == nullptr) return TWELL_ERR_INVALID_ARG;
+  return backward_impl(shape, nullptr, x8, w_up_t, w_down, h, dy, dx, dw_up_t, db_up, dw_down,
+                       workspace, workspace_bytes, stream);
 }

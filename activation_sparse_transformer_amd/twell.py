@@ -34,6 +34,8 @@ EXPORTS = (
     "twell_unpack", "twell_spmm", "twell_spmm_workspace_size", "ell_pack_workspace_size",
     "ell_pack", "ell_unpack", "ell_spmm",
     "ffn_sparse_backward_workspace_size", "ffn_sparse_backward", "ffn_sparse_gated_forward",
+    "twell_act8_pack", "twell_act8_unpack", "ffn_sparse_backward_act8_workspace_size",
+    "ffn_sparse_backward_act8",
 )
 
 
@@ -65,6 +67,10 @@ class EllStruct(ctypes.Structure):
         ("dense_rows", ctypes.c_void_p), ("dense_values", ctypes.c_void_p),
         ("n_dense", ctypes.c_void_p), ("dense_capacity", ctypes.c_int64),
     ]
+
+
+class Act8Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -107,6 +113,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ffn_sparse_backward_workspace_size.restype = sz
     lib.ffn_sparse_backward.argtypes = [S, P, P, P, H, P, P, P, P, P, P, sz, P]
     lib.ffn_sparse_backward.restype = I
+    A, i32 = ctypes.POINTER(Act8Struct), ctypes.c_int32
+    lib.twell_act8_pack.argtypes, lib.twell_act8_pack.restype = [i64, i32, i32, P, A, P], I
+    lib.twell_act8_unpack.argtypes, lib.twell_act8_unpack.restype = [i64, i32, i32, A, P, P], I
+    lib.ffn_sparse_backward_act8_workspace_size.argtypes = [S, i64]
+    lib.ffn_sparse_backward_act8_workspace_size.restype = sz
+    lib.ffn_sparse_backward_act8.argtypes = [S, A, P, P, H, P, P, P, P, P, P, sz, P]
+    lib.ffn_sparse_backward_act8.restype = I
     _lib = lib
     return lib
 
@@ -552,6 +565,21 @@ class Grads:
     dw_down: torch.Tensor  # [d_ff, d_model] float32
 
 
+def _grads(out: Optional[Grads], hy: Hybrid, dm: int, dev) -> Grads:
+    """`out` checked, or new gradient tensors of the layer."""
+    n, dt = hy.n_rows, hy.dtype
+    if out is None:
+        out = Grads(torch.empty((n, dm), dtype=dt, device=dev),
+                    torch.empty((hy.d_ff, dm), dtype=torch.float32, device=dev),
+                    torch.empty((hy.d_ff,), dtype=torch.float32, device=dev),
+                    torch.empty((hy.d_ff, dm), dtype=torch.float32, device=dev))
+    _need(out.dx, "dx", dev, dt, (n, dm))
+    _need(out.dw_up_t, "dw_up_t", dev, torch.float32, (hy.d_ff, dm))
+    _need(out.db_up, "db_up", dev, torch.float32, (hy.d_ff,))
+    _need(out.dw_down, "dw_down", dev, torch.float32, (hy.d_ff, dm))
+    return out
+
+
 def ffn_sparse_backward(x: torch.Tensor, w_up_t: torch.Tensor, w_down: torch.Tensor,
                         hy: Hybrid, dy: torch.Tensor, *, out: Optional[Grads] = None,
                         workspace: Optional[torch.Tensor] = None) -> Grads:
@@ -569,15 +597,7 @@ def ffn_sparse_backward(x: torch.Tensor, w_up_t: torch.Tensor, w_down: torch.Ten
     _need(w_up_t, "w_up_t", dev, dt, (hy.d_ff, dm))
     _need(w_down, "w_down", dev, dt, (hy.d_ff, dm))
     shape = make_shape(n, dm, hy.d_ff, hy.tile, hy.capacity, dt)
-    if out is None:
-        out = Grads(torch.empty((n, dm), dtype=dt, device=dev),
-                    torch.empty((hy.d_ff, dm), dtype=torch.float32, device=dev),
-                    torch.empty((hy.d_ff,), dtype=torch.float32, device=dev),
-                    torch.empty((hy.d_ff, dm), dtype=torch.float32, device=dev))
-    _need(out.dx, "dx", dev, dt, (n, dm))
-    _need(out.dw_up_t, "dw_up_t", dev, torch.float32, (hy.d_ff, dm))
-    _need(out.db_up, "db_up", dev, torch.float32, (hy.d_ff,))
-    _need(out.dw_down, "dw_down", dev, torch.float32, (hy.d_ff, dm))
+    out = _grads(out, hy, dm, dev)
     if workspace is None:
         ws = backward_workspace_bytes(shape, hy.dense_capacity)
         if ws == 0:
@@ -591,3 +611,107 @@ def ffn_sparse_backward(x: torch.Tensor, w_up_t: torch.Tensor, w_down: torch.Ten
     _check(code, "ffn_sparse_backward")
     return out
 
+
+# ------------------------------------------------------------------ 8-bit checkpoints
+ACT8_BLOCK = 128  # TWELL_ACT8_BLOCK
+
+
+@dataclasses.dataclass
+class Act8:
+    """An 8-bit activation checkpoint of x [N, d_model] (see twell_act8 in twell.h)."""
+
+    d_model: int
+    dtype: torch.dtype    # of x
+    codes: torch.Tensor   # [N, d_model rounded up to 16] int8
+    scales: torch.Tensor  # [N, ceil(d_model / 128)] float32
+
+    @property
+    def n_rows(self) -> int:
+        return self.codes.shape[0]
+
+    @classmethod
+    def empty(cls, n_rows: int, d_model: int, dtype: torch.dtype, device) -> "Act8":
+        return cls(d_model, dtype,
+                   torch.empty((n_rows, -(-d_model // 16) * 16), dtype=torch.int8, device=device),
+                   torch.empty((n_rows, -(-d_model // ACT8_BLOCK)), dtype=torch.float32,
+                               device=device))
+
+    def struct(self) -> Act8Struct:
+        return Act8Struct(_ptr(self.codes), _ptr(self.scales))
+
+    def validate(self, device) -> None:
+        if self.dtype not in _DTYPE_CODE:
+            raise ValueError(f"dtype {self.dtype} is not supported (float32 or bfloat16)")
+        n, d = self.n_rows, self.d_model
+        _need(self.codes, "codes", device, torch.int8, (n, -(-d // 16) * 16))
+        _need(self.scales, "scales", device, torch.float32, (n, -(-d // ACT8_BLOCK)))
+
+
+def twell_act8_pack(x: torch.Tensor, *, out: Optional[Act8] = None) -> Act8:
+    """The 8-bit checkpoint of x [N, d_model]: int8 codes, one scale per row and
+    128 columns."""
+    dev = x.device
+    n, d = x.shape
+    _need(x, "x", dev)
+    if x.dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {x.dtype} is not supported (float32 or bfloat16)")
+    if out is None:
+        out = Act8.empty(n, d, x.dtype, dev)
+    if (out.n_rows, out.d_model, out.dtype) != (n, d, x.dtype):
+        raise ValueError(f"out holds {(out.n_rows, out.d_model)} {out.dtype}, x is {(n, d)} {x.dtype}")
+    out.validate(dev)
+    a = out.struct()
+    _check(load().twell_act8_pack(n, d, _DTYPE_CODE[x.dtype], _ptr(x), ctypes.byref(a),
+                                  _stream(dev)), "twell_act8_pack")
+    return out
+
+
+def twell_act8_unpack(a: Act8, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [N, d_model] of an 8-bit checkpoint, in the checkpoint's dtype."""
+    dev = a.codes.device
+    a.validate(dev)
+    if out is None:
+        out = torch.empty((a.n_rows, a.d_model), dtype=a.dtype, device=dev)
+    _need(out, "x", dev, a.dtype, (a.n_rows, a.d_model))
+    st = a.struct()
+    _check(load().twell_act8_unpack(a.n_rows, a.d_model, _DTYPE_CODE[a.dtype], ctypes.byref(st),
+                                    _ptr(out), _stream(dev)), "twell_act8_unpack")
+    return out
+
+
+def backward_act8_workspace(hy: Hybrid, d_model: int) -> torch.Tensor:
+    """A workspace for ffn_sparse_backward_act8 on this hybrid."""
+    shape = make_shape(hy.n_rows, d_model, hy.d_ff, hy.tile, hy.capacity, hy.dtype)
+    ws = int(load().ffn_sparse_backward_act8_workspace_size(ctypes.byref(shape),
+                                                           hy.dense_capacity))
+    if ws == 0:
+        raise TwellError(TWELL_ERR_UNSUPPORTED, "ffn_sparse_backward_act8_workspace_size")
+    return torch.empty((ws,), dtype=torch.uint8, device=hy.values.device)
+
+
+def ffn_sparse_backward_act8(x8: Act8, w_up_t: torch.Tensor, w_down: torch.Tensor, hy: Hybrid,
+                             dy: torch.Tensor, *, out: Optional[Grads] = None,
+                             workspace: Optional[torch.Tensor] = None) -> Grads:
+    """ffn_sparse_backward with the layer's input x as an 8-bit checkpoint."""
+    dev = dy.device
+    n, dm = dy.shape
+    dt = hy.dtype
+    hy.validate(dev)
+    x8.validate(dev)
+    if (x8.n_rows, x8.d_model, x8.dtype) != (n, dm, dt):
+        raise ValueError(f"x8 holds {(x8.n_rows, x8.d_model)} {x8.dtype}, the layer is "
+                         f"{(n, dm)} {dt}")
+    _need(dy, "dy", dev, dt, (hy.n_rows, dm))
+    _need(w_up_t, "w_up_t", dev, dt, (hy.d_ff, dm))
+    _need(w_down, "w_down", dev, dt, (hy.d_ff, dm))
+    shape = make_shape(n, dm, hy.d_ff, hy.tile, hy.capacity, dt)
+    out = _grads(out, hy, dm, dev)
+    if workspace is None:
+        workspace = backward_act8_workspace(hy, dm)
+    _need(workspace, "workspace", dev, torch.uint8)
+    hs, a = hy.struct(), x8.struct()
+    _check(load().ffn_sparse_backward_act8(
+        ctypes.byref(shape), ctypes.byref(a), _ptr(w_up_t), _ptr(w_down), ctypes.byref(hs),
+        _ptr(dy), _ptr(out.dx), _ptr(out.dw_up_t), _ptr(out.db_up), _ptr(out.dw_down),
+        _ptr(workspace), workspace.numel(), _stream(dev)), "ffn_sparse_backward_act8")
+    return out

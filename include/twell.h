@@ -406,6 +406,53 @@ int ffn_sparse_backward(const twell_shape* shape, const void* x, const void* w_u
                         float* dw_up_t, float* db_up, float* dw_down, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* ---- 8-bit activation checkpoints.  "Nvidia and Sakana make LLMs 30% faster
+ * by doing less math", section "More speed, less power, zero quality loss",
+ * reports lower peak memory in training; between its passes a training step
+ * holds every layer's input x and hidden activations h.  The hybrid h is
+ * sparse already; these calls keep x at half (bf16) or a quarter (float32) of
+ * its bytes and let the backward read it in that form.  Defined by this
+ * interface:
+ *  - x [n_rows][d_model] is split into blocks of TWELL_ACT8_BLOCK columns of
+ *    one row (the last may be shorter).  With a the block's largest
+ *    magnitude: scale = a / 127, code = x * 127 / a rounded to the nearest
+ *    integer, ties to even (both in float32); x reads back as code * scale.
+ *    (Where 127 * scale would round past the largest float, scale is the next
+ *    float below: a finite x reads back finite.)
+ *  - A block of zeros has scale 0.  A block holding a NaN or an infinity has
+ *    scale NaN and codes 0: it reads back as NaN throughout.
+ *  - codes  [n_rows][P] int8, P = d_model rounded up to 16; codes past
+ *    d_model are 0.  scales [n_rows][ceil(d_model / TWELL_ACT8_BLOCK)]. */
+#define TWELL_ACT8_BLOCK 128
+typedef struct twell_act8 {
+  int8_t* codes;
+  float* scales;
+} twell_act8;
+
+/* Write the 8-bit form of x [n_rows][d_model] (dtype: a twell_dtype; d_model a
+ * multiple of 8; n_rows * blocks per row below 2^29, else
+ * TWELL_ERR_UNSUPPORTED). */
+int twell_act8_pack(int64_t n_rows, int32_t d_model, int32_t dtype, const void* x,
+                    const twell_act8* out, void* stream);
+
+/* x [n_rows][d_model] = code * scale, rounded to dtype.  Same limits. */
+int twell_act8_unpack(int64_t n_rows, int32_t d_model, int32_t dtype, const twell_act8* in,
+                      void* x, void* stream);
+
+/* Bytes of device workspace ffn_sparse_backward_act8 needs (0 as for
+ * ffn_sparse_backward_workspace_size). */
+size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape, int64_t dense_capacity);
+
+/* ffn_sparse_backward with the layer's input given as an 8-bit checkpoint.
+ * dw_up_t = dz^T (code * scale) with code * scale taken in float32, and with
+ * dz in float32 for dw_up_t and db_up (dx reads dz rounded to the storage
+ * type, as in ffn_sparse_backward).  Everything else, the limits and the
+ * errors included, is as in ffn_sparse_backward. */
+int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, const void* w_up_t,
+                             const void* w_down, const twell_hybrid* h, const void* dy, void* dx,
+                             float* dw_up_t, float* db_up, float* dw_down, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,28 @@
+"""CPU oracle of the operators around the layer in a training step: 8-bit
+activation checkpoints.  NumPy in float64, from the definitions."""
+from __future__ import annotations
+
+import numpy as np
+
+ACT8_BLOCK = 128
+
+
+def act8_quotients(x: np.ndarray):
+    """x * 127 / a per element in float64, and a [N, blocks]: a is the largest
+    magnitude of the row's block of columns (a zero block's quotients are 0)."""
+    n, d = x.shape
+    nb = -(-d // ACT8_BLOCK)
+    q = np.zeros((n, d))
+    a = np.zeros((n, nb))
+    for b in range(nb):
+        cols = slice(b * ACT8_BLOCK, min(d, (b + 1) * ACT8_BLOCK))
+        top = np.abs(x[:, cols]).max(axis=1) if n else np.zeros(0)
+        a[:, b] = top
+        q[:, cols] = x[:, cols] * 127.0 / np.where(top > 0, top, 1.0)[:, None]
+    return q, a
+
+
+def act8_decode(codes: np.ndarray, scales: np.ndarray, d: int) -> np.ndarray:
+    """code * scale in float64 for codes [N, >= d], scales [N, blocks]."""
+    per_column = np.repeat(scales.astype(np.float64), ACT8_BLOCK, axis=1)[:, :d]
+    return codes[:, :d].astype(np.float64) * per_column
