@@ -303,4 +303,25 @@ hipError_t launch_act8_pack(int64_t n_rows, int d, int elem_bytes, const void* x
 hipError_t launch_act8_unpack(int64_t n_rows, int d, int elem_bytes, const int8_t* codes,
                               const float* scales, void* x, hipStream_t s);
 
+// Token embedding: out = scale * table[tokens], and the table's gradient.
+// tokens are int32 or int64 (index_bytes 4 or 8).
+struct EmbedGradBufs {
+  int32_t* counters;   // [4] places handed out, short ids, long ids (cleared)
+  int32_t* count;      // [vocab] tokens of each id (cleared)
+  int64_t clear_ints;  // ints of counters + count, cleared together
+  int32_t* base;       // [vocab] first place of each used id
+  int32_t* pos;        // [n] a token's place within its id
+  int32_t* perm;       // [n] token numbers, by id
+  int32_t* short_ids;  // [min(n, vocab)] used ids with at most 64 tokens
+  int32_t* long_ids;   // [n / 65 + 1] ids with more
+  size_t bytes;        // total workspace bytes
+};
+EmbedGradBufs embed_grad_carve(int64_t n_tokens, int vocab, void* ws);
+hipError_t launch_embed_forward(int64_t n, int vocab, int d, int elem_bytes, int index_bytes,
+                                float scale, const void* table, const void* tokens, void* out,
+                                hipStream_t s);
+hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, int index_bytes,
+                                 float scale, const void* dout, const void* tokens,
+                                 const EmbedGradBufs& b, float* dtable, hipStream_t s);
+
 }  // namespace twell

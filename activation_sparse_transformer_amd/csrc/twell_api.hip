@@ -4,6 +4,7 @@
 #include "../../include/twell.h"
 #include "kernels.h"
 
+#include <cmath>
 #include <mutex>
 
 #define TWELL_EXPORT extern "C" __attribute__((visibility("default")))
@@ -666,4 +667,54 @@ TWELL_EXPORT int ffn_sparse_backward_act8(const twell_shape* shape, const twell_
   if (x8 == nullptr) return TWELL_ERR_INVALID_ARG;
   return backward_impl(shape, nullptr, x8, w_up_t, w_down, h, dy, dx, dw_up_t, db_up, dw_down,
                        workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ embedding
+namespace twell {
+namespace {
+
+int check_embed(const twell_embed_shape* s) {
+  if (s == nullptr || s->reserved != 0) return TWELL_ERR_INVALID_ARG;
+  if (s->n_tokens < 0 || s->n_tokens > INT32_MAX || s->vocab <= 0) return TWELL_ERR_INVALID_ARG;
+  if (s->d_model <= 0 || s->d_model % 8 != 0) return TWELL_ERR_INVALID_ARG;
+  if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
+  if (!std::isfinite(s->scale)) return TWELL_ERR_INVALID_ARG;
+  return TWELL_OK;
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT int twell_embed_forward(const twell_embed_shape* shape, const void* table,
+                                     const void* tokens, void* out, void* stream) {
+  const int rc = check_embed(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_tokens > 0 && (table == nullptr || tokens == nullptr || out == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(table) || !aligned16(tokens) || !aligned16(out)) return TWELL_ERR_INVALID_ARG;
+  return hip_status(launch_embed_forward(
+      shape->n_tokens, shape->vocab, shape->d_model, elem_bytes(shape->dtype), shape->index_bytes,
+      shape->scale, table, tokens, out, static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT size_t twell_embed_backward_workspace_size(const twell_embed_shape* shape) {
+  if (check_embed(shape) != TWELL_OK) return 0;
+  return embed_grad_carve(shape->n_tokens, shape->vocab, nullptr).bytes;
+}
+
+TWELL_EXPORT int twell_embed_backward(const twell_embed_shape* shape, const void* dout,
+                                      const void* tokens, float* dtable, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  const int rc = check_embed(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_tokens > 0 && (dout == nullptr || tokens == nullptr)) return TWELL_ERR_INVALID_ARG;
+  if (dtable == nullptr || workspace == nullptr) return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(tokens) || !aligned16(dtable) || !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  const EmbedGradBufs b = embed_grad_carve(shape->n_tokens, shape->vocab, workspace);
+  if (workspace_bytes < b.bytes) return TWELL_ERR_WORKSPACE;
+  return hip_status(launch_embed_backward(
+      shape->n_tokens, shape->vocab, shape->d_model, elem_bytes(shape->dtype), shape->index_bytes,
+      shape->scale, dout, tokens, b, dtable, static_cast<hipStream_t>(stream)));
 }

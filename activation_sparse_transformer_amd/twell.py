@@ -36,6 +36,7 @@ EXPORTS = (
     "ffn_sparse_backward_workspace_size", "ffn_sparse_backward", "ffn_sparse_gated_forward",
     "twell_act8_pack", "twell_act8_unpack", "ffn_sparse_backward_act8_workspace_size",
     "ffn_sparse_backward_act8",
+    "twell_embed_forward", "twell_embed_backward_workspace_size", "twell_embed_backward",
 )
 
 
@@ -71,6 +72,14 @@ class EllStruct(ctypes.Structure):
 
 class Act8Struct(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class EmbedShape(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int32), ("d_model", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -120,6 +129,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ffn_sparse_backward_act8_workspace_size.restype = sz
     lib.ffn_sparse_backward_act8.argtypes = [S, A, P, P, H, P, P, P, P, P, P, sz, P]
     lib.ffn_sparse_backward_act8.restype = I
+    M = ctypes.POINTER(EmbedShape)
+    lib.twell_embed_forward.argtypes, lib.twell_embed_forward.restype = [M, P, P, P, P], I
+    lib.twell_embed_backward_workspace_size.argtypes = [M]
+    lib.twell_embed_backward_workspace_size.restype = sz
+    lib.twell_embed_backward.argtypes = [M, P, P, P, P, sz, P]
+    lib.twell_embed_backward.restype = I
     _lib = lib
     return lib
 
@@ -714,4 +729,66 @@ def ffn_sparse_backward_act8(x8: Act8, w_up_t: torch.Tensor, w_down: torch.Tenso
         ctypes.byref(shape), ctypes.byref(a), _ptr(w_up_t), _ptr(w_down), ctypes.byref(hs),
         _ptr(dy), _ptr(out.dx), _ptr(out.dw_up_t), _ptr(out.db_up), _ptr(out.dw_down),
         _ptr(workspace), workspace.numel(), _stream(dev)), "ffn_sparse_backward_act8")
+    return out
+
+
+# ------------------------------------------------------------------ embedding
+_INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _embed_shape(n: int, vocab: int, d: int, dtype: torch.dtype, index: torch.dtype,
+                 scale: float) -> EmbedShape:
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
+    if index not in _INDEX_BYTES:
+        raise ValueError(f"token ids must be int32 or int64, got {index}")
+    return EmbedShape(n, vocab, d, _DTYPE_CODE[dtype], _INDEX_BYTES[index], scale, 0)
+
+
+def twell_embed_forward(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """scale * table[tokens]: table [vocab, d_model], tokens [N] int32 or int64; an
+    id outside the table gives a row of zeros."""
+    dev = table.device
+    vocab, d = table.shape
+    n = tokens.shape[0]
+    _need(table, "table", dev)
+    _need(tokens, "tokens", dev, shape=(n,))
+    shape = _embed_shape(n, vocab, d, table.dtype, tokens.dtype, scale)
+    if out is None:
+        out = torch.empty((n, d), dtype=table.dtype, device=dev)
+    _need(out, "out", dev, table.dtype, (n, d))
+    _check(load().twell_embed_forward(ctypes.byref(shape), _ptr(table), _ptr(tokens), _ptr(out),
+                                      _stream(dev)), "twell_embed_forward")
+    return out
+
+
+def embed_backward_workspace(n_tokens: int, d_model: int, vocab: int, device) -> torch.Tensor:
+    """A workspace for twell_embed_backward of these sizes."""
+    shape = EmbedShape(n_tokens, vocab, d_model, 0, 8, 1.0, 0)
+    ws = int(load().twell_embed_backward_workspace_size(ctypes.byref(shape)))
+    if ws == 0:
+        raise TwellError(TWELL_ERR_INVALID_ARG, "twell_embed_backward_workspace_size")
+    return torch.empty((ws,), dtype=torch.uint8, device=device)
+
+
+def twell_embed_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, *,
+                         scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient [vocab, d_model] float32 of scale * table[tokens] for
+    dout [N, d_model]: every row written, the rows of absent ids zero."""
+    dev = dout.device
+    n, d = dout.shape
+    _need(dout, "dout", dev)
+    _need(tokens, "tokens", dev, shape=(n,))
+    shape = _embed_shape(n, vocab, d, dout.dtype, tokens.dtype, scale)
+    if out is None:
+        out = torch.empty((vocab, d), dtype=torch.float32, device=dev)
+    _need(out, "out", dev, torch.float32, (vocab, d))
+    if workspace is None:
+        workspace = embed_backward_workspace(n, d, vocab, dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    _check(load().twell_embed_backward(ctypes.byref(shape), _ptr(dout), _ptr(tokens), _ptr(out),
+                                       _ptr(workspace), workspace.numel(), _stream(dev)),
+           "twell_embed_backward")
     return out

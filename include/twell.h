@@ -453,6 +453,40 @@ int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, con
                              float* dw_up_t, float* db_up, float* dw_down, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* ---- The token embedding in front of the layers and its gradient.  The
+ * pages train and run whole language models of such layers ("Nvidia and Sakana
+ * make LLMs 30% faster by doing less math"); defined by this interface.
+ * tokens [n_tokens] are int32 or int64 (index_bytes 4 or 8); an id outside
+ * [0, vocab) is padding: its output row is zero and it adds to no gradient.
+ * Requirements: 0 <= n_tokens < 2^31; vocab > 0; d_model > 0 and a multiple of
+ * 8; dtype a twell_dtype; scale finite; reserved 0. */
+typedef struct twell_embed_shape {
+  int64_t n_tokens;
+  int32_t vocab;
+  int32_t d_model;
+  int32_t dtype;       /* twell_dtype of table, out and dout */
+  int32_t index_bytes; /* 4 or 8 */
+  float scale;
+  int32_t reserved;    /* must be 0 */
+} twell_embed_shape;
+
+/* out [n_tokens][d_model] = scale * table[tokens[n]], table [vocab][d_model]:
+ * the product in float32, rounded once to dtype. */
+int twell_embed_forward(const twell_embed_shape* shape, const void* table, const void* tokens,
+                        void* out, void* stream);
+
+/* Bytes of device workspace twell_embed_backward needs (0 for an invalid
+ * shape): counts and segments of the ids, the tokens by id. */
+size_t twell_embed_backward_workspace_size(const twell_embed_shape* shape);
+
+/* dtable [vocab][d_model] float32 = scale * the sum of dout [n_tokens][d_model]
+ * over the tokens of each id (float32 sums in an order fixed by the token
+ * numbers: the result repeats bit for bit).  Every row is written, not added
+ * to; ids without a token get zeros.  workspace: at least the queried bytes,
+ * never NULL, contents undefined on entry and exit. */
+int twell_embed_backward(const twell_embed_shape* shape, const void* dout, const void* tokens,
+                         float* dtable, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
