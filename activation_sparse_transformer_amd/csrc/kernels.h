@@ -324,4 +324,39 @@ hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, in
                                  float scale, const void* dout, const void* tokens,
                                  const EmbedGradBufs& b, float* dtable, hipStream_t s);
 
+// Log probabilities of targets [n_rows], entropy and log-sum-exp per row, and
+// the `top` best columns; logits rows `stride` elements apart.
+constexpr int kLogprobMaxTop = 32;
+struct LogprobArgs {
+  const void* logits;
+  const void* targets;
+  int64_t n_rows, stride;
+  int vocab, top;
+  float scale;
+  float *logp, *entropy, *lse;  // [n_rows]
+  int32_t* top_ids;             // [n_rows][top]
+  float* top_logp;              // [n_rows][top]
+  float4* parts;                // workspace: {m, s, t, 0} per part of a row
+  float* part_top;              // workspace: [parts][top] values, best first
+  int32_t* part_ids;            // workspace: [parts][top] columns
+};
+// Parts a row is split in, each taken by one wave (1: no workspace).
+int logprob_splits(int64_t n_rows, int vocab, int elem_bytes);
+// Sets the workspace parts of `a` (ws nullptr: sizes only); returns its bytes.
+size_t logprob_carve(LogprobArgs* a, int elem_bytes, void* ws);
+hipError_t launch_logprob_forward(const LogprobArgs& a, int elem_bytes, int index_bytes,
+                                  hipStream_t s);
+struct LogprobGradArgs {
+  const void* logits;
+  const void* targets;
+  int64_t n_rows, stride, out_stride;
+  int vocab;
+  float scale;
+  const float *lse, *entropy;     // [n_rows]; entropy is read with dentropy only
+  const float *dlogp, *dentropy;  // [n_rows]; dentropy nullptr: none
+  void* dlogits;
+};
+hipError_t launch_logprob_backward(const LogprobGradArgs& a, int elem_bytes, int index_bytes,
+                                   hipStream_t s);
+
 }  // namespace twell

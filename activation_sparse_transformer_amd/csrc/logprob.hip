@@ -1,0 +1,515 @@
+// Log probabilities of given tokens, with the entropy and the top
+// alternatives of each row, and their gradient.  With z = scale * x,
+//   lse = log sum_j exp z_j,  logp = z_t - lse,  p_j = exp(z_j - lse),
+//   entropy = -sum_j p_j log p_j.
+// The forward pass reads the logits once.  A lane keeps the running maximum m
+// of its x and, with d = (x - m) * scale * log2(e),
+//   s = sum 2^d,   t = sum d 2^d
+// (rescaled when m grows), so that lse = scale m + ln s and
+// entropy = ln s - ln2 * t / s: both terms are non-negative, nothing cancels.
+// A masked place (x = -inf) adds nothing to either sum.
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace twell {
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWaves = kLpThreads / kWave;
+constexpr int kLpLoads = 4;             // 16-byte vectors per lane and batch
+constexpr int kLpWantWaves = 4096;      // waves that keep 256 CUs busy
+constexpr int kLpMinVectors = 128;      // vectors of a row that are worth a wave
+constexpr int kLpMaxSplits = kWave;     // parts of a row: one lane each when joined
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kFarLse = 128.f;        // past it float32 lse moves p by over 2^-17
+constexpr float kFloorExp = -200.f;     // 2^d is 0 from here down, so d * 2^d is too
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+__device__ __forceinline__ float exp2_hw(float d) { return __builtin_amdgcn_exp2f(d); }
+
+template <typename E>
+__device__ __forceinline__ float elem(const uint4& v, int e);
+template <>
+__device__ __forceinline__ float elem<uint16_t>(const uint4& v, int e) {
+  const uint32_t w = e / 2 == 0 ? v.x : e / 2 == 1 ? v.y : e / 2 == 2 ? v.z : v.w;
+  return __uint_as_float(e % 2 == 0 ? w << 16 : w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ float elem<float>(const uint4& v, int e) {
+  return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+}
+
+// Sixteen bytes of -inf.
+template <typename E>
+__device__ __forceinline__ uint4 masked16() {
+  const uint32_t w = sizeof(E) == 2 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(w, w, w, w);
+}
+
+struct SoftStat {
+  float m = kLowest, s = 0.f, t = 0.f;
+  // a larger maximum: 2^d shrinks by f = 2^delta and every d moves by delta
+  __device__ __forceinline__ void raise(float to, float c) {
+    const float delta = fmaxf((m - to) * c, kFloorExp);
+    const float f = exp2_hw(delta);
+    t = f * (t + s * delta);
+    s *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void add(float x, float c) {
+    const float d = (x - m) * c;
+    const float e = exp2_hw(d);
+    s += e;
+    t = fmaf(fmaxf(d, kFloorExp), e, t);
+  }
+};
+
+// The lanes' statistics joined, the same in every lane.
+__device__ __forceinline__ SoftStat join_lanes(SoftStat a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+  a.raise(m, c);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    a.s += __shfl_xor(a.s, o, kWave);
+    a.t += __shfl_xor(a.t, o, kWave);
+  }
+  return a;
+}
+
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+// The best `top` (value, column) pairs seen by a wave, best first, lane i
+// holding the i-th; equal values keep the lower column first because columns
+// come in ascending order.  floor: no smaller or equal value can enter.
+struct TopList {
+  float v = neg_inf();
+  int id = -1;
+  float floor = neg_inf();
+  __device__ __forceinline__ void insert(float x, int col, int top) {
+    const int pos = popc64(wave_ballot(v >= x));
+    if (pos >= top) return;
+    const float uv = __shfl_up(v, 1, kWave);
+    const int ui = __shfl_up(id, 1, kWave);
+    const int lane = lane_id();
+    v = lane == pos ? x : lane > pos ? uv : v;
+    id = lane == pos ? col : lane > pos ? ui : id;
+    floor = fmaxf(floor, lane_value(v, top - 1));
+  }
+};
+
+// The largest float below x (of an x that is not NaN).
+__device__ __forceinline__ float below(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if (x == neg_inf()) return x;
+  if (x == 0.f) return __uint_as_float(0x80000001u);
+  return __uint_as_float(x > 0.f ? u - 1u : u + 1u);
+}
+
+// Takes the vectors' elements above the list's floor into the list; lane l's
+// vector u holds columns col0 + (u * 64 + l) * V.  A first batch sets the
+// floor from the lanes' maxima: `top` lanes hold a value of at least the
+// top-th largest of them.
+template <typename E, int U>
+__device__ __forceinline__ void take_top(const uint4 (&q)[U], const float (&vmax)[U], float bmax,
+                                         int col0, int top, TopList& list) {
+  constexpr int V = 16 / sizeof(E);
+  if (list.floor == neg_inf()) {
+    const int lane = lane_id();
+    int rank = 0;
+    for (int k = 0; k < kWave; ++k) {
+      const float o = lane_value(bmax, k);
+      rank += o > bmax || (o == bmax && k < lane);
+    }
+    const uint64_t at = wave_ballot(rank == top - 1);
+    if (at != 0) list.floor = below(lane_value(bmax, __builtin_ctzll(at)));
+  }
+  if (wave_ballot(bmax > list.floor) == 0) return;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint64_t lanes = wave_ballot(vmax[u] > list.floor);
+    while (lanes != 0) {
+      const int l = __builtin_ctzll(lanes);
+      lanes &= lanes - 1;
+      uint4 w;
+      w.x = __builtin_amdgcn_readlane(q[u].x, l), w.y = __builtin_amdgcn_readlane(q[u].y, l);
+      w.z = __builtin_amdgcn_readlane(q[u].z, l), w.w = __builtin_amdgcn_readlane(q[u].w, l);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = elem<E>(w, e);
+        if (x > list.floor) list.insert(x, col0 + (u * kWave + l) * V + e, top);
+      }
+    }
+  }
+}
+
+template <typename E, int U, bool TOP>
+__device__ __forceinline__ void take_batch(const uint4 (&q)[U], float c, int col0, int top,
+                                           SoftStat& a, TopList& list) {
+  constexpr int V = 16 / sizeof(E);
+  float vmax[U], bmax = neg_inf();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    vmax[u] = elem<E>(q[u], 0);
+#pragma unroll
+    for (int e = 1; e < V; ++e) vmax[u] = fmaxf(vmax[u], elem<E>(q[u], e));
+    bmax = fmaxf(bmax, vmax[u]);
+  }
+  if (bmax > a.m) a.raise(bmax, c);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.add(elem<E>(q[u], e), c);
+  if constexpr (TOP) take_top<E, U>(q, vmax, bmax, col0, top, list);
+}
+
+// The row's outputs from its joined statistics.
+template <typename E, typename I>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const SoftStat& st,
+                                          const TopList& list) {
+  const int lane = lane_id();
+  const E* x = static_cast<const E*>(a.logits) + row * a.stride;
+  const float ln_s = logf(st.s);
+  const bool empty = st.s == 0.f;  // every place masked
+  if (lane == 0) {
+    const int64_t t = static_cast<int64_t>(static_cast<const I*>(a.targets)[row]);
+    float logp = 0.f;
+    if (t >= 0 && t < a.vocab)
+      logp = empty ? neg_inf() : fmaf(ElemTraits<E>::to_f32(x[t]) - st.m, a.scale, -ln_s);
+    a.logp[row] = logp;
+    a.entropy[row] = empty ? 0.f : ln_s - kLn2 * (st.t / st.s);
+    a.lse[row] = empty ? neg_inf() : fmaf(st.m, a.scale, ln_s);
+  }
+  if (lane < a.top) {
+    a.top_ids[row * a.top + lane] = list.id;
+    a.top_logp[row * a.top + lane] =
+        list.id < 0 ? neg_inf() : fmaf(list.v - st.m, a.scale, -ln_s);
+  }
+}
+
+// Wave i of the grid takes part i % splits of row i / splits: the row's whole
+// 16-byte vectors [part * per, (part + 1) * per), the first part also the
+// elements before the first vector and the last one those after the last.
+template <typename E, typename I, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const LogprobArgs a,
+                                                                    int splits, int per,
+                                                                    int64_t n_items) {
+  constexpr int V = 16 / sizeof(E);
+  const int lane = lane_id();
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kLpWaves + threadIdx.x / kWave;
+  if (item >= n_items) return;
+  const int64_t row = item / splits;
+  const int part = static_cast<int>(item - row * splits);
+  const E* x = static_cast<const E*>(a.logits) + row * a.stride;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(E) % V);
+  const int head = min((V - off) % V, a.vocab);
+  const int nv = (a.vocab - head) / V;
+  const uint4* body = reinterpret_cast<const uint4*>(x + head);
+  const float c = a.scale * kLog2e;
+  SoftStat st;
+  TopList list;
+  // at most V - 1 elements from column col0, one per lane
+  auto take_edge = [&](int col0, int n) {
+    const float v = lane < n ? ElemTraits<E>::to_f32(x[col0 + lane]) : neg_inf();
+    if (v > st.m) st.raise(v, c);
+    st.add(v, c);
+    if constexpr (TOP)
+      for (int k = 0; k < n; ++k) {
+        const float w = lane_value(v, k);
+        if (w > list.floor) list.insert(w, col0 + k, a.top);
+      }
+  };
+  if (part == 0 && head > 0) take_edge(0, head);
+  const int end = min(nv, (part + 1) * per);
+  for (int v0 = part * per; v0 < end; v0 += kLpLoads * kWave) {
+    uint4 q[kLpLoads];
+#pragma unroll
+    for (int u = 0; u < kLpLoads; ++u) {
+      const int v = v0 + u * kWave + lane;
+      q[u] = v < end ? body[v] : masked16<E>();
+    }
+    take_batch<E, kLpLoads, TOP>(q, c, head + v0 * V, a.top, st, list);
+  }
+  const int tail0 = head + nv * V;
+  if (part == splits - 1 && tail0 < a.vocab) take_edge(tail0, a.vocab - tail0);
+  st = join_lanes(st, c);
+  if (splits == 1) {
+    write_row<E, I>(a, row, st, list);
+    return;
+  }
+  if (lane == 0) a.parts[item] = make_float4(st.m, st.s, st.t, 0.f);
+  if (TOP && lane < a.top) {
+    a.part_top[item * a.top + lane] = list.v;
+    a.part_ids[item * a.top + lane] = list.id;
+  }
+}
+
+// One wave per row joins its parts: lane l takes part l.  Parts hold ascending
+// columns, so equal values go to the lower part first.
+template <typename E, typename I>
+__global__ __launch_bounds__(kWave) void logprob_join_kernel(const LogprobArgs a, int splits) {
+  __shared__ float vals[kLpMaxSplits * kLogprobMaxTop];
+  __shared__ int ids[kLpMaxSplits * kLogprobMaxTop];
+  const int lane = lane_id();
+  const int64_t row = blockIdx.x;
+  const float c = a.scale * kLog2e;
+  SoftStat st;
+  if (lane < splits) {
+    const float4 p = a.parts[row * splits + lane];
+    st.m = p.x, st.s = p.y, st.t = p.z;
+  }
+  st = join_lanes(st, c);
+  TopList list;
+  if (a.top > 0) {
+    for (int k = lane; k < splits * a.top; k += kWave) {
+      vals[k] = a.part_top[row * splits * a.top + k];
+      ids[k] = a.part_ids[row * splits * a.top + k];
+    }
+    __syncthreads();
+    int at = 0;
+    for (int k = 0; k < a.top; ++k) {
+      const bool have = lane < splits && at < a.top;
+      const float v = have ? vals[lane * a.top + at] : neg_inf();
+      float best = v;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) best = fmaxf(best, __shfl_xor(best, o, kWave));
+      if (best == neg_inf()) break;  // fewer places than asked for
+      const int l = __builtin_ctzll(wave_ballot(v == best));
+      const int id = have ? ids[lane * a.top + at] : -1;
+      const int got = __builtin_amdgcn_readlane(id, l);
+      if (lane == k) list.v = best, list.id = got;
+      if (lane == l) ++at;
+    }
+  }
+  write_row<E, I>(a, row, st, list);
+}
+
+// dlogits of one element: scale * (g * [j is the target] - p * (g + w * (log p + H))).
+// log p = (x - m) * scale - ln_s: m = 0 and ln_s = lse, or a row's own maximum
+// and sum (FAR) where lse alone would not hold them.
+struct RowGrad {
+  float m, ln_s, scale, g, w, h;
+  template <bool ENT, bool FAR>
+  __device__ __forceinline__ float at(float x, bool target) const {
+    const float lp = fmaf(FAR ? x - m : x, scale, -ln_s);
+    const float p = exp2_hw(lp * kLog2e);
+    // a masked place has p = 0 and log p = -inf: its product is 0
+    const float k = ENT ? fmaf(w, fmaxf(lp, kFloorExp) + h, g) : g;
+    const float d = fmaf(-p, k, target ? g : 0.f);
+    return d * scale;
+  }
+};
+
+// The workgroup's statistics of a whole row (every lane gets them).
+template <typename E>
+__device__ SoftStat block_stat(const E* x, int vocab, float c) {
+  __shared__ float3 waves[kLpWaves];
+  SoftStat st;
+  for (int j = threadIdx.x; j < vocab; j += kLpThreads) {
+    const float v = ElemTraits<E>::to_f32(x[j]);
+    if (v > st.m) st.raise(v, c);
+    st.add(v, c);
+  }
+  st = join_lanes(st, c);
+  __syncthreads();
+  if (lane_id() == 0) waves[threadIdx.x / kWave] = make_float3(st.m, st.s, st.t);
+  __syncthreads();
+  SoftStat w;
+  if (lane_id() < kLpWaves) {
+    const float3 p = waves[lane_id()];
+    w.m = p.x, w.s = p.y, w.t = p.z;
+  }
+  return join_lanes(w, c);
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 pack16(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 2)
+      w[i] = ElemTraits<E>::from_f32(f[2 * i]) |
+             static_cast<uint32_t>(ElemTraits<E>::from_f32(f[2 * i + 1])) << 16;
+    else
+      w[i] = __float_as_uint(f[i]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The chunk's elements of one row: kLpThreads * kLpLoads vectors (the row's
+// first chunk also the elements before its first vector, the last one those
+// after its last).  VEC: input and output rows share their alignment.
+template <typename E, bool ENT, bool VEC, bool FAR>
+__device__ __forceinline__ void grad_chunk(const E* x, E* out, const RowGrad& r, int vocab, int t,
+                                           int chunk, int chunks) {
+  constexpr int V = VEC ? 16 / sizeof(E) : 1;
+  typedef ElemTraits<E> Tr;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(E) % V);
+  const int head = min((V - off) % V, vocab);
+  const int nv = (vocab - head) / V;
+  auto one = [&](int j) {
+    out[j] = Tr::from_f32(r.template at<ENT, FAR>(Tr::to_f32(x[j]), j == t));
+  };
+  if (chunk == 0 && static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
+  const int tail0 = head + nv * V;
+  if (chunk == chunks - 1 && static_cast<int>(threadIdx.x) < vocab - tail0)
+    one(tail0 + threadIdx.x);
+  const int v0 = chunk * (kLpThreads * kLpLoads) + threadIdx.x;
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int u = 0; u < kLpLoads; ++u)
+      if (v0 + u * kLpThreads < nv) one(v0 + u * kLpThreads);
+  } else {
+    const uint4* body = reinterpret_cast<const uint4*>(x + head);
+    uint4* to = reinterpret_cast<uint4*>(out + head);
+    uint4 q[kLpLoads];
+#pragma unroll
+    for (int u = 0; u < kLpLoads; ++u) {
+      const int v = v0 + u * kLpThreads;
+      if (v < nv) q[u] = body[v];
+    }
+#pragma unroll
+    for (int u = 0; u < kLpLoads; ++u) {
+      const int v = v0 + u * kLpThreads;
+      if (v >= nv) continue;
+      float f[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        f[e] = r.template at<ENT, FAR>(elem<E>(q[u], e), head + v * V + e == t);
+      to[v] = pack16<E>(f);
+    }
+  }
+}
+
+// A workgroup takes one chunk of a row.  lse is rounded to float32, which
+// moves every p of the row by |lse| * 2^-24 of itself; past kFarLse (a row of
+// the type's lowest values, or logits far from zero) the row's own maximum and
+// sum are formed again instead.  dlogits may be the logits, where nothing may
+// be read again: the chunks of such a row would see each other's results, so
+// there one workgroup forms them and takes the row's chunks in turn.
+template <typename E, typename I, bool ENT, bool VEC>
+__global__ __launch_bounds__(kLpThreads) void logprob_backward_kernel(const LogprobGradArgs a,
+                                                                     int chunks,
+                                                                     int64_t n_items) {
+  for (int64_t item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const int64_t row = item / chunks;
+    const int chunk = static_cast<int>(item - row * chunks);
+    const E* x = static_cast<const E*>(a.logits) + row * a.stride;
+    E* out = static_cast<E*>(a.dlogits) + row * a.out_stride;
+    const int64_t t64 = static_cast<int64_t>(static_cast<const I*>(a.targets)[row]);
+    const int t = t64 >= 0 && t64 < a.vocab ? static_cast<int>(t64) : -1;
+    const float lse = a.lse[row];
+    RowGrad r;
+    r.m = 0.f;
+    r.ln_s = lse;
+    r.scale = a.scale;
+    r.g = t >= 0 ? a.dlogp[row] : 0.f;
+    r.w = ENT ? a.dentropy[row] : 0.f;
+    r.h = ENT ? a.entropy[row] : 0.f;
+    if (lse == neg_inf()) {  // every place masked: no gradient
+      r.ln_s = -neg_inf();
+      r.g = r.w = 0.f;
+    } else if (fabsf(lse) > kFarLse) {
+      if (chunk != 0) continue;
+      const SoftStat st = block_stat<E>(x, a.vocab, a.scale * kLog2e);
+      r.m = st.m;
+      r.ln_s = logf(st.s);
+      __syncthreads();  // every read of the row before its first write
+      for (int k = 0; k < chunks; ++k)
+        grad_chunk<E, ENT, VEC, true>(x, out, r, a.vocab, t, k, chunks);
+      continue;
+    }
+    grad_chunk<E, ENT, VEC, false>(x, out, r, a.vocab, t, chunk, chunks);
+  }
+}
+
+}  // namespace
+
+// Parts a row is split in: enough waves for the whole GPU, but no part under
+// kLpMinVectors vectors.
+int logprob_splits(int64_t n_rows, int vocab, int elem_bytes) {
+  const int nv = vocab / (16 / elem_bytes);
+  const int64_t want = (kLpWantWaves + n_rows - 1) / (n_rows < 1 ? 1 : n_rows);
+  int64_t most = nv / kLpMinVectors;
+  if (most > kLpMaxSplits) most = kLpMaxSplits;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+size_t logprob_carve(LogprobArgs* a, int elem_bytes, void* ws) {
+  const int splits = logprob_splits(a->n_rows, a->vocab, elem_bytes);
+  if (splits == 1) return 0;
+  const size_t parts = static_cast<size_t>(a->n_rows) * splits;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = p == nullptr ? nullptr : p + off;
+    off += (bytes + 255) / 256 * 256;
+    return q;
+  };
+  a->parts = reinterpret_cast<float4*>(take(parts * sizeof(float4)));
+  a->part_top = reinterpret_cast<float*>(take(parts * a->top * 4));
+  a->part_ids = reinterpret_cast<int32_t*>(take(parts * a->top * 4));
+  return off;
+}
+
+hipError_t launch_logprob_forward(const LogprobArgs& a, int elem_bytes, int index_bytes,
+                                  hipStream_t s) {
+  if (a.n_rows == 0) return hipSuccess;
+  const int splits = logprob_splits(a.n_rows, a.vocab, elem_bytes);
+  const int V = 16 / elem_bytes;
+  int per = (a.vocab / V + splits - 1) / splits;
+  per = (per + kWave - 1) / kWave * kWave;
+  const int64_t items = a.n_rows * splits;
+  const unsigned grid = static_cast<unsigned>((items + kLpWaves - 1) / kLpWaves);
+  auto go = [&](auto e, auto i) {
+    typedef decltype(e) E;
+    typedef decltype(i) I;
+    if (a.top > 0)
+      logprob_forward_kernel<E, I, true><<<grid, kLpThreads, 0, s>>>(a, splits, per, items);
+    else
+      logprob_forward_kernel<E, I, false><<<grid, kLpThreads, 0, s>>>(a, splits, per, items);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || splits == 1) return err;
+    logprob_join_kernel<E, I><<<static_cast<unsigned>(a.n_rows), kWave, 0, s>>>(a, splits);
+    return hipGetLastError();
+  };
+  if (elem_bytes == 2)
+    return index_bytes == 8 ? go(uint16_t{}, int64_t{}) : go(uint16_t{}, int32_t{});
+  return index_bytes == 8 ? go(float{}, int64_t{}) : go(float{}, int32_t{});
+}
+
+hipError_t launch_logprob_backward(const LogprobGradArgs& a, int elem_bytes, int index_bytes,
+                                   hipStream_t s) {
+  if (a.n_rows == 0) return hipSuccess;
+  // rows of both arrays start at the same place within 16 bytes
+  const bool vec = (a.stride - a.out_stride) * elem_bytes % 16 == 0;
+  const int per = kLpThreads * kLpLoads;
+  const int nv = vec ? a.vocab / (16 / elem_bytes) : a.vocab;
+  const int chunks = nv < 1 ? 1 : (nv + per - 1) / per;
+  const int64_t items = a.n_rows * chunks;
+  const unsigned grid = static_cast<unsigned>(items < (1 << 23) ? items : (1 << 23));
+  auto go = [&](auto e, auto i, auto ent, auto v) {
+    logprob_backward_kernel<decltype(e), decltype(i), decltype(ent)::value, decltype(v)::value>
+        <<<grid, kLpThreads, 0, s>>>(a, chunks, items);
+    return hipGetLastError();
+  };
+  auto by_vec = [&](auto e, auto i, auto ent) {
+    return vec ? go(e, i, ent, std::true_type{}) : go(e, i, ent, std::false_type{});
+  };
+  auto by_ent = [&](auto e, auto i) {
+    return a.dentropy != nullptr ? by_vec(e, i, std::true_type{}) : by_vec(e, i, std::false_type{});
+  };
+  if (elem_bytes == 2)
+    return index_bytes == 8 ? by_ent(uint16_t{}, int64_t{}) : by_ent(uint16_t{}, int32_t{});
+  return index_bytes == 8 ? by_ent(float{}, int64_t{}) : by_ent(float{}, int32_t{});
+}
+
+}  // namespace twell

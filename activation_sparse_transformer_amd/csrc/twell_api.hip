@@ -718,3 +718,96 @@ TWELL_EXPORT int twell_embed_backward(const twell_embed_shape* shape, const void
       shape->n_tokens, shape->vocab, shape->d_model, elem_bytes(shape->dtype), shape->index_bytes,
       shape->scale, dout, tokens, b, dtable, static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ log probabilities
+namespace twell {
+namespace {
+
+int check_logprob(const twell_logprob_shape* s) {
+  if (s == nullptr || s->reserved != 0) return TWELL_ERR_INVALID_ARG;
+  if (s->n_rows < 0 || s->n_rows > INT32_MAX) return TWELL_ERR_INVALID_ARG;
+  if (s->vocab <= 0 || s->vocab > (1 << 30) || s->row_stride < s->vocab)
+    return TWELL_ERR_INVALID_ARG;
+  if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
+  if (s->top < 0 || s->top > kLogprobMaxTop || s->top > s->vocab) return TWELL_ERR_INVALID_ARG;
+  if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return TWELL_ERR_INVALID_ARG;
+  // a launch holds fewer than 2^32 lanes, a wave per part of a row
+  if (s->n_rows * logprob_splits(s->n_rows, s->vocab, elem_bytes(s->dtype)) >=
+      (int64_t{1} << 26) - 4)
+    return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+LogprobArgs logprob_args(const twell_logprob_shape* s) {
+  LogprobArgs a{};
+  a.n_rows = s->n_rows;
+  a.stride = s->row_stride;
+  a.vocab = s->vocab;
+  a.top = s->top;
+  a.scale = s->scale;
+  return a;
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT size_t twell_logprob_workspace_size(const twell_logprob_shape* shape) {
+  if (check_logprob(shape) != TWELL_OK) return 0;
+  LogprobArgs a = logprob_args(shape);
+  return logprob_carve(&a, elem_bytes(shape->dtype), nullptr);
+}
+
+TWELL_EXPORT int twell_logprob_forward(const twell_logprob_shape* shape, const void* logits,
+                                       const void* targets, float* logp, float* entropy,
+                                       float* lse, int32_t* top_ids, float* top_logp,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_logprob(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_rows > 0) {
+    if (logits == nullptr || targets == nullptr || logp == nullptr || entropy == nullptr ||
+        lse == nullptr)
+      return TWELL_ERR_INVALID_ARG;
+    if (shape->top > 0 && (top_ids == nullptr || top_logp == nullptr)) return TWELL_ERR_INVALID_ARG;
+  }
+  if (!aligned16(logits) || !aligned16(targets) || !aligned16(logp) || !aligned16(entropy) ||
+      !aligned16(lse) || !aligned16(top_ids) || !aligned16(top_logp) || !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  LogprobArgs a = logprob_args(shape);
+  const size_t need = logprob_carve(&a, elem_bytes(shape->dtype), workspace);
+  if (need > 0 && workspace == nullptr) return TWELL_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return TWELL_ERR_WORKSPACE;
+  a.logits = logits;
+  a.targets = targets;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  return hip_status(launch_logprob_forward(a, elem_bytes(shape->dtype), shape->index_bytes,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT int twell_logprob_backward(const twell_logprob_shape* shape, const void* logits,
+                                        const void* targets, const float* lse,
+                                        const float* entropy, const float* dlogp,
+                                        const float* dentropy, void* dlogits, int64_t out_stride,
+                                        void* stream) {
+  const int rc = check_logprob(shape);
+  if (rc != TWELL_OK) return rc;
+  if (out_stride < shape->vocab) return TWELL_ERR_INVALID_ARG;
+  if (shape->n_rows > 0) {
+    if (logits == nullptr || targets == nullptr || lse == nullptr || dlogp == nullptr ||
+        dlogits == nullptr || (dentropy != nullptr && entropy == nullptr))
+      return TWELL_ERR_INVALID_ARG;
+    if (dlogits == logits && out_stride != shape->row_stride) return TWELL_ERR_INVALID_ARG;
+  }
+  if (!aligned16(logits) || !aligned16(targets) || !aligned16(lse) || !aligned16(entropy) ||
+      !aligned16(dlogp) || !aligned16(dentropy) || !aligned16(dlogits))
+    return TWELL_ERR_INVALID_ARG;
+  const LogprobGradArgs a{logits,        targets,      shape->n_rows, shape->row_stride,
+                          out_stride,    shape->vocab, shape->scale,  lse,
+                          entropy,       dlogp,        dentropy,      dlogits};
+  return hip_status(launch_logprob_backward(a, elem_bytes(shape->dtype), shape->index_bytes,
+                                            static_cast<hipStream_t>(stream)));
+}

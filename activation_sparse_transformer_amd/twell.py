@@ -37,6 +37,7 @@ EXPORTS = (
     "twell_act8_pack", "twell_act8_unpack", "ffn_sparse_backward_act8_workspace_size",
     "ffn_sparse_backward_act8",
     "twell_embed_forward", "twell_embed_backward_workspace_size", "twell_embed_backward",
+    "twell_logprob_workspace_size", "twell_logprob_forward", "twell_logprob_backward",
 )
 
 
@@ -79,6 +80,14 @@ class EmbedShape(ctypes.Structure):
         ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int32), ("d_model", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("scale", ctypes.c_float),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class LogprobShape(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("vocab", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("top", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -135,6 +144,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.twell_embed_backward_workspace_size.restype = sz
     lib.twell_embed_backward.argtypes = [M, P, P, P, P, sz, P]
     lib.twell_embed_backward.restype = I
+    L = ctypes.POINTER(LogprobShape)
+    lib.twell_logprob_workspace_size.argtypes = [L]
+    lib.twell_logprob_workspace_size.restype = sz
+    lib.twell_logprob_forward.argtypes = [L, P, P, P, P, P, P, P, P, sz, P]
+    lib.twell_logprob_forward.restype = I
+    lib.twell_logprob_backward.argtypes = [L, P, P, P, P, P, P, P, i64, P]
+    lib.twell_logprob_backward.restype = I
     _lib = lib
     return lib
 
@@ -791,4 +807,114 @@ def twell_embed_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, *
     _check(load().twell_embed_backward(ctypes.byref(shape), _ptr(dout), _ptr(tokens), _ptr(out),
                                        _ptr(workspace), workspace.numel(), _stream(dev)),
            "twell_embed_backward")
+    return out
+
+
+# ------------------------------------------------------------------ log probabilities
+@dataclasses.dataclass
+class LogProbs:
+    """Everything twell_logprob_forward writes."""
+
+    logp: torch.Tensor      # [N] float32, of the targets (0 where ignored)
+    entropy: torch.Tensor   # [N] float32
+    lse: torch.Tensor       # [N] float32
+    top_ids: torch.Tensor   # [N, top] int32, -1 where there is none
+    top_logp: torch.Tensor  # [N, top] float32
+
+    @classmethod
+    def empty(cls, n_rows: int, top: int, device) -> "LogProbs":
+        f = lambda *s: torch.empty(s, dtype=torch.float32, device=device)
+        return cls(f(n_rows), f(n_rows), f(n_rows),
+                   torch.empty((n_rows, top), dtype=torch.int32, device=device), f(n_rows, top))
+
+
+def _need_rows(t: torch.Tensor, name: str, device, shape=None) -> None:
+    """A matrix whose rows are contiguous, at any distance from each other."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in _DTYPE_CODE:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported (float32 or bfloat16)")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
+            t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be a matrix of contiguous rows")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _logprob_shape(logits: torch.Tensor, targets: torch.Tensor, top: int,
+                   scale: float) -> LogprobShape:
+    dev = logits.device
+    _need_rows(logits, "logits", dev)
+    n, vocab = logits.shape
+    _need(targets, "targets", dev, shape=(n,))
+    if targets.dtype not in _INDEX_BYTES:
+        raise ValueError(f"targets must be int32 or int64, got {targets.dtype}")
+    return LogprobShape(n, _row_stride(logits), vocab, _DTYPE_CODE[logits.dtype],
+                        _INDEX_BYTES[targets.dtype], top, scale, 0)
+
+
+def logprob_workspace(n_rows: int, vocab: int, top: int, dtype: torch.dtype,
+                      device) -> torch.Tensor:
+    """A workspace for twell_logprob_forward of these sizes (empty when none is needed)."""
+    shape = LogprobShape(n_rows, vocab, vocab, _DTYPE_CODE[dtype], 8, top, 1.0, 0)
+    return torch.empty((int(load().twell_logprob_workspace_size(ctypes.byref(shape))),),
+                       dtype=torch.uint8, device=device)
+
+
+def twell_logprob_forward(logits: torch.Tensor, targets: torch.Tensor, *, top: int = 0,
+                          scale: float = 1.0, out: Optional[LogProbs] = None,
+                          workspace: Optional[torch.Tensor] = None) -> LogProbs:
+    """Log probabilities of targets [N] under softmax(scale * logits [N, vocab]), each row's
+    entropy and log-sum-exp, and its `top` most likely tokens.
+
+    Rows of logits may be any distance apart (a padded vocabulary); targets are int32 or
+    int64, and one outside the vocabulary is ignored."""
+    dev = logits.device
+    shape = _logprob_shape(logits, targets, top, scale)
+    n = logits.shape[0]
+    if out is None:
+        out = LogProbs.empty(n, max(top, 0), dev)
+    for name in ("logp", "entropy", "lse"):
+        _need(getattr(out, name), name, dev, torch.float32, (n,))
+    _need(out.top_ids, "top_ids", dev, torch.int32, (n, max(top, 0)))
+    _need(out.top_logp, "top_logp", dev, torch.float32, (n, max(top, 0)))
+    if workspace is None:
+        workspace = torch.empty((int(load().twell_logprob_workspace_size(ctypes.byref(shape))),),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    _check(load().twell_logprob_forward(
+        ctypes.byref(shape), _ptr(logits), _ptr(targets), _ptr(out.logp), _ptr(out.entropy),
+        _ptr(out.lse), _ptr(out.top_ids), _ptr(out.top_logp), _ptr(workspace), workspace.numel(),
+        _stream(dev)), "twell_logprob_forward")
+    return out
+
+
+def twell_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                           entropy: Optional[torch.Tensor], dlogp: torch.Tensor,
+                           dentropy: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient [N, vocab] of sum(dlogp * logp + dentropy * entropy) with respect to the
+    logits, from the forward's lse and (with dentropy) entropy.  `out` may be the logits."""
+    dev = logits.device
+    shape = _logprob_shape(logits, targets, 0, scale)
+    n = logits.shape[0]
+    _need(lse, "lse", dev, torch.float32, (n,))
+    _need(dlogp, "dlogp", dev, torch.float32, (n,))
+    if dentropy is not None:
+        _need(dentropy, "dentropy", dev, torch.float32, (n,))
+        if entropy is None:
+            raise ValueError("dentropy needs the forward's entropy")
+        _need(entropy, "entropy", dev, torch.float32, (n,))
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    _need_rows(out, "out", dev, logits.shape)
+    if out.dtype != logits.dtype:
+        raise ValueError(f"out must be {logits.dtype}, got {out.dtype}")
+    _check(load().twell_logprob_backward(
+        ctypes.byref(shape), _ptr(logits), _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(dlogp),
+        _ptr(dentropy), _ptr(out), _row_stride(out), _stream(dev)), "twell_logprob_backward")
     return out

@@ -487,6 +487,66 @@ size_t twell_embed_backward_workspace_size(const twell_embed_shape* shape);
 int twell_embed_backward(const twell_embed_shape* shape, const void* dout, const void* tokens,
                          float* dtable, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Log probabilities of given tokens, behind the last layer: the loss of a
+ * training step and its gradient, or the scores of sampled tokens and their
+ * alternatives.  Defined by this interface.  For a row of logits x
+ * [0 .. vocab), with z = scale * x:
+ *   lse = log sum_j exp z_j;  log p_j = z_j - lse;  entropy = -sum_j p_j log p_j
+ *  - logits rows are row_stride elements apart (row_stride >= vocab; any
+ *    parity: rows need no alignment, the first element does).
+ *  - targets [n_rows] are int32 or int64 (index_bytes 4 or 8); a target outside
+ *    [0, vocab) is ignored: its logp is 0 and has no gradient.
+ *  - A place with x = -inf is masked: probability 0, never an alternative.
+ *    A row with nothing else has lse = -inf, entropy 0, logp = -inf and a zero
+ *    gradient.  Finite masks (the type's lowest value) are ordinary values.
+ *  - A row holding NaN or +inf has NaN results (its alternatives are still the
+ *    largest values that are not NaN).
+ *  - The alternatives are the `top` (0 .. TWELL_LOGPROB_MAX_TOP) largest logits,
+ *    largest first, the lowest index first among equals; where fewer places are
+ *    unmasked the rest have id -1 and log probability -inf.
+ * Sums, maxima and probabilities are float32 throughout.
+ * Requirements: n_rows >= 0; 0 < vocab <= 2^30; n_rows * parts of a row (1 for
+ * thousands of rows, at most 64) below 2^26 - 4, else TWELL_ERR_UNSUPPORTED;
+ * dtype a twell_dtype; top <= vocab; scale finite and > 0;
+ * reserved 0. */
+#define TWELL_LOGPROB_MAX_TOP 32
+typedef struct twell_logprob_shape {
+  int64_t n_rows;
+  int64_t row_stride;  /* elements between rows of logits */
+  int32_t vocab;
+  int32_t dtype;       /* twell_dtype of logits and dlogits */
+  int32_t index_bytes; /* 4 or 8 */
+  int32_t top;
+  float scale;
+  int32_t reserved;    /* must be 0 */
+} twell_logprob_shape;
+
+/* Bytes of device workspace twell_logprob_forward needs for this shape: 0 when
+ * a row is not split over workgroups (workspace may then be NULL) and for an
+ * invalid shape. */
+size_t twell_logprob_workspace_size(const twell_logprob_shape* shape);
+
+/* logp, entropy, lse [n_rows] float32 and, for top > 0, top_ids [n_rows][top]
+ * int32 and top_logp [n_rows][top] float32 of logits, in one pass over them. */
+int twell_logprob_forward(const twell_logprob_shape* shape, const void* logits,
+                          const void* targets, float* logp, float* entropy, float* lse,
+                          int32_t* top_ids, float* top_logp, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The gradient of sum_n (dlogp[n] logp[n] + dentropy[n] entropy[n]):
+ *   dlogits_j = scale * (dlogp (1[j = target] - p_j)
+ *                        - dentropy p_j (log p_j + entropy))
+ * from the forward's lse and entropy (entropy is read only with dentropy;
+ * dentropy may be NULL).  dlogits has rows out_stride elements apart and may be
+ * the logits themselves (out_stride == row_stride); columns past vocab are not
+ * written.  shape->top is ignored.  Rows with |lse| > 128, where a float32 lse
+ * is too coarse, are normalised by their own sum formed again (one workgroup
+ * per such row). */
+int twell_logprob_backward(const twell_logprob_shape* shape, const void* logits,
+                           const void* targets, const float* lse, const float* entropy,
+                           const float* dlogp, const float* dentropy, void* dlogits,
+                           int64_t out_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

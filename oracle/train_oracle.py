@@ -42,3 +42,55 @@ def embed_grad(dout: np.ndarray, tokens: np.ndarray, vocab: int, scale: float) -
     ok = (tokens >= 0) & (tokens < vocab)
     np.add.at(out, tokens[ok], dout[ok])
     return out * scale
+
+
+def logprob(x: np.ndarray, targets: np.ndarray, scale: float, top: int):
+    """logp, entropy, lse, ids and log probabilities of the alternatives for logits x
+    [N, V] in float64, row by row from the definitions."""
+    n, v = x.shape
+    logp, entropy, lse = np.zeros(n), np.zeros(n), np.zeros(n)
+    ids, tops = np.full((n, top), -1), np.full((n, top), -np.inf)
+    for r in range(n):
+        live = x[r] != -np.inf
+        if np.isnan(x[r]).any() or (x[r] == np.inf).any():
+            logp[r] = entropy[r] = lse[r] = np.nan
+        elif not live.any():
+            lse[r] = logp[r] = -np.inf
+        else:
+            z = x[r] * scale
+            m = z.max()
+            ln_s = np.log(np.exp(z - m).sum())
+            lse[r] = m + ln_s
+            lp = (z[live] - m) - ln_s
+            entropy[r] = -(np.exp(lp) * lp).sum()
+            if 0 <= targets[r] < v:
+                logp[r] = (z[targets[r]] - m) - ln_s
+        if not 0 <= targets[r] < v:
+            logp[r] = 0.0
+        order = sorted((j for j in np.nonzero(live & ~np.isnan(x[r]))[0]),
+                       key=lambda j: (-x[r, j], j))[:top]
+        ids[r, :len(order)] = order
+        if np.isnan(lse[r]):
+            tops[r, :len(order)] = np.nan
+        elif order:
+            tops[r, :len(order)] = (x[r, order] * scale - m) - ln_s
+    return logp, entropy, lse, ids, tops
+
+
+def logprob_grad(x, targets, scale, dlogp, dentropy):
+    """The gradient of sum(dlogp * logp + dentropy * entropy) in float64."""
+    n, v = x.shape
+    out = np.zeros((n, v))
+    for r in range(n):
+        live = x[r] != -np.inf
+        if not live.any():
+            continue
+        z = x[r] * scale
+        lp = (z[live] - z.max()) - np.log(np.exp(z - z.max()).sum())
+        p = np.exp(lp)
+        g = dlogp[r] if 0 <= targets[r] < v else 0.0
+        d = -g * p - dentropy[r] * p * (lp - (p * lp).sum())
+        out[r, live] = d
+        if g:
+            out[r, targets[r]] += g
+    return out * scale
