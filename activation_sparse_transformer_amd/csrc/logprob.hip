@@ -19,9 +19,11 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / kWave;
 constexpr int kLpLoads = 4;             // 16-byte vectors per lane and batch
-constexpr int kLpWantWaves = 4096;      // waves that keep 256 CUs busy
+constexpr int kLpWantWaves = 4096;      // waves that keep 256 CUs busy (1024 .. 16384 measured:
+                                        // within 5% at 1000 and 2000 rows, 64 rows 40% slower at 1024)
 constexpr int kLpMinVectors = 128;      // vectors of a row that are worth a wave
 constexpr int kLpMaxSplits = kWave;     // parts of a row: one lane each when joined
+constexpr int kLpCand = 4 * kWave;      // candidates packed at a time
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLowest = -3.402823466e38f;
@@ -60,12 +62,13 @@ struct SoftStat {
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ void add(float x, float c) {
+  __device__ __forceinline__ void term(float x, float c, float& ps, float& pt) const {
     const float d = (x - m) * c;
     const float e = exp2_hw(d);
-    s += e;
-    t = fmaf(fmaxf(d, kFloorExp), e, t);
+    ps += e;
+    pt = fmaf(fmaxf(d, kFloorExp), e, pt);
   }
+  __device__ __forceinline__ void add(float x, float c) { term(x, c, s, t); }
 };
 
 // The lanes' statistics joined, the same in every lane.
@@ -86,24 +89,70 @@ __device__ __forceinline__ float lane_value(float v, int l) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
-// The best `top` (value, column) pairs seen by a wave, best first, lane i
-// holding the i-th; equal values keep the lower column first because columns
-// come in ascending order.  floor: no smaller or equal value can enter.
+// The best `top` (value, column) pairs seen by a wave, best first (larger
+// value, then lower column), lane i holding the i-th.  A value at or below
+// `floor` cannot enter from a later column.
 struct TopList {
   float v = neg_inf();
   int id = -1;
   float floor = neg_inf();
-  __device__ __forceinline__ void insert(float x, int col, int top) {
-    const int pos = popc64(wave_ballot(v >= x));
-    if (pos >= top) return;
-    const float uv = __shfl_up(v, 1, kWave);
-    const int ui = __shfl_up(id, 1, kWave);
-    const int lane = lane_id();
-    v = lane == pos ? x : lane > pos ? uv : v;
-    id = lane == pos ? col : lane > pos ? ui : id;
-    floor = fmaxf(floor, lane_value(v, top - 1));
-  }
 };
+
+// Scratch of the list: packed candidates, and entries on their way to their
+// places.
+struct TopScratch {
+  float v[kWave];
+  int id[kWave];
+  float cand[kLpCand];
+  int cand_id[kLpCand];
+};
+
+// Joins the candidates (x, col) of lanes [0, n) into the list; a lane without
+// one holds x = -inf.  Per candidate, one comparison against the other
+// candidates and (unless the list is empty, as for a wave's first batch) one
+// against the list give every entry its new place, four candidates a step so
+// that their latencies overlap; the entries then pass through LDS to their
+// lanes.
+__device__ __forceinline__ void merge_top(int n, float x, int col, int top, TopList& list,
+                                          TopScratch& sc) {
+  const int lane = lane_id();
+  if (lane >= n) x = neg_inf();
+  int place = lane, rank = 0;  // of this lane's list entry, of this lane's candidate
+  auto ahead_of = [](float ax, int ac, float bx, int bc) {
+    return ax > bx || (ax == bx && ac < bc);
+  };
+  const bool empty = __builtin_amdgcn_readlane(list.id, 0) < 0;
+  if (empty) {
+    for (int l0 = 0; l0 < n; l0 += 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        rank += ahead_of(lane_value(x, l0 + k), __builtin_amdgcn_readlane(col, l0 + k), x, col);
+    }
+  } else {
+    for (int l0 = 0; l0 < n; l0 += 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float cx = lane_value(x, l0 + k);
+        const int cc = __builtin_amdgcn_readlane(col, l0 + k);
+        rank += ahead_of(cx, cc, x, col);
+        const bool ahead = ahead_of(cx, cc, list.v, list.id);
+        place += ahead;
+        // the list entries this candidate is not ahead of come before it
+        const int before = popc64(wave_ballot(!ahead));
+        rank += lane == l0 + k ? before : 0;
+      }
+    }
+  }
+  const bool cand = x > neg_inf();
+  if (empty) sc.v[lane] = neg_inf(), sc.id[lane] = -1;
+  else if (place < kWave) sc.v[place] = list.v, sc.id[place] = list.id;
+  __builtin_amdgcn_wave_barrier();
+  if (cand && rank < kWave) sc.v[rank] = x, sc.id[rank] = col;
+  __builtin_amdgcn_wave_barrier();
+  list.v = sc.v[lane], list.id = sc.id[lane];
+  __builtin_amdgcn_wave_barrier();
+  list.floor = fmaxf(list.floor, lane_value(list.v, top - 1));
+}
 
 // The largest float below x (of an x that is not NaN).
 __device__ __forceinline__ float below(float x) {
@@ -113,77 +162,161 @@ __device__ __forceinline__ float below(float x) {
   return __uint_as_float(x > 0.f ? u - 1u : u + 1u);
 }
 
-// Takes the vectors' elements above the list's floor into the list; lane l's
-// vector u holds columns col0 + (u * 64 + l) * V.  A first batch sets the
-// floor from the lanes' maxima: `top` lanes hold a value of at least the
-// top-th largest of them.
-template <typename E, int U>
-__device__ __forceinline__ void take_top(const uint4 (&q)[U], const float (&vmax)[U], float bmax,
-                                         int col0, int top, TopList& list) {
-  constexpr int V = 16 / sizeof(E);
-  if (list.floor == neg_inf()) {
-    const int lane = lane_id();
-    int rank = 0;
-    for (int k = 0; k < kWave; ++k) {
-      const float o = lane_value(bmax, k);
-      rank += o > bmax || (o == bmax && k < lane);
-    }
-    const uint64_t at = wave_ballot(rank == top - 1);
-    if (at != 0) list.floor = below(lane_value(bmax, __builtin_ctzll(at)));
+// A float that orders as the whole number it comes from, and back.
+__device__ __forceinline__ int order_of(float x) {
+  const int u = __float_as_int(x);
+  return u ^ ((u >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_order(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// A floor that leaves few of a set of which the lanes hold one element each:
+// just below a value that at least `top` of them reach, the largest such one
+// to within 2^-12 of their spread (-inf where fewer lanes hold one at all).
+__device__ __forceinline__ float floor_of(float x, int top) {
+  float hi = x, lo = x == neg_inf() ? -neg_inf() : x;
+  if (popc64(wave_ballot(x > neg_inf())) < top) return neg_inf();
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    hi = fmaxf(hi, __shfl_xor(hi, o, kWave));
+    lo = fminf(lo, __shfl_xor(lo, o, kWave));
   }
+  // [a, b): at least `top` lanes are at or above a
+  int64_t a = order_of(lo), b = static_cast<int64_t>(order_of(hi)) + 1;
+  const int key = order_of(x);
+#pragma unroll 1
+  for (int k = 0; k < 12 && b - a > 1; ++k) {
+    const int64_t mid = (a + b) >> 1;
+    if (popc64(wave_ballot(key >= static_cast<int>(mid) && x > neg_inf())) >= top) a = mid;
+    else b = mid;
+  }
+  return below(of_order(static_cast<int>(a)));
+}
+
+// Merges n packed candidates (n <= kLpCand), 64 at a time.
+__device__ __forceinline__ void merge_packed(int n, int top, TopList& list, TopScratch& sc) {
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int i = 0; i < n; i += kWave)
+    merge_top(min(n - i, kWave), sc.cand[i + lane_id()], sc.cand_id[i + lane_id()], top, list, sc);
+}
+
+// Inclusive sum over the lanes, by DPP.
+__device__ __forceinline__ int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast15, rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast31, rows 2 and 3
+  return v;
+}
+
+// Takes the batch's elements above the list's floor into the list; lane l's
+// vector u holds columns col0 + (u * 64 + l) * V.  Each lane marks its own, a
+// scan gives it their places, and it picks them from a copy of the batch in
+// LDS (registers cannot be indexed).  They are few once the list is warm
+// (about top * ln of the batches seen, in all).  Where they are many (the
+// first batch, a rising row) the floor is raised first, by the lanes' maxima.
+// Many equal values may still pass it; those go in 64 columns at a time.
+template <typename E, int U>
+__device__ __forceinline__ void take_top(const uint4 (&q)[U], float bmax, int col0, int top,
+                                         TopList& list, TopScratch& sc, E* stage) {
+  constexpr int V = 16 / sizeof(E);
   if (wave_ballot(bmax > list.floor) == 0) return;
+  const int lane = lane_id();
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    uint64_t lanes = wave_ballot(vmax[u] > list.floor);
-    while (lanes != 0) {
-      const int l = __builtin_ctzll(lanes);
-      lanes &= lanes - 1;
-      uint4 w;
-      w.x = __builtin_amdgcn_readlane(q[u].x, l), w.y = __builtin_amdgcn_readlane(q[u].y, l);
-      w.z = __builtin_amdgcn_readlane(q[u].z, l), w.w = __builtin_amdgcn_readlane(q[u].w, l);
+  for (int u = 0; u < U; ++u) reinterpret_cast<uint4*>(stage)[u * kWave + lane] = q[u];
+  bool raised = list.floor == neg_inf();
+  if (raised) list.floor = floor_of(bmax, top);
+  for (;;) {
+    const float floor = list.floor;
+    uint32_t mine = 0;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x = elem<E>(w, e);
-        if (x > list.floor) list.insert(x, col0 + (u * kWave + l) * V + e, top);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) mine |= elem<E>(q[u], e) > floor ? 1u << (u * V + e) : 0u;
+    const int end = lane_scan(__popc(mine));
+    const int n = __builtin_amdgcn_readlane(end, kWave - 1);
+    if (n <= (raised ? kLpCand : kWave)) {
+      int at = end - __popc(mine);
+      __builtin_amdgcn_wave_barrier();
+      for (; mine != 0; mine &= mine - 1, ++at) {
+        const int b = __builtin_ctz(mine);
+        const int i = (b / V * kWave + lane) * V + b % V;
+        sc.cand[at] = ElemTraits<E>::to_f32(stage[i]);
+        sc.cand_id[at] = col0 + i;
       }
+      merge_packed(n, top, list, sc);
+      return;
     }
+    if (raised) break;
+    raised = true;
+    list.floor = fmaxf(floor, floor_of(bmax, top));
+  }
+  const float floor = list.floor;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int i = 0; i < U * V; ++i) {
+    const float x = ElemTraits<E>::to_f32(stage[i * kWave + lane]);
+    if (wave_ballot(x > floor && x >= lane_value(list.v, top - 1)) != 0)
+      merge_top(kWave, x > floor ? x : neg_inf(), col0 + i * kWave + lane, top, list, sc);
   }
 }
 
 template <typename E, int U, bool TOP>
 __device__ __forceinline__ void take_batch(const uint4 (&q)[U], float c, int col0, int top,
-                                           SoftStat& a, TopList& list) {
+                                           SoftStat& a, TopList& list, TopScratch* sc, E* stage) {
   constexpr int V = 16 / sizeof(E);
-  float vmax[U], bmax = neg_inf();
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    vmax[u] = elem<E>(q[u], 0);
-#pragma unroll
-    for (int e = 1; e < V; ++e) vmax[u] = fmaxf(vmax[u], elem<E>(q[u], e));
-    bmax = fmaxf(bmax, vmax[u]);
-  }
-  if (bmax > a.m) a.raise(bmax, c);
+  float bmax = neg_inf();
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int e = 0; e < V; ++e) a.add(elem<E>(q[u], e), c);
-  if constexpr (TOP) take_top<E, U>(q, vmax, bmax, col0, top, list);
+    for (int e = 0; e < V; ++e) bmax = fmaxf(bmax, elem<E>(q[u], e));
+  if (bmax > a.m) a.raise(bmax, c);
+  // the batch's own sums first, one per vector: a lane's chain of additions to
+  // s and t is then one per batch, not one per element (error of the entropy
+  // over 131072 columns: 7e-8 against 9e-7, the same time)
+  float ps[U], pt[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    ps[u] = pt[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.term(elem<E>(q[u], e), c, ps[u], pt[u]);
+  }
+#pragma unroll
+  for (int u = 1; u < U; ++u) {
+    ps[0] += ps[u];
+    pt[0] += pt[u];
+  }
+  a.s += ps[0];
+  a.t += pt[0];
+  if constexpr (TOP) take_top<E, U>(q, bmax, col0, top, list, *sc, stage);
 }
 
+// A row's target, read before the row's reductions: whether there is one, and
+// its logit (lane 0's; the others do without).
+struct Target {
+  bool given = false;
+  float x = 0.f;
+  template <typename E, typename I>
+  __device__ __forceinline__ void load(const LogprobArgs& a, int64_t row) {
+    if (lane_id() != 0) return;
+    const int64_t t = static_cast<int64_t>(static_cast<const I*>(a.targets)[row]);
+    given = t >= 0 && t < a.vocab;
+    if (given) x = ElemTraits<E>::to_f32(static_cast<const E*>(a.logits)[row * a.stride + t]);
+  }
+};
+
 // The row's outputs from its joined statistics.
-template <typename E, typename I>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const SoftStat& st,
-                                          const TopList& list) {
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const Target& t,
+                                          const SoftStat& st, const TopList& list) {
   const int lane = lane_id();
-  const E* x = static_cast<const E*>(a.logits) + row * a.stride;
   const float ln_s = logf(st.s);
   const bool empty = st.s == 0.f;  // every place masked
   if (lane == 0) {
-    const int64_t t = static_cast<int64_t>(static_cast<const I*>(a.targets)[row]);
-    float logp = 0.f;
-    if (t >= 0 && t < a.vocab)
-      logp = empty ? neg_inf() : fmaf(ElemTraits<E>::to_f32(x[t]) - st.m, a.scale, -ln_s);
-    a.logp[row] = logp;
+    a.logp[row] = !t.given ? 0.f : empty ? neg_inf() : fmaf(t.x - st.m, a.scale, -ln_s);
     a.entropy[row] = empty ? 0.f : ln_s - kLn2 * (st.t / st.s);
     a.lse[row] = empty ? neg_inf() : fmaf(st.m, a.scale, ln_s);
   }
@@ -213,6 +346,10 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
   const int nv = (a.vocab - head) / V;
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
   const float c = a.scale * kLog2e;
+  __shared__ TopScratch scratch[TOP ? kLpWaves : 1];
+  __shared__ uint4 staged[TOP ? kLpWaves : 1][kLpLoads * kWave];
+  const int wave = TOP ? threadIdx.x / kWave : 0;
+  TopScratch* sc = scratch + wave;
   SoftStat st;
   TopList list;
   // at most V - 1 elements from column col0, one per lane
@@ -220,11 +357,10 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
     const float v = lane < n ? ElemTraits<E>::to_f32(x[col0 + lane]) : neg_inf();
     if (v > st.m) st.raise(v, c);
     st.add(v, c);
-    if constexpr (TOP)
-      for (int k = 0; k < n; ++k) {
-        const float w = lane_value(v, k);
-        if (w > list.floor) list.insert(w, col0 + k, a.top);
-      }
+    if constexpr (TOP) {
+      if (wave_ballot(v > list.floor) != 0)
+        merge_top(n, v > list.floor ? v : neg_inf(), col0 + lane, a.top, list, *sc);
+    }
   };
   if (part == 0 && head > 0) take_edge(0, head);
   const int end = min(nv, (part + 1) * per);
@@ -235,13 +371,16 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
       const int v = v0 + u * kWave + lane;
       q[u] = v < end ? body[v] : masked16<E>();
     }
-    take_batch<E, kLpLoads, TOP>(q, c, head + v0 * V, a.top, st, list);
+    take_batch<E, kLpLoads, TOP>(q, c, head + v0 * V, a.top, st, list, sc,
+                                  reinterpret_cast<E*>(staged[wave]));
   }
   const int tail0 = head + nv * V;
   if (part == splits - 1 && tail0 < a.vocab) take_edge(tail0, a.vocab - tail0);
+  Target target;
+  if (splits == 1) target.load<E, I>(a, row);
   st = join_lanes(st, c);
   if (splits == 1) {
-    write_row<E, I>(a, row, st, list);
+    write_row(a, row, target, st, list);
     return;
   }
   if (lane == 0) a.parts[item] = make_float4(st.m, st.s, st.t, 0.f);
@@ -251,44 +390,70 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
   }
 }
 
-// One wave per row joins its parts: lane l takes part l.  Parts hold ascending
-// columns, so equal values go to the lower part first.
+// One workgroup per row joins its parts: lane l takes part l's statistics.  The
+// parts' lists (best first) are cut at the floor that their best values give,
+// packed in any order, and merged by the first wave.
 template <typename E, typename I>
-__global__ __launch_bounds__(kWave) void logprob_join_kernel(const LogprobArgs a, int splits) {
-  __shared__ float vals[kLpMaxSplits * kLogprobMaxTop];
-  __shared__ int ids[kLpMaxSplits * kLogprobMaxTop];
-  const int lane = lane_id();
+__global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobArgs a,
+                                                                 int splits) {
+  __shared__ TopScratch sc;
+  __shared__ int n;
+  constexpr int kPer = kLpMaxSplits * kLogprobMaxTop / kLpThreads;
+  const int lane = lane_id(), tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   const float c = a.scale * kLog2e;
+  const float* vals = a.part_top + row * splits * a.top;
+  const int32_t* ids = a.part_ids + row * splits * a.top;
+  const int total = splits * a.top;
   SoftStat st;
+  TopList list;
+  Target target;
   if (lane < splits) {
     const float4 p = a.parts[row * splits + lane];
     st.m = p.x, st.s = p.y, st.t = p.z;
   }
-  st = join_lanes(st, c);
-  TopList list;
-  if (a.top > 0) {
-    for (int k = lane; k < splits * a.top; k += kWave) {
-      vals[k] = a.part_top[row * splits * a.top + k];
-      ids[k] = a.part_ids[row * splits * a.top + k];
+  if (tid < kWave) target.load<E, I>(a, row);
+  float floor = neg_inf();
+  if (total > 0) {
+    float x[kPer];
+    int col[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = k * kLpThreads + tid;
+      x[k] = i < total ? vals[i] : neg_inf();
+      col[k] = i < total ? ids[i] : -1;
+    }
+    // one element per lane: the first places of every part's list
+    const int place = lane / splits;
+    floor = floor_of(lane < total && place < a.top ? vals[lane % splits * a.top + place]
+                                                   : neg_inf(), a.top);
+    if (tid == 0) n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (!(x[k] > floor)) continue;
+      const int at = atomicAdd(&n, 1);
+      if (at < kLpCand) sc.cand[at] = x[k], sc.cand_id[at] = col[k];
     }
     __syncthreads();
-    int at = 0;
-    for (int k = 0; k < a.top; ++k) {
-      const bool have = lane < splits && at < a.top;
-      const float v = have ? vals[lane * a.top + at] : neg_inf();
-      float best = v;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) best = fmaxf(best, __shfl_xor(best, o, kWave));
-      if (best == neg_inf()) break;  // fewer places than asked for
-      const int l = __builtin_ctzll(wave_ballot(v == best));
-      const int id = have ? ids[lane * a.top + at] : -1;
-      const int got = __builtin_amdgcn_readlane(id, l);
-      if (lane == k) list.v = best, list.id = got;
-      if (lane == l) ++at;
+  }
+  if (tid >= kWave) return;
+  if (total > 0) {
+    const int count = n;
+    if (count <= kLpCand) {
+      merge_packed(count, a.top, list, sc);
+    } else {  // many equal values
+#pragma unroll 1
+      for (int i0 = 0; i0 < total; i0 += kWave) {
+        const int i = i0 + lane;
+        const float x = i < total ? vals[i] : neg_inf();
+        const int col = i < total ? ids[i] : -1;
+        if (wave_ballot(x > floor && x >= lane_value(list.v, a.top - 1)) != 0)
+          merge_top(kWave, x > floor ? x : neg_inf(), col, a.top, list, sc);
+      }
     }
   }
-  write_row<E, I>(a, row, st, list);
+  write_row(a, row, target, join_lanes(st, c), list);
 }
 
 // dlogits of one element: scale * (g * [j is the target] - p * (g + w * (log p + H))).
@@ -478,7 +643,7 @@ hipError_t launch_logprob_forward(const LogprobArgs& a, int elem_bytes, int inde
       logprob_forward_kernel<E, I, false><<<grid, kLpThreads, 0, s>>>(a, splits, per, items);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || splits == 1) return err;
-    logprob_join_kernel<E, I><<<static_cast<unsigned>(a.n_rows), kWave, 0, s>>>(a, splits);
+    logprob_join_kernel<E, I><<<static_cast<unsigned>(a.n_rows), kLpThreads, 0, s>>>(a, splits);
     return hipGetLastError();
   };
   if (elem_bytes == 2)
