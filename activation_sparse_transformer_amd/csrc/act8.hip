@@ -108,17 +108,23 @@ __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
   }
   // a power of two that keeps x * 127 and the quotient in the normal range
   const float up = a > 0x1p100f ? 0x1p-32f : a < 0x1p-90f ? 0x1p60f : 1.f;
-  const float den = a * up;
+  const float den = a * up, r = 1.f / den, k127 = 127.f * up;
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    w[j] = 0;
+    uint32_t u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float q = (f[4 * j + k] * up) * 127.f / den;
-      const int code = finite && top != 0 ? static_cast<int>(rintf(q)) : 0;
-      w[j] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * k);
+      // the quotient from the rounded reciprocal and one exact remainder: a
+      // product, a fused remainder and a correction instead of a division
+      const float t = f[4 * j + k] * k127;
+      const float q0 = t * r;
+      const float q = fmaf(fmaf(-q0, den, t), r, q0);
+      // 1.5 * 2^23 + q: the sum's last byte is q rounded to even
+      u[k] = __float_as_uint(q + 0x1.8p23f);
     }
+    const uint32_t lo = perm_b32(u[1], u[0], 0x0c0c0400u), hi = perm_b32(u[3], u[2], 0x0c0c0400u);
+    w[j] = finite && top != 0 ? lo | hi << 16 : 0u;
   }
   if (c < pitch)
     *reinterpret_cast<uint4*>(codes + row * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
