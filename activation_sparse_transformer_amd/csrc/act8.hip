@@ -8,6 +8,8 @@
 // real quotient, ties included.  A block of zeros has scale 0; a block that
 // holds a NaN or an infinity has scale NaN and codes 0, so that it reads back
 // as NaN instead of losing it.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -15,47 +17,41 @@ namespace twell {
 namespace {
 
 constexpr int kActThreads = 256;
-constexpr int kActCols = 16;                         // columns per lane
-constexpr int kActLanes = kAct8Block / kActCols;     // lanes per block of columns
-constexpr int kActUnits = kActThreads / kActLanes;   // blocks of columns per workgroup
 
-// Elements c .. c + 7 of a row as float32.
+// A lane takes one 16-byte vector of x: 8 (bf16) or 4 (float32) columns.
 template <typename E>
-__device__ __forceinline__ void load8(const E* p, float* f);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float* f) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+struct ActLane {
+  static constexpr int kCols = 16 / sizeof(E);
+  static constexpr int kLanes = kAct8Block / kCols;  // per block of columns
+  static constexpr int kWords = kCols / 4;           // 32-bit words of codes
+};
+
+template <typename E>
+__device__ __forceinline__ void widen(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* f) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(p)[i];
-    f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+    if constexpr (sizeof(E) == 2) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      f[i] = __uint_as_float(w[i]);
+    }
   }
 }
 
 template <typename E>
-__device__ __forceinline__ void store8(E* p, const float* f);
-template <>
-__device__ __forceinline__ void store8<uint16_t>(uint16_t* p, const float* f) {
+__device__ __forceinline__ uint4 narrow(const float* f) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = ElemTraits<uint16_t>::from_f32(f[2 * i]) |
-           static_cast<uint32_t>(ElemTraits<uint16_t>::from_f32(f[2 * i + 1])) << 16;
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 2)
+      w[i] = ElemTraits<E>::from_f32(f[2 * i]) |
+             static_cast<uint32_t>(ElemTraits<E>::from_f32(f[2 * i + 1])) << 16;
+    else
+      w[i] = __float_as_uint(f[i]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Unit (row, k) of the workgroup's units u0 + i: one 64-bit division per
@@ -67,37 +63,47 @@ __device__ __forceinline__ void unit_of(int64_t u0, int i, int per_row, int64_t&
   k = static_cast<int>(q % static_cast<uint32_t>(per_row));
 }
 
-// kActLanes lanes take one (row, block): the largest magnitude as an integer
-// (NaN bits exceed infinity's), then each lane's 16 codes.
+// The largest v of the group of P lanes (P = 16 or 32), in every lane of it:
+// quads, half rows and rows by DPP, the other row of a pair by a swap.
+template <int P>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  auto up = [&](auto ctrl) {
+    const int t = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), decltype(ctrl)::value, 0xf,
+                                              0xf, false);
+    v = max(v, static_cast<uint32_t>(t));
+  };
+  up(std::integral_constant<int, 0xb1>{});   // quad_perm [1, 0, 3, 2]
+  up(std::integral_constant<int, 0x4e>{});   // quad_perm [2, 3, 0, 1]
+  up(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  up(std::integral_constant<int, 0x140>{});  // row_mirror
+  if constexpr (P == 32)
+    v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16, kWave)));
+  return v;
+}
+
+// kLanes lanes take one (row, block): the largest magnitude as an integer
+// (NaN bits exceed infinity's), then each lane's codes.  Bound by HBM.
 template <typename E>
 __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
     const E* __restrict__ x, int64_t n_units, int d, int nb, int pitch,
     int8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int l = threadIdx.x % kActLanes;
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kActUnits;
-  const int i = threadIdx.x / kActLanes;
+  typedef ActLane<E> A;
+  constexpr int kUnits = kActThreads / A::kLanes;
+  const int l = threadIdx.x % A::kLanes;
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kUnits;
+  const int i = threadIdx.x / A::kLanes;
   if (u0 + i >= n_units) return;
   int64_t row;
   int b;
   unit_of(u0, i, nb, row, b);
-  const int c = b * kAct8Block + l * kActCols;
-  const E* src = x + row * d + c;
-  float f[kActCols];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (c + 8 * h < d) {
-      load8<E>(src + 8 * h, f + 8 * h);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[8 * h + k] = 0.f;
-    }
-  }
+  const int c = b * kAct8Block + l * A::kCols;
+  float f[A::kCols];
+  widen<E>(c < d ? load_once(reinterpret_cast<const uint4*>(x + row * d + c))
+                 : make_uint4(0, 0, 0, 0), f);
   uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < kActCols; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 1; o < kActLanes; o <<= 1)
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o, kWave)));
+  for (int k = 0; k < A::kCols; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
+  top = group_max<A::kLanes>(top);
   const float a = __uint_as_float(top);
   const bool finite = top < 0x7f800000u;
   if (l == 0) {
@@ -109,9 +115,9 @@ __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
   // a power of two that keeps x * 127 and the quotient in the normal range
   const float up = a > 0x1p100f ? 0x1p-32f : a < 0x1p-90f ? 0x1p60f : 1.f;
   const float den = a * up, r = 1.f / den, k127 = 127.f * up;
-  uint32_t w[4];
+  uint32_t w[A::kWords];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < A::kWords; ++j) {
     uint32_t u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -126,31 +132,59 @@ __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
     const uint32_t lo = perm_b32(u[1], u[0], 0x0c0c0400u), hi = perm_b32(u[3], u[2], 0x0c0c0400u);
     w[j] = finite && top != 0 ? lo | hi << 16 : 0u;
   }
-  if (c < pitch)
-    *reinterpret_cast<uint4*>(codes + row * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (c >= pitch) return;
+  if constexpr (A::kWords == 2)
+    *reinterpret_cast<uint2*>(codes + row * pitch + c) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(codes + row * pitch + c) = w[0];
 }
 
-// One lane takes 16 codes of one row.
+// One lane makes one 16-byte vector of x.  Bound by HBM.
 template <typename E>
 __global__ __launch_bounds__(kActThreads) void act8_unpack_kernel(
     const int8_t* __restrict__ codes, const float* __restrict__ scales, int64_t n_units, int d,
     int nb, int pitch, E* __restrict__ x) {
+  typedef ActLane<E> A;
   const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kActThreads;
   if (u0 + threadIdx.x >= n_units) return;
   int64_t row;
   int q;
-  unit_of(u0, threadIdx.x, pitch / kActCols, row, q);
-  const int c = q * kActCols;
-  const uint4 v = *reinterpret_cast<const uint4*>(codes + row * pitch + c);
+  unit_of(u0, threadIdx.x, d / A::kCols, row, q);
+  const int c = q * A::kCols;
+  const int8_t* src = codes + row * pitch + c;
+  uint32_t w[2] = {};
+  if constexpr (A::kWords == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
   const float s = scales[row * nb + c / kAct8Block];
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float f[kActCols];
+  float f[A::kCols];
 #pragma unroll
-  for (int k = 0; k < kActCols; ++k)
+  for (int k = 0; k < A::kCols; ++k)
     f[k] = static_cast<float>(static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)))) * s;
-  E* dst = x + row * d + c;
-  store8<E>(dst, f);
-  if (c + 8 < d) store8<E>(dst + 8, f + 8);
+  store_once(x + row * d + c, narrow<E>(f));
+}
+
+template <typename E>
+hipError_t pack(int64_t n_rows, int d, const void* x, int8_t* codes, float* scales,
+                hipStream_t s) {
+  const int64_t units = n_rows * act8_blocks(d);
+  const int per = kActThreads / ActLane<E>::kLanes;
+  act8_pack_kernel<E><<<static_cast<unsigned>((units + per - 1) / per), kActThreads, 0, s>>>(
+      static_cast<const E*>(x), units, d, act8_blocks(d), act8_pitch(d), codes, scales);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t unpack(int64_t n_rows, int d, const int8_t* codes, const float* scales, void* x,
+                  hipStream_t s) {
+  const int64_t units = n_rows * (d / ActLane<E>::kCols);
+  act8_unpack_kernel<E>
+      <<<static_cast<unsigned>((units + kActThreads - 1) / kActThreads), kActThreads, 0, s>>>(
+          codes, scales, units, d, act8_blocks(d), act8_pitch(d), static_cast<E*>(x));
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -158,31 +192,15 @@ __global__ __launch_bounds__(kActThreads) void act8_unpack_kernel(
 hipError_t launch_act8_pack(int64_t n_rows, int d, int elem_bytes, const void* x, int8_t* codes,
                             float* scales, hipStream_t s) {
   if (n_rows == 0) return hipSuccess;
-  const int nb = act8_blocks(d), pitch = act8_pitch(d);
-  const int64_t units = n_rows * nb;
-  const unsigned grid = static_cast<unsigned>((units + kActUnits - 1) / kActUnits);
-  if (elem_bytes == 2)
-    act8_pack_kernel<uint16_t><<<grid, kActThreads, 0, s>>>(static_cast<const uint16_t*>(x), units,
-                                                            d, nb, pitch, codes, scales);
-  else
-    act8_pack_kernel<float><<<grid, kActThreads, 0, s>>>(static_cast<const float*>(x), units, d,
-                                                         nb, pitch, codes, scales);
-  return hipGetLastError();
+  return elem_bytes == 2 ? pack<uint16_t>(n_rows, d, x, codes, scales, s)
+                         : pack<float>(n_rows, d, x, codes, scales, s);
 }
 
 hipError_t launch_act8_unpack(int64_t n_rows, int d, int elem_bytes, const int8_t* codes,
                               const float* scales, void* x, hipStream_t s) {
   if (n_rows == 0) return hipSuccess;
-  const int nb = act8_blocks(d), pitch = act8_pitch(d);
-  const int64_t units = n_rows * (pitch / kActCols);
-  const unsigned grid = static_cast<unsigned>((units + kActThreads - 1) / kActThreads);
-  if (elem_bytes == 2)
-    act8_unpack_kernel<uint16_t><<<grid, kActThreads, 0, s>>>(codes, scales, units, d, nb, pitch,
-                                                              static_cast<uint16_t*>(x));
-  else
-    act8_unpack_kernel<float><<<grid, kActThreads, 0, s>>>(codes, scales, units, d, nb, pitch,
-                                                           static_cast<float*>(x));
-  return hipGetLastError();
+  return elem_bytes == 2 ? unpack<uint16_t>(n_rows, d, codes, scales, x, s)
+                         : unpack<float>(n_rows, d, codes, scales, x, s);
 }
 
 }  // namespace twell

@@ -15,7 +15,7 @@ namespace {
 constexpr int kEmbThreads = 256;
 constexpr int kEmbWaves = kEmbThreads / kWave;
 constexpr int kEmbLoads = 4;  // 16-byte vectors per lane of a lookup item
-constexpr unsigned kEmbMaxBlocks = 1u << 20;
+constexpr unsigned kEmbMaxBlocks = 1u << 23;  // below 2^32 lanes
 
 constexpr int kGradThreads = 1024;
 constexpr int kGradWaves = kGradThreads / kWave;
@@ -67,21 +67,20 @@ __device__ __forceinline__ uint4 scaled16(const uint4& v, float scale) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One wave per (token, chunk of kEmbLoads * 64 vectors).
+// One wave per (token, chunk of kEmbLoads * 64 vectors).  Bound by HBM: rows
+// that repeat come from the caches, the output is stored past them.
 template <typename E, typename I>
 __global__ __launch_bounds__(kEmbThreads) void embed_forward_kernel(
     const E* __restrict__ table, const I* __restrict__ tokens, int64_t n_items, int chunks, int d,
     int vocab, float scale, E* __restrict__ out) {
   constexpr int V = 16 / sizeof(E);
-  const int lane = lane_id();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kEmbWaves;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEmbWaves + threadIdx.x / kWave; i < n_items;
        i += stride) {
     const int64_t n = i / chunks;
-    const int c0 = static_cast<int>(i - n * chunks) * (kEmbLoads * kWave * V) + lane * V;
+    const int c0 = (static_cast<int>(i - n * chunks) * (kEmbLoads * kWave) + lane_id()) * V;
     const int id = token_id(tokens, n, vocab);
     const E* src = table + static_cast<int64_t>(max(id, 0)) * d;
-    E* dst = out + n * d;
     uint4 v[kEmbLoads];
 #pragma unroll
     for (int k = 0; k < kEmbLoads; ++k) {
@@ -92,8 +91,7 @@ __global__ __launch_bounds__(kEmbThreads) void embed_forward_kernel(
     for (int k = 0; k < kEmbLoads; ++k) {
       const int c = c0 + k * kWave * V;
       if (c < d)
-        *reinterpret_cast<uint4*>(dst + c) =
-            id >= 0 ? scaled16<E>(v[k], scale) : make_uint4(0, 0, 0, 0);
+        store_once(out + n * d + c, id >= 0 ? scaled16<E>(v[k], scale) : make_uint4(0, 0, 0, 0));
     }
   }
 }
@@ -118,31 +116,26 @@ __global__ __launch_bounds__(kEmbThreads) void embed_count_kernel(const I* __res
   }
 }
 
-// Zero the rows of dtable in [r0, r1) whose id no token has: wave w of n_waves.
-__device__ __forceinline__ void zero_unused(const int32_t* __restrict__ count, int64_t r0,
-                                            int64_t r1, int d, float* __restrict__ dtable,
-                                            int64_t w, int64_t n_waves) {
-  for (int64_t r = r0 + w; r < r1; r += n_waves) {
-    if (count[r] != 0) continue;
-    float* row = dtable + r * d;
-    for (int c = lane_id() * 4; c < d; c += kWave * 4)
-      *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+// Zero vector v (4 floats) of dtable unless its row's id has a token: one
+// vector per lane and workgroups in the order of memory.
+__device__ __forceinline__ void zero_unused(const int32_t* __restrict__ count, int64_t v,
+                                            int64_t end, int d, float* __restrict__ dtable) {
+  if (v >= end || count[v / (d / 4)] != 0) return;
+  store_once(dtable + v * 4, make_uint4(0, 0, 0, 0));
 }
 
 // Workgroups below n_alloc: each id's first place (base), and the lists of the
 // ids with at most kShort tokens and of those with more, from the counts.
 // Segments and list entries are handed out with one atomic per workgroup, so
-// their order varies; no result depends on it.  The others zero the first
-// half of the unused rows meanwhile.
+// their order varies; no result depends on it.  The others zero the unused
+// rows' vectors below `half` meanwhile.
 __global__ __launch_bounds__(kGradThreads) void embed_alloc_kernel(
     const EmbedGradBufs b, int vocab, int n_alloc, int d, int64_t half,
     float* __restrict__ dtable) {
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   if (static_cast<int>(blockIdx.x) >= n_alloc) {
-    zero_unused(b.count, 0, half, d, dtable,
-                static_cast<int64_t>(blockIdx.x - n_alloc) * kGradWaves + wave,
-                static_cast<int64_t>(gridDim.x - n_alloc) * kGradWaves);
+    zero_unused(b.count, static_cast<int64_t>(blockIdx.x - n_alloc) * kGradThreads + tid, half, d,
+                dtable);
     return;
   }
   __shared__ int tot[3][kGradWaves];
@@ -191,15 +184,15 @@ __global__ __launch_bounds__(kGradThreads) void embed_alloc_kernel(
 }
 
 // Workgroups below n_place put the token numbers in their segments; the others
-// zero the second half of the unused rows.
+// zero the unused rows' vectors from `half` on.
 template <typename I>
 __global__ __launch_bounds__(kGradThreads) void embed_place_kernel(
     const EmbedGradBufs b, const I* __restrict__ tokens, int64_t n_tokens, int vocab, int n_place,
     int d, int64_t half, float* __restrict__ dtable) {
   if (static_cast<int>(blockIdx.x) >= n_place) {
-    zero_unused(b.count, half, vocab, d, dtable,
-                static_cast<int64_t>(blockIdx.x - n_place) * kGradWaves + threadIdx.x / kWave,
-                static_cast<int64_t>(gridDim.x - n_place) * kGradWaves);
+    zero_unused(b.count,
+                half + static_cast<int64_t>(blockIdx.x - n_place) * kGradThreads + threadIdx.x,
+                static_cast<int64_t>(vocab) * (d / 4), d, dtable);
     return;
   }
   for (int64_t n = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x; n < n_tokens;
@@ -400,8 +393,8 @@ hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, in
     embed_count_kernel<<<cgrid, kEmbThreads, 0, s>>>(static_cast<const int32_t*>(tokens), n, vocab,
                                                      b.count, b.pos);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t half = vocab / 2;
-  const unsigned fill = blocks_for(half + 1, kGradWaves, 2048);
+  const int64_t vectors = static_cast<int64_t>(vocab) * (d / 4), half = vectors / 2;
+  const unsigned fill = static_cast<unsigned>((vectors - half + kGradThreads - 1) / kGradThreads);
   const unsigned n_alloc = blocks_for(vocab, kAllocIds, 1u << 30);
   embed_alloc_kernel<<<n_alloc + fill, kGradThreads, 0, s>>>(b, vocab, static_cast<int>(n_alloc),
                                                              d, half, dtable);

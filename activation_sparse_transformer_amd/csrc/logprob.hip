@@ -18,7 +18,9 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / kWave;
-constexpr int kLpLoads = 4;             // 16-byte vectors per lane and batch
+constexpr int kLpLoads = 4;             // 16-byte vectors per lane and batch (forward)
+constexpr int kLpGradLoads = 4;         // 16-byte vectors per lane and chunk (backward; 1: 118 us, 2: 104,
+                                        // 4: 102 for 4096 x 32768 bf16)
 constexpr int kLpWantWaves = 4096;      // waves that keep 256 CUs busy (1024 .. 16384 measured:
                                         // within 5% at 1000 and 2000 rows, 64 rows 40% slower at 1024)
 constexpr int kLpMinVectors = 128;      // vectors of a row that are worth a wave
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
 #pragma unroll
     for (int u = 0; u < kLpLoads; ++u) {
       const int v = v0 + u * kWave + lane;
-      q[u] = v < end ? body[v] : masked16<E>();
+      q[u] = v < end ? load_once(body + v) : masked16<E>();
     }
     take_batch<E, kLpLoads, TOP>(q, c, head + v0 * V, a.top, st, list, sc,
                                   reinterpret_cast<E*>(staged[wave]));
@@ -508,66 +510,76 @@ __device__ __forceinline__ uint4 pack16(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The chunk's elements of one row: kLpThreads * kLpLoads vectors (the row's
-// first chunk also the elements before its first vector, the last one those
-// after its last).  VEC: input and output rows share their alignment.
-template <typename E, bool ENT, bool VEC, bool FAR>
-__device__ __forceinline__ void grad_chunk(const E* x, E* out, const RowGrad& r, int vocab, int t,
-                                           int chunk, int chunks) {
-  constexpr int V = VEC ? 16 / sizeof(E) : 1;
+// One chunk of a row: kLpThreads * kLpGradLoads vectors, for the row's first
+// chunk also the elements before its first vector and for the last one those
+// after its last.  VEC: input and output rows share their alignment.
+template <typename E, bool VEC>
+struct GradChunk {
+  static constexpr int V = VEC ? 16 / sizeof(E) : 1;
   typedef ElemTraits<E> Tr;
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(E) % V);
-  const int head = min((V - off) % V, vocab);
-  const int nv = (vocab - head) / V;
-  auto one = [&](int j) {
-    out[j] = Tr::from_f32(r.template at<ENT, FAR>(Tr::to_f32(x[j]), j == t));
-  };
-  if (chunk == 0 && static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
-  const int tail0 = head + nv * V;
-  if (chunk == chunks - 1 && static_cast<int>(threadIdx.x) < vocab - tail0)
-    one(tail0 + threadIdx.x);
-  const int v0 = chunk * (kLpThreads * kLpLoads) + threadIdx.x;
-  if constexpr (!VEC) {
+  const E* x;
+  E* out;
+  int vocab, chunk, chunks, head, nv;
+  uint4 q[kLpGradLoads];
+  __device__ __forceinline__ GradChunk(const E* x_, E* out_, int vocab_, int chunk_, int chunks_)
+      : x(x_), out(out_), vocab(vocab_), chunk(chunk_), chunks(chunks_) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(E) % V);
+    head = min((V - off) % V, vocab);
+    nv = (vocab - head) / V;
+  }
+  __device__ __forceinline__ int at(int u) const {
+    return (chunk * kLpGradLoads + u) * kLpThreads + static_cast<int>(threadIdx.x);
+  }
+  __device__ __forceinline__ void load() {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < kLpLoads; ++u)
-      if (v0 + u * kLpThreads < nv) one(v0 + u * kLpThreads);
-  } else {
-    const uint4* body = reinterpret_cast<const uint4*>(x + head);
-    uint4* to = reinterpret_cast<uint4*>(out + head);
-    uint4 q[kLpLoads];
-#pragma unroll
-    for (int u = 0; u < kLpLoads; ++u) {
-      const int v = v0 + u * kLpThreads;
-      if (v < nv) q[u] = body[v];
-    }
-#pragma unroll
-    for (int u = 0; u < kLpLoads; ++u) {
-      const int v = v0 + u * kLpThreads;
-      if (v >= nv) continue;
-      float f[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        f[e] = r.template at<ENT, FAR>(elem<E>(q[u], e), head + v * V + e == t);
-      to[v] = pack16<E>(f);
+      for (int u = 0; u < kLpGradLoads; ++u)
+        if (at(u) < nv) q[u] = load_once(reinterpret_cast<const uint4*>(x + head) + at(u));
     }
   }
-}
+  template <bool ENT, bool FAR>
+  __device__ __forceinline__ void finish(const RowGrad& r, int t) const {
+    auto one = [&](int j) {
+      out[j] = Tr::from_f32(r.template at<ENT, FAR>(Tr::to_f32(x[j]), j == t));
+    };
+    if (chunk == 0 && static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
+    const int tail0 = head + nv * V;
+    if (chunk == chunks - 1 && static_cast<int>(threadIdx.x) < vocab - tail0)
+      one(tail0 + threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < kLpGradLoads; ++u) {
+      const int v = at(u);
+      if (v >= nv) continue;
+      if constexpr (!VEC) {
+        one(v);
+      } else {
+        float f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          f[e] = r.template at<ENT, FAR>(elem<E>(q[u], e), head + v * V + e == t);
+        store_once(reinterpret_cast<uint4*>(out + head) + v, pack16<E>(f));
+      }
+    }
+  }
+};
 
-// A workgroup takes one chunk of a row.  lse is rounded to float32, which
-// moves every p of the row by |lse| * 2^-24 of itself; past kFarLse (a row of
-// the type's lowest values, or logits far from zero) the row's own maximum and
-// sum are formed again instead.  dlogits may be the logits, where nothing may
-// be read again: the chunks of such a row would see each other's results, so
-// there one workgroup forms them and takes the row's chunks in turn.
+// A workgroup takes one chunk of a row; its logits are on their way before the
+// row's scalars are read.  lse is rounded to float32, which moves every p of
+// the row by |lse| * 2^-24 of itself; past kFarLse (a row of the type's lowest
+// values, or logits far from zero) the row's own maximum and sum are formed
+// again instead.  dlogits may be the logits, where the chunks of such a row
+// would see each other's results: there one workgroup forms the sums and takes
+// the row's chunks in turn.
 template <typename E, typename I, bool ENT, bool VEC>
 __global__ __launch_bounds__(kLpThreads) void logprob_backward_kernel(const LogprobGradArgs a,
                                                                      int chunks,
                                                                      int64_t n_items) {
   for (int64_t item = blockIdx.x; item < n_items; item += gridDim.x) {
     const int64_t row = item / chunks;
-    const int chunk = static_cast<int>(item - row * chunks);
     const E* x = static_cast<const E*>(a.logits) + row * a.stride;
     E* out = static_cast<E*>(a.dlogits) + row * a.out_stride;
+    GradChunk<E, VEC> c(x, out, a.vocab, static_cast<int>(item - row * chunks), chunks);
+    c.load();
     const int64_t t64 = static_cast<int64_t>(static_cast<const I*>(a.targets)[row]);
     const int t = t64 >= 0 && t64 < a.vocab ? static_cast<int>(t64) : -1;
     const float lse = a.lse[row];
@@ -575,23 +587,27 @@ __global__ __launch_bounds__(kLpThreads) void logprob_backward_kernel(const Logp
     r.m = 0.f;
     r.ln_s = lse;
     r.scale = a.scale;
-    r.g = t >= 0 ? a.dlogp[row] : 0.f;
+    r.g = a.dlogp[row];
+    if (t < 0) r.g = 0.f;
     r.w = ENT ? a.dentropy[row] : 0.f;
     r.h = ENT ? a.entropy[row] : 0.f;
     if (lse == neg_inf()) {  // every place masked: no gradient
       r.ln_s = -neg_inf();
       r.g = r.w = 0.f;
     } else if (fabsf(lse) > kFarLse) {
-      if (chunk != 0) continue;
+      if (c.chunk != 0) continue;
       const SoftStat st = block_stat<E>(x, a.vocab, a.scale * kLog2e);
       r.m = st.m;
       r.ln_s = logf(st.s);
       __syncthreads();  // every read of the row before its first write
-      for (int k = 0; k < chunks; ++k)
-        grad_chunk<E, ENT, VEC, true>(x, out, r, a.vocab, t, k, chunks);
+      for (int k = 0; k < chunks; ++k) {
+        GradChunk<E, VEC> ck(x, out, a.vocab, k, chunks);
+        ck.load();
+        ck.template finish<ENT, true>(r, t);
+      }
       continue;
     }
-    grad_chunk<E, ENT, VEC, false>(x, out, r, a.vocab, t, chunk, chunks);
+    c.template finish<ENT, false>(r, t);
   }
 }
 
@@ -656,7 +672,7 @@ hipError_t launch_logprob_backward(const LogprobGradArgs& a, int elem_bytes, int
   if (a.n_rows == 0) return hipSuccess;
   // rows of both arrays start at the same place within 16 bytes
   const bool vec = (a.stride - a.out_stride) * elem_bytes % 16 == 0;
-  const int per = kLpThreads * kLpLoads;
+  const int per = kLpThreads * kLpGradLoads;
   const int nv = vec ? a.vocab / (16 / elem_bytes) : a.vocab;
   const int chunks = nv < 1 ? 1 : (nv + per - 1) / per;
   const int64_t items = a.n_rows * chunks;
