@@ -17,14 +17,35 @@ constexpr int kEmbWaves = kEmbThreads / kWave;
 constexpr int kEmbLoads = 4;  // 16-byte vectors per lane of a lookup item
 constexpr unsigned kEmbMaxBlocks = 1u << 23;  // below 2^32 lanes
 
-constexpr int kGradThreads = 1024;
+constexpr int kGradThreads = 256;
 constexpr int kGradWaves = kGradThreads / kWave;
-constexpr int kAllocPer = 4;                         // ids per thread of the allocation
+constexpr int kAllocPer = 16;                        // ids per thread of the allocation
 constexpr int kAllocIds = kGradThreads * kAllocPer;  // ids per workgroup
-constexpr int kShort = kWave;                        // longest segment a wave takes
-constexpr int kWindow = 16384;                       // token numbers per bitmap
-constexpr int kLongLanes = 8;                        // lanes per row of a long segment
-constexpr int kLongStreams = kGradThreads / kLongLanes;
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderWaves = kOrderThreads / kWave;
+// The one-workgroup sort: at most kSortMax tokens, a token's number below its
+// id in one 32-bit key, kSortBits bits of it per pass.
+constexpr int kSortThreads = 512;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kSortNBits = 13;
+constexpr int kSortMax = 1 << kSortNBits;
+constexpr int kSortPer = kSortMax / kSortThreads;    // keys per lane
+constexpr int kSortBits = 6;
+constexpr int kSortBins = 1 << kSortBits;
+static_assert(kSortBins * kSortWaves == kSortThreads, "a thread per (bin, wave)");
+constexpr int kWindow = 1 << 19;                     // token numbers per bitmap (64 KB)
+// Segments by length: a wave takes one of at most kShort tokens row after row,
+// one of at most kMedium as 8 streams of rows (8 lanes a row), and a workgroup
+// any longer one as kLongStreams streams.
+constexpr int kShort = 8;
+constexpr int kMedium = kWave;
+constexpr int kStreamLanes = 8;
+constexpr int kWaveStreams = kWave / kStreamLanes;
+constexpr int kRowThreads = 256;
+constexpr int kRowWaves = kRowThreads / kWave;
+constexpr int kLongStreams = kRowThreads / kStreamLanes;
+constexpr int kRowBlocks = 8192;  // at most, of the rows' launch (2048: 50 us, 4096: 45, 8192: 43
+                                 // for 8192 tokens of 4096 float32)
 
 // The id of token n, or -1 where it is outside [0, vocab).
 template <typename I>
@@ -96,62 +117,75 @@ __global__ __launch_bounds__(kEmbThreads) void embed_forward_kernel(
   }
 }
 
-__global__ __launch_bounds__(kEmbThreads) void embed_clear_kernel(int32_t* __restrict__ p,
-                                                                  int64_t n) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEmbThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kEmbThreads)
-    p[i] = 0;
+// The table's gradient is mostly rows of zeros (ids no token has), and
+// zeroing them is most of the time: the launches that group the tokens carry
+// it, in workgroups past their own n_own, one 16-byte vector per lane in the
+// order of memory (a 32768 x 2048 table in 42 us, 6.3 TB/s; workgroups of 1024
+// lanes 47 us).  Before the counts are known (`count` null) a share also
+// zeroes used rows, which the last launch then overwrites.
+struct ZeroShare {
+  int64_t begin, end;    // vectors of dtable
+  const int32_t* count;  // skip the rows of used ids, or null
+};
+__device__ __forceinline__ void zero_share(const ZeroShare& z, int64_t block, int d,
+                                           float* __restrict__ dtable) {
+  const int64_t v = z.begin + block * blockDim.x + threadIdx.x;
+  if (v >= z.end || (z.count != nullptr && z.count[v / (d / 4)] != 0)) return;
+  store_once(dtable + v * 4, make_uint4(0, 0, 0, 0));
+}
+
+__global__ __launch_bounds__(kGradThreads) void embed_clear_kernel(int32_t* __restrict__ p,
+                                                                   int64_t n, int n_own,
+                                                                   ZeroShare z, int d,
+                                                                   float* __restrict__ dtable) {
+  if (static_cast<int>(blockIdx.x) >= n_own) {
+    zero_share(z, blockIdx.x - n_own, d, dtable);
+    return;
+  }
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+  if (i < n) p[i] = 0;
 }
 
 // count[id] = tokens of that id; pos[n] = a place of its own within the id.
 template <typename I>
-__global__ __launch_bounds__(kEmbThreads) void embed_count_kernel(const I* __restrict__ tokens,
-                                                                  int64_t n_tokens, int vocab,
-                                                                  int32_t* __restrict__ count,
-                                                                  int32_t* __restrict__ pos) {
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kEmbThreads + threadIdx.x; n < n_tokens;
-       n += static_cast<int64_t>(gridDim.x) * kEmbThreads) {
-    const int id = token_id(tokens, n, vocab);
-    if (id >= 0) pos[n] = atomicAdd(count + id, 1);
-  }
-}
-
-// Zero vector v (4 floats) of dtable unless its row's id has a token: one
-// vector per lane and workgroups in the order of memory.
-__device__ __forceinline__ void zero_unused(const int32_t* __restrict__ count, int64_t v,
-                                            int64_t end, int d, float* __restrict__ dtable) {
-  if (v >= end || count[v / (d / 4)] != 0) return;
-  store_once(dtable + v * 4, make_uint4(0, 0, 0, 0));
-}
-
-// Workgroups below n_alloc: each id's first place (base), and the lists of the
-// ids with at most kShort tokens and of those with more, from the counts.
-// Segments and list entries are handed out with one atomic per workgroup, so
-// their order varies; no result depends on it.  The others zero the unused
-// rows' vectors below `half` meanwhile.
-__global__ __launch_bounds__(kGradThreads) void embed_alloc_kernel(
-    const EmbedGradBufs b, int vocab, int n_alloc, int d, int64_t half,
-    float* __restrict__ dtable) {
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-  if (static_cast<int>(blockIdx.x) >= n_alloc) {
-    zero_unused(b.count, static_cast<int64_t>(blockIdx.x - n_alloc) * kGradThreads + tid, half, d,
-                dtable);
+__global__ __launch_bounds__(kGradThreads) void embed_count_kernel(
+    const I* __restrict__ tokens, int64_t n_tokens, int vocab, int32_t* __restrict__ count,
+    int32_t* __restrict__ pos, int n_own, ZeroShare z, int d, float* __restrict__ dtable) {
+  if (static_cast<int>(blockIdx.x) >= n_own) {
+    zero_share(z, blockIdx.x - n_own, d, dtable);
     return;
   }
-  __shared__ int tot[3][kGradWaves];
-  __shared__ int first[3];
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+  if (n >= n_tokens) return;
+  const int id = token_id(tokens, n, vocab);
+  if (id >= 0) pos[n] = atomicAdd(count + id, 1);
+}
+
+// Each id's first place (base) and the lists of the short, medium and long
+// ids, from the counts.  Segments and list entries are handed out with one
+// atomic per workgroup, so their order varies; no result depends on it.
+__global__ __launch_bounds__(kGradThreads) void embed_alloc_kernel(
+    const EmbedGradBufs b, int vocab, int n_own, ZeroShare z, int d, float* __restrict__ dtable) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  if (static_cast<int>(blockIdx.x) >= n_own) {
+    zero_share(z, blockIdx.x - n_own, d, dtable);
+    return;
+  }
+  __shared__ int tot[4][kGradWaves];
+  __shared__ int first[4];
   const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kAllocIds + tid * kAllocPer;
-  int c[kAllocPer], mine[3] = {0, 0, 0};
+  int c[kAllocPer], mine[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int k = 0; k < kAllocPer; ++k) {
     c[k] = v0 + k < vocab ? b.count[v0 + k] : 0;
     mine[0] += c[k];
     mine[1] += c[k] > 0 && c[k] <= kShort;
-    mine[2] += c[k] > kShort;
+    mine[2] += c[k] > kShort && c[k] <= kMedium;
+    mine[3] += c[k] > kMedium;
   }
-  int at[3];
+  int at[4];
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
+  for (int q = 0; q < 4; ++q) {
     int sc = mine[q];
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
@@ -162,52 +196,220 @@ __global__ __launch_bounds__(kGradThreads) void embed_alloc_kernel(
     at[q] = sc - mine[q];
   }
   __syncthreads();
-  if (tid < 3) {
+  if (tid < 4) {
     int all = 0;
     for (int w = 0; w < kGradWaves; ++w) all += tot[tid][w];
     first[tid] = all > 0 ? atomicAdd(b.counters + tid, all) : 0;
   }
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
+  for (int q = 0; q < 4; ++q) {
     at[q] += first[q];
     for (int w = 0; w < wave; ++w) at[q] += tot[q][w];
   }
 #pragma unroll
   for (int k = 0; k < kAllocPer; ++k) {
     if (c[k] == 0) continue;
-    b.base[v0 + k] = at[0];
+    const int32_t id = static_cast<int32_t>(v0 + k);
+    b.base[id] = at[0];
+    const int4 seg = make_int4(id, at[0], c[k], 0);
     at[0] += c[k];
-    if (c[k] <= kShort) b.short_ids[at[1]++] = static_cast<int32_t>(v0 + k);
-    else b.long_ids[at[2]++] = static_cast<int32_t>(v0 + k);
+    if (c[k] <= kShort) b.short_segs[at[1]++] = seg;
+    else if (c[k] <= kMedium) b.medium_segs[at[2]++] = seg;
+    else b.long_segs[at[3]++] = seg;
   }
 }
 
-// Workgroups below n_place put the token numbers in their segments; the others
-// zero the unused rows' vectors from `half` on.
+// The token numbers into their segments.
 template <typename I>
 __global__ __launch_bounds__(kGradThreads) void embed_place_kernel(
-    const EmbedGradBufs b, const I* __restrict__ tokens, int64_t n_tokens, int vocab, int n_place,
-    int d, int64_t half, float* __restrict__ dtable) {
-  if (static_cast<int>(blockIdx.x) >= n_place) {
-    zero_unused(b.count,
-                half + static_cast<int64_t>(blockIdx.x - n_place) * kGradThreads + threadIdx.x,
-                static_cast<int64_t>(vocab) * (d / 4), d, dtable);
+    const EmbedGradBufs b, const I* __restrict__ tokens, int64_t n_tokens, int vocab, int n_own,
+    ZeroShare z, int d, float* __restrict__ dtable) {
+  if (static_cast<int>(blockIdx.x) >= n_own) {
+    zero_share(z, blockIdx.x - n_own, d, dtable);
     return;
   }
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x; n < n_tokens;
-       n += static_cast<int64_t>(n_place) * kGradThreads) {
-    const int id = token_id(tokens, n, vocab);
-    if (id >= 0) b.perm[b.base[id] + b.pos[n]] = static_cast<int32_t>(n);
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+  if (n >= n_tokens) return;
+  const int id = token_id(tokens, n, vocab);
+  if (id >= 0) b.perm[b.base[id] + b.pos[n]] = static_cast<int32_t>(n);
+}
+
+// The token numbers of each long segment in ascending order, into `sorted`
+// (where the places were): a workgroup sets them in a bitmap of kWindow token
+// numbers (order-free), numbers its bits by a scan and lists them.
+__global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
+    const EmbedGradBufs b, int64_t n_tokens) {
+  __shared__ uint32_t bits[kWindow / 32];
+  __shared__ int wave_tot[kOrderWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int n_long = b.counters[3];
+  for (int i = blockIdx.x; i < n_long; i += gridDim.x) {
+    const int4 seg = b.long_segs[i];
+    int32_t* out = b.pos + seg.y;
+    for (int64_t w0 = 0; w0 < n_tokens; w0 += kWindow) {
+      const int words = static_cast<int>((min(n_tokens - w0, int64_t{kWindow}) + 31) / 32);
+      const int per = (words + kOrderThreads - 1) / kOrderThreads;  // words per thread
+      for (int k = tid; k < words; k += kOrderThreads) bits[k] = 0;
+      __syncthreads();
+      for (int k = tid; k < seg.z; k += kOrderThreads) {
+        const int64_t o = b.perm[seg.y + k] - w0;
+        if (o >= 0 && o < kWindow) atomicOr(bits + o / 32, 1u << (o % 32));
+      }
+      __syncthreads();
+      int pc = 0;
+      for (int k = tid * per; k < min((tid + 1) * per, words); ++k) pc += __popc(bits[k]);
+      int sc = pc;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int u = __shfl_up(sc, o, kWave);
+        if (lane >= o) sc += u;
+      }
+      if (lane == kWave - 1) wave_tot[wave] = sc;
+      __syncthreads();
+      int at = sc - pc, all = 0;
+      for (int w = 0; w < kOrderWaves; ++w) {
+        at += w < wave ? wave_tot[w] : 0;
+        all += wave_tot[w];
+      }
+      for (int k = tid * per; k < min((tid + 1) * per, words); ++k)
+        for (uint32_t m = bits[k]; m != 0; m &= m - 1)
+          out[at++] = static_cast<int32_t>(w0 + k * 32 + __builtin_ctz(m));
+      out += all;
+      __syncthreads();  // the next window rewrites bits and wave_tot
+    }
   }
 }
 
-// acc += rows ranks r, r + step, ... below cnt of the list, columns c..c + V.
-template <typename E, typename Row>
+// Up to kSortMax tokens are grouped by one workgroup, in one launch that zeroes
+// the whole table meanwhile: a stable radix sort of the keys (id, token number)
+// by id, then the segments between changes of id.  Key i = wave * chunk +
+// round * 64 + lane keeps the tokens' order; a pass ranks a wave's keys of equal
+// digit by ballots and a running count, numbers (digit, wave) by a scan, and
+// moves the keys through LDS.
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
+    const EmbedGradBufs b, const I* __restrict__ tokens, int n_tokens, int vocab, int id_bits,
+    ZeroShare z, int d, float* __restrict__ dtable) {
+  __shared__ uint32_t keys[kSortMax];
+  __shared__ int cnt[kSortWaves][kSortBins];
+  __shared__ int wave_tot[kSortWaves];
+  __shared__ int lists[4];
+  if (blockIdx.x > 0) {
+    zero_share(z, blockIdx.x - 1, d, dtable);
+    return;
+  }
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int rounds = (n_tokens + kSortThreads - 1) / kSortThreads;
+  const int chunk = rounds * kWave, total = rounds * kSortThreads;
+  // exclusive sum over the workgroup's threads
+  auto block_scan = [&](int v) {
+    int sc = v;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int u = __shfl_up(sc, o, kWave);
+      if (lane >= o) sc += u;
+    }
+    if (lane == kWave - 1) wave_tot[wave] = sc;
+    __syncthreads();
+    int at = sc - v;
+    for (int w = 0; w < wave; ++w) at += wave_tot[w];
+    __syncthreads();
+    return at;
+  };
+  uint32_t key[kSortPer];
+#pragma unroll
+  for (int r = 0; r < kSortPer; ++r) {
+    if (r >= rounds) break;
+    const int n = wave * chunk + r * kWave + lane;
+    const int id = n < n_tokens ? token_id(tokens, n, vocab) : -1;
+    // padding sorts behind the last id
+    key[r] = static_cast<uint32_t>(id >= 0 ? id : vocab) << kSortNBits |
+             static_cast<uint32_t>(n & (kSortMax - 1));
+  }
+  for (int bit = 0; bit < id_bits; bit += kSortBits) {
+    const int shift = kSortNBits + bit;
+    cnt[wave][lane] = 0;
+    __builtin_amdgcn_wave_barrier();
+    int rank[kSortPer];
+#pragma unroll
+    for (int r = 0; r < kSortPer; ++r) {
+      if (r >= rounds) break;
+      const int bin = key[r] >> shift & (kSortBins - 1);
+      uint64_t same = ~0ull;
+#pragma unroll
+      for (int k = 0; k < kSortBits; ++k) {
+        const bool set = (bin >> k & 1) != 0;
+        const uint64_t m = wave_ballot(set);
+        same &= set ? m : ~m;
+      }
+      const int before = cnt[wave][bin], below = popc_below(same);
+      rank[r] = before + below;
+      __builtin_amdgcn_wave_barrier();
+      if (below == 0) cnt[wave][bin] = before + popc64(same);
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    const int mine = cnt[tid % kSortWaves][tid / kSortWaves];
+    const int first = block_scan(mine);
+    cnt[tid % kSortWaves][tid / kSortWaves] = first;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortPer; ++r) {
+      if (r >= rounds) break;
+      keys[cnt[wave][key[r] >> shift & (kSortBins - 1)] + rank[r]] = key[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortPer; ++r) {
+      if (r >= rounds) break;
+      key[r] = keys[wave * chunk + r * kWave + lane];
+    }
+    __syncthreads();
+  }
+  // keys again as they are (no pass: one id), then thread t takes keys
+  // [t * rounds, (t + 1) * rounds) for the segments
+#pragma unroll
+  for (int r = 0; r < kSortPer; ++r) {
+    if (r >= rounds) break;
+    const int i = wave * chunk + r * kWave + lane;
+    keys[i] = key[r];
+    if (i < n_tokens) b.perm[i] = static_cast<int32_t>(key[r] & (kSortMax - 1));
+  }
+  if (tid < 4) lists[tid] = 0;
+  __syncthreads();
+  auto head_at = [&](int i) {
+    return i == 0 || keys[i] >> kSortNBits != keys[i - 1] >> kSortNBits;
+  };
+  int heads = 0;
+  for (int i = tid * rounds; i < (tid + 1) * rounds; ++i) heads += head_at(i);
+  int at = block_scan(heads);
+  // b.pos: where each segment starts, and the end
+  for (int i = tid * rounds; i < (tid + 1) * rounds; ++i)
+    if (head_at(i)) b.pos[at++] = i;
+  if (tid == kSortThreads - 1) b.pos[at] = total, lists[0] = at;
+  __threadfence_block();
+  __syncthreads();
+  const int n_segs = lists[0];
+  for (int k = tid; k < n_segs; k += kSortThreads) {
+    const int i = b.pos[k], c = b.pos[k + 1] - i;
+    const int id = static_cast<int>(keys[i] >> kSortNBits);
+    if (id >= vocab) continue;  // padding
+    const int4 seg = make_int4(id, i, c, 0);
+    if (c <= kShort) b.short_segs[atomicAdd(lists + 1, 1)] = seg;
+    else if (c <= kMedium) b.medium_segs[atomicAdd(lists + 2, 1)] = seg;
+    else b.long_segs[atomicAdd(lists + 3, 1)] = seg;
+  }
+  __syncthreads();
+  if (tid < 4) b.counters[tid] = lists[tid];
+}
+
+// acc += the rows of ranks r, r + step, ... below cnt, columns c .. c + V:
+// U rows in flight, added in rank order.
+template <typename E, int U, typename Row>
 __device__ __forceinline__ void add_rows(const E* __restrict__ dout, int d, int c, int r, int step,
                                          int cnt, Row row, float* acc) {
   constexpr int V = 16 / sizeof(E);
-  constexpr int U = 4;
   for (; r < cnt; r += U * step) {
     uint4 v[U];
 #pragma unroll
@@ -226,106 +428,140 @@ __device__ __forceinline__ void add_rows(const E* __restrict__ dout, int d, int 
   }
 }
 
-// The rows of the used ids.  Items [0, n_long * long_slices): a workgroup sums
-// one slice of kLongLanes * V columns of a long segment: per window of kWindow
-// token numbers it sets the segment's tokens in a bitmap (order-free), numbers
-// its bits by a scan, lists them in ascending order, and stream q of
-// kLongStreams adds the listed rows q, q + kLongStreams, ...; the streams'
-// sums are added in a fixed tree.  Then items of the short segments: a wave
-// sums one slice of 64 * V columns, its token numbers ranked in registers.
+// scale * acc to V columns of a row.
+template <int V>
+__device__ __forceinline__ void put_row(float* to, const float* acc, float scale) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    *reinterpret_cast<float4*>(to + i) = make_float4(acc[i] * scale, acc[i + 1] * scale,
+                                                     acc[i + 2] * scale, acc[i + 3] * scale);
+}
+
+// Token numbers of a segment of cnt <= 64, one per lane and in the order they
+// came, to ascending order: lane r gets the r-th smallest.
+__device__ __forceinline__ int sorted_segment(int mine, int cnt) {
+  const int lane = lane_id();
+  int rank = 0;
+  for (int k = 0; k < cnt; ++k) rank += __builtin_amdgcn_readlane(mine, k) < mine;
+  // lanes past the segment push to lanes past it
+  return __builtin_amdgcn_ds_permute((lane < cnt ? rank : lane) * 4, mine);
+}
+
+// The streams' sums, added over the lanes of a wave in a fixed order.
+template <int V>
+__device__ __forceinline__ void join_streams(float* acc) {
+#pragma unroll
+  for (int o = kStreamLanes; o < kWave; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], o, kWave);
+}
+
+// The rows of the used ids, as items (segment, slice of columns): a
+// workgroup's for long segments, whose streams' sums meet in LDS; a wave's for
+// medium and short ones, whose token numbers are ranked in registers.
+// Bound by the latency of dout's rows for few tokens and by HBM for many.
 template <typename E>
-__global__ __launch_bounds__(kGradThreads) void embed_rows_kernel(
-    const EmbedGradBufs b, const E* __restrict__ dout, int64_t n_tokens, int d, float scale,
-    float* __restrict__ dtable) {
+__global__ __launch_bounds__(kRowThreads) void embed_rows_kernel(
+    const EmbedGradBufs b, const int32_t* __restrict__ long_order, const E* __restrict__ dout,
+    int d, float scale, float* __restrict__ dtable) {
   constexpr int V = 16 / sizeof(E);
-  __shared__ uint32_t bits[kWindow / 32];
-  __shared__ uint16_t list[kWindow];
-  __shared__ int wave_tot[kGradWaves];
-  __shared__ float part[kGradWaves][kLongLanes * V];
+  constexpr int kStreamCols = kStreamLanes * V, kShortCols = kWave * V;
+  __shared__ float part[kRowWaves][kStreamCols];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-  const int long_slices = (d + kLongLanes * V - 1) / (kLongLanes * V);
-  const int64_t n_long = static_cast<int64_t>(b.counters[2]) * long_slices;
-  for (int64_t item = blockIdx.x; item < n_long; item += gridDim.x) {
-    const int id = b.long_ids[item / long_slices];
-    const int c = (static_cast<int>(item % long_slices) * kLongLanes + tid % kLongLanes) * V;
-    const int cc = min(c, d - V);
-    const int L = b.count[id];
-    const int32_t* seg = b.perm + b.base[id];
-    float acc[V];
+  float acc[V];
+  auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int64_t w0 = 0; w0 < n_tokens; w0 += kWindow) {
-      if (tid < kWindow / 32) bits[tid] = 0;
-      __syncthreads();
-      for (int k = tid; k < L; k += kGradThreads) {
-        const int64_t o = seg[k] - w0;
-        if (o >= 0 && o < kWindow) atomicOr(bits + o / 32, 1u << (o % 32));
-      }
-      __syncthreads();
-      uint32_t m = tid < kWindow / 32 ? bits[tid] : 0;
-      const int pc = __popc(m);
-      int sc = pc;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int u = __shfl_up(sc, o, kWave);
-        if (lane >= o) sc += u;
-      }
-      if (lane == kWave - 1) wave_tot[wave] = sc;
-      __syncthreads();
-      int at = sc - pc, cnt = 0;
-      for (int w = 0; w < kGradWaves; ++w) {
-        at += w < wave ? wave_tot[w] : 0;
-        cnt += wave_tot[w];
-      }
-      for (; m != 0; m &= m - 1) list[at++] = static_cast<uint16_t>(tid * 32 + __ffs(m) - 1);
-      __syncthreads();
-      add_rows<E>(dout, d, cc, tid / kLongLanes, kLongStreams, cnt,
-                  [&](int r) { return w0 + list[r]; }, acc);
-      __syncthreads();  // the next window rewrites bits and list
-    }
-#pragma unroll
-    for (int o = kLongLanes; o < kWave; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], o, kWave);
-    if (lane < kLongLanes)
+  };
+  const int stream_slices = (d + kStreamCols - 1) / kStreamCols;
+  const int64_t n_long = static_cast<int64_t>(b.counters[3]) * stream_slices;
+  for (int64_t item = blockIdx.x; item < n_long; item += gridDim.x) {
+    const int4 seg = b.long_segs[item / stream_slices];
+    const int c0 = static_cast<int>(item % stream_slices) * kStreamCols;
+    const int32_t* sorted = long_order + seg.y;
+    clear();
+    add_rows<E, 8>(dout, d, min(c0 + tid % kStreamLanes * V, d - V), tid / kStreamLanes,
+                   kLongStreams, seg.z, [&](int r) { return static_cast<int64_t>(sorted[r]); },
+                   acc);
+    join_streams<V>(acc);
+    if (lane < kStreamLanes)
 #pragma unroll
       for (int i = 0; i < V; ++i) part[wave][lane * V + i] = acc[i];
     __syncthreads();
-    const int col = static_cast<int>(item % long_slices) * kLongLanes * V + tid;
-    if (tid < kLongLanes * V && col < d) {
+    if (tid < kStreamCols && c0 + tid < d) {
       float s = 0.f;
-      for (int w = 0; w < kGradWaves; ++w) s += part[w][tid];
-      dtable[static_cast<int64_t>(id) * d + col] = s * scale;
+#pragma unroll
+      for (int w = 0; w < kRowWaves; ++w) s += part[w][tid];
+      dtable[static_cast<int64_t>(seg.x) * d + c0 + tid] = s * scale;
     }
     __syncthreads();
   }
-  const int slices = (d + kWave * V - 1) / (kWave * V);
-  const int64_t n_short = static_cast<int64_t>(b.counters[1]) * slices;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kGradWaves + wave; item < n_short;
-       item += static_cast<int64_t>(gridDim.x) * kGradWaves) {
-    const int id = b.short_ids[item / slices];
-    const int c = (static_cast<int>(item % slices) * kWave + lane) * V;
-    const int cc = min(c, d - V);
-    const int cnt = b.count[id];
-    const int32_t* seg = b.perm + b.base[id];
-    const int mine = seg[min(lane, cnt - 1)];
-    int rank = 0;
-    for (int k = 0; k < cnt; ++k) rank += __shfl(mine, k, kWave) < mine;
-    // lane r takes the token number of rank r (lanes past the segment push to
-    // lanes past it)
-    const int sorted = __builtin_amdgcn_ds_permute((lane < cnt ? rank : lane) * 4, mine);
-    float acc[V];
+  // a wave's items: (medium segment, slice), then (short segment, slice).  The
+  // next item's token numbers and the one after's segment are read while an
+  // item is summed, so the three dependent reads of an item do not add up.
+  const int64_t waves = static_cast<int64_t>(gridDim.x) * kRowWaves;
+  const int short_slices = (d + kShortCols - 1) / kShortCols;
+  const int64_t n_medium = static_cast<int64_t>(b.counters[2]) * stream_slices;
+  const int64_t n_items = n_medium + static_cast<int64_t>(b.counters[1]) * short_slices;
+  struct Item {
+    int4 seg = make_int4(0, 0, 0, 0);
+    int slice = 0;
+  };
+  auto item_at = [&](int64_t i) {
+    Item t;
+    if (i >= n_items) return t;
+    const bool medium = i < n_medium;
+    const int64_t k = medium ? i : i - n_medium;
+    const int slices = medium ? stream_slices : short_slices;
+    const int64_t q = k >> 32 ? k / slices : static_cast<uint32_t>(k) / static_cast<uint32_t>(slices);
+    t.seg = (medium ? b.medium_segs : b.short_segs)[q];
+    t.slice = static_cast<int>(k - q * slices);
+    return t;
+  };
+  auto tokens_of = [&](const Item& t) {
+    return t.seg.z > 0 ? b.perm[t.seg.y + min(lane, t.seg.z - 1)] : 0;
+  };
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kRowWaves + wave;
+  Item now = item_at(i), next = item_at(i + waves);
+  int tokens = tokens_of(now);
+  for (; i < n_items; i += waves) {
+    const int after = tokens_of(next);
+    const Item third = item_at(i + 2 * waves);
+    const int cnt = __builtin_amdgcn_readfirstlane(now.seg.z);
+    const int sorted = sorted_segment(tokens, cnt);
+    float* row = dtable + static_cast<int64_t>(now.seg.x) * d;
+    clear();
+    if (i < n_medium) {
+      const int c = (now.slice * kStreamLanes + lane % kStreamLanes) * V;
+      // every lane runs the same number of steps, for the shuffles
+      constexpr int U = 4;
+      for (int r0 = 0; r0 < cnt; r0 += U * kWaveStreams) {
+        uint4 v[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    add_rows<E>(dout, d, cc, 0, 1, cnt,
-                [&](int r) { return static_cast<int64_t>(__shfl(sorted, r, kWave)); }, acc);
-    if (c < d) {
-      float* row = dtable + static_cast<int64_t>(id) * d + c;
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * kWaveStreams + lane / kStreamLanes;
+          const int64_t n = __shfl(sorted, min(r, cnt - 1), kWave);
+          v[u] = *reinterpret_cast<const uint4*>(dout + n * d + min(c, d - V));
+        }
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        *reinterpret_cast<float4*>(row + i) = make_float4(
-            acc[i] * scale, acc[i + 1] * scale, acc[i + 2] * scale, acc[i + 3] * scale);
+        for (int u = 0; u < U; ++u) {
+          if (r0 + u * kWaveStreams + lane / kStreamLanes >= cnt) continue;
+          float f[V];
+          unpack16<E>(v[u], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] += f[e];
+        }
+      }
+      join_streams<V>(acc);
+      if (lane < kStreamLanes && c < d) put_row<V>(row + c, acc, scale);
+    } else {
+      const int c = (now.slice * kWave + lane) * V;
+      add_rows<E, kShort>(dout, d, min(c, d - V), 0, 1, cnt, [&](int r) {
+        return static_cast<int64_t>(__builtin_amdgcn_readlane(sorted, r));
+      }, acc);
+      if (c < d) put_row<V>(row + c, acc, scale);
     }
+    now = next, next = third, tokens = after;
   }
 }
 
@@ -349,10 +585,12 @@ EmbedGradBufs embed_grad_carve(int64_t n_tokens, int vocab, void* ws) {
   b.count = take(vocab);
   b.clear_ints = static_cast<int64_t>(off / 4);
   b.base = take(vocab);
-  b.pos = take(n_tokens);
+  b.pos = take(n_tokens + kSortThreads);  // the sort rounds its keys up
   b.perm = take(n_tokens);
-  b.short_ids = take(n_tokens < vocab ? n_tokens : vocab);
-  b.long_ids = take(n_tokens / (kShort + 1) + 1);
+  auto segs = [&](int64_t n) { return reinterpret_cast<int4*>(take(4 * n)); };
+  b.short_segs = segs(n_tokens < vocab ? n_tokens : vocab);
+  b.medium_segs = segs(n_tokens / (kShort + 1) + 1);
+  b.long_segs = segs(n_tokens / (kMedium + 1) + 1);
   b.bytes = off;
   return b;
 }
@@ -378,46 +616,90 @@ hipError_t launch_embed_forward(int64_t n, int vocab, int d, int elem_bytes, int
   return index_bytes == 8 ? go(float{}, int64_t{}) : go(float{}, int32_t{});
 }
 
+namespace {
+
+// The segments of the tokens and the zeroing, by the general sequence: the
+// counts, segments for the used ids, the tokens into them, the long segments
+// in order.
+template <typename I>
+hipError_t group_tokens(int64_t n, int vocab, int d, const I* ids, const EmbedGradBufs& b,
+                        float* dtable, hipStream_t s) {
+  // Shares of the zeroing per launch, about as long as each launch's own work
+  // takes.  With more tokens than ids most rows are used, and zeroing them
+  // early would be lost work.
+  const int64_t vectors = static_cast<int64_t>(vocab) * (d / 4);
+  const double early = n < vocab ? 1.0 : 0.0;
+  const double upto[4] = {0.2 * early, 0.5 * early, 0.75, 1.0};
+  ZeroShare z[4];
+  unsigned fill[4];
+  for (int k = 0; k < 4; ++k) {
+    z[k].begin = k == 0 ? 0 : z[k - 1].end;
+    z[k].end = k == 3 ? vectors : static_cast<int64_t>(upto[k] * static_cast<double>(vectors));
+    z[k].count = k < 2 ? nullptr : b.count;
+    fill[k] = static_cast<unsigned>((z[k].end - z[k].begin + kGradThreads - 1) / kGradThreads);
+  }
+  auto own = [](int64_t items, int per) { return static_cast<int>((items + per - 1) / per); };
+  hipError_t e;
+  const int clear = own(b.clear_ints, kGradThreads), each = own(n, kGradThreads),
+            alloc = own(vocab, kAllocIds);
+  embed_clear_kernel<<<clear + fill[0], kGradThreads, 0, s>>>(b.counters, b.clear_ints, clear, z[0],
+                                                              d, dtable);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (each + fill[1] > 0)
+    embed_count_kernel<<<each + fill[1], kGradThreads, 0, s>>>(ids, n, vocab, b.count, b.pos, each,
+                                                               z[1], d, dtable);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  embed_alloc_kernel<<<alloc + fill[2], kGradThreads, 0, s>>>(b, vocab, alloc, z[2], d, dtable);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (each + fill[3] > 0)
+    embed_place_kernel<<<each + fill[3], kGradThreads, 0, s>>>(b, ids, n, vocab, each, z[3], d,
+                                                               dtable);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (n > kMedium)
+    embed_order_kernel<<<blocks_for(n / (kMedium + 1), 1, 256), kOrderThreads, 0, s>>>(b, n);
+  return hipGetLastError();
+}
+
+// The same by one workgroup beside the zeroing of the whole table.
+template <typename I>
+hipError_t sort_tokens(int64_t n, int vocab, int d, const I* ids, const EmbedGradBufs& b,
+                       float* dtable, hipStream_t s) {
+  const int64_t vectors = static_cast<int64_t>(vocab) * (d / 4);
+  const ZeroShare z{0, vectors, nullptr};
+  const unsigned fill = static_cast<unsigned>((vectors + kSortThreads - 1) / kSortThreads);
+  int id_bits = 0;
+  while (vocab >> id_bits != 0) ++id_bits;  // ids 0 .. vocab (padding)
+  embed_sort_kernel<<<1 + fill, kSortThreads, 0, s>>>(b, ids, static_cast<int>(n), vocab, id_bits,
+                                                      z, d, dtable);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, int index_bytes,
                                  float scale, const void* dout, const void* tokens,
                                  const EmbedGradBufs& b, float* dtable, hipStream_t s) {
-  hipError_t e;
-  embed_clear_kernel<<<blocks_for(b.clear_ints, kEmbThreads, 2048), kEmbThreads, 0, s>>>(
-      b.counters, b.clear_ints);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const unsigned cgrid = blocks_for(n, kEmbThreads, 4096);
-  if (index_bytes == 8)
-    embed_count_kernel<<<cgrid, kEmbThreads, 0, s>>>(static_cast<const int64_t*>(tokens), n, vocab,
-                                                     b.count, b.pos);
-  else
-    embed_count_kernel<<<cgrid, kEmbThreads, 0, s>>>(static_cast<const int32_t*>(tokens), n, vocab,
-                                                     b.count, b.pos);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t vectors = static_cast<int64_t>(vocab) * (d / 4), half = vectors / 2;
-  const unsigned fill = static_cast<unsigned>((vectors - half + kGradThreads - 1) / kGradThreads);
-  const unsigned n_alloc = blocks_for(vocab, kAllocIds, 1u << 30);
-  embed_alloc_kernel<<<n_alloc + fill, kGradThreads, 0, s>>>(b, vocab, static_cast<int>(n_alloc),
-                                                             d, half, dtable);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const unsigned n_place = blocks_for(n, kGradThreads, 1024);
-  if (index_bytes == 8)
-    embed_place_kernel<<<n_place + fill, kGradThreads, 0, s>>>(
-        b, static_cast<const int64_t*>(tokens), n, vocab, static_cast<int>(n_place), d, half,
-        dtable);
-  else
-    embed_place_kernel<<<n_place + fill, kGradThreads, 0, s>>>(
-        b, static_cast<const int32_t*>(tokens), n, vocab, static_cast<int>(n_place), d, half,
-        dtable);
-  if ((e = hipGetLastError()) != hipSuccess || n == 0) return e;
+  // One workgroup sorts while the others zero the table, two launches in all,
+  // unless the tokens or ids exceed its keys or most rows are used anyway
+  // (zeroing them first would be lost work).
+  const bool sort = n <= kSortMax && n < vocab && vocab < 1 << (32 - kSortNBits);
+  auto group = [&](const auto* ids) {
+    return sort ? sort_tokens(n, vocab, d, ids, b, dtable, s)
+                : group_tokens(n, vocab, d, ids, b, dtable, s);
+  };
+  const hipError_t e = index_bytes == 8 ? group(static_cast<const int64_t*>(tokens))
+                                        : group(static_cast<const int32_t*>(tokens));
+  if (e != hipSuccess) return e;
+  const int32_t* long_order = sort ? b.perm : b.pos;
   const int V = 16 / elem_bytes;
   const int64_t items = (n < vocab ? n : vocab) * ((d + kWave * V - 1) / (kWave * V));
-  const unsigned grid = blocks_for(items, kGradWaves, 2048);
+  const unsigned grid = blocks_for(items, kRowWaves, kRowBlocks);
   if (elem_bytes == 2)
-    embed_rows_kernel<<<grid, kGradThreads, 0, s>>>(b, static_cast<const uint16_t*>(dout), n, d,
-                                                    scale, dtable);
+    embed_rows_kernel<<<grid, kRowThreads, 0, s>>>(b, long_order, static_cast<const uint16_t*>(dout),
+                                                   d, scale, dtable);
   else
-    embed_rows_kernel<<<grid, kGradThreads, 0, s>>>(b, static_cast<const float*>(dout), n, d,
-                                                    scale, dtable);
+    embed_rows_kernel<<<grid, kRowThreads, 0, s>>>(b, long_order, static_cast<const float*>(dout),
+                                                   d, scale, dtable);
   return hipGetLastError();
 }
 

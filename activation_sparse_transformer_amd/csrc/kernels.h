@@ -306,14 +306,17 @@ hipError_t launch_act8_unpack(int64_t n_rows, int d, int elem_bytes, const int8_
 // Token embedding: out = scale * table[tokens], and the table's gradient.
 // tokens are int32 or int64 (index_bytes 4 or 8).
 struct EmbedGradBufs {
-  int32_t* counters;   // [4] places handed out, short ids, long ids (cleared)
+  int32_t* counters;   // [4] places, short, medium and long ids handed out (cleared)
   int32_t* count;      // [vocab] tokens of each id (cleared)
   int64_t clear_ints;  // ints of counters + count, cleared together
   int32_t* base;       // [vocab] first place of each used id
-  int32_t* pos;        // [n] a token's place within its id
+  int32_t* pos;        // [n + 512] a token's place within its id, then the long ids' tokens in
+                       // order (the sort: where its segments start)
   int32_t* perm;       // [n] token numbers, by id
-  int32_t* short_ids;  // [min(n, vocab)] used ids with at most 64 tokens
-  int32_t* long_ids;   // [n / 65 + 1] ids with more
+  // used ids as {id, first place, tokens, 0}
+  int4* short_segs;    // [min(n, vocab)] of at most 8 tokens
+  int4* medium_segs;   // [n / 9 + 1] of at most 64
+  int4* long_segs;     // [n / 65 + 1] of more
   size_t bytes;        // total workspace bytes
 };
 EmbedGradBufs embed_grad_carve(int64_t n_tokens, int vocab, void* ws);

@@ -680,6 +680,9 @@ int check_embed(const twell_embed_shape* s) {
   if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
   if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
   if (!std::isfinite(s->scale)) return TWELL_ERR_INVALID_ARG;
+  // a launch holds fewer than 2^32 lanes, one per four columns of a share
+  if (static_cast<int64_t>(s->vocab) * s->d_model >= (int64_t{1} << 33))
+    return TWELL_ERR_UNSUPPORTED;
   return TWELL_OK;
 }
 

@@ -75,7 +75,13 @@ def run_grad(dout, t, vocab, scale):
     (4097, 4097, 64, "each", torch.int64),
     (40000, 1000, 64, "zipf", torch.int32),  # several windows of token numbers
     (40000, 5, 8, "same", torch.int64),
-    (200, 9000, 1032, "none", torch.int64)])
+    (200, 9000, 1032, "none", torch.int64),
+    (8192, 100000, 64, "zipf", torch.int32),   # the most tokens and ids that one workgroup sorts
+    (8193, 100000, 64, "zipf", torch.int64),
+    (700, (1 << 19) - 1, 8, "zipf", torch.int64),
+    (700, 1 << 19, 8, "zipf", torch.int64),
+    (600000, 700000, 8, "zipf", torch.int32),  # past one bitmap of token numbers
+    (513, 600, 16, "same", torch.int64)])
 def test_gradient_matches_oracle(n, vocab, d, kind, index, dtype):
     say(f"embed grad {dtype} n={n} vocab={vocab} d={d} {kind}")
     g = torch.Generator().manual_seed(n + d)
