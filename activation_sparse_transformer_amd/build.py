@@ -23,7 +23,7 @@ ARCH = "gfx950"
 
 SOURCES = ["twell_api.hip", "gemm_bf16.hip", "gemm_f32.hip", "route.hip", "spmm.hip", "skinny.hip",
            "ell.hip", "backward.hip", "gate.hip", "act8.hip",
-           "embed.hip", "logprob.hip"]
+           "backward_act8.hip", "embed.hip", "logprob.hip"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"--offload-arch={ARCH}",

@@ -470,125 +470,6 @@ __global__ __launch_bounds__(kBwdThreads) void bwd_slice_up_kernel(
   }
 }
 
-// Pass B from an 8-bit checkpoint: x[n][c] = code * scale of c's block of
-// kAct8Block columns.  A lane holds 16 columns of the slice per vector, all of
-// one block, so per entry the scale goes into the factor: dW_up^T[j] +=
-// (dz * scale) * code.  dz stays float32 here and in db; only the copy that
-// feeds dx is rounded to E.
-template <int P, int NVL, int U, bool CHECK>
-__device__ __forceinline__ void up8_step(int e0, int cnt, const int4& mine, float zmine,
-                                         const int8_t* __restrict__ codes,
-                                         const float* __restrict__ scales, int pitch, int nb,
-                                         const int (&col)[NVL], float* acc) {
-  constexpr int GPW = kWave / P;
-  const int grp = lane_id() / P;
-  float z[U][NVL];
-  uint4 xv[U][NVL];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = e0 + u * GPW + grp;
-    const int src = CHECK ? min(e, cnt - 1) : e;
-    const int64_t row = __shfl(mine.x, src, kWave);
-#pragma unroll
-    for (int v = 0; v < NVL; ++v) {
-      xv[u][v] = *reinterpret_cast<const uint4*>(codes + row * pitch + col[v]);
-      z[u][v] = scales[row * nb + col[v] / kAct8Block];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = e0 + u * GPW + grp;
-    const float dz = __shfl(zmine, CHECK ? min(e, cnt - 1) : e, kWave);
-    const bool live = !CHECK || e < cnt;
-#pragma unroll
-    for (int v = 0; v < NVL; ++v) {
-      // a lane past the entries adds nothing, whatever (NaN) scale it read
-      const float f = live ? dz * z[u][v] : 0.f;
-      const uint32_t w[4] = {xv[u][v].x, xv[u][v].y, xv[u][v].z, xv[u][v].w};
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        acc[v * 16 + i] = fmaf(
-            f, static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)))), acc[v * 16 + i]);
-    }
-  }
-}
-
-template <typename E, int P, int NVL>
-__global__ __launch_bounds__(kBwdThreads) void bwd_slice_up8_kernel(
-    const int32_t* __restrict__ offsets, const int4* __restrict__ ents,
-    const int8_t* __restrict__ codes, const float* __restrict__ scales, int pitch, int nb,
-    const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int S, int sw,
-    int64_t sparse_slots, E* __restrict__ dz_vals, E* __restrict__ dz_dense,
-    float* __restrict__ dw_up_t, float* __restrict__ db) {
-  constexpr int GPW = kWave / P;
-  constexpr int UP = GPW * NVL >= 8 ? 1 : 8 / (GPW * NVL);
-  const int lane = lane_id(), grp = lane / P, l = lane % P;
-  const int s = blockIdx.x % S;
-  const int j = (blockIdx.x / S) * kBwdWaves + threadIdx.x / kWave;
-  if (j >= dff) return;
-  const int cs = s * sw;
-  int col[NVL];
-  bool cok[NVL];
-#pragma unroll
-  for (int v = 0; v < NVL; ++v) {
-    const int c = (v * P + l) * 16;
-    cok[v] = c < sw;
-    col[v] = cs + (cok[v] ? c : 0);
-  }
-  float* out = dw_up_t + static_cast<int64_t>(j) * dm;
-  // a slice's last lane may hold only 8 columns (d_model is a multiple of 8)
-  auto store = [&](const float* acc) {
-#pragma unroll
-    for (int v = 0; v < NVL; ++v)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        if (cok[v] && (i < 8 || col[v] + 8 < dm))
-          *reinterpret_cast<float4*>(out + col[v] + i) =
-              acc == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f)
-                             : make_float4(acc[v * 16 + i], acc[v * 16 + i + 1],
-                                           acc[v * 16 + i + 2], acc[v * 16 + i + 3]);
-  };
-  const int b = offsets[j], L = offsets[j + 1] - b;
-  if (L == 0) {  // no entry: zero rows and bias
-    if (grp == 0) store(nullptr);
-    if (s == 0 && lane == 0) db[j] = 0.f;
-    return;
-  }
-  float acc[NVL * 16];
-#pragma unroll
-  for (int i = 0; i < NVL * 16; ++i) acc[i] = 0.f;
-  float sdz = 0.f;
-  for (int base = 0; base < L; base += kWave) {
-    const int cnt = min(kWave, L - base);
-    const int64_t me = b + base + min(lane, cnt - 1);
-    const int4 mine = ents[me];
-    float d = part[me];
-    for (int t = 1; t < n_part; ++t) d += part[t * pstride + me];
-    int e0 = 0;
-    for (; e0 + GPW * UP <= cnt; e0 += GPW * UP)
-      up8_step<P, NVL, UP, false>(e0, cnt, mine, d, codes, scales, pitch, nb, col, acc);
-    for (; e0 < cnt; e0 += GPW)
-      up8_step<P, NVL, 1, true>(e0, cnt, mine, d, codes, scales, pitch, nb, col, acc);
-    if (s == 0 && lane < cnt) {
-      const E dze = ElemTraits<E>::from_f32(d);
-      const int64_t slot = mine.z;
-      if (slot < sparse_slots) dz_vals[slot] = dze;
-      else dz_dense[slot - sparse_slots] = dze;
-      sdz += d;
-    }
-  }
-#pragma unroll
-  for (int o = P; o < kWave; o <<= 1)
-#pragma unroll
-    for (int i = 0; i < NVL * 16; ++i) acc[i] += __shfl_xor(acc[i], o, kWave);
-  if (grp == 0) store(acc);
-  if (s == 0) {
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) sdz += __shfl_xor(sdz, o, kWave);
-    if (lane == 0) db[j] = sdz;
-  }
-}
-
 unsigned grid_for(int64_t waves) {
   const int64_t blocks = (waves + kBwdWaves - 1) / kBwdWaves;
   return static_cast<unsigned>(blocks < 1 ? 1 : (blocks > kBwdMaxBlocks ? kBwdMaxBlocks : blocks));
@@ -627,51 +508,10 @@ SlicePlan bwd_slice_plan(int d_model, int elem_bytes) {
 
 namespace {
 
-// The same for 8-bit rows: a lane's vector is 16 columns, and a slice holds
-// whole vectors (its 16 columns then lie in one block of scales).
-SlicePlan act8_slice_plan(int d_model) {
-  SlicePlan p;
-  p.S = d_model % (8 * 16) == 0 ? 8 : 1;
-  p.sw = d_model / p.S;
-  const int vs = (p.sw + 15) / 16;
-  p.P = vs <= 8 ? 8 : vs <= 16 ? 16 : vs <= 32 ? 32 : kWave;
-  const int nvl = (vs + p.P - 1) / p.P;
-  p.nvl = nvl <= 2 ? nvl : 0;
-  return p;
-}
-
-template <typename E, int P, int NVL>
-hipError_t launch_slice_up8(const Geometry& g, const SlicePlan& sp, int n_part,
-                            const BwdWorkspace& w, const BwdAct8& x8, float* dw_up_t, float* db,
-                            hipStream_t s) {
-  const unsigned blocks =
-      static_cast<unsigned>((g.d_ff + kBwdWaves - 1) / kBwdWaves) * static_cast<unsigned>(sp.S);
-  bwd_slice_up8_kernel<E, P, NVL><<<blocks, kBwdThreads, 0, s>>>(
-      w.offsets, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model), act8_blocks(g.d_model),
-      w.part_dz, w.part_stride, n_part, g.d_ff, g.d_model, sp.S, sp.sw,
-      g.n_rows * g.n_tiles * g.capacity, static_cast<E*>(w.dz_vals), static_cast<E*>(w.dz_dense),
-      dw_up_t, db);
-  return hipGetLastError();
-}
-
-template <typename E>
-hipError_t launch_up8(const Geometry& g, int n_part, const BwdWorkspace& w, const BwdAct8& x8,
-                      float* dw_up_t, float* db, hipStream_t s) {
-  const SlicePlan sp = act8_slice_plan(g.d_model);
-  switch (sp.P * 8 + sp.nvl) {
-    case 8 * 8 + 1: return launch_slice_up8<E, 8, 1>(g, sp, n_part, w, x8, dw_up_t, db, s);
-    case 16 * 8 + 1: return launch_slice_up8<E, 16, 1>(g, sp, n_part, w, x8, dw_up_t, db, s);
-    case 32 * 8 + 1: return launch_slice_up8<E, 32, 1>(g, sp, n_part, w, x8, dw_up_t, db, s);
-    case 64 * 8 + 1: return launch_slice_up8<E, 64, 1>(g, sp, n_part, w, x8, dw_up_t, db, s);
-    case 64 * 8 + 2: return launch_slice_up8<E, 64, 2>(g, sp, n_part, w, x8, dw_up_t, db, s);
-    default: return hipErrorInvalidValue;
-  }
-}
-
 template <typename E, int P, int NVL>
 hipError_t launch_slices(const Geometry& g, const SlicePlan& sp, const BwdWorkspace& w,
-                         const void* x, const BwdAct8* x8, const void* dy, const void* w_down,
-                         float* dw_up_t, float* db, float* dw_down, hipStream_t s) {
+                         const void* x, const void* dy, const void* w_down, float* dw_up_t,
+                         float* db, float* dw_down, hipStream_t s) {
   const unsigned blocks =
       static_cast<unsigned>((g.d_ff + kBwdWaves - 1) / kBwdWaves) * static_cast<unsigned>(sp.S);
   bwd_slice_down_kernel<E, P, NVL><<<blocks, kBwdThreads, 0, s>>>(
@@ -679,7 +519,6 @@ hipError_t launch_slices(const Geometry& g, const SlicePlan& sp, const BwdWorksp
       g.d_model, sp.S, sp.sw, w.part_dz, w.part_stride, dw_down);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (x8 != nullptr) return launch_up8<E>(g, sp.S, w, *x8, dw_up_t, db, s);
   bwd_slice_up_kernel<E, P, NVL><<<blocks, kBwdThreads, 0, s>>>(
       w.offsets, w.ents, static_cast<const E*>(x), w.part_dz, w.part_stride, g.d_ff, g.d_model,
       sp.S, sp.sw,
@@ -690,16 +529,16 @@ hipError_t launch_slices(const Geometry& g, const SlicePlan& sp, const BwdWorksp
 
 template <typename E>
 hipError_t launch_neuron_pass(const Geometry& g, const BwdWorkspace& w, const void* x,
-                              const BwdAct8* x8, const void* dy, const void* w_down,
-                              float* dw_up_t, float* db, float* dw_down, hipStream_t s) {
+                              const void* dy, const void* w_down, float* dw_up_t, float* db,
+                              float* dw_down, hipStream_t s) {
   const SlicePlan sp = bwd_slice_plan(g.d_model, sizeof(E));
   switch (sp.P * 8 + sp.nvl) {
-    case 8 * 8 + 1: return launch_slices<E, 8, 1>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
-    case 16 * 8 + 1: return launch_slices<E, 16, 1>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
-    case 32 * 8 + 1: return launch_slices<E, 32, 1>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
-    case 64 * 8 + 1: return launch_slices<E, 64, 1>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
-    case 64 * 8 + 2: return launch_slices<E, 64, 2>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
-    case 64 * 8 + 4: return launch_slices<E, 64, 4>(g, sp, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
+    case 8 * 8 + 1: return launch_slices<E, 8, 1>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
+    case 16 * 8 + 1: return launch_slices<E, 16, 1>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
+    case 32 * 8 + 1: return launch_slices<E, 32, 1>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
+    case 64 * 8 + 1: return launch_slices<E, 64, 1>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
+    case 64 * 8 + 2: return launch_slices<E, 64, 2>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
+    case 64 * 8 + 4: return launch_slices<E, 64, 4>(g, sp, w, x, dy, w_down, dw_up_t, db, dw_down, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -754,9 +593,9 @@ BwdWorkspace bwd_carve(const Geometry& g, int elem_bytes, int64_t dense_cap, voi
 }
 
 hipError_t launch_backward(const Geometry& g, int elem_bytes, const BwdHybrid& hy, const void* x,
-                           const BwdAct8* x8, const void* w_up_t, const void* w_down,
-                           const void* dy, const BwdWorkspace& w, void* dx, float* dw_up_t,
-                           float* db, float* dw_down, hipStream_t s) {
+                           const void* w_up_t, const void* w_down, const void* dy,
+                           const BwdWorkspace& w, void* dx, float* dw_up_t, float* db,
+                           float* dw_down, hipStream_t s) {
   const int64_t wsize = static_cast<int64_t>(g.d_ff) * g.d_model;
   hipError_t e;
   if (g.n_rows == 0) {  // no rows: every gradient is zero (dx has no rows)
@@ -805,8 +644,8 @@ hipError_t launch_backward(const Geometry& g, int elem_bytes, const BwdHybrid& h
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if ((e = columns(std::false_type{})) != hipSuccess) return e;
   // 3. dz at every entry, weight and bias gradients (two passes over column slices)
-  e = bf ? launch_neuron_pass<uint16_t>(g, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s)
-         : launch_neuron_pass<float>(g, w, x, x8, dy, w_down, dw_up_t, db, dw_down, s);
+  e = bf ? launch_neuron_pass<uint16_t>(g, w, x, dy, w_down, dw_up_t, db, dw_down, s)
+         : launch_neuron_pass<float>(g, w, x, dy, w_down, dw_up_t, db, dw_down, s);
   if (e != hipSuccess) return e;
   // 4. dx = dz W_up^T: every row by the TwELL gather (a stored dense row has
   // no live slot, so it gets 0 there), then the stored dense rows by the

@@ -1,0 +1,721 @@
+// The layer's backward pass from an 8-bit checkpoint of its input.  Same
+// gradients as the plain backward (dz = dy W_down^T where h is non-zero,
+// dW_down = h^T dy, dW_up^T = dz^T x, db = column sums of dz, dx = dz W_up),
+// with x = code * scale formed on the way and dz kept in float32 throughout.
+//
+// The non-zeros of h become one list in two orders: by neuron and then row
+// (ents: row, h, and the place p in the other order), and by row and then
+// neuron (cols; dz is stored there).  A bitmap over (neuron, row), set with
+// order-free atomics, gives the neuron-major places, so every sum below runs
+// in a fixed order.  Three passes gather rows of dy, x and W_up:
+//   down: per entry the dot of dy[row] with W_down[j], dW_down[j] += h dy[row];
+//   up:   dz; dW_up^T[j] += dz x[row], db[j] += dz;
+//   dx:   dx[row] += dz W_up[j], for TwELL and dense rows alike.
+// Each gathers 335 k x 2048 columns at the 1B layer, from the L2 of the XCD
+// that a column slice is dealt to; they are bound by the instructions per
+// gathered vector and by the rate at which the L1 returns data, not by HBM.
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+#include "vec_ops.h"
+
+namespace twell {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kCols = 16;  // columns of a gathered row per lane and vector group
+constexpr int kScanThreads = 1024;
+constexpr int kScanPer = 16;
+
+__device__ __forceinline__ int64_t wave_index() {
+  return static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
+}
+
+__device__ __forceinline__ int64_t stored_rows(const BwdHybrid& hy) {
+  return hy.cap <= 0 ? 0 : min(static_cast<int64_t>(max(*hy.n_dense, 0)), hy.cap);
+}
+
+__global__ __launch_bounds__(kThreads) void a8_zero_kernel(uint4* __restrict__ p, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// row_slot[n] = m + 1 for the stored dense row m of token row n (0: none).
+__global__ __launch_bounds__(kThreads) void a8_dense_kernel(BwdHybrid hy, int64_t n_rows,
+                                                            int32_t* __restrict__ row_slot) {
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (m >= stored_rows(hy)) return;
+  const int64_t r = hy.dense_rows[m];
+  if (r >= 0 && r < n_rows) row_slot[r] = static_cast<int32_t>(m + 1);
+}
+
+// One wave per token row visits its non-zeros in ascending neuron order:
+// visit(rank within the row, neuron, h).  Returns how many there are.
+template <typename E, typename Visit>
+__device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slot, int dff, int T,
+                                         int C, int nt, Visit visit) {
+  typedef ElemTraits<E> Tr;
+  constexpr int V = 16 / sizeof(E);
+  constexpr int U = 4;  // dense vectors in flight
+  const int lane = lane_id();
+  int run = 0;
+  if (slot > 0) {
+    const E* row = static_cast<const E*>(hy.dense_values) + static_cast<int64_t>(slot - 1) * dff;
+    for (int c0 = 0; c0 < dff; c0 += U * kWave * V) {
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + (u * kWave + lane) * V;
+        q[u] = c < dff ? load_once(reinterpret_cast<const uint4*>(row + c))
+                       : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        E v[V];
+        *reinterpret_cast<uint4*>(v) = q[u];
+        int below = 0, all = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint64_t m = wave_ballot(Tr::abs_bits(v[e]) != 0u);
+          below += popc_below(m);
+          all += popc64(m);
+        }
+        if (all == 0) continue;
+        int p = run + below;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (Tr::abs_bits(v[e]) != 0u)
+            visit(p++, c0 + (u * kWave + lane) * V + e, Tr::to_f32(v[e]));
+        run += all;
+      }
+    }
+    return run;
+  }
+  const int nslots = nt * C;
+  const E* vrow = static_cast<const E*>(hy.vals) + n * nslots;
+  const uint8_t* irow = hy.idx + n * nslots;
+  for (int s0 = 0; s0 < nslots; s0 += kWave) {
+    const int s = s0 + lane;
+    const int t = s / C;
+    int local = T;
+    if (s < nslots && s - t * C < static_cast<int>(hy.cnt[n * nt + t])) local = irow[s];
+    const uint64_t m = wave_ballot(local < T);
+    if (local < T) visit(run + popc_below(m), t * T + local, Tr::to_f32(vrow[s]));
+    run += popc64(m);
+  }
+  return run;
+}
+
+// Bit n % 64 of bits[j][n / 64] for every non-zero; row_count[n] = theirs.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void a8_mark_kernel(
+    BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
+    const int32_t* __restrict__ row_slot, int64_t n_words, unsigned long long* __restrict__ bits,
+    int32_t* __restrict__ row_count) {
+  const int64_t n = wave_index();
+  if (n >= n_rows) return;
+  const unsigned long long bit = 1ull << (n & 63);
+  unsigned long long* word = bits + (n >> 6);
+  const int c = visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, [&](int, int j, float) {
+    atomicOr(word + static_cast<int64_t>(j) * n_words, bit);
+  });
+  if (lane_id() == 0) row_count[n] = c;
+}
+
+// Per neuron (one wave each): lpre[j][b] = set bits of its words below b;
+// neuron_count[j] = all.
+__global__ __launch_bounds__(kThreads) void a8_prefix_kernel(
+    const unsigned long long* __restrict__ bits, int64_t n_words, int dff,
+    int32_t* __restrict__ lpre, int32_t* __restrict__ neuron_count) {
+  const int lane = lane_id();
+  const int64_t j = wave_index();
+  if (j >= dff) return;
+  int run = 0;
+  for (int64_t b0 = 0; b0 < n_words; b0 += kWave) {
+    const int64_t b = b0 + lane;
+    const int c = b < n_words ? __popcll(bits[j * n_words + b]) : 0;
+    int v = c;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int u = __shfl_up(v, o, kWave);
+      if (lane >= o) v += u;
+    }
+    if (b < n_words) lpre[j * n_words + b] = run + v - c;
+    run += __shfl(v, kWave - 1, kWave);
+  }
+  if (lane == 0) neuron_count[j] = run;
+}
+
+// Exclusive sums: workgroup 0 of the neurons' counts, workgroup 1 of the rows'.
+__global__ __launch_bounds__(kScanThreads) void a8_scan_kernel(
+    const int32_t* __restrict__ neuron_count, int64_t n_neurons, int32_t* __restrict__ neuron_off,
+    const int32_t* __restrict__ row_count, int64_t n_rows, int32_t* __restrict__ row_off) {
+  __shared__ int wave_tot[kScanThreads / kWave];
+  const bool rows = blockIdx.x == 1;
+  const int32_t* in = rows ? row_count : neuron_count;
+  int32_t* out = rows ? row_off : neuron_off;
+  const int64_t n = rows ? n_rows : n_neurons;
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  int carry = 0;
+  for (int64_t r0 = 0; r0 < n; r0 += kScanThreads * kScanPer) {
+    const int64_t i0 = r0 + static_cast<int64_t>(tid) * kScanPer;
+    int v[kScanPer], local = 0;
+#pragma unroll
+    for (int k = 0; k < kScanPer; k += 4) {
+      if (i0 + k + 4 <= n) {
+        const int4 q = *reinterpret_cast<const int4*>(in + i0 + k);
+        v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k + e] = i0 + k + e < n ? in[i0 + k + e] : 0;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) local += v[k];
+    int sc = local;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int u = __shfl_up(sc, o, kWave);
+      if (lane >= o) sc += u;
+    }
+    if (lane == kWave - 1) wave_tot[wave] = sc;
+    __syncthreads();
+    int run = carry + sc - local, total = 0;
+    for (int w = 0; w < kScanThreads / kWave; ++w) {
+      run += w < wave ? wave_tot[w] : 0;
+      total += wave_tot[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) {
+      if (i0 + k < n) out[i0 + k] = run;
+      run += v[k];
+    }
+    carry += total;
+    __syncthreads();  // wave_tot is rewritten by the next round
+  }
+  if (tid == 0) out[n] = carry;
+}
+
+// Every non-zero into both orders.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void a8_fill_kernel(
+    BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
+    const int32_t* __restrict__ row_slot, int64_t n_words,
+    const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
+    const int32_t* __restrict__ neuron_off, const int32_t* __restrict__ row_off,
+    int4* __restrict__ ents, int32_t* __restrict__ cols) {
+  const int64_t n = wave_index();
+  if (n >= n_rows) return;
+  const unsigned long long bit = 1ull << (n & 63);
+  const int first = row_off[n];
+  visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, [&](int rank, int j, float h) {
+    const int64_t w = static_cast<int64_t>(j) * n_words + (n >> 6);
+    const int at = neuron_off[j] + lpre[w] + __popcll(bits[w] & (bit - 1));
+    ents[at] = make_int4(static_cast<int>(n), static_cast<int>(__float_as_uint(h)), first + rank,
+                         0);
+    cols[first + rank] = j;
+  });
+}
+
+// ---- The gathering passes.  A slice of sw columns is covered by P lanes of
+// NV * 16 columns each, 64 / P entries at a time; block b takes slice b % S, so
+// that a slice's rows stay in the L2 of the XCDs it is dealt to.
+// HALF: d_model is no multiple of 16, so a row's last vector group has 8.
+template <int P, int NV, bool HALF>
+struct Slice {
+  static constexpr int kGroups = kWave / P;
+  static constexpr int kSteps = kGroups * NV >= 8 ? 1 : 8 / (kGroups * NV);  // passes in flight
+  static constexpr int kEntries = kGroups * kSteps;                          // per step
+  static constexpr int kAcc = NV * kCols;
+  int col[NV];   // first column of each of the lane's vector groups
+  bool ok[NV];   // whether it lies in the slice
+  int end;       // columns of a whole row
+  __device__ __forceinline__ bool half(int v) const { return HALF && col[v] + 8 >= end; }
+  __device__ __forceinline__ Slice(int s, int sw, int dm) : end(dm) {
+    const int l = lane_id() % P;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * P + l) * kCols;
+      ok[v] = c < sw;
+      col[v] = s * sw + (ok[v] ? c : 0);  // a lane past the slice reads its first columns
+    }
+  }
+};
+
+// 16 columns of a row of E.  `half`: only the first 8 exist (a row's last
+// vector group, d_model being a multiple of 8).
+template <typename E>
+struct Vec16 {
+  static constexpr int kLoads = kCols * sizeof(E) / 16;
+  uint4 q[kLoads];
+  __device__ __forceinline__ void load(const E* p, bool half) {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+      q[k] = half && k >= kLoads / 2 ? make_uint4(0, 0, 0, 0)
+                                     : reinterpret_cast<const uint4*>(p)[k];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) q[k] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void keep(bool k) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) q[i] = keep_if(k, q[i]);
+  }
+  __device__ __forceinline__ float dot(const Vec16& o) const {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) s += dot16<E>(q[k], o.q[k]);
+    return s;
+  }
+  __device__ __forceinline__ void axpy(float* acc, uint32_t sbits) const {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) axpy16<E>(acc + k * (16 / sizeof(E)), sbits, q[k]);
+  }
+  // acc += f * q with f in float32
+  __device__ __forceinline__ void fma32(float* acc, float f) const {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(E) == 2) {
+          float* a = acc + k * 8 + 2 * i;
+          a[0] = fmaf(f, __uint_as_float(w[i] << 16), a[0]);
+          a[1] = fmaf(f, __uint_as_float(w[i] & 0xffff0000u), a[1]);
+        } else {
+          acc[k * 4 + i] = fmaf(f, __uint_as_float(w[i]), acc[k * 4 + i]);
+        }
+      }
+    }
+  }
+};
+
+typedef uint32_t swap_pair_t __attribute__((ext_vector_type(2)));
+
+// The groups' sums added, in a fixed order, and spread: afterwards a lane of
+// group g holds the kAcc / kGroups columns from g * kAcc / kGroups of its kAcc
+// in acc[0 ..].  Each step swaps half a wave (or alternate rows of 16) of two
+// accumulators and adds, which halves their number.
+template <int P, int N>
+__device__ __forceinline__ void join_groups(float (&acc)[N]) {
+  if constexpr (P <= 32) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const swap_pair_t r = __builtin_bit_cast(
+          swap_pair_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i]),
+                                                        __float_as_uint(acc[i + N / 2]), false,
+                                                        false));
+      acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+  }
+  if constexpr (P <= 16) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const swap_pair_t r = __builtin_bit_cast(
+          swap_pair_t, __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i]),
+                                                        __float_as_uint(acc[i + N / 4]), false,
+                                                        false));
+      acc[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+  }
+}
+
+// The first column, in the lane's kAcc, that join_groups leaves with it.
+template <int P, int N>
+__device__ __forceinline__ int joined_first() {
+  const int lane = lane_id();
+  int c = 0;
+  if constexpr (P <= 32) c += lane / 32 * (N / 2);
+  if constexpr (P <= 16) c += lane / 16 % 2 * (N / 4);
+  return c;
+}
+
+// The joined sums (or zeros) to the lane's columns of a row.
+template <typename O, int P, int NV, bool HALF>
+__device__ __forceinline__ void store_joined(O* row, const Slice<P, NV, HALF>& sl, const float* acc) {
+  constexpr int N = NV * kCols, kEach = N / (kWave / P);
+  const int first = joined_first<P, N>();
+#pragma unroll
+  for (int i = 0; i < kEach; i += 4) {
+    const int v = NV == 1 ? 0 : (first + i) / kCols, in = (first + i) % kCols;
+    const int c = (NV == 1 || v == 0 ? sl.col[0] : sl.col[NV - 1]) + in;
+    const bool ok = (NV == 1 || v == 0 ? sl.ok[0] : sl.ok[NV - 1]) && c < sl.end;
+    if (!ok) continue;
+    if constexpr (sizeof(O) == 4) {
+      *reinterpret_cast<float4*>(row + c) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    } else {
+      uint32_t w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        w[k] = ElemTraits<O>::from_f32(acc[i + 2 * k]) |
+               static_cast<uint32_t>(ElemTraits<O>::from_f32(acc[i + 2 * k + 1])) << 16;
+      *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+// Down: a wave per (neuron, slice).  part[s * pstride + entry] = the slice's
+// dot of dy[row] with W_down[j]; dW_down[j][slice] = sum of h dy[row].
+template <typename E, int P, int NV, bool HALF>
+__global__ __launch_bounds__(kThreads) void a8_down_kernel(
+    const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
+    const E* __restrict__ dy, const E* __restrict__ w_down, int dff, int dm, int S, int sw,
+    float* __restrict__ part, int64_t pstride, float* __restrict__ dw_down) {
+  typedef Slice<P, NV, HALF> Sl;
+  const int lane = lane_id(), grp = lane / P;
+  const int s = blockIdx.x % S;
+  const int j = (blockIdx.x / S) * kWaves + threadIdx.x / kWave;
+  if (j >= dff) return;
+  const Sl sl(s, sw, dm);
+  const int b = neuron_off[j], L = neuron_off[j + 1] - b;
+  float acc[Sl::kAcc];
+#pragma unroll
+  for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
+  Vec16<E> w[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    w[v].clear();
+    if (L > 0 && sl.ok[v])
+      w[v].load(w_down + static_cast<int64_t>(j) * dm + sl.col[v], sl.half(v));
+  }
+  for (int base = 0; base < L; base += kWave) {
+    const int cnt = min(kWave, L - base);
+    const int4 mine = ents[b + base + min(lane, cnt - 1)];
+    float mypd = 0.f;  // lane t: the chunk's entry t
+    auto step = [&](int e0, auto check) {
+      constexpr bool CHECK = decltype(check)::value;
+      Vec16<E> y[Sl::kSteps][NV];
+      uint32_t hb[Sl::kSteps];
+      float pd[Sl::kSteps];
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        const int e = e0 + u * Sl::kGroups + grp;
+        const int64_t row = __shfl(mine.x, e, kWave);
+        hb[u] = store_bits<E>(static_cast<uint32_t>(__shfl(mine.y, e, kWave)));
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          y[u][v].load(dy + row * dm + sl.col[v], sl.half(v));
+      }
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        pd[u] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (CHECK) y[u][v].keep(e0 + u * Sl::kGroups + grp < cnt);
+          pd[u] += y[u][v].dot(w[v]);
+        }
+      }
+      group_totals<P, Sl::kSteps>(pd);
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        // entry e's partial is in the last lane of its group; lane e takes it
+        const int e_u = e0 + u * Sl::kGroups;
+        const float got = __shfl(pd[u], (lane - e_u) * P + P - 1, kWave);
+        if (lane >= e_u && lane < e_u + Sl::kGroups) mypd = got;
+      }
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) y[u][v].axpy(acc + v * kCols, hb[u]);
+    };
+    int e0 = 0;
+    for (; e0 + Sl::kEntries <= cnt; e0 += Sl::kEntries) step(e0, std::false_type{});
+    if (e0 < cnt) step(e0, std::true_type{});
+    if (lane < cnt) part[s * pstride + b + base + lane] = mypd;
+  }
+  join_groups<P>(acc);
+  store_joined(dw_down + static_cast<int64_t>(j) * dm, sl, acc);
+}
+
+// Up: a wave per (neuron, slice).  dz = the n_part partial dots added in slice
+// order; slice 0 stores it at its place in the row order and adds db[j];
+// dW_up^T[j][slice] = sum of (dz * scale) * code.  A vector group's 16 columns
+// lie in one block of scales.
+template <int P, int NV, bool HALF>
+__global__ __launch_bounds__(kThreads) void a8_up_kernel(
+    const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
+    const int8_t* __restrict__ codes, const float* __restrict__ scales, int pitch, int nb,
+    const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int S, int sw,
+    float* __restrict__ dz, float* __restrict__ dw_up_t, float* __restrict__ db) {
+  typedef Slice<P, NV, HALF> Sl;
+  const int lane = lane_id(), grp = lane / P;
+  const int s = blockIdx.x % S;
+  const int j = (blockIdx.x / S) * kWaves + threadIdx.x / kWave;
+  if (j >= dff) return;
+  const Sl sl(s, sw, dm);
+  const int b = neuron_off[j], L = neuron_off[j + 1] - b;
+  float acc[Sl::kAcc];
+#pragma unroll
+  for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
+  float sum = 0.f;
+  for (int base = 0; base < L; base += kWave) {
+    const int cnt = min(kWave, L - base);
+    const int64_t me = b + base + min(lane, cnt - 1);
+    const int4 mine = ents[me];
+    float d = part[me];
+    if (n_part == 8) {  // the loads together
+      float p[7];
+#pragma unroll
+      for (int t = 0; t < 7; ++t) p[t] = part[(t + 1) * pstride + me];
+#pragma unroll
+      for (int t = 0; t < 7; ++t) d += p[t];
+    } else {
+      for (int t = 1; t < n_part; ++t) d += part[t * pstride + me];
+    }
+    // a lane past the entries repeats the last one with a factor of zero: its
+    // row's scale is NaN only where the neuron's sum is NaN already
+    if (lane >= cnt) d = 0.f;
+    for (int e0 = 0; e0 < cnt; e0 += Sl::kEntries) {
+      uint4 q[Sl::kSteps][NV];
+      float f[Sl::kSteps][NV];
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        const int64_t row = __shfl(mine.x, e0 + u * Sl::kGroups + grp, kWave);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          q[u][v] = *reinterpret_cast<const uint4*>(codes + row * pitch + sl.col[v]);
+          f[u][v] = scales[row * nb + sl.col[v] / kAct8Block];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        const float dzu = __shfl(d, e0 + u * Sl::kGroups + grp, kWave);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float z = dzu * f[u][v];
+          const uint32_t w[4] = {q[u][v].x, q[u][v].y, q[u][v].z, q[u][v].w};
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            acc[v * kCols + i] =
+                fmaf(z, static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)))),
+                     acc[v * kCols + i]);
+        }
+      }
+    }
+    if (s == 0 && lane < cnt) {
+      dz[mine.z] = d;
+      sum += d;
+    }
+  }
+  join_groups<P>(acc);
+  store_joined(dw_up_t + static_cast<int64_t>(j) * dm, sl, acc);
+  if (s == 0) {
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
+    if (lane == 0) db[j] = sum;
+  }
+}
+
+// dx: a wave per (token row, slice): dx[n][slice] = sum of dz W_up^T[j], in
+// float32, rounded once.
+template <typename E, int P, int NV, bool HALF>
+__global__ __launch_bounds__(kThreads) void a8_dx_kernel(
+    const int32_t* __restrict__ row_off, const int32_t* __restrict__ cols,
+    const float* __restrict__ dz, const E* __restrict__ w_up_t, int64_t n_rows, int dm, int S,
+    int sw, E* __restrict__ dx) {
+  typedef Slice<P, NV, HALF> Sl;
+  const int lane = lane_id(), grp = lane / P;
+  const int s = blockIdx.x % S;
+  const int64_t n = static_cast<int64_t>(blockIdx.x / S) * kWaves + threadIdx.x / kWave;
+  if (n >= n_rows) return;
+  const Sl sl(s, sw, dm);
+  const int b = row_off[n], L = row_off[n + 1] - b;
+  float acc[Sl::kAcc];
+#pragma unroll
+  for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
+  for (int base = 0; base < L; base += kWave) {
+    const int cnt = min(kWave, L - base);
+    const int my_col = cols[b + base + min(lane, cnt - 1)];
+    const float my_dz = dz[b + base + min(lane, cnt - 1)];
+    auto step = [&](int e0, auto check) {
+      constexpr bool CHECK = decltype(check)::value;
+      Vec16<E> w[Sl::kSteps][NV];
+      float f[Sl::kSteps];
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        const int e = e0 + u * Sl::kGroups + grp;
+        const int64_t j = __shfl(my_col, e, kWave);
+        f[u] = __shfl(my_dz, e, kWave);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          w[u][v].load(w_up_t + j * dm + sl.col[v], sl.half(v));
+      }
+#pragma unroll
+      for (int u = 0; u < Sl::kSteps; ++u) {
+        const bool live = !CHECK || e0 + u * Sl::kGroups + grp < cnt;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (CHECK) w[u][v].keep(live);
+          w[u][v].fma32(acc + v * kCols, live ? f[u] : 0.f);
+        }
+      }
+    };
+    int e0 = 0;
+    for (; e0 + Sl::kEntries <= cnt; e0 += Sl::kEntries) step(e0, std::false_type{});
+    if (e0 < cnt) step(e0, std::true_type{});
+  }
+  join_groups<P>(acc);
+  store_joined(dx + n * dm, sl, acc);
+}
+
+// Column slices: S of sw columns, S up to 8 (one per XCD) as long as a slice
+// keeps 256 columns and whole vector groups; P lanes of nv vector groups cover
+// one (nv = 0: too wide).
+SlicePlan slice_plan(int dm) {
+  SlicePlan p;
+  p.S = 8;
+  while (p.S > 1 && (dm % (p.S * kCols) != 0 || dm / p.S < 256)) p.S /= 2;
+  p.sw = dm / p.S;
+  const int groups = (p.sw + kCols - 1) / kCols;
+  p.P = groups <= 16 ? 16 : groups <= 32 ? 32 : kWave;
+  p.nvl = groups <= kWave ? 1 : groups <= 2 * kWave ? 2 : 0;
+  return p;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+int64_t clamped(const Geometry& g, int64_t cap) {
+  return cap <= 0 ? 0 : cap < g.n_rows ? cap : g.n_rows;
+}
+
+struct Space {
+  unsigned long long* bits;  // [d_ff][words] (neuron, row) bitmap
+  int32_t* row_slot;         // [N]
+  int64_t zero_vecs;         // 16-byte vectors of bits + row_slot
+  int32_t *row_count, *row_off, *lpre, *neuron_count, *neuron_off, *cols;
+  int4* ents;   // {row, h as float32 bits, place in row order, 0}, by neuron then row
+  float* dz;    // by row then neuron
+  float* part;  // [S][entries] partial dots
+  int64_t entries;
+  size_t bytes;
+};
+
+Space carve(const Geometry& g, int64_t cap, void* ws) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* q = p == nullptr ? nullptr : p + off;
+    off += align256(bytes);
+    return q;
+  };
+  const size_t n = static_cast<size_t>(g.n_rows), dff = static_cast<size_t>(g.d_ff);
+  const size_t words = dff * ((n + 63) / 64);
+  Space w{};
+  w.entries = bwd_max_entries(g, cap);
+  const size_t ents = static_cast<size_t>(w.entries);
+  w.bits = static_cast<unsigned long long*>(take(words * 8));
+  w.row_slot = static_cast<int32_t*>(take(n * 4));
+  w.zero_vecs = static_cast<int64_t>(off / 16);
+  w.row_count = static_cast<int32_t*>(take(n * 4));
+  w.row_off = static_cast<int32_t*>(take((n + 1) * 4));
+  w.lpre = static_cast<int32_t*>(take(words * 4));
+  w.neuron_count = static_cast<int32_t*>(take(dff * 4));
+  w.neuron_off = static_cast<int32_t*>(take((dff + 1) * 4));
+  w.cols = static_cast<int32_t*>(take(ents * 4));
+  w.ents = static_cast<int4*>(take(ents * sizeof(int4)));
+  w.dz = static_cast<float*>(take(ents * 4));
+  w.part = static_cast<float*>(take(static_cast<size_t>(slice_plan(g.d_model).S) * ents * 4));
+  w.bytes = off;
+  return w;
+}
+
+unsigned blocks(int64_t items, int per) { return static_cast<unsigned>((items + per - 1) / per); }
+
+template <typename E, int P, int NV, bool HALF>
+hipError_t gather_passes(const Geometry& g, const SlicePlan& sp, const Space& w, const BwdAct8& x8,
+                         const void* w_up_t, const void* w_down, const void* dy, void* dx,
+                         float* dw_up_t, float* db, float* dw_down, hipStream_t s) {
+  const unsigned by_neuron = blocks(g.d_ff, kWaves) * static_cast<unsigned>(sp.S);
+  a8_down_kernel<E, P, NV, HALF><<<by_neuron, kThreads, 0, s>>>(
+      w.neuron_off, w.ents, static_cast<const E*>(dy), static_cast<const E*>(w_down), g.d_ff,
+      g.d_model, sp.S, sp.sw, w.part, w.entries, dw_down);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a8_up_kernel<P, NV, HALF><<<by_neuron, kThreads, 0, s>>>(
+      w.neuron_off, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model), act8_blocks(g.d_model),
+      w.part, w.entries, sp.S, g.d_ff, g.d_model, sp.S, sp.sw, w.dz, dw_up_t, db);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a8_dx_kernel<E, P, NV, HALF><<<blocks(g.n_rows, kWaves) * static_cast<unsigned>(sp.S), kThreads, 0,
+                           s>>>(w.row_off, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows,
+                                g.d_model, sp.S, sp.sw, static_cast<E*>(dx));
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, const void* w_up_t,
+                    const void* w_down, const void* dy, const Space& w, void* dx, float* dw_up_t,
+                    float* db, float* dw_down, hipStream_t s) {
+  const int64_t n_words = (g.n_rows + 63) / 64, cap = clamped(g, hy.cap);
+  hipError_t e;
+  auto zero = [&](void* p, int64_t vecs) {
+    a8_zero_kernel<<<blocks(vecs, kThreads), kThreads, 0, s>>>(static_cast<uint4*>(p), vecs);
+    return hipGetLastError();
+  };
+  if (g.n_rows == 0) {  // zero weight and bias gradients
+    const int64_t weights = static_cast<int64_t>(g.d_ff) * g.d_model / 4;
+    if ((e = zero(dw_up_t, weights)) != hipSuccess) return e;
+    if ((e = zero(dw_down, weights)) != hipSuccess) return e;
+    return zero(db, g.d_ff / 4);
+  }
+  if ((e = zero(w.bits, w.zero_vecs)) != hipSuccess) return e;
+  if (cap > 0) {
+    a8_dense_kernel<<<blocks(cap, kThreads), kThreads, 0, s>>>(hy, g.n_rows, w.row_slot);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  a8_mark_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
+      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, w.row_slot, n_words, w.bits,
+      w.row_count);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a8_prefix_kernel<<<blocks(g.d_ff, kWaves), kThreads, 0, s>>>(w.bits, n_words, g.d_ff, w.lpre,
+                                                              w.neuron_count);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a8_scan_kernel<<<2, kScanThreads, 0, s>>>(w.neuron_count, g.d_ff, w.neuron_off, w.row_count,
+                                           g.n_rows, w.row_off);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a8_fill_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
+      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, w.row_slot, n_words, w.bits, w.lpre,
+      w.neuron_off, w.row_off, w.ents, w.cols);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const SlicePlan sp = slice_plan(g.d_model);
+  auto go = [&](auto p, auto nv, auto half) {
+    return gather_passes<E, decltype(p)::value, decltype(nv)::value, decltype(half)::value>(
+        g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db, dw_down, s);
+  };
+  auto by_half = [&](auto p, auto nv) {
+    return g.d_model % kCols == 0 ? go(p, nv, std::false_type{}) : go(p, nv, std::true_type{});
+  };
+  typedef std::integral_constant<int, 1> One;
+  if (sp.nvl == 2)
+    return by_half(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (sp.nvl != 1) return hipErrorInvalidValue;
+  if (sp.P == 16) return by_half(std::integral_constant<int, 16>{}, One{});
+  if (sp.P == 32) return by_half(std::integral_constant<int, 32>{}, One{});
+  return by_half(std::integral_constant<int, 64>{}, One{});
+}
+
+}  // namespace
+
+bool bwd_act8_supported(const Geometry& g) {
+  // a launch holds fewer than 2^32 lanes: 64 per row or neuron and slice, one
+  // per 128 bits of the bitmap
+  const int64_t most = (int64_t{1} << 23) - 8;
+  return slice_plan(g.d_model).nvl != 0 && g.n_rows < most && g.d_ff < most &&
+         g.n_rows * g.d_ff < int64_t{1} << 38;
+}
+
+size_t bwd_act8_bytes(const Geometry& g, int64_t cap) { return carve(g, cap, nullptr).bytes; }
+
+hipError_t launch_backward_act8(const Geometry& g, int elem_bytes, const BwdHybrid& hy,
+                                const BwdAct8& x8, const void* w_up_t, const void* w_down,
+                                const void* dy, void* ws, void* dx, float* dw_up_t, float* db,
+                                float* dw_down, hipStream_t s) {
+  const Space w = carve(g, hy.cap, ws);
+  return elem_bytes == 2
+             ? backward<uint16_t>(g, hy, x8, w_up_t, w_down, dy, w, dx, dw_up_t, db, dw_down, s)
+             : backward<float>(g, hy, x8, w_up_t, w_down, dy, w, dx, dw_up_t, db, dw_down, s);
+}
+
+}  // namespace twell

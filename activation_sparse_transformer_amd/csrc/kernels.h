@@ -263,15 +263,22 @@ bool bwd_supported(const Geometry& g, int elem_bytes);
 int64_t bwd_max_entries(const Geometry& g, int64_t dense_cap);
 // Parts of a workspace at `ws` (nullptr: sizes only, in .bytes).
 BwdWorkspace bwd_carve(const Geometry& g, int elem_bytes, int64_t dense_cap, void* ws);
-// x as rows of the storage type, or (x8 given, x unused) as an 8-bit checkpoint.
+hipError_t launch_backward(const Geometry& g, int elem_bytes, const BwdHybrid& hy, const void* x,
+                           const void* w_up_t, const void* w_down, const void* dy,
+                           const BwdWorkspace& w, void* dx, float* dw_up_t, float* db,
+                           float* dw_down, hipStream_t s);
+
+// The same from x as an 8-bit checkpoint, dz held in float32.
 struct BwdAct8 {
   const int8_t* codes;
   const float* scales;
 };
-hipError_t launch_backward(const Geometry& g, int elem_bytes, const BwdHybrid& hy, const void* x,
-                           const BwdAct8* x8, const void* w_up_t, const void* w_down,
-                           const void* dy, const BwdWorkspace& w, void* dx, float* dw_up_t,
-                           float* db, float* dw_down, hipStream_t s);
+bool bwd_act8_supported(const Geometry& g);
+size_t bwd_act8_bytes(const Geometry& g, int64_t dense_cap);
+hipError_t launch_backward_act8(const Geometry& g, int elem_bytes, const BwdHybrid& hy,
+                                const BwdAct8& x8, const void* w_up_t, const void* w_down,
+                                const void* dy, void* ws, void* dx, float* dw_up_t, float* db,
+                                float* dw_down, hipStream_t s);
 
 // The ReLU-gated FFN's up branch on a packed and routed gate: each stored
 // non-zero g (TwELL slots of the sparse rows sparse_rows[0 .. *n_sparse),

@@ -571,14 +571,10 @@ TWELL_EXPORT size_t ffn_sparse_backward_workspace_size(const twell_shape* shape,
   return bwd_carve(geometry(shape), elem_bytes(shape->dtype), dense_capacity, nullptr).bytes;
 }
 
-namespace twell {
-namespace {
-
-// ffn_sparse_backward with x as rows (x8 null) or as an 8-bit checkpoint.
-int backward_impl(const twell_shape* shape, const void* x, const twell_act8* x8,
-                  const void* w_up_t, const void* w_down, const twell_hybrid* h, const void* dy,
-                  void* dx, float* dw_up_t, float* db_up, float* dw_down, void* workspace,
-                  size_t workspace_bytes, void* stream) {
+TWELL_EXPORT int ffn_sparse_backward(const twell_shape* shape, const void* x, const void* w_up_t,
+                                     const void* w_down, const twell_hybrid* h, const void* dy,
+                                     void* dx, float* dw_up_t, float* db_up, float* dw_down,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_shape(shape, true);
   if (rc != TWELL_OK) return rc;
   const Geometry g = geometry(shape);
@@ -586,36 +582,20 @@ int backward_impl(const twell_shape* shape, const void* x, const twell_act8* x8,
   if ((rc = check_backward_shape(shape, h->dense_capacity)) != TWELL_OK) return rc;
   if (dw_up_t == nullptr || db_up == nullptr || dw_down == nullptr || workspace == nullptr)
     return TWELL_ERR_INVALID_ARG;
-  const bool have_x = x8 == nullptr ? x != nullptr : x8->codes != nullptr && x8->scales != nullptr;
   if (g.n_rows > 0 &&
-      (!have_x || w_up_t == nullptr || w_down == nullptr || dy == nullptr || dx == nullptr))
+      (x == nullptr || w_up_t == nullptr || w_down == nullptr || dy == nullptr || dx == nullptr))
     return TWELL_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_up_t) || !aligned16(w_down) || !aligned16(dy) ||
       !aligned16(dx) || !aligned16(dw_up_t) || !aligned16(db_up) || !aligned16(dw_down) ||
       !aligned16(workspace))
-    return TWELL_ERR_INVALID_ARG;
-  if (x8 != nullptr && (!aligned16(x8->codes) || !aligned16(x8->scales)))
     return TWELL_ERR_INVALID_ARG;
   const int eb = elem_bytes(shape->dtype);
   const BwdWorkspace w = bwd_carve(g, eb, h->dense_capacity, workspace);
   if (workspace_bytes < w.bytes) return TWELL_ERR_WORKSPACE;
   const BwdHybrid hy{h->values,       h->indices, h->counts,         h->dense_rows,
                      h->dense_values, h->n_dense, h->dense_capacity};
-  const BwdAct8 a8{x8 == nullptr ? nullptr : x8->codes, x8 == nullptr ? nullptr : x8->scales};
-  return hip_status(launch_backward(g, eb, hy, x, x8 == nullptr ? nullptr : &a8, w_up_t, w_down,
-                                    dy, w, dx, dw_up_t, db_up, dw_down,
-                                    static_cast<hipStream_t>(stream)));
-}
-
-}  // namespace
-}  // namespace twell
-
-TWELL_EXPORT int ffn_sparse_backward(const twell_shape* shape, const void* x, const void* w_up_t,
-                                     const void* w_down, const twell_hybrid* h, const void* dy,
-                                     void* dx, float* dw_up_t, float* db_up, float* dw_down,
-                                     void* workspace, size_t workspace_bytes, void* stream) {
-  return backward_impl(shape, x, nullptr, w_up_t, w_down, h, dy, dx, dw_up_t, db_up, dw_down,
-                       workspace, workspace_bytes, stream);
+  return hip_status(launch_backward(g, eb, hy, x, w_up_t, w_down, dy, w, dx, dw_up_t, db_up,
+                                    dw_down, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ 8-bit checkpoints
@@ -654,9 +634,22 @@ TWELL_EXPORT int twell_act8_unpack(int64_t n_rows, int32_t d_model, int32_t dtyp
                                        x, static_cast<hipStream_t>(stream)));
 }
 
+namespace twell {
+namespace {
+
+int check_backward_act8(const twell_shape* s, int64_t dense_capacity) {
+  const int rc = check_backward_shape(s, dense_capacity);
+  if (rc != TWELL_OK) return rc;
+  return bwd_act8_supported(geometry(s)) ? TWELL_OK : TWELL_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace twell
+
 TWELL_EXPORT size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape,
                                                             int64_t dense_capacity) {
-  return ffn_sparse_backward_workspace_size(shape, dense_capacity);
+  if (check_backward_act8(shape, dense_capacity) != TWELL_OK) return 0;
+  return bwd_act8_bytes(geometry(shape), dense_capacity);
 }
 
 TWELL_EXPORT int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8,
@@ -664,9 +657,28 @@ TWELL_EXPORT int ffn_sparse_backward_act8(const twell_shape* shape, const twell_
                                           const twell_hybrid* h, const void* dy, void* dx,
                                           float* dw_up_t, float* db_up, float* dw_down,
                                           void* workspace, size_t workspace_bytes, void* stream) {
-  if (x8 == nullptr) return TWELL_ERR_INVALID_ARG;
-  return backward_impl(shape, nullptr, x8, w_up_t, w_down, h, dy, dx, dw_up_t, db_up, dw_down,
-                       workspace, workspace_bytes, stream);
+  int rc = check_shape(shape, true);
+  if (rc != TWELL_OK) return rc;
+  const Geometry g = geometry(shape);
+  if ((rc = check_hybrid(h, g.n_rows)) != TWELL_OK) return rc;
+  if ((rc = check_backward_act8(shape, h->dense_capacity)) != TWELL_OK) return rc;
+  if (x8 == nullptr || dw_up_t == nullptr || db_up == nullptr || dw_down == nullptr ||
+      workspace == nullptr)
+    return TWELL_ERR_INVALID_ARG;
+  if (g.n_rows > 0 && (x8->codes == nullptr || x8->scales == nullptr || w_up_t == nullptr ||
+                       w_down == nullptr || dy == nullptr || dx == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(x8->codes) || !aligned16(x8->scales) || !aligned16(w_up_t) ||
+      !aligned16(w_down) || !aligned16(dy) || !aligned16(dx) || !aligned16(dw_up_t) ||
+      !aligned16(db_up) || !aligned16(dw_down) || !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  if (workspace_bytes < bwd_act8_bytes(g, h->dense_capacity)) return TWELL_ERR_WORKSPACE;
+  const BwdHybrid hy{h->values,       h->indices, h->counts,         h->dense_rows,
+                     h->dense_values, h->n_dense, h->dense_capacity};
+  return hip_status(launch_backward_act8(g, elem_bytes(shape->dtype), hy,
+                                         BwdAct8{x8->codes, x8->scales}, w_up_t, w_down, dy,
+                                         workspace, dx, dw_up_t, db_up, dw_down,
+                                         static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ embedding

@@ -439,15 +439,19 @@ int twell_act8_pack(int64_t n_rows, int32_t d_model, int32_t dtype, const void* 
 int twell_act8_unpack(int64_t n_rows, int32_t d_model, int32_t dtype, const twell_act8* in,
                       void* x, void* stream);
 
-/* Bytes of device workspace ffn_sparse_backward_act8 needs (0 as for
- * ffn_sparse_backward_workspace_size). */
+/* Bytes of device workspace ffn_sparse_backward_act8 needs for this shape and a
+ * hybrid h with `dense_capacity` dense-row slots (0 for an invalid or
+ * unsupported shape): a (neuron, row) bitmap of h's non-zeros with its word
+ * prefixes, and per TwELL slot and stored dense element an entry in neuron
+ * order, a column and a dz in row order, and the dz's partial dots. */
 size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape, int64_t dense_capacity);
 
-/* ffn_sparse_backward with the layer's input given as an 8-bit checkpoint.
- * dw_up_t = dz^T (code * scale) with code * scale taken in float32, and with
- * dz in float32 for dw_up_t and db_up (dx reads dz rounded to the storage
- * type, as in ffn_sparse_backward).  Everything else, the limits and the
- * errors included, is as in ffn_sparse_backward. */
+/* The gradients of ffn_sparse_backward with the layer's input given as an 8-bit
+ * checkpoint: x = code * scale, and dw_up_t = dz^T x.  dz is held in float32
+ * throughout (ffn_sparse_backward rounds it to the storage type), so dx too is
+ * a float32 sum rounded once.  Sums run in a fixed order.  Arguments, limits
+ * and errors are those of ffn_sparse_backward, with n_rows and d_ff below
+ * 2^23 - 8 and n_rows * d_ff below 2^38 (else TWELL_ERR_UNSUPPORTED). */
 int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, const void* w_up_t,
                              const void* w_down, const twell_hybrid* h, const void* dy, void* dx,
                              float* dw_up_t, float* db_up, float* dw_down, void* workspace,
