@@ -219,74 +219,75 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
   });
 }
 
-// ---- The gathering passes.  A slice of sw columns is covered by P lanes of
-// NV * 16 columns each, 64 / P entries at a time; block b takes slice b % S, so
-// that a slice's rows stay in the L2 of the XCDs it is dealt to.
-// HALF: d_model is no multiple of 16, so a row's last vector group has 8.
-template <int P, int NV, bool HALF>
+// ---- The gathering passes.  A slice of sw columns is covered by P lanes, 64 / P
+// rows at a time; block b takes slice b % S, so that a slice's rows stay in the
+// L2 of the XCDs it is dealt to.  A lane holds kAcc = 16 NV columns as chunks
+// of V columns (16 bytes of the gathered type): chunk k of lane l is columns
+// (k P + l) V ..., so that one load of the group is one run of bytes.
+// FULL: the group covers the slice exactly.
+template <int V, int P, int NV, bool FULL>
 struct Slice {
+  static constexpr int kAcc = NV * kCols, kChunks = kAcc / V;
   static constexpr int kGroups = kWave / P;
-  static constexpr int kSteps = kGroups * NV >= 8 ? 1 : 8 / (kGroups * NV);  // passes in flight
-  static constexpr int kEntries = kGroups * kSteps;                          // per step
-  static constexpr int kAcc = NV * kCols;
-  int col[NV];   // first column of each of the lane's vector groups
-  bool ok[NV];   // whether it lies in the slice
-  int end;       // columns of a whole row
-  __device__ __forceinline__ bool half(int v) const { return HALF && col[v] + 8 >= end; }
-  __device__ __forceinline__ Slice(int s, int sw, int dm) : end(dm) {
+  static constexpr int kSteps = kGroups * NV >= 8 ? 1 : 8 / (kGroups * NV);  // rows in flight
+  static constexpr int kEntries = kGroups * kSteps;                          // rows per step
+  int first;  // column of the lane's chunk 0
+  int lim;    // columns of the slice past `first`
+  __device__ __forceinline__ Slice(int s, int sw) {
     const int l = lane_id() % P;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * P + l) * kCols;
-      ok[v] = c < sw;
-      col[v] = s * sw + (ok[v] ? c : 0);  // a lane past the slice reads its first columns
-    }
+    first = s * sw + l * V;
+    lim = sw - l * V;
+  }
+  __device__ __forceinline__ bool ok(int k) const { return FULL || k * P * V < lim; }
+  // a chunk past the slice reads the slice's first columns instead
+  __device__ __forceinline__ int col(int k) const {
+    return ok(k) ? first + k * P * V : first - lane_id() % P * V;
+  }
+  // the column of accumulator i
+  __device__ __forceinline__ int col_of(int i) const { return first + i / V * (P * V) + i % V; }
+  // how many columns the lane's row may be written at, from accumulator i's on
+  __device__ __forceinline__ bool may_write(int i) const {
+    return FULL || i / V * (P * V) + i % V < lim;
   }
 };
 
-// 16 columns of a row of E.  `half`: only the first 8 exist (a row's last
-// vector group, d_model being a multiple of 8).
-template <typename E>
-struct Vec16 {
-  static constexpr int kLoads = kCols * sizeof(E) / 16;
-  uint4 q[kLoads];
-  __device__ __forceinline__ void load(const E* p, bool half) {
+// A lane's chunks of one row of E.
+template <typename E, typename Sl>
+struct Row {
+  static constexpr int V = 16 / sizeof(E), K = Sl::kChunks;
+  uint4 q[K];
+  __device__ __forceinline__ void load(const E* row, const Sl& sl) {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k)
-      q[k] = half && k >= kLoads / 2 ? make_uint4(0, 0, 0, 0)
-                                     : reinterpret_cast<const uint4*>(p)[k];
+    for (int k = 0; k < K; ++k) q[k] = *reinterpret_cast<const uint4*>(row + sl.col(k));
   }
-  __device__ __forceinline__ void clear() {
+  // zero where `keep` is false or the chunk is past the slice
+  __device__ __forceinline__ void keep(bool keep, const Sl& sl) {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) q[k] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < K; ++k) q[k] = keep_if(keep && sl.ok(k), q[k]);
   }
-  __device__ __forceinline__ void keep(bool k) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) q[i] = keep_if(k, q[i]);
-  }
-  __device__ __forceinline__ float dot(const Vec16& o) const {
+  __device__ __forceinline__ float dot(const Row& o) const {
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) s += dot16<E>(q[k], o.q[k]);
+    for (int k = 0; k < K; ++k) s += dot16<E>(q[k], o.q[k]);
     return s;
   }
   __device__ __forceinline__ void axpy(float* acc, uint32_t sbits) const {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) axpy16<E>(acc + k * (16 / sizeof(E)), sbits, q[k]);
+    for (int k = 0; k < K; ++k) axpy16<E>(acc + k * V, sbits, q[k]);
   }
   // acc += f * q with f in float32
   __device__ __forceinline__ void fma32(float* acc, float f) const {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
+    for (int k = 0; k < K; ++k) {
       const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(E) == 2) {
-          float* a = acc + k * 8 + 2 * i;
+          float* a = acc + k * V + 2 * i;
           a[0] = fmaf(f, __uint_as_float(w[i] << 16), a[0]);
           a[1] = fmaf(f, __uint_as_float(w[i] & 0xffff0000u), a[1]);
         } else {
-          acc[k * 4 + i] = fmaf(f, __uint_as_float(w[i]), acc[k * 4 + i]);
+          acc[k * V + i] = fmaf(f, __uint_as_float(w[i]), acc[k * V + i]);
         }
       }
     }
@@ -333,61 +334,66 @@ __device__ __forceinline__ int joined_first() {
   return c;
 }
 
-// The joined sums (or zeros) to the lane's columns of a row.
-template <typename O, int P, int NV, bool HALF>
-__device__ __forceinline__ void store_joined(O* row, const Slice<P, NV, HALF>& sl, const float* acc) {
-  constexpr int N = NV * kCols, kEach = N / (kWave / P);
-  const int first = joined_first<P, N>();
+// The joined sums to the lane's columns of a row.
+template <int P, typename O, typename Sl>
+__device__ __forceinline__ void store_joined(O* row, const Sl& sl, const float* acc) {
+  constexpr int kEach = Sl::kAcc / Sl::kGroups;
+  const int first = joined_first<P, Sl::kAcc>();
 #pragma unroll
   for (int i = 0; i < kEach; i += 4) {
-    const int v = NV == 1 ? 0 : (first + i) / kCols, in = (first + i) % kCols;
-    const int c = (NV == 1 || v == 0 ? sl.col[0] : sl.col[NV - 1]) + in;
-    const bool ok = (NV == 1 || v == 0 ? sl.ok[0] : sl.ok[NV - 1]) && c < sl.end;
-    if (!ok) continue;
+    if (!sl.may_write(first + i)) continue;
+    O* to = row + sl.col_of(first + i);
     if constexpr (sizeof(O) == 4) {
-      *reinterpret_cast<float4*>(row + c) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      *reinterpret_cast<float4*>(to) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     } else {
       uint32_t w[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         w[k] = ElemTraits<O>::from_f32(acc[i + 2 * k]) |
                static_cast<uint32_t>(ElemTraits<O>::from_f32(acc[i + 2 * k + 1])) << 16;
-      *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
     }
   }
 }
 
+// The neuron or row group and the slice of a workgroup: S is a power of two.
+struct Place {
+  int slice;
+  int64_t item;  // this wave's
+  __device__ __forceinline__ explicit Place(int log_s) {
+    slice = static_cast<int>(blockIdx.x) & ((1 << log_s) - 1);
+    item = static_cast<int64_t>(blockIdx.x >> log_s) * kWaves + threadIdx.x / kWave;
+  }
+};
+
 // Down: a wave per (neuron, slice).  part[s * pstride + entry] = the slice's
 // dot of dy[row] with W_down[j]; dW_down[j][slice] = sum of h dy[row].
-template <typename E, int P, int NV, bool HALF>
+template <typename E, int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_down_kernel(
     const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
-    const E* __restrict__ dy, const E* __restrict__ w_down, int dff, int dm, int S, int sw,
+    const E* __restrict__ dy, const E* __restrict__ w_down, int dff, int dm, int log_s, int sw,
     float* __restrict__ part, int64_t pstride, float* __restrict__ dw_down) {
-  typedef Slice<P, NV, HALF> Sl;
+  typedef Slice<16 / sizeof(E), P, NV, FULL> Sl;
+  typedef Row<E, Sl> R;
   const int lane = lane_id(), grp = lane / P;
-  const int s = blockIdx.x % S;
-  const int j = (blockIdx.x / S) * kWaves + threadIdx.x / kWave;
-  if (j >= dff) return;
-  const Sl sl(s, sw, dm);
+  const Place at(log_s);
+  if (at.item >= dff) return;
+  const int j = static_cast<int>(at.item);
+  const Sl sl(at.slice, sw);
   const int b = neuron_off[j], L = neuron_off[j + 1] - b;
   float acc[Sl::kAcc];
 #pragma unroll
   for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
-  Vec16<E> w[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    w[v].clear();
-    if (L > 0 && sl.ok[v])
-      w[v].load(w_down + static_cast<int64_t>(j) * dm + sl.col[v], sl.half(v));
-  }
+  R w;
+  w.load(w_down + static_cast<int64_t>(j) * dm, sl);
+  if (!FULL) w.keep(true, sl);
   for (int base = 0; base < L; base += kWave) {
     const int cnt = min(kWave, L - base);
     const int4 mine = ents[b + base + min(lane, cnt - 1)];
     float mypd = 0.f;  // lane t: the chunk's entry t
     auto step = [&](int e0, auto check) {
       constexpr bool CHECK = decltype(check)::value;
-      Vec16<E> y[Sl::kSteps][NV];
+      R y[Sl::kSteps];
       uint32_t hb[Sl::kSteps];
       float pd[Sl::kSteps];
 #pragma unroll
@@ -395,18 +401,12 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
         const int e = e0 + u * Sl::kGroups + grp;
         const int64_t row = __shfl(mine.x, e, kWave);
         hb[u] = store_bits<E>(static_cast<uint32_t>(__shfl(mine.y, e, kWave)));
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          y[u][v].load(dy + row * dm + sl.col[v], sl.half(v));
+        y[u].load(dy + row * dm, sl);
       }
 #pragma unroll
       for (int u = 0; u < Sl::kSteps; ++u) {
-        pd[u] = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if (CHECK) y[u][v].keep(e0 + u * Sl::kGroups + grp < cnt);
-          pd[u] += y[u][v].dot(w[v]);
-        }
+        if (CHECK) y[u].keep(e0 + u * Sl::kGroups + grp < cnt, sl);
+        pd[u] = y[u].dot(w);
       }
       group_totals<P, Sl::kSteps>(pd);
 #pragma unroll
@@ -417,35 +417,33 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
         if (lane >= e_u && lane < e_u + Sl::kGroups) mypd = got;
       }
 #pragma unroll
-      for (int u = 0; u < Sl::kSteps; ++u)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) y[u][v].axpy(acc + v * kCols, hb[u]);
+      for (int u = 0; u < Sl::kSteps; ++u) y[u].axpy(acc, hb[u]);
     };
     int e0 = 0;
     for (; e0 + Sl::kEntries <= cnt; e0 += Sl::kEntries) step(e0, std::false_type{});
     if (e0 < cnt) step(e0, std::true_type{});
-    if (lane < cnt) part[s * pstride + b + base + lane] = mypd;
+    if (lane < cnt) part[at.slice * pstride + b + base + lane] = mypd;
   }
   join_groups<P>(acc);
-  store_joined(dw_down + static_cast<int64_t>(j) * dm, sl, acc);
+  store_joined<P>(dw_down + static_cast<int64_t>(j) * dm, sl, acc);
 }
 
 // Up: a wave per (neuron, slice).  dz = the n_part partial dots added in slice
 // order; slice 0 stores it at its place in the row order and adds db[j];
-// dW_up^T[j][slice] = sum of (dz * scale) * code.  A vector group's 16 columns
-// lie in one block of scales.
-template <int P, int NV, bool HALF>
+// dW_up^T[j][slice] = sum of (dz * scale) * code.  A chunk's 16 columns lie in
+// one block of scales.
+template <int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_up_kernel(
     const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
     const int8_t* __restrict__ codes, const float* __restrict__ scales, int pitch, int nb,
-    const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int S, int sw,
+    const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int log_s, int sw,
     float* __restrict__ dz, float* __restrict__ dw_up_t, float* __restrict__ db) {
-  typedef Slice<P, NV, HALF> Sl;
+  typedef Slice<kCols, P, NV, FULL> Sl;
   const int lane = lane_id(), grp = lane / P;
-  const int s = blockIdx.x % S;
-  const int j = (blockIdx.x / S) * kWaves + threadIdx.x / kWave;
-  if (j >= dff) return;
-  const Sl sl(s, sw, dm);
+  const Place at(log_s);
+  if (at.item >= dff) return;
+  const int j = static_cast<int>(at.item);
+  const Sl sl(at.slice, sw);
   const int b = neuron_off[j], L = neuron_off[j + 1] - b;
   float acc[Sl::kAcc];
 #pragma unroll
@@ -476,8 +474,8 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
         const int64_t row = __shfl(mine.x, e0 + u * Sl::kGroups + grp, kWave);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          q[u][v] = *reinterpret_cast<const uint4*>(codes + row * pitch + sl.col[v]);
-          f[u][v] = scales[row * nb + sl.col[v] / kAct8Block];
+          q[u][v] = *reinterpret_cast<const uint4*>(codes + row * pitch + sl.col(v));
+          f[u][v] = scales[row * nb + sl.col(v) / kAct8Block];
         }
       }
 #pragma unroll
@@ -495,14 +493,14 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
         }
       }
     }
-    if (s == 0 && lane < cnt) {
+    if (at.slice == 0 && lane < cnt) {
       dz[mine.z] = d;
       sum += d;
     }
   }
   join_groups<P>(acc);
-  store_joined(dw_up_t + static_cast<int64_t>(j) * dm, sl, acc);
-  if (s == 0) {
+  store_joined<P>(dw_up_t + static_cast<int64_t>(j) * dm, sl, acc);
+  if (at.slice == 0) {
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
     if (lane == 0) db[j] = sum;
@@ -511,17 +509,18 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
 
 // dx: a wave per (token row, slice): dx[n][slice] = sum of dz W_up^T[j], in
 // float32, rounded once.
-template <typename E, int P, int NV, bool HALF>
+template <typename E, int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
     const int32_t* __restrict__ row_off, const int32_t* __restrict__ cols,
-    const float* __restrict__ dz, const E* __restrict__ w_up_t, int64_t n_rows, int dm, int S,
+    const float* __restrict__ dz, const E* __restrict__ w_up_t, int64_t n_rows, int dm, int log_s,
     int sw, E* __restrict__ dx) {
-  typedef Slice<P, NV, HALF> Sl;
+  typedef Slice<16 / sizeof(E), P, NV, FULL> Sl;
+  typedef Row<E, Sl> R;
   const int lane = lane_id(), grp = lane / P;
-  const int s = blockIdx.x % S;
-  const int64_t n = static_cast<int64_t>(blockIdx.x / S) * kWaves + threadIdx.x / kWave;
+  const Place at(log_s);
+  const int64_t n = at.item;
   if (n >= n_rows) return;
-  const Sl sl(s, sw, dm);
+  const Sl sl(at.slice, sw);
   const int b = row_off[n], L = row_off[n + 1] - b;
   float acc[Sl::kAcc];
 #pragma unroll
@@ -532,25 +531,20 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
     const float my_dz = dz[b + base + min(lane, cnt - 1)];
     auto step = [&](int e0, auto check) {
       constexpr bool CHECK = decltype(check)::value;
-      Vec16<E> w[Sl::kSteps][NV];
+      R w[Sl::kSteps];
       float f[Sl::kSteps];
 #pragma unroll
       for (int u = 0; u < Sl::kSteps; ++u) {
         const int e = e0 + u * Sl::kGroups + grp;
         const int64_t j = __shfl(my_col, e, kWave);
         f[u] = __shfl(my_dz, e, kWave);
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          w[u][v].load(w_up_t + j * dm + sl.col[v], sl.half(v));
+        w[u].load(w_up_t + j * dm, sl);
       }
 #pragma unroll
       for (int u = 0; u < Sl::kSteps; ++u) {
         const bool live = !CHECK || e0 + u * Sl::kGroups + grp < cnt;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if (CHECK) w[u][v].keep(live);
-          w[u][v].fma32(acc + v * kCols, live ? f[u] : 0.f);
-        }
+        if (CHECK) w[u].keep(live, sl);
+        w[u].fma32(acc, live ? f[u] : 0.f);
       }
     };
     int e0 = 0;
@@ -558,7 +552,7 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
     if (e0 < cnt) step(e0, std::true_type{});
   }
   join_groups<P>(acc);
-  store_joined(dx + n * dm, sl, acc);
+  store_joined<P>(dx + n * dm, sl, acc);
 }
 
 // Column slices: S of sw columns, S up to 8 (one per XCD) as long as a slice
@@ -624,23 +618,24 @@ Space carve(const Geometry& g, int64_t cap, void* ws) {
 
 unsigned blocks(int64_t items, int per) { return static_cast<unsigned>((items + per - 1) / per); }
 
-template <typename E, int P, int NV, bool HALF>
+template <typename E, int P, int NV, bool FULL>
 hipError_t gather_passes(const Geometry& g, const SlicePlan& sp, const Space& w, const BwdAct8& x8,
                          const void* w_up_t, const void* w_down, const void* dy, void* dx,
                          float* dw_up_t, float* db, float* dw_down, hipStream_t s) {
   const unsigned by_neuron = blocks(g.d_ff, kWaves) * static_cast<unsigned>(sp.S);
-  a8_down_kernel<E, P, NV, HALF><<<by_neuron, kThreads, 0, s>>>(
+  const int log_s = __builtin_ctz(static_cast<unsigned>(sp.S));
+  a8_down_kernel<E, P, NV, FULL><<<by_neuron, kThreads, 0, s>>>(
       w.neuron_off, w.ents, static_cast<const E*>(dy), static_cast<const E*>(w_down), g.d_ff,
-      g.d_model, sp.S, sp.sw, w.part, w.entries, dw_down);
+      g.d_model, log_s, sp.sw, w.part, w.entries, dw_down);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  a8_up_kernel<P, NV, HALF><<<by_neuron, kThreads, 0, s>>>(
+  a8_up_kernel<P, NV, FULL><<<by_neuron, kThreads, 0, s>>>(
       w.neuron_off, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model), act8_blocks(g.d_model),
-      w.part, w.entries, sp.S, g.d_ff, g.d_model, sp.S, sp.sw, w.dz, dw_up_t, db);
+      w.part, w.entries, sp.S, g.d_ff, g.d_model, log_s, sp.sw, w.dz, dw_up_t, db);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  a8_dx_kernel<E, P, NV, HALF><<<blocks(g.n_rows, kWaves) * static_cast<unsigned>(sp.S), kThreads, 0,
+  a8_dx_kernel<E, P, NV, FULL><<<blocks(g.n_rows, kWaves) * static_cast<unsigned>(sp.S), kThreads, 0,
                            s>>>(w.row_off, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows,
-                                g.d_model, sp.S, sp.sw, static_cast<E*>(dx));
+                                g.d_model, log_s, sp.sw, static_cast<E*>(dx));
   return hipGetLastError();
 }
 
@@ -680,20 +675,21 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
       w.neuron_off, w.row_off, w.ents, w.cols);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const SlicePlan sp = slice_plan(g.d_model);
-  auto go = [&](auto p, auto nv, auto half) {
-    return gather_passes<E, decltype(p)::value, decltype(nv)::value, decltype(half)::value>(
-        g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db, dw_down, s);
-  };
-  auto by_half = [&](auto p, auto nv) {
-    return g.d_model % kCols == 0 ? go(p, nv, std::false_type{}) : go(p, nv, std::true_type{});
+  auto go = [&](auto p, auto nv) {
+    constexpr int P = decltype(p)::value, NV = decltype(nv)::value;
+    if (sp.sw == P * NV * kCols)
+      return gather_passes<E, P, NV, true>(g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db,
+                                           dw_down, s);
+    return gather_passes<E, P, NV, false>(g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db,
+                                          dw_down, s);
   };
   typedef std::integral_constant<int, 1> One;
   if (sp.nvl == 2)
-    return by_half(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
   if (sp.nvl != 1) return hipErrorInvalidValue;
-  if (sp.P == 16) return by_half(std::integral_constant<int, 16>{}, One{});
-  if (sp.P == 32) return by_half(std::integral_constant<int, 32>{}, One{});
-  return by_half(std::integral_constant<int, 64>{}, One{});
+  if (sp.P == 16) return go(std::integral_constant<int, 16>{}, One{});
+  if (sp.P == 32) return go(std::integral_constant<int, 32>{}, One{});
+  return go(std::integral_constant<int, 64>{}, One{});
 }
 
 }  // namespace
