@@ -51,16 +51,37 @@ __global__ __launch_bounds__(kThreads) void a8_dense_kernel(BwdHybrid hy, int64_
   if (r >= 0 && r < n_rows) row_slot[r] = static_cast<int32_t>(m + 1);
 }
 
-// One wave per token row visits its non-zeros in ascending neuron order:
-// visit(rank within the row, neuron, h).  Returns how many there are.
-template <typename E, typename Visit>
+// A wave's non-zeros on their way from a row to the lists: a step of the row
+// appends at most kStep, full groups of 64 are then taken one per lane, so
+// that the dependent reads and atomics of 64 of them run together.
+constexpr int kStep = 8 * kWave;
+struct Stage {
+  int j[kStep + kWave];
+  float h[kStep + kWave];
+};
+
+// One wave per token row: take(rank within the row, neuron, h) for its
+// non-zeros in ascending neuron order, a lane each.  Returns how many there are.
+template <typename E, typename Take>
 __device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slot, int dff, int T,
-                                         int C, int nt, Visit visit) {
+                                         int C, int nt, Stage& st, Take take) {
   typedef ElemTraits<E> Tr;
   constexpr int V = 16 / sizeof(E);
   constexpr int U = 4;  // dense vectors in flight
   const int lane = lane_id();
-  int run = 0;
+  int done = 0, held = 0;  // taken, and staged
+  auto take_full = [&] {
+    __builtin_amdgcn_wave_barrier();
+    int at = 0;
+    for (; held - at >= kWave; at += kWave, done += kWave)
+      take(done + lane, st.j[at + lane], st.h[at + lane]);
+    if (at == 0) return;
+    held -= at;
+    const int j = st.j[at + lane];
+    const float h = st.h[at + lane];
+    __builtin_amdgcn_wave_barrier();
+    st.j[lane] = j, st.h[lane] = h;
+  };
   if (slot > 0) {
     const E* row = static_cast<const E*>(hy.dense_values) + static_cast<int64_t>(slot - 1) * dff;
     for (int c0 = 0; c0 < dff; c0 += U * kWave * V) {
@@ -83,29 +104,49 @@ __device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slo
           all += popc64(m);
         }
         if (all == 0) continue;
-        int p = run + below;
+        int p = held + below;
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (Tr::abs_bits(v[e]) != 0u)
-            visit(p++, c0 + (u * kWave + lane) * V + e, Tr::to_f32(v[e]));
-        run += all;
+          if (Tr::abs_bits(v[e]) != 0u) {
+            st.j[p] = c0 + (u * kWave + lane) * V + e;
+            st.h[p++] = Tr::to_f32(v[e]);
+          }
+        held += all;
+        take_full();
       }
     }
-    return run;
+  } else {
+    const int nslots = nt * C;
+    const E* vrow = static_cast<const E*>(hy.vals) + n * nslots;
+    const uint8_t* irow = hy.idx + n * nslots;
+    for (int s0 = 0; s0 < nslots; s0 += U * kWave) {
+      int local[U], tile[U];
+      E v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s = s0 + u * kWave + lane;
+        tile[u] = s / C;
+        local[u] = T;
+        if (s < nslots && s - tile[u] * C < static_cast<int>(hy.cnt[n * nt + tile[u]]))
+          local[u] = irow[s];
+        v[u] = s < nslots ? vrow[s] : E(0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint64_t m = wave_ballot(local[u] < T);
+        if (local[u] < T) {
+          const int p = held + popc_below(m);
+          st.j[p] = tile[u] * T + local[u];
+          st.h[p] = Tr::to_f32(v[u]);
+        }
+        held += popc64(m);
+      }
+      take_full();
+    }
   }
-  const int nslots = nt * C;
-  const E* vrow = static_cast<const E*>(hy.vals) + n * nslots;
-  const uint8_t* irow = hy.idx + n * nslots;
-  for (int s0 = 0; s0 < nslots; s0 += kWave) {
-    const int s = s0 + lane;
-    const int t = s / C;
-    int local = T;
-    if (s < nslots && s - t * C < static_cast<int>(hy.cnt[n * nt + t])) local = irow[s];
-    const uint64_t m = wave_ballot(local < T);
-    if (local < T) visit(run + popc_below(m), t * T + local, Tr::to_f32(vrow[s]));
-    run += popc64(m);
-  }
-  return run;
+  __builtin_amdgcn_wave_barrier();
+  if (lane < held) take(done + lane, st.j[lane], st.h[lane]);
+  return done + held;
 }
 
 // Bit n % 64 of bits[j][n / 64] for every non-zero; row_count[n] = theirs.
@@ -114,13 +155,15 @@ __global__ __launch_bounds__(kThreads) void a8_mark_kernel(
     BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
     const int32_t* __restrict__ row_slot, int64_t n_words, unsigned long long* __restrict__ bits,
     int32_t* __restrict__ row_count) {
+  __shared__ Stage stage[kWaves];
   const int64_t n = wave_index();
   if (n >= n_rows) return;
   const unsigned long long bit = 1ull << (n & 63);
   unsigned long long* word = bits + (n >> 6);
-  const int c = visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, [&](int, int j, float) {
-    atomicOr(word + static_cast<int64_t>(j) * n_words, bit);
-  });
+  const int c = visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, stage[threadIdx.x / kWave],
+                             [&](int, int j, float) {
+                               atomicOr(word + static_cast<int64_t>(j) * n_words, bit);
+                             });
   if (lane_id() == 0) row_count[n] = c;
 }
 
@@ -206,11 +249,13 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
     const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
     const int32_t* __restrict__ neuron_off, const int32_t* __restrict__ row_off,
     int4* __restrict__ ents, int32_t* __restrict__ cols) {
+  __shared__ Stage stage[kWaves];
   const int64_t n = wave_index();
   if (n >= n_rows) return;
   const unsigned long long bit = 1ull << (n & 63);
   const int first = row_off[n];
-  visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, [&](int rank, int j, float h) {
+  visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, stage[threadIdx.x / kWave],
+               [&](int rank, int j, float h) {
     const int64_t w = static_cast<int64_t>(j) * n_words + (n >> 6);
     const int at = neuron_off[j] + lpre[w] + __popcll(bits[w] & (bit - 1));
     ents[at] = make_int4(static_cast<int>(n), static_cast<int>(__float_as_uint(h)), first + rank,
@@ -225,12 +270,13 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
 // of V columns (16 bytes of the gathered type): chunk k of lane l is columns
 // (k P + l) V ..., so that one load of the group is one run of bytes.
 // FULL: the group covers the slice exactly.
-template <int V, int P, int NV, bool FULL>
+template <int V, int P, int NV, bool FULL, int FLIGHT = 8>
 struct Slice {
   static constexpr int kAcc = NV * kCols, kChunks = kAcc / V;
   static constexpr int kGroups = kWave / P;
-  static constexpr int kSteps = kGroups * NV >= 8 ? 1 : 8 / (kGroups * NV);  // rows in flight
-  static constexpr int kEntries = kGroups * kSteps;                          // rows per step
+  // rows per step, in flight together: FLIGHT groups of columns
+  static constexpr int kSteps = kGroups * NV >= FLIGHT ? 1 : FLIGHT / (kGroups * NV);
+  static constexpr int kEntries = kGroups * kSteps;
   int first;  // column of the lane's chunk 0
   int lim;    // columns of the slice past `first`
   __device__ __forceinline__ Slice(int s, int sw) {
@@ -259,6 +305,11 @@ struct Row {
   __device__ __forceinline__ void load(const E* row, const Sl& sl) {
 #pragma unroll
     for (int k = 0; k < K; ++k) q[k] = *reinterpret_cast<const uint4*>(row + sl.col(k));
+  }
+  // a row that is read once
+  __device__ __forceinline__ void load_past(const E* row, const Sl& sl) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) q[k] = load_once(reinterpret_cast<const uint4*>(row + sl.col(k)));
   }
   // zero where `keep` is false or the chunk is past the slice
   __device__ __forceinline__ void keep(bool keep, const Sl& sl) {
@@ -344,7 +395,8 @@ __device__ __forceinline__ void store_joined(O* row, const Sl& sl, const float* 
     if (!sl.may_write(first + i)) continue;
     O* to = row + sl.col_of(first + i);
     if constexpr (sizeof(O) == 4) {
-      *reinterpret_cast<float4*>(to) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      store_once(to, make_uint4(__float_as_uint(acc[i]), __float_as_uint(acc[i + 1]),
+                                __float_as_uint(acc[i + 2]), __float_as_uint(acc[i + 3])));
     } else {
       uint32_t w[2];
 #pragma unroll
@@ -362,7 +414,9 @@ struct Place {
   int64_t item;  // this wave's
   __device__ __forceinline__ explicit Place(int log_s) {
     slice = static_cast<int>(blockIdx.x) & ((1 << log_s) - 1);
-    item = static_cast<int64_t>(blockIdx.x >> log_s) * kWaves + threadIdx.x / kWave;
+    // in a scalar register, as are its offsets and counts then
+    item = static_cast<int64_t>(blockIdx.x >> log_s) * kWaves +
+           __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   }
 };
 
@@ -385,7 +439,7 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
 #pragma unroll
   for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
   R w;
-  w.load(w_down + static_cast<int64_t>(j) * dm, sl);
+  w.load_past(w_down + static_cast<int64_t>(j) * dm, sl);
   if (!FULL) w.keep(true, sl);
   for (int base = 0; base < L; base += kWave) {
     const int cnt = min(kWave, L - base);
@@ -431,14 +485,15 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
 // Up: a wave per (neuron, slice).  dz = the n_part partial dots added in slice
 // order; slice 0 stores it at its place in the row order and adds db[j];
 // dW_up^T[j][slice] = sum of (dz * scale) * code.  A chunk's 16 columns lie in
-// one block of scales.
+// one block of scales.  Four rows in flight, not eight: the registers saved are
+// worth more as waves (76 against 91 us at the 1B layer).
 template <int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_up_kernel(
     const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
     const int8_t* __restrict__ codes, const float* __restrict__ scales, int pitch, int nb,
     const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int log_s, int sw,
     float* __restrict__ dz, float* __restrict__ dw_up_t, float* __restrict__ db) {
-  typedef Slice<kCols, P, NV, FULL> Sl;
+  typedef Slice<kCols, P, NV, FULL, 4> Sl;
   const int lane = lane_id(), grp = lane / P;
   const Place at(log_s);
   if (at.item >= dff) return;
@@ -556,8 +611,8 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
 }
 
 // Column slices: S of sw columns, S up to 8 (one per XCD) as long as a slice
-// keeps 256 columns and whole vector groups; P lanes of nv vector groups cover
-// one (nv = 0: too wide).
+// keeps 256 columns and whole chunks of every pass; P lanes of 16 nv columns
+// cover one (nv = 0: too wide).
 SlicePlan slice_plan(int dm) {
   SlicePlan p;
   p.S = 8;
@@ -618,25 +673,53 @@ Space carve(const Geometry& g, int64_t cap, void* ws) {
 
 unsigned blocks(int64_t items, int per) { return static_cast<unsigned>((items + per - 1) / per); }
 
-template <typename E, int P, int NV, bool FULL>
-hipError_t gather_passes(const Geometry& g, const SlicePlan& sp, const Space& w, const BwdAct8& x8,
-                         const void* w_up_t, const void* w_down, const void* dy, void* dx,
-                         float* dw_up_t, float* db, float* dw_down, hipStream_t s) {
-  const unsigned by_neuron = blocks(g.d_ff, kWaves) * static_cast<unsigned>(sp.S);
-  const int log_s = __builtin_ctz(static_cast<unsigned>(sp.S));
-  a8_down_kernel<E, P, NV, FULL><<<by_neuron, kThreads, 0, s>>>(
-      w.neuron_off, w.ents, static_cast<const E*>(dy), static_cast<const E*>(w_down), g.d_ff,
-      g.d_model, log_s, sp.sw, w.part, w.entries, dw_down);
-  hipError_t e = hipGetLastError();
+// fn(P, NV, FULL) as types for the plan's widths.
+template <typename Fn>
+hipError_t with_plan(const SlicePlan& sp, Fn fn) {
+  auto go = [&](auto p, auto nv) {
+    return sp.sw == decltype(p)::value * decltype(nv)::value * kCols ? fn(p, nv, std::true_type{})
+                                                                     : fn(p, nv, std::false_type{});
+  };
+  typedef std::integral_constant<int, 1> One;
+  if (sp.nvl == 2)
+    return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (sp.nvl != 1) return hipErrorInvalidValue;
+  if (sp.P == 16) return go(std::integral_constant<int, 16>{}, One{});
+  if (sp.P == 32) return go(std::integral_constant<int, 32>{}, One{});
+  return go(std::integral_constant<int, 64>{}, One{});
+}
+
+template <typename E>
+hipError_t gather_passes(const Geometry& g, const Space& w, const BwdAct8& x8, const void* w_up_t,
+                         const void* w_down, const void* dy, void* dx, float* dw_up_t, float* db,
+                         float* dw_down, hipStream_t s) {
+  const SlicePlan sp = slice_plan(g.d_model);
+  const unsigned neurons = blocks(g.d_ff, kWaves), rows = blocks(g.n_rows, kWaves);
+  auto log2 = [](int v) { return __builtin_ctz(static_cast<unsigned>(v)); };
+  hipError_t e = with_plan(sp, [&](auto p, auto nv, auto full) {
+    a8_down_kernel<E, decltype(p)::value, decltype(nv)::value, decltype(full)::value>
+        <<<neurons * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
+            w.neuron_off, w.ents, static_cast<const E*>(dy), static_cast<const E*>(w_down), g.d_ff,
+            g.d_model, log2(sp.S), sp.sw, w.part, w.entries, dw_down);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
-  a8_up_kernel<P, NV, FULL><<<by_neuron, kThreads, 0, s>>>(
-      w.neuron_off, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model), act8_blocks(g.d_model),
-      w.part, w.entries, sp.S, g.d_ff, g.d_model, log_s, sp.sw, w.dz, dw_up_t, db);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  a8_dx_kernel<E, P, NV, FULL><<<blocks(g.n_rows, kWaves) * static_cast<unsigned>(sp.S), kThreads, 0,
-                           s>>>(w.row_off, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows,
-                                g.d_model, log_s, sp.sw, static_cast<E*>(dx));
-  return hipGetLastError();
+  e = with_plan(sp, [&](auto p, auto nv, auto full) {
+    a8_up_kernel<decltype(p)::value, decltype(nv)::value, decltype(full)::value>
+        <<<neurons * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
+            w.neuron_off, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model),
+            act8_blocks(g.d_model), w.part, w.entries, sp.S, g.d_ff, g.d_model, log2(sp.S), sp.sw,
+            w.dz, dw_up_t, db);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  return with_plan(sp, [&](auto p, auto nv, auto full) {
+    a8_dx_kernel<E, decltype(p)::value, decltype(nv)::value, decltype(full)::value>
+        <<<rows * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
+            w.row_off, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows, g.d_model, log2(sp.S),
+            sp.sw, static_cast<E*>(dx));
+    return hipGetLastError();
+  });
 }
 
 template <typename E>
@@ -674,22 +757,7 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
       hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, w.row_slot, n_words, w.bits, w.lpre,
       w.neuron_off, w.row_off, w.ents, w.cols);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const SlicePlan sp = slice_plan(g.d_model);
-  auto go = [&](auto p, auto nv) {
-    constexpr int P = decltype(p)::value, NV = decltype(nv)::value;
-    if (sp.sw == P * NV * kCols)
-      return gather_passes<E, P, NV, true>(g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db,
-                                           dw_down, s);
-    return gather_passes<E, P, NV, false>(g, sp, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db,
-                                          dw_down, s);
-  };
-  typedef std::integral_constant<int, 1> One;
-  if (sp.nvl == 2)
-    return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (sp.nvl != 1) return hipErrorInvalidValue;
-  if (sp.P == 16) return go(std::integral_constant<int, 16>{}, One{});
-  if (sp.P == 32) return go(std::integral_constant<int, 32>{}, One{});
-  return go(std::integral_constant<int, 64>{}, One{});
+  return gather_passes<E>(g, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db, dw_down, s);
 }
 
 }  // namespace
