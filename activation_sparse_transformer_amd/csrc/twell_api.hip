@@ -33,7 +33,8 @@ int check_shape(const twell_shape* s, bool need_model) {
   return TWELL_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 // ELL rows: one tile spanning the row (tile == d_ff), capacity = width.
 int check_ell_shape(const twell_shape* s, bool need_model) {
@@ -707,7 +708,8 @@ TWELL_EXPORT int twell_embed_forward(const twell_embed_shape* shape, const void*
   if (rc != TWELL_OK) return rc;
   if (shape->n_tokens > 0 && (table == nullptr || tokens == nullptr || out == nullptr))
     return TWELL_ERR_INVALID_ARG;
-  if (!aligned16(table) || !aligned16(tokens) || !aligned16(out)) return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(table) || !aligned(tokens, shape->index_bytes) || !aligned16(out))
+    return TWELL_ERR_INVALID_ARG;
   return hip_status(launch_embed_forward(
       shape->n_tokens, shape->vocab, shape->d_model, elem_bytes(shape->dtype), shape->index_bytes,
       shape->scale, table, tokens, out, static_cast<hipStream_t>(stream)));
@@ -725,7 +727,8 @@ TWELL_EXPORT int twell_embed_backward(const twell_embed_shape* shape, const void
   if (rc != TWELL_OK) return rc;
   if (shape->n_tokens > 0 && (dout == nullptr || tokens == nullptr)) return TWELL_ERR_INVALID_ARG;
   if (dtable == nullptr || workspace == nullptr) return TWELL_ERR_INVALID_ARG;
-  if (!aligned16(dout) || !aligned16(tokens) || !aligned16(dtable) || !aligned16(workspace))
+  if (!aligned16(dout) || !aligned(tokens, shape->index_bytes) || !aligned16(dtable) ||
+      !aligned16(workspace))
     return TWELL_ERR_INVALID_ARG;
   const EmbedGradBufs b = embed_grad_carve(shape->n_tokens, shape->vocab, workspace);
   if (workspace_bytes < b.bytes) return TWELL_ERR_WORKSPACE;
@@ -785,8 +788,9 @@ TWELL_EXPORT int twell_logprob_forward(const twell_logprob_shape* shape, const v
       return TWELL_ERR_INVALID_ARG;
     if (shape->top > 0 && (top_ids == nullptr || top_logp == nullptr)) return TWELL_ERR_INVALID_ARG;
   }
-  if (!aligned16(logits) || !aligned16(targets) || !aligned16(logp) || !aligned16(entropy) ||
-      !aligned16(lse) || !aligned16(top_ids) || !aligned16(top_logp) || !aligned16(workspace))
+  if (!aligned16(logits) || !aligned(targets, shape->index_bytes) || !aligned(logp, 4) ||
+      !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 4) || !aligned(top_logp, 4) ||
+      !aligned16(workspace))
     return TWELL_ERR_INVALID_ARG;
   LogprobArgs a = logprob_args(shape);
   const size_t need = logprob_carve(&a, elem_bytes(shape->dtype), workspace);
@@ -817,8 +821,8 @@ TWELL_EXPORT int twell_logprob_backward(const twell_logprob_shape* shape, const 
       return TWELL_ERR_INVALID_ARG;
     if (dlogits == logits && out_stride != shape->row_stride) return TWELL_ERR_INVALID_ARG;
   }
-  if (!aligned16(logits) || !aligned16(targets) || !aligned16(lse) || !aligned16(entropy) ||
-      !aligned16(dlogp) || !aligned16(dentropy) || !aligned16(dlogits))
+  if (!aligned16(logits) || !aligned(targets, shape->index_bytes) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || !aligned(dlogp, 4) || !aligned(dentropy, 4) || !aligned16(dlogits))
     return TWELL_ERR_INVALID_ARG;
   const LogprobGradArgs a{logits,        targets,      shape->n_rows, shape->row_stride,
                           out_stride,    shape->vocab, shape->scale,  lse,

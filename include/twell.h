@@ -460,8 +460,9 @@ int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, con
 /* ---- The token embedding in front of the layers and its gradient.  The
  * pages train and run whole language models of such layers ("Nvidia and Sakana
  * make LLMs 30% faster by doing less math"); defined by this interface.
- * tokens [n_tokens] are int32 or int64 (index_bytes 4 or 8); an id outside
- * [0, vocab) is padding: its output row is zero and it adds to no gradient.
+ * tokens [n_tokens] are int32 or int64 (index_bytes 4 or 8; aligned to that
+ * only, so that a part of a longer text will do); an id outside [0, vocab) is
+ * padding: its output row is zero and it adds to no gradient.
  * Requirements: 0 <= n_tokens < 2^31; vocab > 0; d_model > 0 and a multiple of
  * 8; vocab * d_model < 2^33 (TWELL_ERR_UNSUPPORTED); dtype a twell_dtype; scale
  * finite; reserved 0. */
@@ -500,7 +501,8 @@ int twell_embed_backward(const twell_embed_shape* shape, const void* dout, const
  *  - logits rows are row_stride elements apart (row_stride >= vocab; any
  *    parity: rows need no alignment, the first element does).
  *  - targets [n_rows] are int32 or int64 (index_bytes 4 or 8); a target outside
- *    [0, vocab) is ignored: its logp is 0 and has no gradient.
+ *    [0, vocab) is ignored: its logp is 0 and has no gradient.  targets and the
+ *    arrays per row are aligned to their elements only.
  *  - A place with x = -inf is masked: probability 0, never an alternative.
  *    A row with nothing else has lse = -inf, entropy 0, logp = -inf and a zero
  *    gradient.  Finite masks (the type's lowest value) are ordinary values.

@@ -128,6 +128,22 @@ def test_gradient_against_differences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_part_of_a_longer_text(index):
+    """Ids that start anywhere in their own array."""
+    say(f"embed unaligned ids {index}")
+    text = token_ids(4, 300, 40, index, "zipf").cuda()
+    table = torch.randn((40, 64), device="cuda")
+    for first in (1, 2, 3):
+        part = text[first:]
+        assert torch.equal(twell.twell_embed_forward(table, part),
+                           twell.twell_embed_forward(table, part.clone()))
+        dout = torch.randn((len(part), 64), device="cuda")
+        assert torch.equal(twell.twell_embed_backward(dout, part, 40),
+                           twell.twell_embed_backward(dout, part.clone(), 40))
+
+
+@pytest.mark.gpu
 def test_special_values_stay_in_their_rows():
     """NaN and infinite gradients reach their own id only; no token leaves the table zero."""
     say("embed special values")
@@ -243,7 +259,7 @@ def test_host_checks():
                dict(dtype=3), dict(index_bytes=2), dict(scale=float("inf")), dict(reserved=1)):
         assert fwd(shape(**kw), p, p, p) == bad, kw
         assert lib.twell_embed_backward_workspace_size(ctypes.byref(shape(**kw))) == 0
-    assert fwd(shape(), None, p, p) == bad and fwd(shape(), p, p + 8, p) == bad
+    assert fwd(shape(), None, p, p) == bad and fwd(shape(), p, p + 4, p) == bad and fwd(shape(), p + 8, p, p) == bad
     assert lib.twell_embed_forward(None, p, p, p, None) == bad
     need = lib.twell_embed_backward_workspace_size(ctypes.byref(shape()))
     bwd = lambda *a: lib.twell_embed_backward(ctypes.byref(shape()), *a, None)

@@ -208,6 +208,26 @@ def test_backward_against_differences():
 
 
 @pytest.mark.gpu
+def test_parts_of_longer_arrays():
+    """Targets and per-row arrays that start anywhere in their own arrays."""
+    say("logprob unaligned rows")
+    x, t = make(9, 50, 3000, torch.bfloat16)
+    x, t = x.cuda(), torch.cat([t[:1], t]).cuda()[1:]
+    ref = twell.twell_logprob_forward(x, t.clone(), top=3)
+    shift = lambda a: torch.cat([a.reshape(-1)[:1], a.reshape(-1)])[1:].view(a.shape)
+    out = twell.LogProbs(*(shift(getattr(ref, f)).zero_() for f in (
+        "logp", "entropy", "lse", "top_ids", "top_logp")))
+    twell.twell_logprob_forward(x, t, top=3, out=out)
+    g = shift(torch.linspace(-1, 1, 50, device="cuda"))
+    d = twell.twell_logprob_backward(x, t, out.lse, out.entropy, g, g)
+    dref = twell.twell_logprob_backward(x, t.clone(), ref.lse, ref.entropy, g.clone(), g.clone())
+    torch.cuda.synchronize()
+    for f in ("logp", "entropy", "lse", "top_ids", "top_logp"):
+        assert torch.equal(getattr(out, f), getattr(ref, f))
+    assert torch.equal(d, dref)
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """More than 2^31 logits: the last row is scored and differentiated."""
     say("logprob offsets past 2^31")
@@ -323,7 +343,8 @@ def test_host_checks():
         assert lib.twell_logprob_workspace_size(ctypes.byref(shape(**kw))) == 0
     assert fwd(shape(n_rows=1 << 27)) == twell.TWELL_ERR_UNSUPPORTED
     assert fwd(shape(), x=None) == bad and fwd(shape(), ids=None) == bad
-    assert fwd(shape(), x=p + 2) == bad and fwd(shape(), logp=p + 4) == bad
+    assert fwd(shape(), x=p + 8) == bad and fwd(shape(), logp=p + 2) == bad
+    assert fwd(shape(), t=p + 4) == bad
     s = shape(vocab=100000, row_stride=100000)
     need = lib.twell_logprob_workspace_size(ctypes.byref(s))
     assert need > 0 and fwd(s, ws=None, wsb=need) == bad
