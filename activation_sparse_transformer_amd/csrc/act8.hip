@@ -17,6 +17,7 @@ namespace twell {
 namespace {
 
 constexpr int kActThreads = 256;
+constexpr int kPackUnits = 2;
 
 // A lane takes one 16-byte vector of x: 8 (bf16) or 4 (float32) columns.
 template <typename E>
@@ -81,8 +82,10 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
-// kLanes lanes take one (row, block): the largest magnitude as an integer
-// (NaN bits exceed infinity's), then each lane's codes.  Bound by HBM.
+// kLanes lanes take one (row, block) at a time: the largest magnitude as an
+// integer (NaN bits exceed infinity's), then each lane's codes.  kPackUnits
+// blocks per lane, read together, keep enough bytes in flight behind the
+// reductions.  Bound by HBM.
 template <typename E>
 __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
     const E* __restrict__ x, int64_t n_units, int d, int nb, int pitch,
@@ -90,53 +93,62 @@ __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
   typedef ActLane<E> A;
   constexpr int kUnits = kActThreads / A::kLanes;
   const int l = threadIdx.x % A::kLanes;
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kUnits;
-  const int i = threadIdx.x / A::kLanes;
-  if (u0 + i >= n_units) return;
-  int64_t row;
-  int b;
-  unit_of(u0, i, nb, row, b);
-  const int c = b * kAct8Block + l * A::kCols;
-  float f[A::kCols];
-  widen<E>(c < d ? load_once(reinterpret_cast<const uint4*>(x + row * d + c))
-                 : make_uint4(0, 0, 0, 0), f);
-  uint32_t top = 0;
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kUnits * kPackUnits);
+  int64_t row[kPackUnits];
+  int b[kPackUnits];
+  uint4 v[kPackUnits];
 #pragma unroll
-  for (int k = 0; k < A::kCols; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
-  top = group_max<A::kLanes>(top);
-  const float a = __uint_as_float(top);
-  const bool finite = top < 0x7f800000u;
-  if (l == 0) {
-    float scale = a / 127.f;
-    // near the largest float the product 127 * scale may round past it
-    if (scale * 127.f > 3.402823466e38f) scale = __uint_as_float(__float_as_uint(scale) - 1u);
-    scales[row * nb + b] = finite ? scale : __uint_as_float(0x7fc00000u);
+  for (int n = 0; n < kPackUnits; ++n) {
+    const int i = n * kUnits + threadIdx.x / A::kLanes;
+    unit_of(u0, i, nb, row[n], b[n]);
+    const int c = b[n] * kAct8Block + l * A::kCols;
+    v[n] = u0 + i < n_units && c < d ? load_once(reinterpret_cast<const uint4*>(x + row[n] * d + c))
+                                     : make_uint4(0, 0, 0, 0);
   }
-  // a power of two that keeps x * 127 and the quotient in the normal range
-  const float up = a > 0x1p100f ? 0x1p-32f : a < 0x1p-90f ? 0x1p60f : 1.f;
-  const float den = a * up, r = 1.f / den, k127 = 127.f * up;
-  uint32_t w[A::kWords];
 #pragma unroll
-  for (int j = 0; j < A::kWords; ++j) {
-    uint32_t u[4];
+  for (int n = 0; n < kPackUnits; ++n) {
+    if (u0 + n * kUnits + threadIdx.x / A::kLanes >= n_units) return;
+    const int c = b[n] * kAct8Block + l * A::kCols;
+    float f[A::kCols];
+    widen<E>(v[n], f);
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // the quotient from the rounded reciprocal and one exact remainder: a
-      // product, a fused remainder and a correction instead of a division
-      const float t = f[4 * j + k] * k127;
-      const float q0 = t * r;
-      const float q = fmaf(fmaf(-q0, den, t), r, q0);
-      // 1.5 * 2^23 + q: the sum's last byte is q rounded to even
-      u[k] = __float_as_uint(q + 0x1.8p23f);
+    for (int k = 0; k < A::kCols; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
+    top = group_max<A::kLanes>(top);
+    const float a = __uint_as_float(top);
+    const bool finite = top < 0x7f800000u;
+    if (l == 0) {
+      float scale = a / 127.f;
+      // near the largest float the product 127 * scale may round past it
+      if (scale * 127.f > 3.402823466e38f) scale = __uint_as_float(__float_as_uint(scale) - 1u);
+      scales[row[n] * nb + b[n]] = finite ? scale : __uint_as_float(0x7fc00000u);
     }
-    const uint32_t lo = perm_b32(u[1], u[0], 0x0c0c0400u), hi = perm_b32(u[3], u[2], 0x0c0c0400u);
-    w[j] = finite && top != 0 ? lo | hi << 16 : 0u;
+    // a power of two that keeps x * 127 and the quotient in the normal range
+    const float up = a > 0x1p100f ? 0x1p-32f : a < 0x1p-90f ? 0x1p60f : 1.f;
+    const float den = a * up, r = 1.f / den, k127 = 127.f * up;
+    uint32_t w[A::kWords];
+#pragma unroll
+    for (int j = 0; j < A::kWords; ++j) {
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // the quotient from the rounded reciprocal and one exact remainder: a
+        // product, a fused remainder and a correction instead of a division
+        const float t = f[4 * j + k] * k127;
+        const float q0 = t * r;
+        const float q = fmaf(fmaf(-q0, den, t), r, q0);
+        // 1.5 * 2^23 + q: the sum's last byte is q rounded to even
+        u[k] = __float_as_uint(q + 0x1.8p23f);
+      }
+      const uint32_t lo = perm_b32(u[1], u[0], 0x0c0c0400u);
+      const uint32_t hi = perm_b32(u[3], u[2], 0x0c0c0400u);
+      w[j] = finite && top != 0 ? lo | hi << 16 : 0u;
+    }
+    if (c >= pitch) continue;
+    int8_t* to = codes + row[n] * pitch + c;
+    if constexpr (A::kWords == 2) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(to) = w[0];
   }
-  if (c >= pitch) return;
-  if constexpr (A::kWords == 2)
-    *reinterpret_cast<uint2*>(codes + row * pitch + c) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(codes + row * pitch + c) = w[0];
 }
 
 // One lane makes one 16-byte vector of x.  Bound by HBM.
@@ -171,7 +183,7 @@ template <typename E>
 hipError_t pack(int64_t n_rows, int d, const void* x, int8_t* codes, float* scales,
                 hipStream_t s) {
   const int64_t units = n_rows * act8_blocks(d);
-  const int per = kActThreads / ActLane<E>::kLanes;
+  const int per = kActThreads / ActLane<E>::kLanes * kPackUnits;
   act8_pack_kernel<E><<<static_cast<unsigned>((units + per - 1) / per), kActThreads, 0, s>>>(
       static_cast<const E*>(x), units, d, act8_blocks(d), act8_pitch(d), codes, scales);
   return hipGetLastError();
