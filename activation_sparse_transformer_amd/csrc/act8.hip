@@ -11,7 +11,8 @@
 #include <type_traits>
 
 #include "common.h"
-#include "kernels.h"
+#include "stream_ops.h"
+#include "train_kernels.h"
 
 namespace twell {
 namespace {

@@ -17,7 +17,8 @@
 #include <type_traits>
 
 #include "common.h"
-#include "kernels.h"
+#include "stream_ops.h"
+#include "train_kernels.h"
 #include "vec_ops.h"
 
 namespace twell {

@@ -7,7 +7,8 @@
 // its token numbers in ascending order.  Sums therefore run in a fixed order
 // and repeat bit for bit, and no floating-point atomic is used.
 #include "common.h"
-#include "kernels.h"
+#include "stream_ops.h"
+#include "train_kernels.h"
 
 namespace twell {
 namespace {

@@ -3,6 +3,7 @@
 // is enqueued on the caller's stream; nothing here synchronises the host.
 #include "../../include/twell.h"
 #include "kernels.h"
+#include "train_kernels.h"
 
 #include <cmath>
 #include <mutex>

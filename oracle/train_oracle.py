@@ -1,5 +1,6 @@
 """CPU oracle of the operators around the layer in a training step: 8-bit
-activation checkpoints, the token embedding.  NumPy in float64, from the definitions."""
+activation checkpoints, the token embedding, log probabilities.  NumPy in
+float64, from the definitions."""
 from __future__ import annotations
 
 import numpy as np
