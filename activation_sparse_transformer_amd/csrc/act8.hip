@@ -86,7 +86,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 // kLanes lanes take one (row, block) at a time: the largest magnitude as an
 // integer (NaN bits exceed infinity's), then each lane's codes.  kPackUnits
 // blocks per lane, read together, keep enough bytes in flight behind the
-// reductions.  Bound by HBM.
+// reductions (1: 79 us, 2: 71, 4: 79 at 16384 x 8192 bf16, 5.7 TB/s).  Bound by
+// HBM.
 template <typename E>
 __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
     const E* __restrict__ x, int64_t n_units, int d, int nb, int pitch,
@@ -152,7 +153,8 @@ __global__ __launch_bounds__(kActThreads) void act8_pack_kernel(
   }
 }
 
-// One lane makes one 16-byte vector of x.  Bound by HBM.
+// One lane makes one 16-byte vector of x.  Bound by HBM: 16384 x 8192 bf16 73
+// us, 5.6 TB/s; 8192 x 4096 float32 25 us, 6.8 TB/s.
 template <typename E>
 __global__ __launch_bounds__(kActThreads) void act8_unpack_kernel(
     const int8_t* __restrict__ codes, const float* __restrict__ scales, int64_t n_units, int d,

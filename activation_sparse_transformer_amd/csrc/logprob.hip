@@ -330,7 +330,12 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
   }
 }
 
-// Wave i of the grid takes part i % splits of row i / splits: the row's whole
+// One pass over the logits, a wave per row (or part of one) so that nothing
+// waits on a barrier.  4096 x 131072 bf16 with 5 alternatives: 194 us, 5.5
+// TB/s, without alternatives 189; float32 6.0 TB/s.  Bound by HBM and, in bf16,
+// as much by the ten or so instruction slots per element (the exponential is
+// four): a batch prefetched ahead, or one fused multiply-add for d, change
+// nothing.  Wave i of the grid takes part i % splits of row i / splits: the row's whole
 // 16-byte vectors [part * per, (part + 1) * per), the first part also the
 // elements before the first vector and the last one those after the last.
 template <typename E, typename I, bool TOP>
@@ -395,7 +400,8 @@ __global__ __launch_bounds__(kLpThreads) void logprob_forward_kernel(const Logpr
 
 // One workgroup per row joins its parts: lane l takes part l's statistics.  The
 // parts' lists (best first) are cut at the floor that their best values give,
-// packed in any order, and merged by the first wave.
+// packed in any order, and merged by the first wave.  16 rows of 64 parts with
+// 20 alternatives: 6.6 us after the parts' own 7.6, all of it latency.
 template <typename E, typename I>
 __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobArgs a,
                                                                  int splits) {
@@ -565,7 +571,8 @@ struct GradChunk {
 };
 
 // A workgroup takes one chunk of a row; its logits are on their way before the
-// row's scalars are read.  lse is rounded to float32, which moves every p of
+// row's scalars are read (102 -> 97 us).  4096 x 32768 bf16: 95 us, 5.7 TB/s;
+// 2000 x 49999 float32 with the entropy's part: 139 us, 5.8 TB/s; bound by HBM.  lse is rounded to float32, which moves every p of
 // the row by |lse| * 2^-24 of itself; past kFarLse (a row of the type's lowest
 // values, or logits far from zero) the row's own maximum and sum are formed
 // again instead.  dlogits may be the logits, where the chunks of such a row
