@@ -286,7 +286,7 @@ __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
 
 // Up to kSortMax tokens are grouped by one workgroup, in one launch that zeroes
 // the whole table meanwhile (32768 x 2048: 44 us, 6.1 TB/s of zeros; the
-// general sequence's five launches beside the same zeroing: 56 us): a stable radix sort of the keys (id, token number)
+// general sequence's five launches, which zero as much: 56 us): a stable radix sort of the keys (id, token number)
 // by id, then the segments between changes of id.  Key i = wave * chunk +
 // round * 64 + lane keeps the tokens' order; a pass ranks a wave's keys of equal
 // digit by ballots and a running count, numbers (digit, wave) by a scan, and
@@ -371,8 +371,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
     }
     __syncthreads();
   }
-  // keys again as they are (no pass: one id), then thread t takes keys
-  // [t * rounds, (t + 1) * rounds) for the segments
+  // the sorted keys, and in them the segments: a wave numbers the changes of id
+  // in its own chunk by ballots, after those of the waves before it
 #pragma unroll
   for (int r = 0; r < kSortPer; ++r) {
     if (r >= rounds) break;
@@ -382,19 +382,33 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
   }
   if (tid < 4) lists[tid] = 0;
   __syncthreads();
-  auto head_at = [&](int i) {
-    return i == 0 || keys[i] >> kSortNBits != keys[i - 1] >> kSortNBits;
-  };
-  int heads = 0;
-  for (int i = tid * rounds; i < (tid + 1) * rounds; ++i) heads += head_at(i);
-  int at = block_scan(heads);
+  uint32_t heads = 0;  // bit r: this lane's key of round r starts a segment
+  int n_heads = 0;     // the wave's
+#pragma unroll
+  for (int r = 0; r < kSortPer; ++r) {
+    if (r >= rounds) break;
+    const int i = wave * chunk + r * kWave + lane;
+    const bool head = i == 0 || key[r] >> kSortNBits != keys[i - 1] >> kSortNBits;
+    heads |= head ? 1u << r : 0u;
+    n_heads += popc64(wave_ballot(head));
+  }
+  if (lane == 0) wave_tot[wave] = n_heads;
+  __syncthreads();
+  int at = 0, n_segs = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    at += w < wave ? wave_tot[w] : 0;
+    n_segs += wave_tot[w];
+  }
   // b.pos: where each segment starts, and the end
-  for (int i = tid * rounds; i < (tid + 1) * rounds; ++i)
-    if (head_at(i)) b.pos[at++] = i;
-  if (tid == kSortThreads - 1) b.pos[at] = total, lists[0] = at;
+  for (int r = 0; r < rounds; ++r) {
+    const bool head = (heads >> r & 1) != 0;
+    const uint64_t m = wave_ballot(head);
+    if (head) b.pos[at + popc_below(m)] = wave * chunk + r * kWave + lane;
+    at += popc64(m);
+  }
+  if (tid == 0) b.pos[n_segs] = total;
   __threadfence_block();
   __syncthreads();
-  const int n_segs = lists[0];
   for (int k = tid; k < n_segs; k += kSortThreads) {
     const int i = b.pos[k], c = b.pos[k + 1] - i;
     const int id = static_cast<int>(keys[i] >> kSortNBits);
@@ -405,7 +419,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
     else b.long_segs[atomicAdd(lists + 3, 1)] = seg;
   }
   __syncthreads();
-  if (tid < 4) b.counters[tid] = lists[tid];
+  if (tid > 0 && tid < 4) b.counters[tid] = lists[tid];
 }
 
 // acc += the rows of ranks r, r + step, ... below cnt, columns c .. c + V:
