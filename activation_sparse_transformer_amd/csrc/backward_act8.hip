@@ -46,13 +46,22 @@ __global__ __launch_bounds__(kThreads) void a8_zero_kernel(uint4* __restrict__ p
   if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// row_slot[n] = m + 1 for the stored dense row m of token row n (0: none).
-__global__ __launch_bounds__(kThreads) void a8_dense_kernel(BwdHybrid hy, int64_t n_rows,
-                                                            int32_t* __restrict__ row_slot) {
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (m >= stored_rows(hy)) return;
-  const int64_t r = hy.dense_rows[m];
-  if (r >= 0 && r < n_rows) row_slot[r] = static_cast<int32_t>(m + 1);
+// m + 1 for the stored dense row m of token row n (0: none): a search of the
+// ascending list by all lanes of the wave, 64 places a step.
+__device__ __forceinline__ int dense_slot(const BwdHybrid& hy, int64_t n) {
+  const int lane = lane_id();
+  int lo = 0, hi = static_cast<int>(stored_rows(hy));
+  while (hi - lo > kWave) {
+    const int step = (hi - lo + kWave - 1) / kWave;
+    const int i = lo + lane * step;
+    const int under = popc64(wave_ballot(i < hi && hy.dense_rows[i] <= n));
+    if (under == 0) return 0;
+    lo += (under - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const uint64_t at =
+      wave_ballot(lo + lane < hi && hy.dense_rows[lo + lane] == n);
+  return at != 0 ? lo + __builtin_ctzll(at) + 1 : 0;
 }
 
 // A wave's non-zeros on their way from a row to the lists: a step of the row
@@ -157,14 +166,13 @@ __device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slo
 template <typename E>
 __global__ __launch_bounds__(kThreads) void a8_mark_kernel(
     BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
-    const int32_t* __restrict__ row_slot, int64_t n_words, unsigned long long* __restrict__ bits,
-    int32_t* __restrict__ row_count) {
+    int64_t n_words, unsigned long long* __restrict__ bits, int32_t* __restrict__ row_count) {
   __shared__ Stage stage[kWaves];
   const int64_t n = wave_index();
   if (n >= n_rows) return;
   const unsigned long long bit = 1ull << (n & 63);
   unsigned long long* word = bits + (n >> 6);
-  const int c = visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, stage[threadIdx.x / kWave],
+  const int c = visit_row<E>(hy, n, dense_slot(hy, n), dff, T, C, nt, stage[threadIdx.x / kWave],
                              [&](int, int j, float) {
                                atomicOr(word + static_cast<int64_t>(j) * n_words, bit);
                              });
@@ -249,8 +257,7 @@ __global__ __launch_bounds__(kScanThreads) void a8_scan_kernel(
 template <typename E>
 __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
     BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
-    const int32_t* __restrict__ row_slot, int64_t n_words,
-    const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
+    int64_t n_words, const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
     const int32_t* __restrict__ neuron_off, const int32_t* __restrict__ row_off,
     int4* __restrict__ ents, int32_t* __restrict__ cols) {
   __shared__ Stage stage[kWaves];
@@ -258,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
   if (n >= n_rows) return;
   const unsigned long long bit = 1ull << (n & 63);
   const int first = row_off[n];
-  visit_row<E>(hy, n, row_slot[n], dff, T, C, nt, stage[threadIdx.x / kWave],
+  visit_row<E>(hy, n, dense_slot(hy, n), dff, T, C, nt, stage[threadIdx.x / kWave],
                [&](int rank, int j, float h) {
     const int64_t w = static_cast<int64_t>(j) * n_words + (n >> 6);
     const int at = neuron_off[j] + lpre[w] + __popcll(bits[w] & (bit - 1));
@@ -630,14 +637,9 @@ SlicePlan slice_plan(int dm) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-int64_t clamped(const Geometry& g, int64_t cap) {
-  return cap <= 0 ? 0 : cap < g.n_rows ? cap : g.n_rows;
-}
-
 struct Space {
   unsigned long long* bits;  // [d_ff][words] (neuron, row) bitmap
-  int32_t* row_slot;         // [N]
-  int64_t zero_vecs;         // 16-byte vectors of bits + row_slot
+  int64_t zero_vecs;         // 16-byte vectors of bits
   int32_t *row_count, *row_off, *lpre, *neuron_count, *neuron_off, *cols;
   int4* ents;   // {row, h as float32 bits, place in row order, 0}, by neuron then row
   float* dz;    // by row then neuron
@@ -660,7 +662,6 @@ Space carve(const Geometry& g, int64_t cap, void* ws) {
   w.entries = bwd_max_entries(g, cap);
   const size_t ents = static_cast<size_t>(w.entries);
   w.bits = static_cast<unsigned long long*>(take(words * 8));
-  w.row_slot = static_cast<int32_t*>(take(n * 4));
   w.zero_vecs = static_cast<int64_t>(off / 16);
   w.row_count = static_cast<int32_t*>(take(n * 4));
   w.row_off = static_cast<int32_t*>(take((n + 1) * 4));
@@ -730,7 +731,7 @@ template <typename E>
 hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, const void* w_up_t,
                     const void* w_down, const void* dy, const Space& w, void* dx, float* dw_up_t,
                     float* db, float* dw_down, hipStream_t s) {
-  const int64_t n_words = (g.n_rows + 63) / 64, cap = clamped(g, hy.cap);
+  const int64_t n_words = (g.n_rows + 63) / 64;
   hipError_t e;
   auto zero = [&](void* p, int64_t vecs) {
     a8_zero_kernel<<<blocks(vecs, kThreads), kThreads, 0, s>>>(static_cast<uint4*>(p), vecs);
@@ -743,12 +744,8 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
     return zero(db, g.d_ff / 4);
   }
   if ((e = zero(w.bits, w.zero_vecs)) != hipSuccess) return e;
-  if (cap > 0) {
-    a8_dense_kernel<<<blocks(cap, kThreads), kThreads, 0, s>>>(hy, g.n_rows, w.row_slot);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   a8_mark_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
-      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, w.row_slot, n_words, w.bits,
+      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, n_words, w.bits,
       w.row_count);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   a8_prefix_kernel<<<blocks(g.d_ff, kWaves), kThreads, 0, s>>>(w.bits, n_words, g.d_ff, w.lpre,
@@ -758,7 +755,7 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
                                            g.n_rows, w.row_off);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   a8_fill_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
-      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, w.row_slot, n_words, w.bits, w.lpre,
+      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, n_words, w.bits, w.lpre,
       w.neuron_off, w.row_off, w.ents, w.cols);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   return gather_passes<E>(g, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db, dw_down, s);

@@ -449,7 +449,8 @@ size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape, int64_t
 /* The gradients of ffn_sparse_backward with the layer's input given as an 8-bit
  * checkpoint: x = code * scale, and dw_up_t = dz^T x.  dz is held in float32
  * throughout (ffn_sparse_backward rounds it to the storage type), so dx too is
- * a float32 sum rounded once.  Sums run in a fixed order.  Arguments, limits
+ * a float32 sum rounded once.  Sums run in a fixed order.  h's dense_rows must
+ * be strictly ascending (as the packs write them).  Arguments, limits
  * and errors are those of ffn_sparse_backward, with n_rows and d_ff below
  * 2^23 - 8 and n_rows * d_ff below 2^38 (else TWELL_ERR_UNSUPPORTED). */
 int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, const void* w_up_t,
