@@ -3,20 +3,24 @@
 // dW_down = h^T dy, dW_up^T = dz^T x, db = column sums of dz, dx = dz W_up),
 // with x = code * scale formed on the way and dz kept in float32 throughout.
 //
-// The non-zeros of h become one list in two orders: by neuron and then row
-// (ents: row, h, and the place p in the other order), and by row and then
-// neuron (cols; dz is stored there).  A bitmap over (neuron, row), set with
-// order-free atomics, gives the neuron-major places, so every sum below runs
-// in a fixed order.  Three passes gather rows of dy, x and W_up:
+// The non-zeros of h become one list in two orders: by row and then neuron
+// (cols; h is stored there, later dz), and by neuron and then row (ents: row, h,
+// and the place p in the other order).  A row has room for all that it can hold,
+// so its entries go there without a count of the others; a bitmap over (row,
+// neuron) gives the neuron-major places, so every sum below runs in a fixed
+// order.  At the 1B layer this takes 48 us (rows 16, bits 7, their sums 11, the
+// neuron order 15), chains of dependent reads each.  Three passes gather rows
+// of dy, x and W_up:
 //   down: per entry the dot of dy[row] with W_down[j], dW_down[j] += h dy[row];
 //   up:   dz; dW_up^T[j] += dz x[row], db[j] += dz;
 //   dx:   dx[row] += dz W_up[j], for TwELL and dense rows alike.
 // Each gathers 335 k x 2048 columns at the 1B layer, from the L2 of the XCD
-// that a column slice is dealt to: down 91 us and dx 72 us for 1.37 GB, up 76
+// that a column slice is dealt to: down 90 us and dx 70 us for 1.37 GB, up 77
 // us for 0.69 GB of codes.  They are bound by the latency and the number of the
 // gathers in flight, not by HBM (the gradients' own 134 MB and the weights are
 // 35 us of it) and not by their instructions: with a fifth fewer of those
 // (entries handed out by DPP broadcasts, unrolled) they took as long or longer.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -32,13 +36,15 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kCols = 16;  // columns of a gathered row per lane and vector group
 constexpr int kScanThreads = 1024;
 constexpr int kScanPer = 16;
+constexpr int64_t kDenseBlocks = 1024;
+constexpr int kBitCols = 2048;
 
 __device__ __forceinline__ int64_t wave_index() {
   return static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
 }
 
-__device__ __forceinline__ int64_t stored_rows(const BwdHybrid& hy) {
-  return hy.cap <= 0 ? 0 : min(static_cast<int64_t>(max(*hy.n_dense, 0)), hy.cap);
+__device__ __forceinline__ int64_t stored_rows(const BwdHybrid& hy, int64_t n_rows) {
+  return hy.cap <= 0 ? 0 : min(static_cast<int64_t>(max(*hy.n_dense, 0)), min(hy.cap, n_rows));
 }
 
 __global__ __launch_bounds__(kThreads) void a8_zero_kernel(uint4* __restrict__ p, int64_t n) {
@@ -48,9 +54,9 @@ __global__ __launch_bounds__(kThreads) void a8_zero_kernel(uint4* __restrict__ p
 
 // m + 1 for the stored dense row m of token row n (0: none): a search of the
 // ascending list by all lanes of the wave, 64 places a step.
-__device__ __forceinline__ int dense_slot(const BwdHybrid& hy, int64_t n) {
+__device__ __forceinline__ int dense_slot(const BwdHybrid& hy, int64_t n_rows, int64_t n) {
   const int lane = lane_id();
-  int lo = 0, hi = static_cast<int>(stored_rows(hy));
+  int lo = 0, hi = static_cast<int>(stored_rows(hy, n_rows));
   while (hi - lo > kWave) {
     const int step = (hi - lo + kWave - 1) / kWave;
     const int i = lo + lane * step;
@@ -64,74 +70,35 @@ __device__ __forceinline__ int dense_slot(const BwdHybrid& hy, int64_t n) {
   return at != 0 ? lo + __builtin_ctzll(at) + 1 : 0;
 }
 
-// A wave's non-zeros on their way from a row to the lists: a step of the row
-// appends at most kStep, full groups of 64 are then taken one per lane, so
-// that the dependent reads and atomics of 64 of them run together.
-constexpr int kStep = 8 * kWave;
-struct Stage {
-  int j[kStep + kWave];
-  float h[kStep + kWave];
-};
+// Where row n's part of the row order starts: a row has room for all of its
+// slots (`slot` - 1 < 0) or, as stored dense row slot - 1, for d_ff entries.
+__device__ __forceinline__ int64_t row_start(int64_t n_rows, int64_t n, int slot, int dff,
+                                             int nslots) {
+  return slot > 0 ? n_rows * nslots + static_cast<int64_t>(slot - 1) * dff : n * nslots;
+}
 
-// One wave per token row: take(rank within the row, neuron, h) for its
-// non-zeros in ascending neuron order, a lane each.  Returns how many there are.
-template <typename E, typename Take>
-__device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slot, int dff, int T,
-                                         int C, int nt, Stage& st, Take take) {
+// The row order: every non-zero's neuron and value, ascending in a row, whose
+// {start, count} is row_at[n].  The first row_blocks workgroups take a TwELL row
+// per wave, the others a dense row each.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void a8_rows_kernel(
+    BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt, unsigned row_blocks,
+    int2* __restrict__ row_at, int32_t* __restrict__ cols, float* __restrict__ vals) {
   typedef ElemTraits<E> Tr;
   constexpr int V = 16 / sizeof(E);
-  constexpr int U = 4;  // dense vectors in flight
-  const int lane = lane_id();
-  int done = 0, held = 0;  // taken, and staged
-  auto take_full = [&] {
-    __builtin_amdgcn_wave_barrier();
-    int at = 0;
-    for (; held - at >= kWave; at += kWave, done += kWave)
-      take(done + lane, st.j[at + lane], st.h[at + lane]);
-    if (at == 0) return;
-    held -= at;
-    const int j = st.j[at + lane];
-    const float h = st.h[at + lane];
-    __builtin_amdgcn_wave_barrier();
-    st.j[lane] = j, st.h[lane] = h;
-  };
-  if (slot > 0) {
-    const E* row = static_cast<const E*>(hy.dense_values) + static_cast<int64_t>(slot - 1) * dff;
-    for (int c0 = 0; c0 < dff; c0 += U * kWave * V) {
-      uint4 q[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = c0 + (u * kWave + lane) * V;
-        q[u] = c < dff ? load_once(reinterpret_cast<const uint4*>(row + c))
-                       : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        E v[V];
-        *reinterpret_cast<uint4*>(v) = q[u];
-        int below = 0, all = 0;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const uint64_t m = wave_ballot(Tr::abs_bits(v[e]) != 0u);
-          below += popc_below(m);
-          all += popc64(m);
-        }
-        if (all == 0) continue;
-        int p = held + below;
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (Tr::abs_bits(v[e]) != 0u) {
-            st.j[p] = c0 + (u * kWave + lane) * V + e;
-            st.h[p++] = Tr::to_f32(v[e]);
-          }
-        held += all;
-        take_full();
-      }
-    }
-  } else {
-    const int nslots = nt * C;
+  constexpr int U = 4;  // vectors, or slots, of a lane in flight
+  constexpr int kWaveCols = U * kWave * V, kChunk = kWaves * kWaveCols;
+  __shared__ uint16_t found[kChunk];  // columns of the chunk's non-zeros, ascending
+  __shared__ int wave_found[kWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int nslots = nt * C;
+  if (blockIdx.x < row_blocks) {
+    const int64_t n = wave_index();
+    if (n >= n_rows || dense_slot(hy, n_rows, n) > 0) return;
+    const int64_t start = row_start(n_rows, n, 0, dff, nslots);
     const E* vrow = static_cast<const E*>(hy.vals) + n * nslots;
     const uint8_t* irow = hy.idx + n * nslots;
+    int held = 0;
     for (int s0 = 0; s0 < nslots; s0 += U * kWave) {
       int local[U], tile[U];
       E v[U];
@@ -148,70 +115,182 @@ __device__ __forceinline__ int visit_row(const BwdHybrid& hy, int64_t n, int slo
       for (int u = 0; u < U; ++u) {
         const uint64_t m = wave_ballot(local[u] < T);
         if (local[u] < T) {
-          const int p = held + popc_below(m);
-          st.j[p] = tile[u] * T + local[u];
-          st.h[p] = Tr::to_f32(v[u]);
+          const int64_t p = start + held + popc_below(m);
+          cols[p] = tile[u] * T + local[u];
+          vals[p] = Tr::to_f32(v[u]);
         }
         held += popc64(m);
       }
-      take_full();
     }
+    if (lane == 0) row_at[n] = make_int2(static_cast<int>(start), held);
+    return;
   }
-  __builtin_amdgcn_wave_barrier();
-  if (lane < held) take(done + lane, st.j[lane], st.h[lane]);
-  return done + held;
+  const int64_t stored = stored_rows(hy, n_rows);
+  for (int64_t m = blockIdx.x - row_blocks; m < stored; m += gridDim.x - row_blocks) {
+    const int64_t n = hy.dense_rows[m];
+    if (n < 0 || n >= n_rows) continue;
+    const int64_t start = row_start(n_rows, n, static_cast<int>(m) + 1, dff, nslots);
+    const E* row = static_cast<const E*>(hy.dense_values) + m * dff;
+    int held = 0;
+    for (int c0 = 0; c0 < dff; c0 += kChunk) {
+      uint4 q[U];
+      const int first = wave * kWaveCols + lane * V;  // of the lane's, in the chunk
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + first + u * kWave * V;
+        q[u] = c < dff ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+      }
+      // the lane's non-zeros per vector, then those of the lanes up to it: two
+      // counts (at most 64 V) in a register
+      uint32_t mine[U / 2], upto[U / 2];
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          E v[V];
+          *reinterpret_cast<uint4*>(v) = q[u + k];
+#pragma unroll
+          for (int e = 0; e < V; ++e) c += (Tr::abs_bits(v[e]) != 0u ? 1u : 0u) << (16 * k);
+        }
+        mine[u / 2] = upto[u / 2] = c;
+      }
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1)
+#pragma unroll
+        for (int h = 0; h < U / 2; ++h) {
+          const uint32_t got = __shfl_up(upto[h], o, kWave);
+          if (lane >= o) upto[h] += got;
+        }
+      int before[U], total = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        before[u] = total + static_cast<int>((upto[u / 2] - mine[u / 2]) >> (16 * (u % 2)) & 0xffff);
+        total += static_cast<int>(__shfl(upto[u / 2], kWave - 1, kWave) >> (16 * (u % 2)) & 0xffff);
+      }
+      if (lane == 0) wave_found[wave] = total;
+      __syncthreads();
+      int base = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        base += w < wave ? wave_found[w] : 0;
+        all += wave_found[w];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        E v[V];
+        *reinterpret_cast<uint4*>(v) = q[u];
+        int p = base + before[u];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (Tr::abs_bits(v[e]) != 0u)
+            found[p++] = static_cast<uint16_t>(first + u * kWave * V + e);
+      }
+      __syncthreads();
+      for (int i = tid; i < all; i += kThreads) {
+        const int j = c0 + found[i];
+        cols[start + held + i] = j;
+        vals[start + held + i] = Tr::to_f32(row[j]);
+      }
+      held += all;
+      __syncthreads();  // found and wave_found are rewritten by the next chunk
+    }
+    if (tid == 0) row_at[n] = make_int2(static_cast<int>(start), held);
+  }
 }
 
-// Bit n % 64 of bits[j][n / 64] for every non-zero; row_count[n] = theirs.
-template <typename E>
-__global__ __launch_bounds__(kThreads) void a8_mark_kernel(
-    BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
-    int64_t n_words, unsigned long long* __restrict__ bits, int32_t* __restrict__ row_count) {
-  __shared__ Stage stage[kWaves];
-  const int64_t n = wave_index();
-  if (n >= n_rows) return;
-  const unsigned long long bit = 1ull << (n & 63);
-  unsigned long long* word = bits + (n >> 6);
-  const int c = visit_row<E>(hy, n, dense_slot(hy, n), dff, T, C, nt, stage[threadIdx.x / kWave],
-                             [&](int, int j, float) {
-                               atomicOr(word + static_cast<int64_t>(j) * n_words, bit);
-                             });
-  if (lane_id() == 0) row_count[n] = c;
+// bits[w][j]: bit r is set where row 64 w + r has a non-zero at neuron j.  A
+// workgroup per word and kBitCols neurons collects its bits in LDS (integer
+// ors: no order) from the lists of the 64 rows, which needs no cleared memory:
+// 7 us at the 1B layer.  Or-ing its 335 k bits into memory as the rows are read
+// took 5 us more, with the clearing.
+__global__ __launch_bounds__(kScanThreads) void a8_bits_kernel(
+    const int2* __restrict__ row_at, const int32_t* __restrict__ cols, int64_t n_rows, int dff,
+    int n_slices, unsigned long long* __restrict__ bits) {
+  __shared__ unsigned long long word[kBitCols];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int64_t w = blockIdx.x / n_slices;
+  const int j0 = static_cast<int>(blockIdx.x % n_slices) * kBitCols;
+  for (int i = tid; i < kBitCols; i += kScanThreads) word[i] = 0;
+  __syncthreads();
+  constexpr int kRows = kWave / (kScanThreads / kWave);  // of a wave
+  constexpr int U = 2;  // entries of a row in flight, of all the wave's rows together
+  int2 at[kRows];
+  int longest = 0;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t n = w * kWave + wave * kRows + k;
+    at[k] = n < n_rows ? row_at[n] : make_int2(0, 0);
+    longest = max(longest, at[k].y);
+  }
+  for (int i0 = lane; i0 < longest; i0 += U * kWave) {
+    int j[kRows][U];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kWave;
+        j[k][u] = i < at[k].y ? cols[static_cast<int64_t>(at[k].x) + i] - j0 : -1;
+      }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (static_cast<unsigned>(j[k][u]) < kBitCols)
+          atomicOr(word + j[k][u], 1ull << (wave * kRows + k));
+  }
+  __syncthreads();
+  for (int i = tid; i < min(kBitCols, dff - j0); i += kScanThreads) bits[w * dff + j0 + i] = word[i];
 }
 
-// Per neuron (one wave each): lpre[j][b] = set bits of its words below b;
-// neuron_count[j] = all.
-__global__ __launch_bounds__(kThreads) void a8_prefix_kernel(
+// Per neuron (a lane of every wave; the words in runs, one a wave): lpre[b][j] =
+// set bits of its words below b; neuron_count[j] = all.
+__global__ __launch_bounds__(kScanThreads) void a8_prefix_kernel(
     const unsigned long long* __restrict__ bits, int64_t n_words, int dff,
     int32_t* __restrict__ lpre, int32_t* __restrict__ neuron_count) {
-  const int lane = lane_id();
-  const int64_t j = wave_index();
-  if (j >= dff) return;
-  int run = 0;
-  for (int64_t b0 = 0; b0 < n_words; b0 += kWave) {
-    const int64_t b = b0 + lane;
-    const int c = b < n_words ? __popcll(bits[j * n_words + b]) : 0;
-    int v = c;
+  constexpr int kRuns = kScanThreads / kWave;
+  constexpr int U = 4;
+  __shared__ int run_total[kRuns][kWave];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kWave + lane;
+  const int64_t jr = j < dff ? j : dff - 1;
+  const int64_t per = (n_words + kRuns - 1) / kRuns;
+  const int64_t b0 = min(wave * per, n_words), b1 = min(b0 + per, n_words);
+  int total = 0;
+  for (int64_t b = b0; b < b1; b += U)
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int u = __shfl_up(v, o, kWave);
-      if (lane >= o) v += u;
+    for (int u = 0; u < U; ++u) {
+      const int c = __popcll(bits[min(b + u, n_words - 1) * dff + jr]);
+      total += b + u < b1 ? c : 0;
     }
-    if (b < n_words) lpre[j * n_words + b] = run + v - c;
-    run += __shfl(v, kWave - 1, kWave);
+  run_total[wave][lane] = total;
+  __syncthreads();
+  int run = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    run += k < wave ? run_total[k][lane] : 0;
+    all += run_total[k][lane];
   }
-  if (lane == 0) neuron_count[j] = run;
+  if (j >= dff) return;
+  for (int64_t b = b0; b < b1; b += U) {
+    int c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) c[u] = __popcll(bits[min(b + u, n_words - 1) * dff + j]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u < b1) {
+        lpre[(b + u) * dff + j] = run;
+        run += c[u];
+      }
+  }
+  if (wave == 0) neuron_count[j] = all;
 }
 
-// Exclusive sums: workgroup 0 of the neurons' counts, workgroup 1 of the rows'.
-__global__ __launch_bounds__(kScanThreads) void a8_scan_kernel(
-    const int32_t* __restrict__ neuron_count, int64_t n_neurons, int32_t* __restrict__ neuron_off,
-    const int32_t* __restrict__ row_count, int64_t n_rows, int32_t* __restrict__ row_off) {
+// Exclusive sums of the neurons' counts.
+__global__ __launch_bounds__(kScanThreads) void a8_scan_kernel(const int32_t* __restrict__ in,
+                                                               int64_t n,
+                                                               int32_t* __restrict__ out) {
   __shared__ int wave_tot[kScanThreads / kWave];
-  const bool rows = blockIdx.x == 1;
-  const int32_t* in = rows ? row_count : neuron_count;
-  int32_t* out = rows ? row_off : neuron_off;
-  const int64_t n = rows ? n_rows : n_neurons;
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   int carry = 0;
   for (int64_t r0 = 0; r0 < n; r0 += kScanThreads * kScanPer) {
@@ -253,26 +332,48 @@ __global__ __launch_bounds__(kScanThreads) void a8_scan_kernel(
   if (tid == 0) out[n] = carry;
 }
 
-// Every non-zero into both orders.
-template <typename E>
+// Every non-zero into the neuron order, from its place in the row order:
+// workgroups as for those.
 __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
-    BwdHybrid hy, int64_t n_rows, int dff, int T, int C, int nt,
-    int64_t n_words, const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
-    const int32_t* __restrict__ neuron_off, const int32_t* __restrict__ row_off,
-    int4* __restrict__ ents, int32_t* __restrict__ cols) {
-  __shared__ Stage stage[kWaves];
-  const int64_t n = wave_index();
-  if (n >= n_rows) return;
-  const unsigned long long bit = 1ull << (n & 63);
-  const int first = row_off[n];
-  visit_row<E>(hy, n, dense_slot(hy, n), dff, T, C, nt, stage[threadIdx.x / kWave],
-               [&](int rank, int j, float h) {
-    const int64_t w = static_cast<int64_t>(j) * n_words + (n >> 6);
-    const int at = neuron_off[j] + lpre[w] + __popcll(bits[w] & (bit - 1));
-    ents[at] = make_int4(static_cast<int>(n), static_cast<int>(__float_as_uint(h)), first + rank,
-                         0);
-    cols[first + rank] = j;
-  });
+    BwdHybrid hy, int64_t n_rows, int64_t dense_from, int dff, unsigned row_blocks,
+    const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
+    const int32_t* __restrict__ neuron_off, const int2* __restrict__ row_at,
+    const int32_t* __restrict__ cols, const float* __restrict__ vals, int4* __restrict__ ents) {
+  constexpr int U = 2;  // entries of a lane whose dependent reads overlap
+  auto place = [&](int64_t n, int2 at, int first, int stride) {
+    const unsigned long long below = (1ull << (n & 63)) - 1;
+    for (int i0 = first; i0 < at.y; i0 += U * stride) {
+      int j[U], h[U], to[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t p = at.x + min(i0 + u * stride, at.y - 1);
+        j[u] = cols[p];
+        h[u] = static_cast<int>(__float_as_uint(vals[p]));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t w = (n >> 6) * dff + j[u];
+        to[u] = neuron_off[j[u]] + lpre[w] + __popcll(bits[w] & below);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * stride < at.y)
+          ents[to[u]] = make_int4(static_cast<int>(n), h[u], at.x + i0 + u * stride, 0);
+    }
+  };
+  if (blockIdx.x < row_blocks) {
+    const int64_t n = wave_index();
+    if (n >= n_rows) return;
+    const int2 at = row_at[n];
+    if (at.x < dense_from) place(n, at, lane_id(), kWave);
+    return;
+  }
+  const int64_t stored = stored_rows(hy, n_rows);
+  for (int64_t m = blockIdx.x - row_blocks; m < stored; m += gridDim.x - row_blocks) {
+    const int64_t n = hy.dense_rows[m];
+    if (n < 0 || n >= n_rows) continue;
+    place(n, row_at[n], threadIdx.x, kThreads);
+  }
 }
 
 // ---- The gathering passes.  A slice of sw columns is covered by P lanes, 64 / P
@@ -577,7 +678,7 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
 // float32, rounded once.
 template <typename E, int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
-    const int32_t* __restrict__ row_off, const int32_t* __restrict__ cols,
+    const int2* __restrict__ row_at, const int32_t* __restrict__ cols,
     const float* __restrict__ dz, const E* __restrict__ w_up_t, int64_t n_rows, int dm, int log_s,
     int sw, E* __restrict__ dx) {
   typedef Slice<16 / sizeof(E), P, NV, FULL> Sl;
@@ -587,7 +688,7 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
   const int64_t n = at.item;
   if (n >= n_rows) return;
   const Sl sl(at.slice, sw);
-  const int b = row_off[n], L = row_off[n + 1] - b;
+  const int b = row_at[n].x, L = row_at[n].y;
   float acc[Sl::kAcc];
 #pragma unroll
   for (int i = 0; i < Sl::kAcc; ++i) acc[i] = 0.f;
@@ -638,11 +739,11 @@ SlicePlan slice_plan(int dm) {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Space {
-  unsigned long long* bits;  // [d_ff][words] (neuron, row) bitmap
-  int64_t zero_vecs;         // 16-byte vectors of bits
-  int32_t *row_count, *row_off, *lpre, *neuron_count, *neuron_off, *cols;
+  unsigned long long* bits;  // [words][d_ff] (row, neuron) bitmap
+  int2* row_at;              // {start, count} of each row's entries in the row order
+  int32_t *lpre, *neuron_count, *neuron_off, *cols;
   int4* ents;   // {row, h as float32 bits, place in row order, 0}, by neuron then row
-  float* dz;    // by row then neuron
+  float* dz;    // by row then neuron: h until the neuron order is filled, then dz
   float* part;  // [S][entries] partial dots
   int64_t entries;
   size_t bytes;
@@ -662,9 +763,7 @@ Space carve(const Geometry& g, int64_t cap, void* ws) {
   w.entries = bwd_max_entries(g, cap);
   const size_t ents = static_cast<size_t>(w.entries);
   w.bits = static_cast<unsigned long long*>(take(words * 8));
-  w.zero_vecs = static_cast<int64_t>(off / 16);
-  w.row_count = static_cast<int32_t*>(take(n * 4));
-  w.row_off = static_cast<int32_t*>(take((n + 1) * 4));
+  w.row_at = static_cast<int2*>(take(n * sizeof(int2)));
   w.lpre = static_cast<int32_t*>(take(words * 4));
   w.neuron_count = static_cast<int32_t*>(take(dff * 4));
   w.neuron_off = static_cast<int32_t*>(take((dff + 1) * 4));
@@ -721,7 +820,7 @@ hipError_t gather_passes(const Geometry& g, const Space& w, const BwdAct8& x8, c
   return with_plan(sp, [&](auto p, auto nv, auto full) {
     a8_dx_kernel<E, decltype(p)::value, decltype(nv)::value, decltype(full)::value>
         <<<rows * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
-            w.row_off, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows, g.d_model, log2(sp.S),
+            w.row_at, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows, g.d_model, log2(sp.S),
             sp.sw, static_cast<E*>(dx));
     return hipGetLastError();
   });
@@ -743,20 +842,25 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
     if ((e = zero(dw_down, weights)) != hipSuccess) return e;
     return zero(db, g.d_ff / 4);
   }
-  if ((e = zero(w.bits, w.zero_vecs)) != hipSuccess) return e;
-  a8_mark_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
-      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, n_words, w.bits,
-      w.row_count);
+  // past the rows' workgroups, up to kDenseBlocks for the dense rows
+  const unsigned row_blocks = blocks(g.n_rows, kWaves);
+  const unsigned all_blocks =
+      row_blocks + static_cast<unsigned>(std::clamp<int64_t>(hy.cap, 0, kDenseBlocks));
+  a8_rows_kernel<E><<<all_blocks, kThreads, 0, s>>>(hy, g.n_rows, g.d_ff, g.tile, g.capacity,
+                                                    g.n_tiles, row_blocks, w.row_at, w.cols, w.dz);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  a8_prefix_kernel<<<blocks(g.d_ff, kWaves), kThreads, 0, s>>>(w.bits, n_words, g.d_ff, w.lpre,
-                                                              w.neuron_count);
+  const unsigned slices = blocks(g.d_ff, kBitCols);
+  a8_bits_kernel<<<static_cast<unsigned>(n_words) * slices, kScanThreads, 0, s>>>(
+      w.row_at, w.cols, g.n_rows, g.d_ff, static_cast<int>(slices), w.bits);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  a8_scan_kernel<<<2, kScanThreads, 0, s>>>(w.neuron_count, g.d_ff, w.neuron_off, w.row_count,
-                                           g.n_rows, w.row_off);
+  a8_prefix_kernel<<<blocks(g.d_ff, kWave), kScanThreads, 0, s>>>(w.bits, n_words, g.d_ff, w.lpre,
+                                                                 w.neuron_count);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  a8_fill_kernel<E><<<blocks(g.n_rows, kWaves), kThreads, 0, s>>>(
-      hy, g.n_rows, g.d_ff, g.tile, g.capacity, g.n_tiles, n_words, w.bits, w.lpre,
-      w.neuron_off, w.row_off, w.ents, w.cols);
+  a8_scan_kernel<<<1, kScanThreads, 0, s>>>(w.neuron_count, g.d_ff, w.neuron_off);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  a8_fill_kernel<<<all_blocks, kThreads, 0, s>>>(
+      hy, g.n_rows, g.n_rows * g.n_tiles * g.capacity, g.d_ff, row_blocks, w.bits, w.lpre,
+      w.neuron_off, w.row_at, w.cols, w.dz, w.ents);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   return gather_passes<E>(g, w, x8, w_up_t, w_down, dy, dx, dw_up_t, db, dw_down, s);
 }
