@@ -38,6 +38,8 @@ constexpr int kScanThreads = 1024;
 constexpr int kScanPer = 16;
 constexpr int64_t kDenseBlocks = 1024;
 constexpr int kBitCols = 2048;
+constexpr int kSliceCols = 2 * kWave * kCols;  // of the widest slice
+constexpr int kMaxCols = 8 * kSliceCols;
 
 __device__ __forceinline__ int64_t wave_index() {
   return static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
@@ -390,11 +392,11 @@ struct Slice {
   static constexpr int kSteps = kGroups * NV >= FLIGHT ? 1 : FLIGHT / (kGroups * NV);
   static constexpr int kEntries = kGroups * kSteps;
   int first;  // column of the lane's chunk 0
-  int lim;    // columns of the slice past `first`
-  __device__ __forceinline__ Slice(int s, int sw) {
+  int lim;    // columns of the slice past `first`; the last slice may be shorter
+  __device__ __forceinline__ Slice(int s, int sw, int dm) {
     const int l = lane_id() % P;
     first = s * sw + l * V;
-    lim = sw - l * V;
+    lim = min(sw, dm - s * sw) - l * V;
   }
   __device__ __forceinline__ bool ok(int k) const { return FULL || k * P * V < lim; }
   // a chunk past the slice reads the slice's first columns instead
@@ -545,7 +547,7 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
   const Place at(log_s);
   if (at.item >= dff) return;
   const int j = static_cast<int>(at.item);
-  const Sl sl(at.slice, sw);
+  const Sl sl(at.slice, sw, dm);
   const int b = neuron_off[j], L = neuron_off[j + 1] - b;
   float acc[Sl::kAcc];
 #pragma unroll
@@ -610,7 +612,7 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
   const Place at(log_s);
   if (at.item >= dff) return;
   const int j = static_cast<int>(at.item);
-  const Sl sl(at.slice, sw);
+  const Sl sl(at.slice, sw, dm);
   const int b = neuron_off[j], L = neuron_off[j + 1] - b;
   float acc[Sl::kAcc];
 #pragma unroll
@@ -687,7 +689,7 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
   const Place at(log_s);
   const int64_t n = at.item;
   if (n >= n_rows) return;
-  const Sl sl(at.slice, sw);
+  const Sl sl(at.slice, sw, dm);
   const int b = row_at[n].x, L = row_at[n].y;
   float acc[Sl::kAcc];
 #pragma unroll
@@ -724,15 +726,19 @@ __global__ __launch_bounds__(kThreads) void a8_dx_kernel(
 
 // Column slices: S of sw columns, S up to 8 (one per XCD) as long as a slice
 // keeps 256 columns and whole chunks of every pass; P lanes of 16 nv columns
-// cover one (nv = 0: too wide).
+// cover one (nv = 0: too wide).  A width that divides only into slices too wide
+// for a wave takes eight of whole chunks, the last one shorter (not empty: the
+// other seven hold at most 7 (dm / 8 + 16) columns, under dm from 897 on).
 SlicePlan slice_plan(int dm) {
-  SlicePlan p;
+  SlicePlan p{};
+  if (dm > kMaxCols) return p;
   p.S = 8;
   while (p.S > 1 && (dm % (p.S * kCols) != 0 || dm / p.S < 256)) p.S /= 2;
-  p.sw = dm / p.S;
+  if (dm > p.S * kSliceCols) p.S = 8;
+  p.sw = p.S == 1 ? dm : (dm + p.S * kCols - 1) / (p.S * kCols) * kCols;
   const int groups = (p.sw + kCols - 1) / kCols;
   p.P = groups <= 16 ? 16 : groups <= 32 ? 32 : kWave;
-  p.nvl = groups <= kWave ? 1 : groups <= 2 * kWave ? 2 : 0;
+  p.nvl = groups <= kWave ? 1 : 2;
   return p;
 }
 
@@ -779,10 +785,11 @@ unsigned blocks(int64_t items, int per) { return static_cast<unsigned>((items + 
 
 // fn(P, NV, FULL) as types for the plan's widths.
 template <typename Fn>
-hipError_t with_plan(const SlicePlan& sp, Fn fn) {
+hipError_t with_plan(const SlicePlan& sp, int dm, Fn fn) {
   auto go = [&](auto p, auto nv) {
-    return sp.sw == decltype(p)::value * decltype(nv)::value * kCols ? fn(p, nv, std::true_type{})
-                                                                     : fn(p, nv, std::false_type{});
+    return sp.sw == decltype(p)::value * decltype(nv)::value * kCols && sp.S * sp.sw == dm
+               ? fn(p, nv, std::true_type{})
+               : fn(p, nv, std::false_type{});
   };
   typedef std::integral_constant<int, 1> One;
   if (sp.nvl == 2)
@@ -800,7 +807,7 @@ hipError_t gather_passes(const Geometry& g, const Space& w, const BwdAct8& x8, c
   const SlicePlan sp = slice_plan(g.d_model);
   const unsigned neurons = blocks(g.d_ff, kWaves), rows = blocks(g.n_rows, kWaves);
   auto log2 = [](int v) { return __builtin_ctz(static_cast<unsigned>(v)); };
-  hipError_t e = with_plan(sp, [&](auto p, auto nv, auto full) {
+  hipError_t e = with_plan(sp, g.d_model, [&](auto p, auto nv, auto full) {
     a8_down_kernel<E, decltype(p)::value, decltype(nv)::value, decltype(full)::value>
         <<<neurons * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
             w.neuron_off, w.ents, static_cast<const E*>(dy), static_cast<const E*>(w_down), g.d_ff,
@@ -808,7 +815,7 @@ hipError_t gather_passes(const Geometry& g, const Space& w, const BwdAct8& x8, c
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  e = with_plan(sp, [&](auto p, auto nv, auto full) {
+  e = with_plan(sp, g.d_model, [&](auto p, auto nv, auto full) {
     a8_up_kernel<decltype(p)::value, decltype(nv)::value, decltype(full)::value>
         <<<neurons * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
             w.neuron_off, w.ents, x8.codes, x8.scales, act8_pitch(g.d_model),
@@ -817,7 +824,7 @@ hipError_t gather_passes(const Geometry& g, const Space& w, const BwdAct8& x8, c
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  return with_plan(sp, [&](auto p, auto nv, auto full) {
+  return with_plan(sp, g.d_model, [&](auto p, auto nv, auto full) {
     a8_dx_kernel<E, decltype(p)::value, decltype(nv)::value, decltype(full)::value>
         <<<rows * static_cast<unsigned>(sp.S), kThreads, 0, s>>>(
             w.row_at, w.cols, w.dz, static_cast<const E*>(w_up_t), g.n_rows, g.d_model, log2(sp.S),

@@ -553,13 +553,19 @@ TWELL_EXPORT int ell_spmm(const twell_shape* shape, const twell_ell* in, const v
 namespace twell {
 namespace {
 
-// The backward's shape rules on top of check_shape: every entry's place fits
-// an int32.
-int check_backward_shape(const twell_shape* s, int64_t dense_capacity) {
-  int rc = check_shape(s, true);
+// What both backward passes need on top of check_shape: every place in their
+// lists of h's non-zeros fits an int32.  Each has widths of its own besides.
+int check_backward_lists(const twell_shape* s, int64_t dense_capacity) {
+  const int rc = check_shape(s, true);
   if (rc != TWELL_OK) return rc;
   if (dense_capacity < 0) return TWELL_ERR_INVALID_ARG;
-  if (bwd_max_entries(geometry(s), dense_capacity) > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
+  return bwd_max_entries(geometry(s), dense_capacity) > INT32_MAX ? TWELL_ERR_UNSUPPORTED
+                                                                  : TWELL_OK;
+}
+
+int check_backward_shape(const twell_shape* s, int64_t dense_capacity) {
+  const int rc = check_backward_lists(s, dense_capacity);
+  if (rc != TWELL_OK) return rc;
   if (!bwd_supported(geometry(s), elem_bytes(s->dtype))) return TWELL_ERR_UNSUPPORTED;
   return TWELL_OK;
 }
@@ -640,7 +646,7 @@ namespace twell {
 namespace {
 
 int check_backward_act8(const twell_shape* s, int64_t dense_capacity) {
-  const int rc = check_backward_shape(s, dense_capacity);
+  const int rc = check_backward_lists(s, dense_capacity);
   if (rc != TWELL_OK) return rc;
   return bwd_act8_supported(geometry(s)) ? TWELL_OK : TWELL_ERR_UNSUPPORTED;
 }

@@ -393,8 +393,8 @@ size_t ffn_sparse_backward_workspace_size(const twell_shape* shape, int64_t dens
  * from dense_values only; after a TWELL_ERR_DENSE_CAPACITY forward the rows
  * past dense_capacity hold no non-zero, so they contribute nothing and get
  * dx = 0.
- * d_model is at most 16384 (bf16) or 8192 (float32), else
- * TWELL_ERR_UNSUPPORTED.
+ * d_model: any multiple of 8 up to 2048 (bf16) or 1024 (float32); above, up to
+ * 16384 or 8192, a multiple of 64 or 32; else TWELL_ERR_UNSUPPORTED.
  * Arguments: shape (host pointer; the forward's shape); x, w_up_t, w_down,
  * dy [n_rows][d_model] inputs in dtype; h (host pointer to device pointers)
  * the stored activations; dx, dw_up_t, db_up, dw_down outputs; workspace of
@@ -450,9 +450,10 @@ size_t ffn_sparse_backward_act8_workspace_size(const twell_shape* shape, int64_t
  * checkpoint: x = code * scale, and dw_up_t = dz^T x.  dz is held in float32
  * throughout (ffn_sparse_backward rounds it to the storage type), so dx too is
  * a float32 sum rounded once.  Sums run in a fixed order.  h's dense_rows must
- * be strictly ascending (as the packs write them).  Arguments, limits
- * and errors are those of ffn_sparse_backward, with n_rows and d_ff below
- * 2^23 - 8 and n_rows * d_ff below 2^38 (else TWELL_ERR_UNSUPPORTED). */
+ * be strictly ascending (as the packs write them).  Arguments and errors are
+ * those of ffn_sparse_backward.  Limits, else TWELL_ERR_UNSUPPORTED: d_model at
+ * most 16384 in both dtypes (any multiple of 8); n_rows and d_ff below 2^23 - 8;
+ * n_rows * d_ff below 2^38; TwELL slots and stored dense elements below 2^31. */
 int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, const void* w_up_t,
                              const void* w_down, const twell_hybrid* h, const void* dy, void* dx,
                              float* dw_up_t, float* db_up, float* dw_down, void* workspace,
