@@ -321,7 +321,9 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
   if (lane == 0) {
     a.logp[row] = !t.given ? 0.f : empty ? neg_inf() : fmaf(t.x - st.m, a.scale, -ln_s);
     a.entropy[row] = empty ? 0.f : ln_s - kLn2 * (st.t / st.s);
-    a.lse[row] = empty ? neg_inf() : fmaf(st.m, a.scale, ln_s);
+    // below float32's range its lowest value: -inf is a masked row's alone
+    const float lse = fmaf(st.m, a.scale, ln_s);
+    a.lse[row] = empty ? neg_inf() : lse == neg_inf() ? kLowest : lse;
   }
   if (lane < a.top) {
     a.top_ids[row * a.top + lane] = list.id;

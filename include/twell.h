@@ -507,7 +507,8 @@ int twell_embed_backward(const twell_embed_shape* shape, const void* dout, const
  *    arrays per row are aligned to their elements only.
  *  - A place with x = -inf is masked: probability 0, never an alternative.
  *    A row with nothing else has lse = -inf, entropy 0, logp = -inf and a zero
- *    gradient.  Finite masks (the type's lowest value) are ordinary values.
+ *    gradient.  Finite masks (the type's lowest value) are ordinary values; an
+ *    lse of such a row below float32's range is float32's lowest value, not -inf.
  *  - A row holding NaN or +inf has NaN results (its alternatives are still the
  *    largest values that are not NaN).
  *  - The alternatives are the `top` (0 .. TWELL_LOGPROB_MAX_TOP) largest logits,
