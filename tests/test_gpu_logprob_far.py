@@ -1,5 +1,6 @@
-"""The log-probability gradient where float32 log-sum-exps are out of range: rows of the type's
-lowest value under a scale above 1.
+"""The log-probability gradient where float32 log-sum-exps are coarse or out of range: rows past
+|lse| = 128 that span several workgroups' chunks, in place and not, and rows of the type's lowest
+value under a scale above 1, whose scaled logits leave float32.
 
 Tolerances are those of the ordinary rows (test_gpu_logprob.py): a gradient element within 1e-5 of
 (|dlogp| + |dentropy| (1 + entropy)) * scale, plus its rounding to bfloat16."""
@@ -8,9 +9,31 @@ import pytest
 import torch
 
 from gpu_helpers import as_f64, say
-from test_gpu_logprob import run_backward
+from test_gpu_logprob import check_backward, odd_rows, run_backward
 
 BOTH = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+
+
+@pytest.mark.gpu
+@BOTH
+@pytest.mark.parametrize("v", [20011, 70000])
+@pytest.mark.parametrize("ent", [True, False])
+@pytest.mark.parametrize("form", ["same rows", "shifted rows", "in place"])
+def test_far_rows_of_several_chunks(form, ent, v, dtype):
+    """A row's chunks (8192 bfloat16 or 4096 float32 columns) belong to different workgroups."""
+    say(f"logprob grad far rows {dtype} v={v} ent={ent} {form}")
+    x, t = odd_rows(v, dtype)
+    t[4] = 1
+    keep = [r for r in range(16) if r not in (13, 14)]
+    dlogp = torch.linspace(-1, 2, 16)
+    dent = torch.linspace(1, -1, 16) if ent else None
+    f, got = run_backward(x, t, 1.0, dlogp, dent, v + 5, v + (6 if form == "shifted rows" else 5),
+                          form == "in place")
+    lse = as_f64(f.lse)
+    assert (np.abs(lse[[1, 8, 11, 15]]) > 128).all()
+    assert not got[0].any() and np.isnan(got[[13, 14]]).any(axis=1).all()
+    check_backward(got[keep], x[keep], t[keep], 1.0, dlogp[keep], dent[keep] if ent else None,
+                   as_f64(f.entropy)[keep])
 
 
 @pytest.mark.gpu
