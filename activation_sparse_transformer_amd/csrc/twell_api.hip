@@ -756,7 +756,8 @@ int check_logprob(const twell_logprob_shape* s) {
   if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
   if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
   if (s->top < 0 || s->top > kLogprobMaxTop || s->top > s->vocab) return TWELL_ERR_INVALID_ARG;
-  if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return TWELL_ERR_INVALID_ARG;
+  // 2^127: the exponents are taken in base 2, and scale * log2(e) stays finite
+  if (!(s->scale > 0.f) || s->scale > 0x1p127f) return TWELL_ERR_INVALID_ARG;
   // a launch holds fewer than 2^32 lanes, a wave per part of a row
   if (s->n_rows * logprob_splits(s->n_rows, s->vocab, elem_bytes(s->dtype)) >=
       (int64_t{1} << 26) - 4)

@@ -517,8 +517,7 @@ int twell_embed_backward(const twell_embed_shape* shape, const void* dout, const
  * Sums, maxima and probabilities are float32 throughout.
  * Requirements: n_rows >= 0; 0 < vocab <= 2^30; n_rows * parts of a row (1 for
  * thousands of rows, at most 64) below 2^26 - 4, else TWELL_ERR_UNSUPPORTED;
- * dtype a twell_dtype; top <= vocab; scale finite and > 0;
- * reserved 0. */
+ * dtype a twell_dtype; top <= vocab; 0 < scale <= 2^127; reserved 0. */
 #define TWELL_LOGPROB_MAX_TOP 32
 typedef struct twell_logprob_shape {
   int64_t n_rows;
