@@ -14,8 +14,8 @@ namespace twell {
 // 8-bit activation checkpoints: int8 codes [n_rows][act8_pitch(d)] and one
 // float32 scale per row and block of kAct8Block columns.
 constexpr int kAct8Block = 128;
-inline int act8_blocks(int d) { return (d + kAct8Block - 1) / kAct8Block; }
-inline int act8_pitch(int d) { return (d + 15) / 16 * 16; }
+inline int act8_blocks(int d) { return (d - 1) / kAct8Block + 1; }
+inline int act8_pitch(int d) { return ((d - 1) / 16 + 1) * 16; }
 hipError_t launch_act8_pack(int64_t n_rows, int d, int elem_bytes, const void* x, int8_t* codes,
                             float* scales, hipStream_t s);
 hipError_t launch_act8_unpack(int64_t n_rows, int d, int elem_bytes, const int8_t* codes,

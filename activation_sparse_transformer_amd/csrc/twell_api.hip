@@ -618,6 +618,7 @@ int check_act8(int64_t n_rows, int32_t d_model, int32_t dtype, const void* x,
   if (n_rows > 0 && (x == nullptr || a->codes == nullptr || a->scales == nullptr))
     return TWELL_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(a->codes) || !aligned16(a->scales)) return TWELL_ERR_INVALID_ARG;
+  if (d_model > INT32_MAX - 15) return TWELL_ERR_UNSUPPORTED;  // a row of codes, rounded up
   // a launch holds fewer than 2^32 lanes, at most 32 of them per block
   if (n_rows * act8_blocks(d_model) >= (int64_t{1} << 27) - 8) return TWELL_ERR_UNSUPPORTED;
   return TWELL_OK;

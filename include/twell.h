@@ -430,8 +430,8 @@ typedef struct twell_act8 {
 } twell_act8;
 
 /* Write the 8-bit form of x [n_rows][d_model] (dtype: a twell_dtype; d_model a
- * multiple of 8; n_rows * blocks per row below 2^27 - 8, else
- * TWELL_ERR_UNSUPPORTED). */
+ * multiple of 8; d_model below 2^31 - 8 and n_rows * blocks per row below
+ * 2^27 - 8, else TWELL_ERR_UNSUPPORTED). */
 int twell_act8_pack(int64_t n_rows, int32_t d_model, int32_t dtype, const void* x,
                     const twell_act8* out, void* stream);
 
