@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kRowThreads) void embed_rows_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
   };
-  const int stream_slices = (d + kStreamCols - 1) / kStreamCols;
+  const int stream_slices = (d - 1) / kStreamCols + 1;
   const int64_t n_long = static_cast<int64_t>(b.counters[3]) * stream_slices;
   for (int64_t item = blockIdx.x; item < n_long; item += gridDim.x) {
     const int4 seg = b.long_segs[item / stream_slices];
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kRowThreads) void embed_rows_kernel(
   // next item's token numbers and the one after's segment are read while an
   // item is summed, so the three dependent reads of an item do not add up.
   const int64_t waves = static_cast<int64_t>(gridDim.x) * kRowWaves;
-  const int short_slices = (d + kShortCols - 1) / kShortCols;
+  const int short_slices = (d - 1) / kShortCols + 1;
   const int64_t n_medium = static_cast<int64_t>(b.counters[2]) * stream_slices;
   const int64_t n_items = n_medium + static_cast<int64_t>(b.counters[1]) * short_slices;
   struct Item {
@@ -619,7 +619,7 @@ hipError_t launch_embed_forward(int64_t n, int vocab, int d, int elem_bytes, int
                                 hipStream_t s) {
   if (n == 0) return hipSuccess;
   const int per = kEmbLoads * kWave * 16 / elem_bytes;
-  const int chunks = (d + per - 1) / per;
+  const int chunks = (d - 1) / per + 1;
   const int64_t items = n * chunks;
   const unsigned grid = blocks_for(items, kEmbWaves, kEmbMaxBlocks);
   auto go = [&](auto e, auto i) {
@@ -711,7 +711,7 @@ hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, in
   if (e != hipSuccess) return e;
   const int32_t* long_order = sort ? b.perm : b.pos;
   const int V = 16 / elem_bytes;
-  const int64_t items = (n < vocab ? n : vocab) * ((d + kWave * V - 1) / (kWave * V));
+  const int64_t items = (n < vocab ? n : vocab) * ((d - 1) / (kWave * V) + 1);
   const unsigned grid = blocks_for(items, kRowWaves, kRowBlocks);
   if (elem_bytes == 2)
     embed_rows_kernel<<<grid, kRowThreads, 0, s>>>(b, long_order, static_cast<const uint16_t*>(dout),
