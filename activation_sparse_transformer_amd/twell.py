@@ -192,10 +192,20 @@ def _need(t: torch.Tensor, name: str, device, dtype=None, shape=None) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _int32(**sizes: int) -> None:
+    """The C structures' sizes: a larger value would be cut to its low 32 bits.  Callers ask only
+    where one is past 31 bits or negative (0.1 us a call instead of 0.7)."""
+    for name, v in sizes.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name} {v} does not fit 32 bits")
+
+
 def make_shape(n_rows: int, d_model: int, d_ff: int, tile: int, capacity: int,
                dtype: torch.dtype) -> Shape:
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
+    if (d_model | d_ff | tile | capacity) >> 31:
+        _int32(d_model=d_model, d_ff=d_ff, tile=tile, capacity=capacity)
     return Shape(n_rows, d_model, d_ff, tile, capacity, _DTYPE_CODE[dtype], 0)
 
 
@@ -680,6 +690,8 @@ class Act8:
         if self.dtype not in _DTYPE_CODE:
             raise ValueError(f"dtype {self.dtype} is not supported (float32 or bfloat16)")
         n, d = self.n_rows, self.d_model
+        if d >> 31:
+            _int32(d_model=d)
         _need(self.codes, "codes", device, torch.int8, (n, -(-d // 16) * 16))
         _need(self.scales, "scales", device, torch.float32, (n, -(-d // ACT8_BLOCK)))
 
@@ -692,6 +704,8 @@ def twell_act8_pack(x: torch.Tensor, *, out: Optional[Act8] = None) -> Act8:
     _need(x, "x", dev)
     if x.dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype {x.dtype} is not supported (float32 or bfloat16)")
+    if d >> 31:
+        _int32(d_model=d)
     if out is None:
         out = Act8.empty(n, d, x.dtype, dev)
     if (out.n_rows, out.d_model, out.dtype) != (n, d, x.dtype):
@@ -764,6 +778,8 @@ def _embed_shape(n: int, vocab: int, d: int, dtype: torch.dtype, index: torch.dt
         raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
     if index not in _INDEX_BYTES:
         raise ValueError(f"token ids must be int32 or int64, got {index}")
+    if (vocab | d) >> 31:
+        _int32(vocab=vocab, d_model=d)
     return EmbedShape(n, vocab, d, _DTYPE_CODE[dtype], _INDEX_BYTES[index], scale, 0)
 
 
@@ -787,7 +803,7 @@ def twell_embed_forward(table: torch.Tensor, tokens: torch.Tensor, *, scale: flo
 
 def embed_backward_workspace(n_tokens: int, d_model: int, vocab: int, device) -> torch.Tensor:
     """A workspace for twell_embed_backward of these sizes."""
-    shape = EmbedShape(n_tokens, vocab, d_model, 0, 8, 1.0, 0)
+    shape = _embed_shape(n_tokens, vocab, d_model, torch.float32, torch.int64, 1.0)
     ws = int(load().twell_embed_backward_workspace_size(ctypes.byref(shape)))
     if ws == 0:
         raise TwellError(TWELL_ERR_INVALID_ARG, "twell_embed_backward_workspace_size")
@@ -859,6 +875,8 @@ def _logprob_shape(logits: torch.Tensor, targets: torch.Tensor, top: int,
     _need(targets, "targets", dev, shape=(n,))
     if targets.dtype not in _INDEX_BYTES:
         raise ValueError(f"targets must be int32 or int64, got {targets.dtype}")
+    if (vocab | top) >> 31:
+        _int32(vocab=vocab, top=top)
     return LogprobShape(n, _row_stride(logits), vocab, _DTYPE_CODE[logits.dtype],
                         _INDEX_BYTES[targets.dtype], top, scale, 0)
 
@@ -866,6 +884,8 @@ def _logprob_shape(logits: torch.Tensor, targets: torch.Tensor, top: int,
 def logprob_workspace(n_rows: int, vocab: int, top: int, dtype: torch.dtype,
                       device) -> torch.Tensor:
     """A workspace for twell_logprob_forward of these sizes (empty when none is needed)."""
+    if (vocab | top) >> 31:
+        _int32(vocab=vocab, top=top)
     shape = LogprobShape(n_rows, vocab, vocab, _DTYPE_CODE[dtype], 8, top, 1.0, 0)
     return torch.empty((int(load().twell_logprob_workspace_size(ctypes.byref(shape))),),
                        dtype=torch.uint8, device=device)

@@ -31,3 +31,22 @@ def test_act8_widths_at_the_end_of_int32():
     assert both(0, top - 16) == {OK}
     assert both(8, top - 16) == {UNSUPPORTED}   # 2^27 blocks
     assert both(0, top - 8) == both(1, top - 8) == {UNSUPPORTED}
+
+
+def test_sizes_past_int32_are_refused():
+    """The structures hold 32-bit sizes; a larger one must not be cut to its low bits."""
+    big = 2 ** 32 + 128
+    x = torch.empty((1, big), dtype=torch.bfloat16, device="meta")
+    ids = torch.empty((1,), dtype=torch.int64, device="meta")
+    for call in (lambda: twell.twell_act8_pack(x),
+                 lambda: twell.twell_act8_unpack(twell.Act8.empty(1, big, torch.bfloat16, "meta")),
+                 lambda: twell.twell_embed_forward(x, ids),
+                 lambda: twell.twell_embed_backward(x, ids, 10),
+                 lambda: twell.twell_embed_backward(x[:, :64].contiguous(), ids, big),
+                 lambda: twell.embed_backward_workspace(1, 8, big, "meta"),
+                 lambda: twell.twell_logprob_forward(x, ids),
+                 lambda: twell.twell_logprob_forward(x[:, :64], ids, top=big),
+                 lambda: twell.logprob_workspace(1, big, 0, torch.float32, "meta"),
+                 lambda: twell.make_shape(1, big, 512, 64, 4, torch.float32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
