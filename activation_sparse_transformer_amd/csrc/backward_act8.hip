@@ -50,8 +50,9 @@ __device__ __forceinline__ int64_t stored_rows(const BwdHybrid& hy, int64_t n_ro
 }
 
 __global__ __launch_bounds__(kThreads) void a8_zero_kernel(uint4* __restrict__ p, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride)
+    p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // m + 1 for the stored dense row m of token row n (0: none): a search of the
@@ -840,7 +841,9 @@ hipError_t backward(const Geometry& g, const BwdHybrid& hy, const BwdAct8& x8, c
   const int64_t n_words = (g.n_rows + 63) / 64;
   hipError_t e;
   auto zero = [&](void* p, int64_t vecs) {
-    a8_zero_kernel<<<blocks(vecs, kThreads), kThreads, 0, s>>>(static_cast<uint4*>(p), vecs);
+    const int64_t most = int64_t{1} << 23;  // a launch holds fewer than 2^32 lanes
+    a8_zero_kernel<<<blocks(std::min(vecs, most * kThreads), kThreads), kThreads, 0, s>>>(
+        static_cast<uint4*>(p), vecs);
     return hipGetLastError();
   };
   if (g.n_rows == 0) {  // zero weight and bias gradients
