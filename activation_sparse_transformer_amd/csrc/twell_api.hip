@@ -701,10 +701,15 @@ int check_embed(const twell_embed_shape* s) {
   if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
   if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
   if (!std::isfinite(s->scale)) return TWELL_ERR_INVALID_ARG;
-  // a launch holds fewer than 2^32 lanes, one per four columns of a share
-  if (static_cast<int64_t>(s->vocab) * s->d_model >= (int64_t{1} << 33))
-    return TWELL_ERR_UNSUPPORTED;
   return TWELL_OK;
+}
+
+int check_embed_grad(const twell_embed_shape* s) {
+  const int rc = check_embed(s);
+  if (rc != TWELL_OK) return rc;
+  // a launch holds fewer than 2^32 lanes, one per four columns of a share
+  return static_cast<int64_t>(s->vocab) * s->d_model >= (int64_t{1} << 33) ? TWELL_ERR_UNSUPPORTED
+                                                                          : TWELL_OK;
 }
 
 }  // namespace
@@ -724,14 +729,14 @@ TWELL_EXPORT int twell_embed_forward(const twell_embed_shape* shape, const void*
 }
 
 TWELL_EXPORT size_t twell_embed_backward_workspace_size(const twell_embed_shape* shape) {
-  if (check_embed(shape) != TWELL_OK) return 0;
+  if (check_embed_grad(shape) != TWELL_OK) return 0;
   return embed_grad_carve(shape->n_tokens, shape->vocab, nullptr).bytes;
 }
 
 TWELL_EXPORT int twell_embed_backward(const twell_embed_shape* shape, const void* dout,
                                       const void* tokens, float* dtable, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-  const int rc = check_embed(shape);
+  const int rc = check_embed_grad(shape);
   if (rc != TWELL_OK) return rc;
   if (shape->n_tokens > 0 && (dout == nullptr || tokens == nullptr)) return TWELL_ERR_INVALID_ARG;
   if (dtable == nullptr || workspace == nullptr) return TWELL_ERR_INVALID_ARG;

@@ -466,8 +466,8 @@ int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, con
  * only, so that a part of a longer text will do); an id outside [0, vocab) is
  * padding: its output row is zero and it adds to no gradient.
  * Requirements: 0 <= n_tokens < 2^31; vocab > 0; d_model > 0 and a multiple of
- * 8; vocab * d_model < 2^33 (TWELL_ERR_UNSUPPORTED); dtype a twell_dtype; scale
- * finite; reserved 0. */
+ * 8; dtype a twell_dtype; scale finite; reserved 0; for the gradient also
+ * vocab * d_model < 2^33 (else TWELL_ERR_UNSUPPORTED). */
 typedef struct twell_embed_shape {
   int64_t n_tokens;
   int32_t vocab;

@@ -24,3 +24,16 @@ def test_widest_row():
     grad = twell.twell_embed_backward(out, ids, 1, out=torch.full((1, d), 9.0, device="cuda"))
     assert all(torch.equal(g, o.float()) for g, o in zip(grad[0].split(1 << 28),
                                                          out[0].split(1 << 28)))
+
+
+@pytest.mark.gpu
+def test_lookup_in_a_table_past_2_33_elements():
+    say("embed 2^20 + 1 ids of 8192")
+    vocab, d = (1 << 20) + 1, 8192
+    table = torch.empty((vocab, d), dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([vocab - 1, 0, vocab, 1 << 19, vocab - 2], device="cuda")
+    for v, k in ((1.0, 0), (2.0, 1 << 19), (3.0, vocab - 2), (4.0, vocab - 1)):
+        table[k] = v
+    out = twell.twell_embed_forward(table, ids)
+    want = torch.tensor([4.0, 1.0, 0.0, 2.0, 3.0], device="cuda").bfloat16()
+    assert torch.equal(out, want[:, None].expand(5, d))

@@ -50,3 +50,12 @@ def test_sizes_past_int32_are_refused():
                  lambda: twell.make_shape(1, big, 512, 64, 4, torch.float32)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_lookup_in_the_largest_tables():
+    """Only the gradient's launches are bound by the table's size."""
+    lib = twell.load()
+    s = twell.EmbedShape(0, 1 << 20, 8192, 1, 8, 1.0, 0)  # 2^33 elements
+    assert lib.twell_embed_forward(ctypes.byref(s), P, None, None, None) == OK
+    assert lib.twell_embed_backward(ctypes.byref(s), None, None, P, P, 1 << 40, None) == UNSUPPORTED
+    assert lib.twell_embed_backward_workspace_size(ctypes.byref(s)) == 0
