@@ -548,7 +548,8 @@ int twell_logprob_forward(const twell_logprob_shape* shape, const void* logits,
  * from the forward's lse and entropy (entropy is read only with dentropy;
  * dentropy may be NULL).  dlogits has rows out_stride elements apart and may be
  * the logits themselves (out_stride == row_stride); columns past vocab are not
- * written.  shape->top is ignored.  Rows with |lse| > 128, where a float32 lse
+ * written.  shape->top is checked as in the forward and has no other effect
+ * (0 will do).  Rows with |lse| > 128, where a float32 lse
  * is too coarse, are normalised by their own sum formed again (one workgroup
  * per such row). */
 int twell_logprob_backward(const twell_logprob_shape* shape, const void* logits,
