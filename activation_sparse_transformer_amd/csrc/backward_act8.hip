@@ -41,6 +41,14 @@ constexpr int kBitCols = 2048;
 constexpr int kSliceCols = 2 * kWave * kCols;  // of the widest slice
 constexpr int kMaxCols = 8 * kSliceCols;
 
+// A non-zero in the neuron order.  Twelve bytes: with one per place that h could
+// fill, a fourth word would be 134 MB of workspace at the 1B layer.
+struct Entry {
+  int32_t row;
+  uint32_t h;     // as float32 bits
+  int32_t place;  // in the row order
+};
+
 __device__ __forceinline__ int64_t wave_index() {
   return static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
 }
@@ -341,17 +349,18 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
     BwdHybrid hy, int64_t n_rows, int64_t dense_from, int dff, unsigned row_blocks,
     const unsigned long long* __restrict__ bits, const int32_t* __restrict__ lpre,
     const int32_t* __restrict__ neuron_off, const int2* __restrict__ row_at,
-    const int32_t* __restrict__ cols, const float* __restrict__ vals, int4* __restrict__ ents) {
+    const int32_t* __restrict__ cols, const float* __restrict__ vals, Entry* __restrict__ ents) {
   constexpr int U = 2;  // entries of a lane whose dependent reads overlap
   auto place = [&](int64_t n, int2 at, int first, int stride) {
     const unsigned long long below = (1ull << (n & 63)) - 1;
     for (int i0 = first; i0 < at.y; i0 += U * stride) {
-      int j[U], h[U], to[U];
+      int j[U], to[U];
+      uint32_t h[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t p = at.x + min(i0 + u * stride, at.y - 1);
         j[u] = cols[p];
-        h[u] = static_cast<int>(__float_as_uint(vals[p]));
+        h[u] = __float_as_uint(vals[p]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -361,7 +370,7 @@ __global__ __launch_bounds__(kThreads) void a8_fill_kernel(
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (i0 + u * stride < at.y)
-          ents[to[u]] = make_int4(static_cast<int>(n), h[u], at.x + i0 + u * stride, 0);
+          ents[to[u]] = Entry{static_cast<int>(n), h[u], at.x + i0 + u * stride};
     }
   };
   if (blockIdx.x < row_blocks) {
@@ -539,7 +548,7 @@ struct Place {
 // dot of dy[row] with W_down[j]; dW_down[j][slice] = sum of h dy[row].
 template <typename E, int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_down_kernel(
-    const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
+    const int32_t* __restrict__ neuron_off, const Entry* __restrict__ ents,
     const E* __restrict__ dy, const E* __restrict__ w_down, int dff, int dm, int log_s, int sw,
     float* __restrict__ part, int64_t pstride, float* __restrict__ dw_down) {
   typedef Slice<16 / sizeof(E), P, NV, FULL> Sl;
@@ -558,7 +567,7 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
   if (!FULL) w.keep(true, sl);
   for (int base = 0; base < L; base += kWave) {
     const int cnt = min(kWave, L - base);
-    const int4 mine = ents[b + base + min(lane, cnt - 1)];
+    const Entry mine = ents[b + base + min(lane, cnt - 1)];
     float mypd = 0.f;  // lane t: the chunk's entry t
     auto step = [&](int e0, auto check) {
       constexpr bool CHECK = decltype(check)::value;
@@ -568,8 +577,8 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
 #pragma unroll
       for (int u = 0; u < Sl::kSteps; ++u) {
         const int e = e0 + u * Sl::kGroups + grp;
-        const int64_t row = __shfl(mine.x, e, kWave);
-        hb[u] = store_bits<E>(static_cast<uint32_t>(__shfl(mine.y, e, kWave)));
+        const int64_t row = __shfl(mine.row, e, kWave);
+        hb[u] = store_bits<E>(__shfl(mine.h, e, kWave));
         y[u].load(dy + row * dm, sl);
       }
 #pragma unroll
@@ -604,7 +613,7 @@ __global__ __launch_bounds__(kThreads) void a8_down_kernel(
 // worth more as waves (76 against 91 us at the 1B layer).
 template <int P, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads) void a8_up_kernel(
-    const int32_t* __restrict__ neuron_off, const int4* __restrict__ ents,
+    const int32_t* __restrict__ neuron_off, const Entry* __restrict__ ents,
     const int8_t* __restrict__ codes, const float* __restrict__ scales, int pitch, int nb,
     const float* __restrict__ part, int64_t pstride, int n_part, int dff, int dm, int log_s, int sw,
     float* __restrict__ dz, float* __restrict__ dw_up_t, float* __restrict__ db) {
@@ -622,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
   for (int base = 0; base < L; base += kWave) {
     const int cnt = min(kWave, L - base);
     const int64_t me = b + base + min(lane, cnt - 1);
-    const int4 mine = ents[me];
+    const Entry mine = ents[me];
     float d = part[me];
     if (n_part == 8) {  // the loads together
       float p[7];
@@ -641,7 +650,7 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
       float f[Sl::kSteps][NV];
 #pragma unroll
       for (int u = 0; u < Sl::kSteps; ++u) {
-        const int64_t row = __shfl(mine.x, e0 + u * Sl::kGroups + grp, kWave);
+        const int64_t row = __shfl(mine.row, e0 + u * Sl::kGroups + grp, kWave);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           q[u][v] = *reinterpret_cast<const uint4*>(codes + row * pitch + sl.col(v));
@@ -664,7 +673,7 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
       }
     }
     if (at.slice == 0 && lane < cnt) {
-      dz[mine.z] = d;
+      dz[mine.place] = d;
       sum += d;
     }
   }
@@ -749,7 +758,7 @@ struct Space {
   unsigned long long* bits;  // [words][d_ff] (row, neuron) bitmap
   int2* row_at;              // {start, count} of each row's entries in the row order
   int32_t *lpre, *neuron_count, *neuron_off, *cols;
-  int4* ents;   // {row, h as float32 bits, place in row order, 0}, by neuron then row
+  Entry* ents;  // by neuron then row
   float* dz;    // by row then neuron: h until the neuron order is filled, then dz
   float* part;  // [S][entries] partial dots
   int64_t entries;
@@ -775,7 +784,7 @@ Space carve(const Geometry& g, int64_t cap, void* ws) {
   w.neuron_count = static_cast<int32_t*>(take(dff * 4));
   w.neuron_off = static_cast<int32_t*>(take((dff + 1) * 4));
   w.cols = static_cast<int32_t*>(take(ents * 4));
-  w.ents = static_cast<int4*>(take(ents * sizeof(int4)));
+  w.ents = static_cast<Entry*>(take(ents * sizeof(Entry)));
   w.dz = static_cast<float*>(take(ents * 4));
   w.part = static_cast<float*>(take(static_cast<size_t>(slice_plan(g.d_model).S) * ents * 4));
   w.bytes = off;
