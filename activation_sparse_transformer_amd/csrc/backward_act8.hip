@@ -16,10 +16,13 @@
 //   dx:   dx[row] += dz W_up[j], for TwELL and dense rows alike.
 // Each gathers 335 k x 2048 columns at the 1B layer, from the L2 of the XCD
 // that a column slice is dealt to: down 90 us and dx 70 us for 1.37 GB, up 77
-// us for 0.69 GB of codes.  They are bound by the latency and the number of the
-// gathers in flight, not by HBM (the gradients' own 134 MB and the weights are
-// 35 us of it) and not by their instructions: with a fifth fewer of those
-// (entries handed out by DPP broadcasts, unrolled) they took as long or longer.
+// us for 0.69 GB of codes.  They are bound by the path that returns loaded data
+// to the registers: it is busy for 82% (down), 76% (up) and 76% (dx) of their
+// cycles, with 85-90% of the reads hitting the L2 at 170-225 cycles and the
+// vector units busy for 19%.  Up reads half the bytes in 1.3 times dx's loads:
+// beside a row's codes it loads their scale, and per entry eight partial dots.
+// With a fifth fewer instructions (entries handed out by DPP broadcasts,
+// unrolled) the passes took as long or longer.
 #include <algorithm>
 #include <type_traits>
 
@@ -633,7 +636,9 @@ __global__ __launch_bounds__(kThreads) void a8_up_kernel(
     const int64_t me = b + base + min(lane, cnt - 1);
     const Entry mine = ents[me];
     float d = part[me];
-    if (n_part == 8) {  // the loads together
+    // eight loads together (1B layer 270 us; one after another 293); two or four
+    // of them, of narrower layers, are within 1% either way and take the loop
+    if (n_part == 8) {
       float p[7];
 #pragma unroll
       for (int t = 0; t < 7; ++t) p[t] = part[(t + 1) * pstride + me];

@@ -285,9 +285,9 @@ __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
 }
 
 // Up to kSortMax tokens are grouped by one workgroup, in one launch that zeroes
-// the whole table meanwhile (32768 x 2048: 44 us, 6.1 TB/s of zeros; the
-// general sequence's five launches, which zero as much: 56 us): a stable radix sort of the keys (id, token number)
-// by id, then the segments between changes of id.  Key i = wave * chunk +
+// the whole table meanwhile (32768 x 2048: 44 us, 6.1 TB/s of zeros): a stable
+// radix sort of the keys (id, token number) by id, then the segments between
+// changes of id.  Key i = wave * chunk +
 // round * 64 + lane keeps the tokens' order; a pass ranks a wave's keys of equal
 // digit by ballots and a running count, numbers (digit, wave) by a scan, and
 // moves the keys through LDS.
@@ -639,7 +639,10 @@ namespace {
 
 // The segments of the tokens and the zeroing, by the general sequence: the
 // counts, segments for the used ids, the tokens into them, the long segments
-// in order.
+// in order.  16384 tokens of 2048 bf16: 116 us for 32768 ids (the zeros about 65,
+// the rows 48), 89 us for 8000; of 4096 float32 and 49999 ids 239 us (157, 78).
+// The count launch alone takes 22 us of the second: an id's tokens all count on
+// one address.
 template <typename I>
 hipError_t group_tokens(int64_t n, int vocab, int d, const I* ids, const EmbedGradBufs& b,
                         float* dtable, hipStream_t s) {
@@ -700,7 +703,10 @@ hipError_t launch_embed_backward(int64_t n, int vocab, int d, int elem_bytes, in
                                  const EmbedGradBufs& b, float* dtable, hipStream_t s) {
   // One workgroup sorts while the others zero the table, two launches in all,
   // unless the tokens or ids exceed its keys or most rows are used anyway
-  // (zeroing them first would be lost work).
+  // (zeroing them first would be lost work).  It is ahead of the general
+  // sequence up to the most tokens its keys hold: 53 against 60 us for 1024
+  // tokens, 59 against 69 for 4096, 65 against 80 for 8192 (32768 x 2048 bf16),
+  // 179 against 195 for 8192 of 49999 x 4096 float32.
   const bool sort = n <= kSortMax && n < vocab && vocab < 1 << (32 - kSortNBits);
   auto group = [&](const auto* ids) {
     return sort ? sort_tokens(n, vocab, d, ids, b, dtable, s)

@@ -333,8 +333,8 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 }
 
 // One pass over the logits, a wave per row (or part of one) so that nothing
-// waits on a barrier.  4096 x 131072 bf16 with 5 alternatives: 194 us, 5.5
-// TB/s, without alternatives 189; float32 6.0 TB/s.  Bound by HBM and, in bf16,
+// waits on a barrier.  4096 x 131072 bf16 with 5 alternatives: 194-210 us over
+// runs and cards, 5.1-5.5 TB/s, without alternatives 184-190; float32 6.0 TB/s.  Bound by HBM and, in bf16,
 // as much by the ten or so instruction slots per element (the exponential is
 // four): a batch prefetched ahead, or one fused multiply-add for d, change
 // nothing.  Wave i of the grid takes part i % splits of row i / splits: the row's whole
@@ -574,12 +574,14 @@ struct GradChunk {
 
 // A workgroup takes one chunk of a row; its logits are on their way before the
 // row's scalars are read (102 -> 97 us).  4096 x 32768 bf16: 95 us, 5.7 TB/s;
-// 2000 x 49999 float32 with the entropy's part: 139 us, 5.8 TB/s; bound by HBM.  lse is rounded to float32, which moves every p of
-// the row by |lse| * 2^-24 of itself; past kFarLse (a row of the type's lowest
-// values, or logits far from zero) the row's own maximum and sum are formed
-// again instead.  dlogits may be the logits, where the chunks of such a row
-// would see each other's results: there one workgroup forms the sums and takes
-// the row's chunks in turn.
+// 2000 x 49999 float32 with the entropy's part: 139 us, 5.8 TB/s; bound by HBM.
+// lse is rounded to float32, which moves every p of the row by |lse| * 2^-24 of
+// itself; past kFarLse (a row of the type's lowest values, or logits far from
+// zero) the row's own maximum and sum are formed again instead.  dlogits may be
+// the logits, where the chunks of such a row would see each other's results:
+// there one workgroup forms the sums and takes the row's chunks in turn.  That
+// costs: 4096 x 32768 bf16 with 80% of such rows 986 us, 16 x 131072 with
+// nearly all 224 us against 11 without.
 template <typename E, typename I, bool ENT, bool VEC>
 __global__ __launch_bounds__(kLpThreads) void logprob_backward_kernel(const LogprobGradArgs a,
                                                                      int chunks,
