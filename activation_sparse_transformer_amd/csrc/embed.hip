@@ -34,6 +34,7 @@ constexpr int kSortPer = kSortMax / kSortThreads;    // keys per lane
 constexpr int kSortBits = 6;
 constexpr int kSortBins = 1 << kSortBits;
 static_assert(kSortBins * kSortWaves == kSortThreads, "a thread per (bin, wave)");
+static_assert(kOrderThreads <= kEmbedGradStep, "the widest step over an id's tokens");
 constexpr int kWindow = 1 << 19;                     // token numbers per bitmap (64 KB)
 // Segments by length: a wave takes one of at most kShort tokens row after row,
 // one of at most kMedium as 8 streams of rows (8 lanes a row), and a workgroup

@@ -35,6 +35,7 @@ hipError_t launch_backward_act8(const Geometry& g, int elem_bytes, const BwdHybr
 
 // Token embedding: out = scale * table[tokens], and the table's gradient.
 // tokens are int32 or int64 (index_bytes 4 or 8).
+constexpr int kEmbedGradStep = 1024;  // most tokens that a loop over an id's steps by
 struct EmbedGradBufs {
   int32_t* counters;   // [4] places, short, medium and long ids handed out (cleared)
   int32_t* count;      // [vocab] tokens of each id (cleared)

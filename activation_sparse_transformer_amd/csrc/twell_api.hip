@@ -707,6 +707,8 @@ int check_embed(const twell_embed_shape* s) {
 int check_embed_grad(const twell_embed_shape* s) {
   const int rc = check_embed(s);
   if (rc != TWELL_OK) return rc;
+  // the loops over an id's tokens step past the last one in int32
+  if (s->n_tokens > INT32_MAX - kEmbedGradStep + 1) return TWELL_ERR_UNSUPPORTED;
   // a launch holds fewer than 2^32 lanes, one per four columns of a share
   return static_cast<int64_t>(s->vocab) * s->d_model >= (int64_t{1} << 33) ? TWELL_ERR_UNSUPPORTED
                                                                           : TWELL_OK;

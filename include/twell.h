@@ -467,7 +467,8 @@ int ffn_sparse_backward_act8(const twell_shape* shape, const twell_act8* x8, con
  * padding: its output row is zero and it adds to no gradient.
  * Requirements: 0 <= n_tokens < 2^31; vocab > 0; d_model > 0 and a multiple of
  * 8; dtype a twell_dtype; scale finite; reserved 0; for the gradient also
- * vocab * d_model < 2^33 (else TWELL_ERR_UNSUPPORTED). */
+ * vocab * d_model < 2^33 and n_tokens <= 2^31 - 1024 (else
+ * TWELL_ERR_UNSUPPORTED). */
 typedef struct twell_embed_shape {
   int64_t n_tokens;
   int32_t vocab;

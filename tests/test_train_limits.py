@@ -59,3 +59,14 @@ def test_lookup_in_the_largest_tables():
     assert lib.twell_embed_forward(ctypes.byref(s), P, None, None, None) == OK
     assert lib.twell_embed_backward(ctypes.byref(s), None, None, P, P, 1 << 40, None) == UNSUPPORTED
     assert lib.twell_embed_backward_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_embedding_gradient_of_almost_2_31_tokens():
+    """Its loops over one id's tokens step by up to 1024 past the last of them, in int32."""
+    lib = twell.load()
+    s = lambda n: ctypes.byref(twell.EmbedShape(n, 10, 8, 1, 8, 1.0, 0))
+    size = lib.twell_embed_backward_workspace_size
+    assert size(s(2 ** 31 - 1024)) > 0
+    for n in (2 ** 31 - 1023, 2 ** 31 - 1):
+        assert size(s(n)) == 0
+        assert lib.twell_embed_backward(s(n), P, P, P, P, 1 << 40, None) == UNSUPPORTED
