@@ -1,7 +1,7 @@
 // Host-side launchers of the operators around the layer in a training step
 // (internal to libtwell.so): 8-bit activation checkpoints and the backward pass
-// from one, the token embedding, log probabilities.  Every launcher only
-// enqueues on `s` and returns hipGetLastError().
+// from one, the token embedding, log probabilities, the norms around the layer.
+// Every launcher only enqueues on `s` and returns hipGetLastError().
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -92,5 +92,32 @@ struct LogprobGradArgs {
 };
 hipError_t launch_logprob_backward(const LogprobGradArgs& a, int elem_bytes, int index_bytes,
                                    hipStream_t s);
+
+// Norms around the layer: residual_out = alpha residual + gate * norm(y) * w_post,
+// x = norm(residual_out) * w_pre.  Weights are float32 [d], each may be null.
+constexpr int kNormMaxWidth = 16384;
+struct NormArgs {
+  int64_t n_rows;
+  int d;
+  float alpha, eps;
+  const float *w_post, *gate, *w_pre;
+};
+hipError_t launch_norm_forward(const NormArgs& a, int elem_bytes, const void* residual,
+                               const void* y, void* residual_out, void* x, hipStream_t s);
+template <typename E>
+struct NormGradPtrs {
+  const E *residual_out, *y, *d_residual_out, *dx;
+  E *d_residual, *dy;
+};
+struct NormGradArgs {
+  const void *residual_out, *y, *d_residual_out, *dx;
+  void *d_residual, *dy;
+  float *dw_post, *dgate, *dw_pre;
+  float* sums;  // workspace: [2][groups][d]
+};
+// Groups of lanes the rows are dealt to, each with column sums of its own.
+int norm_grad_groups(int64_t n_rows, int d);
+hipError_t launch_norm_backward(const NormArgs& a, int elem_bytes, const NormGradArgs& p,
+                                hipStream_t s);
 
 }  // namespace twell

@@ -846,3 +846,89 @@ TWELL_EXPORT int twell_logprob_backward(const twell_logprob_shape* shape, const 
   return hip_status(launch_logprob_backward(a, elem_bytes(shape->dtype), shape->index_bytes,
                                             static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ norms around the layer
+namespace twell {
+namespace {
+
+int check_norm(const twell_norm_shape* s) {
+  if (s == nullptr || s->n_rows < 0 || s->n_rows > INT32_MAX) return TWELL_ERR_INVALID_ARG;
+  if (s->d_model <= 0 || s->d_model % 8 != 0) return TWELL_ERR_INVALID_ARG;
+  if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (!std::isfinite(s->residual_scale)) return TWELL_ERR_INVALID_ARG;
+  if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return TWELL_ERR_INVALID_ARG;
+  return s->d_model > kNormMaxWidth ? TWELL_ERR_UNSUPPORTED : TWELL_OK;
+}
+
+size_t norm_grad_bytes(const twell_norm_shape* s) {
+  return 2 * sizeof(float) * static_cast<size_t>(s->d_model) *
+         norm_grad_groups(s->n_rows, s->d_model);
+}
+
+NormArgs norm_args(const twell_norm_shape* s, const float* w_post, const float* gate,
+                   const float* w_pre) {
+  return NormArgs{s->n_rows, s->d_model, s->residual_scale, s->eps, w_post, gate, w_pre};
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT int twell_norm_forward(const twell_norm_shape* shape, const void* residual,
+                                    const void* y, const float* w_post, const float* gate,
+                                    const float* w_pre, void* residual_out, void* x,
+                                    void* stream) {
+  const int rc = check_norm(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_rows > 0) {
+    if (residual == nullptr || (w_pre == nullptr) != (x == nullptr)) return TWELL_ERR_INVALID_ARG;
+    if ((y == nullptr) != (residual_out == nullptr)) return TWELL_ERR_INVALID_ARG;
+    if (y == nullptr && (w_post != nullptr || gate != nullptr || w_pre == nullptr ||
+                         shape->residual_scale != 1.f))
+      return TWELL_ERR_INVALID_ARG;
+  }
+  if (!aligned16(residual) || !aligned16(y) || !aligned16(w_post) || !aligned16(gate) ||
+      !aligned16(w_pre) || !aligned16(residual_out) || !aligned16(x))
+    return TWELL_ERR_INVALID_ARG;
+  return hip_status(launch_norm_forward(norm_args(shape, w_post, gate, w_pre),
+                                        elem_bytes(shape->dtype), residual, y, residual_out, x,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT size_t twell_norm_backward_workspace_size(const twell_norm_shape* shape) {
+  return check_norm(shape) != TWELL_OK ? 0 : norm_grad_bytes(shape);
+}
+
+TWELL_EXPORT int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
+                                     const void* y, const float* w_post, const float* gate,
+                                     const float* w_pre, const void* d_residual_out,
+                                     const void* dx, void* d_residual, void* dy, float* dw_post,
+                                     float* dgate, float* dw_pre, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  const int rc = check_norm(shape);
+  if (rc != TWELL_OK) return rc;
+  if ((w_post == nullptr) != (dw_post == nullptr) || (gate == nullptr) != (dgate == nullptr) ||
+      (w_pre == nullptr) != (dw_pre == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (shape->n_rows > 0) {
+    if (d_residual == nullptr || (y == nullptr) != (dy == nullptr)) return TWELL_ERR_INVALID_ARG;
+    if (w_pre != nullptr ? residual_out == nullptr || dx == nullptr
+                         : d_residual_out == nullptr || dx != nullptr)
+      return TWELL_ERR_INVALID_ARG;
+    if (y == nullptr && (w_post != nullptr || gate != nullptr || w_pre == nullptr ||
+                         shape->residual_scale != 1.f))
+      return TWELL_ERR_INVALID_ARG;
+    if (workspace == nullptr) return TWELL_ERR_INVALID_ARG;
+  }
+  if (!aligned16(residual_out) || !aligned16(y) || !aligned16(w_post) || !aligned16(gate) ||
+      !aligned16(w_pre) || !aligned16(d_residual_out) || !aligned16(dx) ||
+      !aligned16(d_residual) || !aligned16(dy) || !aligned16(dw_post) || !aligned16(dgate) ||
+      !aligned16(dw_pre) || !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  if (workspace_bytes < norm_grad_bytes(shape)) return TWELL_ERR_WORKSPACE;
+  const NormGradArgs p{residual_out, y,      d_residual_out, dx,
+                       d_residual,   dy,     dw_post,        dgate,
+                       dw_pre,       static_cast<float*>(workspace)};
+  return hip_status(launch_norm_backward(norm_args(shape, w_post, gate, w_pre),
+                                         elem_bytes(shape->dtype), p,
+                                         static_cast<hipStream_t>(stream)));
+}

@@ -38,6 +38,7 @@ EXPORTS = (
     "ffn_sparse_backward_act8",
     "twell_embed_forward", "twell_embed_backward_workspace_size", "twell_embed_backward",
     "twell_logprob_workspace_size", "twell_logprob_forward", "twell_logprob_backward",
+    "twell_norm_forward", "twell_norm_backward_workspace_size", "twell_norm_backward",
 )
 
 
@@ -88,6 +89,13 @@ class LogprobShape(ctypes.Structure):
         ("n_rows", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("vocab", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("top", ctypes.c_int32),
         ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64), ("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
     ]
 
 
@@ -151,6 +159,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.twell_logprob_forward.restype = I
     lib.twell_logprob_backward.argtypes = [L, P, P, P, P, P, P, P, i64, P]
     lib.twell_logprob_backward.restype = I
+    N = ctypes.POINTER(NormShape)
+    lib.twell_norm_forward.argtypes, lib.twell_norm_forward.restype = [N, *[P] * 8], I
+    lib.twell_norm_backward_workspace_size.argtypes = [N]
+    lib.twell_norm_backward_workspace_size.restype = sz
+    lib.twell_norm_backward.argtypes, lib.twell_norm_backward.restype = [N, *[P] * 13, sz, P], I
     _lib = lib
     return lib
 
@@ -174,6 +187,17 @@ def _stream(device: torch.device) -> int:
     if _raw_stream is not None and device.index is not None:
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _here(device: torch.device) -> int:
+    """The current stream of `device`, which has to be the current GPU: the library launches
+    there."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current GPU is "
+                         f"{torch.cuda.current_device()}")
+    return _stream(device)
 
 
 def _check(code: int, where: str) -> None:
@@ -947,4 +971,129 @@ def twell_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, lse: tor
     _check(load().twell_logprob_backward(
         ctypes.byref(shape), _ptr(logits), _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(dlogp),
         _ptr(dentropy), _ptr(out), _row_stride(out), _stream(dev)), "twell_logprob_backward")
+    return out
+
+
+# ------------------------------------------------------------------ norms around the layer
+@dataclasses.dataclass
+class NormOut:
+    """Everything twell_norm_forward writes."""
+
+    residual: torch.Tensor        # [N, d_model] dtype; the residual itself without y
+    x: Optional[torch.Tensor]     # [N, d_model] dtype; None without w_pre
+
+
+@dataclasses.dataclass
+class NormGrads:
+    """Everything twell_norm_backward writes; None where there is no such input."""
+
+    d_residual: torch.Tensor         # [N, d_model] dtype
+    dy: Optional[torch.Tensor]       # [N, d_model] dtype
+    dw_post: Optional[torch.Tensor]  # [d_model] float32
+    dgate: Optional[torch.Tensor]    # [d_model] float32
+    dw_pre: Optional[torch.Tensor]   # [d_model] float32
+
+
+def _norm_shape(n: int, d: int, dtype: torch.dtype, residual_scale: float,
+                eps: float) -> NormShape:
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
+    if d >> 31:
+        _int32(d_model=d)
+    return NormShape(n, d, _DTYPE_CODE[dtype], residual_scale, eps)
+
+
+def _need_norm_weights(dev, d: int, w_post, gate, w_pre) -> None:
+    for name, w in (("w_post", w_post), ("gate", gate), ("w_pre", w_pre)):
+        if w is not None:
+            _need(w, name, dev, torch.float32, (d,))
+
+
+def twell_norm_forward(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                       w_post: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       w_pre: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                       eps: float = 1e-6, out: Optional[NormOut] = None) -> NormOut:
+    """The end of one block and the beginning of the next, on rows [N, d_model]:
+
+        residual' = residual_scale * residual + gate * norm(y) * w_post
+        x = norm(residual') * w_pre,   norm(v) = v / sqrt(mean(v^2) + eps)
+
+    Without w_post, y is not normalised; without y there is only x; without w_pre, no x.
+    Weights are [d_model] float32.  `out` may hold residual and y themselves."""
+    dev, dt = residual.device, residual.dtype
+    n, d = residual.shape
+    _need(residual, "residual", dev)
+    shape = _norm_shape(n, d, dt, residual_scale, eps)
+    _need_norm_weights(dev, d, w_post, gate, w_pre)
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need y")
+    if y is None and w_pre is None:
+        raise ValueError("nothing to do without y and w_pre")
+    if out is None:
+        out = NormOut(residual if y is None else torch.empty_like(residual),
+                      None if w_pre is None else torch.empty_like(residual))
+    if y is not None:
+        _need(y, "y", dev, dt, (n, d))
+        _need(out.residual, "residual out", dev, dt, (n, d))
+    if w_pre is not None:
+        _need(out.x, "x", dev, dt, (n, d))
+    _check(load().twell_norm_forward(
+        ctypes.byref(shape), _ptr(residual), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+        _ptr(out.residual) if y is not None else None, _ptr(out.x) if w_pre is not None else None,
+        _here(dev)), "twell_norm_forward")
+    return out
+
+
+def norm_backward_workspace(n_rows: int, d_model: int, dtype: torch.dtype,
+                            device) -> torch.Tensor:
+    """A workspace for twell_norm_backward of these sizes."""
+    shape = _norm_shape(n_rows, d_model, dtype, 1.0, 1e-6)
+    return torch.empty((int(load().twell_norm_backward_workspace_size(ctypes.byref(shape))),),
+                       dtype=torch.uint8, device=device)
+
+
+def twell_norm_backward(residual_out: torch.Tensor, y: Optional[torch.Tensor],
+                        d_residual_out: Optional[torch.Tensor], dx: Optional[torch.Tensor], *,
+                        w_post: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None,
+                        w_pre: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                        eps: float = 1e-6, out: Optional[NormGrads] = None,
+                        workspace: Optional[torch.Tensor] = None) -> NormGrads:
+    """Gradients of sum(d_residual_out * residual' + dx * x) of twell_norm_forward, from its
+    residual' and y.  d_residual_out may be None (zero), dx is None without w_pre."""
+    dev, dt = residual_out.device, residual_out.dtype
+    n, d = residual_out.shape
+    _need(residual_out, "residual_out", dev)
+    shape = _norm_shape(n, d, dt, residual_scale, eps)
+    _need_norm_weights(dev, d, w_post, gate, w_pre)
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need y")
+    if (dx is None) != (w_pre is None):
+        raise ValueError("dx and w_pre come together")
+    if w_pre is None and (y is None or d_residual_out is None):
+        raise ValueError("without w_pre, y and d_residual_out are needed")
+    for name, t in (("y", y), ("d_residual_out", d_residual_out), ("dx", dx)):
+        if t is not None:
+            _need(t, name, dev, dt, (n, d))
+    if out is None:
+        f = lambda w: None if w is None else torch.empty((d,), dtype=torch.float32, device=dev)
+        out = NormGrads(torch.empty_like(residual_out), None if y is None else torch.empty_like(y),
+                        f(w_post), f(gate), f(w_pre))
+    _need(out.d_residual, "d_residual", dev, dt, (n, d))
+    if y is not None:
+        _need(out.dy, "dy", dev, dt, (n, d))
+    for name, w, g in (("dw_post", w_post, out.dw_post), ("dgate", gate, out.dgate),
+                       ("dw_pre", w_pre, out.dw_pre)):
+        if w is not None:
+            _need(g, name, dev, torch.float32, (d,))
+    if workspace is None:
+        workspace = norm_backward_workspace(n, d, dt, dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    given = lambda w, g: _ptr(g) if w is not None else None
+    _check(load().twell_norm_backward(
+        ctypes.byref(shape), _ptr(residual_out), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+        _ptr(d_residual_out), _ptr(dx), _ptr(out.d_residual), given(y, out.dy),
+        given(w_post, out.dw_post), given(gate, out.dgate), given(w_pre, out.dw_pre),
+        _ptr(workspace), workspace.numel(), _here(dev)), "twell_norm_backward")
     return out

@@ -558,6 +558,58 @@ int twell_logprob_backward(const twell_logprob_shape* shape, const void* logits,
                            const float* dlogp, const float* dentropy, void* dlogits,
                            int64_t out_stride, void* stream);
 
+/* ---- The norms before and after the layer, with its gate and residual scale:
+ * what makes the layer's input x of a residual stream r and adds its output y
+ * to it.  Defined by this interface.  Per row of d_model columns:
+ *   u  = y / sqrt(mean(y^2) + eps) * w_post       (u = y without w_post)
+ *   r' = residual_scale * r + gate * u            (gate 1 without one)
+ *   x  = r' / sqrt(mean(r'^2) + eps) * w_pre
+ * so that one call ends a block and begins the next: y and w_post of the block
+ * before, w_pre of the one behind.
+ *  - r, y, r' and x are [n_rows][d_model] in dtype; w_post, gate and w_pre are
+ *    [d_model] float32.
+ *  - Without y (in front of the first block) r' = r: residual_out, w_post and
+ *    gate are NULL, w_pre is given and residual_scale is 1.  Without w_pre
+ *    (behind the last block) x is NULL.
+ *  - All arithmetic is float32, and r' and x are rounded once each (x is formed
+ *    from r' before its rounding).  Rows whose squares pass float32's range
+ *    (elements of about 1e19) are not normalised.
+ * Requirements: 0 <= n_rows < 2^31; d_model > 0 and a multiple of 8, at most
+ * 16384 (else TWELL_ERR_UNSUPPORTED); dtype a twell_dtype; residual_scale
+ * finite; eps positive and finite. */
+typedef struct twell_norm_shape {
+  int64_t n_rows;
+  int32_t d_model;
+  int32_t dtype;        /* twell_dtype of the rows */
+  float residual_scale;
+  float eps;
+} twell_norm_shape;
+
+/* residual_out = r', x.  residual_out may be residual, and x may be y (the same
+ * buffer, not one shifted against the other). */
+int twell_norm_forward(const twell_norm_shape* shape, const void* residual, const void* y,
+                       const float* w_post, const float* gate, const float* w_pre,
+                       void* residual_out, void* x, void* stream);
+
+/* Bytes of device workspace twell_norm_backward needs (0 for an invalid shape and
+ * for no rows): partial column sums. */
+size_t twell_norm_backward_workspace_size(const twell_norm_shape* shape);
+
+/* The gradients of sum(d_residual_out * r' + dx * x) from the forward's
+ * residual_out (r' as stored; r itself in a call without y; read only with
+ * w_pre) and y:
+ *   d_residual, dy in dtype; dw_post, dgate, dw_pre [d_model] float32.
+ * dy is given exactly with y, dx exactly with w_pre, and a weight's gradient
+ * exactly with the weight.  d_residual_out may be NULL (zero) with w_pre.  Weight
+ * gradients are written, not added to, by sums in a fixed order; n_rows == 0
+ * writes zeros.  d_residual and dy may be any of the inputs of their shape (the
+ * same buffer, not one shifted). */
+int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out, const void* y,
+                        const float* w_post, const float* gate, const float* w_pre,
+                        const void* d_residual_out, const void* dx, void* d_residual, void* dy,
+                        float* dw_post, float* dgate, float* dw_pre, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

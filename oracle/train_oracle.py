@@ -1,6 +1,6 @@
 """CPU oracle of the operators around the layer in a training step: 8-bit
-activation checkpoints, the token embedding, log probabilities.  NumPy in
-float64, from the definitions."""
+activation checkpoints, the token embedding, log probabilities, the norms around
+the layer.  NumPy in float64, from the definitions."""
 from __future__ import annotations
 
 import numpy as np
@@ -95,3 +95,51 @@ def logprob_grad(x, targets, scale, dlogp, dentropy):
         if g:
             out[r, targets[r]] += g
     return out * scale
+
+
+def norm(residual, y, w_post, gate, w_pre, alpha: float, eps: float):
+    """(r', x) of the norms around the layer; y, the weights or x may be None."""
+    r = residual
+    if y is not None:
+        u = y
+        if w_post is not None:
+            u = y / np.sqrt((y * y).mean(axis=1, keepdims=True) + eps) * w_post
+        r = alpha * residual + (u if gate is None else gate * u)
+    x = None
+    if w_pre is not None:
+        x = r / np.sqrt((r * r).mean(axis=1, keepdims=True) + eps) * w_pre
+    return r, x
+
+
+def norm_grad(residual_out, y, w_post, gate, w_pre, dr, dx, alpha: float, eps: float) -> dict:
+    """Gradients of sum(dr * r' + dx * x) from r' and y, with the size of what each sum adds up
+    ("of_" names: the same formulas over magnitudes), by which float32 results are judged."""
+    n, d = residual_out.shape
+    g = np.zeros((n, d)) if dr is None else dr
+    of_g = np.abs(g)
+    out = {}
+    if w_pre is not None:
+        rstd = 1 / np.sqrt((residual_out ** 2).mean(axis=1, keepdims=True) + eps)
+        rn, p = residual_out * rstd, dx * w_pre
+        g = g + rstd * (p - rn * (p * rn).mean(axis=1, keepdims=True))
+        of_g = of_g + rstd * (np.abs(p) + np.abs(rn) * np.abs(p * rn).mean(axis=1, keepdims=True))
+        out.update(dw_pre=(dx * rn).sum(axis=0), of_dw_pre=np.abs(dx * rn).sum(axis=0))
+    out.update(d_residual=alpha * g, of_d_residual=np.abs(alpha) * of_g)
+    if y is not None:
+        w = np.ones(d) if gate is None else gate
+        q, of_q, yn = g * w, of_g * np.abs(w), y
+        dy, of_dy = q, of_q
+        if w_post is not None:
+            q, of_q = q * w_post, of_q * np.abs(w_post)
+            ystd = 1 / np.sqrt((y * y).mean(axis=1, keepdims=True) + eps)
+            yn = y * ystd
+            dy = ystd * (q - yn * (q * yn).mean(axis=1, keepdims=True))
+            of_dy = ystd * (of_q + np.abs(yn) * (of_q * np.abs(yn)).mean(axis=1, keepdims=True))
+        out.update(dy=dy, of_dy=of_dy)
+        total, of_total = (g * yn).sum(axis=0), (of_g * np.abs(yn)).sum(axis=0)
+        if w_post is not None:
+            out.update(dw_post=total * w, of_dw_post=of_total * np.abs(w))
+        if gate is not None:
+            by = np.ones(d) if w_post is None else w_post
+            out.update(dgate=total * by, of_dgate=of_total * np.abs(by))
+    return out
