@@ -1,0 +1,629 @@
+// The output head's log probabilities without its logits, and their gradient.
+//
+// z[v][n] = scale * w[v] . x[n] is formed a tile at a time on MFMA, with the
+// vocabulary along the tile's rows: a lane then holds one token's column, and the
+// running maximum m and sum of exp(z - m) of a tile cost no lane exchange but the
+// one between the wave's halves.  The forward pass keeps {m, s} per tile and token
+// and joins them:  lse = m + log s,  logp = z_target - lse.
+//
+// The gradient takes the vocabulary in pieces, so that what it keeps of the logits
+// stays a part of them.  Per piece, with p = exp(z - m) / s and g = scale * dlogp:
+//   dl[n][v] = g[n] (1[v = target] - p)     from z formed again
+//   dx += dl w,   dw = dl^T x
+// dl is held as bfloat16 parts like the operands beside it: one part when x and w
+// are bfloat16 (its rounding, 2^-9 of each element, is of the size of dx's and dw's
+// own), three when they are float32.  Every product is K-major on both sides: w and
+// x are transposed once, dl is written both ways.
+#include <algorithm>
+
+#include "nt_gemm.h"
+#include "train_kernels.h"
+
+namespace twell {
+namespace {
+
+using nt::f32x16_t;
+using nt::Operand;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+typedef nt::Config<256, 256, 4, 2, 2> Big;
+typedef nt::Config<128, 128, 2, 2, 2> Mid;
+typedef nt::Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
+typedef nt::Config<128, 32, 4, 1, 4> Bare;  // at most 32
+
+__device__ __forceinline__ int64_t target_of(const void* targets, int index_bytes, int64_t n) {
+  return index_bytes == 8 ? static_cast<const int64_t*>(targets)[n]
+                          : static_cast<const int32_t*>(targets)[n];
+}
+
+// v of the lane with the other half's rows of the same column
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// ---------------------------------------------------------------- operand parts
+// parts [PARTS][rows][ld] of src [rows][d]; columns past d are zeros.
+template <typename E, int PARTS>
+__global__ __launch_bounds__(256) void split_kernel(const E* __restrict__ src, int64_t rows, int d,
+                                                    int ld, uint16_t* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int runs = ld / 8;
+  const int64_t row = i / runs;
+  const int c = static_cast<int>(i % runs) * 8;
+  if (row >= rows) return;
+  uint32_t w[PARTS][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t lo[PARTS] = {}, hi[PARTS] = {};
+    if (c < d) {
+      const E* s = src + row * d + c + 2 * k;
+      nt::split<PARTS>(ElemTraits<E>::to_f32(s[0]), lo);
+      nt::split<PARTS>(ElemTraits<E>::to_f32(s[1]), hi);
+    }
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+  }
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p)
+    *reinterpret_cast<uint4*>(out + (p * rows + row) * ld + c) =
+        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// parts [PARTS][d][ld] of the transpose of src [rows][d]; rows past the end, and
+// rows without a target (targets not null), are zeros: whatever x holds there
+// meets gradients of zero, and a NaN must not spread.
+template <typename E, int PARTS>
+__global__ __launch_bounds__(256) void transpose_kernel(const E* __restrict__ src, int rows, int d,
+                                                        int ld, const void* __restrict__ targets,
+                                                        int index_bytes, int vocab,
+                                                        uint16_t* __restrict__ out) {
+  __shared__ float tile[64][65];
+  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int run = threadIdx.x + 256 * i;
+    const int r = run / 8, c = run % 8 * 8;
+    bool live = r0 + r < rows && c0 + c < d;
+    if (live && targets != nullptr) {
+      const int64_t t = target_of(targets, index_bytes, r0 + r);
+      live = t >= 0 && t < vocab;
+    }
+    const E* s = src + static_cast<int64_t>(r0 + r) * d + c0 + c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tile[r][c + k] = live ? ElemTraits<E>::to_f32(s[k]) : 0.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int run = threadIdx.x + 256 * i;
+    const int c = run / 8, r = run % 8 * 8;
+    if (c0 + c >= d) continue;  // r0 + 64 <= ld
+    uint32_t w[PARTS][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint16_t lo[PARTS], hi[PARTS];
+      nt::split<PARTS>(tile[r + 2 * k][c], lo);
+      nt::split<PARTS>(tile[r + 2 * k + 1][c], hi);
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+    }
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+      *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(p) * d + c0 + c) * ld + r0 + r) =
+          make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+  }
+}
+
+// ---------------------------------------------------------------- forward
+struct StatsArgs {
+  Operand w, x;      // w: a piece of the vocabulary, from column v0
+  int v0, vocab;     // whole vocabulary
+  int ksteps;
+  float scale;
+  const void* targets;
+  int index_bytes;
+  float2* parts;     // [tiles][n], this piece's first tile onwards
+  float* target_z;   // [n], z of the target, written by the tile that holds it
+};
+
+template <class CF, int PARTS>
+__global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_blocks,
+                                                            int n_blocks) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
+  int mb, nb;
+  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  f32x16_t acc[CF::FM][CF::FN];
+  nt::mainloop<CF, PARTS>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  const int row0 = mb * CF::BM + nt::block_row<CF>();
+  const int half = lane_id() >> 5;
+  const int wave_row = row0 - 4 * half;  // the wave's first row
+  float2* joint = reinterpret_cast<float2*>(lds);  // [WAVES_M][BN]
+  const int wm = threadIdx.x / kWave / CF::WAVES_N;
+#pragma unroll
+  for (int j = 0; j < CF::FN; ++j) {
+    const int col = nt::block_col<CF>() + 32 * j;
+    const int n = nb * CF::BN + col;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        acc[i][j][r] *= a.scale;
+        if (row0 + nt::row_of(i, r) < a.w.rows) m = fmaxf(m, acc[i][j][r]);
+      }
+    m = fmaxf(m, other_half(m));
+    const float base = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (row0 + nt::row_of(i, r) < a.w.rows)
+          s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
+    s += other_half(s);
+    if (half == 0) joint[wm * CF::BN + col] = make_float2(m, s);
+    // the target's z, where this wave's rows hold it
+    int64_t t = -1;
+    if (n < a.x.rows) {
+      t = target_of(a.targets, a.index_bytes, n);
+      t = t >= 0 && t < a.vocab ? t - a.v0 - wave_row : -1;
+    }
+    const bool mine = t >= 0 && t < CF::WTM && wave_row + t < a.w.rows &&
+                      ((static_cast<int>(t) >> 2) & 1) == half;
+    if (wave_ballot(mine) != 0) {
+      const int rel = static_cast<int>(t) - 4 * half;
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (rel == nt::row_of(i, r)) z = acc[i][j][r];
+      if (mine) a.target_z[n] = z;
+    }
+  }
+  __syncthreads();
+  for (int col = threadIdx.x; col < CF::BN; col += CF::NT) {
+    const int n = nb * CF::BN + col;
+    if (n >= a.x.rows) continue;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < CF::WAVES_M; ++w) m = fmaxf(m, joint[w * CF::BN + col].x);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < CF::WAVES_M; ++w) {
+      const float2 p = joint[w * CF::BN + col];
+      s += p.y * __builtin_amdgcn_exp2f((p.x - base) * kLog2e);
+    }
+    a.parts[static_cast<int64_t>(mb) * a.x.rows + n] = make_float2(m, s);
+  }
+}
+
+// Joins the tiles' {m, s} of 16 tokens a workgroup, in 16 streams of tiles.
+__global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ parts,
+                                                        int tiles, int64_t n_rows,
+                                                        const void* __restrict__ targets,
+                                                        int index_bytes, int vocab,
+                                                        const float* __restrict__ target_z,
+                                                        float* __restrict__ logp,
+                                                        float* __restrict__ lse,
+                                                        float2* __restrict__ stats) {
+  __shared__ float2 joint[16][16];
+  const int col = threadIdx.x % 16, stream = threadIdx.x / 16;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 16 + col;
+  float m = -INFINITY, s = 0.f;
+  if (n < n_rows)
+    for (int t = stream; t < tiles; t += 16) {
+      const float2 p = parts[t * n_rows + n];
+      const float top = fmaxf(m, p.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) +
+          p.y * __builtin_amdgcn_exp2f((p.x - base) * kLog2e);
+      m = top;
+    }
+  joint[stream][col] = make_float2(m, s);
+  __syncthreads();
+  if (stream != 0 || n >= n_rows) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) m = fmaxf(m, joint[w][col].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w)
+    s += joint[w][col].y * __builtin_amdgcn_exp2f((joint[w][col].x - base) * kLog2e);
+  const float log_s = logf(s);  // -inf for a row with nothing left
+  const int64_t t = target_of(targets, index_bytes, n);
+  stats[n] = make_float2(m, s);
+  lse[n] = base + log_s;
+  float lp = 0.f;
+  // a row with nothing left: z - lse would be -inf + inf
+  if (t >= 0 && t < vocab) lp = m == -INFINITY && s == 0.f ? -INFINITY : target_z[n] - base - log_s;
+  logp[n] = lp;
+}
+
+// ---------------------------------------------------------------- gradient
+struct DlArgs {
+  Operand w, x;
+  int v0, vocab;
+  int ksteps;
+  float scale;
+  const void* targets;
+  int index_bytes;
+  const float2* stats;
+  const float* dlogp;
+  uint16_t* dl;    // [PARTS][n][ldv]
+  uint16_t* dlt;   // [PARTS][piece][ldn]
+  int ldv, ldn;
+};
+
+template <class CF, int PARTS>
+__global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks, int n_blocks) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
+  int mb, nb;
+  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  f32x16_t acc[CF::FM][CF::FN];
+  nt::mainloop<CF, PARTS>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  const int row0 = mb * CF::BM + nt::block_row<CF>();
+  const int64_t n_rows = a.x.rows;
+#pragma unroll
+  for (int j = 0; j < CF::FN; ++j) {
+    const int n = nb * CF::BN + nt::block_col<CF>() + 32 * j;
+    float g = 0.f, m = 0.f, inv = 0.f;
+    int t = -1;  // of the piece
+    bool given = false;
+    if (n < n_rows) {
+      const int64_t target = target_of(a.targets, a.index_bytes, n);
+      const float2 st = a.stats[n];
+      given = target >= 0 && target < a.vocab && !(st.x == -INFINITY && st.y == 0.f);
+      if (given) {
+        t = static_cast<int>(target) - a.v0;
+        g = a.dlogp[n] * a.scale;
+        m = st.x;
+        inv = 1.f / st.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int v = row0 + nt::row_of(i, 4 * q);
+        uint16_t part[4][PARTS];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float z = acc[i][j][4 * q + k] * a.scale;
+          const float p = __builtin_amdgcn_exp2f((z - m) * kLog2e) * inv;
+          const float d = given && v + k < a.w.rows ? g * ((v + k == t ? 1.f : 0.f) - p) : 0.f;
+          nt::split<PARTS>(d, part[k]);
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+          if (n < n_rows && v < a.ldv)
+            *reinterpret_cast<uint2*>(a.dl + (p * n_rows + n) * a.ldv + v) =
+                make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
+                           part[2][p] | static_cast<uint32_t>(part[3][p]) << 16);
+          if (n < a.ldn) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (v + k < a.w.rows)
+                a.dlt[(static_cast<int64_t>(p) * a.w.rows + v + k) * a.ldn + n] = part[k][p];
+          }
+        }
+      }
+  }
+}
+
+// out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, as floats
+// (ACC: slice after slice in out, added to where `add`) or as E.
+template <class CF, int PARTS, typename E, bool ACC>
+__global__ __launch_bounds__(CF::NT) void head_product_kernel(Operand A, Operand B, int ksteps,
+                                                              int m_blocks, int n_blocks,
+                                                              bool add, E* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
+  int mb, nb;
+  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  const int slices = gridDim.y, slice = blockIdx.y;
+  const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
+  const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
+  f32x16_t acc[CF::FM][CF::FN];
+  nt::mainloop<CF, PARTS>(A, mb * CF::BM, B, nb * CF::BN, s0 * nt::kStep, s1 - s0, lds, acc);
+  const int row0 = mb * CF::BM + nt::block_row<CF>();
+  if (ACC) out += static_cast<int64_t>(slice) * A.rows * B.rows;
+#pragma unroll
+  for (int j = 0; j < CF::FN; ++j) {
+    const int col = nb * CF::BN + nt::block_col<CF>() + 32 * j;
+    if (col >= B.rows) continue;
+    E* line = out + static_cast<int64_t>(col) * A.rows;
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = row0 + nt::row_of(i, 4 * q);
+        if (row >= A.rows) continue;  // A.rows is a multiple of 8
+        const f32x16_t& c = acc[i][j];
+        if constexpr (sizeof(E) == 2) {
+          typedef ElemTraits<uint16_t> Tr;
+          *reinterpret_cast<uint2*>(line + row) =
+              make_uint2(Tr::from_f32(c[4 * q]) |
+                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 1])) << 16,
+                         Tr::from_f32(c[4 * q + 2]) |
+                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 3])) << 16);
+        } else {
+          float4* at = reinterpret_cast<float4*>(line + row);
+          float4 v = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+          if (ACC && add) {
+            const float4 old = *at;
+            v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
+          }
+          *at = v;
+        }
+      }
+  }
+}
+
+// dx = the sum of the slices, rounded; 8 elements a lane.
+template <typename E>
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ sums,
+                                                      int slices, int64_t elems,
+                                                      E* __restrict__ dx) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= elems) return;
+  float v[8] = {};
+  for (int s = 0; s < slices; ++s)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += sums[s * elems + i + k];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) dx[i + k] = ElemTraits<E>::from_f32(v[k]);
+}
+
+__global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count;
+       i += static_cast<int64_t>(gridDim.x) * 256)
+    p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- sizes
+int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
+
+int parts_of(int elem_bytes) { return elem_bytes == 2 ? 1 : 3; }
+
+// Whether x and w serve as operands where they are.
+bool direct(int elem_bytes, int d) { return elem_bytes == 2 && d % 64 == 0; }
+
+// A tile for a product of `rows` x `cols`: the widest that covers few columns once;
+// 256 x 256 where that many tiles fill the CUs (one workgroup each), else 128 x 128
+// (two each).
+enum Tile { kBare, kFew, kMid, kBig };
+Tile tile_for(int64_t rows, int64_t cols) {
+  if (cols <= 32) return kBare;
+  if (cols <= 64) return kFew;
+  return blocks(rows, 256) * blocks(cols, 256) >= 192 ? kBig : kMid;
+}
+template <class F>
+hipError_t with_tile(Tile t, const F& f) {
+  switch (t) {
+    case kBare: return f(Bare());
+    case kFew: return f(Few());
+    case kMid: return f(Mid());
+    default: return f(Big());
+  }
+}
+int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
+
+// Columns of the vocabulary taken at a time: all where the forward pass reads w in
+// place, else as many as keep what is made per column within `budget`, in equal
+// pieces.
+int piece_of(int vocab, size_t per_column, size_t budget) {
+  const int64_t most = std::max<int64_t>(budget / per_column / 256 * 256, 1024);
+  const int64_t pieces = blocks(vocab, static_cast<int>(std::min<int64_t>(most, vocab)));
+  return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
+}
+
+struct Carve {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t count) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += (count * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
+
+struct ForwardPlan {
+  int piece, tiles;
+  uint16_t *xp, *wp;
+  float2* parts;
+  float* target_z;
+  size_t bytes;
+};
+ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
+  ForwardPlan p{};
+  const size_t ld = up64(a.d), part_bytes = 2 * parts_of(elem_bytes) * ld;
+  const bool in_place = direct(elem_bytes, a.d);
+  p.piece = in_place ? a.vocab : piece_of(a.vocab, part_bytes, size_t{128} << 20);
+  // tiles of a piece start at its first column: pieces but the last are whole tiles
+  const Tile t = tile_for(p.piece, a.n_rows);
+  p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(t)));
+  Carve c{static_cast<char*>(ws)};
+  p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
+  p.target_z = c.take<float>(a.n_rows);
+  if (!in_place) {
+    p.xp = c.take<uint16_t>(part_bytes / 2 * a.n_rows);
+    p.wp = c.take<uint16_t>(part_bytes / 2 * p.piece);
+  }
+  p.bytes = c.used;
+  return p;
+}
+
+struct BackwardPlan {
+  int piece, slices;
+  int ldn;
+  uint16_t *xp, *wp, *xt, *wt, *dl, *dlt;
+  float* sums;
+  size_t bytes;
+};
+BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
+  BackwardPlan p{};
+  const size_t P = parts_of(elem_bytes), ld = up64(a.d), n = a.n_rows;
+  const bool in_place = direct(elem_bytes, a.d);
+  p.ldn = static_cast<int>(up64(n));
+  const size_t per_column = 2 * P * (n + p.ldn + a.d + (in_place ? 0 : ld));
+  p.piece = piece_of(a.vocab, per_column, size_t{192} << 20);
+  const size_t ldv = up64(p.piece);
+  // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
+  const Tile t = tile_for(a.d, n);
+  const int64_t tiles = blocks(a.d, tile_rows(t)) *
+                        blocks(n, t == kBig ? 256 : t == kMid ? 128 : t == kFew ? 64 : 32);
+  p.slices = static_cast<int>(std::clamp<int64_t>(384 / std::max<int64_t>(tiles, 1), 1,
+                                                  std::min<int64_t>(32, ldv / 256 + 1)));
+  Carve c{static_cast<char*>(ws)};
+  p.xt = c.take<uint16_t>(P * a.d * p.ldn);
+  p.wt = c.take<uint16_t>(P * a.d * ldv);
+  p.dl = c.take<uint16_t>(P * n * ldv);
+  p.dlt = c.take<uint16_t>(P * p.piece * p.ldn);
+  p.sums = c.take<float>(p.slices * n * a.d);
+  if (!in_place) {
+    p.xp = c.take<uint16_t>(P * ld * n);
+    p.wp = c.take<uint16_t>(P * ld * p.piece);
+  }
+  p.bytes = c.used;
+  return p;
+}
+
+// ---------------------------------------------------------------- launches
+template <typename E, int P>
+void split(const void* src, int64_t row0, int64_t rows, int d, uint16_t* out, hipStream_t s) {
+  const int ld = static_cast<int>(up64(d));
+  split_kernel<E, P><<<static_cast<uint32_t>(blocks(rows * (ld / 8), 256)), 256, 0, s>>>(
+      static_cast<const E*>(src) + row0 * d, rows, d, ld, out);
+}
+
+template <typename E, int P>
+void transpose(const void* src, int64_t row0, int rows, int d, const HeadArgs* masked,
+               uint16_t* out, hipStream_t s) {
+  const int ld = static_cast<int>(up64(rows));
+  transpose_kernel<E, P><<<dim3(ld / 64, static_cast<uint32_t>(blocks(d, 64))), 256, 0, s>>>(
+      static_cast<const E*>(src) + row0 * d, rows, d, ld,
+      masked != nullptr ? masked->targets : nullptr, masked != nullptr ? masked->index_bytes : 0,
+      masked != nullptr ? masked->vocab : 0, out);
+}
+
+// The operand of `rows` rows from row0 of src: in place, or its parts in `to`.
+template <typename E, int P>
+Operand operand(const void* src, int64_t row0, int rows, int d, uint16_t* to, hipStream_t s) {
+  const int ld = static_cast<int>(up64(d));
+  if (direct(sizeof(E), d))
+    return Operand{static_cast<const uint16_t*>(src) + row0 * d, 0, d, rows};
+  split<E, P>(src, row0, rows, d, to, s);
+  return Operand{to, static_cast<int64_t>(rows) * ld, ld, rows};
+}
+
+template <typename E, int P>
+hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* stats,
+                   hipStream_t s) {
+  const ForwardPlan p = forward_plan(a, sizeof(E), ws);
+  const int n = static_cast<int>(a.n_rows);
+  const Operand x = operand<E, P>(a.x, 0, n, a.d, p.xp, s);
+  const Tile tile = tile_for(p.piece, n);
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+    const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
+    const Operand w = operand<E, P>(a.w, v0, rows, a.d, p.wp, s);
+    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, static_cast<int>(up64(a.d) / 64),
+                      a.scale, a.targets, a.index_bytes,
+                      p.parts + v0 / tile_rows(tile) * a.n_rows, p.target_z};
+    const hipError_t e = with_tile(tile, [&](auto cf) {
+      typedef decltype(cf) CF;
+      const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
+      head_stats_kernel<CF, P><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  head_join_kernel<<<static_cast<uint32_t>(blocks(n, 16)), 256, 0, s>>>(
+      p.parts, p.tiles, a.n_rows, a.targets, a.index_bytes, a.vocab, p.target_z, logp, lse,
+      reinterpret_cast<float2*>(stats));
+  return hipGetLastError();
+}
+
+template <typename E, int P>
+hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, void* ws, void* dx,
+                    void* dw, hipStream_t s) {
+  if (a.n_rows == 0) {
+    const int64_t count = static_cast<int64_t>(a.vocab) * a.d * sizeof(E) / 16;
+    head_zero_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(count, 256), 1 << 20)), 256,
+                       0, s>>>(static_cast<uint4*>(dw), count);
+    return hipGetLastError();
+  }
+  const BackwardPlan p = backward_plan(a, sizeof(E), ws);
+  const int n = static_cast<int>(a.n_rows);
+  const Operand x = operand<E, P>(a.x, 0, n, a.d, p.xp, s);
+  transpose<E, P>(a.x, 0, n, a.d, &a, p.xt, s);
+  const Operand xt{p.xt, static_cast<int64_t>(a.d) * p.ldn, p.ldn, a.d};
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+    const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
+    const int ldv = static_cast<int>(up64(rows));
+    const Operand w = operand<E, P>(a.w, v0, rows, a.d, p.wp, s);
+    transpose<E, P>(a.w, v0, rows, a.d, nullptr, p.wt, s);
+    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, static_cast<int>(up64(a.d) / 64), a.scale,
+                   a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
+                   p.dlt, ldv, p.ldn};
+    hipError_t e = with_tile(tile_for(rows, n), [&](auto cf) {
+      typedef decltype(cf) CF;
+      // ldn columns of dlt are written, of them the last as zeros
+      const int mb = static_cast<int>(blocks(rows, CF::BM));
+      const int nb = static_cast<int>(blocks(p.ldn, CF::BN));
+      head_dl_kernel<CF, P><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    const Operand wt{p.wt, static_cast<int64_t>(a.d) * ldv, ldv, a.d};
+    const Operand dl{p.dl, static_cast<int64_t>(n) * ldv, ldv, n};
+    const Operand dlt{p.dlt, static_cast<int64_t>(rows) * p.ldn, p.ldn, rows};
+    e = with_tile(tile_for(a.d, n), [&](auto cf) {
+      typedef decltype(cf) CF;
+      const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
+      head_product_kernel<CF, P, float, true>
+          <<<dim3(static_cast<uint32_t>(mb) * nb, p.slices), CF::NT, 0, s>>>(
+              wt, dl, ldv / 64, mb, nb, v0 > 0, p.sums);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    e = with_tile(tile_for(a.d, rows), [&](auto cf) {
+      typedef decltype(cf) CF;
+      const int mb = static_cast<int>(blocks(a.d, CF::BM));
+      const int nb = static_cast<int>(blocks(rows, CF::BN));
+      head_product_kernel<CF, P, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+          xt, dlt, p.ldn / 64, mb, nb, false, static_cast<E*>(dw) + v0 * a.d);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  const int64_t elems = a.n_rows * a.d;
+  head_dx_kernel<E><<<static_cast<uint32_t>(blocks(elems / 8, 256)), 256, 0, s>>>(
+      p.sums, p.slices, elems, static_cast<E*>(dx));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t head_forward_bytes(const HeadArgs& a, int elem_bytes) {
+  return a.n_rows == 0 ? 0 : forward_plan(a, elem_bytes, nullptr).bytes;
+}
+size_t head_backward_bytes(const HeadArgs& a, int elem_bytes) {
+  return a.n_rows == 0 ? 0 : backward_plan(a, elem_bytes, nullptr).bytes;
+}
+
+hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
+                               float* lse, float* stats, hipStream_t s) {
+  if (a.n_rows == 0) return hipSuccess;
+  return elem_bytes == 2 ? forward<uint16_t, 1>(a, ws, logp, lse, stats, s)
+                         : forward<float, 3>(a, ws, logp, lse, stats, s);
+}
+
+hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* stats,
+                                const float* dlogp, void* ws, void* dx, void* dw, hipStream_t s) {
+  return elem_bytes == 2 ? backward<uint16_t, 1>(a, stats, dlogp, ws, dx, dw, s)
+                         : backward<float, 3>(a, stats, dlogp, ws, dx, dw, s);
+}
+
+}  // namespace twell

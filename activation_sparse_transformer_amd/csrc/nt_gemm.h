@@ -1,0 +1,213 @@
+// Products C = A B^T of K-major bfloat16 operands on MFMA (32x32x16), and of
+// float32 operands held as bfloat16 parts.
+//
+// A float32 v is the sum of three bfloat16 parts, each the rounding of what the
+// ones before leave: 8 + 8 + 8 bits, so the sum is v.  Of the nine products of
+// two such values the six largest are formed; those left out are below 2^-25 of
+// the whole, the rounding of the float32 sum.  At 1/6 of the bfloat16 rate this
+// is still faster than MFMA's own float32 form (1/16).  Two parts and three
+// products leave 2^-17, for values that are rounded to bfloat16 in the end.
+//
+// Operands are [parts][rows][ld], ld a multiple of 64 with zeros past the
+// contraction's length; rows past the end read the last row and feed outputs
+// that no epilogue stores.
+#pragma once
+
+#include "common.h"
+
+namespace twell {
+namespace nt {
+
+constexpr int kStep = 64;  // K elements of one LDS stage
+
+struct Operand {
+  const uint16_t* p;
+  int64_t part;  // elements between parts
+  int64_t ld;    // elements between rows
+  int rows;
+};
+
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
+typedef __attribute__((ext_vector_type(4))) int i32x4_t;
+
+// Rows of 64 elements in LDS, the 16-byte chunk kc of row r at position kc ^
+// swizzle(r): the 32 rows x 2 chunks of a fragment read fall on distinct banks.
+__device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
+__device__ __forceinline__ int tile_offset(int r, int kc) {
+  return r * kStep + ((kc ^ swizzle(r)) << 3);
+}
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
+struct Config {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = NW * kWave;
+  static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;  // a wave's tile
+  static constexpr int FM = WTM / 32, FN = WTN / 32;            // its 32x32 blocks
+  static constexpr int A_ISSUE = BM / (8 * NW), B_ISSUE = BN / (8 * NW);  // copies a stage
+  static constexpr int STAGE = (BM + BN) * kStep;  // elements
+  static_assert(A_ISSUE * 8 * NW == BM && B_ISSUE * 8 * NW == BN, "whole 1 KB copies per wave");
+  static_assert(FM * 32 == WTM && FN * 32 == WTN, "32x32 blocks");
+};
+
+// Copies of one operand: instruction i of a wave fills 1 KB = 8 rows; lane l
+// fetches the chunk that belongs at LDS position l.
+template <int ISSUE, int NW>
+__device__ __forceinline__ void sources(const Operand& o, int r0, int k0,
+                                        const uint16_t* (&src)[ISSUE]) {
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int i = 0; i < ISSUE; ++i) {
+    const int r = (wave + NW * i) * 8 + lane / 8;
+    const int kc = (lane & 7) ^ swizzle(r);
+    src[i] = o.p + static_cast<int64_t>(min(r0 + r, o.rows - 1)) * o.ld + k0 + kc * 8;
+  }
+}
+template <int ISSUE, int NW>
+__device__ __forceinline__ void issue(const uint16_t* const* src, int64_t offset,
+                                      uint16_t* tile) {
+  const int wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int i = 0; i < ISSUE; ++i)
+    __builtin_amdgcn_global_load_lds(src[i] + offset, tile + (wave + NW * i) * 512, 16, 0, 0);
+}
+
+// The steps of a contraction: the products of parts one after another at each
+// 64 elements of K (the stages of one K come from the caches).
+constexpr int products(int parts) { return parts == 1 ? 1 : parts == 2 ? 3 : 6; }
+template <int PARTS>
+struct Walk {
+  int64_t part_a, part_b;
+  int k = 0, q = 0;
+  __device__ __forceinline__ void next() {
+    if (++q == products(PARTS)) {
+      q = 0;
+      k += kStep;
+    }
+  }
+  // parts (a, b): (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
+  __device__ __forceinline__ int64_t a() const {
+    return PARTS == 1 ? k : ((0x850 >> (2 * q)) & 3) * part_a + k;
+  }
+  __device__ __forceinline__ int64_t b() const {
+    return PARTS == 1 ? k : ((0x244 >> (2 * q)) & 3) * part_b + k;
+  }
+};
+
+// All but the last N copies of every wave landed, and every wave is done with its
+// LDS reads so far.
+template <int N>
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// acc = A[m0 .., k0 .. k0 + 64 ksteps) B[n0 .., the same]^T.  `lds`: STAGES stages.
+// Copies run STAGES - 1 stages ahead of the products.
+template <class CF, int PARTS>
+__device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand& B, int n0, int k0,
+                                         int ksteps, uint16_t* lds,
+                                         f32x16_t (&acc)[CF::FM][CF::FN]) {
+#pragma unroll
+  for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < CF::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const uint16_t* asrc[CF::A_ISSUE];
+  const uint16_t* bsrc[CF::B_ISSUE];
+  sources<CF::A_ISSUE, CF::NW>(A, m0, k0, asrc);
+  sources<CF::B_ISSUE, CF::NW>(B, n0, k0, bsrc);
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+  constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
+  const int steps = ksteps * products(PARTS);
+  Walk<PARTS> walk{A.part, B.part};
+  int fill = 0;  // the stage that the next copies go to
+  auto copy = [&]() {
+    uint16_t* stage = lds + fill * CF::STAGE;
+    issue<CF::A_ISSUE, CF::NW>(asrc, walk.a(), stage);
+    issue<CF::B_ISSUE, CF::NW>(bsrc, walk.b(), stage + CF::BM * kStep);
+    walk.next();
+    fill = fill + 1 == CF::STAGES ? 0 : fill + 1;
+  };
+  for (int s = 0; s < AHEAD && s < steps; ++s) copy();
+  int cur = 0;
+  for (int s = 0; s < steps; ++s) {
+    // stages s + 1 .. s + AHEAD - 1 may be in flight; near the end there are fewer
+    if (s + AHEAD <= steps) meet<(AHEAD - 1) * COPIES>();
+    else meet<0>();
+    if (s + AHEAD < steps) copy();
+    const uint16_t* sA = lds + cur * CF::STAGE;
+    const uint16_t* sB = sA + CF::BM * kStep;
+#pragma unroll
+    for (int ks = 0; ks < kStep / 16; ++ks) {
+      const int kc = ks * 2 + (lane >> 5);
+      bf16x8_t a[CF::FM], b[CF::FN];
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+        a[i] = *reinterpret_cast<const bf16x8_t*>(
+            sA + tile_offset(wm * CF::WTM + i * 32 + (lane & 31), kc));
+#pragma unroll
+      for (int j = 0; j < CF::FN; ++j)
+        b[j] = *reinterpret_cast<const bf16x8_t*>(
+            sB + tile_offset(wn * CF::WTN + j * 32 + (lane & 31), kc));
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < CF::FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    }
+    cur = cur + 1 == CF::STAGES ? 0 : cur + 1;
+  }
+  __syncthreads();  // the stages are free for the epilogue
+}
+
+// Element (i, r) of a lane's accumulators is row block_row<CF>() + row_of(i, r),
+// element j column block_col<CF>() + 32 j of the block.
+template <class CF>
+__device__ __forceinline__ int block_row() {
+  return threadIdx.x / kWave / CF::WAVES_N * CF::WTM + 4 * (lane_id() >> 5);
+}
+__device__ __forceinline__ constexpr int row_of(int i, int r) {
+  return i * 32 + (r >> 2) * 8 + (r & 3);
+}
+template <class CF>
+__device__ __forceinline__ int block_col() {
+  return threadIdx.x / kWave % CF::WAVES_N * CF::WTN + (lane_id() & 31);
+}
+
+// Tile b of m_blocks x n_blocks.  Workgroups are dealt round-robin to the 8 XCDs:
+// each XCD gets a contiguous run of tiles, walked in groups of 4 row blocks, so
+// that tiles running together share operands in its L2.
+__device__ __forceinline__ void tile_of(int b, int m_blocks, int n_blocks, int& mb, int& nb) {
+  const int total = m_blocks * n_blocks;
+  const int each = total / 8, more = total % 8, x = b % 8;
+  const int t = x * each + min(x, more) + b / 8;
+  const int per_group = 4 * n_blocks;
+  const int g = t / per_group, in = t - g * per_group;
+  const int rows = min(4, m_blocks - g * 4);
+  mb = g * 4 + in % rows;
+  nb = in / rows;
+}
+
+// The bfloat16 parts of v, most significant first.
+template <int PARTS>
+__device__ __forceinline__ void split(float v, uint16_t (&part)[PARTS]) {
+  typedef ElemTraits<uint16_t> Tr;
+  part[0] = Tr::from_f32(v);
+  if constexpr (PARTS > 1) {
+    const uint32_t u = __float_as_uint(v);
+    const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+    // a value that would round past the largest bfloat16 is cut instead
+    if (finite && (part[0] & 0x7f80u) == 0x7f80u) part[0] = static_cast<uint16_t>(u >> 16);
+    float rest = finite ? v - Tr::to_f32(part[0]) : 0.f;
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) {
+      part[i] = Tr::from_f32(rest);
+      rest -= Tr::to_f32(part[i]);
+    }
+  }
+}
+
+}  // namespace nt
+}  // namespace twell

@@ -120,4 +120,20 @@ int norm_grad_groups(int64_t n_rows, int d);
 hipError_t launch_norm_backward(const NormArgs& a, int elem_bytes, const NormGradArgs& p,
                                 hipStream_t s);
 
+// Log probabilities of targets [n_rows] under softmax(scale * x w^T) without the
+// logits, and their gradient.  x [n_rows][d], w [vocab][d].
+struct HeadArgs {
+  const void *x, *w, *targets;
+  int64_t n_rows;
+  int vocab, d, index_bytes;
+  float scale;
+};
+size_t head_forward_bytes(const HeadArgs& a, int elem_bytes);
+size_t head_backward_bytes(const HeadArgs& a, int elem_bytes);
+// stats [n_rows][2]: each row's largest z and its sum of exp(z - that)
+hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
+                               float* lse, float* stats, hipStream_t s);
+hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* stats,
+                                const float* dlogp, void* ws, void* dx, void* dw, hipStream_t s);
+
 }  // namespace twell

@@ -932,3 +932,85 @@ TWELL_EXPORT int twell_norm_backward(const twell_norm_shape* shape, const void* 
                                          elem_bytes(shape->dtype), p,
                                          static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ head log probabilities
+namespace twell {
+namespace {
+
+int check_head(const twell_head_shape* s) {
+  if (s == nullptr || s->reserved != 0) return TWELL_ERR_INVALID_ARG;
+  if (s->n_rows < 0 || s->vocab <= 0 || s->d_model <= 0 || s->d_model % 8 != 0)
+    return TWELL_ERR_INVALID_ARG;
+  if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (s->index_bytes != 4 && s->index_bytes != 8) return TWELL_ERR_INVALID_ARG;
+  if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return TWELL_ERR_INVALID_ARG;
+  // a launch holds fewer than 2^32 lanes
+  if (s->n_rows > 1 << 24 || s->vocab > 1 << 24 || s->d_model > 1 << 16)
+    return TWELL_ERR_UNSUPPORTED;
+  if (s->n_rows * s->vocab > int64_t{1} << 38 || s->n_rows * s->d_model > int64_t{1} << 34 ||
+      static_cast<int64_t>(s->vocab) * s->d_model > int64_t{1} << 36)
+    return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+HeadArgs head_args(const twell_head_shape* s, const void* x, const void* w, const void* targets) {
+  return HeadArgs{x, w, targets, s->n_rows, s->vocab, s->d_model, s->index_bytes, s->scale};
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT size_t twell_head_logprob_workspace_size(const twell_head_shape* shape) {
+  if (check_head(shape) != TWELL_OK) return 0;
+  return head_forward_bytes(head_args(shape, nullptr, nullptr, nullptr),
+                            elem_bytes(shape->dtype));
+}
+
+TWELL_EXPORT int twell_head_logprob_forward(const twell_head_shape* shape, const void* x,
+                                            const void* w, const void* targets, float* logp,
+                                            float* lse, float* stats, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  const int rc = check_head(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_rows > 0 && (x == nullptr || w == nullptr || targets == nullptr ||
+                            logp == nullptr || lse == nullptr || stats == nullptr ||
+                            workspace == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned(targets, shape->index_bytes) ||
+      !aligned(logp, 4) || !aligned(lse, 4) || !aligned(stats, 8) || !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  const HeadArgs a = head_args(shape, x, w, targets);
+  const int eb = elem_bytes(shape->dtype);
+  if (workspace_bytes < head_forward_bytes(a, eb)) return TWELL_ERR_WORKSPACE;
+  return hip_status(launch_head_forward(a, eb, workspace, logp, lse, stats,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+TWELL_EXPORT size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape) {
+  if (check_head(shape) != TWELL_OK) return 0;
+  return head_backward_bytes(head_args(shape, nullptr, nullptr, nullptr),
+                             elem_bytes(shape->dtype));
+}
+
+TWELL_EXPORT int twell_head_logprob_backward(const twell_head_shape* shape, const void* x,
+                                             const void* w, const void* targets,
+                                             const float* stats, const float* dlogp, void* dx,
+                                             void* dw, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  const int rc = check_head(shape);
+  if (rc != TWELL_OK) return rc;
+  if (shape->n_rows > 0 && (x == nullptr || w == nullptr || targets == nullptr ||
+                            stats == nullptr || dlogp == nullptr || dx == nullptr ||
+                            workspace == nullptr))
+    return TWELL_ERR_INVALID_ARG;
+  if (dw == nullptr) return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned(targets, shape->index_bytes) ||
+      !aligned(stats, 8) || !aligned(dlogp, 4) || !aligned16(dx) || !aligned16(dw) ||
+      !aligned16(workspace))
+    return TWELL_ERR_INVALID_ARG;
+  const HeadArgs a = head_args(shape, x, w, targets);
+  const int eb = elem_bytes(shape->dtype);
+  if (workspace_bytes < head_backward_bytes(a, eb)) return TWELL_ERR_WORKSPACE;
+  return hip_status(launch_head_backward(a, eb, stats, dlogp, workspace, dx, dw,
+                                         static_cast<hipStream_t>(stream)));
+}

@@ -39,6 +39,8 @@ EXPORTS = (
     "twell_embed_forward", "twell_embed_backward_workspace_size", "twell_embed_backward",
     "twell_logprob_workspace_size", "twell_logprob_forward", "twell_logprob_backward",
     "twell_norm_forward", "twell_norm_backward_workspace_size", "twell_norm_backward",
+    "twell_head_logprob_workspace_size", "twell_head_logprob_forward",
+    "twell_head_logprob_backward_workspace_size", "twell_head_logprob_backward",
 )
 
 
@@ -96,6 +98,14 @@ class NormShape(ctypes.Structure):
     _fields_ = [
         ("n_rows", ctypes.c_int64), ("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
+    ]
+
+
+class HeadShape(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("d_model", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -164,6 +174,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.twell_norm_backward_workspace_size.argtypes = [N]
     lib.twell_norm_backward_workspace_size.restype = sz
     lib.twell_norm_backward.argtypes, lib.twell_norm_backward.restype = [N, *[P] * 13, sz, P], I
+    D = ctypes.POINTER(HeadShape)
+    for name in ("twell_head_logprob_workspace_size", "twell_head_logprob_backward_workspace_size"):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [D], sz
+    lib.twell_head_logprob_forward.argtypes = [D, *[P] * 7, sz, P]
+    lib.twell_head_logprob_forward.restype = I
+    lib.twell_head_logprob_backward.argtypes = [D, *[P] * 8, sz, P]
+    lib.twell_head_logprob_backward.restype = I
     _lib = lib
     return lib
 
@@ -1096,4 +1113,109 @@ def twell_norm_backward(residual_out: torch.Tensor, y: Optional[torch.Tensor],
         _ptr(d_residual_out), _ptr(dx), _ptr(out.d_residual), given(y, out.dy),
         given(w_post, out.dw_post), given(gate, out.dgate), given(w_pre, out.dw_pre),
         _ptr(workspace), workspace.numel(), _here(dev)), "twell_norm_backward")
+    return out
+
+
+# ------------------------------------------------------------------ head log probabilities
+@dataclasses.dataclass
+class HeadLogProbs:
+    """Everything twell_head_logprob_forward writes."""
+
+    logp: torch.Tensor   # [N] float32, of the targets (0 where ignored)
+    lse: torch.Tensor    # [N] float32
+    stats: torch.Tensor  # [N, 2] float32: largest z, sum of exp(z - that); for the gradient
+
+
+@dataclasses.dataclass
+class HeadGrads:
+    """Everything twell_head_logprob_backward writes."""
+
+    dx: torch.Tensor  # [N, d_model] dtype
+    dw: torch.Tensor  # [vocab, d_model] dtype
+
+
+def _head_shape(n: int, vocab: int, d: int, dtype: torch.dtype, index: torch.dtype,
+                scale: float) -> HeadShape:
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
+    if index not in _INDEX_BYTES:
+        raise ValueError(f"targets must be int32 or int64, got {index}")
+    if (vocab | d) >> 31:
+        _int32(vocab=vocab, d_model=d)
+    return HeadShape(n, vocab, d, _DTYPE_CODE[dtype], _INDEX_BYTES[index], scale, 0)
+
+
+def _head_operands(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                   scale: float) -> HeadShape:
+    dev = x.device
+    n, d = x.shape
+    vocab = w.shape[0]
+    shape = _head_shape(n, vocab, d, x.dtype, targets.dtype, scale)
+    _need(x, "x", dev)
+    _need(w, "w", dev, x.dtype, (vocab, d))
+    _need(targets, "targets", dev, shape=(n,))
+    return shape
+
+
+def _head_bytes(shape: HeadShape, backward: bool) -> int:
+    lib = load()
+    f = (lib.twell_head_logprob_backward_workspace_size if backward
+         else lib.twell_head_logprob_workspace_size)
+    return int(f(ctypes.byref(shape)))
+
+
+def head_logprob_workspace(n_rows: int, vocab: int, d_model: int, dtype: torch.dtype, device,
+                           backward: bool = False) -> torch.Tensor:
+    """A workspace for twell_head_logprob_forward, or with `backward` for its gradient."""
+    shape = _head_shape(n_rows, vocab, d_model, dtype, torch.int64, 1.0)
+    return torch.empty((_head_bytes(shape, backward),), dtype=torch.uint8, device=device)
+
+
+def twell_head_logprob_forward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, *,
+                               scale: float = 1.0, out: Optional[HeadLogProbs] = None,
+                               workspace: Optional[torch.Tensor] = None) -> HeadLogProbs:
+    """Log probabilities of targets [N] under softmax(scale * x @ w.T) and each row's
+    log-sum-exp, for hidden states x [N, d_model] and an output head w [vocab, d_model],
+    without the logits.  A target outside the vocabulary is ignored."""
+    dev = x.device
+    shape = _head_operands(x, w, targets, scale)
+    n = shape.n_rows
+    if out is None:
+        f = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)
+        out = HeadLogProbs(f(n), f(n), f(n, 2))
+    _need(out.logp, "logp", dev, torch.float32, (n,))
+    _need(out.lse, "lse", dev, torch.float32, (n,))
+    _need(out.stats, "stats", dev, torch.float32, (n, 2))
+    if workspace is None:
+        workspace = torch.empty((_head_bytes(shape, False),), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    _check(load().twell_head_logprob_forward(
+        ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(targets), _ptr(out.logp), _ptr(out.lse),
+        _ptr(out.stats), _ptr(workspace), workspace.numel(), _here(dev)),
+        "twell_head_logprob_forward")
+    return out
+
+
+def twell_head_logprob_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                                stats: torch.Tensor, dlogp: torch.Tensor, *, scale: float = 1.0,
+                                out: Optional[HeadGrads] = None,
+                                workspace: Optional[torch.Tensor] = None) -> HeadGrads:
+    """The gradients dx, dw of sum(dlogp * logp) of twell_head_logprob_forward, from its
+    stats."""
+    dev = x.device
+    shape = _head_operands(x, w, targets, scale)
+    n = shape.n_rows
+    _need(stats, "stats", dev, torch.float32, (n, 2))
+    _need(dlogp, "dlogp", dev, torch.float32, (n,))
+    if out is None:
+        out = HeadGrads(torch.empty_like(x), torch.empty_like(w))
+    _need(out.dx, "dx", dev, x.dtype, x.shape)
+    _need(out.dw, "dw", dev, w.dtype, w.shape)
+    if workspace is None:
+        workspace = torch.empty((_head_bytes(shape, True),), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    _check(load().twell_head_logprob_backward(
+        ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(targets), _ptr(stats), _ptr(dlogp),
+        _ptr(out.dx), _ptr(out.dw), _ptr(workspace), workspace.numel(), _here(dev)),
+        "twell_head_logprob_backward")
     return out

@@ -610,6 +610,64 @@ int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
                         float* dw_post, float* dgate, float* dw_pre, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* ---- Log probabilities of given tokens from the last hidden states and the
+ * output head's weights, without the logits: for vocabularies whose [n_rows][vocab]
+ * logits (and their gradient) would not fit or would cost more than the products.
+ * Defined by this interface, after twell_logprob_*.  With x [n_rows][d_model] and
+ * w [vocab][d_model] (one row per token, as an embedding table) in dtype:
+ *   z_v = scale * (x_n . w_v);  lse = log sum_v exp z_v;  logp = z_target - lse
+ *  - targets [n_rows] are int32 or int64 (index_bytes 4 or 8); a target outside
+ *    [0, vocab) is ignored: its logp is 0, and its row of x has no gradient and
+ *    adds to none, whatever that row holds.  targets and the arrays per row are
+ *    aligned to their elements only.
+ *  - z is a float32 sum (float32 operands: six products of bfloat16 parts, as exact
+ *    as float32 ones); maxima, sums and probabilities are float32.  It is never
+ *    stored: the gradient forms it again.
+ *  - A row with a NaN, or an infinity that meets its product, has NaN results; a
+ *    float32 infinity in x or w makes every z of its row or column NaN.  z = -inf
+ *    has probability 0; a row with nothing else has lse = logp = -inf and a zero
+ *    gradient.
+ * Requirements: n_rows >= 0; vocab > 0; d_model > 0 and a multiple of 8; dtype a
+ * twell_dtype; scale positive and finite; reserved 0.  Limits, else
+ * TWELL_ERR_UNSUPPORTED: n_rows and vocab at most 2^24, d_model at most 2^16,
+ * n_rows * vocab at most 2^38, n_rows * d_model at most 2^34, vocab * d_model at
+ * most 2^36. */
+typedef struct twell_head_shape {
+  int64_t n_rows;
+  int32_t vocab;
+  int32_t d_model;
+  int32_t dtype;       /* twell_dtype of x, w, dx and dw */
+  int32_t index_bytes; /* 4 or 8 */
+  float scale;
+  int32_t reserved;    /* must be 0 */
+} twell_head_shape;
+
+/* Bytes of device workspace twell_head_logprob_forward needs (0 for an invalid
+ * shape and for no rows): a maximum and a sum per row and 128 or 256 columns; in
+ * float32, or where d_model is no multiple of 64, parts of x and of a piece of w. */
+size_t twell_head_logprob_workspace_size(const twell_head_shape* shape);
+
+/* logp and lse [n_rows] float32, and stats [n_rows][2] float32 (8-byte aligned):
+ * each row's largest z and its sum of exp(z - that), which the gradient takes. */
+int twell_head_logprob_forward(const twell_head_shape* shape, const void* x, const void* w,
+                               const void* targets, float* logp, float* lse, float* stats,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace twell_head_logprob_backward needs (0 for an invalid
+ * shape and for no rows): the gradient of a piece of the vocabulary's logits and
+ * transposed operands, about 200 MB beside float32 sums of dx. */
+size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape);
+
+/* The gradients of sum_n dlogp[n] logp[n] from the forward's stats:
+ *   dl = scale * dlogp (1[v = target] - exp(z_v) / sum exp z);  dx = dl w,  dw = dl^T x
+ * dx [n_rows][d_model] and dw [vocab][d_model] in dtype, written, not added to; sums
+ * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w) or as
+ * three bfloat16 parts (float32).  n_rows == 0 writes a zero dw. */
+int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, const void* w,
+                                const void* targets, const float* stats, const float* dlogp,
+                                void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,6 @@
 """CPU oracle of the operators around the layer in a training step: 8-bit
 activation checkpoints, the token embedding, log probabilities, the norms around
-the layer.  NumPy in float64, from the definitions."""
+the layer, the output head.  NumPy in float64, from the definitions."""
 from __future__ import annotations
 
 import numpy as np
@@ -143,3 +143,33 @@ def norm_grad(residual_out, y, w_post, gate, w_pre, dr, dx, alpha: float, eps: f
             by = np.ones(d) if w_post is None else w_post
             out.update(dgate=total * by, of_dgate=of_total * np.abs(by))
     return out
+
+
+def head_logprob(x, w, targets, scale: float):
+    """(logp, lse, stats, z) of targets under softmax(z), z = scale * x w^T; a target outside the
+    vocabulary has logp 0."""
+    z = scale * (x @ w.T)
+    m = z.max(axis=1)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        s = np.where(np.isneginf(m), 0.0, np.exp(z - m[:, None]).sum(axis=1))
+        lse = np.where(np.isneginf(m), -np.inf, m + np.log(s))
+    ok = (targets >= 0) & (targets < len(w))
+    at = z[np.arange(len(z)), np.where(ok, targets, 0)]
+    with np.errstate(invalid="ignore"):
+        logp = np.where(ok, np.where(np.isneginf(lse), -np.inf, at - lse), 0.0)
+    return logp, lse, np.stack([m, s], axis=1), z
+
+
+def head_logprob_grad(x, w, targets, dlogp, scale: float):
+    """(dx, dw, dl) of sum(dlogp * logp); rows without a target take no part."""
+    ok = (targets >= 0) & (targets < len(w))
+    dl = np.zeros((len(x), len(w)))
+    logp, lse, _, z = head_logprob(x[ok], w, targets[ok], scale)
+    live = ~np.isneginf(lse)
+    with np.errstate(invalid="ignore"):
+        p = np.where(live[:, None], np.exp(z - lse[:, None]), 0.0)
+    d = -p
+    d[np.arange(len(d)), targets[ok]] += 1
+    dl[ok] = np.where(live[:, None], d, 0.0) * (scale * dlogp[ok])[:, None]
+    x = np.where(ok[:, None], x, 0.0)
+    return dl @ w, dl.T @ x, dl
