@@ -24,7 +24,7 @@ ARCH = "gfx950"
 SOURCES = ["twell_api.hip", "gemm_bf16.hip", "gemm_f32.hip", "route.hip", "spmm.hip", "skinny.hip",
            "ell.hip", "backward.hip", "gate.hip", "act8.hip",
            "backward_act8.hip", "embed.hip", "logprob.hip",
-           "norm.hip", "head.hip"]
+           "norm.hip", "head.hip", "orth.hip"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"--offload-arch={ARCH}",

@@ -22,15 +22,9 @@
 namespace twell {
 namespace {
 
-using nt::f32x16_t;
-using nt::Operand;
+using namespace nt;
 
 constexpr float kLog2e = 1.44269504088896340736f;
-
-typedef nt::Config<256, 256, 4, 2, 2> Big;
-typedef nt::Config<128, 128, 2, 2, 2> Mid;
-typedef nt::Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
-typedef nt::Config<128, 32, 4, 1, 4> Bare;  // at most 32
 
 __device__ __forceinline__ int64_t target_of(const void* targets, int index_bytes, int64_t n) {
   return index_bytes == 8 ? static_cast<const int64_t*>(targets)[n]
@@ -311,54 +305,6 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   }
 }
 
-// out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, as floats
-// (ACC: slice after slice in out, added to where `add`) or as E.
-template <class CF, int PARTS, typename E, bool ACC>
-__global__ __launch_bounds__(CF::NT) void head_product_kernel(Operand A, Operand B, int ksteps,
-                                                              int m_blocks, int n_blocks,
-                                                              bool add, E* __restrict__ out) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
-  int mb, nb;
-  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
-  const int slices = gridDim.y, slice = blockIdx.y;
-  const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
-  const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
-  f32x16_t acc[CF::FM][CF::FN];
-  nt::mainloop<CF, PARTS>(A, mb * CF::BM, B, nb * CF::BN, s0 * nt::kStep, s1 - s0, lds, acc);
-  const int row0 = mb * CF::BM + nt::block_row<CF>();
-  if (ACC) out += static_cast<int64_t>(slice) * A.rows * B.rows;
-#pragma unroll
-  for (int j = 0; j < CF::FN; ++j) {
-    const int col = nb * CF::BN + nt::block_col<CF>() + 32 * j;
-    if (col >= B.rows) continue;
-    E* line = out + static_cast<int64_t>(col) * A.rows;
-#pragma unroll
-    for (int i = 0; i < CF::FM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = row0 + nt::row_of(i, 4 * q);
-        if (row >= A.rows) continue;  // A.rows is a multiple of 8
-        const f32x16_t& c = acc[i][j];
-        if constexpr (sizeof(E) == 2) {
-          typedef ElemTraits<uint16_t> Tr;
-          *reinterpret_cast<uint2*>(line + row) =
-              make_uint2(Tr::from_f32(c[4 * q]) |
-                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 1])) << 16,
-                         Tr::from_f32(c[4 * q + 2]) |
-                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 3])) << 16);
-        } else {
-          float4* at = reinterpret_cast<float4*>(line + row);
-          float4 v = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
-          if (ACC && add) {
-            const float4 old = *at;
-            v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
-          }
-          *at = v;
-        }
-      }
-  }
-}
-
 // dx = the sum of the slices, rounded; 8 elements a lane.
 template <typename E>
 __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ sums,
@@ -381,33 +327,10 @@ __global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count)
 }
 
 // ---------------------------------------------------------------- sizes
-int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
-int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
-
 int parts_of(int elem_bytes) { return elem_bytes == 2 ? 1 : 3; }
 
 // Whether x and w serve as operands where they are.
 bool direct(int elem_bytes, int d) { return elem_bytes == 2 && d % 64 == 0; }
-
-// A tile for a product of `rows` x `cols`: the widest that covers few columns once;
-// 256 x 256 where that many tiles fill the CUs (one workgroup each), else 128 x 128
-// (two each).
-enum Tile { kBare, kFew, kMid, kBig };
-Tile tile_for(int64_t rows, int64_t cols) {
-  if (cols <= 32) return kBare;
-  if (cols <= 64) return kFew;
-  return blocks(rows, 256) * blocks(cols, 256) >= 192 ? kBig : kMid;
-}
-template <class F>
-hipError_t with_tile(Tile t, const F& f) {
-  switch (t) {
-    case kBare: return f(Bare());
-    case kFew: return f(Few());
-    case kMid: return f(Mid());
-    default: return f(Big());
-  }
-}
-int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
 
 // Columns of the vocabulary taken at a time: all where the forward pass reads w in
 // place, else as many as keep what is made per column within `budget`, in equal
@@ -417,17 +340,6 @@ int piece_of(int vocab, size_t per_column, size_t budget) {
   const int64_t pieces = blocks(vocab, static_cast<int>(std::min<int64_t>(most, vocab)));
   return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
 }
-
-struct Carve {
-  char* base;
-  size_t used = 0;
-  template <typename T>
-  T* take(size_t count) {
-    T* p = reinterpret_cast<T*>(base + used);
-    used += (count * sizeof(T) + 255) / 256 * 256;
-    return p;
-  }
-};
 
 struct ForwardPlan {
   int piece, tiles;
@@ -471,11 +383,7 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.piece = piece_of(a.vocab, per_column, size_t{192} << 20);
   const size_t ldv = up64(p.piece);
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  const Tile t = tile_for(a.d, n);
-  const int64_t tiles = blocks(a.d, tile_rows(t)) *
-                        blocks(n, t == kBig ? 256 : t == kMid ? 128 : t == kFew ? 64 : 32);
-  p.slices = static_cast<int>(std::clamp<int64_t>(384 / std::max<int64_t>(tiles, 1), 1,
-                                                  std::min<int64_t>(32, ldv / 256 + 1)));
+  p.slices = slices_for(a.d, n, ldv / 64);
   Carve c{static_cast<char*>(ws)};
   p.xt = c.take<uint16_t>(P * a.d * p.ldn);
   p.wt = c.take<uint16_t>(P * a.d * ldv);
@@ -582,9 +490,9 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     e = with_tile(tile_for(a.d, n), [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      head_product_kernel<CF, P, float, true>
+      nt::product_kernel<CF, P, float, true>
           <<<dim3(static_cast<uint32_t>(mb) * nb, p.slices), CF::NT, 0, s>>>(
-              wt, dl, ldv / 64, mb, nb, v0 > 0, p.sums);
+              wt, dl, ldv / 64, mb, nb, v0 > 0, a.d, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -592,8 +500,8 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      head_product_kernel<CF, P, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
-          xt, dlt, p.ldn / 64, mb, nb, false, static_cast<E*>(dw) + v0 * a.d);
+      nt::product_kernel<CF, P, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+          xt, dlt, p.ldn / 64, mb, nb, false, a.d, static_cast<E*>(dw) + v0 * a.d);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

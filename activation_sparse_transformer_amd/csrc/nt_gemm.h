@@ -13,6 +13,8 @@
 // that no epilogue stores.
 #pragma once
 
+#include <algorithm>
+
 #include "common.h"
 
 namespace twell {
@@ -208,6 +210,105 @@ __device__ __forceinline__ void split(float v, uint16_t (&part)[PARTS]) {
     }
   }
 }
+
+// out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, lines of
+// `pitch` elements (a multiple of 8, not under A.rows; what lies past A.rows is
+// undefined): as floats (ACC: slice after slice in out, added to where `add`) or as E.
+template <class CF, int PARTS, typename E, bool ACC>
+__global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, int ksteps,
+                                                         int m_blocks, int n_blocks, bool add,
+                                                         int pitch, E* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
+  int mb, nb;
+  tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  const int slices = gridDim.y, slice = blockIdx.y;
+  const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
+  const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
+  f32x16_t acc[CF::FM][CF::FN];
+  mainloop<CF, PARTS>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
+  const int row0 = mb * CF::BM + block_row<CF>();
+  if (ACC) out += static_cast<int64_t>(slice) * pitch * B.rows;
+#pragma unroll
+  for (int j = 0; j < CF::FN; ++j) {
+    const int col = nb * CF::BN + block_col<CF>() + 32 * j;
+    if (col >= B.rows) continue;
+    E* line = out + static_cast<int64_t>(col) * pitch;
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = row0 + row_of(i, 4 * q);
+        if (row >= pitch) continue;
+        const f32x16_t& c = acc[i][j];
+        if constexpr (sizeof(E) == 2) {
+          typedef ElemTraits<uint16_t> Tr;
+          *reinterpret_cast<uint2*>(line + row) =
+              make_uint2(Tr::from_f32(c[4 * q]) |
+                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 1])) << 16,
+                         Tr::from_f32(c[4 * q + 2]) |
+                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 3])) << 16);
+        } else {
+          float4* at = reinterpret_cast<float4*>(line + row);
+          float4 v = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+          if (ACC && add) {
+            const float4 old = *at;
+            v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
+          }
+          *at = v;
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+typedef Config<256, 256, 4, 2, 2> Big;
+typedef Config<128, 128, 2, 2, 2> Mid;
+typedef Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
+typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32
+
+inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+inline int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
+
+// A tile for a product of `rows` x `cols`: the widest that covers few columns once;
+// 256 x 256 where that many tiles fill the CUs (one workgroup each), else 128 x 128
+// (two each).
+enum Tile { kBare, kFew, kMid, kBig };
+inline Tile tile_for(int64_t rows, int64_t cols) {
+  if (cols <= 32) return kBare;
+  if (cols <= 64) return kFew;
+  return blocks(rows, 256) * blocks(cols, 256) >= 192 ? kBig : kMid;
+}
+template <class F>
+hipError_t with_tile(Tile t, const F& f) {
+  switch (t) {
+    case kBare: return f(Bare());
+    case kFew: return f(Few());
+    case kMid: return f(Mid());
+    default: return f(Big());
+  }
+}
+inline int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
+inline int tile_cols(Tile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kFew ? 64 : 32; }
+
+// Slices of K for a product whose tiles alone do not fill the CUs: as many as do,
+// of at least 4 steps.
+inline int slices_for(int64_t rows, int64_t cols, int64_t ksteps) {
+  const Tile t = tile_for(rows, cols);
+  const int64_t tiles = blocks(rows, tile_rows(t)) * blocks(cols, tile_cols(t));
+  return static_cast<int>(
+      std::clamp<int64_t>(384 / std::max<int64_t>(tiles, 1), 1, std::clamp<int64_t>(ksteps / 4, 1, 32)));
+}
+
+struct Carve {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t count) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += (count * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
 
 }  // namespace nt
 }  // namespace twell

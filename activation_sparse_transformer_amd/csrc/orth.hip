@@ -1,0 +1,294 @@
+// The orthogonalised update of a weight matrix M by Newton-Schulz products: with
+// X = M / (|M|_F + eps), its shorter side m along the rows,
+//   G = X X^T,   B = b G + c G G,   X <- a X + B X        (steps times)
+// every singular value s of X becomes a s + b s^3 + c s^5, which the usual
+// coefficients drive towards 1.
+//
+// All products run on MFMA over bfloat16 parts of float32 values (nt_gemm.h): three
+// parts for a float32 M, two for a bfloat16 one, whose result is rounded to 2^-9.  A
+// product leaves float32 partial sums, slices of K where its tiles are few; a pass
+// over them adds the slices, forms G, B or the next X in float32 and writes its
+// parts, X also transposed, since both G and B X contract K-major operands.
+#include <algorithm>
+
+#include "nt_gemm.h"
+#include "train_kernels.h"
+
+namespace twell {
+namespace {
+
+using namespace nt;
+
+constexpr int kNormBlocks = 1024;
+
+// Partial sums of squares in double: no float32 value squared leaves its range.
+template <typename E>
+__global__ __launch_bounds__(256) void orth_norm_kernel(const E* __restrict__ m, int64_t elems,
+                                                        double* __restrict__ parts) {
+  __shared__ double lds[256];
+  double s = 0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < elems;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const double v = ElemTraits<E>::to_f32(m[i]);
+    s += v * v;
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  for (int h = 128; h > 0; h /= 2) {
+    if (static_cast<int>(threadIdx.x) < h) lds[threadIdx.x] += lds[threadIdx.x + h];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) parts[blockIdx.x] = lds[0];
+}
+
+// The factor 1 / (|M|_F + eps), from the parts in a fixed order, by every workgroup.
+__device__ __forceinline__ double inverse_norm(const double* __restrict__ parts, int count,
+                                               float eps, double* lds) {
+  double s = 0;
+  for (int i = threadIdx.x; i < count; i += 256) s += parts[i];
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  for (int h = 128; h > 0; h /= 2) {
+    if (static_cast<int>(threadIdx.x) < h) lds[threadIdx.x] += lds[threadIdx.x + h];
+    __syncthreads();
+  }
+  const double total = lds[0];
+  __syncthreads();
+  return 1.0 / (sqrt(total) + static_cast<double>(eps));
+}
+
+struct Matrix {  // parts of [rows][cols], and of its transpose
+  uint16_t *p, *t;
+  int rows, cols, ld, ldt;
+};
+
+// 8 values of row i, from column j on: their parts, and a place in the tile that is
+// written transposed.
+template <int P>
+__device__ __forceinline__ void put_row(const Matrix& x, int i, int j, const float (&v)[8]) {
+  uint32_t w[P][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t lo[P], hi[P];
+    split<P>(v[2 * k], lo);
+    split<P>(v[2 * k + 1], hi);
+#pragma unroll
+    for (int p = 0; p < P; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    *reinterpret_cast<uint4*>(x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j) =
+        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// The transposed parts of a tile in LDS (zeros past the matrix).
+template <int P>
+__device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
+                                               const float (&tile)[64][65]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int run = threadIdx.x + 256 * u;
+    const int j = run / 8, i = run % 8 * 8;
+    if (j0 + j >= x.cols) continue;
+    const Matrix t{x.t, nullptr, x.cols, 0, x.ldt, 0};
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = tile[i + k][j];
+    put_row<P>(t, j0 + j, i0 + i, v);
+  }
+}
+
+// X = M / (|M|_F + eps): one 64 x 64 tile a workgroup.  `tall`: M is [cols][rows].
+template <typename E, int P>
+__global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m, bool tall,
+                                                         const double* __restrict__ parts,
+                                                         int count, float eps, Matrix x) {
+  __shared__ double sum[256];
+  __shared__ float tile[64][65];
+  const double inv = inverse_norm(parts, count, eps, sum);
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+  for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+    const int slow = e / 64, fast = e % 64;
+    const int i = tall ? fast : slow, j = tall ? slow : fast;
+    float v = 0.f;
+    if (i0 + i < x.rows && j0 + j < x.cols) {
+      const int64_t at = tall ? static_cast<int64_t>(j0 + j) * x.rows + i0 + i
+                              : static_cast<int64_t>(i0 + i) * x.cols + j0 + j;
+      v = static_cast<float>(static_cast<double>(ElemTraits<E>::to_f32(m[at])) * inv);
+    }
+    tile[i][j] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int run = threadIdx.x + 256 * u;
+    const int i = run / 8, j = run % 8 * 8;
+    if (i0 + i >= x.rows) continue;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = tile[i][j + k];
+    put_row<P>(x, i0 + i, j0 + j, v);
+  }
+  put_transposed<P>(x, i0, j0, tile);
+}
+
+// v = keep * (old's value) + take * (the sum of the slices), to out's parts (and
+// their transpose where out.t), or to `last` [rows][cols] as E, transposed where
+// `tall`.  sums [slices][rows][pitch].  old and out may be one matrix: a workgroup
+// reads its tile of old before it writes.
+template <typename E, int P>
+__global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restrict__ sums,
+                                                          int slices, int pitch, float keep,
+                                                          float take, Matrix old, Matrix out,
+                                                          E* __restrict__ last, bool tall,
+                                                          float scale) {
+  __shared__ float tile[64][65];
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+  const int64_t plane = static_cast<int64_t>(out.rows) * pitch;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int run = threadIdx.x + 256 * u;
+    const int i = run / 8, j = run % 8 * 8;
+    float v[8] = {};
+    if (i0 + i < out.rows) {
+      const float* s = sums + static_cast<int64_t>(i0 + i) * pitch + j0 + j;
+      for (int q = 0; q < slices; ++q) {
+        const float4 a = *reinterpret_cast<const float4*>(s + q * plane);
+        const float4 b = *reinterpret_cast<const float4*>(s + q * plane + 4);
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+      float o[8] = {};
+      if (old.p != nullptr) {
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p) {
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              old.p + (static_cast<int64_t>(p) * old.rows + i0 + i) * old.ld + j0 + j);
+          const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] += __uint_as_float(d[k] << 16);
+            o[2 * k + 1] += __uint_as_float(d[k] & 0xffff0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = j0 + j + k < out.cols ? fmaf(keep, o[k], take * v[k]) : 0.f;
+      }
+      if (last == nullptr) put_row<P>(out, i0 + i, j0 + j, v);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
+  }
+  if (last == nullptr && out.t == nullptr) return;
+  __syncthreads();
+  if (last == nullptr) {
+    put_transposed<P>(out, i0, j0, tile);
+    return;
+  }
+  for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+    const int slow = e / 64, fast = e % 64;
+    const int i = tall ? fast : slow, j = tall ? slow : fast;
+    if (i0 + i >= out.rows || j0 + j >= out.cols) continue;
+    last[tall ? static_cast<int64_t>(j0 + j) * out.rows + i0 + i
+              : static_cast<int64_t>(i0 + i) * out.cols + j0 + j] =
+        ElemTraits<E>::from_f32(scale * tile[i][j]);
+  }
+}
+
+template <typename E>
+constexpr int parts_for() {
+  return sizeof(E) == 2 ? 2 : 3;
+}
+
+struct Plan {
+  int m, n, ldm, ldn;
+  int gram_slices, square_slices, update_slices;
+  double* norm;
+  uint16_t *x, *xt, *g, *b;
+  float* sums;
+  size_t bytes;
+};
+Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
+  Plan p{};
+  const size_t P = elem_bytes == 2 ? 2 : 3;
+  p.m = std::min(a.rows, a.cols);
+  p.n = std::max(a.rows, a.cols);
+  p.ldm = static_cast<int>(up64(p.m));
+  p.ldn = static_cast<int>(up64(p.n));
+  p.gram_slices = slices_for(p.m, p.m, p.ldn / 64);
+  p.square_slices = slices_for(p.m, p.m, p.ldm / 64);
+  p.update_slices = slices_for(p.n, p.m, p.ldm / 64);
+  const size_t square = static_cast<size_t>(p.m) * p.ldm, whole = static_cast<size_t>(p.m) * p.ldn;
+  Carve c{static_cast<char*>(ws)};
+  p.norm = c.take<double>(kNormBlocks);
+  p.x = c.take<uint16_t>(P * whole);
+  p.xt = c.take<uint16_t>(P * p.n * p.ldm);
+  p.g = c.take<uint16_t>(P * square);
+  p.b = c.take<uint16_t>(P * square);
+  p.sums = c.take<float>(std::max(std::max(p.gram_slices, p.square_slices) * square,
+                                  p.update_slices * whole));
+  p.bytes = c.used;
+  return p;
+}
+
+template <int P>
+hipError_t product(const Operand& A, const Operand& B, int ksteps, int slices, int pitch,
+                   float* sums, hipStream_t s) {
+  return with_tile(tile_for(A.rows, B.rows), [&](auto cf) {
+    typedef decltype(cf) CF;
+    const int mb = static_cast<int>(blocks(A.rows, CF::BM));
+    const int nb = static_cast<int>(blocks(B.rows, CF::BN));
+    product_kernel<CF, P, float, true><<<dim3(static_cast<uint32_t>(mb) * nb, slices), CF::NT, 0,
+                                         s>>>(A, B, ksteps, mb, nb, false, pitch, sums);
+    return hipGetLastError();
+  });
+}
+
+template <typename E>
+hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
+  constexpr int P = parts_for<E>();
+  const Plan p = plan_of(a, sizeof(E), ws);
+  const bool tall = a.rows > a.cols;
+  const int64_t elems = static_cast<int64_t>(a.rows) * a.cols;
+  const int count = static_cast<int>(std::min<int64_t>(blocks(elems, 2048), kNormBlocks));
+  const E* in = static_cast<const E*>(a.in);
+  orth_norm_kernel<E><<<count, 256, 0, s>>>(in, elems, p.norm);
+  const Matrix x{p.x, p.xt, p.m, p.n, p.ldn, p.ldm};
+  const Matrix g{p.g, nullptr, p.m, p.m, p.ldm, 0}, b{p.b, nullptr, p.m, p.m, p.ldm, 0};
+  const Matrix none{};
+  const dim3 whole(p.ldn / 64, p.ldm / 64), square(p.ldm / 64, p.ldm / 64);
+  orth_start_kernel<E, P><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, x);
+  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m};
+  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n};
+  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
+  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
+  E* no_output = nullptr;
+  for (int i = 0; i < a.steps; ++i) {
+    hipError_t e = product<P>(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
+    if (e != hipSuccess) return e;
+    orth_finish_kernel<E, P><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f, 1.f, none,
+                                                    g, no_output, false, 1.f);
+    if ((e = product<P>(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
+      return e;
+    orth_finish_kernel<E, P><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm, a.b, a.c, g, b,
+                                                    no_output, false, 1.f);
+    if ((e = product<P>(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
+      return e;
+    orth_finish_kernel<E, P><<<whole, 256, 0, s>>>(
+        p.sums, p.update_slices, p.ldn, a.a, 1.f, x, x,
+        i + 1 == a.steps ? static_cast<E*>(a.out) : no_output, tall, a.scale);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t orth_bytes(const OrthArgs& a, int elem_bytes) { return plan_of(a, elem_bytes, nullptr).bytes; }
+
+hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s) {
+  return elem_bytes == 2 ? orthogonalize<uint16_t>(a, ws, s) : orthogonalize<float>(a, ws, s);
+}
+
+}  // namespace twell

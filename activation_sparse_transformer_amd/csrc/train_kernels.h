@@ -136,4 +136,15 @@ hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, floa
 hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* stats,
                                 const float* dlogp, void* ws, void* dx, void* dw, hipStream_t s);
 
+// The orthogonalised update of in [rows][cols] by `steps` Newton-Schulz steps with
+// coefficients a, b, c; out may be in.
+struct OrthArgs {
+  const void* in;
+  void* out;
+  int rows, cols, steps;
+  float a, b, c, eps, scale;
+};
+size_t orth_bytes(const OrthArgs& a, int elem_bytes);
+hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s);
+
 }  // namespace twell

@@ -5,6 +5,7 @@
 #include "kernels.h"
 #include "train_kernels.h"
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -1013,4 +1014,46 @@ TWELL_EXPORT int twell_head_logprob_backward(const twell_head_shape* shape, cons
   if (workspace_bytes < head_backward_bytes(a, eb)) return TWELL_ERR_WORKSPACE;
   return hip_status(launch_head_backward(a, eb, stats, dlogp, workspace, dx, dw,
                                          static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ orthogonalised updates
+namespace twell {
+namespace {
+
+int check_orth(const twell_orth_shape* s) {
+  if (s == nullptr || s->rows <= 0 || s->cols <= 0) return TWELL_ERR_INVALID_ARG;
+  if (s->dtype != TWELL_F32 && s->dtype != TWELL_BF16) return TWELL_ERR_INVALID_ARG;
+  if (s->steps < 1 || s->steps > TWELL_ORTH_MAX_STEPS) return TWELL_ERR_INVALID_ARG;
+  if (!std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c) ||
+      !std::isfinite(s->scale))
+    return TWELL_ERR_INVALID_ARG;
+  if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return TWELL_ERR_INVALID_ARG;
+  if (s->rows > 1 << 20 || s->cols > 1 << 20 || std::min(s->rows, s->cols) > 1 << 16 ||
+      static_cast<int64_t>(s->rows) * s->cols > int64_t{1} << 32)
+    return TWELL_ERR_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+OrthArgs orth_args(const twell_orth_shape* s, const void* in, void* out) {
+  return OrthArgs{in, out, s->rows, s->cols, s->steps, s->a, s->b, s->c, s->eps, s->scale};
+}
+
+}  // namespace
+}  // namespace twell
+
+TWELL_EXPORT size_t twell_orthogonalize_workspace_size(const twell_orth_shape* shape) {
+  if (check_orth(shape) != TWELL_OK) return 0;
+  return orth_bytes(orth_args(shape, nullptr, nullptr), elem_bytes(shape->dtype));
+}
+
+TWELL_EXPORT int twell_orthogonalize(const twell_orth_shape* shape, const void* m, void* out,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_orth(shape);
+  if (rc != TWELL_OK) return rc;
+  if (m == nullptr || out == nullptr || workspace == nullptr) return TWELL_ERR_INVALID_ARG;
+  if (!aligned16(m) || !aligned16(out) || !aligned16(workspace)) return TWELL_ERR_INVALID_ARG;
+  const OrthArgs a = orth_args(shape, m, out);
+  const int eb = elem_bytes(shape->dtype);
+  if (workspace_bytes < orth_bytes(a, eb)) return TWELL_ERR_WORKSPACE;
+  return hip_status(launch_orthogonalize(a, eb, workspace, static_cast<hipStream_t>(stream)));
 }

@@ -41,6 +41,7 @@ EXPORTS = (
     "twell_norm_forward", "twell_norm_backward_workspace_size", "twell_norm_backward",
     "twell_head_logprob_workspace_size", "twell_head_logprob_forward",
     "twell_head_logprob_backward_workspace_size", "twell_head_logprob_backward",
+    "twell_orthogonalize_workspace_size", "twell_orthogonalize",
 )
 
 
@@ -106,6 +107,14 @@ class HeadShape(ctypes.Structure):
         ("n_rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("d_model", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32), ("scale", ctypes.c_float),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class OrthShape(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+        ("c", ctypes.c_float), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
     ]
 
 
@@ -181,6 +190,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.twell_head_logprob_forward.restype = I
     lib.twell_head_logprob_backward.argtypes = [D, *[P] * 8, sz, P]
     lib.twell_head_logprob_backward.restype = I
+    O = ctypes.POINTER(OrthShape)
+    lib.twell_orthogonalize_workspace_size.argtypes = [O]
+    lib.twell_orthogonalize_workspace_size.restype = sz
+    lib.twell_orthogonalize.argtypes, lib.twell_orthogonalize.restype = [O, P, P, P, sz, P], I
     _lib = lib
     return lib
 
@@ -1218,4 +1231,46 @@ def twell_head_logprob_backward(x: torch.Tensor, w: torch.Tensor, targets: torch
         ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(targets), _ptr(stats), _ptr(dlogp),
         _ptr(out.dx), _ptr(out.dw), _ptr(workspace), workspace.numel(), _here(dev)),
         "twell_head_logprob_backward")
+    return out
+
+
+# ------------------------------------------------------------------ orthogonalised updates
+def _orth_shape(rows: int, cols: int, dtype: torch.dtype, steps: int = 5,
+                coefficients=(3.4445, -4.775, 2.0315), eps: float = 1e-7,
+                scale: float = 1.0) -> OrthShape:
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {dtype} is not supported (float32 or bfloat16)")
+    if (rows | cols | steps) >> 31:
+        _int32(rows=rows, cols=cols, steps=steps)
+    return OrthShape(rows, cols, _DTYPE_CODE[dtype], steps, *coefficients, eps, scale)
+
+
+def orthogonalize_workspace(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A workspace for twell_orthogonalize of this matrix."""
+    shape = _orth_shape(rows, cols, dtype)
+    ws = int(load().twell_orthogonalize_workspace_size(ctypes.byref(shape)))
+    if ws == 0:
+        raise TwellError(TWELL_ERR_UNSUPPORTED, "twell_orthogonalize_workspace_size")
+    return torch.empty((ws,), dtype=torch.uint8, device=device)
+
+
+def twell_orthogonalize(m: torch.Tensor, *, steps: int = 5,
+                        coefficients=(3.4445, -4.775, 2.0315), eps: float = 1e-7,
+                        scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The orthogonalised update of a weight's gradient or momentum m [rows, cols]: `steps`
+    Newton-Schulz steps X <- a X + (b G + c G G) X, G = X X^T, from X = m / (|m| + eps), times
+    `scale`.  `out` may be m."""
+    dev = m.device
+    rows, cols = m.shape
+    _need(m, "m", dev)
+    shape = _orth_shape(rows, cols, m.dtype, steps, coefficients, eps, scale)
+    if out is None:
+        out = torch.empty_like(m)
+    _need(out, "out", dev, m.dtype, (rows, cols))
+    if workspace is None:
+        workspace = orthogonalize_workspace(rows, cols, m.dtype, dev)
+    _need(workspace, "workspace", dev, torch.uint8)
+    _check(load().twell_orthogonalize(ctypes.byref(shape), _ptr(m), _ptr(out), _ptr(workspace),
+                                      workspace.numel(), _here(dev)), "twell_orthogonalize")
     return out

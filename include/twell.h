@@ -668,6 +668,40 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
                                 void* dx, void* dw, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* ---- The orthogonalised update of a weight matrix, as a momentum optimiser takes
+ * it of the layer's dw_up_t or dw_down.  Defined by this interface.  For M
+ * [rows][cols], taken transposed where rows > cols:
+ *   X = M / (|M|_F + eps);  steps times:  G = X X^T,  X <- a X + (b G + c G G) X
+ *   out = scale * X
+ * which replaces every singular value s of X by a polynomial's iterate: towards 1
+ * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
+ *  - Sums and X are float32, held between the products as bfloat16 parts: three
+ *    (exact) for a float32 M, two (2^-17) for a bfloat16 one, whose out is rounded
+ *    to 2^-8 at the end.  |M|_F is summed in double.
+ *  - M = 0 gives 0; an infinity or NaN in M gives NaN.
+ * Requirements: rows, cols > 0; dtype a twell_dtype (of m and out); 1 <= steps <=
+ * TWELL_ORTH_MAX_STEPS; a, b, c and scale finite; eps positive and finite.  Limits,
+ * else TWELL_ERR_UNSUPPORTED: rows and cols at most 2^20, the smaller at most 2^16,
+ * rows * cols at most 2^32. */
+#define TWELL_ORTH_MAX_STEPS 64
+typedef struct twell_orth_shape {
+  int32_t rows;
+  int32_t cols;
+  int32_t dtype;
+  int32_t steps;
+  float a, b, c;
+  float eps;
+  float scale;
+} twell_orth_shape;
+
+/* Bytes of device workspace twell_orthogonalize needs (0 for an invalid shape): X's
+ * parts in both orders, G's and B's, and float32 products. */
+size_t twell_orthogonalize_workspace_size(const twell_orth_shape* shape);
+
+/* out [rows][cols] = the orthogonalised m [rows][cols]; out may be m. */
+int twell_orthogonalize(const twell_orth_shape* shape, const void* m, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,6 @@
 """CPU oracle of the operators around the layer in a training step: 8-bit
 activation checkpoints, the token embedding, log probabilities, the norms around
-the layer, the output head.  NumPy in float64, from the definitions."""
+the layer, the output head, orthogonalised updates.  NumPy in float64, from the definitions."""
 from __future__ import annotations
 
 import numpy as np
@@ -173,3 +173,13 @@ def head_logprob_grad(x, w, targets, dlogp, scale: float):
     dl[ok] = np.where(live[:, None], d, 0.0) * (scale * dlogp[ok])[:, None]
     x = np.where(ok[:, None], x, 0.0)
     return dl @ w, dl.T @ x, dl
+
+
+def orthogonalize(m, steps: int, coefficients, eps: float, scale: float):
+    """scale * U f(S) V^T of m / (|m| + eps) = U S V^T, f the steps' polynomial iterated on the
+    singular values."""
+    a, b, c = coefficients
+    u, s, vt = np.linalg.svd(m / (np.sqrt((m * m).sum()) + eps), full_matrices=False)
+    for _ in range(steps):
+        s = a * s + b * s ** 3 + c * s ** 5
+    return scale * (u * s) @ vt
