@@ -10,10 +10,12 @@
 // stays a part of them.  Per piece, with p = exp(z - m) / s and g = scale * dlogp:
 //   dl[n][v] = g[n] (1[v = target] - p)     from z formed again
 //   dx += dl w,   dw = dl^T x
-// dl is held as bfloat16 parts like the operands beside it: one part when x and w
-// are bfloat16 (its rounding, 2^-9 of each element, is of the size of dx's and dw's
-// own), three when they are float32.  Every product is K-major on both sides: w and
-// x are transposed once, dl is written both ways.
+// With bfloat16 x and w, dl is held in bfloat16: its rounding, 2^-9 of each element,
+// is of the size of dx's and dw's own.  With float32 ones every operand is two
+// half-precision parts (nt_gemm.h), w scaled by its largest element, x by each row's;
+// dl / g lies in [-1, 1] and is scaled by 2^14, with g taken into dx at the end and
+// into the x of dw.  Every product is K-major on both sides: w and x are transposed
+// once, dl is written both ways.
 #include <algorithm>
 
 #include "nt_gemm.h"
@@ -34,77 +36,197 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int index_byte
 // v of the lane with the other half's rows of the same column
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
-// ---------------------------------------------------------------- operand parts
-// parts [PARTS][rows][ld] of src [rows][d]; columns past d are zeros.
-template <typename E, int PARTS>
-__global__ __launch_bounds__(256) void split_kernel(const E* __restrict__ src, int64_t rows, int d,
-                                                    int ld, uint16_t* __restrict__ out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int runs = ld / 8;
-  const int64_t row = i / runs;
-  const int c = static_cast<int>(i % runs) * 8;
-  if (row >= rows) return;
-  uint32_t w[PARTS][4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint16_t lo[PARTS] = {}, hi[PARTS] = {};
-    if (c < d) {
-      const E* s = src + row * d + c + 2 * k;
-      nt::split<PARTS>(ElemTraits<E>::to_f32(s[0]), lo);
-      nt::split<PARTS>(ElemTraits<E>::to_f32(s[1]), hi);
-    }
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
-  }
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p)
-    *reinterpret_cast<uint4*>(out + (p * rows + row) * ld + c) =
-        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+// The form of operands of elements E.
+template <typename E>
+constexpr Form form_of() {
+  return sizeof(E) == 2 ? kBf16 : kHalves;
+}
+constexpr int kDlExponent = 14;  // of dl / g in halves
+
+__device__ __forceinline__ bool has_target(const void* targets, int index_bytes, int vocab,
+                                           int64_t n) {
+  const int64_t t = target_of(targets, index_bytes, n);
+  return t >= 0 && t < vocab;
 }
 
-// parts [PARTS][d][ld] of the transpose of src [rows][d]; rows past the end, and
-// rows without a target (targets not null), are zeros: whatever x holds there
-// meets gradients of zero, and a NaN must not spread.
-template <typename E, int PARTS>
-__global__ __launch_bounds__(256) void transpose_kernel(const E* __restrict__ src, int rows, int d,
-                                                        int ld, const void* __restrict__ targets,
-                                                        int index_bytes, int vocab,
-                                                        uint16_t* __restrict__ out) {
+// ---------------------------------------------------------------- operand parts
+// 8 scaled values from column c of a row of parts; `part`: elements between parts.
+template <Form F>
+__device__ __forceinline__ void put_run(uint16_t* row, int64_t part, int c, const float (&v)[8]) {
+  constexpr int P = parts_of(F);
+  uint32_t w[P][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t lo[P], hi[P];
+    nt::split<F>(v[2 * k], lo);
+    nt::split<F>(v[2 * k + 1], hi);
+#pragma unroll
+    for (int p = 0; p < P; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    *reinterpret_cast<uint4*>(row + p * part + c) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+template <typename E>
+__device__ __forceinline__ void load_run(const E* p, float (&v)[8]) {
+  if constexpr (sizeof(E) == 2) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+// The largest finite magnitude of v and m
+__device__ __forceinline__ float max_finite(float m, float v) {
+  v = fabsf(v);
+  return v < INFINITY ? fmaxf(m, v) : m;
+}
+__device__ __forceinline__ float wave_max(float m) {
+#pragma unroll
+  for (int h = 32; h > 0; h /= 2) m = fmaxf(m, __shfl_xor(m, h));
+  return m;
+}
+
+__global__ void head_clear_kernel(float* amax) { amax[threadIdx.x] = 0.f; }
+
+// *amax = max(*amax, the largest finite magnitude of src): an order-free atomic on the
+// bits of non-negative floats.
+__global__ __launch_bounds__(256) void head_amax_kernel(const float* __restrict__ src,
+                                                        int64_t runs, float* amax) {
+  float m = 0.f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < runs;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    float v[8];
+    load_run(src + i * 8, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
+  }
+  m = wave_max(m);
+  if (lane_id() == 0) atomicMax(reinterpret_cast<int*>(amax), __float_as_int(m));
+}
+
+// parts [rows][ld] of a piece of w, src [rows][d], scaled by *amax (halves); columns
+// past d are zeros.
+template <typename E>
+__global__ __launch_bounds__(256) void head_w_kernel(const E* __restrict__ src, int64_t rows,
+                                                     int d, int ld, const float* amax,
+                                                     uint16_t* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = i / (ld / 8);
+  const int c = static_cast<int>(i % (ld / 8)) * 8;
+  if (row >= rows) return;
+  float v[8] = {};
+  if (c < d) load_run(src + row * d + c, v);
+  if constexpr (form_of<E>() == kHalves) {
+    const float f = power_of_two(exponent_for(*amax));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+  }
+  put_run<form_of<E>()>(out + row * ld, rows * ld, c, v);
+}
+
+// parts [rows][ld] of x, a wave a row.  Halves: scaled by the row's largest element,
+// what undoes it in undo[row]; and, for the gradient (dlogp not null), *amax = the
+// largest of |scale dlogp x| over rows with a target.
+template <typename E>
+__global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
+                                                     const float* __restrict__ dlogp,
+                                                     float* __restrict__ undo, float* amax,
+                                                     uint16_t* __restrict__ out) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  if (row >= a.n_rows) return;
+  const E* src = static_cast<const E*>(a.x) + row * a.d;
+  float f = 1.f;
+  if constexpr (form_of<E>() == kHalves) {
+    float m = 0.f;
+    for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
+      float v[8];
+      load_run(src + c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
+    }
+    m = wave_max(m);
+    const int e = exponent_for(m);
+    f = power_of_two(e);
+    if (lane_id() == 0) {
+      undo[row] = power_of_two(-e);
+      if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
+        atomicMax(reinterpret_cast<int*>(amax),
+                  __float_as_int(max_finite(0.f, dlogp[row] * a.scale * m)));
+    }
+  }
+  for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
+    float v[8] = {};
+    if (c < a.d) load_run(src + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+    put_run<form_of<E>()>(out + row * ld, a.n_rows * ld, c, v);
+  }
+}
+
+// parts [d][ld] of the transpose of src [rows][d]; rows past the end are zeros.
+// Halves: scaled by *amax.  X: src is x, and rows without a target are zeros (whatever
+// x holds there meets gradients of zero, and a NaN must not spread); in halves the rows
+// are scale * dlogp * x.
+template <typename E, bool X>
+__global__ __launch_bounds__(256) void head_transpose_kernel(HeadArgs a, const E* __restrict__ src,
+                                                             int rows, int ld,
+                                                             const float* __restrict__ dlogp,
+                                                             const float* amax,
+                                                             uint16_t* __restrict__ out) {
   __shared__ float tile[64][65];
   const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
+  float f = 1.f;
+  if constexpr (form_of<E>() == kHalves) f = power_of_two(exponent_for(*amax));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int run = threadIdx.x + 256 * i;
     const int r = run / 8, c = run % 8 * 8;
-    bool live = r0 + r < rows && c0 + c < d;
-    if (live && targets != nullptr) {
-      const int64_t t = target_of(targets, index_bytes, r0 + r);
-      live = t >= 0 && t < vocab;
-    }
-    const E* s = src + static_cast<int64_t>(r0 + r) * d + c0 + c;
+    bool live = r0 + r < rows && c0 + c < a.d;
+    if (X && live) live = has_target(a.targets, a.index_bytes, a.vocab, r0 + r);
+    float v[8] = {};
+    if (live) {
+      load_run(src + static_cast<int64_t>(r0 + r) * a.d + c0 + c, v);
+      if constexpr (form_of<E>() == kHalves) {
+        const float g = X ? dlogp[r0 + r] * a.scale : 1.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) tile[r][c + k] = live ? ElemTraits<E>::to_f32(s[k]) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tile[r][c + k] = v[k];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int run = threadIdx.x + 256 * i;
     const int c = run / 8, r = run % 8 * 8;
-    if (c0 + c >= d) continue;  // r0 + 64 <= ld
-    uint32_t w[PARTS][4];
+    if (c0 + c >= a.d) continue;  // r0 + 64 <= ld
+    float v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint16_t lo[PARTS], hi[PARTS];
-      nt::split<PARTS>(tile[r + 2 * k][c], lo);
-      nt::split<PARTS>(tile[r + 2 * k + 1][c], hi);
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
-    }
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p)
-      *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(p) * d + c0 + c) * ld + r0 + r) =
-          make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    for (int k = 0; k < 8; ++k) v[k] = tile[r + k][c];
+    put_run<form_of<E>()>(out + static_cast<int64_t>(c0 + c) * ld,
+                          static_cast<int64_t>(a.d) * ld, r0 + r, v);
   }
+}
+
+// What a column of accumulators is multiplied by to be z: scale, and the powers of two
+// of both operands undone.
+template <Form F, class Args>
+__device__ __forceinline__ float z_factor(const Args& a, int64_t n) {
+  if constexpr (F == kHalves)
+    return a.scale * (n < a.x.rows ? a.undo[n] : 0.f) * power_of_two(-exponent_for(*a.amax));
+  return a.scale;
 }
 
 // ---------------------------------------------------------------- forward
@@ -113,20 +235,21 @@ struct StatsArgs {
   int v0, vocab;     // whole vocabulary
   int ksteps;
   float scale;
+  const float *amax, *undo;  // halves: of w, and per row of x
   const void* targets;
   int index_bytes;
   float2* parts;     // [tiles][n], this piece's first tile onwards
   float* target_z;   // [n], z of the target, written by the tile that holds it
 };
 
-template <class CF, int PARTS>
+template <class CF, Form F>
 __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_blocks,
                                                             int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
   nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
-  nt::mainloop<CF, PARTS>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  nt::mainloop<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
   const int half = lane_id() >> 5;
   const int wave_row = row0 - 4 * half;  // the wave's first row
@@ -136,12 +259,13 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
   for (int j = 0; j < CF::FN; ++j) {
     const int col = nt::block_col<CF>() + 32 * j;
     const int n = nb * CF::BN + col;
+    const float f = z_factor<F>(a, n);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        acc[i][j][r] *= a.scale;
+        acc[i][j][r] *= f;
         if (row0 + nt::row_of(i, r) < a.w.rows) m = fmaxf(m, acc[i][j][r]);
       }
     m = fmaxf(m, other_half(m));
@@ -240,28 +364,30 @@ struct DlArgs {
   int v0, vocab;
   int ksteps;
   float scale;
+  const float *amax, *undo;  // halves: of w, and per row of x
   const void* targets;
   int index_bytes;
   const float2* stats;
   const float* dlogp;
-  uint16_t* dl;    // [PARTS][n][ldv]
-  uint16_t* dlt;   // [PARTS][piece][ldn]
+  uint16_t* dl;    // [parts][n][ldv]
+  uint16_t* dlt;   // [parts][piece][ldn]
   int ldv, ldn;
 };
 
-template <class CF, int PARTS>
+template <class CF, Form F>
 __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks, int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
   nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
-  nt::mainloop<CF, PARTS>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  nt::mainloop<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
   const int64_t n_rows = a.x.rows;
 #pragma unroll
   for (int j = 0; j < CF::FN; ++j) {
     const int n = nb * CF::BN + nt::block_col<CF>() + 32 * j;
     float g = 0.f, m = 0.f, inv = 0.f;
+    const float f = z_factor<F>(a, n);
     int t = -1;  // of the piece
     bool given = false;
     if (n < n_rows) {
@@ -270,7 +396,7 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
       given = target >= 0 && target < a.vocab && !(st.x == -INFINITY && st.y == 0.f);
       if (given) {
         t = static_cast<int>(target) - a.v0;
-        g = a.dlogp[n] * a.scale;
+        g = F == kBf16 ? a.dlogp[n] * a.scale : power_of_two(kDlExponent);
         m = st.x;
         inv = 1.f / st.y;
       }
@@ -280,16 +406,16 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int v = row0 + nt::row_of(i, 4 * q);
-        uint16_t part[4][PARTS];
+        uint16_t part[4][parts_of(F)];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float z = acc[i][j][4 * q + k] * a.scale;
+          const float z = acc[i][j][4 * q + k] * f;
           const float p = __builtin_amdgcn_exp2f((z - m) * kLog2e) * inv;
           const float d = given && v + k < a.w.rows ? g * ((v + k == t ? 1.f : 0.f) - p) : 0.f;
-          nt::split<PARTS>(d, part[k]);
+          nt::split<F>(d, part[k]);
         }
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
+        for (int p = 0; p < parts_of(F); ++p) {
           if (n < n_rows && v < a.ldv)
             *reinterpret_cast<uint2*>(a.dl + (p * n_rows + n) * a.ldv + v) =
                 make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
@@ -305,19 +431,36 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   }
 }
 
-// dx = the sum of the slices, rounded; 8 elements a lane.
+// dx = the sum of the slices, rounded; 8 elements a lane.  Halves: times scale * dlogp
+// of the row and the powers of two undone.
 template <typename E>
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ sums,
-                                                      int slices, int64_t elems,
-                                                      E* __restrict__ dx) {
+__global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* __restrict__ sums,
+                                                      int slices, const float* __restrict__ dlogp,
+                                                      const float* amax, E* __restrict__ dx) {
+  const int64_t elems = a.n_rows * a.d;
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= elems) return;
   float v[8] = {};
-  for (int s = 0; s < slices; ++s)
+  for (int s = 0; s < slices; ++s) {
+    float p[8];
+    load_run(sums + s * elems + i, p);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += sums[s * elems + i + k];
+    for (int k = 0; k < 8; ++k) v[k] += p[k];
+  }
+  if constexpr (form_of<E>() == kHalves) {
+    const int64_t n = i / a.d;
+    const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
+    const float g = given ? dlogp[n] * a.scale : 0.f;
+    const float f = power_of_two(-kDlExponent - exponent_for(*amax));
 #pragma unroll
-  for (int k = 0; k < 8; ++k) dx[i + k] = ElemTraits<E>::from_f32(v[k]);
+    for (int k = 0; k < 8; ++k) v[k] = given ? v[k] * f * g : 0.f;
+  }
+  if constexpr (sizeof(E) == 2) {
+    put_run<kBf16>(reinterpret_cast<uint16_t*>(dx) + i, 0, 0, v);
+  } else {
+    *reinterpret_cast<float4*>(dx + i) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(dx + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 __global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count) {
@@ -327,7 +470,7 @@ __global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count)
 }
 
 // ---------------------------------------------------------------- sizes
-int parts_of(int elem_bytes) { return elem_bytes == 2 ? 1 : 3; }
+int part_count(int elem_bytes) { return elem_bytes == 2 ? 1 : 2; }
 
 // Whether x and w serve as operands where they are.
 bool direct(int elem_bytes, int d) { return elem_bytes == 2 && d % 64 == 0; }
@@ -341,16 +484,19 @@ int piece_of(int vocab, size_t per_column, size_t budget) {
   return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
 }
 
+constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
+
 struct ForwardPlan {
   int piece, tiles;
   uint16_t *xp, *wp;
+  float *amax, *undo;
   float2* parts;
   float* target_z;
   size_t bytes;
 };
 ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   ForwardPlan p{};
-  const size_t ld = up64(a.d), part_bytes = 2 * parts_of(elem_bytes) * ld;
+  const size_t ld = up64(a.d), part_bytes = 2 * part_count(elem_bytes) * ld;
   const bool in_place = direct(elem_bytes, a.d);
   p.piece = in_place ? a.vocab : piece_of(a.vocab, part_bytes, size_t{128} << 20);
   // tiles of a piece start at its first column: pieces but the last are whole tiles
@@ -360,6 +506,8 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
   p.target_z = c.take<float>(a.n_rows);
   if (!in_place) {
+    p.amax = c.take<float>(kAmax);
+    p.undo = c.take<float>(a.n_rows);
     p.xp = c.take<uint16_t>(part_bytes / 2 * a.n_rows);
     p.wp = c.take<uint16_t>(part_bytes / 2 * p.piece);
   }
@@ -371,12 +519,12 @@ struct BackwardPlan {
   int piece, slices;
   int ldn;
   uint16_t *xp, *wp, *xt, *wt, *dl, *dlt;
-  float* sums;
+  float *amax, *undo, *sums;
   size_t bytes;
 };
 BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   BackwardPlan p{};
-  const size_t P = parts_of(elem_bytes), ld = up64(a.d), n = a.n_rows;
+  const size_t P = part_count(elem_bytes), ld = up64(a.d), n = a.n_rows;
   const bool in_place = direct(elem_bytes, a.d);
   p.ldn = static_cast<int>(up64(n));
   const size_t per_column = 2 * P * (n + p.ldn + a.d + (in_place ? 0 : ld));
@@ -391,6 +539,8 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.dlt = c.take<uint16_t>(P * p.piece * p.ldn);
   p.sums = c.take<float>(p.slices * n * a.d);
   if (!in_place) {
+    p.amax = c.take<float>(kAmax);
+    p.undo = c.take<float>(n);
     p.xp = c.take<uint16_t>(P * ld * n);
     p.wp = c.take<uint16_t>(P * ld * p.piece);
   }
@@ -399,50 +549,64 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
 }
 
 // ---------------------------------------------------------------- launches
-template <typename E, int P>
-void split(const void* src, int64_t row0, int64_t rows, int d, uint16_t* out, hipStream_t s) {
-  const int ld = static_cast<int>(up64(d));
-  split_kernel<E, P><<<static_cast<uint32_t>(blocks(rows * (ld / 8), 256)), 256, 0, s>>>(
-      static_cast<const E*>(src) + row0 * d, rows, d, ld, out);
+int columns(const HeadArgs& a) { return static_cast<int>(up64(a.d)); }
+
+// The operand x, in place or as parts in xp; halves: amax of w (and of the gradient's x)
+// on the way.
+template <typename E>
+Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* undo, uint16_t* xp,
+                  hipStream_t s) {
+  const int n = static_cast<int>(a.n_rows), ld = columns(a);
+  if (direct(sizeof(E), a.d)) return Operand{static_cast<const uint16_t*>(a.x), 0, a.d, n};
+  if constexpr (form_of<E>() == kHalves) {
+    head_clear_kernel<<<1, kAmax, 0, s>>>(amax);
+    const int64_t runs = static_cast<int64_t>(a.vocab) * a.d / 8;
+    head_amax_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(runs, 1024), 2048)), 256, 0,
+                       s>>>(static_cast<const float*>(a.w), runs, amax);
+  }
+  head_x_kernel<E><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo,
+                                                                      amax + 1, xp);
+  return Operand{xp, a.n_rows * ld, ld, n};
 }
 
-template <typename E, int P>
-void transpose(const void* src, int64_t row0, int rows, int d, const HeadArgs* masked,
+// The operand of columns [v0, v0 + rows) of the vocabulary.
+template <typename E>
+Operand w_operand(const HeadArgs& a, int64_t v0, int rows, const float* amax, uint16_t* wp,
+                  hipStream_t s) {
+  const E* src = static_cast<const E*>(a.w) + v0 * a.d;
+  const int ld = columns(a);
+  if (direct(sizeof(E), a.d)) return Operand{reinterpret_cast<const uint16_t*>(src), 0, a.d, rows};
+  head_w_kernel<E><<<static_cast<uint32_t>(blocks(static_cast<int64_t>(rows) * (ld / 8), 256)), 256,
+                     0, s>>>(src, rows, a.d, ld, amax, wp);
+  return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows};
+}
+
+template <typename E, bool X>
+void transpose(const HeadArgs& a, const E* src, int rows, const float* dlogp, const float* amax,
                uint16_t* out, hipStream_t s) {
   const int ld = static_cast<int>(up64(rows));
-  transpose_kernel<E, P><<<dim3(ld / 64, static_cast<uint32_t>(blocks(d, 64))), 256, 0, s>>>(
-      static_cast<const E*>(src) + row0 * d, rows, d, ld,
-      masked != nullptr ? masked->targets : nullptr, masked != nullptr ? masked->index_bytes : 0,
-      masked != nullptr ? masked->vocab : 0, out);
+  head_transpose_kernel<E, X><<<dim3(ld / 64, static_cast<uint32_t>(blocks(a.d, 64))), 256, 0, s>>>(
+      a, src, rows, ld, dlogp, amax, out);
 }
 
-// The operand of `rows` rows from row0 of src: in place, or its parts in `to`.
-template <typename E, int P>
-Operand operand(const void* src, int64_t row0, int rows, int d, uint16_t* to, hipStream_t s) {
-  const int ld = static_cast<int>(up64(d));
-  if (direct(sizeof(E), d))
-    return Operand{static_cast<const uint16_t*>(src) + row0 * d, 0, d, rows};
-  split<E, P>(src, row0, rows, d, to, s);
-  return Operand{to, static_cast<int64_t>(rows) * ld, ld, rows};
-}
-
-template <typename E, int P>
+template <typename E>
 hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* stats,
                    hipStream_t s) {
+  constexpr Form F = form_of<E>();
   const ForwardPlan p = forward_plan(a, sizeof(E), ws);
   const int n = static_cast<int>(a.n_rows);
-  const Operand x = operand<E, P>(a.x, 0, n, a.d, p.xp, s);
+  const Operand x = x_operand<E>(a, nullptr, p.amax, p.undo, p.xp, s);
   const Tile tile = tile_for(p.piece, n);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
-    const Operand w = operand<E, P>(a.w, v0, rows, a.d, p.wp, s);
-    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, static_cast<int>(up64(a.d) / 64),
-                      a.scale, a.targets, a.index_bytes,
+    const Operand w = w_operand<E>(a, v0, rows, p.amax, p.wp, s);
+    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, p.amax,
+                      p.undo, a.targets, a.index_bytes,
                       p.parts + v0 / tile_rows(tile) * a.n_rows, p.target_z};
     const hipError_t e = with_tile(tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      head_stats_kernel<CF, P><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      head_stats_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -453,9 +617,10 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
   return hipGetLastError();
 }
 
-template <typename E, int P>
+template <typename E>
 hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, void* ws, void* dx,
                     void* dw, hipStream_t s) {
+  constexpr Form F = form_of<E>();
   if (a.n_rows == 0) {
     const int64_t count = static_cast<int64_t>(a.vocab) * a.d * sizeof(E) / 16;
     head_zero_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(count, 256), 1 << 20)), 256,
@@ -464,15 +629,17 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
   }
   const BackwardPlan p = backward_plan(a, sizeof(E), ws);
   const int n = static_cast<int>(a.n_rows);
-  const Operand x = operand<E, P>(a.x, 0, n, a.d, p.xp, s);
-  transpose<E, P>(a.x, 0, n, a.d, &a, p.xt, s);
+  const float* const amax_w = F == kHalves ? p.amax : nullptr;
+  const float* const amax_x = F == kHalves ? p.amax + 1 : nullptr;
+  const Operand x = x_operand<E>(a, dlogp, p.amax, p.undo, p.xp, s);
+  transpose<E, true>(a, static_cast<const E*>(a.x), n, dlogp, amax_x, p.xt, s);
   const Operand xt{p.xt, static_cast<int64_t>(a.d) * p.ldn, p.ldn, a.d};
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const int ldv = static_cast<int>(up64(rows));
-    const Operand w = operand<E, P>(a.w, v0, rows, a.d, p.wp, s);
-    transpose<E, P>(a.w, v0, rows, a.d, nullptr, p.wt, s);
-    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, static_cast<int>(up64(a.d) / 64), a.scale,
+    const Operand w = w_operand<E>(a, v0, rows, amax_w, p.wp, s);
+    transpose<E, false>(a, static_cast<const E*>(a.w) + v0 * a.d, rows, nullptr, amax_w, p.wt, s);
+    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, amax_w, p.undo,
                    a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
                    p.dlt, ldv, p.ldn};
     hipError_t e = with_tile(tile_for(rows, n), [&](auto cf) {
@@ -480,7 +647,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
       // ldn columns of dlt are written, of them the last as zeros
       const int mb = static_cast<int>(blocks(rows, CF::BM));
       const int nb = static_cast<int>(blocks(p.ldn, CF::BN));
-      head_dl_kernel<CF, P><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      head_dl_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -490,9 +657,9 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     e = with_tile(tile_for(a.d, n), [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      nt::product_kernel<CF, P, float, true>
+      product_kernel<CF, F, float, true>
           <<<dim3(static_cast<uint32_t>(mb) * nb, p.slices), CF::NT, 0, s>>>(
-              wt, dl, ldv / 64, mb, nb, v0 > 0, a.d, p.sums);
+              wt, dl, ldv / 64, mb, nb, v0 > 0, a.d, nullptr, 0, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -500,15 +667,15 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      nt::product_kernel<CF, P, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
-          xt, dlt, p.ldn / 64, mb, nb, false, a.d, static_cast<E*>(dw) + v0 * a.d);
+      product_kernel<CF, F, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+          xt, dlt, p.ldn / 64, mb, nb, false, a.d, amax_x, -kDlExponent,
+          static_cast<E*>(dw) + v0 * a.d);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
   }
-  const int64_t elems = a.n_rows * a.d;
-  head_dx_kernel<E><<<static_cast<uint32_t>(blocks(elems / 8, 256)), 256, 0, s>>>(
-      p.sums, p.slices, elems, static_cast<E*>(dx));
+  head_dx_kernel<E><<<static_cast<uint32_t>(blocks(a.n_rows * a.d / 8, 256)), 256, 0, s>>>(
+      a, p.sums, p.slices, dlogp, amax_w, static_cast<E*>(dx));
   return hipGetLastError();
 }
 
@@ -524,14 +691,14 @@ size_t head_backward_bytes(const HeadArgs& a, int elem_bytes) {
 hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
                                float* lse, float* stats, hipStream_t s) {
   if (a.n_rows == 0) return hipSuccess;
-  return elem_bytes == 2 ? forward<uint16_t, 1>(a, ws, logp, lse, stats, s)
-                         : forward<float, 3>(a, ws, logp, lse, stats, s);
+  return elem_bytes == 2 ? forward<uint16_t>(a, ws, logp, lse, stats, s)
+                         : forward<float>(a, ws, logp, lse, stats, s);
 }
 
 hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* stats,
                                 const float* dlogp, void* ws, void* dx, void* dw, hipStream_t s) {
-  return elem_bytes == 2 ? backward<uint16_t, 1>(a, stats, dlogp, ws, dx, dw, s)
-                         : backward<float, 3>(a, stats, dlogp, ws, dx, dw, s);
+  return elem_bytes == 2 ? backward<uint16_t>(a, stats, dlogp, ws, dx, dw, s)
+                         : backward<float>(a, stats, dlogp, ws, dx, dw, s);
 }
 
 }  // namespace twell

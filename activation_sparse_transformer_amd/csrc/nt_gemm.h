@@ -1,12 +1,18 @@
-// Products C = A B^T of K-major bfloat16 operands on MFMA (32x32x16), and of
-// float32 operands held as bfloat16 parts.
-//
-// A float32 v is the sum of three bfloat16 parts, each the rounding of what the
-// ones before leave: 8 + 8 + 8 bits, so the sum is v.  Of the nine products of
-// two such values the six largest are formed; those left out are below 2^-25 of
-// the whole, the rounding of the float32 sum.  At 1/6 of the bfloat16 rate this
-// is still faster than MFMA's own float32 form (1/16).  Two parts and three
-// products leave 2^-17, for values that are rounded to bfloat16 in the end.
+// Products C = A B^T of K-major operands on MFMA (32x32x16).  An operand is held in
+// one of three forms:
+//  - kBf16:    one bfloat16 part, as bfloat16 tensors are;
+//  - kHalves:  two half-precision parts hi + lo of a float32 value times a power of
+//              two that brings the matrix (or row) below 2^15.  Both round to 11 bits,
+//              so |lo| <= 2^-11 |v| and hi + lo is within 2^-23 of v (2^-24 in the
+//              mean), or within 2^-25 (2^-40 of the largest) where lo is subnormal;
+//              MFMA keeps subnormal inputs.  Of the four products lo lo, 2^-24 of the
+//              whole in the mean and at most 2^-22, is left out: three products, where
+//              three bfloat16 parts would take six for the same 24 bits and MFMA's own
+//              float32 form sixteen times one.  MFMA cuts a sum's last bits at every
+//              step, so the two small products go over the whole of K first and the
+//              large one last: no more cuts at the sum's full size than a product of
+//              one part has.
+//  - kHalf:    the hi part alone.
 //
 // Operands are [parts][rows][ld], ld a multiple of 64 with zeros past the
 // contraction's length; rows past the end read the last row and feed outputs
@@ -21,6 +27,10 @@ namespace twell {
 namespace nt {
 
 constexpr int kStep = 64;  // K elements of one LDS stage
+
+enum Form { kBf16, kHalf, kHalves };
+constexpr int parts_of(Form f) { return f == kHalves ? 2 : 1; }
+constexpr int products_of(Form f) { return f == kHalves ? 3 : 1; }
 
 struct Operand {
   const uint16_t* p;
@@ -74,27 +84,34 @@ __device__ __forceinline__ void issue(const uint16_t* const* src, int64_t offset
     __builtin_amdgcn_global_load_lds(src[i] + offset, tile + (wave + NW * i) * 512, 16, 0, 0);
 }
 
-// The steps of a contraction: the products of parts one after another at each
-// 64 elements of K (the stages of one K come from the caches).
-constexpr int products(int parts) { return parts == 1 ? 1 : parts == 2 ? 3 : 6; }
-template <int PARTS>
+// The steps of a contraction: a product of parts after another, each over the whole
+// of K, in the order hi lo, lo hi, hi hi.
+template <Form F>
 struct Walk {
   int64_t part_a, part_b;
+  int end;  // of K
   int k = 0, q = 0;
   __device__ __forceinline__ void next() {
-    if (++q == products(PARTS)) {
-      q = 0;
-      k += kStep;
+    k += kStep;
+    if (F == kHalves && k == end) {
+      k = 0;
+      ++q;
     }
   }
-  // parts (a, b): (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
-  __device__ __forceinline__ int64_t a() const {
-    return PARTS == 1 ? k : ((0x850 >> (2 * q)) & 3) * part_a + k;
-  }
-  __device__ __forceinline__ int64_t b() const {
-    return PARTS == 1 ? k : ((0x244 >> (2 * q)) & 3) * part_b + k;
-  }
+  __device__ __forceinline__ int64_t a() const { return F == kHalves && q == 1 ? part_a + k : k; }
+  __device__ __forceinline__ int64_t b() const { return F == kHalves && q == 0 ? part_b + k : k; }
 };
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+template <Form F>
+__device__ __forceinline__ f32x16_t mfma(i32x4_t a, i32x4_t b, f32x16_t c) {
+  if constexpr (F == kBf16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
 
 // All but the last N copies of every wave landed, and every wave is done with its
 // LDS reads so far.
@@ -105,7 +122,7 @@ __device__ __forceinline__ void meet() {
 
 // acc = A[m0 .., k0 .. k0 + 64 ksteps) B[n0 .., the same]^T.  `lds`: STAGES stages.
 // Copies run STAGES - 1 stages ahead of the products.
-template <class CF, int PARTS>
+template <class CF, Form F>
 __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand& B, int n0, int k0,
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
@@ -122,8 +139,8 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
   constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
-  const int steps = ksteps * products(PARTS);
-  Walk<PARTS> walk{A.part, B.part};
+  const int steps = ksteps * products_of(F);
+  Walk<F> walk{A.part, B.part, ksteps * kStep};
   int fill = 0;  // the stage that the next copies go to
   auto copy = [&]() {
     uint16_t* stage = lds + fill * CF::STAGE;
@@ -144,20 +161,20 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
 #pragma unroll
     for (int ks = 0; ks < kStep / 16; ++ks) {
       const int kc = ks * 2 + (lane >> 5);
-      bf16x8_t a[CF::FM], b[CF::FN];
+      i32x4_t a[CF::FM], b[CF::FN];
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i)
-        a[i] = *reinterpret_cast<const bf16x8_t*>(
+        a[i] = *reinterpret_cast<const i32x4_t*>(
             sA + tile_offset(wm * CF::WTM + i * 32 + (lane & 31), kc));
 #pragma unroll
       for (int j = 0; j < CF::FN; ++j)
-        b[j] = *reinterpret_cast<const bf16x8_t*>(
+        b[j] = *reinterpret_cast<const i32x4_t*>(
             sB + tile_offset(wn * CF::WTN + j * 32 + (lane & 31), kc));
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
         for (int j = 0; j < CF::FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = mfma<F>(a[i], b[j], acc[i][j]);
     }
     cur = cur + 1 == CF::STAGES ? 0 : cur + 1;
   }
@@ -192,32 +209,40 @@ __device__ __forceinline__ void tile_of(int b, int m_blocks, int n_blocks, int& 
   nb = in / rows;
 }
 
-// The bfloat16 parts of v, most significant first.
-template <int PARTS>
-__device__ __forceinline__ void split(float v, uint16_t (&part)[PARTS]) {
-  typedef ElemTraits<uint16_t> Tr;
-  part[0] = Tr::from_f32(v);
-  if constexpr (PARTS > 1) {
-    const uint32_t u = __float_as_uint(v);
-    const bool finite = (u & 0x7f800000u) != 0x7f800000u;
-    // a value that would round past the largest bfloat16 is cut instead
-    if (finite && (part[0] & 0x7f80u) == 0x7f80u) part[0] = static_cast<uint16_t>(u >> 16);
-    float rest = finite ? v - Tr::to_f32(part[0]) : 0.f;
-#pragma unroll
-    for (int i = 1; i < PARTS; ++i) {
-      part[i] = Tr::from_f32(rest);
-      rest -= Tr::to_f32(part[i]);
+// The parts of v (scaled already), the larger first.
+template <Form F>
+__device__ __forceinline__ void split(float v, uint16_t (&part)[parts_of(F)]) {
+  if constexpr (F == kBf16) {
+    part[0] = ElemTraits<uint16_t>::from_f32(v);
+  } else {
+    const _Float16 hi = static_cast<_Float16>(v);
+    part[0] = __builtin_bit_cast(uint16_t, hi);
+    if constexpr (F == kHalves) {
+      // an infinity or NaN is hi's alone
+      const bool finite = (part[0] & 0x7c00u) != 0x7c00u;
+      part[1] = __builtin_bit_cast(
+          uint16_t, static_cast<_Float16>(finite ? v - static_cast<float>(hi) : 0.f));
     }
   }
 }
 
+// The exponent e by which a matrix or row of largest magnitude m is scaled: 2^14 <= m
+// 2^e < 2^15 (at most 100, so that 2^-e is a float32; m = 0 and non-finite m: 0).
+__device__ __forceinline__ int exponent_for(float m) {
+  const int b = static_cast<int>(__float_as_uint(m) >> 23) & 0xff;
+  return b == 0xff || m == 0.f ? 0 : min(14 + 127 - max(b, 1), 100);
+}
+__device__ __forceinline__ float power_of_two(int e) { return ldexpf(1.f, e); }
+
 // out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, lines of
 // `pitch` elements (a multiple of 8, not under A.rows; what lies past A.rows is
 // undefined): as floats (ACC: slice after slice in out, added to where `add`) or as E.
-template <class CF, int PARTS, typename E, bool ACC>
+// Times 2^(exponent - exponent_for(*amax)) where amax is given.
+template <class CF, Form F, typename E, bool ACC>
 __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, int ksteps,
                                                          int m_blocks, int n_blocks, bool add,
-                                                         int pitch, E* __restrict__ out) {
+                                                         int pitch, const float* amax,
+                                                         int exponent, E* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
   tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
@@ -225,9 +250,18 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
-  mainloop<CF, PARTS>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
+  mainloop<CF, F>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
   const int row0 = mb * CF::BM + block_row<CF>();
   if (ACC) out += static_cast<int64_t>(slice) * pitch * B.rows;
+  if (amax != nullptr) {
+    const float f = power_of_two(exponent - exponent_for(*amax));
+#pragma unroll
+    for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < CF::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= f;
+  }
 #pragma unroll
   for (int j = 0; j < CF::FN; ++j) {
     const int col = nb * CF::BN + block_col<CF>() + 32 * j;

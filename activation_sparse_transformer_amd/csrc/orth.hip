@@ -4,12 +4,14 @@
 // every singular value s of X becomes a s + b s^3 + c s^5, which the usual
 // coefficients drive towards 1.
 //
-// All products run on MFMA over bfloat16 parts of float32 values (nt_gemm.h): three
-// parts for a float32 M, two for a bfloat16 one, whose result is rounded to 2^-9.  A
-// product leaves float32 partial sums, slices of K where its tiles are few; a pass
-// over them adds the slices, forms G, B or the next X in float32 and writes its
-// parts, X also transposed, since both G and B X contract K-major operands.
+// All products run on MFMA over half-precision parts of float32 values (nt_gemm.h).
+// |X| <= 1 at the start, and max |a s + b s^3 + c s^5| bounds it after each step, so the
+// powers of two that the parts are scaled by are known on the host.  A product leaves
+// float32 partial sums, slices of K where its tiles are few; a pass over them adds the
+// slices, forms G, B or the next X in float32 and writes its parts, X also transposed,
+// since both G and B X contract K-major operands.
 #include <algorithm>
+#include <cmath>
 
 #include "nt_gemm.h"
 #include "train_kernels.h"
@@ -62,27 +64,24 @@ struct Matrix {  // parts of [rows][cols], and of its transpose
   int rows, cols, ld, ldt;
 };
 
-// 8 values of row i, from column j on: their parts, and a place in the tile that is
-// written transposed.
-template <int P>
+// 8 scaled values of row i, from column j on, as parts.
 __device__ __forceinline__ void put_row(const Matrix& x, int i, int j, const float (&v)[8]) {
-  uint32_t w[P][4];
+  uint32_t w[2][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint16_t lo[P], hi[P];
-    split<P>(v[2 * k], lo);
-    split<P>(v[2 * k + 1], hi);
+    uint16_t lo[2], hi[2];
+    split<kHalves>(v[2 * k], lo);
+    split<kHalves>(v[2 * k + 1], hi);
 #pragma unroll
-    for (int p = 0; p < P; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+    for (int p = 0; p < 2; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
   }
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < 2; ++p)
     *reinterpret_cast<uint4*>(x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j) =
         make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 // The transposed parts of a tile in LDS (zeros past the matrix).
-template <int P>
 __device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
                                                const float (&tile)[64][65]) {
 #pragma unroll
@@ -94,18 +93,20 @@ __device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = tile[i + k][j];
-    put_row<P>(t, j0 + j, i0 + i, v);
+    put_row(t, j0 + j, i0 + i, v);
   }
 }
 
-// X = M / (|M|_F + eps): one 64 x 64 tile a workgroup.  `tall`: M is [cols][rows].
-template <typename E, int P>
+// X = 2^exponent M / (|M|_F + eps): one 64 x 64 tile a workgroup.  `tall`: M is
+// [cols][rows].
+template <typename E>
 __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m, bool tall,
                                                          const double* __restrict__ parts,
-                                                         int count, float eps, Matrix x) {
+                                                         int count, float eps, int exponent,
+                                                         Matrix x) {
   __shared__ double sum[256];
   __shared__ float tile[64][65];
-  const double inv = inverse_norm(parts, count, eps, sum);
+  const double inv = ldexp(inverse_norm(parts, count, eps, sum), exponent);
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   for (int e = threadIdx.x; e < 64 * 64; e += 256) {
     const int slow = e / 64, fast = e % 64;
@@ -127,21 +128,20 @@ __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = tile[i][j + k];
-    put_row<P>(x, i0 + i, j0 + j, v);
+    put_row(x, i0 + i, j0 + j, v);
   }
-  put_transposed<P>(x, i0, j0, tile);
+  put_transposed(x, i0, j0, tile);
 }
 
 // v = keep * (old's value) + take * (the sum of the slices), to out's parts (and
 // their transpose where out.t), or to `last` [rows][cols] as E, transposed where
 // `tall`.  sums [slices][rows][pitch].  old and out may be one matrix: a workgroup
 // reads its tile of old before it writes.
-template <typename E, int P>
+template <typename E>
 __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restrict__ sums,
                                                           int slices, int pitch, float keep,
                                                           float take, Matrix old, Matrix out,
-                                                          E* __restrict__ last, bool tall,
-                                                          float scale) {
+                                                          E* __restrict__ last, bool tall) {
   __shared__ float tile[64][65];
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const int64_t plane = static_cast<int64_t>(out.rows) * pitch;
@@ -161,14 +161,16 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
       float o[8] = {};
       if (old.p != nullptr) {
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) {
+        for (int p = 1; p >= 0; --p) {
           const uint4 w = *reinterpret_cast<const uint4*>(
               old.p + (static_cast<int64_t>(p) * old.rows + i0 + i) * old.ld + j0 + j);
           const uint32_t d[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            o[2 * k] += __uint_as_float(d[k] << 16);
-            o[2 * k + 1] += __uint_as_float(d[k] & 0xffff0000u);
+            typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+            const f16x2_t h = __builtin_bit_cast(f16x2_t, d[k]);
+            o[2 * k] += static_cast<float>(h[0]);
+            o[2 * k + 1] += static_cast<float>(h[1]);
           }
         }
       }
@@ -176,7 +178,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
       for (int k = 0; k < 8; ++k) {
         v[k] = j0 + j + k < out.cols ? fmaf(keep, o[k], take * v[k]) : 0.f;
       }
-      if (last == nullptr) put_row<P>(out, i0 + i, j0 + j, v);
+      if (last == nullptr) put_row(out, i0 + i, j0 + j, v);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
   if (last == nullptr && out.t == nullptr) return;
   __syncthreads();
   if (last == nullptr) {
-    put_transposed<P>(out, i0, j0, tile);
+    put_transposed(out, i0, j0, tile);
     return;
   }
   for (int e = threadIdx.x; e < 64 * 64; e += 256) {
@@ -193,13 +195,8 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
     if (i0 + i >= out.rows || j0 + j >= out.cols) continue;
     last[tall ? static_cast<int64_t>(j0 + j) * out.rows + i0 + i
               : static_cast<int64_t>(i0 + i) * out.cols + j0 + j] =
-        ElemTraits<E>::from_f32(scale * tile[i][j]);
+        ElemTraits<E>::from_f32(tile[i][j]);
   }
-}
-
-template <typename E>
-constexpr int parts_for() {
-  return sizeof(E) == 2 ? 2 : 3;
 }
 
 struct Plan {
@@ -210,9 +207,9 @@ struct Plan {
   float* sums;
   size_t bytes;
 };
-Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
+Plan plan_of(const OrthArgs& a, void* ws) {
   Plan p{};
-  const size_t P = elem_bytes == 2 ? 2 : 3;
+  const size_t P = parts_of(kHalves);
   p.m = std::min(a.rows, a.cols);
   p.n = std::max(a.rows, a.cols);
   p.ldm = static_cast<int>(up64(p.m));
@@ -233,23 +230,51 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   return p;
 }
 
-template <int P>
 hipError_t product(const Operand& A, const Operand& B, int ksteps, int slices, int pitch,
                    float* sums, hipStream_t s) {
   return with_tile(tile_for(A.rows, B.rows), [&](auto cf) {
     typedef decltype(cf) CF;
     const int mb = static_cast<int>(blocks(A.rows, CF::BM));
     const int nb = static_cast<int>(blocks(B.rows, CF::BN));
-    product_kernel<CF, P, float, true><<<dim3(static_cast<uint32_t>(mb) * nb, slices), CF::NT, 0,
-                                         s>>>(A, B, ksteps, mb, nb, false, pitch, sums);
+    product_kernel<CF, kHalves, float, true>
+        <<<dim3(static_cast<uint32_t>(mb) * nb, slices), CF::NT, 0, s>>>(
+            A, B, ksteps, mb, nb, false, pitch, nullptr, 0, sums);
     return hipGetLastError();
   });
 }
 
+// The exponent by which values up to `bound` are scaled: below 2^15 (of halves, whose
+// largest is 2^16 - 2^5), with room for roundings.
+int exponent_below(double bound) {
+  int e;
+  std::frexp(std::max(bound * 1.0625, 1e-30), &e);  // bound * 1.0625 < 2^e
+  return std::max(15 - e, -100);
+}
+
+// max |a s + b s^3 + c s^5| over 0 <= s <= top: at the end or where the derivative
+// a + 3 b t + 5 c t^2, t = s^2, is 0.
+double step_bound(const OrthArgs& p, double top) {
+  const double a = p.a, b = p.b, c = p.c;
+  const auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+  double most = f(top);
+  const auto at = [&](double t) {
+    if (t > 0 && t < top * top) most = std::max(most, f(std::sqrt(t)));
+  };
+  if (c != 0) {
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+      at((-3 * b + std::sqrt(d)) / (10 * c));
+      at((-3 * b - std::sqrt(d)) / (10 * c));
+    }
+  } else if (b != 0) {
+    at(-a / (3 * b));
+  }
+  return most;
+}
+
 template <typename E>
 hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
-  constexpr int P = parts_for<E>();
-  const Plan p = plan_of(a, sizeof(E), ws);
+  const Plan p = plan_of(a, ws);
   const bool tall = a.rows > a.cols;
   const int64_t elems = static_cast<int64_t>(a.rows) * a.cols;
   const int count = static_cast<int>(std::min<int64_t>(blocks(elems, 2048), kNormBlocks));
@@ -259,33 +284,47 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   const Matrix g{p.g, nullptr, p.m, p.m, p.ldm, 0}, b{p.b, nullptr, p.m, p.m, p.ldm, 0};
   const Matrix none{};
   const dim3 whole(p.ldn / 64, p.ldm / 64), square(p.ldm / 64, p.ldm / 64);
-  orth_start_kernel<E, P><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, x);
+  double bound = 1.0;  // of X's singular values
+  int ex = exponent_below(bound);
+  orth_start_kernel<E><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
   const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m};
   const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n};
   const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
   const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
   E* no_output = nullptr;
   for (int i = 0; i < a.steps; ++i) {
-    hipError_t e = product<P>(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
+    const bool end = i + 1 == a.steps;
+    const double t = bound * bound;
+    const int eg = exponent_below(t);
+    const int eb = exponent_below(std::fabs(a.b) * t + std::fabs(a.c) * t * t);
+    bound = step_bound(a, bound);
+    const int next = exponent_below(bound);
+    // factors with the powers of two of what goes in undone and of what comes out applied
+    const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
+    hipError_t e = product(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
     if (e != hipSuccess) return e;
-    orth_finish_kernel<E, P><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f, 1.f, none,
-                                                    g, no_output, false, 1.f);
-    if ((e = product<P>(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
+    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f,
+                                                 factor(1, eg - 2 * ex), none, g, no_output, false);
+    if ((e = product(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
       return e;
-    orth_finish_kernel<E, P><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm, a.b, a.c, g, b,
-                                                    no_output, false, 1.f);
-    if ((e = product<P>(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
+    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm,
+                                                 factor(a.b, eb - eg), factor(a.c, eb - 2 * eg), g,
+                                                 b, no_output, false);
+    if ((e = product(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
       return e;
-    orth_finish_kernel<E, P><<<whole, 256, 0, s>>>(
-        p.sums, p.update_slices, p.ldn, a.a, 1.f, x, x,
-        i + 1 == a.steps ? static_cast<E*>(a.out) : no_output, tall, a.scale);
+    const double scale = end ? a.scale : 1.0;
+    const int out = end ? 0 : next;
+    orth_finish_kernel<E><<<whole, 256, 0, s>>>(
+        p.sums, p.update_slices, p.ldn, factor(scale * a.a, out - ex), factor(scale, out - eb - ex),
+        x, x, end ? static_cast<E*>(a.out) : no_output, tall);
+    ex = next;
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t orth_bytes(const OrthArgs& a, int elem_bytes) { return plan_of(a, elem_bytes, nullptr).bytes; }
+size_t orth_bytes(const OrthArgs& a) { return plan_of(a, nullptr).bytes; }
 
 hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s) {
   return elem_bytes == 2 ? orthogonalize<uint16_t>(a, ws, s) : orthogonalize<float>(a, ws, s);

@@ -144,7 +144,7 @@ struct OrthArgs {
   int rows, cols, steps;
   float a, b, c, eps, scale;
 };
-size_t orth_bytes(const OrthArgs& a, int elem_bytes);
+size_t orth_bytes(const OrthArgs& a);
 hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s);
 
 }  // namespace twell

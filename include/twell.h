@@ -620,13 +620,14 @@ int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
  *    [0, vocab) is ignored: its logp is 0, and its row of x has no gradient and
  *    adds to none, whatever that row holds.  targets and the arrays per row are
  *    aligned to their elements only.
- *  - z is a float32 sum (float32 operands: six products of bfloat16 parts, as exact
- *    as float32 ones); maxima, sums and probabilities are float32.  It is never
- *    stored: the gradient forms it again.
+ *  - z is a float32 sum; maxima, sums and probabilities are float32.  It is never
+ *    stored: the gradient forms it again.  float32 x and w enter the products with 22
+ *    bits and more, elements under 2^-18 of the largest of their row of x, or of w, with
+ *    an error of 2^-40 of that largest instead.
  *  - A row with a NaN, or an infinity that meets its product, has NaN results; a
- *    float32 infinity in x or w makes every z of its row or column NaN.  z = -inf
- *    has probability 0; a row with nothing else has lse = logp = -inf and a zero
- *    gradient.
+ *    float32 infinity in x or w makes every z of its row or column infinite or NaN.
+ *    z = -inf has probability 0; a row with nothing else has lse = logp = -inf and a
+ *    zero gradient.
  * Requirements: n_rows >= 0; vocab > 0; d_model > 0 and a multiple of 8; dtype a
  * twell_dtype; scale positive and finite; reserved 0.  Limits, else
  * TWELL_ERR_UNSUPPORTED: n_rows and vocab at most 2^24, d_model at most 2^16,
@@ -661,8 +662,9 @@ size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape)
 /* The gradients of sum_n dlogp[n] logp[n] from the forward's stats:
  *   dl = scale * dlogp (1[v = target] - exp(z_v) / sum exp z);  dx = dl w,  dw = dl^T x
  * dx [n_rows][d_model] and dw [vocab][d_model] in dtype, written, not added to; sums
- * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w) or as
- * three bfloat16 parts (float32).  n_rows == 0 writes a zero dw. */
+ * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w) or
+ * with 22 bits and more (float32; dl / dlogp and scale * dlogp * x within 2^-40 of
+ * their largest).  n_rows == 0 writes a zero dw. */
 int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, const void* w,
                                 const void* targets, const float* stats, const float* dlogp,
                                 void* dx, void* dw, void* workspace, size_t workspace_bytes,
@@ -675,9 +677,9 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
  *   out = scale * X
  * which replaces every singular value s of X by a polynomial's iterate: towards 1
  * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
- *  - Sums and X are float32, held between the products as bfloat16 parts: three
- *    (exact) for a float32 M, two (2^-17) for a bfloat16 one, whose out is rounded
- *    to 2^-8 at the end.  |M|_F is summed in double.
+ *  - Sums are float32; X, G and B enter the products with 22 bits and more, elements
+ *    far below the matrix's bound with an error of 2^-40 of it.  |M|_F is summed in
+ *    double.
  *  - M = 0 gives 0; an infinity or NaN in M gives NaN.
  * Requirements: rows, cols > 0; dtype a twell_dtype (of m and out); 1 <= steps <=
  * TWELL_ORTH_MAX_STEPS; a, b, c and scale finite; eps positive and finite.  Limits,
