@@ -249,7 +249,7 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
   int mb, nb;
   nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
-  nt::mainloop<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  nt::multiply<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
   const int half = lane_id() >> 5;
   const int wave_row = row0 - 4 * half;  // the wave's first row
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   int mb, nb;
   nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
-  nt::mainloop<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
+  nt::multiply<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
   const int64_t n_rows = a.x.rows;
 #pragma unroll

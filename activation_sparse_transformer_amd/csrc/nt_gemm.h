@@ -12,7 +12,8 @@
 //              step, so the two small products go over the whole of K first and the
 //              large one last: no more cuts at the sum's full size than a product of
 //              one part has.
-//  - kHalf:    the hi part alone.
+//  - kHalf:    the hi part alone, within 2^-11 of v.
+// A product's form is that of both operands, or kMixed: A in kHalf, B in kHalves.
 //
 // Operands are [parts][rows][ld], ld a multiple of 64 with zeros past the
 // contraction's length; rows past the end read the last row and feed outputs
@@ -28,9 +29,9 @@ namespace nt {
 
 constexpr int kStep = 64;  // K elements of one LDS stage
 
-enum Form { kBf16, kHalf, kHalves };
+enum Form { kBf16, kHalf, kHalves, kMixed };
 constexpr int parts_of(Form f) { return f == kHalves ? 2 : 1; }
-constexpr int products_of(Form f) { return f == kHalves ? 3 : 1; }
+constexpr int products_of(Form f) { return f == kHalves ? 3 : f == kMixed ? 2 : 1; }
 
 struct Operand {
   const uint16_t* p;
@@ -85,21 +86,25 @@ __device__ __forceinline__ void issue(const uint16_t* const* src, int64_t offset
 }
 
 // The steps of a contraction: a product of parts after another, each over the whole
-// of K, in the order hi lo, lo hi, hi hi.
+// of K, in the order lo hi (kHalves), hi lo, hi hi.
 template <Form F>
 struct Walk {
   int64_t part_a, part_b;
   int end;  // of K
-  int k = 0, q = 0;
+  int k = 0, left = products_of(F) - 1;
   __device__ __forceinline__ void next() {
     k += kStep;
-    if (F == kHalves && k == end) {
+    if (products_of(F) > 1 && k == end) {
       k = 0;
-      ++q;
+      --left;
     }
   }
-  __device__ __forceinline__ int64_t a() const { return F == kHalves && q == 1 ? part_a + k : k; }
-  __device__ __forceinline__ int64_t b() const { return F == kHalves && q == 0 ? part_b + k : k; }
+  __device__ __forceinline__ int64_t a() const {
+    return F == kHalves && left == 2 ? part_a + k : k;
+  }
+  __device__ __forceinline__ int64_t b() const {
+    return products_of(F) > 1 && left == 1 ? part_b + k : k;
+  }
 };
 
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
@@ -181,6 +186,146 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
   __syncthreads();  // the stages are free for the epilogue
 }
 
+// ---- The same for waves of 64 x 128 (2 x 4 blocks), software-pipelined.  Each 16-wide
+// K step is one asm block: the 8 MFMAs of the fragments in hand with the 6 LDS reads
+// of the next step's fragments between them, and a wait for those reads at its end
+// (no read is in flight when the block ends).  The MFMAs of a stage's last step run
+// behind the next stage's barrier, beside the reads of its first step.  Same products
+// in the same order as mainloop.
+struct Fragments {
+  i32x4_t a[2], b[4];
+};
+
+#define NT_PIPE_STEP(MFMA)                                                                    \
+  asm volatile(                                                                               \
+      "ds_read_b128 %[na0], %[p0]\n\t" MFMA " %[c00], %[a0], %[b0], %[c00]\n\t"               \
+      "ds_read_b128 %[na1], %[p1]\n\t" MFMA " %[c01], %[a0], %[b1], %[c01]\n\t"               \
+      "ds_read_b128 %[nb0], %[p2]\n\t" MFMA " %[c02], %[a0], %[b2], %[c02]\n\t"               \
+      "ds_read_b128 %[nb1], %[p3]\n\t" MFMA " %[c03], %[a0], %[b3], %[c03]\n\t"               \
+      "ds_read_b128 %[nb2], %[p4]\n\t" MFMA " %[c10], %[a1], %[b0], %[c10]\n\t"               \
+      "ds_read_b128 %[nb3], %[p5]\n\t" MFMA " %[c11], %[a1], %[b1], %[c11]\n\t" MFMA          \
+      " %[c12], %[a1], %[b2], %[c12]\n\t" MFMA " %[c13], %[a1], %[b3], %[c13]\n\t"            \
+      "s_waitcnt lgkmcnt(0)\n\t"                                                              \
+      : [c00] "+v"(c[0][0]), [c01] "+v"(c[0][1]), [c02] "+v"(c[0][2]), [c03] "+v"(c[0][3]),   \
+        [c10] "+v"(c[1][0]), [c11] "+v"(c[1][1]), [c12] "+v"(c[1][2]), [c13] "+v"(c[1][3]),   \
+        [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1]), [nb0] "=&v"(nxt.b[0]),                  \
+        [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])                   \
+      : [a0] "v"(cur.a[0]), [a1] "v"(cur.a[1]), [b0] "v"(cur.b[0]), [b1] "v"(cur.b[1]),       \
+        [b2] "v"(cur.b[2]), [b3] "v"(cur.b[3]), [p0] "v"(at[0]), [p1] "v"(at[1]),             \
+        [p2] "v"(at[2]), [p3] "v"(at[3]), [p4] "v"(at[4]), [p5] "v"(at[5])                    \
+      : "memory")
+
+template <Form F>
+__device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][4], const Fragments& cur,
+                                          Fragments& nxt, const uint32_t (&at)[6]) {
+  if constexpr (F == kBf16) NT_PIPE_STEP("v_mfma_f32_32x32x16_bf16");
+  else NT_PIPE_STEP("v_mfma_f32_32x32x16_f16");
+}
+#undef NT_PIPE_STEP
+
+__device__ __forceinline__ void pipe_load(Fragments& nxt, const uint32_t (&at)[6]) {
+  asm volatile(
+      "ds_read_b128 %[na0], %[p0]\n\t"
+      "ds_read_b128 %[na1], %[p1]\n\t"
+      "ds_read_b128 %[nb0], %[p2]\n\t"
+      "ds_read_b128 %[nb1], %[p3]\n\t"
+      "ds_read_b128 %[nb2], %[p4]\n\t"
+      "ds_read_b128 %[nb3], %[p5]\n\t"
+      "s_waitcnt lgkmcnt(0)\n\t"
+      : [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1]), [nb0] "=&v"(nxt.b[0]),
+        [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])
+      : [p0] "v"(at[0]), [p1] "v"(at[1]), [p2] "v"(at[2]), [p3] "v"(at[3]), [p4] "v"(at[4]),
+        [p5] "v"(at[5])
+      : "memory");
+}
+
+// VALU writes of the accumulators before MFMAs in asm, and MFMA results before VALU
+// reads: the accumulators are operands, so neither moves across the wait.
+__device__ __forceinline__ void settle(f32x16_t (&c)[2][4]) {
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"
+               : "+v"(c[0][0]), "+v"(c[0][1]), "+v"(c[0][2]), "+v"(c[0][3]), "+v"(c[1][0]),
+                 "+v"(c[1][1]), "+v"(c[1][2]), "+v"(c[1][3]));
+}
+
+template <class CF, Form F>
+__device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Operand& B, int n0,
+                                              int k0, int ksteps, uint16_t* lds,
+                                              f32x16_t (&acc)[2][4]) {
+  static_assert(CF::FM == 2 && CF::FN == 4 && CF::STAGES == 2, "2 x 4 blocks of 32x32 per wave");
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int steps = ksteps * products_of(F);
+  if (steps == 0) return;
+  settle(acc);
+  const uint16_t* asrc[CF::A_ISSUE];
+  const uint16_t* bsrc[CF::B_ISSUE];
+  sources<CF::A_ISSUE, CF::NW>(A, m0, k0, asrc);
+  sources<CF::B_ISSUE, CF::NW>(B, n0, k0, bsrc);
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+  typedef __attribute__((address_space(3))) uint16_t lds_u16;
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u16*)lds));
+  uint32_t at[4][6];  // LDS addresses of the fragments of each K step in stage 0
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    const int kc = ks * 2 + (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      at[ks][i] = base + 2u * tile_offset(wm * CF::WTM + i * 32 + (lane & 31), kc);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      at[ks][2 + j] = base + 2u * (CF::BM * kStep +
+                                   tile_offset(wn * CF::WTN + j * 32 + (lane & 31), kc));
+  }
+  Walk<F> walk{A.part, B.part, ksteps * kStep};
+  auto copy = [&](int stage) {
+    uint16_t* to = lds + stage * CF::STAGE;
+    issue<CF::A_ISSUE, CF::NW>(asrc, walk.a(), to);
+    issue<CF::B_ISSUE, CF::NW>(bsrc, walk.b(), to + CF::BM * kStep);
+    walk.next();
+  };
+  Fragments f0, f1;
+  copy(0);
+  meet<0>();
+  if (steps > 1) copy(1);
+  pipe_load(f0, at[0]);
+  pipe_step<F>(acc, f0, f1, at[1]);
+  pipe_step<F>(acc, f1, f0, at[2]);
+  pipe_step<F>(acc, f0, f1, at[3]);
+  for (int s = 1; s < steps; ++s) {  // f1: the fragments of the last K step of stage s - 1
+    meet<0>();
+    if (s + 1 < steps) copy((s + 1) & 1);
+    const uint32_t shift = static_cast<uint32_t>(s & 1) * (CF::STAGE * 2);
+    uint32_t a[4][6];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int q = 0; q < 6; ++q) a[ks][q] = at[ks][q] + shift;
+    pipe_step<F>(acc, f1, f0, a[0]);
+    pipe_step<F>(acc, f0, f1, a[1]);
+    pipe_step<F>(acc, f1, f0, a[2]);
+    pipe_step<F>(acc, f0, f1, a[3]);
+  }
+  settle(acc);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = mfma<F>(f1.a[i], f1.b[j], acc[i][j]);
+  __syncthreads();  // the stages are free for the epilogue
+}
+
+template <class CF, Form F>
+__device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand& B, int n0, int k0,
+                                         int ksteps, uint16_t* lds,
+                                         f32x16_t (&acc)[CF::FM][CF::FN]) {
+  if constexpr (CF::FM == 2 && CF::FN == 4) mainloop_pipe<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
+  else mainloop<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
+}
+
 // Element (i, r) of a lane's accumulators is row block_row<CF>() + row_of(i, r),
 // element j column block_col<CF>() + 32 j of the block.
 template <class CF>
@@ -250,7 +395,7 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
-  mainloop<CF, F>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
+  multiply<CF, F>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
   const int row0 = mb * CF::BM + block_row<CF>();
   if (ACC) out += static_cast<int64_t>(slice) * pitch * B.rows;
   if (amax != nullptr) {

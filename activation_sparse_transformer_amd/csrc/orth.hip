@@ -5,6 +5,12 @@
 // coefficients drive towards 1.
 //
 // All products run on MFMA over half-precision parts of float32 values (nt_gemm.h).
+// X, G and B are held in two parts.  For a bfloat16 M the X of X X^T and of B X enters
+// by its first part alone, an eighth of the rounding that M itself carries, in 1, 3 and
+// 2 products instead of 3, 3 and 3; a X keeps both parts, so the rounding of one step is
+// not handed to the next (14336 x 4096: 0.0005 beside the output's own 0.0017; with a X
+// rounded too 0.0016).  G and B stay in two parts: a diagonal G of one value would be
+// off by one common factor.
 // |X| <= 1 at the start, and max |a s + b s^3 + c s^5| bounds it after each step, so the
 // powers of two that the parts are scaled by are known on the host.  A product leaves
 // float32 partial sums, slices of K where its tiles are few; a pass over them adds the
@@ -59,29 +65,32 @@ __device__ __forceinline__ double inverse_norm(const double* __restrict__ parts,
   return 1.0 / (sqrt(total) + static_cast<double>(eps));
 }
 
-struct Matrix {  // parts of [rows][cols], and of its transpose
+struct Matrix {  // two parts of [rows][cols], and the parts of its transpose
   uint16_t *p, *t;
   int rows, cols, ld, ldt;
 };
 
 // 8 scaled values of row i, from column j on, as parts.
+template <Form F>
 __device__ __forceinline__ void put_row(const Matrix& x, int i, int j, const float (&v)[8]) {
-  uint32_t w[2][4];
+  constexpr int P = parts_of(F);
+  uint32_t w[P][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint16_t lo[2], hi[2];
-    split<kHalves>(v[2 * k], lo);
-    split<kHalves>(v[2 * k + 1], hi);
+    uint16_t lo[P], hi[P];
+    split<F>(v[2 * k], lo);
+    split<F>(v[2 * k + 1], hi);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+    for (int p = 0; p < P; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
   }
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+  for (int p = 0; p < P; ++p)
     *reinterpret_cast<uint4*>(x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j) =
         make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 // The transposed parts of a tile in LDS (zeros past the matrix).
+template <Form F>
 __device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
                                                const float (&tile)[64][65]) {
 #pragma unroll
@@ -93,13 +102,13 @@ __device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = tile[i + k][j];
-    put_row(t, j0 + j, i0 + i, v);
+    put_row<F>(t, j0 + j, i0 + i, v);
   }
 }
 
 // X = 2^exponent M / (|M|_F + eps): one 64 x 64 tile a workgroup.  `tall`: M is
 // [cols][rows].
-template <typename E>
+template <typename E, Form F>
 __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m, bool tall,
                                                          const double* __restrict__ parts,
                                                          int count, float eps, int exponent,
@@ -128,16 +137,16 @@ __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = tile[i][j + k];
-    put_row(x, i0 + i, j0 + j, v);
+    put_row<kHalves>(x, i0 + i, j0 + j, v);
   }
-  put_transposed(x, i0, j0, tile);
+  put_transposed<F>(x, i0, j0, tile);
 }
 
 // v = keep * (old's value) + take * (the sum of the slices), to out's parts (and
 // their transpose where out.t), or to `last` [rows][cols] as E, transposed where
 // `tall`.  sums [slices][rows][pitch].  old and out may be one matrix: a workgroup
 // reads its tile of old before it writes.
-template <typename E>
+template <typename E, Form F>
 __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restrict__ sums,
                                                           int slices, int pitch, float keep,
                                                           float take, Matrix old, Matrix out,
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
       for (int k = 0; k < 8; ++k) {
         v[k] = j0 + j + k < out.cols ? fmaf(keep, o[k], take * v[k]) : 0.f;
       }
-      if (last == nullptr) put_row(out, i0 + i, j0 + j, v);
+      if (last == nullptr) put_row<kHalves>(out, i0 + i, j0 + j, v);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
@@ -186,7 +195,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
   if (last == nullptr && out.t == nullptr) return;
   __syncthreads();
   if (last == nullptr) {
-    put_transposed(out, i0, j0, tile);
+    put_transposed<F>(out, i0, j0, tile);
     return;
   }
   for (int e = threadIdx.x; e < 64 * 64; e += 256) {
@@ -207,9 +216,10 @@ struct Plan {
   float* sums;
   size_t bytes;
 };
-Plan plan_of(const OrthArgs& a, void* ws) {
+constexpr Form x_form(int elem_bytes) { return elem_bytes == 2 ? kHalf : kHalves; }
+Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   Plan p{};
-  const size_t P = parts_of(kHalves);
+  const size_t P = parts_of(kHalves), PX = parts_of(x_form(elem_bytes));
   p.m = std::min(a.rows, a.cols);
   p.n = std::max(a.rows, a.cols);
   p.ldm = static_cast<int>(up64(p.m));
@@ -221,7 +231,7 @@ Plan plan_of(const OrthArgs& a, void* ws) {
   Carve c{static_cast<char*>(ws)};
   p.norm = c.take<double>(kNormBlocks);
   p.x = c.take<uint16_t>(P * whole);
-  p.xt = c.take<uint16_t>(P * p.n * p.ldm);
+  p.xt = c.take<uint16_t>(PX * p.n * p.ldm);
   p.g = c.take<uint16_t>(P * square);
   p.b = c.take<uint16_t>(P * square);
   p.sums = c.take<float>(std::max(std::max(p.gram_slices, p.square_slices) * square,
@@ -230,13 +240,14 @@ Plan plan_of(const OrthArgs& a, void* ws) {
   return p;
 }
 
+template <Form F>
 hipError_t product(const Operand& A, const Operand& B, int ksteps, int slices, int pitch,
                    float* sums, hipStream_t s) {
   return with_tile(tile_for(A.rows, B.rows), [&](auto cf) {
     typedef decltype(cf) CF;
     const int mb = static_cast<int>(blocks(A.rows, CF::BM));
     const int nb = static_cast<int>(blocks(B.rows, CF::BN));
-    product_kernel<CF, kHalves, float, true>
+    product_kernel<CF, F, float, true>
         <<<dim3(static_cast<uint32_t>(mb) * nb, slices), CF::NT, 0, s>>>(
             A, B, ksteps, mb, nb, false, pitch, nullptr, 0, sums);
     return hipGetLastError();
@@ -274,7 +285,8 @@ double step_bound(const OrthArgs& p, double top) {
 
 template <typename E>
 hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
-  const Plan p = plan_of(a, ws);
+  constexpr Form X = x_form(sizeof(E));
+  const Plan p = plan_of(a, sizeof(E), ws);
   const bool tall = a.rows > a.cols;
   const int64_t elems = static_cast<int64_t>(a.rows) * a.cols;
   const int count = static_cast<int>(std::min<int64_t>(blocks(elems, 2048), kNormBlocks));
@@ -286,7 +298,7 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   const dim3 whole(p.ldn / 64, p.ldm / 64), square(p.ldm / 64, p.ldm / 64);
   double bound = 1.0;  // of X's singular values
   int ex = exponent_below(bound);
-  orth_start_kernel<E><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
+  orth_start_kernel<E, X><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
   const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m};
   const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n};
   const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
@@ -301,20 +313,20 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
     const int next = exponent_below(bound);
     // factors with the powers of two of what goes in undone and of what comes out applied
     const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
-    hipError_t e = product(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
+    hipError_t e = product<X>(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
     if (e != hipSuccess) return e;
-    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f,
+    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f,
                                                  factor(1, eg - 2 * ex), none, g, no_output, false);
-    if ((e = product(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
+    if ((e = product<kHalves>(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
       return e;
-    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm,
+    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm,
                                                  factor(a.b, eb - eg), factor(a.c, eb - 2 * eg), g,
                                                  b, no_output, false);
-    if ((e = product(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
+    if ((e = product<X == kHalf ? kMixed : kHalves>(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
       return e;
     const double scale = end ? a.scale : 1.0;
     const int out = end ? 0 : next;
-    orth_finish_kernel<E><<<whole, 256, 0, s>>>(
+    orth_finish_kernel<E, X><<<whole, 256, 0, s>>>(
         p.sums, p.update_slices, p.ldn, factor(scale * a.a, out - ex), factor(scale, out - eb - ex),
         x, x, end ? static_cast<E*>(a.out) : no_output, tall);
     ex = next;
@@ -324,7 +336,7 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t orth_bytes(const OrthArgs& a) { return plan_of(a, nullptr).bytes; }
+size_t orth_bytes(const OrthArgs& a, int elem_bytes) { return plan_of(a, elem_bytes, nullptr).bytes; }
 
 hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s) {
   return elem_bytes == 2 ? orthogonalize<uint16_t>(a, ws, s) : orthogonalize<float>(a, ws, s);

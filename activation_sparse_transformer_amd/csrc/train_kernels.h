@@ -144,7 +144,7 @@ struct OrthArgs {
   int rows, cols, steps;
   float a, b, c, eps, scale;
 };
-size_t orth_bytes(const OrthArgs& a);
+size_t orth_bytes(const OrthArgs& a, int elem_bytes);
 hipError_t launch_orthogonalize(const OrthArgs& a, int elem_bytes, void* ws, hipStream_t s);
 
 }  // namespace twell

@@ -1043,7 +1043,7 @@ OrthArgs orth_args(const twell_orth_shape* s, const void* in, void* out) {
 
 TWELL_EXPORT size_t twell_orthogonalize_workspace_size(const twell_orth_shape* shape) {
   if (check_orth(shape) != TWELL_OK) return 0;
-  return orth_bytes(orth_args(shape, nullptr, nullptr));
+  return orth_bytes(orth_args(shape, nullptr, nullptr), elem_bytes(shape->dtype));
 }
 
 TWELL_EXPORT int twell_orthogonalize(const twell_orth_shape* shape, const void* m, void* out,
@@ -1053,7 +1053,7 @@ TWELL_EXPORT int twell_orthogonalize(const twell_orth_shape* shape, const void* 
   if (m == nullptr || out == nullptr || workspace == nullptr) return TWELL_ERR_INVALID_ARG;
   if (!aligned16(m) || !aligned16(out) || !aligned16(workspace)) return TWELL_ERR_INVALID_ARG;
   const OrthArgs a = orth_args(shape, m, out);
-  if (workspace_bytes < orth_bytes(a)) return TWELL_ERR_WORKSPACE;
-  return hip_status(launch_orthogonalize(a, elem_bytes(shape->dtype), workspace,
-                                         static_cast<hipStream_t>(stream)));
+  const int eb = elem_bytes(shape->dtype);
+  if (workspace_bytes < orth_bytes(a, eb)) return TWELL_ERR_WORKSPACE;
+  return hip_status(launch_orthogonalize(a, eb, workspace, static_cast<hipStream_t>(stream)));
 }

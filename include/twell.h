@@ -678,8 +678,9 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
  * which replaces every singular value s of X by a polynomial's iterate: towards 1
  * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
  *  - Sums are float32; X, G and B enter the products with 22 bits and more, elements
- *    far below the matrix's bound with an error of 2^-40 of it.  |M|_F is summed in
- *    double.
+ *    far below the matrix's bound with an error of 2^-40 of it.  A bfloat16 M's X is
+ *    rounded to 11 bits after each step, an eighth of M's own rounding.  |M|_F is summed
+ *    in double.
  *  - M = 0 gives 0; an infinity or NaN in M gives NaN.
  * Requirements: rows, cols > 0; dtype a twell_dtype (of m and out); 1 <= steps <=
  * TWELL_ORTH_MAX_STEPS; a, b, c and scale finite; eps positive and finite.  Limits,
