@@ -247,7 +247,7 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
                                                             int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
-  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  nt::tile_of(nt::run_of(blockIdx.x, gridDim.x), m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
   nt::multiply<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
@@ -378,7 +378,7 @@ template <class CF, Form F>
 __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks, int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
-  nt::tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
+  nt::tile_of(nt::run_of(blockIdx.x, gridDim.x), m_blocks, n_blocks, mb, nb);
   f32x16_t acc[CF::FM][CF::FN];
   nt::multiply<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
@@ -486,8 +486,14 @@ int piece_of(int vocab, size_t per_column, size_t budget) {
 
 constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
 
+// Stages of a contraction over d columns.
+int64_t stages(const HeadArgs& a, int elem_bytes) {
+  return up64(a.d) / 64 * (elem_bytes == 2 ? 1 : products_of(kHalves));
+}
+
 struct ForwardPlan {
   int piece, tiles;
+  Tile tile;
   uint16_t *xp, *wp;
   float *amax, *undo;
   float2* parts;
@@ -500,8 +506,8 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const bool in_place = direct(elem_bytes, a.d);
   p.piece = in_place ? a.vocab : piece_of(a.vocab, part_bytes, size_t{128} << 20);
   // tiles of a piece start at its first column: pieces but the last are whole tiles
-  const Tile t = tile_for(p.piece, a.n_rows);
-  p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(t)));
+  p.tile = cut_for(p.piece, a.n_rows, stages(a, elem_bytes), 1, false).tile;
+  p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(p.tile)));
   Carve c{static_cast<char*>(ws)};
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
   p.target_z = c.take<float>(a.n_rows);
@@ -516,8 +522,9 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
 }
 
 struct BackwardPlan {
-  int piece, slices;
-  int ldn;
+  int piece, ldn;
+  Tile dl_tile;
+  Cut dx_cut;
   uint16_t *xp, *wp, *xt, *wt, *dl, *dlt;
   float *amax, *undo, *sums;
   size_t bytes;
@@ -531,13 +538,15 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.piece = piece_of(a.vocab, per_column, size_t{192} << 20);
   const size_t ldv = up64(p.piece);
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  p.slices = slices_for(a.d, n, ldv / 64);
+  const int products = elem_bytes == 2 ? 1 : products_of(kHalves);
+  p.dx_cut = cut_for(a.d, n, ldv / 64 * products, 32, false);
+  p.dl_tile = cut_for(p.piece, n, stages(a, elem_bytes), 1, false).tile;
   Carve c{static_cast<char*>(ws)};
   p.xt = c.take<uint16_t>(P * a.d * p.ldn);
   p.wt = c.take<uint16_t>(P * a.d * ldv);
   p.dl = c.take<uint16_t>(P * n * ldv);
   p.dlt = c.take<uint16_t>(P * p.piece * p.ldn);
-  p.sums = c.take<float>(p.slices * n * a.d);
+  p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
   if (!in_place) {
     p.amax = c.take<float>(kAmax);
     p.undo = c.take<float>(n);
@@ -596,14 +605,13 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
   const ForwardPlan p = forward_plan(a, sizeof(E), ws);
   const int n = static_cast<int>(a.n_rows);
   const Operand x = x_operand<E>(a, nullptr, p.amax, p.undo, p.xp, s);
-  const Tile tile = tile_for(p.piece, n);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const Operand w = w_operand<E>(a, v0, rows, p.amax, p.wp, s);
     const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, p.amax,
                       p.undo, a.targets, a.index_bytes,
-                      p.parts + v0 / tile_rows(tile) * a.n_rows, p.target_z};
-    const hipError_t e = with_tile(tile, [&](auto cf) {
+                      p.parts + v0 / tile_rows(p.tile) * a.n_rows, p.target_z};
+    const hipError_t e = with_tile(p.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       head_stats_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
@@ -642,7 +650,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     const DlArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, amax_w, p.undo,
                    a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
                    p.dlt, ldv, p.ldn};
-    hipError_t e = with_tile(tile_for(rows, n), [&](auto cf) {
+    hipError_t e = with_tile(p.dl_tile, [&](auto cf) {
       typedef decltype(cf) CF;
       // ldn columns of dlt are written, of them the last as zeros
       const int mb = static_cast<int>(blocks(rows, CF::BM));
@@ -654,16 +662,17 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     const Operand wt{p.wt, static_cast<int64_t>(a.d) * ldv, ldv, a.d};
     const Operand dl{p.dl, static_cast<int64_t>(n) * ldv, ldv, n};
     const Operand dlt{p.dlt, static_cast<int64_t>(rows) * p.ldn, p.ldn, rows};
-    e = with_tile(tile_for(a.d, n), [&](auto cf) {
+    e = with_tile(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       product_kernel<CF, F, float, true>
-          <<<dim3(static_cast<uint32_t>(mb) * nb, p.slices), CF::NT, 0, s>>>(
+          <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
               wt, dl, ldv / 64, mb, nb, v0 > 0, a.d, nullptr, 0, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    e = with_tile(tile_for(a.d, rows), [&](auto cf) {
+    const Cut dw_cut = cut_for(a.d, rows, p.ldn / 64 * products_of(F), 1, false);
+    e = with_tile(dw_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
@@ -675,7 +684,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     if (e != hipSuccess) return e;
   }
   head_dx_kernel<E><<<static_cast<uint32_t>(blocks(a.n_rows * a.d / 8, 256)), 256, 0, s>>>(
-      a, p.sums, p.slices, dlogp, amax_w, static_cast<E*>(dx));
+      a, p.sums, p.dx_cut.slices, dlogp, amax_w, static_cast<E*>(dx));
   return hipGetLastError();
 }
 

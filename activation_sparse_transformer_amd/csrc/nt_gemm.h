@@ -340,18 +340,29 @@ __device__ __forceinline__ int block_col() {
   return threadIdx.x / kWave % CF::WAVES_N * CF::WTN + (lane_id() & 31);
 }
 
-// Tile b of m_blocks x n_blocks.  Workgroups are dealt round-robin to the 8 XCDs:
-// each XCD gets a contiguous run of tiles, walked in groups of 4 row blocks, so
-// that tiles running together share operands in its L2.
-__device__ __forceinline__ void tile_of(int b, int m_blocks, int n_blocks, int& mb, int& nb) {
-  const int total = m_blocks * n_blocks;
+// Workgroups are dealt round-robin to the 8 XCDs: workgroup b of `total` takes place
+// run_of(b, total), so that each XCD gets a contiguous run of places.
+__device__ __forceinline__ int run_of(int b, int total) {
   const int each = total / 8, more = total % 8, x = b % 8;
-  const int t = x * each + min(x, more) + b / 8;
+  return x * each + min(x, more) + b / 8;
+}
+
+// Tile t of m_blocks x n_blocks, in groups of 4 row blocks, so that tiles running
+// together share operands in an XCD's L2.
+__device__ __forceinline__ void tile_of(int t, int m_blocks, int n_blocks, int& mb, int& nb) {
   const int per_group = 4 * n_blocks;
   const int g = t / per_group, in = t - g * per_group;
   const int rows = min(4, m_blocks - g * 4);
   mb = g * 4 + in % rows;
   nb = in / rows;
+}
+
+// Tile t of those with mb <= nb, column by column.
+__device__ __forceinline__ void triangle_of(int t, int& mb, int& nb) {
+  nb = static_cast<int>((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+  while (nb * (nb + 1) / 2 > t) --nb;
+  while ((nb + 1) * (nb + 2) / 2 <= t) ++nb;
+  mb = t - nb * (nb + 1) / 2;
 }
 
 // The parts of v (scaled already), the larger first.
@@ -382,7 +393,9 @@ __device__ __forceinline__ float power_of_two(int e) { return ldexpf(1.f, e); }
 // out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, lines of
 // `pitch` elements (a multiple of 8, not under A.rows; what lies past A.rows is
 // undefined): as floats (ACC: slice after slice in out, added to where `add`) or as E.
-// Times 2^(exponent - exponent_for(*amax)) where amax is given.
+// Times 2^(exponent - exponent_for(*amax)) where amax is given.  n_blocks == 0: C is
+// symmetric, and only the tiles of m_blocks x m_blocks with rows up to the columns' are
+// formed.
 template <class CF, Form F, typename E, bool ACC>
 __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, int ksteps,
                                                          int m_blocks, int n_blocks, bool add,
@@ -390,8 +403,10 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
                                                          int exponent, E* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
-  tile_of(blockIdx.x, m_blocks, n_blocks, mb, nb);
   const int slices = gridDim.y, slice = blockIdx.y;
+  const int t = run_of(blockIdx.x, gridDim.x);
+  if (n_blocks == 0) triangle_of(t, mb, nb);
+  else tile_of(t, m_blocks, n_blocks, mb, nb);
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
@@ -448,15 +463,7 @@ typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32
 inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 inline int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
 
-// A tile for a product of `rows` x `cols`: the widest that covers few columns once;
-// 256 x 256 where that many tiles fill the CUs (one workgroup each), else 128 x 128
-// (two each).
 enum Tile { kBare, kFew, kMid, kBig };
-inline Tile tile_for(int64_t rows, int64_t cols) {
-  if (cols <= 32) return kBare;
-  if (cols <= 64) return kFew;
-  return blocks(rows, 256) * blocks(cols, 256) >= 192 ? kBig : kMid;
-}
 template <class F>
 hipError_t with_tile(Tile t, const F& f) {
   switch (t) {
@@ -469,13 +476,43 @@ hipError_t with_tile(Tile t, const F& f) {
 inline int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
 inline int tile_cols(Tile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kFew ? 64 : 32; }
 
-// Slices of K for a product whose tiles alone do not fill the CUs: as many as do,
-// of at least 4 steps.
-inline int slices_for(int64_t rows, int64_t cols, int64_t ksteps) {
-  const Tile t = tile_for(rows, cols);
-  const int64_t tiles = blocks(rows, tile_rows(t)) * blocks(cols, tile_cols(t));
-  return static_cast<int>(
-      std::clamp<int64_t>(384 / std::max<int64_t>(tiles, 1), 1, std::clamp<int64_t>(ksteps / 4, 1, 32)));
+// How a product of `rows` x `cols` over `steps` stages is cut: its tile, and slices of K.
+struct Cut {
+  Tile tile;
+  int slices;
+};
+// At most 64 columns: the narrowest tile, and slices until two workgroups a CU are
+// there.  Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us
+// to fill and to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us),
+// with as many slices as pay for writing and adding up their float32 sums (5 TB/s).
+inline Cut cut_for(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle) {
+  if (cols <= 64 && !triangle) {
+    const Tile t = cols <= 32 ? kBare : kFew;
+    const int64_t tiles = blocks(rows, tile_rows(t));
+    return {t, static_cast<int>(std::clamp<int64_t>(512 / tiles, 1,
+                                                    std::clamp<int64_t>(steps / 4, 1, most_slices)))};
+  }
+  Cut best{kMid, 1};
+  double least = 1e300;
+  for (const Tile t : {kBig, kMid}) {
+    const int64_t mb = blocks(rows, tile_rows(t)), nb = blocks(cols, tile_cols(t));
+    const int64_t tiles = triangle ? mb * (mb + 1) / 2 : mb * nb;
+    for (int s = 1; s <= most_slices && s <= std::max<int64_t>(steps / 4, 1); ++s) {
+      const double each = static_cast<double>(blocks(steps, s));
+      const int64_t groups = tiles * s;
+      double us;
+      if (t == kBig) us = blocks(groups, 256) * (each * 2.1 + 6);
+      else if (groups <= 256) us = each * 0.78 + 4;
+      else us = blocks(groups, 512) * (each * 1.25 + 4);
+      if (most_slices > 1) us += static_cast<double>(s) * tiles * tile_rows(t) * tile_cols(t) * 8 / 5e6;
+      if (us < least) {
+        least = us;
+        best = {t, s};
+      }
+      if (groups > 1024) break;
+    }
+  }
+  return best;
 }
 
 struct Carve {

@@ -144,15 +144,19 @@ __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m
 
 // v = keep * (old's value) + take * (the sum of the slices), to out's parts (and
 // their transpose where out.t), or to `last` [rows][cols] as E, transposed where
-// `tall`.  sums [slices][rows][pitch].  old and out may be one matrix: a workgroup
-// reads its tile of old before it writes.
+// `tall`.  sums [slices][rows][pitch]; `block`: out is symmetric and sums holds its tiles
+// of that size with columns up to the rows', the rest is their mirror image.  old and out
+// may be one matrix: a workgroup reads its tile of old before it writes.
 template <typename E, Form F>
 __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restrict__ sums,
-                                                          int slices, int pitch, float keep,
-                                                          float take, Matrix old, Matrix out,
+                                                          int slices, int block, int pitch,
+                                                          float keep, float take, Matrix old,
+                                                          Matrix out,
                                                           E* __restrict__ last, bool tall) {
   __shared__ float tile[64][65];
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+  const bool mirror = block != 0 && i0 / block != j0 / block;
+  if (mirror && j0 > i0) return;
   const int64_t plane = static_cast<int64_t>(out.rows) * pitch;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -192,8 +196,9 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
 #pragma unroll
     for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
   }
-  if (last == nullptr && out.t == nullptr) return;
+  if (last == nullptr && out.t == nullptr && !mirror) return;
   __syncthreads();
+  if (mirror) out.t = out.p, out.ldt = out.ld;
   if (last == nullptr) {
     put_transposed<F>(out, i0, j0, tile);
     return;
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
 
 struct Plan {
   int m, n, ldm, ldn;
-  int gram_slices, square_slices, update_slices;
+  Cut gram, square, update;
   double* norm;
   uint16_t *x, *xt, *g, *b;
   float* sums;
@@ -224,9 +229,10 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   p.n = std::max(a.rows, a.cols);
   p.ldm = static_cast<int>(up64(p.m));
   p.ldn = static_cast<int>(up64(p.n));
-  p.gram_slices = slices_for(p.m, p.m, p.ldn / 64);
-  p.square_slices = slices_for(p.m, p.m, p.ldm / 64);
-  p.update_slices = slices_for(p.n, p.m, p.ldm / 64);
+  const int gram = PX == 2 ? 3 : 1, update = PX == 2 ? 3 : 2;  // products
+  p.gram = cut_for(p.m, p.m, p.ldn / 64 * gram, 32, true);
+  p.square = cut_for(p.m, p.m, p.ldm / 64 * 3, 32, true);
+  p.update = cut_for(p.n, p.m, p.ldm / 64 * update, 32, false);
   const size_t square = static_cast<size_t>(p.m) * p.ldm, whole = static_cast<size_t>(p.m) * p.ldn;
   Carve c{static_cast<char*>(ws)};
   p.norm = c.take<double>(kNormBlocks);
@@ -234,22 +240,23 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   p.xt = c.take<uint16_t>(PX * p.n * p.ldm);
   p.g = c.take<uint16_t>(P * square);
   p.b = c.take<uint16_t>(P * square);
-  p.sums = c.take<float>(std::max(std::max(p.gram_slices, p.square_slices) * square,
-                                  p.update_slices * whole));
+  p.sums = c.take<float>(std::max(std::max(p.gram.slices, p.square.slices) * square,
+                                  p.update.slices * whole));
   p.bytes = c.used;
   return p;
 }
 
 template <Form F>
-hipError_t product(const Operand& A, const Operand& B, int ksteps, int slices, int pitch,
-                   float* sums, hipStream_t s) {
-  return with_tile(tile_for(A.rows, B.rows), [&](auto cf) {
+hipError_t product(const Operand& A, const Operand& B, int ksteps, const Cut& cut, bool triangle,
+                   int pitch, float* sums, hipStream_t s) {
+  return with_tile(cut.tile, [&](auto cf) {
     typedef decltype(cf) CF;
     const int mb = static_cast<int>(blocks(A.rows, CF::BM));
     const int nb = static_cast<int>(blocks(B.rows, CF::BN));
-    product_kernel<CF, F, float, true>
-        <<<dim3(static_cast<uint32_t>(mb) * nb, slices), CF::NT, 0, s>>>(
-            A, B, ksteps, mb, nb, false, pitch, nullptr, 0, sums);
+    const uint32_t tiles = triangle ? static_cast<uint32_t>(mb) * (mb + 1) / 2
+                                    : static_cast<uint32_t>(mb) * nb;
+    product_kernel<CF, F, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
+        A, B, ksteps, mb, triangle ? 0 : nb, false, pitch, nullptr, 0, sums);
     return hipGetLastError();
   });
 }
@@ -313,21 +320,23 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
     const int next = exponent_below(bound);
     // factors with the powers of two of what goes in undone and of what comes out applied
     const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
-    hipError_t e = product<X>(xo, xo, p.ldn / 64, p.gram_slices, p.ldm, p.sums, s);
+    hipError_t e = product<X>(xo, xo, p.ldn / 64, p.gram, true, p.ldm, p.sums, s);
     if (e != hipSuccess) return e;
-    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.gram_slices, p.ldm, 0.f,
+    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.gram.slices,
+                                                          tile_rows(p.gram.tile), p.ldm, 0.f,
                                                  factor(1, eg - 2 * ex), none, g, no_output, false);
-    if ((e = product<kHalves>(go, go, p.ldm / 64, p.square_slices, p.ldm, p.sums, s)) != hipSuccess)
+    if ((e = product<kHalves>(go, go, p.ldm / 64, p.square, true, p.ldm, p.sums, s)) != hipSuccess)
       return e;
-    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.square_slices, p.ldm,
+    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.square.slices,
+                                                          tile_rows(p.square.tile), p.ldm,
                                                  factor(a.b, eb - eg), factor(a.c, eb - 2 * eg), g,
                                                  b, no_output, false);
-    if ((e = product<X == kHalf ? kMixed : kHalves>(xt, bo, p.ldm / 64, p.update_slices, p.ldn, p.sums, s)) != hipSuccess)
+    if ((e = product<X == kHalf ? kMixed : kHalves>(xt, bo, p.ldm / 64, p.update, false, p.ldn, p.sums, s)) != hipSuccess)
       return e;
     const double scale = end ? a.scale : 1.0;
     const int out = end ? 0 : next;
     orth_finish_kernel<E, X><<<whole, 256, 0, s>>>(
-        p.sums, p.update_slices, p.ldn, factor(scale * a.a, out - ex), factor(scale, out - eb - ex),
+        p.sums, p.update.slices, 0, p.ldn, factor(scale * a.a, out - ex), factor(scale, out - eb - ex),
         x, x, end ? static_cast<E*>(a.out) : no_output, tall);
     ex = next;
   }
