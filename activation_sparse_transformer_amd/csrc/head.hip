@@ -14,8 +14,8 @@
 // is of the size of dx's and dw's own.  With float32 ones every operand is two
 // half-precision parts (nt_gemm.h), w scaled by its largest element, x by each row's;
 // dl / g lies in [-1, 1] and is scaled by 2^14, with g taken into dx at the end and
-// into the x of dw.  Every product is K-major on both sides: w and x are transposed
-// once, dl is written both ways.
+// into the x of dw.  Both products read w, x and dl as they lie, turning fragments with
+// LDS transpose reads where K runs along a column.
 #include <algorithm>
 
 #include "nt_gemm.h"
@@ -100,19 +100,30 @@ __device__ __forceinline__ float wave_max(float m) {
 __global__ void head_clear_kernel(float* amax) { amax[threadIdx.x] = 0.f; }
 
 // *amax = max(*amax, the largest finite magnitude of src): an order-free atomic on the
-// bits of non-negative floats.
+// bits of non-negative floats.  4 runs a lane, one workgroup after another.
+constexpr int kAmaxRuns = 4 * 256;
 __global__ __launch_bounds__(256) void head_amax_kernel(const float* __restrict__ src,
                                                         int64_t runs, float* amax) {
-  float m = 0.f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < runs;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    float v[8];
-    load_run(src + i * 8, v);
+  __shared__ float lds[4];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kAmaxRuns + threadIdx.x;
+  float v[4][8] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
-  }
+  for (int u = 0; u < 4; ++u)
+    if (i0 + u * 256 < runs) load_run(src + (i0 + u * 256) * 8, v[u]);
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max_finite(m, v[u][k]);
   m = wave_max(m);
-  if (lane_id() == 0) atomicMax(reinterpret_cast<int*>(amax), __float_as_int(m));
+  if (lane_id() == 0) lds[threadIdx.x / kWave] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    m = fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+    // most workgroups find a larger one there already
+    if (m > __hip_atomic_load(amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+      atomicMax(reinterpret_cast<int*>(amax), __float_as_int(m));
+  }
 }
 
 // parts [rows][ld] of a piece of w, src [rows][d], scaled by *amax (halves); columns
@@ -174,49 +185,29 @@ __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
   }
 }
 
-// parts [d][ld] of the transpose of src [rows][d]; rows past the end are zeros.
-// Halves: scaled by *amax.  X: src is x, and rows without a target are zeros (whatever
-// x holds there meets gradients of zero, and a NaN must not spread); in halves the rows
-// are scale * dlogp * x.
-template <typename E, bool X>
-__global__ __launch_bounds__(256) void head_transpose_kernel(HeadArgs a, const E* __restrict__ src,
-                                                             int rows, int ld,
-                                                             const float* __restrict__ dlogp,
-                                                             const float* amax,
-                                                             uint16_t* __restrict__ out) {
-  __shared__ float tile[64][65];
-  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-  float f = 1.f;
-  if constexpr (form_of<E>() == kHalves) f = power_of_two(exponent_for(*amax));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int run = threadIdx.x + 256 * i;
-    const int r = run / 8, c = run % 8 * 8;
-    bool live = r0 + r < rows && c0 + c < a.d;
-    if (X && live) live = has_target(a.targets, a.index_bytes, a.vocab, r0 + r);
-    float v[8] = {};
-    if (live) {
-      load_run(src + static_cast<int64_t>(r0 + r) * a.d + c0 + c, v);
-      if constexpr (form_of<E>() == kHalves) {
-        const float g = X ? dlogp[r0 + r] * a.scale : 1.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) tile[r][c + k] = v[k];
+// parts [lines][ld] of dw's x, a wave a row: rows without a target, and past the end, are
+// zeros (whatever x holds there meets gradients of zero, and a NaN must not spread).
+// Halves: scale * dlogp * x, scaled by *amax.
+template <typename E>
+__global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, int64_t lines, int ld,
+                                                      const float* __restrict__ dlogp,
+                                                      const float* amax,
+                                                      uint16_t* __restrict__ out) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  if (row >= lines) return;
+  const bool live = row < a.n_rows && has_target(a.targets, a.index_bytes, a.vocab, row);
+  const E* src = static_cast<const E*>(a.x) + row * a.d;
+  float f = 1.f, g = 1.f;
+  if constexpr (form_of<E>() == kHalves) {
+    f = power_of_two(exponent_for(*amax));
+    if (live) g = dlogp[row] * a.scale;
   }
-  __syncthreads();
+  for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
+    float v[8] = {};
+    if (live && c < a.d) load_run(src + c, v);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int run = threadIdx.x + 256 * i;
-    const int c = run / 8, r = run % 8 * 8;
-    if (c0 + c >= a.d) continue;  // r0 + 64 <= ld
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = tile[r + k][c];
-    put_run<form_of<E>()>(out + static_cast<int64_t>(c0 + c) * ld,
-                          static_cast<int64_t>(a.d) * ld, r0 + r, v);
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
+    put_run<form_of<E>()>(out + row * ld, lines * ld, c, v);
   }
 }
 
@@ -369,9 +360,8 @@ struct DlArgs {
   int index_bytes;
   const float2* stats;
   const float* dlogp;
-  uint16_t* dl;    // [parts][n][ldv]
-  uint16_t* dlt;   // [parts][piece][ldn]
-  int ldv, ldn;
+  uint16_t* dl;  // [parts][n][ldv]
+  int ldv;
 };
 
 template <class CF, Form F>
@@ -420,12 +410,6 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
             *reinterpret_cast<uint2*>(a.dl + (p * n_rows + n) * a.ldv + v) =
                 make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
                            part[2][p] | static_cast<uint32_t>(part[3][p]) << 16);
-          if (n < a.ldn) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (v + k < a.w.rows)
-                a.dlt[(static_cast<int64_t>(p) * a.w.rows + v + k) * a.ldn + n] = part[k][p];
-          }
         }
       }
   }
@@ -525,7 +509,7 @@ struct BackwardPlan {
   int piece, ldn;
   Tile dl_tile;
   Cut dx_cut;
-  uint16_t *xp, *wp, *xt, *wt, *dl, *dlt;
+  uint16_t *xp, *wp, *gx, *dl;
   float *amax, *undo, *sums;
   size_t bytes;
 };
@@ -534,7 +518,7 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const size_t P = part_count(elem_bytes), ld = up64(a.d), n = a.n_rows;
   const bool in_place = direct(elem_bytes, a.d);
   p.ldn = static_cast<int>(up64(n));
-  const size_t per_column = 2 * P * (n + p.ldn + a.d + (in_place ? 0 : ld));
+  const size_t per_column = 2 * P * (n + (in_place ? 0 : ld));
   p.piece = piece_of(a.vocab, per_column, size_t{192} << 20);
   const size_t ldv = up64(p.piece);
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
@@ -542,10 +526,8 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.dx_cut = cut_for(a.d, n, ldv / 64 * products, 32, false);
   p.dl_tile = cut_for(p.piece, n, stages(a, elem_bytes), 1, false).tile;
   Carve c{static_cast<char*>(ws)};
-  p.xt = c.take<uint16_t>(P * a.d * p.ldn);
-  p.wt = c.take<uint16_t>(P * a.d * ldv);
+  p.gx = c.take<uint16_t>(P * p.ldn * ld);
   p.dl = c.take<uint16_t>(P * n * ldv);
-  p.dlt = c.take<uint16_t>(P * p.piece * p.ldn);
   p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
   if (!in_place) {
     p.amax = c.take<float>(kAmax);
@@ -566,16 +548,16 @@ template <typename E>
 Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* undo, uint16_t* xp,
                   hipStream_t s) {
   const int n = static_cast<int>(a.n_rows), ld = columns(a);
-  if (direct(sizeof(E), a.d)) return Operand{static_cast<const uint16_t*>(a.x), 0, a.d, n};
+  if (direct(sizeof(E), a.d)) return Operand{static_cast<const uint16_t*>(a.x), 0, a.d, n, 0};
   if constexpr (form_of<E>() == kHalves) {
     head_clear_kernel<<<1, kAmax, 0, s>>>(amax);
     const int64_t runs = static_cast<int64_t>(a.vocab) * a.d / 8;
-    head_amax_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(runs, 1024), 2048)), 256, 0,
-                       s>>>(static_cast<const float*>(a.w), runs, amax);
+    head_amax_kernel<<<static_cast<uint32_t>(blocks(runs, kAmaxRuns)), 256, 0, s>>>(
+        static_cast<const float*>(a.w), runs, amax);
   }
   head_x_kernel<E><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo,
                                                                       amax + 1, xp);
-  return Operand{xp, a.n_rows * ld, ld, n};
+  return Operand{xp, a.n_rows * ld, ld, n, 0};
 }
 
 // The operand of columns [v0, v0 + rows) of the vocabulary.
@@ -584,18 +566,10 @@ Operand w_operand(const HeadArgs& a, int64_t v0, int rows, const float* amax, ui
                   hipStream_t s) {
   const E* src = static_cast<const E*>(a.w) + v0 * a.d;
   const int ld = columns(a);
-  if (direct(sizeof(E), a.d)) return Operand{reinterpret_cast<const uint16_t*>(src), 0, a.d, rows};
+  if (direct(sizeof(E), a.d)) return Operand{reinterpret_cast<const uint16_t*>(src), 0, a.d, rows, 0};
   head_w_kernel<E><<<static_cast<uint32_t>(blocks(static_cast<int64_t>(rows) * (ld / 8), 256)), 256,
                      0, s>>>(src, rows, a.d, ld, amax, wp);
-  return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows};
-}
-
-template <typename E, bool X>
-void transpose(const HeadArgs& a, const E* src, int rows, const float* dlogp, const float* amax,
-               uint16_t* out, hipStream_t s) {
-  const int ld = static_cast<int>(up64(rows));
-  head_transpose_kernel<E, X><<<dim3(ld / 64, static_cast<uint32_t>(blocks(a.d, 64))), 256, 0, s>>>(
-      a, src, rows, ld, dlogp, amax, out);
+  return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows, 0};
 }
 
 template <typename E>
@@ -640,34 +614,33 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
   const float* const amax_w = F == kHalves ? p.amax : nullptr;
   const float* const amax_x = F == kHalves ? p.amax + 1 : nullptr;
   const Operand x = x_operand<E>(a, dlogp, p.amax, p.undo, p.xp, s);
-  transpose<E, true>(a, static_cast<const E*>(a.x), n, dlogp, amax_x, p.xt, s);
-  const Operand xt{p.xt, static_cast<int64_t>(a.d) * p.ldn, p.ldn, a.d};
+  const int ld = columns(a);
+  head_gx_kernel<E><<<static_cast<uint32_t>(blocks(p.ldn, 4)), 256, 0, s>>>(a, p.ldn, ld, dlogp,
+                                                                           amax_x, p.gx);
+  const Operand gx{p.gx, static_cast<int64_t>(p.ldn) * ld, ld, a.d, p.ldn};
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const int ldv = static_cast<int>(up64(rows));
     const Operand w = w_operand<E>(a, v0, rows, amax_w, p.wp, s);
-    transpose<E, false>(a, static_cast<const E*>(a.w) + v0 * a.d, rows, nullptr, amax_w, p.wt, s);
     const DlArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, amax_w, p.undo,
-                   a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
-                   p.dlt, ldv, p.ldn};
+                   a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl, ldv};
     hipError_t e = with_tile(p.dl_tile, [&](auto cf) {
       typedef decltype(cf) CF;
-      // ldn columns of dlt are written, of them the last as zeros
-      const int mb = static_cast<int>(blocks(rows, CF::BM));
-      const int nb = static_cast<int>(blocks(p.ldn, CF::BN));
+      const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       head_dl_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const Operand wt{p.wt, static_cast<int64_t>(a.d) * ldv, ldv, a.d};
-    const Operand dl{p.dl, static_cast<int64_t>(n) * ldv, ldv, n};
-    const Operand dlt{p.dlt, static_cast<int64_t>(rows) * p.ldn, p.ldn, rows};
+    // dx: K is the vocabulary, along w's columns; dw: K is the rows, along dl's and gx's
+    const Operand wt{w.p, w.part, w.ld, a.d, rows};
+    const Operand dl{p.dl, static_cast<int64_t>(n) * ldv, ldv, n, 0};
+    const Operand dlt{p.dl, static_cast<int64_t>(n) * ldv, ldv, ldv, n};
     e = with_tile(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      product_kernel<CF, F, float, true>
+      product_kernel<CF, F, true, false, float, true>
           <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
-              wt, dl, ldv / 64, mb, nb, v0 > 0, a.d, nullptr, 0, p.sums);
+              wt, dl, ldv / 64, mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -676,8 +649,8 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      product_kernel<CF, F, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
-          xt, dlt, p.ldn / 64, mb, nb, false, a.d, amax_x, -kDlExponent,
+      product_kernel<CF, F, true, true, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+          gx, dlt, p.ldn / 64, mb, nb, rows, false, a.d, amax_x, -kDlExponent,
           static_cast<E*>(dw) + v0 * a.d);
       return hipGetLastError();
     });

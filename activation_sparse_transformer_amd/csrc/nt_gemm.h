@@ -1,4 +1,4 @@
-// Products C = A B^T of K-major operands on MFMA (32x32x16).  An operand is held in
+// Products C = A B^T on MFMA (32x32x16).  An operand is held in
 // one of three forms:
 //  - kBf16:    one bfloat16 part, as bfloat16 tensors are;
 //  - kHalves:  two half-precision parts hi + lo of a float32 value times a power of
@@ -15,9 +15,11 @@
 //  - kHalf:    the hi part alone, within 2^-11 of v.
 // A product's form is that of both operands, or kMixed: A in kHalf, B in kHalves.
 //
-// Operands are [parts][rows][ld], ld a multiple of 64 with zeros past the
-// contraction's length; rows past the end read the last row and feed outputs
-// that no epilogue stores.
+// Operands are [parts][rows][ld], K along a row: ld a multiple of 64 with zeros past
+// the contraction's length; rows past the end read the last row and feed outputs that
+// no epilogue stores.  Or turned, [parts][depth][ld] with K along the column: rows (a
+// multiple of 8) are then columns of that, and K past `depth` reads its last line, for
+// which the other operand holds zeros.
 #pragma once
 
 #include <algorithm>
@@ -36,8 +38,9 @@ constexpr int products_of(Form f) { return f == kHalves ? 3 : f == kMixed ? 2 : 
 struct Operand {
   const uint16_t* p;
   int64_t part;  // elements between parts
-  int64_t ld;    // elements between rows
+  int64_t ld;    // elements between rows (turned: between steps of K)
   int rows;
+  int depth;     // turned: K
 };
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
@@ -63,27 +66,110 @@ struct Config {
   static_assert(FM * 32 == WTM && FN * 32 == WTN, "32x32 blocks");
 };
 
-// Copies of one operand: instruction i of a wave fills 1 KB = 8 rows; lane l
-// fetches the chunk that belongs at LDS position l.
-template <int ISSUE, int NW>
-__device__ __forceinline__ void sources(const Operand& o, int r0, int k0,
-                                        const uint16_t* (&src)[ISSUE]) {
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+// Copies of one operand to a stage: instruction i of a wave fills 1 KB; lane l fetches
+// the chunk that belongs at LDS position l.  SIZE: the block's rows.
+template <int SIZE, int NW, bool TURNED>
+struct Copies;
+
+template <int SIZE, int NW>
+struct Copies<SIZE, NW, false> {  // 8 rows of 64 elements each
+  static constexpr int ISSUE = SIZE / (8 * NW);
+  const uint16_t* src[ISSUE];
+  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0) {
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
 #pragma unroll
-  for (int i = 0; i < ISSUE; ++i) {
-    const int r = (wave + NW * i) * 8 + lane / 8;
-    const int kc = (lane & 7) ^ swizzle(r);
-    src[i] = o.p + static_cast<int64_t>(min(r0 + r, o.rows - 1)) * o.ld + k0 + kc * 8;
+    for (int i = 0; i < ISSUE; ++i) {
+      const int r = (wave + NW * i) * 8 + lane / 8;
+      const int kc = (lane & 7) ^ swizzle(r);
+      src[i] = o.p + static_cast<int64_t>(min(r0 + r, o.rows - 1)) * o.ld + k0 + kc * 8;
+    }
   }
-}
-template <int ISSUE, int NW>
-__device__ __forceinline__ void issue(const uint16_t* const* src, int64_t offset,
-                                      uint16_t* tile) {
-  const int wave = threadIdx.x / kWave;
+  __device__ __forceinline__ void issue(int k, int64_t part, uint16_t* tile) const {
+    const int wave = threadIdx.x / kWave;
 #pragma unroll
-  for (int i = 0; i < ISSUE; ++i)
-    __builtin_amdgcn_global_load_lds(src[i] + offset, tile + (wave + NW * i) * 512, 16, 0, 0);
+    for (int i = 0; i < ISSUE; ++i)
+      __builtin_amdgcn_global_load_lds(src[i] + part + k, tile + (wave + NW * i) * 512, 16, 0, 0);
+  }
+};
+
+// A turned operand's stage: 64 lines (k) of SIZE elements, the 32-byte chunk c of line k
+// at position c ^ turned_swizzle(k): the 4 lines x 32 bytes that 16 lanes of a transpose
+// read take fall on distinct banks.
+__device__ __forceinline__ int turned_swizzle(int k) { return (k & 3) ^ ((k >> 1) & 4); }
+template <int SIZE>
+__device__ __forceinline__ int turned_offset(int k, int r) {
+  return k * SIZE + ((((r >> 4) ^ turned_swizzle(k)) & (SIZE / 16 - 1)) << 4) + (r & 15);
 }
+
+template <int SIZE, int NW>
+struct Copies<SIZE, NW, true> {  // 512 / SIZE lines each
+  static constexpr int ISSUE = SIZE / (8 * NW);
+  const uint16_t* src[ISSUE];
+  int line[ISSUE];
+  int64_t ld;
+  int last;
+  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0) {
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    ld = o.ld;
+    last = o.depth - 1;
+#pragma unroll
+    for (int i = 0; i < ISSUE; ++i) {
+      const int k = (wave + NW * i) * (512 / SIZE) + lane * 8 / SIZE;
+      const int at = lane * 8 % SIZE;
+      const int r = (((at >> 4) ^ turned_swizzle(k)) & (SIZE / 16 - 1)) * 16 + (at & 15);
+      src[i] = o.p + min(r0 + r, o.rows - 8);
+      line[i] = k0 + k;
+    }
+  }
+  __device__ __forceinline__ void issue(int k, int64_t part, uint16_t* tile) const {
+    const int wave = threadIdx.x / kWave;
+#pragma unroll
+    for (int i = 0; i < ISSUE; ++i)
+      __builtin_amdgcn_global_load_lds(src[i] + part + min(line[i] + k, last) * ld,
+                                       tile + (wave + NW * i) * 512, 16, 0, 0);
+  }
+};
+
+// The fragments of a wave's blocks of 32 rows from row r0 of a stage: 16-wide K step ks.
+template <int SIZE, int BLOCKS, bool TURNED>
+struct Reader;
+
+template <int SIZE, int BLOCKS>
+struct Reader<SIZE, BLOCKS, false> {
+  int row;
+  __device__ __forceinline__ explicit Reader(int r0) : row(r0 + (lane_id() & 31)) {}
+  __device__ __forceinline__ i32x4_t read(const uint16_t* tile, int i, int ks) const {
+    return *reinterpret_cast<const i32x4_t*>(
+        tile + tile_offset(row + i * 32, ks * 2 + (lane_id() >> 5)));
+  }
+};
+
+template <int SIZE, int BLOCKS>
+struct Reader<SIZE, BLOCKS, true> {
+  // lanes 16 h + L of a half hold rows 16 h + L; a transpose read of 16 lanes takes lines
+  // k .. k + 3 of 16 rows, lane L pointing at line k + L / 4, row 4 (L % 4)
+  int at[BLOCKS];
+  __device__ __forceinline__ explicit Reader(int r0) {
+    const int l = lane_id(), L = l & 15;
+    const int k = (l >> 5) * 8 + L / 4;
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i)
+      at[i] = turned_offset<SIZE>(k, r0 + i * 32 + ((l >> 4) & 1) * 16 + 4 * (L & 3));
+  }
+  __device__ __forceinline__ i32x4_t read(const uint16_t* tile, int i, int ks) const {
+    typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4_t;
+    typedef __attribute__((address_space(3))) s16x4_t lds_v4;
+    typedef __attribute__((address_space(3))) uint16_t lds_u16;
+    // 4 and 16 lines on, the swizzle is the same
+    const uint16_t* p = tile + at[i] + ks * 16 * SIZE;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_u16*)(p)));
+    const s16x4_t hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_u16*)(p + 4 * SIZE)));
+    typedef __attribute__((ext_vector_type(2))) int i32x2_t;
+    const i32x2_t a = __builtin_bit_cast(i32x2_t, lo), b = __builtin_bit_cast(i32x2_t, hi);
+    return i32x4_t{a[0], a[1], b[0], b[1]};
+  }
+};
 
 // The steps of a contraction: a product of parts after another, each over the whole
 // of K, in the order lo hi (kHalves), hi lo, hi hi.
@@ -99,11 +185,9 @@ struct Walk {
       --left;
     }
   }
-  __device__ __forceinline__ int64_t a() const {
-    return F == kHalves && left == 2 ? part_a + k : k;
-  }
+  __device__ __forceinline__ int64_t a() const { return F == kHalves && left == 2 ? part_a : 0; }
   __device__ __forceinline__ int64_t b() const {
-    return products_of(F) > 1 && left == 1 ? part_b + k : k;
+    return products_of(F) > 1 && left == 1 ? part_b : 0;
   }
 };
 
@@ -127,7 +211,7 @@ __device__ __forceinline__ void meet() {
 
 // acc = A[m0 .., k0 .. k0 + 64 ksteps) B[n0 .., the same]^T.  `lds`: STAGES stages.
 // Copies run STAGES - 1 stages ahead of the products.
-template <class CF, Form F>
+template <class CF, Form F, bool TA, bool TB>
 __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand& B, int n0, int k0,
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
@@ -137,20 +221,19 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
     for (int j = 0; j < CF::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const uint16_t* asrc[CF::A_ISSUE];
-  const uint16_t* bsrc[CF::B_ISSUE];
-  sources<CF::A_ISSUE, CF::NW>(A, m0, k0, asrc);
-  sources<CF::B_ISSUE, CF::NW>(B, n0, k0, bsrc);
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
-  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+  const Copies<CF::BM, CF::NW, TA> a_copies(A, m0, k0);
+  const Copies<CF::BN, CF::NW, TB> b_copies(B, n0, k0);
+  const int wave = threadIdx.x / kWave;
+  const Reader<CF::BM, CF::FM, TA> a_reader(wave / CF::WAVES_N * CF::WTM);
+  const Reader<CF::BN, CF::FN, TB> b_reader(wave % CF::WAVES_N * CF::WTN);
   constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
   const int steps = ksteps * products_of(F);
   Walk<F> walk{A.part, B.part, ksteps * kStep};
   int fill = 0;  // the stage that the next copies go to
   auto copy = [&]() {
     uint16_t* stage = lds + fill * CF::STAGE;
-    issue<CF::A_ISSUE, CF::NW>(asrc, walk.a(), stage);
-    issue<CF::B_ISSUE, CF::NW>(bsrc, walk.b(), stage + CF::BM * kStep);
+    a_copies.issue(walk.k, walk.a(), stage);
+    b_copies.issue(walk.k, walk.b(), stage + CF::BM * kStep);
     walk.next();
     fill = fill + 1 == CF::STAGES ? 0 : fill + 1;
   };
@@ -165,21 +248,15 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
     const uint16_t* sB = sA + CF::BM * kStep;
 #pragma unroll
     for (int ks = 0; ks < kStep / 16; ++ks) {
-      const int kc = ks * 2 + (lane >> 5);
       i32x4_t a[CF::FM], b[CF::FN];
 #pragma unroll
-      for (int i = 0; i < CF::FM; ++i)
-        a[i] = *reinterpret_cast<const i32x4_t*>(
-            sA + tile_offset(wm * CF::WTM + i * 32 + (lane & 31), kc));
+      for (int i = 0; i < CF::FM; ++i) a[i] = a_reader.read(sA, i, ks);
 #pragma unroll
-      for (int j = 0; j < CF::FN; ++j)
-        b[j] = *reinterpret_cast<const i32x4_t*>(
-            sB + tile_offset(wn * CF::WTN + j * 32 + (lane & 31), kc));
+      for (int j = 0; j < CF::FN; ++j) b[j] = b_reader.read(sB, j, ks);
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < CF::FN; ++j)
-          acc[i][j] = mfma<F>(a[i], b[j], acc[i][j]);
+        for (int j = 0; j < CF::FN; ++j) acc[i][j] = mfma<F>(a[i], b[j], acc[i][j]);
     }
     cur = cur + 1 == CF::STAGES ? 0 : cur + 1;
   }
@@ -261,10 +338,8 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   const int steps = ksteps * products_of(F);
   if (steps == 0) return;
   settle(acc);
-  const uint16_t* asrc[CF::A_ISSUE];
-  const uint16_t* bsrc[CF::B_ISSUE];
-  sources<CF::A_ISSUE, CF::NW>(A, m0, k0, asrc);
-  sources<CF::B_ISSUE, CF::NW>(B, n0, k0, bsrc);
+  const Copies<CF::BM, CF::NW, false> a_copies(A, m0, k0);
+  const Copies<CF::BN, CF::NW, false> b_copies(B, n0, k0);
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
   typedef __attribute__((address_space(3))) uint16_t lds_u16;
@@ -284,8 +359,8 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   Walk<F> walk{A.part, B.part, ksteps * kStep};
   auto copy = [&](int stage) {
     uint16_t* to = lds + stage * CF::STAGE;
-    issue<CF::A_ISSUE, CF::NW>(asrc, walk.a(), to);
-    issue<CF::B_ISSUE, CF::NW>(bsrc, walk.b(), to + CF::BM * kStep);
+    a_copies.issue(walk.k, walk.a(), to);
+    b_copies.issue(walk.k, walk.b(), to + CF::BM * kStep);
     walk.next();
   };
   Fragments f0, f1;
@@ -318,12 +393,14 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   __syncthreads();  // the stages are free for the epilogue
 }
 
-template <class CF, Form F>
+template <class CF, Form F, bool TA = false, bool TB = false>
 __device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand& B, int n0, int k0,
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
-  if constexpr (CF::FM == 2 && CF::FN == 4) mainloop_pipe<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
-  else mainloop<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
+  if constexpr (CF::FM == 2 && CF::FN == 4 && !TA && !TB)
+    mainloop_pipe<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
+  else
+    mainloop<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
 }
 
 // Element (i, r) of a lane's accumulators is row block_row<CF>() + row_of(i, r),
@@ -390,16 +467,16 @@ __device__ __forceinline__ int exponent_for(float m) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return ldexpf(1.f, e); }
 
-// out[col][row] (+)= A[row] . B[col] over one slice of K per blockIdx.y, lines of
+// out[col][row] (+)= A[row] . B[col], col < cols, over one slice of K per blockIdx.y, lines of
 // `pitch` elements (a multiple of 8, not under A.rows; what lies past A.rows is
 // undefined): as floats (ACC: slice after slice in out, added to where `add`) or as E.
 // Times 2^(exponent - exponent_for(*amax)) where amax is given.  n_blocks == 0: C is
 // symmetric, and only the tiles of m_blocks x m_blocks with rows up to the columns' are
 // formed.
-template <class CF, Form F, typename E, bool ACC>
+template <class CF, Form F, bool TA, bool TB, typename E, bool ACC>
 __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, int ksteps,
-                                                         int m_blocks, int n_blocks, bool add,
-                                                         int pitch, const float* amax,
+                                                         int m_blocks, int n_blocks, int cols,
+                                                         bool add, int pitch, const float* amax,
                                                          int exponent, E* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
@@ -410,9 +487,9 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
-  multiply<CF, F>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
+  multiply<CF, F, TA, TB>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
   const int row0 = mb * CF::BM + block_row<CF>();
-  if (ACC) out += static_cast<int64_t>(slice) * pitch * B.rows;
+  if (ACC) out += static_cast<int64_t>(slice) * pitch * cols;
   if (amax != nullptr) {
     const float f = power_of_two(exponent - exponent_for(*amax));
 #pragma unroll
@@ -425,7 +502,7 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
 #pragma unroll
   for (int j = 0; j < CF::FN; ++j) {
     const int col = nb * CF::BN + block_col<CF>() + 32 * j;
-    if (col >= B.rows) continue;
+    if (col >= cols) continue;
     E* line = out + static_cast<int64_t>(col) * pitch;
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)

@@ -255,8 +255,8 @@ hipError_t product(const Operand& A, const Operand& B, int ksteps, const Cut& cu
     const int nb = static_cast<int>(blocks(B.rows, CF::BN));
     const uint32_t tiles = triangle ? static_cast<uint32_t>(mb) * (mb + 1) / 2
                                     : static_cast<uint32_t>(mb) * nb;
-    product_kernel<CF, F, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
-        A, B, ksteps, mb, triangle ? 0 : nb, false, pitch, nullptr, 0, sums);
+    product_kernel<CF, F, false, false, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
+        A, B, ksteps, mb, triangle ? 0 : nb, B.rows, false, pitch, nullptr, 0, sums);
     return hipGetLastError();
   });
 }
@@ -306,10 +306,10 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   double bound = 1.0;  // of X's singular values
   int ex = exponent_below(bound);
   orth_start_kernel<E, X><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
-  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m};
-  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n};
-  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
-  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m};
+  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m, 0};
+  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n, 0};
+  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, 0};
+  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, 0};
   E* no_output = nullptr;
   for (int i = 0; i < a.steps; ++i) {
     const bool end = i + 1 == a.steps;
