@@ -244,6 +244,7 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
   const int row0 = mb * CF::BM + nt::block_row<CF>();
   const int half = lane_id() >> 5;
   const int wave_row = row0 - 4 * half;  // the wave's first row
+  const bool full = (mb + 1) * CF::BM <= a.w.rows;
   float2* joint = reinterpret_cast<float2*>(lds);  // [WAVES_M][BN]
   const int wm = threadIdx.x / kWave / CF::WAVES_N;
 #pragma unroll
@@ -256,18 +257,17 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        acc[i][j][r] *= f;
-        if (row0 + nt::row_of(i, r) < a.w.rows) m = fmaxf(m, acc[i][j][r]);
+        if (!full && row0 + nt::row_of(i, r) >= a.w.rows) acc[i][j][r] = -INFINITY;
+        m = fmaxf(m, acc[i][j][r]);
       }
-    m = fmaxf(m, other_half(m));
+    m = fmaxf(m, other_half(m)) * f;
     const float base = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        if (row0 + nt::row_of(i, r) < a.w.rows)
-          s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
+        s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -base) * kLog2e);
     s += other_half(s);
     if (half == 0) joint[wm * CF::BN + col] = make_float2(m, s);
     // the target's z, where this wave's rows hold it
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (rel == nt::row_of(i, r)) z = acc[i][j][r];
-      if (mine) a.target_z[n] = z;
+      if (mine) a.target_z[n] = z * f;
     }
   }
   __syncthreads();
@@ -350,6 +350,24 @@ __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict
 }
 
 // ---------------------------------------------------------------- gradient
+// Part p of two values, packed.
+template <Form F>
+__device__ __forceinline__ uint32_t pack_part(float a, float b, int p) {
+  if constexpr (F == kBf16) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+  } else {
+    _Float16 x = static_cast<_Float16>(a), y = static_cast<_Float16>(b);
+    if (p == 1) {  // what the first part leaves; |a| is at most 2^14, or NaN
+      x = static_cast<_Float16>(a == a ? a - static_cast<float>(x) : 0.f);
+      y = static_cast<_Float16>(b == b ? b - static_cast<float>(y) : 0.f);
+    }
+    return __builtin_bit_cast(uint16_t, x) |
+           static_cast<uint32_t>(__builtin_bit_cast(uint16_t, y)) << 16;
+  }
+}
+
 struct DlArgs {
   Operand w, x;
   int v0, vocab;
@@ -372,46 +390,77 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   f32x16_t acc[CF::FM][CF::FN];
   nt::multiply<CF, F>(a.w, mb * CF::BM, a.x, nb * CF::BN, 0, a.ksteps, lds, acc);
   const int row0 = mb * CF::BM + nt::block_row<CF>();
+  const int half = lane_id() >> 5;
+  const int wave_row = row0 - 4 * half;  // the wave's first row
+  const bool full = (mb + 1) * CF::BM <= a.w.rows;
   const int64_t n_rows = a.x.rows;
 #pragma unroll
   for (int j = 0; j < CF::FN; ++j) {
     const int n = nb * CF::BN + nt::block_col<CF>() + 32 * j;
-    float g = 0.f, m = 0.f, inv = 0.f;
     const float f = z_factor<F>(a, n);
-    int t = -1;  // of the piece
+    float g = 0.f, m = 0.f, share = 0.f;  // share = -g / sum
+    int t = -1;  // the target, of the wave's rows
     bool given = false;
     if (n < n_rows) {
       const int64_t target = target_of(a.targets, a.index_bytes, n);
       const float2 st = a.stats[n];
       given = target >= 0 && target < a.vocab && !(st.x == -INFINITY && st.y == 0.f);
       if (given) {
-        t = static_cast<int>(target) - a.v0;
+        t = static_cast<int>(target) - a.v0 - wave_row;
         g = F == kBf16 ? a.dlogp[n] * a.scale : power_of_two(kDlExponent);
         m = st.x;
-        inv = 1.f / st.y;
+        share = -g / st.y;
       }
     }
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int v = row0 + nt::row_of(i, 4 * q);
-        uint16_t part[4][parts_of(F)];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float z = acc[i][j][4 * q + k] * f;
-          const float p = __builtin_amdgcn_exp2f((z - m) * kLog2e) * inv;
-          const float d = given && v + k < a.w.rows ? g * ((v + k == t ? 1.f : 0.f) - p) : 0.f;
-          nt::split<F>(d, part[k]);
-        }
-#pragma unroll
-        for (int p = 0; p < parts_of(F); ++p) {
-          if (n < n_rows && v < a.ldv)
-            *reinterpret_cast<uint2*>(a.dl + (p * n_rows + n) * a.ldv + v) =
-                make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
-                           part[2][p] | static_cast<uint32_t>(part[3][p]) << 16);
-        }
+      for (int r = 0; r < 16; ++r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -m) * kLog2e);
+        acc[i][j][r] = given && (full || row0 + nt::row_of(i, r) < a.w.rows) ? share * e : 0.f;
       }
+    const bool mine = t >= 0 && t < CF::WTM && wave_row + t < a.w.rows && ((t >> 2) & 1) == half;
+    if (wave_ballot(mine) != 0) {
+      const int rel = mine ? t - 4 * half : -1;
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (rel == nt::row_of(i, r)) acc[i][j][r] += g;
+    }
+  }
+  // a part at a time through LDS, so that its rows are stored whole: the 16-byte chunk c
+  // of row n at position c ^ n, which spreads the 32 rows of a write over the banks
+  constexpr int CHUNKS = CF::BM / 8;
+  static_assert(CF::BM * CF::BN <= CF::STAGES * CF::STAGE, "the tile fits the stages");
+#pragma unroll
+  for (int p = 0; p < parts_of(F); ++p) {
+    if (p > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < CF::FN; ++j) {
+      const int col = nt::block_col<CF>() + 32 * j;
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = nt::block_row<CF>() + nt::row_of(i, 4 * q);
+          uint32_t w[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            w[k] = pack_part<F>(acc[i][j][4 * q + 2 * k], acc[i][j][4 * q + 2 * k + 1], p);
+          *reinterpret_cast<uint2*>(lds + col * CF::BM + (((row >> 3) ^ col) & (CHUNKS - 1)) * 8 +
+                                    (row & 7)) = make_uint2(w[0], w[1]);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < CF::BN * CHUNKS; e += CF::NT) {
+      const int col = e / CHUNKS, c = e % CHUNKS;
+      const int64_t n = nb * CF::BN + col;
+      const int v = mb * CF::BM + c * 8;
+      if (n < n_rows && v < a.ldv)
+        *reinterpret_cast<uint4*>(a.dl + (p * n_rows + n) * a.ldv + v) =
+            *reinterpret_cast<const uint4*>(lds + col * CF::BM + ((c ^ col) & (CHUNKS - 1)) * 8);
+    }
   }
 }
 
