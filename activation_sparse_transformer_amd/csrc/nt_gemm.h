@@ -130,46 +130,70 @@ struct Copies<SIZE, NW, true> {  // 512 / SIZE lines each
   }
 };
 
-// The fragments of a wave's blocks of 32 rows from row r0 of a stage: 16-wide K step ks.
-template <int SIZE, int BLOCKS, bool TURNED>
-struct Reader;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u16*)p));
+}
 
-template <int SIZE, int BLOCKS>
-struct Reader<SIZE, BLOCKS, false> {
-  int row;
-  __device__ __forceinline__ explicit Reader(int r0) : row(r0 + (lane_id() & 31)) {}
-  __device__ __forceinline__ i32x4_t read(const uint16_t* tile, int i, int ks) const {
-    return *reinterpret_cast<const i32x4_t*>(
-        tile + tile_offset(row + i * 32, ks * 2 + (lane_id() >> 5)));
-  }
-};
+// LDS byte offsets, within a stage, of a lane's fragments of the block of 32 rows from r0.
+// K along rows: of 16-wide K step ks, a 16-byte read.  Turned: of step 0; lanes 16 h + L
+// of a half hold rows 16 h + L, a transpose read of 16 lanes takes lines k .. k + 3 of 16
+// rows, lane L pointing at line k + L / 4, row 4 (L % 4), and a fragment is two of them,
+// 4 lines apart.  Steps are 16 lines apart: 4 and 16 lines on, the swizzle is the same.
+__device__ __forceinline__ uint32_t straight_at(int r0, int ks) {
+  return 2u * tile_offset(r0 + (lane_id() & 31), ks * 2 + (lane_id() >> 5));
+}
+template <int SIZE>
+__device__ __forceinline__ uint32_t turned_at(int r0) {
+  const int l = lane_id(), L = l & 15;
+  return 2u * turned_offset<SIZE>((l >> 5) * 8 + L / 4, r0 + ((l >> 4) & 1) * 16 + 4 * (L & 3));
+}
 
-template <int SIZE, int BLOCKS>
-struct Reader<SIZE, BLOCKS, true> {
-  // lanes 16 h + L of a half hold rows 16 h + L; a transpose read of 16 lanes takes lines
-  // k .. k + 3 of 16 rows, lane L pointing at line k + L / 4, row 4 (L % 4)
-  int at[BLOCKS];
-  __device__ __forceinline__ explicit Reader(int r0) {
-    const int l = lane_id(), L = l & 15;
-    const int k = (l >> 5) * 8 + L / 4;
+typedef __attribute__((ext_vector_type(2))) int i32x2_t;
+__device__ __forceinline__ i32x4_t joined(i32x2_t a, i32x2_t b) {
+  return i32x4_t{a[0], a[1], b[0], b[1]};
+}
+
+// The fragments of all K steps of a turned stage, of one block of rows.  The transpose
+// reads are asm, as the compiler puts a wait for every copy in flight before its own.
+template <int SIZE>
+__device__ __forceinline__ void read_turned(uint32_t at, i32x4_t (&f)[4]) {
+  i32x2_t v[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%9\n\t"
+      "ds_read_b64_tr_b16 %2, %8 offset:%10\n\t"
+      "ds_read_b64_tr_b16 %3, %8 offset:%11\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %5, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %6, %8 offset:%14\n\t"
+      "ds_read_b64_tr_b16 %7, %8 offset:%15\n\t"
+      "s_waitcnt lgkmcnt(0)\n\t"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+        "=&v"(v[7])
+      : "v"(at), "n"(8 * SIZE), "n"(32 * SIZE), "n"(40 * SIZE), "n"(64 * SIZE), "n"(72 * SIZE),
+        "n"(96 * SIZE), "n"(104 * SIZE)
+      : "memory");
 #pragma unroll
-    for (int i = 0; i < BLOCKS; ++i)
-      at[i] = turned_offset<SIZE>(k, r0 + i * 32 + ((l >> 4) & 1) * 16 + 4 * (L & 3));
+  for (int ks = 0; ks < 4; ++ks) f[ks] = joined(v[2 * ks], v[2 * ks + 1]);
+}
+
+// The fragments of all K steps of a stage at `tile`, of BLOCKS blocks of rows from r0.
+template <int SIZE, int BLOCKS, bool TURNED>
+__device__ __forceinline__ void read_stage(const uint16_t* tile, int r0,
+                                           i32x4_t (&f)[BLOCKS][4]) {
+#pragma unroll
+  for (int i = 0; i < BLOCKS; ++i) {
+    if constexpr (TURNED) {
+      read_turned<SIZE>(lds_address(tile) + turned_at<SIZE>(r0 + 32 * i), f[i]);
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        f[i][ks] = *reinterpret_cast<const i32x4_t*>(reinterpret_cast<const char*>(tile) +
+                                                     straight_at(r0 + 32 * i, ks));
+    }
   }
-  __device__ __forceinline__ i32x4_t read(const uint16_t* tile, int i, int ks) const {
-    typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4_t;
-    typedef __attribute__((address_space(3))) s16x4_t lds_v4;
-    typedef __attribute__((address_space(3))) uint16_t lds_u16;
-    // 4 and 16 lines on, the swizzle is the same
-    const uint16_t* p = tile + at[i] + ks * 16 * SIZE;
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_u16*)(p)));
-    const s16x4_t hi =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)((lds_u16*)(p + 4 * SIZE)));
-    typedef __attribute__((ext_vector_type(2))) int i32x2_t;
-    const i32x2_t a = __builtin_bit_cast(i32x2_t, lo), b = __builtin_bit_cast(i32x2_t, hi);
-    return i32x4_t{a[0], a[1], b[0], b[1]};
-  }
-};
+}
 
 // The steps of a contraction: a product of parts after another, each over the whole
 // of K, in the order lo hi (kHalves), hi lo, hi hi.
@@ -224,8 +248,7 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
   const Copies<CF::BM, CF::NW, TA> a_copies(A, m0, k0);
   const Copies<CF::BN, CF::NW, TB> b_copies(B, n0, k0);
   const int wave = threadIdx.x / kWave;
-  const Reader<CF::BM, CF::FM, TA> a_reader(wave / CF::WAVES_N * CF::WTM);
-  const Reader<CF::BN, CF::FN, TB> b_reader(wave % CF::WAVES_N * CF::WTN);
+  const int ra = wave / CF::WAVES_N * CF::WTM, rb = wave % CF::WAVES_N * CF::WTN;
   constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
   const int steps = ksteps * products_of(F);
   Walk<F> walk{A.part, B.part, ksteps * kStep};
@@ -246,18 +269,15 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
     if (s + AHEAD < steps) copy();
     const uint16_t* sA = lds + cur * CF::STAGE;
     const uint16_t* sB = sA + CF::BM * kStep;
+    i32x4_t a[CF::FM][4], b[CF::FN][4];
+    read_stage<CF::BM, CF::FM, TA>(sA, ra, a);
+    read_stage<CF::BN, CF::FN, TB>(sB, rb, b);
 #pragma unroll
-    for (int ks = 0; ks < kStep / 16; ++ks) {
-      i32x4_t a[CF::FM], b[CF::FN];
-#pragma unroll
-      for (int i = 0; i < CF::FM; ++i) a[i] = a_reader.read(sA, i, ks);
-#pragma unroll
-      for (int j = 0; j < CF::FN; ++j) b[j] = b_reader.read(sB, j, ks);
+    for (int ks = 0; ks < kStep / 16; ++ks)
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < CF::FN; ++j) acc[i][j] = mfma<F>(a[i], b[j], acc[i][j]);
-    }
+        for (int j = 0; j < CF::FN; ++j) acc[i][j] = mfma<F>(a[i][ks], b[j][ks], acc[i][j]);
     cur = cur + 1 == CF::STAGES ? 0 : cur + 1;
   }
   __syncthreads();  // the stages are free for the epilogue
@@ -272,49 +292,97 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
 struct Fragments {
   i32x4_t a[2], b[4];
 };
+struct Addresses {  // LDS addresses of the next fragments (turned: of K step 0)
+  uint32_t a[2], b[4];
+};
 
-#define NT_PIPE_STEP(MFMA)                                                                    \
-  asm volatile(                                                                               \
-      "ds_read_b128 %[na0], %[p0]\n\t" MFMA " %[c00], %[a0], %[b0], %[c00]\n\t"               \
-      "ds_read_b128 %[na1], %[p1]\n\t" MFMA " %[c01], %[a0], %[b1], %[c01]\n\t"               \
-      "ds_read_b128 %[nb0], %[p2]\n\t" MFMA " %[c02], %[a0], %[b2], %[c02]\n\t"               \
-      "ds_read_b128 %[nb1], %[p3]\n\t" MFMA " %[c03], %[a0], %[b3], %[c03]\n\t"               \
-      "ds_read_b128 %[nb2], %[p4]\n\t" MFMA " %[c10], %[a1], %[b0], %[c10]\n\t"               \
-      "ds_read_b128 %[nb3], %[p5]\n\t" MFMA " %[c11], %[a1], %[b1], %[c11]\n\t" MFMA          \
-      " %[c12], %[a1], %[b2], %[c12]\n\t" MFMA " %[c13], %[a1], %[b3], %[c13]\n\t"            \
-      "s_waitcnt lgkmcnt(0)\n\t"                                                              \
-      : [c00] "+v"(c[0][0]), [c01] "+v"(c[0][1]), [c02] "+v"(c[0][2]), [c03] "+v"(c[0][3]),   \
-        [c10] "+v"(c[1][0]), [c11] "+v"(c[1][1]), [c12] "+v"(c[1][2]), [c13] "+v"(c[1][3]),   \
-        [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1]), [nb0] "=&v"(nxt.b[0]),                  \
-        [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])                   \
-      : [a0] "v"(cur.a[0]), [a1] "v"(cur.a[1]), [b0] "v"(cur.b[0]), [b1] "v"(cur.b[1]),       \
-        [b2] "v"(cur.b[2]), [b3] "v"(cur.b[3]), [p0] "v"(at[0]), [p1] "v"(at[1]),             \
-        [p2] "v"(at[2]), [p3] "v"(at[3]), [p4] "v"(at[4]), [p5] "v"(at[5])                    \
-      : "memory")
+// The reads of fragment `f` (a0, a1, b0 .. b3) at address p##f
+#define NT_READ(f) "ds_read_b128 %[n" #f "], %[p" #f "]\n\t"
+#define NT_READ_TURNED(f, lo, hi)                                     \
+  "ds_read_b64_tr_b16 %[n" #f "], %[p" #f "] offset:%[" #lo "]\n\t"  \
+  "ds_read_b64_tr_b16 %[h" #f "], %[p" #f "] offset:%[" #hi "]\n\t"
+#define NT_READ_TA(f) NT_READ_TURNED(f, lo_a, hi_a)
+#define NT_READ_TB(f) NT_READ_TURNED(f, lo_b, hi_b)
+#define NT_ACC                                                                                \
+  [c00] "+v"(c[0][0]), [c01] "+v"(c[0][1]), [c02] "+v"(c[0][2]), [c03] "+v"(c[0][3]),         \
+      [c10] "+v"(c[1][0]), [c11] "+v"(c[1][1]), [c12] "+v"(c[1][2]), [c13] "+v"(c[1][3])
+#define NT_OUT_A [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1])
+#define NT_OUT_B                                                                              \
+  [nb0] "=&v"(nxt.b[0]), [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])
+#define NT_OUT_TA [na0] "=&v"(la[0]), [ha0] "=&v"(ha[0]), [na1] "=&v"(la[1]), [ha1] "=&v"(ha[1])
+#define NT_OUT_TB                                                                             \
+  [nb0] "=&v"(lb[0]), [hb0] "=&v"(hb[0]), [nb1] "=&v"(lb[1]), [hb1] "=&v"(hb[1]),             \
+      [nb2] "=&v"(lb[2]), [hb2] "=&v"(hb[2]), [nb3] "=&v"(lb[3]), [hb3] "=&v"(hb[3])
+#define NT_CUR                                                                                \
+  [a0] "v"(cur.a[0]), [a1] "v"(cur.a[1]), [b0] "v"(cur.b[0]), [b1] "v"(cur.b[1]),             \
+      [b2] "v"(cur.b[2]), [b3] "v"(cur.b[3])
+#define NT_AT                                                                                 \
+  [pa0] "v"(at.a[0]), [pa1] "v"(at.a[1]), [pb0] "v"(at.b[0]), [pb1] "v"(at.b[1]),             \
+      [pb2] "v"(at.b[2]), [pb3] "v"(at.b[3]), [lo_a] "n"(32 * KS * CF::BM),                   \
+      [hi_a] "n"(32 * KS * CF::BM + 8 * CF::BM), [lo_b] "n"(32 * KS * CF::BN),                \
+      [hi_b] "n"(32 * KS * CF::BN + 8 * CF::BN)
+#define NT_STEP(MFMA, RA, RB, OUT_A, OUT_B)                                                   \
+  asm volatile(RA(a0) MFMA " %[c00], %[a0], %[b0], %[c00]\n\t" RA(a1) MFMA                    \
+               " %[c01], %[a0], %[b1], %[c01]\n\t" RB(b0) MFMA                                \
+               " %[c02], %[a0], %[b2], %[c02]\n\t" RB(b1) MFMA                                \
+               " %[c03], %[a0], %[b3], %[c03]\n\t" RB(b2) MFMA                                \
+               " %[c10], %[a1], %[b0], %[c10]\n\t" RB(b3) MFMA                                \
+               " %[c11], %[a1], %[b1], %[c11]\n\t" MFMA " %[c12], %[a1], %[b2], %[c12]\n\t"   \
+               MFMA " %[c13], %[a1], %[b3], %[c13]\n\ts_waitcnt lgkmcnt(0)\n\t"               \
+               : NT_ACC, OUT_A, OUT_B                                                         \
+               : NT_CUR, NT_AT                                                                \
+               : "memory")
+#define NT_LOAD(RA, RB, OUT_A, OUT_B)                                                         \
+  asm volatile(RA(a0) RA(a1) RB(b0) RB(b1) RB(b2) RB(b3) "s_waitcnt lgkmcnt(0)\n\t"           \
+               : OUT_A, OUT_B                                                                 \
+               : NT_AT                                                                        \
+               : "memory")
 
-template <Form F>
+// The MFMAs of cur beside the reads of nxt, K step KS of its stage.  First: the reads alone.
+template <class CF, Form F, bool TA, bool TB, int KS, bool FIRST = false>
 __device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][4], const Fragments& cur,
-                                          Fragments& nxt, const uint32_t (&at)[6]) {
-  if constexpr (F == kBf16) NT_PIPE_STEP("v_mfma_f32_32x32x16_bf16");
-  else NT_PIPE_STEP("v_mfma_f32_32x32x16_f16");
+                                          Fragments& nxt, const Addresses& at) {
+  static_assert(TA || !TB, "no product turns its columns alone");
+  i32x2_t la[2], ha[2], lb[4], hb[4];
+  if constexpr (FIRST) {
+    if constexpr (TA && TB) NT_LOAD(NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
+    else if constexpr (TA) NT_LOAD(NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
+    else NT_LOAD(NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
+  } else if constexpr (F == kBf16) {
+#define NT_MFMA "v_mfma_f32_32x32x16_bf16"
+    if constexpr (TA && TB) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
+    else if constexpr (TA) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
+    else NT_STEP(NT_MFMA, NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
+#undef NT_MFMA
+  } else {
+#define NT_MFMA "v_mfma_f32_32x32x16_f16"
+    if constexpr (TA && TB) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
+    else if constexpr (TA) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
+    else NT_STEP(NT_MFMA, NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
+#undef NT_MFMA
+  }
+  if constexpr (TA) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) nxt.a[i] = joined(la[i], ha[i]);
+  }
+  if constexpr (TB) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) nxt.b[j] = joined(lb[j], hb[j]);
+  }
 }
-#undef NT_PIPE_STEP
-
-__device__ __forceinline__ void pipe_load(Fragments& nxt, const uint32_t (&at)[6]) {
-  asm volatile(
-      "ds_read_b128 %[na0], %[p0]\n\t"
-      "ds_read_b128 %[na1], %[p1]\n\t"
-      "ds_read_b128 %[nb0], %[p2]\n\t"
-      "ds_read_b128 %[nb1], %[p3]\n\t"
-      "ds_read_b128 %[nb2], %[p4]\n\t"
-      "ds_read_b128 %[nb3], %[p5]\n\t"
-      "s_waitcnt lgkmcnt(0)\n\t"
-      : [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1]), [nb0] "=&v"(nxt.b[0]),
-        [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])
-      : [p0] "v"(at[0]), [p1] "v"(at[1]), [p2] "v"(at[2]), [p3] "v"(at[3]), [p4] "v"(at[4]),
-        [p5] "v"(at[5])
-      : "memory");
-}
+#undef NT_READ
+#undef NT_READ_TURNED
+#undef NT_READ_TA
+#undef NT_READ_TB
+#undef NT_ACC
+#undef NT_OUT_A
+#undef NT_OUT_B
+#undef NT_OUT_TA
+#undef NT_OUT_TB
+#undef NT_CUR
+#undef NT_AT
+#undef NT_STEP
+#undef NT_LOAD
 
 // VALU writes of the accumulators before MFMAs in asm, and MFMA results before VALU
 // reads: the accumulators are operands, so neither moves across the wait.
@@ -324,7 +392,7 @@ __device__ __forceinline__ void settle(f32x16_t (&c)[2][4]) {
                  "+v"(c[1][1]), "+v"(c[1][2]), "+v"(c[1][3]));
 }
 
-template <class CF, Form F>
+template <class CF, Form F, bool TA, bool TB>
 __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Operand& B, int n0,
                                               int k0, int ksteps, uint16_t* lds,
                                               f32x16_t (&acc)[2][4]) {
@@ -338,23 +406,22 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   const int steps = ksteps * products_of(F);
   if (steps == 0) return;
   settle(acc);
-  const Copies<CF::BM, CF::NW, false> a_copies(A, m0, k0);
-  const Copies<CF::BN, CF::NW, false> b_copies(B, n0, k0);
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
-  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
-  typedef __attribute__((address_space(3))) uint16_t lds_u16;
-  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u16*)lds));
-  uint32_t at[4][6];  // LDS addresses of the fragments of each K step in stage 0
+  const Copies<CF::BM, CF::NW, TA> a_copies(A, m0, k0);
+  const Copies<CF::BN, CF::NW, TB> b_copies(B, n0, k0);
+  const int wave = threadIdx.x / kWave;
+  const int ra = wave / CF::WAVES_N * CF::WTM, rb = wave % CF::WAVES_N * CF::WTN;
+  const uint32_t base_a = lds_address(lds), base_b = base_a + 2 * CF::BM * kStep;
+  Addresses first[4];  // in stage 0, of each K step (turned: the same)
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    const int kc = ks * 2 + (lane >> 5);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      at[ks][i] = base + 2u * tile_offset(wm * CF::WTM + i * 32 + (lane & 31), kc);
+      first[ks].a[i] =
+          base_a + (TA ? turned_at<CF::BM>(ra + 32 * i) : straight_at(ra + 32 * i, ks));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      at[ks][2 + j] = base + 2u * (CF::BM * kStep +
-                                   tile_offset(wn * CF::WTN + j * 32 + (lane & 31), kc));
+      first[ks].b[j] =
+          base_b + (TB ? turned_at<CF::BN>(rb + 32 * j) : straight_at(rb + 32 * j, ks));
   }
   Walk<F> walk{A.part, B.part, ksteps * kStep};
   auto copy = [&](int stage) {
@@ -367,23 +434,26 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   copy(0);
   meet<0>();
   if (steps > 1) copy(1);
-  pipe_load(f0, at[0]);
-  pipe_step<F>(acc, f0, f1, at[1]);
-  pipe_step<F>(acc, f1, f0, at[2]);
-  pipe_step<F>(acc, f0, f1, at[3]);
+  pipe_step<CF, F, TA, TB, 0, true>(acc, f1, f0, first[0]);
+  pipe_step<CF, F, TA, TB, 1>(acc, f0, f1, first[1]);
+  pipe_step<CF, F, TA, TB, 2>(acc, f1, f0, first[2]);
+  pipe_step<CF, F, TA, TB, 3>(acc, f0, f1, first[3]);
   for (int s = 1; s < steps; ++s) {  // f1: the fragments of the last K step of stage s - 1
     meet<0>();
     if (s + 1 < steps) copy((s + 1) & 1);
     const uint32_t shift = static_cast<uint32_t>(s & 1) * (CF::STAGE * 2);
-    uint32_t a[4][6];
+    Addresses at[4];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
+    for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
-      for (int q = 0; q < 6; ++q) a[ks][q] = at[ks][q] + shift;
-    pipe_step<F>(acc, f1, f0, a[0]);
-    pipe_step<F>(acc, f0, f1, a[1]);
-    pipe_step<F>(acc, f1, f0, a[2]);
-    pipe_step<F>(acc, f0, f1, a[3]);
+      for (int i = 0; i < 2; ++i) at[ks].a[i] = first[ks].a[i] + shift;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at[ks].b[j] = first[ks].b[j] + shift;
+    }
+    pipe_step<CF, F, TA, TB, 0>(acc, f1, f0, at[0]);
+    pipe_step<CF, F, TA, TB, 1>(acc, f0, f1, at[1]);
+    pipe_step<CF, F, TA, TB, 2>(acc, f1, f0, at[2]);
+    pipe_step<CF, F, TA, TB, 3>(acc, f0, f1, at[3]);
   }
   settle(acc);
 #pragma unroll
@@ -397,8 +467,8 @@ template <class CF, Form F, bool TA = false, bool TB = false>
 __device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand& B, int n0, int k0,
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
-  if constexpr (CF::FM == 2 && CF::FN == 4 && !TA && !TB)
-    mainloop_pipe<CF, F>(A, m0, B, n0, k0, ksteps, lds, acc);
+  if constexpr (CF::FM == 2 && CF::FN == 4)
+    mainloop_pipe<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
   else
     mainloop<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
 }
