@@ -11,12 +11,15 @@
 //   dl[n][v] = g[n] (1[v = target] - p)     from z formed again
 //   dx += dl w,   dw = dl^T x
 // With bfloat16 x and w, dl is held in bfloat16: its rounding, 2^-9 of each element,
-// is of the size of dx's and dw's own.  With float32 ones every operand is two
-// half-precision parts (nt_gemm.h), w scaled by its largest element, x by each row's;
-// dl / g lies in [-1, 1] and is scaled by 2^14, with g taken into dx at the end and
-// into the x of dw.  Both products read w, x and dl as they lie, turning fragments with
-// LDS transpose reads where K runs along a column.
+// is of the size of dx's and dw's own (with few rows, where it costs next to nothing,
+// as two parts).  With float32 ones every operand is two half-precision parts
+// (nt_gemm.h), w scaled by its largest element, x by each row's; dl / g lies in [-1, 1]
+// and is scaled by 2^14, with g taken into dx at the end and into the x of dw.  With few
+// rows, where reading w is what the call costs, float32 operands and dl stay float32.
+// Both products read w, x and dl as they lie, turning fragments with LDS transpose
+// reads where K runs along a column.
 #include <algorithm>
+#include <type_traits>
 
 #include "nt_gemm.h"
 #include "train_kernels.h"
@@ -36,11 +39,6 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int index_byte
 // v of the lane with the other half's rows of the same column
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
-// The form of operands of elements E.
-template <typename E>
-constexpr Form form_of() {
-  return sizeof(E) == 2 ? kBf16 : kHalves;
-}
 constexpr int kDlExponent = 14;  // of dl / g in halves
 
 __device__ __forceinline__ bool has_target(const void* targets, int index_bytes, int vocab,
@@ -126,10 +124,9 @@ __global__ __launch_bounds__(256) void head_amax_kernel(const float* __restrict_
   }
 }
 
-// parts [rows][ld] of a piece of w, src [rows][d], scaled by *amax (halves); columns
-// past d are zeros.
-template <typename E>
-__global__ __launch_bounds__(256) void head_w_kernel(const E* __restrict__ src, int64_t rows,
+// Halves [2][rows][ld] of a piece of w, src [rows][d], scaled by *amax; columns past d
+// are zeros.
+__global__ __launch_bounds__(256) void head_w_kernel(const float* __restrict__ src, int64_t rows,
                                                      int d, int ld, const float* amax,
                                                      uint16_t* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -138,76 +135,76 @@ __global__ __launch_bounds__(256) void head_w_kernel(const E* __restrict__ src, 
   if (row >= rows) return;
   float v[8] = {};
   if (c < d) load_run(src + row * d + c, v);
-  if constexpr (form_of<E>() == kHalves) {
-    const float f = power_of_two(exponent_for(*amax));
+  const float f = power_of_two(exponent_for(*amax));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= f;
-  }
-  put_run<form_of<E>()>(out + row * ld, rows * ld, c, v);
+  for (int k = 0; k < 8; ++k) v[k] *= f;
+  put_run<kHalves>(out + row * ld, rows * ld, c, v);
 }
 
-// parts [rows][ld] of x, a wave a row.  Halves: scaled by the row's largest element,
-// what undoes it in undo[row]; and, for the gradient (dlogp not null), *amax = the
-// largest of |scale dlogp x| over rows with a target.
-template <typename E>
+// Halves [2][rows][ld] of x, a wave a row, scaled by the row's largest element, what undoes
+// it in undo[row]; and, for the gradient (dlogp not null), *amax = the largest of
+// |scale dlogp x| over rows with a target.
 __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
                                                      const float* __restrict__ dlogp,
                                                      float* __restrict__ undo, float* amax,
                                                      uint16_t* __restrict__ out) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
   if (row >= a.n_rows) return;
-  const E* src = static_cast<const E*>(a.x) + row * a.d;
-  float f = 1.f;
-  if constexpr (form_of<E>() == kHalves) {
-    float m = 0.f;
-    for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
-      float v[8];
-      load_run(src + c, v);
+  const float* src = static_cast<const float*>(a.x) + row * a.d;
+  float m = 0.f;
+  for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
+    float v[8];
+    load_run(src + c, v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
-    }
-    m = wave_max(m);
-    const int e = exponent_for(m);
-    f = power_of_two(e);
-    if (lane_id() == 0) {
-      undo[row] = power_of_two(-e);
-      if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
-        atomicMax(reinterpret_cast<int*>(amax),
-                  __float_as_int(max_finite(0.f, dlogp[row] * a.scale * m)));
-    }
+    for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
+  }
+  m = wave_max(m);
+  const int e = exponent_for(m);
+  const float f = power_of_two(e);
+  if (lane_id() == 0) {
+    undo[row] = power_of_two(-e);
+    if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
+      atomicMax(reinterpret_cast<int*>(amax),
+                __float_as_int(max_finite(0.f, dlogp[row] * a.scale * m)));
   }
   for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
     float v[8] = {};
     if (c < a.d) load_run(src + c, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= f;
-    put_run<form_of<E>()>(out + row * ld, a.n_rows * ld, c, v);
+    put_run<kHalves>(out + row * ld, a.n_rows * ld, c, v);
   }
 }
 
-// parts [lines][ld] of dw's x, a wave a row: rows without a target, and past the end, are
-// zeros (whatever x holds there meets gradients of zero, and a NaN must not spread).
-// Halves: scale * dlogp * x, scaled by *amax.
-template <typename E>
-__global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, int64_t lines, int ld,
-                                                      const float* __restrict__ dlogp,
+// dw's x, [parts][n_rows][d], a wave a row: rows without a target are zeros (whatever x
+// holds there meets gradients of zero, and a NaN must not spread).  Halves: scale * dlogp
+// * x, scaled by *amax; else x as it is.
+template <Form F>
+__global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, const float* __restrict__ dlogp,
                                                       const float* amax,
                                                       uint16_t* __restrict__ out) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
-  if (row >= lines) return;
-  const bool live = row < a.n_rows && has_target(a.targets, a.index_bytes, a.vocab, row);
+  if (row >= a.n_rows) return;
+  const bool live = has_target(a.targets, a.index_bytes, a.vocab, row);
+  typedef std::conditional_t<F == kBf16, uint16_t, float> E;
   const E* src = static_cast<const E*>(a.x) + row * a.d;
   float f = 1.f, g = 1.f;
-  if constexpr (form_of<E>() == kHalves) {
+  if constexpr (F == kHalves) {
     f = power_of_two(exponent_for(*amax));
     if (live) g = dlogp[row] * a.scale;
   }
-  for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
+  for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
     float v[8] = {};
-    if (live && c < a.d) load_run(src + c, v);
+    if (live) load_run(src + c, v);
+    if constexpr (F == kRaw) {
+      float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + row * a.d + c);
+      to[0] = make_float4(v[0], v[1], v[2], v[3]);
+      to[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
-    put_run<form_of<E>()>(out + row * ld, lines * ld, c, v);
+      for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
+      put_run<F>(out + row * a.d, a.n_rows * a.d, c, v);
+    }
   }
 }
 
@@ -356,7 +353,13 @@ __device__ __forceinline__ uint32_t pack_part(float a, float b, int p) {
   if constexpr (F == kBf16) {
     typedef __attribute__((ext_vector_type(2))) float f32x2_t;
     typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+    uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+    if (p == 1)  // what the first part leaves
+      w = __builtin_bit_cast(
+          uint32_t, __builtin_convertvector(f32x2_t{a - __uint_as_float(w << 16),
+                                                    b - __uint_as_float(w & 0xffff0000u)},
+                                            bf16x2_t));
+    return w;
   } else {
     _Float16 x = static_cast<_Float16>(a), y = static_cast<_Float16>(b);
     if (p == 1) {  // what the first part leaves; |a| is at most 2^14, or NaN
@@ -378,11 +381,11 @@ struct DlArgs {
   int index_bytes;
   const float2* stats;
   const float* dlogp;
-  uint16_t* dl;  // [parts][n][ldv]
+  uint16_t* dl;  // [parts][n][ldv]; raw: float [n][ldv]
   int ldv;
 };
 
-template <class CF, Form F>
+template <class CF, Form F, int PARTS>
 __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks, int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
@@ -407,7 +410,7 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
       given = target >= 0 && target < a.vocab && !(st.x == -INFINITY && st.y == 0.f);
       if (given) {
         t = static_cast<int>(target) - a.v0 - wave_row;
-        g = F == kBf16 ? a.dlogp[n] * a.scale : power_of_two(kDlExponent);
+        g = F == kHalves ? power_of_two(kDlExponent) : a.dlogp[n] * a.scale;
         m = st.x;
         share = -g / st.y;
       }
@@ -429,12 +432,29 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
           if (rel == nt::row_of(i, r)) acc[i][j][r] += g;
     }
   }
+  if constexpr (F == kRaw) {
+#pragma unroll
+    for (int j = 0; j < CF::FN; ++j) {
+      const int n = nb * CF::BN + nt::block_col<CF>() + 32 * j;
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int v = row0 + nt::row_of(i, 4 * q);
+          if (n < n_rows && v < a.ldv)
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.dl) + n * int64_t{a.ldv} + v) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+        }
+    }
+    return;
+  }
   // a part at a time through LDS, so that its rows are stored whole: the 16-byte chunk c
   // of row n at position c ^ n, which spreads the 32 rows of a write over the banks
   constexpr int CHUNKS = CF::BM / 8;
   static_assert(CF::BM * CF::BN <= CF::STAGES * CF::STAGE, "the tile fits the stages");
 #pragma unroll
-  for (int p = 0; p < parts_of(F); ++p) {
+  for (int p = 0; p < PARTS; ++p) {
     if (p > 0) __syncthreads();
 #pragma unroll
     for (int j = 0; j < CF::FN; ++j) {
@@ -466,7 +486,7 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
 
 // dx = the sum of the slices, rounded; 8 elements a lane.  Halves: times scale * dlogp
 // of the row and the powers of two undone.
-template <typename E>
+template <typename E, Form F>
 __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* __restrict__ sums,
                                                       int slices, const float* __restrict__ dlogp,
                                                       const float* amax, E* __restrict__ dx) {
@@ -480,7 +500,7 @@ __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* _
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += p[k];
   }
-  if constexpr (form_of<E>() == kHalves) {
+  if constexpr (F == kHalves) {
     const int64_t n = i / a.d;
     const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
     const float g = given ? dlogp[n] * a.scale : 0.f;
@@ -503,11 +523,6 @@ __global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count)
 }
 
 // ---------------------------------------------------------------- sizes
-int part_count(int elem_bytes) { return elem_bytes == 2 ? 1 : 2; }
-
-// Whether x and w serve as operands where they are.
-bool direct(int elem_bytes, int d) { return elem_bytes == 2 && d % 64 == 0; }
-
 // Columns of the vocabulary taken at a time: all where the forward pass reads w in
 // place, else as many as keep what is made per column within `budget`, in equal
 // pieces.
@@ -517,12 +532,15 @@ int piece_of(int vocab, size_t per_column, size_t budget) {
   return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
 }
 
+constexpr size_t kFewPiece = size_t{96} << 20;  // bytes of w
 constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
 
-// Stages of a contraction over d columns.
-int64_t stages(const HeadArgs& a, int elem_bytes) {
-  return up64(a.d) / 64 * (elem_bytes == 2 ? 1 : products_of(kHalves));
+// The form of the operands; and the stages of a product over k.
+Form form_of(int elem_bytes, int64_t n) {
+  return elem_bytes == 2 ? kBf16 : n <= kFewColumns ? kRaw : kHalves;
 }
+int stages(Form f, int64_t k) { return static_cast<int>(blocks(k, f == kRaw ? 32 : 64)); }
+int dl_parts(Form f, int64_t n) { return f == kBf16 && n <= kFewColumns ? 2 : parts_of(f); }
 
 struct ForwardPlan {
   int piece, tiles;
@@ -535,16 +553,18 @@ struct ForwardPlan {
 };
 ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   ForwardPlan p{};
-  const size_t ld = up64(a.d), part_bytes = 2 * part_count(elem_bytes) * ld;
-  const bool in_place = direct(elem_bytes, a.d);
-  p.piece = in_place ? a.vocab : piece_of(a.vocab, part_bytes, size_t{128} << 20);
-  // tiles of a piece start at its first column: pieces but the last are whole tiles
-  p.tile = cut_for(p.piece, a.n_rows, stages(a, elem_bytes), 1, false).tile;
+  const Form f = form_of(elem_bytes, a.n_rows);
+  const size_t ld = up64(a.d), part_bytes = 2 * parts_of(f) * ld;
+  // pieces but the last are whole tiles
+  p.piece = f == kHalves ? piece_of(a.vocab, part_bytes, size_t{128} << 20) : a.vocab;
+  const int64_t steps = stages(f, a.d) * products_of(f);
+  p.tile = a.n_rows <= kFewColumns ? few_cut(p.piece, a.n_rows, steps, 1).tile
+                                   : wide_cut(p.piece, a.n_rows, steps, 1, false).tile;
   p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(p.tile)));
   Carve c{static_cast<char*>(ws)};
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
   p.target_z = c.take<float>(a.n_rows);
-  if (!in_place) {
+  if (f == kHalves) {
     p.amax = c.take<float>(kAmax);
     p.undo = c.take<float>(a.n_rows);
     p.xp = c.take<uint16_t>(part_bytes / 2 * a.n_rows);
@@ -555,7 +575,7 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
 }
 
 struct BackwardPlan {
-  int piece, ldn;
+  int piece;
   Tile dl_tile;
   Cut dx_cut;
   uint16_t *xp, *wp, *gx, *dl;
@@ -564,77 +584,89 @@ struct BackwardPlan {
 };
 BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   BackwardPlan p{};
-  const size_t P = part_count(elem_bytes), ld = up64(a.d), n = a.n_rows;
-  const bool in_place = direct(elem_bytes, a.d);
-  p.ldn = static_cast<int>(up64(n));
-  const size_t per_column = 2 * P * (n + (in_place ? 0 : ld));
-  p.piece = piece_of(a.vocab, per_column, size_t{192} << 20);
+  const Form f = form_of(elem_bytes, a.n_rows);
+  const bool few = a.n_rows <= kFewColumns;
+  const size_t ld = up64(a.d), n = a.n_rows;
+  const size_t element = f == kRaw ? 4 : 2 * dl_parts(f, n);  // bytes of a place of dl
+  // few rows: a piece of w that the Infinity Cache still holds when dx reads it
+  const size_t per_column = few ? static_cast<size_t>(a.d) * elem_bytes
+                                : n * element + (f == kHalves ? 4 * ld : 0);
+  p.piece = piece_of(a.vocab, per_column, few ? kFewPiece : size_t{192} << 20);
   const size_t ldv = up64(p.piece);
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  const int products = elem_bytes == 2 ? 1 : products_of(kHalves);
-  p.dx_cut = cut_for(a.d, n, ldv / 64 * products, 32, false);
-  p.dl_tile = cut_for(p.piece, n, stages(a, elem_bytes), 1, false).tile;
+  if (few) {
+    p.dl_tile = few_cut(p.piece, n, 1, 1).tile;
+    p.dx_cut = few_cut(a.d, n, stages(f, ldv) * (f == kBf16 ? 2 : 1), 32);
+  } else {
+    p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false).tile;
+    p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false);
+  }
   Carve c{static_cast<char*>(ws)};
-  p.gx = c.take<uint16_t>(P * p.ldn * ld);
-  p.dl = c.take<uint16_t>(P * n * ldv);
+  p.gx = c.take<uint16_t>((f == kBf16 ? 1 : 2) * n * a.d);
+  p.dl = c.take<uint16_t>(element / 2 * n * ldv);
   p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
-  if (!in_place) {
+  if (f == kHalves) {
     p.amax = c.take<float>(kAmax);
     p.undo = c.take<float>(n);
-    p.xp = c.take<uint16_t>(P * ld * n);
-    p.wp = c.take<uint16_t>(P * ld * p.piece);
+    p.xp = c.take<uint16_t>(2 * ld * n);
+    p.wp = c.take<uint16_t>(2 * ld * p.piece);
   }
   p.bytes = c.used;
   return p;
 }
 
 // ---------------------------------------------------------------- launches
-int columns(const HeadArgs& a) { return static_cast<int>(up64(a.d)); }
-
 // The operand x, in place or as parts in xp; halves: amax of w (and of the gradient's x)
 // on the way.
-template <typename E>
+template <Form F>
 Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* undo, uint16_t* xp,
                   hipStream_t s) {
-  const int n = static_cast<int>(a.n_rows), ld = columns(a);
-  if (direct(sizeof(E), a.d)) return Operand{static_cast<const uint16_t*>(a.x), 0, a.d, n, 0};
-  if constexpr (form_of<E>() == kHalves) {
-    head_clear_kernel<<<1, kAmax, 0, s>>>(amax);
-    const int64_t runs = static_cast<int64_t>(a.vocab) * a.d / 8;
-    head_amax_kernel<<<static_cast<uint32_t>(blocks(runs, kAmaxRuns)), 256, 0, s>>>(
-        static_cast<const float*>(a.w), runs, amax);
-  }
-  head_x_kernel<E><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo,
-                                                                      amax + 1, xp);
-  return Operand{xp, a.n_rows * ld, ld, n, 0};
+  const int n = static_cast<int>(a.n_rows), units = F == kRaw ? 2 * a.d : a.d;
+  if (F != kHalves) return Operand{static_cast<const uint16_t*>(a.x), 0, units, n, units};
+  const int ld = static_cast<int>(up64(a.d));
+  head_clear_kernel<<<1, kAmax, 0, s>>>(amax);
+  const int64_t runs = static_cast<int64_t>(a.vocab) * a.d / 8;
+  head_amax_kernel<<<static_cast<uint32_t>(blocks(runs, kAmaxRuns)), 256, 0, s>>>(
+      static_cast<const float*>(a.w), runs, amax);
+  head_x_kernel<<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo, amax + 1,
+                                                                   xp);
+  return Operand{xp, a.n_rows * ld, ld, n, ld};
 }
 
 // The operand of columns [v0, v0 + rows) of the vocabulary.
-template <typename E>
+template <Form F>
 Operand w_operand(const HeadArgs& a, int64_t v0, int rows, const float* amax, uint16_t* wp,
                   hipStream_t s) {
-  const E* src = static_cast<const E*>(a.w) + v0 * a.d;
-  const int ld = columns(a);
-  if (direct(sizeof(E), a.d)) return Operand{reinterpret_cast<const uint16_t*>(src), 0, a.d, rows, 0};
-  head_w_kernel<E><<<static_cast<uint32_t>(blocks(static_cast<int64_t>(rows) * (ld / 8), 256)), 256,
-                     0, s>>>(src, rows, a.d, ld, amax, wp);
-  return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows, 0};
+  const int units = F == kRaw ? 2 * a.d : a.d;
+  if (F != kHalves)
+    return Operand{static_cast<const uint16_t*>(a.w) + v0 * units, 0, units, rows, units};
+  const int ld = static_cast<int>(up64(a.d));
+  head_w_kernel<<<static_cast<uint32_t>(blocks(static_cast<int64_t>(rows) * (ld / 8), 256)), 256, 0,
+                  s>>>(static_cast<const float*>(a.w) + v0 * a.d, rows, a.d, ld, amax, wp);
+  return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows, ld};
 }
 
-template <typename E>
+// f(tile) with the tiles for few rows or for many; raw: few.
+template <Form F, class Call>
+hipError_t with_tile(bool few, Tile t, const Call& f) {
+  if constexpr (F == kRaw) return with_few_tile(t, f);
+  else if constexpr (F == kHalves) return with_wide_tile(t, f);
+  else return few ? with_few_tile(t, f) : with_wide_tile(t, f);
+}
+
+template <Form F>
 hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* stats,
                    hipStream_t s) {
-  constexpr Form F = form_of<E>();
-  const ForwardPlan p = forward_plan(a, sizeof(E), ws);
+  const ForwardPlan p = forward_plan(a, F == kBf16 ? 2 : 4, ws);
   const int n = static_cast<int>(a.n_rows);
-  const Operand x = x_operand<E>(a, nullptr, p.amax, p.undo, p.xp, s);
+  const Operand x = x_operand<F>(a, nullptr, p.amax, p.undo, p.xp, s);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
-    const Operand w = w_operand<E>(a, v0, rows, p.amax, p.wp, s);
-    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, p.amax,
+    const Operand w = w_operand<F>(a, v0, rows, p.amax, p.wp, s);
+    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, p.amax,
                       p.undo, a.targets, a.index_bytes,
                       p.parts + v0 / tile_rows(p.tile) * a.n_rows, p.target_z};
-    const hipError_t e = with_tile(p.tile, [&](auto cf) {
+    const hipError_t e = with_tile<F>(n <= kFewColumns, p.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       head_stats_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
@@ -648,64 +680,69 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
   return hipGetLastError();
 }
 
-template <typename E>
+// FEW: at most kFewColumns rows.
+template <Form F, bool FEW>
 hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, void* ws, void* dx,
                     void* dw, hipStream_t s) {
-  constexpr Form F = form_of<E>();
-  if (a.n_rows == 0) {
-    const int64_t count = static_cast<int64_t>(a.vocab) * a.d * sizeof(E) / 16;
-    head_zero_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(count, 256), 1 << 20)), 256,
-                       0, s>>>(static_cast<uint4*>(dw), count);
-    return hipGetLastError();
-  }
+  typedef std::conditional_t<F == kBf16, uint16_t, float> E;
+  constexpr int PARTS = F == kBf16 && FEW ? 2 : parts_of(F);  // dl_parts
+  constexpr Form PRODUCT = F == kBf16 && FEW ? kBf16Two : F;
   const BackwardPlan p = backward_plan(a, sizeof(E), ws);
   const int n = static_cast<int>(a.n_rows);
   const float* const amax_w = F == kHalves ? p.amax : nullptr;
   const float* const amax_x = F == kHalves ? p.amax + 1 : nullptr;
-  const Operand x = x_operand<E>(a, dlogp, p.amax, p.undo, p.xp, s);
-  const int ld = columns(a);
-  head_gx_kernel<E><<<static_cast<uint32_t>(blocks(p.ldn, 4)), 256, 0, s>>>(a, p.ldn, ld, dlogp,
-                                                                           amax_x, p.gx);
-  const Operand gx{p.gx, static_cast<int64_t>(p.ldn) * ld, ld, a.d, p.ldn};
+  const int per = F == kRaw ? 2 : 1;  // 16-bit units of an element
+  const Operand x = x_operand<F>(a, dlogp, p.amax, p.undo, p.xp, s);
+  head_gx_kernel<F><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, dlogp, amax_x, p.gx);
+  const Operand gx{p.gx, a.n_rows * a.d, static_cast<int64_t>(per) * a.d, a.d, n};
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const int ldv = static_cast<int>(up64(rows));
-    const Operand w = w_operand<E>(a, v0, rows, amax_w, p.wp, s);
-    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, columns(a) / 64, a.scale, amax_w, p.undo,
-                   a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl, ldv};
-    hipError_t e = with_tile(p.dl_tile, [&](auto cf) {
+    const Operand w = w_operand<F>(a, v0, rows, amax_w, p.wp, s);
+    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, amax_w, p.undo,
+                   a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
+                   ldv};
+    hipError_t e = with_tile<F>(FEW, p.dl_tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      head_dl_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      if constexpr ((CF::BN <= kFewColumns) == FEW)
+        head_dl_kernel<CF, F, PARTS><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
     // dx: K is the vocabulary, along w's columns; dw: K is the rows, along dl's and gx's
+    const int64_t dl_part = a.n_rows * ldv;
     const Operand wt{w.p, w.part, w.ld, a.d, rows};
-    const Operand dl{p.dl, static_cast<int64_t>(n) * ldv, ldv, n, 0};
-    const Operand dlt{p.dl, static_cast<int64_t>(n) * ldv, ldv, ldv, n};
-    e = with_tile(p.dx_cut.tile, [&](auto cf) {
+    const Operand dl{p.dl, dl_part, static_cast<int64_t>(per) * ldv, n, per * ldv};
+    const Operand dlt{p.dl, dl_part, static_cast<int64_t>(per) * ldv, ldv, n};
+    e = with_tile<F>(FEW, p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      product_kernel<CF, F, true, false, float, true>
-          <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
-              wt, dl, ldv / 64, mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
+      if constexpr ((CF::BN <= kFewColumns) == FEW)
+        product_kernel<CF, PRODUCT, true, false, float, true>
+            <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
+                wt, dl, stages(F, ldv), mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const Cut dw_cut = cut_for(a.d, rows, p.ldn / 64 * products_of(F), 1, false);
-    e = with_tile(dw_cut.tile, [&](auto cf) {
+    const auto dw_product = [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      product_kernel<CF, F, true, true, E, false><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
-          gx, dlt, p.ldn / 64, mb, nb, rows, false, a.d, amax_x, -kDlExponent,
-          static_cast<E*>(dw) + v0 * a.d);
+      product_kernel<CF, PRODUCT, true, true, E, false>
+          <<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+              gx, dlt, stages(F, n), mb, nb, rows, false, a.d, amax_x, -kDlExponent,
+              static_cast<E*>(dw) + v0 * a.d);
       return hipGetLastError();
-    });
+    };
+    if constexpr (FEW)
+      e = dw_product(Mid());
+    else
+      e = with_wide_tile(wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false).tile,
+                         dw_product);
     if (e != hipSuccess) return e;
   }
-  head_dx_kernel<E><<<static_cast<uint32_t>(blocks(a.n_rows * a.d / 8, 256)), 256, 0, s>>>(
+  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d / 8, 256)), 256, 0, s>>>(
       a, p.sums, p.dx_cut.slices, dlogp, amax_w, static_cast<E*>(dx));
   return hipGetLastError();
 }
@@ -722,14 +759,28 @@ size_t head_backward_bytes(const HeadArgs& a, int elem_bytes) {
 hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
                                float* lse, float* stats, hipStream_t s) {
   if (a.n_rows == 0) return hipSuccess;
-  return elem_bytes == 2 ? forward<uint16_t>(a, ws, logp, lse, stats, s)
-                         : forward<float>(a, ws, logp, lse, stats, s);
+  switch (form_of(elem_bytes, a.n_rows)) {
+    case kBf16: return forward<kBf16>(a, ws, logp, lse, stats, s);
+    case kRaw: return forward<kRaw>(a, ws, logp, lse, stats, s);
+    default: return forward<kHalves>(a, ws, logp, lse, stats, s);
+  }
 }
 
 hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* stats,
                                 const float* dlogp, void* ws, void* dx, void* dw, hipStream_t s) {
-  return elem_bytes == 2 ? backward<uint16_t>(a, stats, dlogp, ws, dx, dw, s)
-                         : backward<float>(a, stats, dlogp, ws, dx, dw, s);
+  if (a.n_rows == 0) {
+    const int64_t count = static_cast<int64_t>(a.vocab) * a.d * elem_bytes / 16;
+    head_zero_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(count, 256), 1 << 20)), 256,
+                       0, s>>>(static_cast<uint4*>(dw), count);
+    return hipGetLastError();
+  }
+  switch (form_of(elem_bytes, a.n_rows)) {
+    case kRaw: return backward<kRaw, true>(a, stats, dlogp, ws, dx, dw, s);
+    case kHalves: return backward<kHalves, false>(a, stats, dlogp, ws, dx, dw, s);
+    default:
+      return a.n_rows <= kFewColumns ? backward<kBf16, true>(a, stats, dlogp, ws, dx, dw, s)
+                                     : backward<kBf16, false>(a, stats, dlogp, ws, dx, dw, s);
+  }
 }
 
 }  // namespace twell

@@ -13,13 +13,18 @@
 //              large one last: no more cuts at the sum's full size than a product of
 //              one part has.
 //  - kHalf:    the hi part alone, within 2^-11 of v.
-// A product's form is that of both operands, or kMixed: A in kHalf, B in kHalves.
+//  - kRaw:     float32 as it lies, for few rows, where a pass over the other operand
+//              to split it would cost as much as the product: fragments are split into
+//              three bfloat16 parts (8 + 8 + 8 bits, of any exponent) as they leave
+//              LDS, six products, the five small ones in accumulators of their own.
+// A product's form is that of both operands, or one of a mixed pair: kMixed, A in kHalf
+// and B in kHalves, and kBf16Two, A in kBf16 and B as two bfloat16 parts.
 //
-// Operands are [parts][rows][ld], K along a row: ld a multiple of 64 with zeros past
-// the contraction's length; rows past the end read the last row and feed outputs that
-// no epilogue stores.  Or turned, [parts][depth][ld] with K along the column: rows (a
-// multiple of 8) are then columns of that, and K past `depth` reads its last line, for
-// which the other operand holds zeros.
+// Operands are [parts][rows][ld], K along a row (rows past the end read the last row
+// and feed outputs that no epilogue stores), or turned, [parts][depth][ld] with K along
+// the column (rows, a multiple of 8, are then columns of that).  K past `depth`, a
+// multiple of 8 where it runs along rows, reads zeros.  A kRaw operand is addressed in
+// 16-bit units: ld and a straight operand's depth count two per float.
 #pragma once
 
 #include <algorithm>
@@ -31,17 +36,21 @@ namespace nt {
 
 constexpr int kStep = 64;  // K elements of one LDS stage
 
-enum Form { kBf16, kHalf, kHalves, kMixed };
+enum Form { kBf16, kHalf, kHalves, kMixed, kBf16Two, kRaw };
 constexpr int parts_of(Form f) { return f == kHalves ? 2 : 1; }
-constexpr int products_of(Form f) { return f == kHalves ? 3 : f == kMixed ? 2 : 1; }
+constexpr bool two_parts_of_b(Form f) { return f == kMixed || f == kBf16Two; }
+constexpr int products_of(Form f) { return f == kHalves ? 3 : two_parts_of_b(f) ? 2 : 1; }
+constexpr bool is_bf16(Form f) { return f == kBf16 || f == kBf16Two; }
 
 struct Operand {
   const uint16_t* p;
   int64_t part;  // elements between parts
   int64_t ld;    // elements between rows (turned: between steps of K)
   int rows;
-  int depth;     // turned: K
+  int depth;     // K
 };
+
+__device__ const uint4 kZeros = {0, 0, 0, 0};  // what K past an operand's depth reads
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) int i32x4_t;
@@ -75,20 +84,31 @@ template <int SIZE, int NW>
 struct Copies<SIZE, NW, false> {  // 8 rows of 64 elements each
   static constexpr int ISSUE = SIZE / (8 * NW);
   const uint16_t* src[ISSUE];
-  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0) {
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
+  int left;  // of K
+  static __device__ __forceinline__ int chunk(int i) {
+    const int r = (threadIdx.x / kWave + NW * i) * 8 + lane_id() / 8;
+    return ((lane_id() & 7) ^ swizzle(r)) * 8;
+  }
+  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0) : left(o.depth - k0) {
 #pragma unroll
     for (int i = 0; i < ISSUE; ++i) {
-      const int r = (wave + NW * i) * 8 + lane / 8;
-      const int kc = (lane & 7) ^ swizzle(r);
-      src[i] = o.p + static_cast<int64_t>(min(r0 + r, o.rows - 1)) * o.ld + k0 + kc * 8;
+      const int r = (threadIdx.x / kWave + NW * i) * 8 + lane_id() / 8;
+      src[i] = o.p + static_cast<int64_t>(min(r0 + r, o.rows - 1)) * o.ld + k0 + chunk(i);
     }
   }
   __device__ __forceinline__ void issue(int k, int64_t part, uint16_t* tile) const {
     const int wave = threadIdx.x / kWave;
+    if (k + kStep <= left) {
 #pragma unroll
-    for (int i = 0; i < ISSUE; ++i)
-      __builtin_amdgcn_global_load_lds(src[i] + part + k, tile + (wave + NW * i) * 512, 16, 0, 0);
+      for (int i = 0; i < ISSUE; ++i)
+        __builtin_amdgcn_global_load_lds(src[i] + part + k, tile + (wave + NW * i) * 512, 16, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < ISSUE; ++i)
+        __builtin_amdgcn_global_load_lds(
+            k + chunk(i) < left ? src[i] + part + k : reinterpret_cast<const uint16_t*>(&kZeros),
+            tile + (wave + NW * i) * 512, 16, 0, 0);
+    }
   }
 };
 
@@ -107,26 +127,56 @@ struct Copies<SIZE, NW, true> {  // 512 / SIZE lines each
   const uint16_t* src[ISSUE];
   int line[ISSUE];
   int64_t ld;
-  int last;
-  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0) {
+  int left;  // of K
+  __device__ __forceinline__ Copies(const Operand& o, int r0, int k0)
+      : ld(o.ld), left(o.depth - k0) {
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    ld = o.ld;
-    last = o.depth - 1;
 #pragma unroll
     for (int i = 0; i < ISSUE; ++i) {
-      const int k = (wave + NW * i) * (512 / SIZE) + lane * 8 / SIZE;
+      line[i] = (wave + NW * i) * (512 / SIZE) + lane * 8 / SIZE;
       const int at = lane * 8 % SIZE;
-      const int r = (((at >> 4) ^ turned_swizzle(k)) & (SIZE / 16 - 1)) * 16 + (at & 15);
-      src[i] = o.p + min(r0 + r, o.rows - 8);
-      line[i] = k0 + k;
+      const int r = (((at >> 4) ^ turned_swizzle(line[i])) & (SIZE / 16 - 1)) * 16 + (at & 15);
+      src[i] = o.p + static_cast<int64_t>(k0) * ld + min(r0 + r, o.rows - 8);
     }
   }
   __device__ __forceinline__ void issue(int k, int64_t part, uint16_t* tile) const {
     const int wave = threadIdx.x / kWave;
+    const uint16_t* const zeros = reinterpret_cast<const uint16_t*>(&kZeros);
+    const bool whole = k + kStep <= left;
+#pragma unroll
+    for (int i = 0; i < ISSUE; ++i) {
+      const uint16_t* const p = src[i] + part + (line[i] + k) * ld;
+      __builtin_amdgcn_global_load_lds(whole || line[i] + k < left ? p : zeros,
+                                       tile + (wave + NW * i) * 512, 16, 0, 0);
+    }
+  }
+};
+
+// Floats, a stage of 32 lines of SIZE as they lie: a lane's reads of a column are spread
+// over the banks by the lanes' columns.  k counts floats.
+template <int SIZE, int NW>
+struct RawTurnedCopies {
+  static constexpr int ISSUE = SIZE / (8 * NW);
+  const uint16_t* src[ISSUE];
+  int64_t ld;
+  int left;
+  static __device__ __forceinline__ int line(int i) {
+    return (threadIdx.x / kWave + NW * i) * (256 / SIZE) + lane_id() * 4 / SIZE;
+  }
+  __device__ __forceinline__ RawTurnedCopies(const Operand& o, int r0, int k0)
+      : ld(o.ld), left(o.depth - k0) {
 #pragma unroll
     for (int i = 0; i < ISSUE; ++i)
-      __builtin_amdgcn_global_load_lds(src[i] + part + min(line[i] + k, last) * ld,
-                                       tile + (wave + NW * i) * 512, 16, 0, 0);
+      src[i] = o.p + (k0 + line(i)) * ld + 2 * min(r0 + lane_id() * 4 % SIZE, o.rows - 4);
+  }
+  __device__ __forceinline__ void issue(int k, uint16_t* tile) const {
+    const int wave = threadIdx.x / kWave;
+#pragma unroll
+    for (int i = 0; i < ISSUE; ++i) {
+      const uint16_t* p = src[i] + k * ld;
+      if (line(i) + k >= left) p = reinterpret_cast<const uint16_t*>(&kZeros);
+      __builtin_amdgcn_global_load_lds(p, tile + (wave + NW * i) * 512, 16, 0, 0);
+    }
   }
 };
 
@@ -218,7 +268,7 @@ struct Walk {
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
 template <Form F>
 __device__ __forceinline__ f32x16_t mfma(i32x4_t a, i32x4_t b, f32x16_t c) {
-  if constexpr (F == kBf16)
+  if constexpr (is_bf16(F))
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   else
@@ -348,7 +398,7 @@ __device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][4], const Fragments& 
     if constexpr (TA && TB) NT_LOAD(NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
     else if constexpr (TA) NT_LOAD(NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
     else NT_LOAD(NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
-  } else if constexpr (F == kBf16) {
+  } else if constexpr (is_bf16(F)) {
 #define NT_MFMA "v_mfma_f32_32x32x16_bf16"
     if constexpr (TA && TB) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
     else if constexpr (TA) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
@@ -463,11 +513,136 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   __syncthreads();  // the stages are free for the epilogue
 }
 
+// Three bfloat16 parts of 8 floats.
+__device__ __forceinline__ void split3(const float (&v)[8], i32x4_t (&part)[3]) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a = v[2 * k], b = v[2 * k + 1];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      const uint32_t w =
+          __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+      part[p][k] = static_cast<int>(w);
+      a -= __uint_as_float(w << 16);
+      b -= __uint_as_float(w & 0xffff0000u);
+    }
+  }
+}
+
+// 8 floats of K step ks of a raw stage: row r of a straight one, column r of a turned one.
+template <int SIZE, bool TURNED>
+__device__ __forceinline__ void read_raw(const uint16_t* tile, int r, int ks, float (&v)[8]) {
+  const int half = lane_id() >> 5;
+  if constexpr (TURNED) {
+    const float* p = reinterpret_cast<const float*>(tile) + (ks * 16 + half * 8) * SIZE + r;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = p[k * SIZE];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // not as a float4: the compiler then waits for every copy in flight first
+      const i32x4_t q = *reinterpret_cast<const i32x4_t*>(
+          tile + tile_offset(r, ks * 4 + half * 2 + h));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * h + k] = __int_as_float(q[k]);
+    }
+  }
+}
+
+template <int SIZE, int NW, bool TURNED>
+struct RawCopies : Copies<SIZE, NW, false> {
+  using Copies<SIZE, NW, false>::Copies;
+  __device__ __forceinline__ void issue(int step, uint16_t* tile) const {
+    Copies<SIZE, NW, false>::issue(step * kStep, 0, tile);
+  }
+};
+template <int SIZE, int NW>
+struct RawCopies<SIZE, NW, true> : RawTurnedCopies<SIZE, NW> {
+  // k0 in 16-bit units, as the straight operand's
+  __device__ __forceinline__ RawCopies(const Operand& o, int r0, int k0)
+      : RawTurnedCopies<SIZE, NW>(o, r0, k0 / 2) {}
+  __device__ __forceinline__ void issue(int step, uint16_t* tile) const {
+    RawTurnedCopies<SIZE, NW>::issue(step * (kStep / 2), tile);
+  }
+};
+
+// mainloop for kRaw: stages of 32 floats of K.
+template <class CF, bool TA, bool TB>
+__device__ __forceinline__ void mainloop_raw(const Operand& A, int m0, const Operand& B, int n0,
+                                             int k0, int ksteps, uint16_t* lds,
+                                             f32x16_t (&acc)[CF::FM][CF::FN]) {
+  f32x16_t small[CF::FM][CF::FN];
+#pragma unroll
+  for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < CF::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = small[i][j][r] = 0.f;
+  const RawCopies<CF::BM, CF::NW, TA> a_copies(A, m0, k0);
+  const RawCopies<CF::BN, CF::NW, TB> b_copies(B, n0, k0);
+  const int wave = threadIdx.x / kWave, lane = lane_id() & 31;
+  const int ra = wave / CF::WAVES_N * CF::WTM + lane, rb = wave % CF::WAVES_N * CF::WTN + lane;
+  constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
+  int fill = 0, ahead = 0;
+  auto copy = [&]() {
+    uint16_t* stage = lds + fill * CF::STAGE;
+    a_copies.issue(ahead, stage);
+    b_copies.issue(ahead, stage + CF::BM * kStep);
+    ++ahead;
+    fill = fill + 1 == CF::STAGES ? 0 : fill + 1;
+  };
+  for (int s = 0; s < AHEAD && s < ksteps; ++s) copy();
+  int cur = 0;
+  for (int s = 0; s < ksteps; ++s) {
+    if (s + AHEAD <= ksteps) meet<(AHEAD - 1) * COPIES>();
+    else meet<0>();
+    if (s + AHEAD < ksteps) copy();
+    const uint16_t* sA = lds + cur * CF::STAGE;
+    const uint16_t* sB = sA + CF::BM * kStep;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      i32x4_t a[CF::FM][3], b[CF::FN][3];
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i) {
+        read_raw<CF::BM, TA>(sA, ra + 32 * i, ks, v);
+        split3(v, a[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < CF::FN; ++j) {
+        read_raw<CF::BN, TB>(sB, rb + 32 * j, ks, v);
+        split3(v, b[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < CF::FN; ++j) {
+          small[i][j] = mfma<kBf16>(a[i][0], b[j][2], small[i][j]);
+          small[i][j] = mfma<kBf16>(a[i][2], b[j][0], small[i][j]);
+          small[i][j] = mfma<kBf16>(a[i][1], b[j][1], small[i][j]);
+          small[i][j] = mfma<kBf16>(a[i][0], b[j][1], small[i][j]);
+          small[i][j] = mfma<kBf16>(a[i][1], b[j][0], small[i][j]);
+          acc[i][j] = mfma<kBf16>(a[i][0], b[j][0], acc[i][j]);
+        }
+    }
+    cur = cur + 1 == CF::STAGES ? 0 : cur + 1;
+  }
+#pragma unroll
+  for (int i = 0; i < CF::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < CF::FN; ++j) acc[i][j] += small[i][j];
+  __syncthreads();  // the stages are free for the epilogue
+}
+
 template <class CF, Form F, bool TA = false, bool TB = false>
 __device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand& B, int n0, int k0,
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
-  if constexpr (CF::FM == 2 && CF::FN == 4)
+  if constexpr (F == kRaw)
+    mainloop_raw<CF, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
+  else if constexpr (CF::FM == 2 && CF::FN == 4)
     mainloop_pipe<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
   else
     mainloop<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
@@ -558,7 +733,6 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
   multiply<CF, F, TA, TB>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
-  const int row0 = mb * CF::BM + block_row<CF>();
   if (ACC) out += static_cast<int64_t>(slice) * pitch * cols;
   if (amax != nullptr) {
     const float f = power_of_two(exponent - exponent_for(*amax));
@@ -569,35 +743,51 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] *= f;
   }
+  // 32 columns of every wave at a time through LDS, so that lines are stored whole: the
+  // 16-byte chunk c of column col at position c ^ col, in two buffers taken in turn
+  constexpr int CHUNKS = CF::BM / 4, COLS = CF::WAVES_N * 32;
+  static_assert((CF::FN > 1 ? 2 : 1) * COLS * CF::BM * 2 <= CF::STAGES * CF::STAGE, "buffers fit");
+  const int wave_cols = threadIdx.x / kWave % CF::WAVES_N * 32 + (lane_id() & 31);
 #pragma unroll
   for (int j = 0; j < CF::FN; ++j) {
-    const int col = nb * CF::BN + block_col<CF>() + 32 * j;
-    if (col >= cols) continue;
-    E* line = out + static_cast<int64_t>(col) * pitch;
+    float* buffer = reinterpret_cast<float*>(lds) + (j & 1) * COLS * CF::BM;
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = row0 + row_of(i, 4 * q);
-        if (row >= pitch) continue;
-        const f32x16_t& c = acc[i][j];
-        if constexpr (sizeof(E) == 2) {
-          typedef ElemTraits<uint16_t> Tr;
-          *reinterpret_cast<uint2*>(line + row) =
-              make_uint2(Tr::from_f32(c[4 * q]) |
-                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 1])) << 16,
-                         Tr::from_f32(c[4 * q + 2]) |
-                             static_cast<uint32_t>(Tr::from_f32(c[4 * q + 3])) << 16);
-        } else {
-          float4* at = reinterpret_cast<float4*>(line + row);
-          float4 v = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
-          if (ACC && add) {
-            const float4 old = *at;
-            v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
-          }
-          *at = v;
-        }
+        const int c = (block_row<CF>() + row_of(i, 4 * q)) / 4;
+        const f32x16_t& v = acc[i][j];
+        *reinterpret_cast<float4*>(buffer + wave_cols * CF::BM +
+                                   ((c ^ wave_cols) & (CHUNKS - 1)) * 4) =
+            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
+    __syncthreads();
+    constexpr int STEP = sizeof(E) == 2 ? 2 : 1;  // chunks of a 16-byte store
+    for (int e = threadIdx.x; e < COLS * CHUNKS / STEP; e += CF::NT) {
+      const int at = e / (CHUNKS / STEP), c = e % (CHUNKS / STEP) * STEP;
+      const int col = nb * CF::BN + at / 32 * CF::WTN + j * 32 + at % 32;
+      const int row = mb * CF::BM + c * 4;
+      if (col >= cols || row >= pitch) continue;
+      E* to = out + static_cast<int64_t>(col) * pitch + row;
+      const float* from = buffer + at * CF::BM;
+      float4 v = *reinterpret_cast<const float4*>(from + ((c ^ at) & (CHUNKS - 1)) * 4);
+      if constexpr (sizeof(E) == 2) {
+        const float4 u =
+            *reinterpret_cast<const float4*>(from + (((c + 1) ^ at) & (CHUNKS - 1)) * 4);
+        typedef ElemTraits<uint16_t> Tr;
+        const auto pair = [](float a, float b) {
+          return Tr::from_f32(a) | static_cast<uint32_t>(Tr::from_f32(b)) << 16;
+        };
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(pair(v.x, v.y), pair(v.z, v.w), pair(u.x, u.y), pair(u.z, u.w));
+      } else {
+        if (ACC && add) {
+          const float4 old = *reinterpret_cast<const float4*>(to);
+          v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
+        }
+        *reinterpret_cast<float4*>(to) = v;
+      }
+    }
   }
 }
 
@@ -606,19 +796,19 @@ typedef Config<256, 256, 4, 2, 2> Big;
 typedef Config<128, 128, 2, 2, 2> Mid;
 typedef Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
 typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32
+constexpr int kFewColumns = 64;
 
 inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 inline int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
 
 enum Tile { kBare, kFew, kMid, kBig };
 template <class F>
-hipError_t with_tile(Tile t, const F& f) {
-  switch (t) {
-    case kBare: return f(Bare());
-    case kFew: return f(Few());
-    case kMid: return f(Mid());
-    default: return f(Big());
-  }
+hipError_t with_few_tile(Tile t, const F& f) {
+  return t == kBare ? f(Bare()) : f(Few());
+}
+template <class F>
+hipError_t with_wide_tile(Tile t, const F& f) {
+  return t == kMid ? f(Mid()) : f(Big());
 }
 inline int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
 inline int tile_cols(Tile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kFew ? 64 : 32; }
@@ -628,17 +818,17 @@ struct Cut {
   Tile tile;
   int slices;
 };
-// At most 64 columns: the narrowest tile, and slices until two workgroups a CU are
-// there.  Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us
-// to fill and to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us),
-// with as many slices as pay for writing and adding up their float32 sums (5 TB/s).
-inline Cut cut_for(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle) {
-  if (cols <= 64 && !triangle) {
-    const Tile t = cols <= 32 ? kBare : kFew;
-    const int64_t tiles = blocks(rows, tile_rows(t));
-    return {t, static_cast<int>(std::clamp<int64_t>(512 / tiles, 1,
-                                                    std::clamp<int64_t>(steps / 4, 1, most_slices)))};
-  }
+// At most kFewColumns columns: the narrowest tile, and slices until two workgroups a CU
+// are there.
+inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices) {
+  const Tile t = cols <= 32 ? kBare : kFew;
+  const int64_t most = std::clamp<int64_t>(steps / 4, 1, most_slices);
+  return {t, static_cast<int>(std::clamp<int64_t>(512 / blocks(rows, tile_rows(t)), 1, most))};
+}
+// Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us to fill and
+// to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us), with as many
+// slices as pay for writing and adding up their float32 sums (5 TB/s).
+inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle) {
   Cut best{kMid, 1};
   double least = 1e300;
   for (const Tile t : {kBig, kMid}) {

@@ -230,9 +230,10 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   p.ldm = static_cast<int>(up64(p.m));
   p.ldn = static_cast<int>(up64(p.n));
   const int gram = PX == 2 ? 3 : 1, update = PX == 2 ? 3 : 2;  // products
-  p.gram = cut_for(p.m, p.m, p.ldn / 64 * gram, 32, true);
-  p.square = cut_for(p.m, p.m, p.ldm / 64 * 3, 32, true);
-  p.update = cut_for(p.n, p.m, p.ldm / 64 * update, 32, false);
+  p.gram = wide_cut(p.m, p.m, p.ldn / 64 * gram, 32, true);
+  p.square = wide_cut(p.m, p.m, p.ldm / 64 * 3, 32, true);
+  p.update = p.m <= kFewColumns ? few_cut(p.n, p.m, p.ldm / 64 * update, 32)
+                                : wide_cut(p.n, p.m, p.ldm / 64 * update, 32, false);
   const size_t square = static_cast<size_t>(p.m) * p.ldm, whole = static_cast<size_t>(p.m) * p.ldn;
   Carve c{static_cast<char*>(ws)};
   p.norm = c.take<double>(kNormBlocks);
@@ -246,18 +247,24 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   return p;
 }
 
+template <Form F, class CF>
+hipError_t product(CF, const Operand& A, const Operand& B, int ksteps, const Cut& cut,
+                   bool triangle, int pitch, float* sums, hipStream_t s) {
+  const int mb = static_cast<int>(blocks(A.rows, CF::BM));
+  const int nb = static_cast<int>(blocks(B.rows, CF::BN));
+  const uint32_t tiles =
+      triangle ? static_cast<uint32_t>(mb) * (mb + 1) / 2 : static_cast<uint32_t>(mb) * nb;
+  product_kernel<CF, F, false, false, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
+      A, B, ksteps, mb, triangle ? 0 : nb, B.rows, false, pitch, nullptr, 0, sums);
+  return hipGetLastError();
+}
+
+// sums = A A^T, by its triangle of tiles.
 template <Form F>
-hipError_t product(const Operand& A, const Operand& B, int ksteps, const Cut& cut, bool triangle,
-                   int pitch, float* sums, hipStream_t s) {
-  return with_tile(cut.tile, [&](auto cf) {
-    typedef decltype(cf) CF;
-    const int mb = static_cast<int>(blocks(A.rows, CF::BM));
-    const int nb = static_cast<int>(blocks(B.rows, CF::BN));
-    const uint32_t tiles = triangle ? static_cast<uint32_t>(mb) * (mb + 1) / 2
-                                    : static_cast<uint32_t>(mb) * nb;
-    product_kernel<CF, F, false, false, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
-        A, B, ksteps, mb, triangle ? 0 : nb, B.rows, false, pitch, nullptr, 0, sums);
-    return hipGetLastError();
+hipError_t square_of(const Operand& A, int ksteps, const Cut& cut, int pitch, float* sums,
+                     hipStream_t s) {
+  return with_wide_tile(cut.tile, [&](auto cf) {
+    return product<F>(cf, A, A, ksteps, cut, true, pitch, sums, s);
   });
 }
 
@@ -306,10 +313,10 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   double bound = 1.0;  // of X's singular values
   int ex = exponent_below(bound);
   orth_start_kernel<E, X><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
-  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m, 0};
-  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n, 0};
-  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, 0};
-  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, 0};
+  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m, p.ldn};
+  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n, p.ldm};
+  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, p.ldm};
+  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, p.ldm};
   E* no_output = nullptr;
   for (int i = 0; i < a.steps; ++i) {
     const bool end = i + 1 == a.steps;
@@ -320,19 +327,24 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
     const int next = exponent_below(bound);
     // factors with the powers of two of what goes in undone and of what comes out applied
     const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
-    hipError_t e = product<X>(xo, xo, p.ldn / 64, p.gram, true, p.ldm, p.sums, s);
+    hipError_t e = square_of<X>(xo, p.ldn / 64, p.gram, p.ldm, p.sums, s);
     if (e != hipSuccess) return e;
     orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.gram.slices,
                                                           tile_rows(p.gram.tile), p.ldm, 0.f,
                                                  factor(1, eg - 2 * ex), none, g, no_output, false);
-    if ((e = product<kHalves>(go, go, p.ldm / 64, p.square, true, p.ldm, p.sums, s)) != hipSuccess)
+    if ((e = square_of<kHalves>(go, p.ldm / 64, p.square, p.ldm, p.sums, s)) != hipSuccess)
       return e;
     orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.square.slices,
                                                           tile_rows(p.square.tile), p.ldm,
                                                  factor(a.b, eb - eg), factor(a.c, eb - 2 * eg), g,
                                                  b, no_output, false);
-    if ((e = product<X == kHalf ? kMixed : kHalves>(xt, bo, p.ldm / 64, p.update, false, p.ldn, p.sums, s)) != hipSuccess)
-      return e;
+    const auto update = [&](auto cf) {
+      return product<X == kHalf ? kMixed : kHalves>(cf, xt, bo, p.ldm / 64, p.update, false, p.ldn,
+                                                    p.sums, s);
+    };
+    e = p.m <= kFewColumns ? with_few_tile(p.update.tile, update)
+                           : with_wide_tile(p.update.tile, update);
+    if (e != hipSuccess) return e;
     const double scale = end ? a.scale : 1.0;
     const int out = end ? 0 : next;
     orth_finish_kernel<E, X><<<whole, 256, 0, s>>>(
