@@ -15,7 +15,9 @@
 // as two parts).  With float32 ones every operand is two half-precision parts
 // (nt_gemm.h), w scaled by its largest element, x by each row's; dl / g lies in [-1, 1]
 // and is scaled by 2^14, with g taken into dx at the end and into the x of dw.  With few
-// rows, where reading w is what the call costs, float32 operands and dl stay float32.
+// rows, where reading w is what the call costs, float32 operands and dl stay float32, and
+// z is formed with K cut in slices where the vocabulary alone gives too few workgroups to
+// keep the memory busy, so it goes through the workspace (n_rows of a piece of it).
 // Both products read w, x and dl as they lie, turning fragments with LDS transpose
 // reads where K runs along a column.
 #include <algorithm>
@@ -196,15 +198,9 @@ __global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, const float* _
   for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
     float v[8] = {};
     if (live) load_run(src + c, v);
-    if constexpr (F == kRaw) {
-      float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + row * a.d + c);
-      to[0] = make_float4(v[0], v[1], v[2], v[3]);
-      to[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
-      put_run<F>(out + row * a.d, a.n_rows * a.d, c, v);
-    }
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * g * f;
+    put_run<F>(out + row * a.d, a.n_rows * a.d, c, v);
   }
 }
 
@@ -303,47 +299,111 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
   }
 }
 
+// {m, s} of two disjoint sets of columns, as one.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float base = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - base) * kLog2e) +
+                            b.y * __builtin_amdgcn_exp2f((b.x - base) * kLog2e));
+}
+
+struct RowResults {
+  const void* targets;
+  int index_bytes, vocab;
+  float *logp, *lse;
+  float2* stats;
+};
+__device__ __forceinline__ void finish_row(const RowResults& o, int64_t n, float2 p,
+                                           const float* target_z) {
+  const float base = p.x == -INFINITY ? 0.f : p.x;
+  const float log_s = logf(p.y);  // -inf for a row with nothing left
+  o.stats[n] = p;
+  o.lse[n] = base + log_s;
+  float lp = 0.f;
+  // a row with nothing left: z - lse would be -inf + inf
+  if (has_target(o.targets, o.index_bytes, o.vocab, n))
+    lp = p.x == -INFINITY && p.y == 0.f ? -INFINITY : *target_z - base - log_s;
+  o.logp[n] = lp;
+}
+
 // Joins the tiles' {m, s} of 16 tokens a workgroup, in 16 streams of tiles.
 __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ parts,
                                                         int tiles, int64_t n_rows,
-                                                        const void* __restrict__ targets,
-                                                        int index_bytes, int vocab,
                                                         const float* __restrict__ target_z,
-                                                        float* __restrict__ logp,
-                                                        float* __restrict__ lse,
-                                                        float2* __restrict__ stats) {
+                                                        RowResults o) {
   __shared__ float2 joint[16][16];
   const int col = threadIdx.x % 16, stream = threadIdx.x / 16;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 16 + col;
-  float m = -INFINITY, s = 0.f;
+  float2 p = make_float2(-INFINITY, 0.f);
   if (n < n_rows)
-    for (int t = stream; t < tiles; t += 16) {
-      const float2 p = parts[t * n_rows + n];
-      const float top = fmaxf(m, p.x);
-      const float base = top == -INFINITY ? 0.f : top;
-      s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) +
-          p.y * __builtin_amdgcn_exp2f((p.x - base) * kLog2e);
-      m = top;
-    }
-  joint[stream][col] = make_float2(m, s);
+    for (int t = stream; t < tiles; t += 16) p = join(p, parts[t * n_rows + n]);
+  joint[stream][col] = p;
   __syncthreads();
   if (stream != 0 || n >= n_rows) return;
-  m = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) m = fmaxf(m, joint[w][col].x);
+  for (int w = 1; w < 16; ++w) p = join(p, joint[w][col]);
+  finish_row(o, n, p, target_z + n);
+}
+
+// ---------------------------------------------------------------- few rows
+// z of 4 columns from v: the slices' sums in their order, times scale.
+struct FewZ {
+  const float* sums;  // [slices][n_rows][pitch]
+  int slices, pitch;
+  int rows, v0;       // of the vocabulary
+  float scale;
+};
+__device__ __forceinline__ float4 few_z(const FewZ& z, int64_t n_rows, int64_t n, int v) {
+  float4 t = make_float4(0, 0, 0, 0);
+  for (int s = 0; s < z.slices; ++s) {
+    const float4 q = *reinterpret_cast<const float4*>(z.sums + (s * n_rows + n) * z.pitch + v);
+    t = make_float4(t.x + q.x, t.y + q.y, t.z + q.z, t.w + q.w);
+  }
+  return make_float4(t.x * z.scale, t.y * z.scale, t.z * z.scale, t.w * z.scale);
+}
+
+// {m, s} of kFewChunk columns of a row a workgroup: to parts, or, where one holds the whole
+// vocabulary, the row's results.
+constexpr int kFewChunk = 4096;
+__global__ __launch_bounds__(256) void head_few_stats_kernel(FewZ z, int64_t n_rows,
+                                                             float2* __restrict__ parts,
+                                                             float* __restrict__ target_z,
+                                                             RowResults o) {
+  __shared__ float2 joint[4];
+  const int64_t n = blockIdx.y;
+  const int64_t t = target_of(o.targets, o.index_bytes, n) - z.v0;
+  float v[kFewChunk / 1024][4];
+  float m = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kFewChunk / 1024; ++u) {
+    const int c = blockIdx.x * kFewChunk + (u * 256 + threadIdx.x) * 4;
+    const bool some = c < z.rows;
+    const float4 q = some ? few_z(z, n_rows, n, c) : make_float4(0, 0, 0, 0);
+    v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c + k >= z.rows) v[u][k] = -INFINITY;
+      else if (c + k == t) target_z[n] = v[u][k];
+      m = fmaxf(m, v[u][k]);
+    }
+  }
   const float base = m == -INFINITY ? 0.f : m;
-  s = 0.f;
+  float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < 16; ++w)
-    s += joint[w][col].y * __builtin_amdgcn_exp2f((joint[w][col].x - base) * kLog2e);
-  const float log_s = logf(s);  // -inf for a row with nothing left
-  const int64_t t = target_of(targets, index_bytes, n);
-  stats[n] = make_float2(m, s);
-  lse[n] = base + log_s;
-  float lp = 0.f;
-  // a row with nothing left: z - lse would be -inf + inf
-  if (t >= 0 && t < vocab) lp = m == -INFINITY && s == 0.f ? -INFINITY : target_z[n] - base - log_s;
-  logp[n] = lp;
+  for (int u = 0; u < kFewChunk / 1024; ++u)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += __builtin_amdgcn_exp2f((v[u][k] - base) * kLog2e);
+  float2 p = make_float2(m, s);
+#pragma unroll
+  for (int h = 1; h < kWave; h *= 2)
+    p = join(p, make_float2(__shfl_xor(p.x, h), __shfl_xor(p.y, h)));
+  if (lane_id() == 0) joint[threadIdx.x / kWave] = p;
+  __threadfence_block();
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  p = join(join(joint[0], joint[1]), join(joint[2], joint[3]));
+  if (parts != nullptr) parts[blockIdx.x * n_rows + n] = p;
+  else finish_row(o, n, p, target_z + n);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -353,13 +413,7 @@ __device__ __forceinline__ uint32_t pack_part(float a, float b, int p) {
   if constexpr (F == kBf16) {
     typedef __attribute__((ext_vector_type(2))) float f32x2_t;
     typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
-    uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-    if (p == 1)  // what the first part leaves
-      w = __builtin_bit_cast(
-          uint32_t, __builtin_convertvector(f32x2_t{a - __uint_as_float(w << 16),
-                                                    b - __uint_as_float(w & 0xffff0000u)},
-                                            bf16x2_t));
-    return w;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
   } else {
     _Float16 x = static_cast<_Float16>(a), y = static_cast<_Float16>(b);
     if (p == 1) {  // what the first part leaves; |a| is at most 2^14, or NaN
@@ -381,11 +435,11 @@ struct DlArgs {
   int index_bytes;
   const float2* stats;
   const float* dlogp;
-  uint16_t* dl;  // [parts][n][ldv]; raw: float [n][ldv]
+  uint16_t* dl;  // [parts][n][ldv]
   int ldv;
 };
 
-template <class CF, Form F, int PARTS>
+template <class CF, Form F>
 __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks, int n_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
   int mb, nb;
@@ -432,29 +486,12 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
           if (rel == nt::row_of(i, r)) acc[i][j][r] += g;
     }
   }
-  if constexpr (F == kRaw) {
-#pragma unroll
-    for (int j = 0; j < CF::FN; ++j) {
-      const int n = nb * CF::BN + nt::block_col<CF>() + 32 * j;
-#pragma unroll
-      for (int i = 0; i < CF::FM; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int v = row0 + nt::row_of(i, 4 * q);
-          if (n < n_rows && v < a.ldv)
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.dl) + n * int64_t{a.ldv} + v) =
-                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                            acc[i][j][4 * q + 3]);
-        }
-    }
-    return;
-  }
   // a part at a time through LDS, so that its rows are stored whole: the 16-byte chunk c
   // of row n at position c ^ n, which spreads the 32 rows of a write over the banks
   constexpr int CHUNKS = CF::BM / 8;
   static_assert(CF::BM * CF::BN <= CF::STAGES * CF::STAGE, "the tile fits the stages");
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p) {
+  for (int p = 0; p < parts_of(F); ++p) {
     if (p > 0) __syncthreads();
 #pragma unroll
     for (int j = 0; j < CF::FN; ++j) {
@@ -484,35 +521,202 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   }
 }
 
-// dx = the sum of the slices, rounded; 8 elements a lane.  Halves: times scale * dlogp
-// of the row and the powers of two undone.
+// dx = the sum of the slices, rounded: 4 elements a lane, the slices in 4 streams.  Halves:
+// times scale * dlogp of the row and the powers of two undone.
 template <typename E, Form F>
 __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* __restrict__ sums,
                                                       int slices, const float* __restrict__ dlogp,
                                                       const float* amax, E* __restrict__ dx) {
+  __shared__ float4 joint[3][64];
   const int64_t elems = a.n_rows * a.d;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= elems) return;
-  float v[8] = {};
-  for (int s = 0; s < slices; ++s) {
-    float p[8];
-    load_run(sums + s * elems + i, p);
+  const int at = threadIdx.x % 64, stream = threadIdx.x / 64;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 64 + at) * 4;
+  float4 v = make_float4(0, 0, 0, 0);
+  if (i < elems)
+#pragma unroll 8
+    for (int s = stream; s < slices; s += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(sums + s * elems + i);
+      v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
+    }
+  if (slices > 1) {
+    if (stream > 0) joint[stream - 1][at] = v;
+    __syncthreads();
+    if (stream == 0)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += p[k];
+      for (int w = 0; w < 3; ++w) {
+        const float4 q = joint[w][at];
+        v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
+      }
   }
+  if (stream != 0 || i >= elems) return;
   if constexpr (F == kHalves) {
     const int64_t n = i / a.d;
     const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
-    const float g = given ? dlogp[n] * a.scale : 0.f;
     const float f = power_of_two(-kDlExponent - exponent_for(*amax));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = given ? v[k] * f * g : 0.f;
+    const float g = given ? dlogp[n] * a.scale : 0.f;
+    v = given ? make_float4(v.x * f * g, v.y * f * g, v.z * f * g, v.w * f * g)
+              : make_float4(0, 0, 0, 0);
   }
-  if constexpr (sizeof(E) == 2) {
-    put_run<kBf16>(reinterpret_cast<uint16_t*>(dx) + i, 0, 0, v);
-  } else {
-    *reinterpret_cast<float4*>(dx + i) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(dx + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  if constexpr (sizeof(E) == 2)
+    *reinterpret_cast<uint2*>(dx + i) = make_uint2(pack_part<kBf16>(v.x, v.y, 0),
+                                                   pack_part<kBf16>(v.z, v.w, 0));
+  else
+    *reinterpret_cast<float4*>(dx + i) = v;
+}
+
+// Few rows: bfloat16 parts of dl that the products take, and of the x of dw.
+template <Form F>
+constexpr int kFewDlParts = F == kRaw ? 3 : 2;
+template <Form F>
+constexpr int kFewXParts = F == kRaw ? 3 : 1;
+
+// Few rows: dl of 64 columns of the vocabulary a workgroup, for dx (raw: float [n_rows]
+// [ldv]; bfloat16: two parts of that) and for dw (parts [rows][kn], kn the rows rounded up
+// to 16).
+template <Form F>
+__global__ __launch_bounds__(256) void head_few_dl_kernel(HeadArgs a, FewZ z,
+                                                          const float2* __restrict__ stats,
+                                                          const float* __restrict__ dlogp,
+                                                          uint16_t* __restrict__ dl, int ldv,
+                                                          uint16_t* __restrict__ dlt, int kn) {
+  constexpr int PARTS = kFewDlParts<F>;
+  __shared__ float tile[kFewColumns][65];
+  const int n_rows = static_cast<int>(a.n_rows);
+  const int c = threadIdx.x % 16 * 4, v = blockIdx.x * 64 + c;
+#pragma unroll
+  for (int u = 0; u < kFewColumns / 16; ++u) {
+    const int n = u * 16 + threadIdx.x / 16;
+    float d[4] = {};
+    if (n < n_rows) {
+      const int64_t t = target_of(a.targets, a.index_bytes, n);
+      const float2 st = stats[n];
+      const bool given = t >= 0 && t < a.vocab && !(st.x == -INFINITY && st.y == 0.f);
+      if (given && v < z.rows) {
+        const float g = dlogp[n] * a.scale, share = -g / st.y;
+        const float4 q = few_z(z, n_rows, n, v);
+        const float zs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          d[k] = share * __builtin_amdgcn_exp2f((zs[k] - st.x) * kLog2e);
+          if (v + k == t - z.v0) d[k] += g;
+          if (v + k >= z.rows) d[k] = 0.f;
+        }
+      }
+      if constexpr (F == kRaw) {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(dl) + static_cast<int64_t>(n) * ldv +
+                                   v) = make_float4(d[0], d[1], d[2], d[3]);
+      } else {
+        float e[4] = {d[0], d[1], d[2], d[3]};
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint2 w = make_uint2(pack_part<kBf16>(e[0], e[1], 0),
+                                     pack_part<kBf16>(e[2], e[3], 0));
+          *reinterpret_cast<uint2*>(dl + (static_cast<int64_t>(p) * n_rows + n) * ldv + v) = w;
+          e[0] -= __uint_as_float(w.x << 16), e[1] -= __uint_as_float(w.x & 0xffff0000u);
+          e[2] -= __uint_as_float(w.y << 16), e[3] -= __uint_as_float(w.y & 0xffff0000u);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tile[n][c + k] = d[k];
+  }
+  __syncthreads();
+  const int col = threadIdx.x / 4, n0 = threadIdx.x % 4 * 16;
+  const int64_t row = blockIdx.x * 64 + col;
+  if (row >= z.rows || n0 >= kn) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = tile[n0 + h * 8 + k][col];
+    i32x4_t part[3];
+    split3(e, part);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+      *reinterpret_cast<i32x4_t*>(dlt + (static_cast<int64_t>(p) * z.rows + row) * kn + n0 +
+                                  h * 8) = part[p];
+  }
+}
+
+// Few rows: dw[v][c] = sum over n of dl[n][v] x[n][c] over the rows n with a target, 128
+// columns c a workgroup.  x's parts stay in LDS; a wave takes 32 v at a time, with 4 c to a
+// lane (columns 4 l + j of block j), so that a lane stores 4 adjacent ones: what bounds it
+// is writing dw.
+template <Form F>
+__global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint16_t* __restrict__ dlt,
+                                                          int rows, int kn, void* __restrict__ out) {
+  constexpr int PA = kFewDlParts<F>, PB = kFewXParts<F>;
+  constexpr int PITCH = kFewColumns + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[PB][128][PITCH];
+  typedef std::conditional_t<F == kBf16, uint16_t, float> E;
+  const int c0 = blockIdx.x * 128;
+  // x[8 rows from n0][column], transposed
+  for (int e = threadIdx.x; e < 128 * (kn / 8); e += 256) {
+    const int col = e % 128, n0 = e / 128 * 8;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int n = n0 + k;
+      const bool live = n < a.n_rows && c0 + col < a.d &&
+                        has_target(a.targets, a.index_bytes, a.vocab, n);
+      v[k] = live ? ElemTraits<E>::to_f32(static_cast<const E*>(a.x)[static_cast<int64_t>(n) * a.d +
+                                                                    c0 + col])
+                  : 0.f;
+    }
+    i32x4_t part[3];
+    split3(v, part);
+    const int place = col % 4 * 32 + col / 4;  // column 4 l + j in row 32 j + l
+#pragma unroll
+    for (int p = 0; p < PB; ++p) *reinterpret_cast<i32x4_t*>(&lds[p][place][n0]) = part[p];
+  }
+  __syncthreads();
+  const int l = lane_id() & 31, half = lane_id() >> 5;
+  const int waves = gridDim.y * 4;
+  for (int v0 = (blockIdx.y * 4 + threadIdx.x / kWave) * 32; v0 < rows; v0 += waves * 32) {
+    const int v = min(v0 + l, rows - 1);
+    f32x16_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+    i32x4_t f[kFewColumns / 16][PA];
+#pragma unroll
+    for (int ks = 0; ks < kFewColumns / 16; ++ks)
+      if (ks * 16 < kn)
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+          f[ks][p] = *reinterpret_cast<const i32x4_t*>(
+              dlt + (static_cast<int64_t>(p) * rows + v) * kn + ks * 16 + half * 8);
+#pragma unroll
+    for (int ks = 0; ks < kFewColumns / 16; ++ks)
+      if (ks * 16 < kn)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          i32x4_t b[PB];
+#pragma unroll
+          for (int p = 0; p < PB; ++p)
+            b[p] = *reinterpret_cast<const i32x4_t*>(&lds[p][32 * j + l][ks * 16 + half * 8]);
+          // the small products first; those under 2^-24 are left out
+#pragma unroll
+          for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+              if (sum - p >= 0 && sum - p < PB) acc[j] = mfma<kBf16>(f[ks][p], b[sum - p], acc[j]);
+        }
+    if (c0 + 4 * l >= a.d) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = v0 + 4 * half + row_of(0, r);
+      if (row >= rows) continue;
+      const int64_t at = static_cast<int64_t>(row) * a.d + c0 + 4 * l;
+      if constexpr (F == kBf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+            make_uint2(pack_part<kBf16>(acc[0][r], acc[1][r], 0),
+                       pack_part<kBf16>(acc[2][r], acc[3][r], 0));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) =
+            make_float4(acc[0][r], acc[1][r], acc[2][r], acc[3][r]);
+    }
   }
 }
 
@@ -532,7 +736,6 @@ int piece_of(int vocab, size_t per_column, size_t budget) {
   return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
 }
 
-constexpr size_t kFewPiece = size_t{96} << 20;  // bytes of w
 constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
 
 // The form of the operands; and the stages of a product over k.
@@ -540,7 +743,42 @@ Form form_of(int elem_bytes, int64_t n) {
   return elem_bytes == 2 ? kBf16 : n <= kFewColumns ? kRaw : kHalves;
 }
 int stages(Form f, int64_t k) { return static_cast<int>(blocks(k, f == kRaw ? 32 : 64)); }
-int dl_parts(Form f, int64_t n) { return f == kBf16 && n <= kFewColumns ? 2 : parts_of(f); }
+
+// Few rows, forward and backward: z of a piece of the vocabulary through the workspace.
+struct FewPlan {
+  int piece, kn;
+  Cut z_cut, dx_cut;
+  float *z, *target_z, *sums;
+  float2* parts;
+  uint16_t *dl, *dlt;
+  size_t bytes;
+};
+constexpr size_t kFewPiece = size_t{96} << 20;  // bytes of w that the Infinity Cache still
+                                                // holds when dx reads them
+FewPlan few_plan(const HeadArgs& a, int elem_bytes, bool backward, void* ws) {
+  FewPlan p{};
+  const Form f = form_of(elem_bytes, a.n_rows);
+  const size_t n = a.n_rows;
+  p.piece = backward ? piece_of(a.vocab, static_cast<size_t>(a.d) * elem_bytes, kFewPiece)
+                     : piece_of(a.vocab, 4 * n, size_t{64} << 20);
+  p.kn = static_cast<int>(blocks(n, 16) * 16);
+  p.z_cut = few_cut(p.piece, n, stages(f, a.d), 32);
+  const size_t ldv = up64(p.piece);
+  Carve c{static_cast<char*>(ws)};
+  p.z = c.take<float>(p.z_cut.slices * n * ldv);
+  if (backward) {
+    p.dx_cut = few_cut(a.d, n, stages(f, ldv) * (f == kBf16 ? 2 : 1), 32);
+    p.dl = c.take<uint16_t>(2 * n * ldv);  // floats, or two parts
+    p.dlt = c.take<uint16_t>((f == kRaw ? 3 : 2) * ldv * p.kn);
+    p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
+  } else {
+    // pieces but the last are whole chunks
+    p.parts = c.take<float2>(blocks(a.vocab, kFewChunk) * n + blocks(a.vocab, p.piece) * n);
+    p.target_z = c.take<float>(n);
+  }
+  p.bytes = c.used;
+  return p;
+}
 
 struct ForwardPlan {
   int piece, tiles;
@@ -557,9 +795,7 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const size_t ld = up64(a.d), part_bytes = 2 * parts_of(f) * ld;
   // pieces but the last are whole tiles
   p.piece = f == kHalves ? piece_of(a.vocab, part_bytes, size_t{128} << 20) : a.vocab;
-  const int64_t steps = stages(f, a.d) * products_of(f);
-  p.tile = a.n_rows <= kFewColumns ? few_cut(p.piece, a.n_rows, steps, 1).tile
-                                   : wide_cut(p.piece, a.n_rows, steps, 1, false).tile;
+  p.tile = wide_cut(p.piece, a.n_rows, stages(f, a.d) * products_of(f), 1, false).tile;
   p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(p.tile)));
   Carve c{static_cast<char*>(ws)};
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
@@ -585,31 +821,21 @@ struct BackwardPlan {
 BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   BackwardPlan p{};
   const Form f = form_of(elem_bytes, a.n_rows);
-  const bool few = a.n_rows <= kFewColumns;
-  const size_t ld = up64(a.d), n = a.n_rows;
-  const size_t element = f == kRaw ? 4 : 2 * dl_parts(f, n);  // bytes of a place of dl
-  // few rows: a piece of w that the Infinity Cache still holds when dx reads it
-  const size_t per_column = few ? static_cast<size_t>(a.d) * elem_bytes
-                                : n * element + (f == kHalves ? 4 * ld : 0);
-  p.piece = piece_of(a.vocab, per_column, few ? kFewPiece : size_t{192} << 20);
+  const size_t P = parts_of(f), ld = up64(a.d), n = a.n_rows;
+  p.piece = piece_of(a.vocab, 2 * P * n + (f == kHalves ? 2 * P * ld : 0), size_t{192} << 20);
   const size_t ldv = up64(p.piece);
+  p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false).tile;
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  if (few) {
-    p.dl_tile = few_cut(p.piece, n, 1, 1).tile;
-    p.dx_cut = few_cut(a.d, n, stages(f, ldv) * (f == kBf16 ? 2 : 1), 32);
-  } else {
-    p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false).tile;
-    p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false);
-  }
+  p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false);
   Carve c{static_cast<char*>(ws)};
-  p.gx = c.take<uint16_t>((f == kBf16 ? 1 : 2) * n * a.d);
-  p.dl = c.take<uint16_t>(element / 2 * n * ldv);
+  p.gx = c.take<uint16_t>(P * n * a.d);
+  p.dl = c.take<uint16_t>(P * n * ldv);
   p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
   if (f == kHalves) {
     p.amax = c.take<float>(kAmax);
     p.undo = c.take<float>(n);
-    p.xp = c.take<uint16_t>(2 * ld * n);
-    p.wp = c.take<uint16_t>(2 * ld * p.piece);
+    p.xp = c.take<uint16_t>(P * ld * n);
+    p.wp = c.take<uint16_t>(P * ld * p.piece);
   }
   p.bytes = c.used;
   return p;
@@ -646,12 +872,8 @@ Operand w_operand(const HeadArgs& a, int64_t v0, int rows, const float* amax, ui
   return Operand{wp, static_cast<int64_t>(rows) * ld, ld, rows, ld};
 }
 
-// f(tile) with the tiles for few rows or for many; raw: few.
-template <Form F, class Call>
-hipError_t with_tile(bool few, Tile t, const Call& f) {
-  if constexpr (F == kRaw) return with_few_tile(t, f);
-  else if constexpr (F == kHalves) return with_wide_tile(t, f);
-  else return few ? with_few_tile(t, f) : with_wide_tile(t, f);
+RowResults row_results(const HeadArgs& a, float* logp, float* lse, float* stats) {
+  return RowResults{a.targets, a.index_bytes, a.vocab, logp, lse, reinterpret_cast<float2*>(stats)};
 }
 
 template <Form F>
@@ -666,7 +888,7 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
     const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, p.amax,
                       p.undo, a.targets, a.index_bytes,
                       p.parts + v0 / tile_rows(p.tile) * a.n_rows, p.target_z};
-    const hipError_t e = with_tile<F>(n <= kFewColumns, p.tile, [&](auto cf) {
+    const hipError_t e = with_wide_tile(p.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       head_stats_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
@@ -675,26 +897,21 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
     if (e != hipSuccess) return e;
   }
   head_join_kernel<<<static_cast<uint32_t>(blocks(n, 16)), 256, 0, s>>>(
-      p.parts, p.tiles, a.n_rows, a.targets, a.index_bytes, a.vocab, p.target_z, logp, lse,
-      reinterpret_cast<float2*>(stats));
+      p.parts, p.tiles, a.n_rows, p.target_z, row_results(a, logp, lse, stats));
   return hipGetLastError();
 }
 
-// FEW: at most kFewColumns rows.
-template <Form F, bool FEW>
+template <Form F>
 hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, void* ws, void* dx,
                     void* dw, hipStream_t s) {
   typedef std::conditional_t<F == kBf16, uint16_t, float> E;
-  constexpr int PARTS = F == kBf16 && FEW ? 2 : parts_of(F);  // dl_parts
-  constexpr Form PRODUCT = F == kBf16 && FEW ? kBf16Two : F;
   const BackwardPlan p = backward_plan(a, sizeof(E), ws);
   const int n = static_cast<int>(a.n_rows);
   const float* const amax_w = F == kHalves ? p.amax : nullptr;
   const float* const amax_x = F == kHalves ? p.amax + 1 : nullptr;
-  const int per = F == kRaw ? 2 : 1;  // 16-bit units of an element
   const Operand x = x_operand<F>(a, dlogp, p.amax, p.undo, p.xp, s);
   head_gx_kernel<F><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, dlogp, amax_x, p.gx);
-  const Operand gx{p.gx, a.n_rows * a.d, static_cast<int64_t>(per) * a.d, a.d, n};
+  const Operand gx{p.gx, a.n_rows * a.d, a.d, a.d, n};
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const int ldv = static_cast<int>(up64(rows));
@@ -702,67 +919,152 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     const DlArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, amax_w, p.undo,
                    a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
                    ldv};
-    hipError_t e = with_tile<F>(FEW, p.dl_tile, [&](auto cf) {
+    hipError_t e = with_wide_tile(p.dl_tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      if constexpr ((CF::BN <= kFewColumns) == FEW)
-        head_dl_kernel<CF, F, PARTS><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
+      head_dl_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
     // dx: K is the vocabulary, along w's columns; dw: K is the rows, along dl's and gx's
     const int64_t dl_part = a.n_rows * ldv;
     const Operand wt{w.p, w.part, w.ld, a.d, rows};
-    const Operand dl{p.dl, dl_part, static_cast<int64_t>(per) * ldv, n, per * ldv};
-    const Operand dlt{p.dl, dl_part, static_cast<int64_t>(per) * ldv, ldv, n};
-    e = with_tile<F>(FEW, p.dx_cut.tile, [&](auto cf) {
+    const Operand dl{p.dl, dl_part, ldv, n, ldv};
+    const Operand dlt{p.dl, dl_part, ldv, ldv, n};
+    e = with_wide_tile(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      if constexpr ((CF::BN <= kFewColumns) == FEW)
-        product_kernel<CF, PRODUCT, true, false, float, true>
-            <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
-                wt, dl, stages(F, ldv), mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
+      product_kernel<CF, F, true, false, float, true>
+          <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
+              wt, dl, stages(F, ldv), mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const auto dw_product = [&](auto cf) {
+    const Cut dw_cut = wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false);
+    e = with_wide_tile(dw_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      product_kernel<CF, PRODUCT, true, true, E, false>
+      product_kernel<CF, F, true, true, E, false>
           <<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
               gx, dlt, stages(F, n), mb, nb, rows, false, a.d, amax_x, -kDlExponent,
               static_cast<E*>(dw) + v0 * a.d);
       return hipGetLastError();
-    };
-    if constexpr (FEW)
-      e = dw_product(Mid());
-    else
-      e = with_wide_tile(wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false).tile,
-                         dw_product);
+    });
     if (e != hipSuccess) return e;
   }
-  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d / 8, 256)), 256, 0, s>>>(
+  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d, 256)), 256, 0, s>>>(
       a, p.sums, p.dx_cut.slices, dlogp, amax_w, static_cast<E*>(dx));
+  return hipGetLastError();
+}
+
+// Few rows: z = x w^T of a piece, in slices of K.
+template <Form F>
+hipError_t few_z_product(const HeadArgs& a, const FewPlan& p, int64_t v0, int rows,
+                         hipStream_t s) {
+  const Operand x = x_operand<F>(a, nullptr, nullptr, nullptr, nullptr, s);
+  const Operand w = w_operand<F>(a, v0, rows, nullptr, nullptr, s);
+  return with_few_tile(p.z_cut.tile, [&](auto cf) {
+    typedef decltype(cf) CF;
+    const int mb = static_cast<int>(blocks(rows, CF::BM));
+    product_kernel<CF, F, false, false, float, true>
+        <<<dim3(mb, p.z_cut.slices), CF::NT, 0, s>>>(w, x, stages(F, a.d), mb, 1, x.rows, false,
+                                                     static_cast<int>(up64(rows)), nullptr, 0, p.z);
+    return hipGetLastError();
+  });
+}
+
+FewZ few_z_of(const HeadArgs& a, const FewPlan& p, int64_t v0, int rows) {
+  return FewZ{p.z, p.z_cut.slices, static_cast<int>(up64(rows)), rows, static_cast<int>(v0),
+              a.scale};
+}
+
+template <Form F>
+hipError_t few_forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* stats,
+                       hipStream_t s) {
+  const FewPlan p = few_plan(a, F == kBf16 ? 2 : 4, false, ws);
+  const RowResults o = row_results(a, logp, lse, stats);
+  const bool whole = a.vocab <= kFewChunk;
+  int chunks = 0;
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+    const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
+    const hipError_t e = few_z_product<F>(a, p, v0, rows, s);
+    if (e != hipSuccess) return e;
+    const int more = static_cast<int>(blocks(rows, kFewChunk));
+    head_few_stats_kernel<<<dim3(more, static_cast<uint32_t>(a.n_rows)), 256, 0, s>>>(
+        few_z_of(a, p, v0, rows), a.n_rows, whole ? nullptr : p.parts + chunks * a.n_rows,
+        p.target_z, o);
+    chunks += more;
+  }
+  if (!whole)
+    head_join_kernel<<<static_cast<uint32_t>(blocks(a.n_rows, 16)), 256, 0, s>>>(
+        p.parts, chunks, a.n_rows, p.target_z, o);
+  return hipGetLastError();
+}
+
+template <Form F>
+hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlogp, void* ws,
+                        void* dx, void* dw, hipStream_t s) {
+  typedef std::conditional_t<F == kBf16, uint16_t, float> E;
+  const FewPlan p = few_plan(a, sizeof(E), true, ws);
+  const int n = static_cast<int>(a.n_rows), per = F == kRaw ? 2 : 1;  // 16-bit units a place
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+    const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
+    const int ldv = static_cast<int>(up64(rows));
+    hipError_t e = few_z_product<F>(a, p, v0, rows, s);
+    if (e != hipSuccess) return e;
+    head_few_dl_kernel<F><<<ldv / 64, 256, 0, s>>>(a, few_z_of(a, p, v0, rows),
+                                                   reinterpret_cast<const float2*>(stats), dlogp,
+                                                   p.dl, ldv, p.dlt, p.kn);
+    // dx: K is the vocabulary, along w's columns
+    const Operand wt{w_operand<F>(a, v0, rows, nullptr, nullptr, s).p, 0,
+                     static_cast<int64_t>(per) * a.d, a.d, rows};
+    const Operand dl{p.dl, a.n_rows * ldv, static_cast<int64_t>(per) * ldv, n, per * ldv};
+    e = with_few_tile(p.dx_cut.tile, [&](auto cf) {
+      typedef decltype(cf) CF;
+      const int mb = static_cast<int>(blocks(a.d, CF::BM));
+      product_kernel<CF, F == kBf16 ? kBf16Two : F, true, false, float, true>
+          <<<dim3(mb, p.dx_cut.slices), CF::NT, 0, s>>>(wt, dl, stages(F, ldv), mb, 1, n, v0 > 0,
+                                                        a.d, nullptr, 0, p.sums);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    // a wave takes 32 of the vocabulary at a time: enough workgroups for all CUs, few
+    // enough that each loads x for several
+    const int64_t across = blocks(a.d, 128), down = blocks(rows, 128);
+    const uint32_t groups = static_cast<uint32_t>(
+        std::clamp<int64_t>(1024 / across, 1, std::min<int64_t>(down, 32768)));
+    head_few_dw_kernel<F><<<dim3(static_cast<uint32_t>(across), groups), 256, 0, s>>>(
+        a, p.dlt, rows, p.kn, static_cast<E*>(dw) + v0 * a.d);
+  }
+  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d, 256)), 256, 0, s>>>(
+      a, p.sums, p.dx_cut.slices, dlogp, nullptr, static_cast<E*>(dx));
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t head_forward_bytes(const HeadArgs& a, int elem_bytes) {
-  return a.n_rows == 0 ? 0 : forward_plan(a, elem_bytes, nullptr).bytes;
+  if (a.n_rows == 0) return 0;
+  return a.n_rows <= kFewColumns ? few_plan(a, elem_bytes, false, nullptr).bytes
+                                 : forward_plan(a, elem_bytes, nullptr).bytes;
 }
 size_t head_backward_bytes(const HeadArgs& a, int elem_bytes) {
-  return a.n_rows == 0 ? 0 : backward_plan(a, elem_bytes, nullptr).bytes;
+  if (a.n_rows == 0) return 0;
+  return a.n_rows <= kFewColumns ? few_plan(a, elem_bytes, true, nullptr).bytes
+                                 : backward_plan(a, elem_bytes, nullptr).bytes;
 }
 
 hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
                                float* lse, float* stats, hipStream_t s) {
   if (a.n_rows == 0) return hipSuccess;
+  const bool few = a.n_rows <= kFewColumns;
   switch (form_of(elem_bytes, a.n_rows)) {
-    case kBf16: return forward<kBf16>(a, ws, logp, lse, stats, s);
-    case kRaw: return forward<kRaw>(a, ws, logp, lse, stats, s);
-    default: return forward<kHalves>(a, ws, logp, lse, stats, s);
+    case kRaw: return few_forward<kRaw>(a, ws, logp, lse, stats, s);
+    case kHalves: return forward<kHalves>(a, ws, logp, lse, stats, s);
+    default:
+      return few ? few_forward<kBf16>(a, ws, logp, lse, stats, s)
+                 : forward<kBf16>(a, ws, logp, lse, stats, s);
   }
 }
 
@@ -774,12 +1076,13 @@ hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* 
                        0, s>>>(static_cast<uint4*>(dw), count);
     return hipGetLastError();
   }
+  const bool few = a.n_rows <= kFewColumns;
   switch (form_of(elem_bytes, a.n_rows)) {
-    case kRaw: return backward<kRaw, true>(a, stats, dlogp, ws, dx, dw, s);
-    case kHalves: return backward<kHalves, false>(a, stats, dlogp, ws, dx, dw, s);
+    case kRaw: return few_backward<kRaw>(a, stats, dlogp, ws, dx, dw, s);
+    case kHalves: return backward<kHalves>(a, stats, dlogp, ws, dx, dw, s);
     default:
-      return a.n_rows <= kFewColumns ? backward<kBf16, true>(a, stats, dlogp, ws, dx, dw, s)
-                                     : backward<kBf16, false>(a, stats, dlogp, ws, dx, dw, s);
+      return few ? few_backward<kBf16>(a, stats, dlogp, ws, dx, dw, s)
+                 : backward<kBf16>(a, stats, dlogp, ws, dx, dw, s);
   }
 }
 

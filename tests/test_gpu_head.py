@@ -105,7 +105,10 @@ def check(m):
     (130, 2000, 256, 1.0, torch.int64), (300, 777, 520, 1.0, torch.int64),
     (1000, 2900, 64, 1.0, torch.int64), (5, 20000, 24, 1.0, torch.int64),
     (3000, 4100, 64, 1.0, torch.int64), (4090, 5000, 40, 1.0, torch.int64),
-    (257, 3, 2048, 1.0, torch.int64)])
+    (257, 3, 2048, 1.0, torch.int64), (16, 4096, 136, 1.0, torch.int64),
+    (17, 4097, 1000, 1.0, torch.int64), (48, 9005, 376, 0.7, torch.int64),
+    (64, 300000, 96, 1.0, torch.int64), (2, 150000, 184, 1.0, torch.int32),
+    (70, 70000, 8, 1.0, torch.int64)])
 def test_matches_oracle(n, v, d, scale, index, dtype):
     say(f"head {dtype} n={n} v={v} d={d} scale={scale}")
     check(make(n + v + d, n, v, d, dtype, scale, index))
