@@ -355,6 +355,7 @@ struct FewZ {
 };
 __device__ __forceinline__ float4 few_z(const FewZ& z, int64_t n_rows, int64_t n, int v) {
   float4 t = make_float4(0, 0, 0, 0);
+#pragma unroll 8
   for (int s = 0; s < z.slices; ++s) {
     const float4 q = *reinterpret_cast<const float4*>(z.sums + (s * n_rows + n) * z.pitch + v);
     t = make_float4(t.x + q.x, t.y + q.y, t.z + q.z, t.w + q.w);
@@ -650,6 +651,8 @@ __global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint
   __shared__ __attribute__((aligned(16))) uint16_t lds[PB][128][PITCH];
   typedef std::conditional_t<F == kBf16, uint16_t, float> E;
   const int c0 = blockIdx.x * 128;
+  const uint64_t given =
+      wave_ballot(lane_id() < a.n_rows && has_target(a.targets, a.index_bytes, a.vocab, lane_id()));
   // x[8 rows from n0][column], transposed
   for (int e = threadIdx.x; e < 128 * (kn / 8); e += 256) {
     const int col = e % 128, n0 = e / 128 * 8;
@@ -657,8 +660,7 @@ __global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int n = n0 + k;
-      const bool live = n < a.n_rows && c0 + col < a.d &&
-                        has_target(a.targets, a.index_bytes, a.vocab, n);
+      const bool live = (given >> n & 1) != 0 && c0 + col < a.d;
       v[k] = live ? ElemTraits<E>::to_f32(static_cast<const E*>(a.x)[static_cast<int64_t>(n) * a.d +
                                                                     c0 + col])
                   : 0.f;
@@ -672,14 +674,9 @@ __global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint
   __syncthreads();
   const int l = lane_id() & 31, half = lane_id() >> 5;
   const int waves = gridDim.y * 4;
-  for (int v0 = (blockIdx.y * 4 + threadIdx.x / kWave) * 32; v0 < rows; v0 += waves * 32) {
+  i32x4_t f[kFewColumns / 16][PA];
+  const auto load = [&](int v0) {
     const int v = min(v0 + l, rows - 1);
-    f32x16_t acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
-    i32x4_t f[kFewColumns / 16][PA];
 #pragma unroll
     for (int ks = 0; ks < kFewColumns / 16; ++ks)
       if (ks * 16 < kn)
@@ -687,6 +684,15 @@ __global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint
         for (int p = 0; p < PA; ++p)
           f[ks][p] = *reinterpret_cast<const i32x4_t*>(
               dlt + (static_cast<int64_t>(p) * rows + v) * kn + ks * 16 + half * 8);
+  };
+  const int first = (blockIdx.y * 4 + threadIdx.x / kWave) * 32;
+  if (first < rows) load(first);
+  for (int v0 = first; v0 < rows; v0 += waves * 32) {
+    f32x16_t acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < kFewColumns / 16; ++ks)
       if (ks * 16 < kn)
@@ -703,6 +709,7 @@ __global__ __launch_bounds__(256) void head_few_dw_kernel(HeadArgs a, const uint
             for (int p = 0; p < PA; ++p)
               if (sum - p >= 0 && sum - p < PB) acc[j] = mfma<kBf16>(f[ks][p], b[sum - p], acc[j]);
         }
+    if (v0 + waves * 32 < rows) load(v0 + waves * 32);
     if (c0 + 4 * l >= a.d) continue;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -767,7 +774,9 @@ FewPlan few_plan(const HeadArgs& a, int elem_bytes, bool backward, void* ws) {
   Carve c{static_cast<char*>(ws)};
   p.z = c.take<float>(p.z_cut.slices * n * ldv);
   if (backward) {
-    p.dx_cut = few_cut(a.d, n, stages(f, ldv) * (f == kBf16 ? 2 : 1), 32);
+    // the slices' sums, written and read, stay under a quarter of w
+    p.dx_cut = few_cut(a.d, n, stages(f, ldv) * (f == kBf16 ? 2 : 1),
+                       std::clamp<int64_t>(ldv * elem_bytes / (32 * n), 8, 128));
     p.dl = c.take<uint16_t>(2 * n * ldv);  // floats, or two parts
     p.dlt = c.take<uint16_t>((f == kRaw ? 3 : 2) * ldv * p.kn);
     p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
@@ -958,13 +967,19 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
   return hipGetLastError();
 }
 
+template <Form F, class Call>
+hipError_t with_form_tile(Tile t, const Call& f) {
+  if constexpr (F == kRaw) return with_raw_tile(t, f);
+  else return with_few_tile(t, f);
+}
+
 // Few rows: z = x w^T of a piece, in slices of K.
 template <Form F>
 hipError_t few_z_product(const HeadArgs& a, const FewPlan& p, int64_t v0, int rows,
                          hipStream_t s) {
   const Operand x = x_operand<F>(a, nullptr, nullptr, nullptr, nullptr, s);
   const Operand w = w_operand<F>(a, v0, rows, nullptr, nullptr, s);
-  return with_few_tile(p.z_cut.tile, [&](auto cf) {
+  return with_form_tile<F>(p.z_cut.tile, [&](auto cf) {
     typedef decltype(cf) CF;
     const int mb = static_cast<int>(blocks(rows, CF::BM));
     product_kernel<CF, F, false, false, float, true>
@@ -1020,7 +1035,7 @@ hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlog
     const Operand wt{w_operand<F>(a, v0, rows, nullptr, nullptr, s).p, 0,
                      static_cast<int64_t>(per) * a.d, a.d, rows};
     const Operand dl{p.dl, a.n_rows * ldv, static_cast<int64_t>(per) * ldv, n, per * ldv};
-    e = with_few_tile(p.dx_cut.tile, [&](auto cf) {
+    e = with_form_tile<F>(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       product_kernel<CF, F == kBf16 ? kBf16Two : F, true, false, float, true>
@@ -1029,11 +1044,10 @@ hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlog
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    // a wave takes 32 of the vocabulary at a time: enough workgroups for all CUs, few
-    // enough that each loads x for several
+    // a wave takes 32 of the vocabulary at a time: two workgroups a CU, which load x once
     const int64_t across = blocks(a.d, 128), down = blocks(rows, 128);
     const uint32_t groups = static_cast<uint32_t>(
-        std::clamp<int64_t>(1024 / across, 1, std::min<int64_t>(down, 32768)));
+        std::clamp<int64_t>(blocks(512, static_cast<int>(across)), 1, std::min<int64_t>(down, 32768)));
     head_few_dw_kernel<F><<<dim3(static_cast<uint32_t>(across), groups), 256, 0, s>>>(
         a, p.dlt, rows, p.kn, static_cast<E*>(dw) + v0 * a.d);
   }

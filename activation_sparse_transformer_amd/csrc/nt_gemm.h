@@ -16,7 +16,8 @@
 //  - kRaw:     float32 as it lies, for few rows, where a pass over the other operand
 //              to split it would cost as much as the product: fragments are split into
 //              three bfloat16 parts (8 + 8 + 8 bits, of any exponent) as they leave
-//              LDS, six products, the five small ones in accumulators of their own.
+//              LDS (B's, which all waves share, once a stage by the workgroup), six
+//              products, the five small ones in accumulators of their own.
 // A product's form is that of both operands, or one of a mixed pair: kMixed, A in kHalf
 // and B in kHalves, and kBf16Two, A in kBf16 and B as two bfloat16 parts.
 //
@@ -531,24 +532,23 @@ __device__ __forceinline__ void split3(const float (&v)[8], i32x4_t (&part)[3]) 
   }
 }
 
-// 8 floats of K step ks of a raw stage: row r of a straight one, column r of a turned one.
-template <int SIZE, bool TURNED>
-__device__ __forceinline__ void read_raw(const uint16_t* tile, int r, int ks, float (&v)[8]) {
-  const int half = lane_id() >> 5;
-  if constexpr (TURNED) {
-    const float* p = reinterpret_cast<const float*>(tile) + (ks * 16 + half * 8) * SIZE + r;
+// 8 floats from 8 c on of K of a raw stage: of row r of a straight one, column r of a
+// turned one.
+__device__ __forceinline__ void read_straight8(const uint16_t* tile, int r, int c,
+                                               float (&v)[8]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = p[k * SIZE];
-  } else {
+  for (int h = 0; h < 2; ++h) {
+    // not as a float4: the compiler then waits for every copy in flight first
+    const i32x4_t q = *reinterpret_cast<const i32x4_t*>(tile + tile_offset(r, c * 2 + h));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // not as a float4: the compiler then waits for every copy in flight first
-      const i32x4_t q = *reinterpret_cast<const i32x4_t*>(
-          tile + tile_offset(r, ks * 4 + half * 2 + h));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[4 * h + k] = __int_as_float(q[k]);
-    }
+    for (int k = 0; k < 4; ++k) v[4 * h + k] = __int_as_float(q[k]);
   }
+}
+template <int SIZE>
+__device__ __forceinline__ void read_turned8(const uint16_t* tile, int r, int c, float (&v)[8]) {
+  const float* p = reinterpret_cast<const float*>(tile) + c * 8 * SIZE + r;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = p[k * SIZE];
 }
 
 template <int SIZE, int NW, bool TURNED>
@@ -568,8 +568,18 @@ struct RawCopies<SIZE, NW, true> : RawTurnedCopies<SIZE, NW> {
   }
 };
 
+// Elements that kRaw's B parts take in LDS behind the stages: [3][BN][32], the 16-byte
+// chunk c of a row at position c ^ row / 4.
+template <class CF, Form F>
+constexpr int extra_lds() {
+  return F == kRaw ? 3 * CF::BN * 32 : 0;
+}
+__device__ __forceinline__ int raw_part_offset(int row, int c) {
+  return row * 32 + ((c ^ ((row >> 2) & 3)) << 3);
+}
+
 // mainloop for kRaw: stages of 32 floats of K.
-template <class CF, bool TA, bool TB>
+template <class CF, bool TA>
 __device__ __forceinline__ void mainloop_raw(const Operand& A, int m0, const Operand& B, int n0,
                                              int k0, int ksteps, uint16_t* lds,
                                              f32x16_t (&acc)[CF::FM][CF::FN]) {
@@ -580,9 +590,11 @@ __device__ __forceinline__ void mainloop_raw(const Operand& A, int m0, const Ope
     for (int j = 0; j < CF::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = small[i][j][r] = 0.f;
+  static_assert(CF::NT == 256 && CF::BN * 4 <= CF::NT, "8 floats of B a thread");
   const RawCopies<CF::BM, CF::NW, TA> a_copies(A, m0, k0);
-  const RawCopies<CF::BN, CF::NW, TB> b_copies(B, n0, k0);
-  const int wave = threadIdx.x / kWave, lane = lane_id() & 31;
+  const RawCopies<CF::BN, CF::NW, false> b_copies(B, n0, k0);
+  uint16_t* const parts = lds + CF::STAGES * CF::STAGE;
+  const int wave = threadIdx.x / kWave, lane = lane_id() & 31, half = lane_id() >> 5;
   const int ra = wave / CF::WAVES_N * CF::WTM + lane, rb = wave % CF::WAVES_N * CF::WTN + lane;
   constexpr int AHEAD = CF::STAGES - 1, COPIES = CF::A_ISSUE + CF::B_ISSUE;
   int fill = 0, ahead = 0;
@@ -601,20 +613,33 @@ __device__ __forceinline__ void mainloop_raw(const Operand& A, int m0, const Ope
     if (s + AHEAD < ksteps) copy();
     const uint16_t* sA = lds + cur * CF::STAGE;
     const uint16_t* sB = sA + CF::BM * kStep;
+    if (static_cast<int>(threadIdx.x) < CF::BN * 4) {
+      const int row = threadIdx.x / 4, c = threadIdx.x % 4;
+      float v[8];
+      read_straight8(sB, row, c, v);
+      i32x4_t part[3];
+      split3(v, part);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<i32x4_t*>(parts + p * CF::BN * 32 + raw_part_offset(row, c)) = part[p];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       i32x4_t a[CF::FM][3], b[CF::FN][3];
-      float v[8];
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i) {
-        read_raw<CF::BM, TA>(sA, ra + 32 * i, ks, v);
+        float v[8];
+        if constexpr (TA) read_turned8<CF::BM>(sA, ra + 32 * i, ks * 2 + half, v);
+        else read_straight8(sA, ra + 32 * i, ks * 2 + half, v);
         split3(v, a[i]);
       }
 #pragma unroll
-      for (int j = 0; j < CF::FN; ++j) {
-        read_raw<CF::BN, TB>(sB, rb + 32 * j, ks, v);
-        split3(v, b[j]);
-      }
+      for (int j = 0; j < CF::FN; ++j)
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          b[j][p] = *reinterpret_cast<const i32x4_t*>(
+              parts + p * CF::BN * 32 + raw_part_offset(rb + 32 * j, ks * 2 + half));
 #pragma unroll
       for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
@@ -641,7 +666,7 @@ __device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand
                                          int ksteps, uint16_t* lds,
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
   if constexpr (F == kRaw)
-    mainloop_raw<CF, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
+    mainloop_raw<CF, TA>(A, m0, B, n0, k0, ksteps, lds, acc);
   else if constexpr (CF::FM == 2 && CF::FN == 4)
     mainloop_pipe<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
   else
@@ -723,7 +748,7 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
                                                          int m_blocks, int n_blocks, int cols,
                                                          bool add, int pitch, const float* amax,
                                                          int exponent, E* __restrict__ out) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE + extra_lds<CF, F>()];
   int mb, nb;
   const int slices = gridDim.y, slice = blockIdx.y;
   const int t = run_of(blockIdx.x, gridDim.x);
@@ -796,18 +821,26 @@ typedef Config<256, 256, 4, 2, 2> Big;
 typedef Config<128, 128, 2, 2, 2> Mid;
 typedef Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
 typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32
+// kRaw: two workgroups (with 64 columns) or three a CU, which is worth more than a
+// third stage (9005 x 2376 by 39: 31 us, 42 with one workgroup of three stages)
+typedef Config<128, 64, 4, 1, 2> RawFew;
+typedef Config<128, 32, 4, 1, 2> RawBare;
 constexpr int kFewColumns = 64;
 
 inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 inline int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
 
 enum Tile { kBare, kFew, kMid, kBig };
-template <class F>
-hipError_t with_few_tile(Tile t, const F& f) {
+template <class Call>
+hipError_t with_few_tile(Tile t, const Call& f) {
   return t == kBare ? f(Bare()) : f(Few());
 }
-template <class F>
-hipError_t with_wide_tile(Tile t, const F& f) {
+template <class Call>
+hipError_t with_raw_tile(Tile t, const Call& f) {
+  return t == kBare ? f(RawBare()) : f(RawFew());
+}
+template <class Call>
+hipError_t with_wide_tile(Tile t, const Call& f) {
   return t == kMid ? f(Mid()) : f(Big());
 }
 inline int tile_rows(Tile t) { return t == kBig ? 256 : 128; }
@@ -818,12 +851,12 @@ struct Cut {
   Tile tile;
   int slices;
 };
-// At most kFewColumns columns: the narrowest tile, and slices until two workgroups a CU
-// are there.
-inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices) {
+// At most kFewColumns columns: the narrowest tile, and slices until four workgroups a CU
+// are there (two run at a time), of at least 4 stages.
+inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int64_t most_slices) {
   const Tile t = cols <= 32 ? kBare : kFew;
   const int64_t most = std::clamp<int64_t>(steps / 4, 1, most_slices);
-  return {t, static_cast<int>(std::clamp<int64_t>(512 / blocks(rows, tile_rows(t)), 1, most))};
+  return {t, static_cast<int>(std::clamp<int64_t>(1024 / blocks(rows, tile_rows(t)), 1, most))};
 }
 // Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us to fill and
 // to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us), with as many
