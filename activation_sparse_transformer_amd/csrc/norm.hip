@@ -22,14 +22,19 @@ namespace twell {
 namespace {
 
 constexpr int kRun = 8;  // columns of a lane's run
+// Workgroups of the gradient: two a CU, one of 1024 lanes.  More only make more column sums
+// to add up (4096 x 2048 bf16: 34 us in all with 512, 37 with 1024; 6374 x 5264: 123 with
+// 256, 131 with 512), and loading a row ahead gains nothing.
+constexpr int kNormGroups = 512;
 
-// 8 elements as loaded
+// 8 elements as loaded.  Loads go through the caches: y and the residual come from the
+// call before (gradient of 8192 x 4096 float32 166 us, 176 past the caches); stores do not.
 template <typename E>
 struct Run;
 template <>
 struct Run<uint16_t> {
   uint4 q;
-  __device__ __forceinline__ void load(const uint16_t* p) { q = load_once(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const uint16_t* p) { q = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void floats(float (&f)[kRun]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -52,8 +57,8 @@ template <>
 struct Run<float> {
   uint4 q[2];
   __device__ __forceinline__ void load(const float* p) {
-    q[0] = load_once(reinterpret_cast<const uint4*>(p));
-    q[1] = load_once(reinterpret_cast<const uint4*>(p) + 1);
+    q[0] = *reinterpret_cast<const uint4*>(p);
+    q[1] = *(reinterpret_cast<const uint4*>(p) + 1);
   }
   __device__ __forceinline__ void clear() { q[0] = q[1] = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void floats(float (&f)[kRun]) const {
@@ -130,6 +135,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_forward_kernel(NormArg
   const int t = G < 256 ? threadIdx.x % G : threadIdx.x;
   const int runs = a.d / kRun;
   const float inv_d = 1.f / static_cast<float>(a.d);
+  float post[V][kRun], pre[V][kRun];  // weights
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * G + t;
+    if (c >= runs) continue;
+    if (y != nullptr) post_weights(a, c * kRun, post[i]);
+    if (a.w_pre != nullptr) load_weights(a.w_pre, c * kRun, pre[i]);
+  }
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (G < 256 ? threadIdx.x / G : 0);
        row < a.n_rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
     const int64_t base = row * a.d;
@@ -164,11 +177,10 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_forward_kernel(NormArg
       if (c >= runs) continue;
       rr[i].floats(v[i]);
       if (y != nullptr) {
-        float f[kRun], w[kRun];
+        float f[kRun];
         yr[i].floats(f);
-        post_weights(a, c * kRun, w);
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) v[i][k] = fmaf(f[k] * ystd, w[k], a.alpha * v[i][k]);
+        for (int k = 0; k < kRun; ++k) v[i][k] = fmaf(f[k] * ystd, post[i][k], a.alpha * v[i][k]);
         Run<E>::store(residual_out + base + c * kRun, v[i]);
       }
 #pragma unroll
@@ -184,10 +196,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_forward_kernel(NormArg
     for (int i = 0; i < V; ++i) {
       const int c = i * G + t;
       if (c >= runs) continue;
-      float w[kRun];
-      load_weights(a.w_pre, c * kRun, w);
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) v[i][k] = v[i][k] * rstd * w[k];
+      for (int k = 0; k < kRun; ++k) v[i][k] = v[i][k] * rstd * pre[i][k];
       Run<E>::store(x + base + c * kRun, v[i]);
     }
     // without w_post only lds[1] is used: its reads end before the next row's writes
@@ -196,17 +206,17 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_forward_kernel(NormArg
 }
 
 // A group walks rows group, group + groups, ... and keeps its columns' sums in
-// registers; sums[group][d] (S) and sums[groups + group][d] (dw_pre) are added up
-// by norm_sums_kernel.
+// registers; a workgroup b's sums[b][d] (S) and sums[gridDim.x + b][d] (dw_pre) are added
+// up by norm_sums_kernel.
 template <typename E, int G, int V>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(NormArgs a,
                                                                           NormGradPtrs<E> p,
-                                                                          float* sums,
-                                                                          int groups) {
+                                                                          float* sums) {
   constexpr int ROWS = G < 256 ? 256 / G : 1;
   __shared__ float lds[2][48];
   const int t = G < 256 ? threadIdx.x % G : threadIdx.x;
   const int group = blockIdx.x * ROWS + (G < 256 ? threadIdx.x / G : 0);
+  const int groups = gridDim.x * ROWS;
   const int runs = a.d / kRun;
   const float inv_d = 1.f / static_cast<float>(a.d);
   float post[V][kRun], pre[V][kRun];  // column sums
@@ -309,66 +319,95 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(NormAr
     // without w_post only lds[0] is used: its reads end before the next row's writes
     if (G > kWave && a.w_post == nullptr) __syncthreads();
   }
-  if (group >= groups) return;
+  if constexpr (ROWS > 1) {  // the workgroup's groups, as one
+    __shared__ float joint[ROWS - 1][2][V * G * kRun];
+    const int g = threadIdx.x / G;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int k = 0; k < kRun; ++k)
+        if (g > 0) {
+          joint[g - 1][0][(i * kRun + k) * G + t] = post[i][k];
+          joint[g - 1][1][(i * kRun + k) * G + t] = pre[i][k];
+        }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int k = 0; k < kRun; ++k)
+#pragma unroll
+        for (int o = 0; o < ROWS - 1; ++o) {
+          post[i][k] += joint[o][0][(i * kRun + k) * G + t];
+          pre[i][k] += joint[o][1][(i * kRun + k) * G + t];
+        }
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * G + t;
     if (c >= runs) continue;
-    float* out = sums + static_cast<int64_t>(group) * a.d + c * kRun;
+    float* out = sums + static_cast<int64_t>(blockIdx.x) * a.d + c * kRun;
     if (p.y != nullptr) Run<float>::store(out, post[i]);
     if (a.w_pre != nullptr)
-      Run<float>::store(out + static_cast<int64_t>(groups) * a.d, pre[i]);
+      Run<float>::store(out + static_cast<int64_t>(gridDim.x) * a.d, pre[i]);
   }
 }
 
-// Column sums over the groups' rows of `sums`, in the groups' order within 16
-// streams and then over the streams: 16 columns a workgroup of 16 x 16 lanes.
-constexpr int kSumCols = 16, kSumStreams = 16;
+// Column sums over the workgroups' rows of `sums`, in 64 streams and then over those: 16
+// columns a workgroup, 4 to a lane.
+constexpr int kSumCols = 16, kSumStreams = 64;
 __global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs a, const float* sums, int groups,
                                                         float* dw_post, float* dgate,
                                                         float* dw_pre) {
-  __shared__ float lds[kSumStreams][kSumCols];
-  const int col = threadIdx.x % kSumCols, stream = threadIdx.x / kSumCols;
-  const int c = blockIdx.x * kSumCols + col;
+  __shared__ float4 lds[kSumStreams][kSumCols / 4];
+  const int col = threadIdx.x % 4, stream = threadIdx.x / 4;
+  const int c = blockIdx.x * kSumCols + col * 4;
   const bool is_pre = blockIdx.y == 1;
   if (is_pre ? dw_pre == nullptr : dw_post == nullptr && dgate == nullptr) return;
-  float s = 0.f;
+  const auto add = [](float4 p, float4 q) {
+    return make_float4(p.x + q.x, p.y + q.y, p.z + q.z, p.w + q.w);
+  };
+  float4 s = make_float4(0, 0, 0, 0);
   if (c < a.d) {
     const float* in = sums + (is_pre ? static_cast<int64_t>(groups) * a.d : 0) + c;
-    int g = stream;
-    for (; g + 3 * kSumStreams < groups; g += 4 * kSumStreams) {
-      float v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = in[static_cast<int64_t>(g + u * kSumStreams) * a.d];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) s += v[u];
-    }
-    for (; g < groups; g += kSumStreams) s += in[static_cast<int64_t>(g) * a.d];
+#pragma unroll 8
+    for (int g = stream; g < groups; g += kSumStreams)
+      s = add(s, *reinterpret_cast<const float4*>(in + static_cast<int64_t>(g) * a.d));
   }
   lds[stream][col] = s;
   __syncthreads();
-  if (stream != 0 || c >= a.d) return;
-  s = 0.f;
+  if (stream >= 4 || c >= a.d) return;
+  // 16 streams' sums to a lane, and the four lanes' of a column
 #pragma unroll
-  for (int w = 0; w < kSumStreams; ++w) s += lds[w][col];
-  if (is_pre) {
-    dw_pre[c] = s;
-  } else {
-    if (dw_post != nullptr) dw_post[c] = a.gate != nullptr ? s * a.gate[c] : s;
-    if (dgate != nullptr) dgate[c] = a.w_post != nullptr ? s * a.w_post[c] : s;
+  for (int w = 1; w < kSumStreams / 4; ++w) s = add(s, lds[stream + 4 * w][col]);
+#pragma unroll
+  for (int h = 4; h < 16; h *= 2)
+    s = add(s, make_float4(__shfl_xor(s.x, h), __shfl_xor(s.y, h), __shfl_xor(s.z, h),
+                           __shfl_xor(s.w, h)));
+  if (stream != 0) return;
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (is_pre) {
+      dw_pre[c + k] = v[k];
+    } else {
+      if (dw_post != nullptr) dw_post[c + k] = a.gate != nullptr ? v[k] * a.gate[c + k] : v[k];
+      if (dgate != nullptr) dgate[c + k] = a.w_post != nullptr ? v[k] * a.w_post[c + k] : v[k];
+    }
   }
 }
 
-// The lanes G of a row and runs V of a lane: the smallest G with V <= 2, so that a
-// row's elements stay in registers at full occupancy.
+// The lanes G of a row and runs V of a lane: one run while a workgroup holds enough
+// lanes (16384 x 8192 bf16 forward 204 us; 210 with 512 lanes of two runs, 299 with 256
+// of four).
 template <class F>
 hipError_t with_group(int d, const F& f) {
   const int runs = d / kRun;
   if (runs <= 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   if (runs <= 128) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
   if (runs <= 256) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-  if (runs <= 512) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-  if (runs <= 1024) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  if (runs <= 512) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 1>());
+  if (runs <= 1024) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 1>());
   return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
 }
 
@@ -378,8 +417,11 @@ hipError_t forward(const NormArgs& a, const void* residual, const void* y, void*
   return with_group(a.d, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     constexpr int ROWS = G < 256 ? 256 / G : 1, NT = G < 256 ? 256 : G;
-    // a launch holds fewer than 2^32 lanes; past 2^20 workgroups the rows are walked
-    const int64_t blocks = std::min<int64_t>((a.n_rows + ROWS - 1) / ROWS, 1 << 20);
+    // two rows a group where that leaves 2048 workgroups: the weights are read once for
+    // both (16384 x 8192 bf16 204 us, 228 with one; fewer rows gain nothing).  A launch
+    // holds fewer than 2^32 lanes.
+    const int64_t steps = (a.n_rows + ROWS - 1) / ROWS;
+    const int64_t blocks = std::min<int64_t>(steps >= 4096 ? (steps + 1) / 2 : steps, 1 << 20);
     norm_forward_kernel<E, G, V><<<static_cast<uint32_t>(blocks), NT, 0, s>>>(
         a, static_cast<const E*>(residual), static_cast<const E*>(y),
         static_cast<E*>(residual_out), static_cast<E*>(x));
@@ -392,13 +434,13 @@ hipError_t backward(const NormArgs& a, const NormGradArgs& p, hipStream_t s) {
   const int groups = norm_grad_groups(a.n_rows, a.d);
   return with_group(a.d, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
-    constexpr int ROWS = G < 256 ? 256 / G : 1, NT = G < 256 ? 256 : G;
+    constexpr int NT = G < 256 ? 256 : G;
     if (groups > 0) {
       const NormGradPtrs<E> q{static_cast<const E*>(p.residual_out), static_cast<const E*>(p.y),
                               static_cast<const E*>(p.d_residual_out),
                               static_cast<const E*>(p.dx), static_cast<E*>(p.d_residual),
                               static_cast<E*>(p.dy)};
-      norm_backward_kernel<E, G, V><<<(groups + ROWS - 1) / ROWS, NT, 0, s>>>(a, q, p.sums, groups);
+      norm_backward_kernel<E, G, V><<<groups, NT, 0, s>>>(a, q, p.sums);
     }
     if (p.dw_post != nullptr || p.dgate != nullptr || p.dw_pre != nullptr)
       norm_sums_kernel<<<dim3((a.d + kSumCols - 1) / kSumCols, 2), 256, 0, s>>>(
@@ -411,9 +453,9 @@ hipError_t backward(const NormArgs& a, const NormGradArgs& p, hipStream_t s) {
 
 int norm_grad_groups(int64_t n_rows, int d) {
   const int runs = d / kRun;
-  // 2048 lanes a CU: 8 waves of each SIMD to hide the rows' latency
-  const int most = runs <= 128 ? 4096 : runs <= 512 ? 1024 : runs <= 1024 ? 512 : 256;
-  return static_cast<int>(std::min<int64_t>(n_rows, most));
+  const int64_t rows = runs <= 128 ? (n_rows + 3) / 4 : n_rows;  // steps of a workgroup in all
+  const int most = runs <= 512 ? kNormGroups : kNormGroups / 2;
+  return static_cast<int>(std::min<int64_t>(rows, most));
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, int elem_bytes, const void* residual,

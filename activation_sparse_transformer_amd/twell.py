@@ -219,12 +219,16 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+# the current GPU's number without torch's own checks (0.1 us a call); the GPU is in use by then
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _here(device: torch.device) -> int:
     """The current stream of `device`, which has to be the current GPU: the library launches
     there."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on the GPU, got {device}")
-    if device.index != torch.cuda.current_device():
+    if device.index != _raw_device():
         raise ValueError(f"tensors are on {device}, the current GPU is "
                          f"{torch.cuda.current_device()}")
     return _stream(device)
@@ -236,6 +240,9 @@ def _check(code: int, where: str) -> None:
 
 
 def _need(t: torch.Tensor, name: str, device, dtype=None, shape=None) -> None:
+    if (t.device == device and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if dtype is not None and t.dtype != dtype:

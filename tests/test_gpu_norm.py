@@ -5,8 +5,8 @@ A row's sum of squares adds at most 2 * 8 terms a lane, then 6 lane steps and 16
 carries under 40 roundings of 2^-24 each; a root, a quotient and the products behind it under 10
 more.  So every float32 value is within 2^-18 (64 roundings) of the sum of the magnitudes that
 were added for it, and a result in bfloat16 half a step (2^-8) of itself further.  Column sums add
-n / groups rows in a chain and at most 256 groups in 16 streams: 2^-18 and one rounding more
-per row of a chain; chains here are under 64 rows."""
+the rows of a group in a chain (under 24 here), 4 groups of a workgroup, and at most 512
+workgroups in 64 streams: under 64 roundings more, another 2^-18."""
 import ctypes
 
 import numpy as np
