@@ -213,14 +213,244 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
   }
 }
 
+// ---------------------------------------------------------------- short sides up to 128
+// One launch a step: a workgroup holds G and B, 128 x 128 with zeros past m, in LDS, forms
+// B for itself, and takes 64 columns of X: X' = a X + B X and their part of the next G =
+// X' X'^T, which the next launch adds up.  X stays float32 [m][ld] in memory.  What a step
+// cost before was its six launches (512 x 128: 38 us a step).
+constexpr int kSmallSide = 128, kSmallColumns = 64;
+constexpr int kSmallGram = kSmallSide * kSmallSide;
+constexpr int kSmallSums = 16;  // more workgroups' sums of G are added up by a launch of its own
+
+struct SmallArgs {
+  int m, n, ld;
+  bool tall;
+  const void* in;       // first step: M; X = M / (|M| + eps), and only its G
+  const double* norm;
+  int norm_count;
+  float eps;
+  float* x;             // [m][ld]
+  const float* gram;    // [grams][128][128], times 2^(2 ex)
+  int grams;
+  float g_factor;       // 2^(eg - 2 ex)
+  float b_keep, b_take; // B 2^eb = b_keep * (G 2^eg) + b_take * (G G 2^(2 eg))
+  float x_factor;       // 2^ex
+  float keep, take;     // X' = keep X + take (B 2^eb)(X 2^ex)
+  float next_factor;    // of X' for its G
+  float* next_gram;     // [workgroups][128][128]; null at the last step
+  void* out;            // last step: times scale
+  float scale;
+};
+
+// An operand tile in LDS: rows of K in panels of 64, as a stage's (nt_gemm.h).
+__device__ __forceinline__ int panel_offset(int rows, int r, int k) {
+  return (k >> 6) * rows * kStep + tile_offset(r, (k >> 3) & 7) + (k & 7);
+}
+__device__ __forceinline__ void put8(uint16_t* tile, int rows, int r, int k, const float (&v)[8],
+                                     int part) {
+  uint32_t w[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t lo[2], hi[2];
+    split<kHalves>(v[2 * i], lo);
+    split<kHalves>(v[2 * i + 1], hi);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) w[p][i] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    *reinterpret_cast<uint4*>(tile + p * part + panel_offset(rows, r, k)) =
+        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+__device__ __forceinline__ float value_of(const uint16_t* tile, int part, int at) {
+  return static_cast<float>(__builtin_bit_cast(_Float16, tile[part + at])) +
+         static_cast<float>(__builtin_bit_cast(_Float16, tile[at]));
+}
+
+// acc = A B^T of 32 rows of A from ra and 32 FN of B from rb, K in 16s, the small products
+// of the parts over the whole of K first.
+template <int FN>
+__device__ __forceinline__ void small_product(const uint16_t* a, int rows_a, int part_a, int ra,
+                                              const uint16_t* b, int rows_b, int part_b, int rb,
+                                              int k16, f32x16_t (&acc)[FN]) {
+  const int l = lane_id() & 31, half = lane_id() >> 5;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const uint16_t* ap = a + (q == 0 ? part_a : 0);
+    const uint16_t* bp = b + (q == 1 ? part_b : 0);
+    for (int ks = 0; ks < k16; ++ks) {
+      const int k = ks * 16 + half * 8;
+      const i32x4_t f = *reinterpret_cast<const i32x4_t*>(ap + panel_offset(rows_a, ra + l, k));
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[j] = mfma<kHalves>(f,
+                               *reinterpret_cast<const i32x4_t*>(
+                                   bp + panel_offset(rows_b, rb + 32 * j + l, k)),
+                               acc[j]);
+    }
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(512) void orth_small_kernel(SmallArgs a) {
+  constexpr int N = kSmallSide, C = kSmallColumns;
+  // G, then B: two parts [N][N]; X's block: two parts [C][N], then [N][C]
+  __shared__ __attribute__((aligned(16))) uint16_t g[2 * N * N];
+  __shared__ __attribute__((aligned(16))) uint16_t xb[2 * C * N];
+  __shared__ double sum[512];
+  const int wave = threadIdx.x / kWave, wm = wave / 2 * 32, wn = wave % 2;
+  const int l = lane_id() & 31, half = lane_id() >> 5;
+  const int j0 = blockIdx.x * C;
+  if (a.in == nullptr) {
+#pragma unroll
+    for (int u = 0; u < N * N / 8 / 512; ++u) {
+      const int e = threadIdx.x + u * 512;
+      float v[8] = {};
+#pragma unroll 4
+      for (int s = 0; s < a.grams; ++s) {
+        const float4* p = reinterpret_cast<const float4*>(a.gram + s * kSmallGram + e * 8);
+        const float4 q = p[0], r = p[1];
+        v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
+        v[4] += r.x, v[5] += r.y, v[6] += r.z, v[7] += r.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= a.g_factor;
+      put8(g, N, e / (N / 8), e % (N / 8) * 8, v, N * N);
+    }
+    // columns of X: 8 rows a lane, lanes along the columns
+#pragma unroll
+    for (int u = 0; u < C * N / 8 / 512; ++u) {
+      const int e = threadIdx.x + u * 512;
+      const int c = e % C, i = e / C * 8;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = i + k < a.m && j0 + c < a.n
+                   ? a.x[static_cast<int64_t>(i + k) * a.ld + j0 + c] * a.x_factor
+                   : 0.f;
+      put8(xb, C, c, i, v, C * N);
+    }
+    __syncthreads();
+    f32x16_t acc[2];
+    const int k16 = (a.m + 15) / 16;
+    small_product<2>(g, N, N * N, wm, g, N, N * N, wn * 64, k16, acc);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int at = panel_offset(N, wn * 64 + j * 32 + l, wm + 4 * half + row_of(0, r));
+        acc[j][r] = fmaf(a.b_keep, value_of(g, N * N, at), a.b_take * acc[j][r]);
+      }
+    __syncthreads();
+    // B is symmetric: a lane's 4 rows are 4 columns of its own row
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = panel_offset(N, wn * 64 + j * 32 + l, wm + 4 * half + row_of(0, 4 * q));
+        uint16_t part[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split<kHalves>(acc[j][4 * q + k], part[k]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          *reinterpret_cast<uint2*>(g + p * N * N + at) =
+              make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
+                         part[2][p] | static_cast<uint32_t>(part[3][p]) << 16);
+      }
+    __syncthreads();
+    f32x16_t up[1];
+    small_product<1>(g, N, N * N, wm, xb, C, C * N, wn * 32, k16, up);
+    __syncthreads();  // xb becomes [N][C]
+    const int c = wn * 32 + l, j = j0 + c;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int i = wm + 4 * half + row_of(0, r);
+      float v = 0.f;
+      if (i < a.m && j < a.n) {
+        float* x = a.x + static_cast<int64_t>(i) * a.ld + j;
+        v = fmaf(a.keep, *x, a.take * up[0][r]);
+        if (a.next_gram != nullptr)
+          *x = v;
+        else
+          static_cast<E*>(a.out)[a.tall ? static_cast<int64_t>(j) * a.m + i
+                                        : static_cast<int64_t>(i) * a.n + j] =
+              ElemTraits<E>::from_f32(v * a.scale);
+      }
+      if (a.next_gram != nullptr) {
+        uint16_t part[2];
+        split<kHalves>(v * a.next_factor, part);
+        xb[panel_offset(N, i, c)] = part[0];
+        xb[C * N + panel_offset(N, i, c)] = part[1];
+      }
+    }
+    if (a.next_gram == nullptr) return;
+  } else {
+    double t = 0;
+    for (int i = threadIdx.x; i < a.norm_count; i += 512) t += a.norm[i];
+    sum[threadIdx.x] = t;
+    __syncthreads();
+    for (int h = 256; h > 0; h /= 2) {
+      if (static_cast<int>(threadIdx.x) < h) sum[threadIdx.x] += sum[threadIdx.x + h];
+      __syncthreads();
+    }
+    const double inv = 1.0 / (sqrt(sum[0]) + static_cast<double>(a.eps));
+    for (int e = threadIdx.x; e < N * C; e += 512) {
+      const int i = a.tall ? e % N : e / C, c = a.tall ? e / N : e % C, j = j0 + c;
+      float v = 0.f;
+      if (i < a.m && j < a.n) {
+        const E* in = static_cast<const E*>(a.in);
+        const int64_t at = a.tall ? static_cast<int64_t>(j) * a.m + i
+                                  : static_cast<int64_t>(i) * a.n + j;
+        v = static_cast<float>(static_cast<double>(ElemTraits<E>::to_f32(in[at])) * inv);
+        a.x[static_cast<int64_t>(i) * a.ld + j] = v;
+      }
+      uint16_t part[2];
+      split<kHalves>(v * a.next_factor, part);
+      xb[panel_offset(N, i, c)] = part[0];
+      xb[C * N + panel_offset(N, i, c)] = part[1];
+    }
+  }
+  __syncthreads();
+  f32x16_t acc[2];
+  small_product<2>(xb, N, C * N, wm, xb, N, C * N, wn * 64, C / 16, acc);
+  float* to = a.next_gram + static_cast<int64_t>(blockIdx.x) * kSmallGram;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(to + (wn * 64 + j * 32 + l) * N + wm + 4 * half +
+                                 row_of(0, 4 * q)) =
+          make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+}
+
+// The sum of the workgroups' grams, in 4 streams.
+__global__ __launch_bounds__(256) void orth_gram_kernel(const float* __restrict__ grams, int count,
+                                                        float* __restrict__ out) {
+  __shared__ float joint[4][64];
+  const int at = threadIdx.x % 64, stream = threadIdx.x / 64;
+  const int e = blockIdx.x * 64 + at;
+  float s = 0.f;
+#pragma unroll 8
+  for (int i = stream; i < count; i += 4) s += grams[i * kSmallGram + e];
+  joint[stream][at] = s;
+  __syncthreads();
+  if (stream == 0) out[e] = joint[0][at] + joint[1][at] + joint[2][at] + joint[3][at];
+}
+
 struct Plan {
   int m, n, ldm, ldn;
   Cut gram, square, update;
   double* norm;
   uint16_t *x, *xt, *g, *b;
-  float* sums;
+  float *sums, *small_gram;
+  bool small;
   size_t bytes;
 };
+constexpr int kSmallMost = 8192;
 constexpr Form x_form(int elem_bytes) { return elem_bytes == 2 ? kHalf : kHalves; }
 Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   Plan p{};
@@ -230,6 +460,18 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   p.ldm = static_cast<int>(up64(p.m));
   p.ldn = static_cast<int>(up64(p.n));
   const int gram = PX == 2 ? 3 : 1, update = PX == 2 ? 3 : 2;  // products
+  p.small = p.m <= kSmallSide && p.n <= kSmallMost;
+  if (p.small) {
+    Carve c{static_cast<char*>(ws)};
+    p.norm = c.take<double>(kNormBlocks);
+    p.sums = c.take<float>(static_cast<size_t>(p.m) * p.ldn);
+    // G's sums of the workgroups: two sets taken in turn, or one and their sum in front
+    const size_t groups = p.ldn / kSmallColumns;
+    p.small_gram =
+        c.take<float>((groups <= kSmallSums ? 2 * groups : groups + 1) * size_t{kSmallGram});
+    p.bytes = c.used;
+    return p;
+  }
   p.gram = wide_cut(p.m, p.m, p.ldn / 64 * gram, 32, true);
   p.square = wide_cut(p.m, p.m, p.ldm / 64 * 3, 32, true);
   p.update = p.m <= kFewColumns ? few_cut(p.n, p.m, p.ldm / 64 * update, 32)
@@ -298,6 +540,60 @@ double step_bound(const OrthArgs& p, double top) {
 }
 
 template <typename E>
+hipError_t orthogonalize_small(const OrthArgs& a, const Plan& p, int count, hipStream_t s) {
+  const uint32_t groups = static_cast<uint32_t>(p.ldn / kSmallColumns);
+  const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
+  double bound = 1.0;
+  int ex = exponent_below(bound);
+  SmallArgs k{};
+  k.m = p.m;
+  k.n = p.n;
+  k.ld = p.ldn;
+  k.tall = a.rows > a.cols;
+  k.in = a.in;
+  k.norm = p.norm;
+  k.norm_count = count;
+  k.eps = a.eps;
+  k.x = p.sums;
+  k.next_factor = factor(1, ex);
+  const bool few = groups <= kSmallSums;
+  float* const sets[2] = {p.small_gram + (few ? 0 : kSmallGram),
+                          p.small_gram + (few ? groups : 1) * kSmallGram};
+  k.next_gram = sets[0];
+  k.out = a.out;
+  k.scale = a.scale;
+  orth_small_kernel<E><<<groups, 512, 0, s>>>(k);
+  k.in = nullptr;
+  for (int i = 0; i < a.steps; ++i) {
+    k.gram = k.next_gram;
+    k.grams = static_cast<int>(groups);
+    if (few) {
+      k.next_gram = sets[(i + 1) % 2];
+    } else {
+      orth_gram_kernel<<<kSmallGram / 64, 256, 0, s>>>(k.gram, k.grams, p.small_gram);
+      k.gram = p.small_gram;
+      k.grams = 1;
+    }
+    const double t = bound * bound;
+    const int eg = exponent_below(t);
+    const int eb = exponent_below(std::fabs(a.b) * t + std::fabs(a.c) * t * t);
+    bound = step_bound(a, bound);
+    const int next = exponent_below(bound);
+    k.g_factor = factor(1, eg - 2 * ex);
+    k.b_keep = factor(a.b, eb - eg);
+    k.b_take = factor(a.c, eb - 2 * eg);
+    k.x_factor = factor(1, ex);
+    k.keep = a.a;
+    k.take = factor(1, -eb - ex);
+    k.next_factor = factor(1, next);
+    if (i + 1 == a.steps) k.next_gram = nullptr;
+    orth_small_kernel<E><<<groups, 512, 0, s>>>(k);
+    ex = next;
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
 hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   constexpr Form X = x_form(sizeof(E));
   const Plan p = plan_of(a, sizeof(E), ws);
@@ -306,6 +602,7 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   const int count = static_cast<int>(std::min<int64_t>(blocks(elems, 2048), kNormBlocks));
   const E* in = static_cast<const E*>(a.in);
   orth_norm_kernel<E><<<count, 256, 0, s>>>(in, elems, p.norm);
+  if (p.small) return orthogonalize_small<E>(a, p, count, s);
   const Matrix x{p.x, p.xt, p.m, p.n, p.ldn, p.ldm};
   const Matrix g{p.g, nullptr, p.m, p.m, p.ldm, 0}, b{p.b, nullptr, p.m, p.m, p.ldm, 0};
   const Matrix none{};
