@@ -804,7 +804,7 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const size_t ld = up64(a.d), part_bytes = 2 * parts_of(f) * ld;
   // pieces but the last are whole tiles
   p.piece = f == kHalves ? piece_of(a.vocab, part_bytes, size_t{128} << 20) : a.vocab;
-  p.tile = wide_cut(p.piece, a.n_rows, stages(f, a.d) * products_of(f), 1, false).tile;
+  p.tile = wide_cut(p.piece, a.n_rows, stages(f, a.d) * products_of(f), 1, false, true).tile;
   p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(p.tile)));
   Carve c{static_cast<char*>(ws)};
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
@@ -833,9 +833,9 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const size_t P = parts_of(f), ld = up64(a.d), n = a.n_rows;
   p.piece = piece_of(a.vocab, 2 * P * n + (f == kHalves ? 2 * P * ld : 0), size_t{192} << 20);
   const size_t ldv = up64(p.piece);
-  p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false).tile;
+  p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false, true).tile;
   // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false);
+  p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false, false);
   Carve c{static_cast<char*>(ws)};
   p.gx = c.take<uint16_t>(P * n * a.d);
   p.dl = c.take<uint16_t>(P * n * ldv);
@@ -943,21 +943,20 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     e = with_wide_tile(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
-      product_kernel<CF, F, true, false, float, true>
+      product_kernel<CF, F, true, false>
           <<<dim3(static_cast<uint32_t>(mb) * nb, p.dx_cut.slices), CF::NT, 0, s>>>(
-              wt, dl, stages(F, ldv), mb, nb, n, v0 > 0, a.d, nullptr, 0, p.sums);
+              wt, dl, stages(F, ldv), mb, nb, n, a.d, SumStore{p.sums, a.d, n, v0 > 0});
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const Cut dw_cut = wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false);
+    const Cut dw_cut = wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false, true);
     e = with_wide_tile(dw_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));
-      product_kernel<CF, F, true, true, E, false>
-          <<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
-              gx, dlt, stages(F, n), mb, nb, rows, false, a.d, amax_x, -kDlExponent,
-              static_cast<E*>(dw) + v0 * a.d);
+      product_kernel<CF, F, true, true><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(
+          gx, dlt, stages(F, n), mb, nb, rows, a.d,
+          ElementStore<E>{static_cast<E*>(dw) + v0 * a.d, a.d, amax_x, -kDlExponent});
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -982,9 +981,9 @@ hipError_t few_z_product(const HeadArgs& a, const FewPlan& p, int64_t v0, int ro
   return with_form_tile<F>(p.z_cut.tile, [&](auto cf) {
     typedef decltype(cf) CF;
     const int mb = static_cast<int>(blocks(rows, CF::BM));
-    product_kernel<CF, F, false, false, float, true>
-        <<<dim3(mb, p.z_cut.slices), CF::NT, 0, s>>>(w, x, stages(F, a.d), mb, 1, x.rows, false,
-                                                     static_cast<int>(up64(rows)), nullptr, 0, p.z);
+    const int pitch = static_cast<int>(up64(rows));
+    product_kernel<CF, F, false, false><<<dim3(mb, p.z_cut.slices), CF::NT, 0, s>>>(
+        w, x, stages(F, a.d), mb, 1, x.rows, pitch, SumStore{p.z, pitch, x.rows, false});
     return hipGetLastError();
   });
 }
@@ -1038,9 +1037,9 @@ hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlog
     e = with_form_tile<F>(p.dx_cut.tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
-      product_kernel<CF, F == kBf16 ? kBf16Two : F, true, false, float, true>
-          <<<dim3(mb, p.dx_cut.slices), CF::NT, 0, s>>>(wt, dl, stages(F, ldv), mb, 1, n, v0 > 0,
-                                                        a.d, nullptr, 0, p.sums);
+      product_kernel<CF, F == kBf16 ? kBf16Two : F, true, false>
+          <<<dim3(mb, p.dx_cut.slices), CF::NT, 0, s>>>(wt, dl, stages(F, ldv), mb, 1, n, a.d,
+                                                        SumStore{p.sums, a.d, n, v0 > 0});
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

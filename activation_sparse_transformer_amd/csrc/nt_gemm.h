@@ -737,17 +737,61 @@ __device__ __forceinline__ int exponent_for(float m) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return ldexpf(1.f, e); }
 
-// out[col][row] (+)= A[row] . B[col], col < cols, over one slice of K per blockIdx.y, lines of
-// `pitch` elements (a multiple of 8, not under A.rows; what lies past A.rows is
-// undefined): as floats (ACC: slice after slice in out, added to where `add`) or as E.
-// Times 2^(exponent - exponent_for(*amax)) where amax is given.  n_blocks == 0: C is
-// symmetric, and only the tiles of m_blocks x m_blocks with rows up to the columns' are
-// formed.
-template <class CF, Form F, bool TA, bool TB, typename E, bool ACC>
+// Stores of 8 consecutive values of a line: value (col, row ..) of slice `slice` of a
+// product's K.
+struct SumStore {  // float sums of every slice, added to what is there where `add`
+  float* out;      // [slices][cols][pitch]
+  int pitch, cols;
+  bool add;
+  __device__ __forceinline__ void operator()(int slice, int col, int row, float (&v)[8]) const {
+    float* to = out + (static_cast<int64_t>(slice) * cols + col) * pitch + row;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4* at = reinterpret_cast<float4*>(to) + h;
+      float4 q = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      if (add) {
+        const float4 old = *at;
+        q = make_float4(q.x + old.x, q.y + old.y, q.z + old.z, q.w + old.w);
+      }
+      *at = q;
+    }
+  }
+};
+template <typename E>
+struct ElementStore {  // one slice, times 2^(exponent - exponent_for(*amax)) where amax is given
+  E* out;              // [cols][pitch]
+  int pitch;
+  const float* amax;
+  int exponent;
+  __device__ __forceinline__ void operator()(int, int col, int row, float (&v)[8]) const {
+    E* to = out + static_cast<int64_t>(col) * pitch + row;
+    if (amax != nullptr) {
+      const float f = power_of_two(exponent - exponent_for(*amax));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+    }
+    if constexpr (sizeof(E) == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = ElemTraits<uint16_t>::from_f32(v[2 * k]) |
+               static_cast<uint32_t>(ElemTraits<uint16_t>::from_f32(v[2 * k + 1])) << 16;
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+};
+
+// C[col][row] = A[row] . B[col], rows < `pitch` (a multiple of 8, not under A.rows; what
+// lies past A.rows is undefined), col < cols, over one slice of K per blockIdx.y, handed to
+// `store`.  n_blocks == 0: C is symmetric, and only the tiles of m_blocks x m_blocks with
+// rows up to the columns' are formed.
+template <class CF, Form F, bool TA, bool TB, class Store>
 __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, int ksteps,
                                                          int m_blocks, int n_blocks, int cols,
-                                                         bool add, int pitch, const float* amax,
-                                                         int exponent, E* __restrict__ out) {
+                                                         int pitch, Store store) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE + extra_lds<CF, F>()];
   int mb, nb;
   const int slices = gridDim.y, slice = blockIdx.y;
@@ -758,16 +802,6 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * ksteps / slices);
   f32x16_t acc[CF::FM][CF::FN];
   multiply<CF, F, TA, TB>(A, mb * CF::BM, B, nb * CF::BN, s0 * kStep, s1 - s0, lds, acc);
-  if (ACC) out += static_cast<int64_t>(slice) * pitch * cols;
-  if (amax != nullptr) {
-    const float f = power_of_two(exponent - exponent_for(*amax));
-#pragma unroll
-    for (int i = 0; i < CF::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < CF::FN; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] *= f;
-  }
   // 32 columns of every wave at a time through LDS, so that lines are stored whole: the
   // 16-byte chunk c of column col at position c ^ col, in two buffers taken in turn
   constexpr int CHUNKS = CF::BM / 4, COLS = CF::WAVES_N * 32;
@@ -787,31 +821,16 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
             make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
     __syncthreads();
-    constexpr int STEP = sizeof(E) == 2 ? 2 : 1;  // chunks of a 16-byte store
-    for (int e = threadIdx.x; e < COLS * CHUNKS / STEP; e += CF::NT) {
-      const int at = e / (CHUNKS / STEP), c = e % (CHUNKS / STEP) * STEP;
+    for (int e = threadIdx.x; e < COLS * CHUNKS / 2; e += CF::NT) {
+      const int at = e / (CHUNKS / 2), c = e % (CHUNKS / 2) * 2;
       const int col = nb * CF::BN + at / 32 * CF::WTN + j * 32 + at % 32;
       const int row = mb * CF::BM + c * 4;
       if (col >= cols || row >= pitch) continue;
-      E* to = out + static_cast<int64_t>(col) * pitch + row;
       const float* from = buffer + at * CF::BM;
-      float4 v = *reinterpret_cast<const float4*>(from + ((c ^ at) & (CHUNKS - 1)) * 4);
-      if constexpr (sizeof(E) == 2) {
-        const float4 u =
-            *reinterpret_cast<const float4*>(from + (((c + 1) ^ at) & (CHUNKS - 1)) * 4);
-        typedef ElemTraits<uint16_t> Tr;
-        const auto pair = [](float a, float b) {
-          return Tr::from_f32(a) | static_cast<uint32_t>(Tr::from_f32(b)) << 16;
-        };
-        *reinterpret_cast<uint4*>(to) =
-            make_uint4(pair(v.x, v.y), pair(v.z, v.w), pair(u.x, u.y), pair(u.z, u.w));
-      } else {
-        if (ACC && add) {
-          const float4 old = *reinterpret_cast<const float4*>(to);
-          v = make_float4(v.x + old.x, v.y + old.y, v.z + old.z, v.w + old.w);
-        }
-        *reinterpret_cast<float4*>(to) = v;
-      }
+      const float4 p = *reinterpret_cast<const float4*>(from + ((c ^ at) & (CHUNKS - 1)) * 4);
+      const float4 q = *reinterpret_cast<const float4*>(from + (((c + 1) ^ at) & (CHUNKS - 1)) * 4);
+      float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+      store(slice, col, row, v);
     }
   }
 }
@@ -860,8 +879,10 @@ inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int64_t most_slice
 }
 // Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us to fill and
 // to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us), with as many
-// slices as pay for writing and adding up their float32 sums (5 TB/s).
-inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle) {
+// slices as pay for writing and adding up their float32 sums (5 TB/s); `whole`: one slice
+// writes none.
+inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle,
+                    bool whole) {
   Cut best{kMid, 1};
   double least = 1e300;
   for (const Tile t : {kBig, kMid}) {
@@ -874,7 +895,7 @@ inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, 
       if (t == kBig) us = blocks(groups, 256) * (each * 2.1 + 6);
       else if (groups <= 256) us = each * 0.78 + 4;
       else us = blocks(groups, 512) * (each * 1.25 + 4);
-      if (most_slices > 1) us += static_cast<double>(s) * tiles * tile_rows(t) * tile_cols(t) * 8 / 5e6;
+      if (s > 1 || !whole) us += static_cast<double>(s) * tiles * tile_rows(t) * tile_cols(t) * 8 / 5e6;
       if (us < least) {
         least = us;
         best = {t, s};

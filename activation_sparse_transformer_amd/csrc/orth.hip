@@ -14,8 +14,9 @@
 // |X| <= 1 at the start, and max |a s + b s^3 + c s^5| bounds it after each step, so the
 // powers of two that the parts are scaled by are known on the host.  A product leaves
 // float32 partial sums, slices of K where its tiles are few; a pass over them adds the
-// slices, forms G, B or the next X in float32 and writes its parts, X also transposed,
-// since both G and B X contract K-major operands.
+// slices, forms G, B or the next X in float32 and writes its parts.  Where B X takes one
+// slice, its epilogue does that.  G contracts X's rows and B X its columns, which it reads
+// turned (nt_gemm.h).
 #include <algorithm>
 #include <cmath>
 
@@ -65,50 +66,63 @@ __device__ __forceinline__ double inverse_norm(const double* __restrict__ parts,
   return 1.0 / (sqrt(total) + static_cast<double>(eps));
 }
 
-struct Matrix {  // two parts of [rows][cols], and the parts of its transpose
-  uint16_t *p, *t;
-  int rows, cols, ld, ldt;
+struct Matrix {  // two parts of [rows][cols], columns up to ld zeros
+  uint16_t* p;
+  int rows, cols, ld;
 };
 
 // 8 scaled values of row i, from column j on, as parts.
-template <Form F>
 __device__ __forceinline__ void put_row(const Matrix& x, int i, int j, const float (&v)[8]) {
-  constexpr int P = parts_of(F);
-  uint32_t w[P][4];
+  uint32_t w[2][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint16_t lo[P], hi[P];
-    split<F>(v[2 * k], lo);
-    split<F>(v[2 * k + 1], hi);
+    uint16_t lo[2], hi[2];
+    split<kHalves>(v[2 * k], lo);
+    split<kHalves>(v[2 * k + 1], hi);
 #pragma unroll
-    for (int p = 0; p < P; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+    for (int p = 0; p < 2; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
   }
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < 2; ++p)
     *reinterpret_cast<uint4*>(x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j) =
         make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
-
-// The transposed parts of a tile in LDS (zeros past the matrix).
-template <Form F>
-__device__ __forceinline__ void put_transposed(const Matrix& x, int i0, int j0,
-                                               const float (&tile)[64][65]) {
+// The values of them.
+__device__ __forceinline__ void get_row(const Matrix& x, int i, int j, float (&v)[8]) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int run = threadIdx.x + 256 * u;
-    const int j = run / 8, i = run % 8 * 8;
-    if (j0 + j >= x.cols) continue;
-    const Matrix t{x.t, nullptr, x.cols, 0, x.ldt, 0};
-    float v[8];
+  for (int k = 0; k < 8; ++k) v[k] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = tile[i + k][j];
-    put_row<F>(t, j0 + j, i0 + i, v);
+  for (int p = 1; p >= 0; --p) {
+    const uint4 w = *reinterpret_cast<const uint4*>(
+        x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j);
+    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+      const f16x2_t h = __builtin_bit_cast(f16x2_t, d[k]);
+      v[2 * k] += static_cast<float>(h[0]);
+      v[2 * k + 1] += static_cast<float>(h[1]);
+    }
   }
 }
 
+// The epilogue of B X in one slice: X' = keep X + take (B X).
+struct UpdateStore {
+  Matrix old, out;
+  float keep, take;
+  __device__ __forceinline__ void operator()(int, int i, int j, float (&v)[8]) const {
+    float o[8];
+    get_row(old, i, j, o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = j + k < out.cols ? fmaf(keep, o[k], take * v[k]) : 0.f;
+    put_row(out, i, j, v);
+  }
+};
+
 // X = 2^exponent M / (|M|_F + eps): one 64 x 64 tile a workgroup.  `tall`: M is
 // [cols][rows].
-template <typename E, Form F>
+template <typename E>
 __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m, bool tall,
                                                          const double* __restrict__ parts,
                                                          int count, float eps, int exponent,
@@ -137,22 +151,20 @@ __global__ __launch_bounds__(256) void orth_start_kernel(const E* __restrict__ m
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = tile[i][j + k];
-    put_row<kHalves>(x, i0 + i, j0 + j, v);
+    put_row(x, i0 + i, j0 + j, v);
   }
-  put_transposed<F>(x, i0, j0, tile);
 }
 
-// v = keep * (old's value) + take * (the sum of the slices), to out's parts (and
-// their transpose where out.t), or to `last` [rows][cols] as E, transposed where
-// `tall`.  sums [slices][rows][pitch]; `block`: out is symmetric and sums holds its tiles
-// of that size with columns up to the rows', the rest is their mirror image.  old and out
-// may be one matrix: a workgroup reads its tile of old before it writes.
-template <typename E, Form F>
+// v = keep * (old's value) + take * (the sum of the slices), to out's parts, or to `last`
+// [rows][cols] as E, transposed where `tall`.  sums [slices][rows][pitch]; `block`: out is
+// symmetric and sums holds its tiles of that size with columns up to the rows', the rest is
+// their mirror image.
+template <typename E>
 __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restrict__ sums,
                                                           int slices, int block, int pitch,
                                                           float keep, float take, Matrix old,
-                                                          Matrix out,
-                                                          E* __restrict__ last, bool tall) {
+                                                          Matrix out, E* __restrict__ last,
+                                                          bool tall) {
   __shared__ float tile[64][65];
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
   const bool mirror = block != 0 && i0 / block != j0 / block;
@@ -165,6 +177,7 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
     float v[8] = {};
     if (i0 + i < out.rows) {
       const float* s = sums + static_cast<int64_t>(i0 + i) * pitch + j0 + j;
+#pragma unroll 4
       for (int q = 0; q < slices; ++q) {
         const float4 a = *reinterpret_cast<const float4*>(s + q * plane);
         const float4 b = *reinterpret_cast<const float4*>(s + q * plane + 4);
@@ -172,35 +185,31 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
         v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
       }
       float o[8] = {};
-      if (old.p != nullptr) {
-#pragma unroll
-        for (int p = 1; p >= 0; --p) {
-          const uint4 w = *reinterpret_cast<const uint4*>(
-              old.p + (static_cast<int64_t>(p) * old.rows + i0 + i) * old.ld + j0 + j);
-          const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
-            const f16x2_t h = __builtin_bit_cast(f16x2_t, d[k]);
-            o[2 * k] += static_cast<float>(h[0]);
-            o[2 * k + 1] += static_cast<float>(h[1]);
-          }
-        }
-      }
+      if (old.p != nullptr) get_row(old, i0 + i, j0 + j, o);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[k] = j0 + j + k < out.cols ? fmaf(keep, o[k], take * v[k]) : 0.f;
       }
-      if (last == nullptr) put_row<kHalves>(out, i0 + i, j0 + j, v);
+      if (last == nullptr) put_row(out, i0 + i, j0 + j, v);
     }
+    if (mirror || last != nullptr) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
+      for (int k = 0; k < 8; ++k) tile[i][j + k] = v[k];
+    }
   }
-  if (last == nullptr && out.t == nullptr && !mirror) return;
+  if (last == nullptr && !mirror) return;
   __syncthreads();
-  if (mirror) out.t = out.p, out.ldt = out.ld;
   if (last == nullptr) {
-    put_transposed<F>(out, i0, j0, tile);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int run = threadIdx.x + 256 * u;
+      const int j = run / 8, i = run % 8 * 8;
+      if (j0 + j >= out.rows) continue;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = tile[i + k][j];
+      put_row(out, j0 + j, i0 + i, v);
+    }
     return;
   }
   for (int e = threadIdx.x; e < 64 * 64; e += 256) {
@@ -445,7 +454,7 @@ struct Plan {
   int m, n, ldm, ldn;
   Cut gram, square, update;
   double* norm;
-  uint16_t *x, *xt, *g, *b;
+  uint16_t *x[2], *g, *b;  // X before and after a step
   float *sums, *small_gram;
   bool small;
   size_t bytes;
@@ -472,15 +481,13 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
     p.bytes = c.used;
     return p;
   }
-  p.gram = wide_cut(p.m, p.m, p.ldn / 64 * gram, 32, true);
-  p.square = wide_cut(p.m, p.m, p.ldm / 64 * 3, 32, true);
-  p.update = p.m <= kFewColumns ? few_cut(p.n, p.m, p.ldm / 64 * update, 32)
-                                : wide_cut(p.n, p.m, p.ldm / 64 * update, 32, false);
+  p.gram = wide_cut(p.m, p.m, p.ldn / 64 * gram, 32, true, false);
+  p.square = wide_cut(p.m, p.m, p.ldm / 64 * 3, 32, true, false);
+  p.update = wide_cut(p.n, p.m, p.ldm / 64 * update, 32, false, true);
   const size_t square = static_cast<size_t>(p.m) * p.ldm, whole = static_cast<size_t>(p.m) * p.ldn;
   Carve c{static_cast<char*>(ws)};
   p.norm = c.take<double>(kNormBlocks);
-  p.x = c.take<uint16_t>(P * whole);
-  p.xt = c.take<uint16_t>(PX * p.n * p.ldm);
+  for (uint16_t*& x : p.x) x = c.take<uint16_t>(P * whole);
   p.g = c.take<uint16_t>(P * square);
   p.b = c.take<uint16_t>(P * square);
   p.sums = c.take<float>(std::max(std::max(p.gram.slices, p.square.slices) * square,
@@ -489,24 +496,17 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   return p;
 }
 
-template <Form F, class CF>
-hipError_t product(CF, const Operand& A, const Operand& B, int ksteps, const Cut& cut,
-                   bool triangle, int pitch, float* sums, hipStream_t s) {
-  const int mb = static_cast<int>(blocks(A.rows, CF::BM));
-  const int nb = static_cast<int>(blocks(B.rows, CF::BN));
-  const uint32_t tiles =
-      triangle ? static_cast<uint32_t>(mb) * (mb + 1) / 2 : static_cast<uint32_t>(mb) * nb;
-  product_kernel<CF, F, false, false, float, true><<<dim3(tiles, cut.slices), CF::NT, 0, s>>>(
-      A, B, ksteps, mb, triangle ? 0 : nb, B.rows, false, pitch, nullptr, 0, sums);
-  return hipGetLastError();
-}
-
 // sums = A A^T, by its triangle of tiles.
 template <Form F>
 hipError_t square_of(const Operand& A, int ksteps, const Cut& cut, int pitch, float* sums,
                      hipStream_t s) {
   return with_wide_tile(cut.tile, [&](auto cf) {
-    return product<F>(cf, A, A, ksteps, cut, true, pitch, sums, s);
+    typedef decltype(cf) CF;
+    const int mb = static_cast<int>(blocks(A.rows, CF::BM));
+    product_kernel<CF, F, false, false>
+        <<<dim3(static_cast<uint32_t>(mb) * (mb + 1) / 2, cut.slices), CF::NT, 0, s>>>(
+            A, A, ksteps, mb, 0, A.rows, pitch, SumStore{sums, pitch, A.rows, false});
+    return hipGetLastError();
   });
 }
 
@@ -603,20 +603,22 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
   const E* in = static_cast<const E*>(a.in);
   orth_norm_kernel<E><<<count, 256, 0, s>>>(in, elems, p.norm);
   if (p.small) return orthogonalize_small<E>(a, p, count, s);
-  const Matrix x{p.x, p.xt, p.m, p.n, p.ldn, p.ldm};
-  const Matrix g{p.g, nullptr, p.m, p.m, p.ldm, 0}, b{p.b, nullptr, p.m, p.m, p.ldm, 0};
+  const Matrix g{p.g, p.m, p.m, p.ldm}, b{p.b, p.m, p.m, p.ldm};
   const Matrix none{};
   const dim3 whole(p.ldn / 64, p.ldm / 64), square(p.ldm / 64, p.ldm / 64);
   double bound = 1.0;  // of X's singular values
   int ex = exponent_below(bound);
-  orth_start_kernel<E, X><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex, x);
-  const Operand xo{p.x, static_cast<int64_t>(p.m) * p.ldn, p.ldn, p.m, p.ldn};
-  const Operand xt{p.xt, static_cast<int64_t>(p.n) * p.ldm, p.ldm, p.n, p.ldm};
-  const Operand go{p.g, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, p.ldm};
-  const Operand bo{p.b, static_cast<int64_t>(p.m) * p.ldm, p.ldm, p.m, p.ldm};
+  orth_start_kernel<E><<<whole, 256, 0, s>>>(in, tall, p.norm, count, a.eps, ex,
+                                             Matrix{p.x[0], p.m, p.n, p.ldn});
+  const int64_t part = static_cast<int64_t>(p.m) * p.ldn, square_part = int64_t{p.m} * p.ldm;
+  const Operand go{p.g, square_part, p.ldm, p.m, p.ldm};
+  const Operand bo{p.b, square_part, p.ldm, p.m, p.ldm};
   E* no_output = nullptr;
   for (int i = 0; i < a.steps; ++i) {
     const bool end = i + 1 == a.steps;
+    const Matrix x{p.x[i % 2], p.m, p.n, p.ldn}, after{p.x[(i + 1) % 2], p.m, p.n, p.ldn};
+    const Operand xo{x.p, part, p.ldn, p.m, p.ldn};
+    const Operand xt{x.p, part, p.ldn, p.ldn, p.m};  // turned
     const double t = bound * bound;
     const int eg = exponent_below(t);
     const int eb = exponent_below(std::fabs(a.b) * t + std::fabs(a.c) * t * t);
@@ -626,27 +628,37 @@ hipError_t orthogonalize(const OrthArgs& a, void* ws, hipStream_t s) {
     const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
     hipError_t e = square_of<X>(xo, p.ldn / 64, p.gram, p.ldm, p.sums, s);
     if (e != hipSuccess) return e;
-    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.gram.slices,
-                                                          tile_rows(p.gram.tile), p.ldm, 0.f,
-                                                 factor(1, eg - 2 * ex), none, g, no_output, false);
+    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.gram.slices, tile_rows(p.gram.tile),
+                                                 p.ldm, 0.f, factor(1, eg - 2 * ex), none, g,
+                                                 no_output, false);
     if ((e = square_of<kHalves>(go, p.ldm / 64, p.square, p.ldm, p.sums, s)) != hipSuccess)
       return e;
-    orth_finish_kernel<E, kHalves><<<square, 256, 0, s>>>(p.sums, p.square.slices,
-                                                          tile_rows(p.square.tile), p.ldm,
+    orth_finish_kernel<E><<<square, 256, 0, s>>>(p.sums, p.square.slices,
+                                                 tile_rows(p.square.tile), p.ldm,
                                                  factor(a.b, eb - eg), factor(a.c, eb - 2 * eg), g,
                                                  b, no_output, false);
-    const auto update = [&](auto cf) {
-      return product<X == kHalf ? kMixed : kHalves>(cf, xt, bo, p.ldm / 64, p.update, false, p.ldn,
-                                                    p.sums, s);
-    };
-    e = p.m <= kFewColumns ? with_few_tile(p.update.tile, update)
-                           : with_wide_tile(p.update.tile, update);
-    if (e != hipSuccess) return e;
     const double scale = end ? a.scale : 1.0;
     const int out = end ? 0 : next;
-    orth_finish_kernel<E, X><<<whole, 256, 0, s>>>(
-        p.sums, p.update.slices, 0, p.ldn, factor(scale * a.a, out - ex), factor(scale, out - eb - ex),
-        x, x, end ? static_cast<E*>(a.out) : no_output, tall);
+    const float keep = factor(scale * a.a, out - ex), take = factor(scale, out - eb - ex);
+    const bool fused = p.update.slices == 1 && !end;
+    e = with_wide_tile(p.update.tile, [&](auto cf) {
+      typedef decltype(cf) CF;
+      constexpr Form F = X == kHalf ? kMixed : kHalves;
+      const int mb = static_cast<int>(blocks(p.n, CF::BM)), nb = static_cast<int>(blocks(p.m, CF::BN));
+      const dim3 grid(static_cast<uint32_t>(mb) * nb, p.update.slices);
+      if (fused)
+        product_kernel<CF, F, true, false><<<grid, CF::NT, 0, s>>>(
+            xt, bo, p.ldm / 64, mb, nb, p.m, p.ldn, UpdateStore{x, after, keep, take});
+      else
+        product_kernel<CF, F, true, false><<<grid, CF::NT, 0, s>>>(
+            xt, bo, p.ldm / 64, mb, nb, p.m, p.ldn, SumStore{p.sums, p.ldn, p.m, false});
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    if (!fused)
+      orth_finish_kernel<E><<<whole, 256, 0, s>>>(p.sums, p.update.slices, 0, p.ldn, keep, take, x,
+                                                  after,
+                                                  end ? static_cast<E*>(a.out) : no_output, tall);
     ex = next;
   }
   return hipGetLastError();
