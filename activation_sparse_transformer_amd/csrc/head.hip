@@ -522,8 +522,10 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
   }
 }
 
-// dx = the sum of the slices, rounded: 4 elements a lane, the slices in 4 streams.  Halves:
-// times scale * dlogp of the row and the powers of two undone.
+// dx = the sum of the slices, rounded: 4 elements a lane, the slices in 4 streams; rows
+// without a target zero, also where an infinity of w met their dl.  Halves: times scale *
+// dlogp of the row and the powers of two undone.  The grid is two-dimensional: a launch
+// holds fewer than 2^32 lanes along one.
 template <typename E, Form F>
 __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* __restrict__ sums,
                                                       int slices, const float* __restrict__ dlogp,
@@ -531,7 +533,8 @@ __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* _
   __shared__ float4 joint[3][64];
   const int64_t elems = a.n_rows * a.d;
   const int at = threadIdx.x % 64, stream = threadIdx.x / 64;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 64 + at) * 4;
+  const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t i = (block * 64 + at) * 4;
   float4 v = make_float4(0, 0, 0, 0);
   if (i < elems)
 #pragma unroll 8
@@ -550,13 +553,13 @@ __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* _
       }
   }
   if (stream != 0 || i >= elems) return;
+  const int64_t n = i / a.d;
+  const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
+  if (!given) v = make_float4(0, 0, 0, 0);
   if constexpr (F == kHalves) {
-    const int64_t n = i / a.d;
-    const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
     const float f = power_of_two(-kDlExponent - exponent_for(*amax));
     const float g = given ? dlogp[n] * a.scale : 0.f;
-    v = given ? make_float4(v.x * f * g, v.y * f * g, v.z * f * g, v.w * f * g)
-              : make_float4(0, 0, 0, 0);
+    v = make_float4(v.x * f * g, v.y * f * g, v.z * f * g, v.w * f * g);
   }
   if constexpr (sizeof(E) == 2)
     *reinterpret_cast<uint2*>(dx + i) = make_uint2(pack_part<kBf16>(v.x, v.y, 0),
@@ -885,6 +888,12 @@ RowResults row_results(const HeadArgs& a, float* logp, float* lse, float* stats)
   return RowResults{a.targets, a.index_bytes, a.vocab, logp, lse, reinterpret_cast<float2*>(stats)};
 }
 
+dim3 dx_grid(const HeadArgs& a) {
+  const int64_t all = blocks(a.n_rows * a.d, 256), across = std::min<int64_t>(all, 1 << 20);
+  return dim3(static_cast<uint32_t>(across),
+              static_cast<uint32_t>(blocks(all, static_cast<int>(across))));
+}
+
 template <Form F>
 hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* stats,
                    hipStream_t s) {
@@ -961,7 +970,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     });
     if (e != hipSuccess) return e;
   }
-  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d, 256)), 256, 0, s>>>(
+  head_dx_kernel<E, F><<<dx_grid(a), 256, 0, s>>>(
       a, p.sums, p.dx_cut.slices, dlogp, amax_w, static_cast<E*>(dx));
   return hipGetLastError();
 }
@@ -1050,7 +1059,7 @@ hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlog
     head_few_dw_kernel<F><<<dim3(static_cast<uint32_t>(across), groups), 256, 0, s>>>(
         a, p.dlt, rows, p.kn, static_cast<E*>(dw) + v0 * a.d);
   }
-  head_dx_kernel<E, F><<<static_cast<uint32_t>(blocks(a.n_rows * a.d, 256)), 256, 0, s>>>(
+  head_dx_kernel<E, F><<<dx_grid(a), 256, 0, s>>>(
       a, p.sums, p.dx_cut.slices, dlogp, nullptr, static_cast<E*>(dx));
   return hipGetLastError();
 }

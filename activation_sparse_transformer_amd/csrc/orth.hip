@@ -511,8 +511,9 @@ hipError_t square_of(const Operand& A, int ksteps, const Cut& cut, int pitch, fl
 }
 
 // The exponent by which values up to `bound` are scaled: below 2^15 (of halves, whose
-// largest is 2^16 - 2^5), with room for roundings.
+// largest is 2^16 - 2^5), with room for roundings; past 2^115 they become infinities.
 int exponent_below(double bound) {
+  if (!std::isfinite(bound)) return -100;
   int e;
   std::frexp(std::max(bound * 1.0625, 1e-30), &e);  // bound * 1.0625 < 2^e
   return std::max(15 - e, -100);

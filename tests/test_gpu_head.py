@@ -116,6 +116,14 @@ def test_matches_oracle(n, v, d, scale, index, dtype):
 
 @pytest.mark.gpu
 @BOTH
+@pytest.mark.parametrize("n,v,d", [(20, 60000, 1000), (70, 100000, 1344), (1100, 100000, 64)])
+def test_vocabularies_of_several_pieces(n, v, d, dtype):
+    say(f"head in pieces {dtype} n={n} v={v} d={d}")
+    check(make(n + v + d, n, v, d, dtype))
+
+
+@pytest.mark.gpu
+@BOTH
 @pytest.mark.parametrize("n", [1, 40, 70, 200])
 def test_every_bit_of_the_operands(n, dtype):
     """One product a logit: x and w one-hot rows with values of all mantissa bits.  bfloat16: z is
@@ -151,6 +159,60 @@ def test_masked_rows_spread_nothing(n, v, d, dtype):
     again = backward(m, got.stats)
     assert not got.logp[skip].any() and torch.equal(got.logp, clean.logp)
     assert torch.equal(again.dx, grads.dx) and torch.equal(again.dw, grads.dw)
+
+
+@pytest.mark.gpu
+@BOTH
+@pytest.mark.parametrize("n", [5, 200])
+def test_masked_rows_beside_infinite_weights(n, dtype):
+    """A row without a target has no gradient, also where w holds infinities and NaN."""
+    m = make(3, n, 300, 64, dtype)
+    m["w"][7, 5] = float("inf")
+    m["w"][8, 6] = float("nan")
+    got = forward(m)
+    grads = backward(m, got.stats)
+    skip = (m["t"] < 0) | (m["t"] >= 300)
+    assert not got.logp[skip].any() and torch.isnan(got.logp[~skip]).all()
+    assert not grads.dx[skip].any()
+
+
+@pytest.mark.gpu
+def test_more_elements_than_a_launch_has_lanes():
+    """x and dx past 2^32 elements: rows at both ends have the results of a small call with the
+    same weights, and dw is theirs."""
+    say("2^20 + 72 rows of 4096")
+    n, d, v = (1 << 20) + 72, 4096, 40
+    part = make(4, 144, v, d, torch.bfloat16)
+    part["dlogp"] = torch.full((144,), -2.0 ** -20)
+    x, t = part["x"].cuda(), part["t"].cuda()
+    big = torch.zeros((n, d), dtype=torch.bfloat16, device="cuda")
+    targets = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    # the first and the last 72 rows have targets
+    for rows, at in ((slice(0, 72), slice(0, 72)), (slice(n - 72, n), slice(72, 144))):
+        big[rows] = x[at]
+        targets[rows] = t[at]
+    dlogp = torch.full((n,), -2.0 ** -20, device="cuda")
+    w = part["w"].cuda()
+    got = twell.twell_head_logprob_forward(big, w, targets)
+    grads = twell.twell_head_logprob_backward(big, w, targets, got.stats, dlogp)
+    torch.cuda.synchronize()
+    small = forward(part)
+    ref = backward(part, small.stats)
+    ends = lambda v: torch.cat([v[:72], v[n - 72:]]).double()
+    # both are within ez of z; each dl is then within a step of bfloat16 (2^-7) of the other's,
+    # and sums of |dl| over a row stay under 2 |dlogp|, over a column under its terms' sizes
+    ez = 2 * errors_of_z(as_f64(x), as_f64(w), 1.0).max()
+    for a, b in ((got.logp, small.logp), (got.lse, small.lse)):
+        assert float((ends(a) - b).abs().max()) <= 2 * ez + 2.0 ** -19 * (1 + float(b.abs().max()))
+    step = 2.0 ** -7 + 4 * ez
+    off = (ends(grads.dx) - ref.dx.double()).abs()
+    size = 2 * dlogp[0].abs() * w.double().abs().max()
+    assert bool((off <= 2.0 ** -7 * ref.dx.double().abs() + step * size).all())
+    assert not got.logp[72:n - 72].any()
+    assert not grads.dx[72:n - 72].any()
+    off = (grads.dw.double() - ref.dw.double()).abs()
+    size = dlogp[0].abs() * x.double().abs().sum(0)
+    assert bool((off <= 2.0 ** -7 * ref.dw.double().abs() + step * size).all())
 
 
 @pytest.mark.gpu
