@@ -71,21 +71,26 @@ struct Matrix {  // two parts of [rows][cols], columns up to ld zeros
   int rows, cols, ld;
 };
 
+// The parts of two values, packed: split<kHalves> but for infinities and NaN, which both
+// parts carry (NaN is what M's infinities and NaN make of every result).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&part)[2]) {
+  typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+  const f16x2_t hi = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+  const f16x2_t lo = {static_cast<_Float16>(a - static_cast<float>(hi[0])),
+                      static_cast<_Float16>(b - static_cast<float>(hi[1]))};
+  part[0] = __builtin_bit_cast(uint32_t, hi);
+  part[1] = __builtin_bit_cast(uint32_t, lo);
+}
+
 // 8 scaled values of row i, from column j on, as parts.
 __device__ __forceinline__ void put_row(const Matrix& x, int i, int j, const float (&v)[8]) {
-  uint32_t w[2][4];
+  uint32_t w[4][2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint16_t lo[2], hi[2];
-    split<kHalves>(v[2 * k], lo);
-    split<kHalves>(v[2 * k + 1], hi);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) w[p][k] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
-  }
+  for (int k = 0; k < 4; ++k) split_pair(v[2 * k], v[2 * k + 1], w[k]);
 #pragma unroll
   for (int p = 0; p < 2; ++p)
     *reinterpret_cast<uint4*>(x.p + (static_cast<int64_t>(p) * x.rows + i) * x.ld + j) =
-        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
 }
 // The values of them.
 __device__ __forceinline__ void get_row(const Matrix& x, int i, int j, float (&v)[8]) {
@@ -224,12 +229,16 @@ __global__ __launch_bounds__(256) void orth_finish_kernel(const float* __restric
 
 // ---------------------------------------------------------------- short sides up to 128
 // One launch a step: a workgroup holds G and B, 128 x 128 with zeros past m, in LDS, forms
-// B for itself, and takes 64 columns of X: X' = a X + B X and their part of the next G =
-// X' X'^T, which the next launch adds up.  X stays float32 [m][ld] in memory.  What a step
-// cost before was its six launches (512 x 128: 38 us a step).
-constexpr int kSmallSide = 128, kSmallColumns = 64;
+// B for itself, and takes 128 columns of X: X' = a X + B X and their part of the next G =
+// X' X'^T, which the next launch adds up.  X stays float32 [m][ld] in memory.  512 x 128
+// float32 takes 90 us in all, with a launch a product and pass as below 185; 128 x 65536
+// 265, and 596.  A step's 15 us are spent between barriers: 3 us on loads that wait for the
+// launch before, 5 on splitting G, B and X into parts, 4 on MFMA.
+constexpr int kSmallSide = 128, kSmallColumns = 128, kSmallLanes = 1024;
 constexpr int kSmallGram = kSmallSide * kSmallSide;
-constexpr int kSmallSums = 16;  // more workgroups' sums of G are added up by a launch of its own
+// More workgroups' sums of G are added up by a launch of its own (128 x 768: 97 us, 98 so;
+// 128 x 1024: 104, 97 so).
+constexpr int kSmallSums = 6;
 
 struct SmallArgs {
   int m, n, ld;
@@ -255,159 +264,177 @@ struct SmallArgs {
 __device__ __forceinline__ int panel_offset(int rows, int r, int k) {
   return (k >> 6) * rows * kStep + tile_offset(r, (k >> 3) & 7) + (k & 7);
 }
-__device__ __forceinline__ void put8(uint16_t* tile, int rows, int r, int k, const float (&v)[8],
-                                     int part) {
-  uint32_t w[2][4];
+// 8 and 4 values side by side, as parts; and what the parts hold.
+__device__ __forceinline__ void put8(uint16_t* tile, int part, int at, const float (&v)[8]) {
+  uint32_t w[4][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint16_t lo[2], hi[2];
-    split<kHalves>(v[2 * i], lo);
-    split<kHalves>(v[2 * i + 1], hi);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) w[p][i] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
-  }
+  for (int k = 0; k < 4; ++k) split_pair(v[2 * k], v[2 * k + 1], w[k]);
 #pragma unroll
   for (int p = 0; p < 2; ++p)
-    *reinterpret_cast<uint4*>(tile + p * part + panel_offset(rows, r, k)) =
-        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    *reinterpret_cast<uint4*>(tile + p * part + at) =
+        make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
 }
-__device__ __forceinline__ float value_of(const uint16_t* tile, int part, int at) {
-  return static_cast<float>(__builtin_bit_cast(_Float16, tile[part + at])) +
-         static_cast<float>(__builtin_bit_cast(_Float16, tile[at]));
+__device__ __forceinline__ void put4(uint16_t* tile, int part, int at, const float (&v)[4]) {
+  uint32_t a[2], b[2];
+  split_pair(v[0], v[1], a);
+  split_pair(v[2], v[3], b);
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    *reinterpret_cast<uint2*>(tile + p * part + at) = make_uint2(a[p], b[p]);
+}
+__device__ __forceinline__ void get4(const uint16_t* tile, int part, int at, float (&v)[4]) {
+  typedef __attribute__((ext_vector_type(4))) _Float16 f16x4_t;
+  const f16x4_t hi = __builtin_bit_cast(f16x4_t, *reinterpret_cast<const uint2*>(tile + at));
+  const f16x4_t lo = __builtin_bit_cast(f16x4_t, *reinterpret_cast<const uint2*>(tile + part + at));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = static_cast<float>(lo[k]) + static_cast<float>(hi[k]);
 }
 
-// acc = A B^T of 32 rows of A from ra and 32 FN of B from rb, K in 16s, the small products
+// acc = A B^T of 32 rows of A from ra and 32 of B from rb, K of KS 16s, the small products
 // of the parts over the whole of K first.
-template <int FN>
-__device__ __forceinline__ void small_product(const uint16_t* a, int rows_a, int part_a, int ra,
-                                              const uint16_t* b, int rows_b, int part_b, int rb,
-                                              int k16, f32x16_t (&acc)[FN]) {
+template <int KS>
+__device__ __forceinline__ f32x16_t small_block(const uint16_t* a, int ra, const uint16_t* b,
+                                                int rb) {
+  constexpr int N = kSmallSide, PART = kSmallSide * kSmallSide;
   const int l = lane_id() & 31, half = lane_id() >> 5;
+  f32x16_t acc;
 #pragma unroll
-  for (int j = 0; j < FN; ++j)
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 3; ++q)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const uint16_t* ap = a + (q == 0 ? part_a : 0);
-    const uint16_t* bp = b + (q == 1 ? part_b : 0);
-    for (int ks = 0; ks < k16; ++ks) {
+    for (int ks = 0; ks < KS; ++ks) {
       const int k = ks * 16 + half * 8;
-      const i32x4_t f = *reinterpret_cast<const i32x4_t*>(ap + panel_offset(rows_a, ra + l, k));
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        acc[j] = mfma<kHalves>(f,
-                               *reinterpret_cast<const i32x4_t*>(
-                                   bp + panel_offset(rows_b, rb + 32 * j + l, k)),
-                               acc[j]);
+      acc = mfma<kHalves>(*reinterpret_cast<const i32x4_t*>(a + (q == 0 ? PART : 0) +
+                                                            panel_offset(N, ra + l, k)),
+                          *reinterpret_cast<const i32x4_t*>(b + (q == 1 ? PART : 0) +
+                                                            panel_offset(N, rb + l, k)),
+                          acc);
     }
-  }
+  return acc;
+}
+// The same with K the matrix's shorter side.
+__device__ __forceinline__ f32x16_t small_product(const uint16_t* a, int ra, const uint16_t* b,
+                                                  int rb, int m) {
+  return m > 64 ? small_block<8>(a, ra, b, rb) : small_block<4>(a, ra, b, rb);
+}
+
+// Element i of column c of a block of X', K along the columns: lines of a column each, to be
+// read turned (nt_gemm.h), 64 of them after another.
+__device__ __forceinline__ int turned_place(int c, int i) {
+  return (c >> 6) * kStep * kSmallSide + turned_offset<kSmallSide>(c & 63, i);
+}
+// acc = A A^T of rows ra and rb, the small products first.
+__device__ __forceinline__ f32x16_t small_turned(const uint16_t* tile, int ra, int rb) {
+  constexpr int N = kSmallSide, PART = kSmallSide * kSmallColumns;
+  f32x16_t acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int k0 = 0; k0 < kSmallColumns; k0 += kStep) {
+      i32x4_t f[4], h[4];
+      read_turned<N>(lds_address(tile + (q == 0 ? PART : 0) + k0 * N) + turned_at<N>(ra), f);
+      read_turned<N>(lds_address(tile + (q == 1 ? PART : 0) + k0 * N) + turned_at<N>(rb), h);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) acc = mfma<kHalves>(f[ks], h[ks], acc);
+    }
+  return acc;
 }
 
 template <typename E>
-__global__ __launch_bounds__(512) void orth_small_kernel(SmallArgs a) {
-  constexpr int N = kSmallSide, C = kSmallColumns;
-  // G, then B: two parts [N][N]; X's block: two parts [C][N], then [N][C]
-  __shared__ __attribute__((aligned(16))) uint16_t g[2 * N * N];
-  __shared__ __attribute__((aligned(16))) uint16_t xb[2 * C * N];
-  __shared__ double sum[512];
-  const int wave = threadIdx.x / kWave, wm = wave / 2 * 32, wn = wave % 2;
+__global__ __launch_bounds__(kSmallLanes) void orth_small_kernel(SmallArgs a) {
+  constexpr int N = kSmallSide, C = kSmallColumns, PART = N * N;
+  static_assert(C == N && kSmallLanes == N * C / 1024 * kWave, "a 32 x 32 block a wave");
+  // G, then B: two parts [N][N]; X's block, then X': two parts [C][N]
+  __shared__ __attribute__((aligned(16))) uint16_t g[2 * PART];
+  __shared__ __attribute__((aligned(16))) uint16_t xb[2 * PART];
+  __shared__ double sum[kSmallLanes];
+  const int wave = threadIdx.x / kWave, wm = wave / 4 * 32, wn = wave % 4 * 32;
   const int l = lane_id() & 31, half = lane_id() >> 5;
   const int j0 = blockIdx.x * C;
+  const int c = wn + l, j = j0 + c;  // this lane's column, and row 4 q of its block
+  const auto row = [&](int q) { return wm + 4 * half + row_of(0, 4 * q); };
   if (a.in == nullptr) {
+    float x[4][4];  // its elements of X, which stay as they are until X'
 #pragma unroll
-    for (int u = 0; u < N * N / 8 / 512; ++u) {
-      const int e = threadIdx.x + u * 512;
-      float v[8] = {};
-#pragma unroll 4
-      for (int s = 0; s < a.grams; ++s) {
-        const float4* p = reinterpret_cast<const float4*>(a.gram + s * kSmallGram + e * 8);
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[q][k] = row(q) + k < a.m && j < a.n
+                      ? a.x[static_cast<int64_t>(row(q) + k) * a.ld + j] : 0.f;
+    constexpr int RUNS = N * N / 8 / kSmallLanes;  // of 8, a lane
+    float v[RUNS][8] = {};
+#pragma unroll 2
+    for (int s = 0; s < a.grams; ++s)
+#pragma unroll
+      for (int u = 0; u < RUNS; ++u) {
+        const float4* p = reinterpret_cast<const float4*>(a.gram + s * kSmallGram +
+                                                          (threadIdx.x + u * kSmallLanes) * 8);
         const float4 q = p[0], r = p[1];
-        v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
-        v[4] += r.x, v[5] += r.y, v[6] += r.z, v[7] += r.w;
+        v[u][0] += q.x, v[u][1] += q.y, v[u][2] += q.z, v[u][3] += q.w;
+        v[u][4] += r.x, v[u][5] += r.y, v[u][6] += r.z, v[u][7] += r.w;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= a.g_factor;
-      put8(g, N, e / (N / 8), e % (N / 8) * 8, v, N * N);
+    for (int u = 0; u < RUNS; ++u) {
+      const int e = threadIdx.x + u * kSmallLanes;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] *= a.g_factor;
+      put8(g, PART, panel_offset(N, e / (N / 8), e % (N / 8) * 8), v[u]);
     }
-    // columns of X: 8 rows a lane, lanes along the columns
 #pragma unroll
-    for (int u = 0; u < C * N / 8 / 512; ++u) {
-      const int e = threadIdx.x + u * 512;
-      const int c = e % C, i = e / C * 8;
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        v[k] = i + k < a.m && j0 + c < a.n
-                   ? a.x[static_cast<int64_t>(i + k) * a.ld + j0 + c] * a.x_factor
-                   : 0.f;
-      put8(xb, C, c, i, v, C * N);
+    for (int q = 0; q < 4; ++q) {
+      const float f[4] = {x[q][0] * a.x_factor, x[q][1] * a.x_factor, x[q][2] * a.x_factor,
+                          x[q][3] * a.x_factor};
+      put4(xb, PART, panel_offset(C, c, row(q)), f);
     }
     __syncthreads();
-    f32x16_t acc[2];
-    const int k16 = (a.m + 15) / 16;
-    small_product<2>(g, N, N * N, wm, g, N, N * N, wn * 64, k16, acc);
+    const f32x16_t square = small_product(g, wm, g, wn, a.m);
+    // G and B are symmetric: a lane's 4 rows are 4 columns of its own row
+    float b[4][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int q = 0; q < 4; ++q) {
+      get4(g, PART, panel_offset(N, c, row(q)), b[q]);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int at = panel_offset(N, wn * 64 + j * 32 + l, wm + 4 * half + row_of(0, r));
-        acc[j][r] = fmaf(a.b_keep, value_of(g, N * N, at), a.b_take * acc[j][r]);
-      }
+      for (int k = 0; k < 4; ++k) b[q][k] = fmaf(a.b_keep, b[q][k], a.b_take * square[4 * q + k]);
+    }
     __syncthreads();
-    // B is symmetric: a lane's 4 rows are 4 columns of its own row
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = panel_offset(N, wn * 64 + j * 32 + l, wm + 4 * half + row_of(0, 4 * q));
-        uint16_t part[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split<kHalves>(acc[j][4 * q + k], part[k]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          *reinterpret_cast<uint2*>(g + p * N * N + at) =
-              make_uint2(part[0][p] | static_cast<uint32_t>(part[1][p]) << 16,
-                         part[2][p] | static_cast<uint32_t>(part[3][p]) << 16);
-      }
+    for (int q = 0; q < 4; ++q) put4(g, PART, panel_offset(N, c, row(q)), b[q]);
     __syncthreads();
-    f32x16_t up[1];
-    small_product<1>(g, N, N * N, wm, xb, C, C * N, wn * 32, k16, up);
-    __syncthreads();  // xb becomes [N][C]
-    const int c = wn * 32 + l, j = j0 + c;
+    const f32x16_t up = small_product(g, wm, xb, wn, a.m);
+    __syncthreads();  // xb becomes X'
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = wm + 4 * half + row_of(0, r);
-      float v = 0.f;
-      if (i < a.m && j < a.n) {
-        float* x = a.x + static_cast<int64_t>(i) * a.ld + j;
-        v = fmaf(a.keep, *x, a.take * up[0][r]);
+    for (int q = 0; q < 4; ++q) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = fmaf(a.keep, x[q][k], a.take * up[4 * q + k]);
+        f[k] = v * a.next_factor;
+        const int i = row(q) + k;
+        if (i >= a.m || j >= a.n) continue;
         if (a.next_gram != nullptr)
-          *x = v;
+          a.x[static_cast<int64_t>(i) * a.ld + j] = v;
         else
           static_cast<E*>(a.out)[a.tall ? static_cast<int64_t>(j) * a.m + i
                                         : static_cast<int64_t>(i) * a.n + j] =
               ElemTraits<E>::from_f32(v * a.scale);
       }
-      if (a.next_gram != nullptr) {
-        uint16_t part[2];
-        split<kHalves>(v * a.next_factor, part);
-        xb[panel_offset(N, i, c)] = part[0];
-        xb[C * N + panel_offset(N, i, c)] = part[1];
-      }
+      if (a.next_gram != nullptr) put4(xb, PART, turned_place(c, row(q)), f);
     }
     if (a.next_gram == nullptr) return;
   } else {
     double t = 0;
-    for (int i = threadIdx.x; i < a.norm_count; i += 512) t += a.norm[i];
+    for (int i = threadIdx.x; i < a.norm_count; i += kSmallLanes) t += a.norm[i];
     sum[threadIdx.x] = t;
     __syncthreads();
-    for (int h = 256; h > 0; h /= 2) {
+    for (int h = kSmallLanes / 2; h > 0; h /= 2) {
       if (static_cast<int>(threadIdx.x) < h) sum[threadIdx.x] += sum[threadIdx.x + h];
       __syncthreads();
     }
     const double inv = 1.0 / (sqrt(sum[0]) + static_cast<double>(a.eps));
-    for (int e = threadIdx.x; e < N * C; e += 512) {
+    for (int e = threadIdx.x; e < N * C; e += kSmallLanes) {
       const int i = a.tall ? e % N : e / C, c = a.tall ? e / N : e % C, j = j0 + c;
       float v = 0.f;
       if (i < a.m && j < a.n) {
@@ -417,23 +444,19 @@ __global__ __launch_bounds__(512) void orth_small_kernel(SmallArgs a) {
         v = static_cast<float>(static_cast<double>(ElemTraits<E>::to_f32(in[at])) * inv);
         a.x[static_cast<int64_t>(i) * a.ld + j] = v;
       }
-      uint16_t part[2];
-      split<kHalves>(v * a.next_factor, part);
-      xb[panel_offset(N, i, c)] = part[0];
-      xb[C * N + panel_offset(N, i, c)] = part[1];
+      uint32_t part[2];
+      split_pair(v * a.next_factor, 0.f, part);
+      xb[turned_place(c, i)] = static_cast<uint16_t>(part[0]);
+      xb[PART + turned_place(c, i)] = static_cast<uint16_t>(part[1]);
     }
   }
   __syncthreads();
-  f32x16_t acc[2];
-  small_product<2>(xb, N, C * N, wm, xb, N, C * N, wn * 64, C / 16, acc);
+  const f32x16_t next = small_turned(xb, wm, wn);
   float* to = a.next_gram + static_cast<int64_t>(blockIdx.x) * kSmallGram;
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<float4*>(to + (wn * 64 + j * 32 + l) * N + wm + 4 * half +
-                                 row_of(0, 4 * q)) =
-          make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<float4*>(to + (wn + l) * N + wm + 4 * half + row_of(0, 4 * q)) =
+        make_float4(next[4 * q], next[4 * q + 1], next[4 * q + 2], next[4 * q + 3]);
 }
 
 // The sum of the workgroups' grams, in 4 streams.
@@ -459,7 +482,6 @@ struct Plan {
   bool small;
   size_t bytes;
 };
-constexpr int kSmallMost = 8192;
 constexpr Form x_form(int elem_bytes) { return elem_bytes == 2 ? kHalf : kHalves; }
 Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   Plan p{};
@@ -469,13 +491,13 @@ Plan plan_of(const OrthArgs& a, int elem_bytes, void* ws) {
   p.ldm = static_cast<int>(up64(p.m));
   p.ldn = static_cast<int>(up64(p.n));
   const int gram = PX == 2 ? 3 : 1, update = PX == 2 ? 3 : 2;  // products
-  p.small = p.m <= kSmallSide && p.n <= kSmallMost;
+  p.small = p.m <= kSmallSide;
   if (p.small) {
     Carve c{static_cast<char*>(ws)};
     p.norm = c.take<double>(kNormBlocks);
     p.sums = c.take<float>(static_cast<size_t>(p.m) * p.ldn);
     // G's sums of the workgroups: two sets taken in turn, or one and their sum in front
-    const size_t groups = p.ldn / kSmallColumns;
+    const size_t groups = blocks(p.n, kSmallColumns);
     p.small_gram =
         c.take<float>((groups <= kSmallSums ? 2 * groups : groups + 1) * size_t{kSmallGram});
     p.bytes = c.used;
@@ -542,7 +564,7 @@ double step_bound(const OrthArgs& p, double top) {
 
 template <typename E>
 hipError_t orthogonalize_small(const OrthArgs& a, const Plan& p, int count, hipStream_t s) {
-  const uint32_t groups = static_cast<uint32_t>(p.ldn / kSmallColumns);
+  const uint32_t groups = static_cast<uint32_t>(blocks(p.n, kSmallColumns));
   const auto factor = [](double v, int e) { return static_cast<float>(std::ldexp(v, e)); };
   double bound = 1.0;
   int ex = exponent_below(bound);
@@ -563,7 +585,7 @@ hipError_t orthogonalize_small(const OrthArgs& a, const Plan& p, int count, hipS
   k.next_gram = sets[0];
   k.out = a.out;
   k.scale = a.scale;
-  orth_small_kernel<E><<<groups, 512, 0, s>>>(k);
+  orth_small_kernel<E><<<groups, kSmallLanes, 0, s>>>(k);
   k.in = nullptr;
   for (int i = 0; i < a.steps; ++i) {
     k.gram = k.next_gram;
@@ -588,7 +610,7 @@ hipError_t orthogonalize_small(const OrthArgs& a, const Plan& p, int count, hipS
     k.take = factor(1, -eb - ex);
     k.next_factor = factor(1, next);
     if (i + 1 == a.steps) k.next_gram = nullptr;
-    orth_small_kernel<E><<<groups, 512, 0, s>>>(k);
+    orth_small_kernel<E><<<groups, kSmallLanes, 0, s>>>(k);
     ex = next;
   }
   return hipGetLastError();
