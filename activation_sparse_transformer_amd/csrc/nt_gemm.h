@@ -334,17 +334,19 @@ __device__ __forceinline__ void mainloop(const Operand& A, int m0, const Operand
   __syncthreads();  // the stages are free for the epilogue
 }
 
-// ---- The same for waves of 64 x 128 (2 x 4 blocks), software-pipelined.  Each 16-wide
-// K step is one asm block: the 8 MFMAs of the fragments in hand with the 6 LDS reads
-// of the next step's fragments between them, and a wait for those reads at its end
-// (no read is in flight when the block ends).  The MFMAs of a stage's last step run
-// behind the next stage's barrier, beside the reads of its first step.  Same products
-// in the same order as mainloop.
+// ---- The same for waves of 64 rows and 128 or 64 columns (2 x 4 or 2 x 2 blocks),
+// software-pipelined.  Each 16-wide K step is one asm block: the MFMAs of the fragments in
+// hand with the LDS reads of the next step's fragments between them, and a wait for those
+// reads at its end (no read is in flight when the block ends).  The MFMAs of a stage's last
+// step run behind the next stage's barrier, beside the reads of its first step.  Same
+// products in the same order as mainloop.
+template <int FN>
 struct Fragments {
-  i32x4_t a[2], b[4];
+  i32x4_t a[2], b[FN];
 };
+template <int FN>
 struct Addresses {  // LDS addresses of the next fragments (turned: of K step 0)
-  uint32_t a[2], b[4];
+  uint32_t a[2], b[FN];
 };
 
 // The reads of fragment `f` (a0, a1, b0 .. b3) at address p##f
@@ -354,25 +356,34 @@ struct Addresses {  // LDS addresses of the next fragments (turned: of K step 0)
   "ds_read_b64_tr_b16 %[h" #f "], %[p" #f "] offset:%[" #hi "]\n\t"
 #define NT_READ_TA(f) NT_READ_TURNED(f, lo_a, hi_a)
 #define NT_READ_TB(f) NT_READ_TURNED(f, lo_b, hi_b)
-#define NT_ACC                                                                                \
-  [c00] "+v"(c[0][0]), [c01] "+v"(c[0][1]), [c02] "+v"(c[0][2]), [c03] "+v"(c[0][3]),         \
-      [c10] "+v"(c[1][0]), [c11] "+v"(c[1][1]), [c12] "+v"(c[1][2]), [c13] "+v"(c[1][3])
+// Operand lists, with 2 and with 4 blocks of columns
+#define NT_ACC2                                                                               \
+  [c00] "+v"(c[0][0]), [c01] "+v"(c[0][1]), [c10] "+v"(c[1][0]), [c11] "+v"(c[1][1])
+#define NT_ACC4                                                                               \
+  NT_ACC2, [c02] "+v"(c[0][2]), [c03] "+v"(c[0][3]), [c12] "+v"(c[1][2]), [c13] "+v"(c[1][3])
 #define NT_OUT_A [na0] "=&v"(nxt.a[0]), [na1] "=&v"(nxt.a[1])
-#define NT_OUT_B                                                                              \
-  [nb0] "=&v"(nxt.b[0]), [nb1] "=&v"(nxt.b[1]), [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])
+#define NT_OUT_B2 [nb0] "=&v"(nxt.b[0]), [nb1] "=&v"(nxt.b[1])
+#define NT_OUT_B4 NT_OUT_B2, [nb2] "=&v"(nxt.b[2]), [nb3] "=&v"(nxt.b[3])
 #define NT_OUT_TA [na0] "=&v"(la[0]), [ha0] "=&v"(ha[0]), [na1] "=&v"(la[1]), [ha1] "=&v"(ha[1])
-#define NT_OUT_TB                                                                             \
-  [nb0] "=&v"(lb[0]), [hb0] "=&v"(hb[0]), [nb1] "=&v"(lb[1]), [hb1] "=&v"(hb[1]),             \
-      [nb2] "=&v"(lb[2]), [hb2] "=&v"(hb[2]), [nb3] "=&v"(lb[3]), [hb3] "=&v"(hb[3])
-#define NT_CUR                                                                                \
-  [a0] "v"(cur.a[0]), [a1] "v"(cur.a[1]), [b0] "v"(cur.b[0]), [b1] "v"(cur.b[1]),             \
-      [b2] "v"(cur.b[2]), [b3] "v"(cur.b[3])
-#define NT_AT                                                                                 \
+#define NT_OUT_TB2 [nb0] "=&v"(lb[0]), [hb0] "=&v"(hb[0]), [nb1] "=&v"(lb[1]), [hb1] "=&v"(hb[1])
+#define NT_OUT_TB4                                                                            \
+  NT_OUT_TB2, [nb2] "=&v"(lb[2]), [hb2] "=&v"(hb[2]), [nb3] "=&v"(lb[3]), [hb3] "=&v"(hb[3])
+#define NT_CUR2 [a0] "v"(cur.a[0]), [a1] "v"(cur.a[1]), [b0] "v"(cur.b[0]), [b1] "v"(cur.b[1])
+#define NT_CUR4 NT_CUR2, [b2] "v"(cur.b[2]), [b3] "v"(cur.b[3])
+#define NT_AT2                                                                                \
   [pa0] "v"(at.a[0]), [pa1] "v"(at.a[1]), [pb0] "v"(at.b[0]), [pb1] "v"(at.b[1]),             \
-      [pb2] "v"(at.b[2]), [pb3] "v"(at.b[3]), [lo_a] "n"(32 * KS * CF::BM),                   \
-      [hi_a] "n"(32 * KS * CF::BM + 8 * CF::BM), [lo_b] "n"(32 * KS * CF::BN),                \
-      [hi_b] "n"(32 * KS * CF::BN + 8 * CF::BN)
-#define NT_STEP(MFMA, RA, RB, OUT_A, OUT_B)                                                   \
+      [lo_a] "n"(32 * KS * CF::BM), [hi_a] "n"(32 * KS * CF::BM + 8 * CF::BM),                \
+      [lo_b] "n"(32 * KS * CF::BN), [hi_b] "n"(32 * KS * CF::BN + 8 * CF::BN)
+#define NT_AT4 NT_AT2, [pb2] "v"(at.b[2]), [pb3] "v"(at.b[3])
+#define NT_STEP2(MFMA, RA, RB, OUT_A, OUT_B)                                                  \
+  asm volatile(RA(a0) MFMA " %[c00], %[a0], %[b0], %[c00]\n\t" RA(a1) MFMA                    \
+               " %[c01], %[a0], %[b1], %[c01]\n\t" RB(b0) MFMA                                \
+               " %[c10], %[a1], %[b0], %[c10]\n\t" RB(b1) MFMA                                \
+               " %[c11], %[a1], %[b1], %[c11]\n\ts_waitcnt lgkmcnt(0)\n\t"                    \
+               : NT_ACC2, OUT_A, OUT_B##2                                                     \
+               : NT_CUR2, NT_AT2                                                              \
+               : "memory")
+#define NT_STEP4(MFMA, RA, RB, OUT_A, OUT_B)                                                  \
   asm volatile(RA(a0) MFMA " %[c00], %[a0], %[b0], %[c00]\n\t" RA(a1) MFMA                    \
                " %[c01], %[a0], %[b1], %[c01]\n\t" RB(b0) MFMA                                \
                " %[c02], %[a0], %[b2], %[c02]\n\t" RB(b1) MFMA                                \
@@ -380,37 +391,40 @@ struct Addresses {  // LDS addresses of the next fragments (turned: of K step 0)
                " %[c10], %[a1], %[b0], %[c10]\n\t" RB(b3) MFMA                                \
                " %[c11], %[a1], %[b1], %[c11]\n\t" MFMA " %[c12], %[a1], %[b2], %[c12]\n\t"   \
                MFMA " %[c13], %[a1], %[b3], %[c13]\n\ts_waitcnt lgkmcnt(0)\n\t"               \
-               : NT_ACC, OUT_A, OUT_B                                                         \
-               : NT_CUR, NT_AT                                                                \
+               : NT_ACC4, OUT_A, OUT_B##4                                                     \
+               : NT_CUR4, NT_AT4                                                              \
                : "memory")
-#define NT_LOAD(RA, RB, OUT_A, OUT_B)                                                         \
+#define NT_LOAD2(RA, RB, OUT_A, OUT_B)                                                        \
+  asm volatile(RA(a0) RA(a1) RB(b0) RB(b1) "s_waitcnt lgkmcnt(0)\n\t"                         \
+               : OUT_A, OUT_B##2                                                              \
+               : NT_AT2                                                                       \
+               : "memory")
+#define NT_LOAD4(RA, RB, OUT_A, OUT_B)                                                        \
   asm volatile(RA(a0) RA(a1) RB(b0) RB(b1) RB(b2) RB(b3) "s_waitcnt lgkmcnt(0)\n\t"           \
-               : OUT_A, OUT_B                                                                 \
-               : NT_AT                                                                        \
+               : OUT_A, OUT_B##4                                                              \
+               : NT_AT4                                                                       \
                : "memory")
+#define NT_FORMS(DO, ...)                                                                     \
+  if constexpr (TA && TB) DO(__VA_ARGS__ NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);       \
+  else if constexpr (TA) DO(__VA_ARGS__ NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);            \
+  else DO(__VA_ARGS__ NT_READ, NT_READ, NT_OUT_A, NT_OUT_B)
+#define NT_BF16 "v_mfma_f32_32x32x16_bf16"
+#define NT_F16 "v_mfma_f32_32x32x16_f16"
 
 // The MFMAs of cur beside the reads of nxt, K step KS of its stage.  First: the reads alone.
 template <class CF, Form F, bool TA, bool TB, int KS, bool FIRST = false>
-__device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][4], const Fragments& cur,
-                                          Fragments& nxt, const Addresses& at) {
+__device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][CF::FN], const Fragments<CF::FN>& cur,
+                                          Fragments<CF::FN>& nxt, const Addresses<CF::FN>& at) {
   static_assert(TA || !TB, "no product turns its columns alone");
-  i32x2_t la[2], ha[2], lb[4], hb[4];
-  if constexpr (FIRST) {
-    if constexpr (TA && TB) NT_LOAD(NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
-    else if constexpr (TA) NT_LOAD(NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
-    else NT_LOAD(NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
-  } else if constexpr (is_bf16(F)) {
-#define NT_MFMA "v_mfma_f32_32x32x16_bf16"
-    if constexpr (TA && TB) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
-    else if constexpr (TA) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
-    else NT_STEP(NT_MFMA, NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
-#undef NT_MFMA
+  i32x2_t la[2], ha[2], lb[CF::FN], hb[CF::FN];
+  if constexpr (CF::FN == 4) {
+    if constexpr (FIRST) { NT_FORMS(NT_LOAD4); }
+    else if constexpr (is_bf16(F)) { NT_FORMS(NT_STEP4, NT_BF16,); }
+    else { NT_FORMS(NT_STEP4, NT_F16,); }
   } else {
-#define NT_MFMA "v_mfma_f32_32x32x16_f16"
-    if constexpr (TA && TB) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ_TB, NT_OUT_TA, NT_OUT_TB);
-    else if constexpr (TA) NT_STEP(NT_MFMA, NT_READ_TA, NT_READ, NT_OUT_TA, NT_OUT_B);
-    else NT_STEP(NT_MFMA, NT_READ, NT_READ, NT_OUT_A, NT_OUT_B);
-#undef NT_MFMA
+    if constexpr (FIRST) { NT_FORMS(NT_LOAD2); }
+    else if constexpr (is_bf16(F)) { NT_FORMS(NT_STEP2, NT_BF16,); }
+    else { NT_FORMS(NT_STEP2, NT_F16,); }
   }
   if constexpr (TA) {
 #pragma unroll
@@ -418,40 +432,52 @@ __device__ __forceinline__ void pipe_step(f32x16_t (&c)[2][4], const Fragments& 
   }
   if constexpr (TB) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) nxt.b[j] = joined(lb[j], hb[j]);
+    for (int j = 0; j < CF::FN; ++j) nxt.b[j] = joined(lb[j], hb[j]);
   }
 }
 #undef NT_READ
 #undef NT_READ_TURNED
 #undef NT_READ_TA
 #undef NT_READ_TB
-#undef NT_ACC
+#undef NT_ACC2
+#undef NT_ACC4
 #undef NT_OUT_A
-#undef NT_OUT_B
+#undef NT_OUT_B2
+#undef NT_OUT_B4
 #undef NT_OUT_TA
-#undef NT_OUT_TB
-#undef NT_CUR
-#undef NT_AT
-#undef NT_STEP
-#undef NT_LOAD
+#undef NT_OUT_TB2
+#undef NT_OUT_TB4
+#undef NT_CUR2
+#undef NT_CUR4
+#undef NT_AT2
+#undef NT_AT4
+#undef NT_STEP2
+#undef NT_STEP4
+#undef NT_LOAD2
+#undef NT_LOAD4
+#undef NT_FORMS
+#undef NT_BF16
+#undef NT_F16
 
 // VALU writes of the accumulators before MFMAs in asm, and MFMA results before VALU
 // reads: the accumulators are operands, so neither moves across the wait.
-__device__ __forceinline__ void settle(f32x16_t (&c)[2][4]) {
-  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"
-               : "+v"(c[0][0]), "+v"(c[0][1]), "+v"(c[0][2]), "+v"(c[0][3]), "+v"(c[1][0]),
-                 "+v"(c[1][1]), "+v"(c[1][2]), "+v"(c[1][3]));
+template <int FN>
+__device__ __forceinline__ void settle(f32x16_t (&c)[2][FN]) {
+#pragma unroll
+  for (int j = 0; j < FN; j += 2)
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15"
+                 : "+v"(c[0][j]), "+v"(c[0][j + 1]), "+v"(c[1][j]), "+v"(c[1][j + 1]));
 }
 
 template <class CF, Form F, bool TA, bool TB>
 __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Operand& B, int n0,
                                               int k0, int ksteps, uint16_t* lds,
-                                              f32x16_t (&acc)[2][4]) {
-  static_assert(CF::FM == 2 && CF::FN == 4 && CF::STAGES == 2, "2 x 4 blocks of 32x32 per wave");
+                                              f32x16_t (&acc)[2][CF::FN]) {
+  static_assert(CF::FM == 2 && (CF::FN == 4 || CF::FN == 2) && CF::STAGES == 2, "a wave's blocks");
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < CF::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int steps = ksteps * products_of(F);
@@ -462,7 +488,7 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   const int wave = threadIdx.x / kWave;
   const int ra = wave / CF::WAVES_N * CF::WTM, rb = wave % CF::WAVES_N * CF::WTN;
   const uint32_t base_a = lds_address(lds), base_b = base_a + 2 * CF::BM * kStep;
-  Addresses first[4];  // in stage 0, of each K step (turned: the same)
+  Addresses<CF::FN> first[4];  // in stage 0, of each K step (turned: the same)
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
@@ -470,7 +496,7 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
       first[ks].a[i] =
           base_a + (TA ? turned_at<CF::BM>(ra + 32 * i) : straight_at(ra + 32 * i, ks));
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < CF::FN; ++j)
       first[ks].b[j] =
           base_b + (TB ? turned_at<CF::BN>(rb + 32 * j) : straight_at(rb + 32 * j, ks));
   }
@@ -481,7 +507,7 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
     b_copies.issue(walk.k, walk.b(), to + CF::BM * kStep);
     walk.next();
   };
-  Fragments f0, f1;
+  Fragments<CF::FN> f0, f1;
   copy(0);
   meet<0>();
   if (steps > 1) copy(1);
@@ -493,13 +519,13 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
     meet<0>();
     if (s + 1 < steps) copy((s + 1) & 1);
     const uint32_t shift = static_cast<uint32_t>(s & 1) * (CF::STAGE * 2);
-    Addresses at[4];
+    Addresses<CF::FN> at[4];
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) at[ks].a[i] = first[ks].a[i] + shift;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) at[ks].b[j] = first[ks].b[j] + shift;
+      for (int j = 0; j < CF::FN; ++j) at[ks].b[j] = first[ks].b[j] + shift;
     }
     pipe_step<CF, F, TA, TB, 0>(acc, f1, f0, at[0]);
     pipe_step<CF, F, TA, TB, 1>(acc, f0, f1, at[1]);
@@ -510,7 +536,7 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = mfma<F>(f1.a[i], f1.b[j], acc[i][j]);
+    for (int j = 0; j < CF::FN; ++j) acc[i][j] = mfma<F>(f1.a[i], f1.b[j], acc[i][j]);
   __syncthreads();  // the stages are free for the epilogue
 }
 
@@ -667,7 +693,7 @@ __device__ __forceinline__ void multiply(const Operand& A, int m0, const Operand
                                          f32x16_t (&acc)[CF::FM][CF::FN]) {
   if constexpr (F == kRaw)
     mainloop_raw<CF, TA>(A, m0, B, n0, k0, ksteps, lds, acc);
-  else if constexpr (CF::FM == 2 && CF::FN == 4)
+  else if constexpr (CF::FM == 2)
     mainloop_pipe<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
   else
     mainloop<CF, F, TA, TB>(A, m0, B, n0, k0, ksteps, lds, acc);
@@ -794,8 +820,10 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
                                                          int pitch, Store store) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[CF::STAGES * CF::STAGE + extra_lds<CF, F>()];
   int mb, nb;
-  const int slices = gridDim.y, slice = blockIdx.y;
-  const int t = run_of(blockIdx.x, gridDim.x);
+  const int slices = gridDim.y, tiles = gridDim.x;
+  // an XCD's run lies in one slice, or a few: its share of K stays in its L2
+  const int place = run_of(blockIdx.y * tiles + blockIdx.x, slices * tiles);
+  const int slice = place / tiles, t = place - slice * tiles;
   if (n_blocks == 0) triangle_of(t, mb, nb);
   else tile_of(t, m_blocks, n_blocks, mb, nb);
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * ksteps / slices);
