@@ -21,6 +21,7 @@
 // Both products read w, x and dl as they lie, turning fragments with LDS transpose
 // reads where K runs along a column.
 #include <algorithm>
+#include <numeric>
 #include <type_traits>
 
 #include "nt_gemm.h"
@@ -737,13 +738,34 @@ __global__ __launch_bounds__(256) void head_zero_kernel(uint4* p, int64_t count)
 }
 
 // ---------------------------------------------------------------- sizes
-// Columns of the vocabulary taken at a time: all where the forward pass reads w in
-// place, else as many as keep what is made per column within `budget`, in equal
-// pieces.
-int piece_of(int vocab, size_t per_column, size_t budget) {
-  const int64_t most = std::max<int64_t>(budget / per_column / 256 * 256, 1024);
+// Columns of the vocabulary taken at a time: all where the forward pass reads w in place,
+// else as many as keep what is made per column within `budget`, in equal pieces.
+int64_t most_of(size_t per_column, size_t budget) {
+  return std::max<int64_t>(budget / per_column / 256 * 256, 1024);
+}
+int equal_pieces(int vocab, int64_t most) {
   const int64_t pieces = blocks(vocab, static_cast<int>(std::min<int64_t>(most, vocab)));
   return static_cast<int>(std::min<int64_t>(blocks(blocks(vocab, static_cast<int>(pieces)), 256) * 256, vocab));
+}
+int piece_of(int vocab, size_t per_column, size_t budget) {
+  return equal_pieces(vocab, most_of(per_column, budget));
+}
+// The same, or, if us(columns) promises less for it, the most columns of which 256 x 256
+// tiles of n rows fill the CUs without a rest, and a smaller last piece (2001 x 1000 x 49999
+// float32: 734 us forward with pieces of 32768, 793 with two of 25088; gradient 2145 with
+// pieces of 16384, 2216 with four of 12544).
+template <class Us>
+int piece_of(int vocab, size_t per_column, size_t budget, int64_t n, const Us& us) {
+  const int64_t most = most_of(per_column, budget);
+  const int equal = equal_pieces(vocab, most);
+  const int64_t unit = 65536 / std::gcd(blocks(n, 256), int64_t{256});
+  if (equal >= vocab || most < unit) return equal;
+  const int filled = static_cast<int>(most / unit * unit);
+  const auto all = [&](int piece) {
+    const int rest = vocab % piece;
+    return vocab / piece * us(piece) + (rest > 0 ? us(rest) : 0.0);
+  };
+  return all(filled) < all(equal) ? filled : equal;
 }
 
 constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
@@ -806,8 +828,12 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   const Form f = form_of(elem_bytes, a.n_rows);
   const size_t ld = up64(a.d), part_bytes = 2 * parts_of(f) * ld;
   // pieces but the last are whole tiles
-  p.piece = f == kHalves ? piece_of(a.vocab, part_bytes, size_t{128} << 20) : a.vocab;
-  p.tile = wide_cut(p.piece, a.n_rows, stages(f, a.d) * products_of(f), 1, false, true).tile;
+  const int steps = stages(f, a.d) * products_of(f);
+  const auto cut = [&](int columns) { return wide_cut(columns, a.n_rows, steps, 1, false, true); };
+  p.piece = f == kHalves ? piece_of(a.vocab, part_bytes, size_t{128} << 20, a.n_rows,
+                                    [&](int columns) { return cut(columns).us; })
+                         : a.vocab;
+  p.tile = cut(p.piece).tile;
   p.tiles = static_cast<int>(blocks(a.vocab, tile_rows(p.tile)));
   Carve c{static_cast<char*>(ws)};
   p.parts = c.take<float2>(static_cast<size_t>(p.tiles) * a.n_rows);
@@ -822,9 +848,19 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   return p;
 }
 
+// The cuts of the gradient's products over a piece of the vocabulary.
+Cut dl_cut(const HeadArgs& a, Form f, int columns) {
+  return wide_cut(columns, a.n_rows, stages(f, a.d) * products_of(f), 1, false, true);
+}
+Cut dw_cut(const HeadArgs& a, Form f, int columns) {
+  return wide_cut(a.d, columns, stages(f, a.n_rows) * products_of(f), 1, false, true);
+}
+Cut dx_cut(const HeadArgs& a, Form f, int columns) {  // K is the piece: in slices
+  return wide_cut(a.d, a.n_rows, stages(f, up64(columns)) * products_of(f), 32, false, false);
+}
+
 struct BackwardPlan {
   int piece;
-  Tile dl_tile;
   Cut dx_cut;
   uint16_t *xp, *wp, *gx, *dl;
   float *amax, *undo, *sums;
@@ -834,11 +870,13 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   BackwardPlan p{};
   const Form f = form_of(elem_bytes, a.n_rows);
   const size_t P = parts_of(f), ld = up64(a.d), n = a.n_rows;
-  p.piece = piece_of(a.vocab, 2 * P * n + (f == kHalves ? 2 * P * ld : 0), size_t{192} << 20);
+  p.piece = piece_of(a.vocab, 2 * P * n + (f == kHalves ? 2 * P * ld : 0), size_t{192} << 20, n,
+                     [&](int columns) {
+                       return dl_cut(a, f, columns).us + dw_cut(a, f, columns).us +
+                              dx_cut(a, f, columns).us;
+                     });
   const size_t ldv = up64(p.piece);
-  p.dl_tile = wide_cut(p.piece, n, stages(f, a.d) * products_of(f), 1, false, true).tile;
-  // dx: K is a piece of the vocabulary; split until the tiles fill the CUs
-  p.dx_cut = wide_cut(a.d, n, stages(f, ldv) * products_of(f), 32, false, false);
+  p.dx_cut = dx_cut(a, f, p.piece);
   Carve c{static_cast<char*>(ws)};
   p.gx = c.take<uint16_t>(P * n * a.d);
   p.dl = c.take<uint16_t>(P * n * ldv);
@@ -937,7 +975,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
     const DlArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, amax_w, p.undo,
                    a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
                    ldv};
-    hipError_t e = with_wide_tile(p.dl_tile, [&](auto cf) {
+    hipError_t e = with_wide_tile(dl_cut(a, F, rows).tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(rows, CF::BM)), nb = static_cast<int>(blocks(n, CF::BN));
       head_dl_kernel<CF, F><<<static_cast<uint32_t>(mb) * nb, CF::NT, 0, s>>>(k, mb, nb);
@@ -958,8 +996,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    const Cut dw_cut = wide_cut(a.d, rows, stages(F, n) * products_of(F), 1, false, true);
-    e = with_wide_tile(dw_cut.tile, [&](auto cf) {
+    e = with_wide_tile(dw_cut(a, F, rows).tile, [&](auto cf) {
       typedef decltype(cf) CF;
       const int mb = static_cast<int>(blocks(a.d, CF::BM));
       const int nb = static_cast<int>(blocks(rows, CF::BN));

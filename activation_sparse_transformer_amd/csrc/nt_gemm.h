@@ -897,13 +897,14 @@ inline int tile_cols(Tile t) { return t == kBig ? 256 : t == kMid ? 128 : t == k
 struct Cut {
   Tile tile;
   int slices;
+  double us;  // what it should take (wide_cut)
 };
 // At most kFewColumns columns: the narrowest tile, and slices until four workgroups a CU
 // are there (two run at a time), of at least 4 stages.
 inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int64_t most_slices) {
   const Tile t = cols <= 32 ? kBare : kFew;
   const int64_t most = std::clamp<int64_t>(steps / 4, 1, most_slices);
-  return {t, static_cast<int>(std::clamp<int64_t>(1024 / blocks(rows, tile_rows(t)), 1, most))};
+  return {t, static_cast<int>(std::clamp<int64_t>(1024 / blocks(rows, tile_rows(t)), 1, most)), 0};
 }
 // Else the cheaper of 256 x 256 tiles (one workgroup a CU, 2.1 us a stage, 6 us to fill and
 // to store) and 128 x 128 ones (one a CU 0.78 us a stage, two 1.25, 4 us), with as many
@@ -911,8 +912,7 @@ inline Cut few_cut(int64_t rows, int64_t cols, int64_t steps, int64_t most_slice
 // writes none.
 inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, bool triangle,
                     bool whole) {
-  Cut best{kMid, 1};
-  double least = 1e300;
+  Cut best{kMid, 1, 1e300};
   for (const Tile t : {kBig, kMid}) {
     const int64_t mb = blocks(rows, tile_rows(t)), nb = blocks(cols, tile_cols(t));
     const int64_t tiles = triangle ? mb * (mb + 1) / 2 : mb * nb;
@@ -924,10 +924,7 @@ inline Cut wide_cut(int64_t rows, int64_t cols, int64_t steps, int most_slices, 
       else if (groups <= 256) us = each * 0.78 + 4;
       else us = blocks(groups, 512) * (each * 1.25 + 4);
       if (s > 1 || !whole) us += static_cast<double>(s) * tiles * tile_rows(t) * tile_cols(t) * 8 / 5e6;
-      if (us < least) {
-        least = us;
-        best = {t, s};
-      }
+      if (us < best.us) best = {t, s, us};
       if (groups > 1024) break;
     }
   }
