@@ -114,9 +114,9 @@ struct Copies<SIZE, NW, false> {  // 8 rows of 64 elements each
 };
 
 // A turned operand's stage: 64 lines (k) of SIZE elements, the 32-byte chunk c of line k
-// at position c ^ turned_swizzle(k): the 4 lines x 32 bytes that 16 lanes of a transpose
-// read take fall on distinct banks.
-__device__ __forceinline__ int turned_swizzle(int k) { return (k & 3) ^ ((k >> 1) & 4); }
+// at position c ^ turned_swizzle(k): the 4 lines x 64 bytes that 32 lanes of a transpose
+// read take fall on distinct ones of the 64 banks.
+__device__ __forceinline__ int turned_swizzle(int k) { return (k & 3) << 1 | (k >> 3 & 1); }
 template <int SIZE>
 __device__ __forceinline__ int turned_offset(int k, int r) {
   return k * SIZE + ((((r >> 4) ^ turned_swizzle(k)) & (SIZE / 16 - 1)) << 4) + (r & 15);

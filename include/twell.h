@@ -620,14 +620,14 @@ int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
  *    [0, vocab) is ignored: its logp is 0, and its row of x has no gradient and
  *    adds to none, whatever that row holds.  targets and the arrays per row are
  *    aligned to their elements only.
- *  - z is a float32 sum; maxima, sums and probabilities are float32.  It is never
- *    stored: the gradient forms it again.  float32 x and w enter the products with 22
- *    bits and more, elements under 2^-18 of the largest of their row of x, or of w, with
- *    an error of 2^-40 of that largest instead.
+ *  - z is a float32 sum; maxima, sums and probabilities are float32.  The gradient
+ *    forms z again.  float32 x and w enter the products with 24 bits for up to 64
+ *    rows; for more with 22 bits and more, elements under 2^-18 of the largest of their
+ *    row of x, or of w, with an error of 2^-40 of that largest instead.
  *  - A row with a NaN, or an infinity that meets its product, has NaN results; a
  *    float32 infinity in x or w makes every z of its row or column infinite or NaN.
  *    z = -inf has probability 0; a row with nothing else has lse = logp = -inf and a
- *    zero gradient.
+ *    zero gradient of its z (an infinity in w or x meets that zero as NaN in dx or dw).
  * Requirements: n_rows >= 0; vocab > 0; d_model > 0 and a multiple of 8; dtype a
  * twell_dtype; scale positive and finite; reserved 0.  Limits, else
  * TWELL_ERR_UNSUPPORTED: n_rows and vocab at most 2^24, d_model at most 2^16,
@@ -644,8 +644,9 @@ typedef struct twell_head_shape {
 } twell_head_shape;
 
 /* Bytes of device workspace twell_head_logprob_forward needs (0 for an invalid
- * shape and for no rows): a maximum and a sum per row and 128 or 256 columns; in
- * float32, or where d_model is no multiple of 64, parts of x and of a piece of w. */
+ * shape and for no rows): a maximum and a sum per row and 128 columns or more; for up
+ * to 64 rows z of a piece of the vocabulary, in slices of d_model (under 100 MB);
+ * for more float32 ones parts of x and of a piece of w (128 MB). */
 size_t twell_head_logprob_workspace_size(const twell_head_shape* shape);
 
 /* logp and lse [n_rows] float32, and stats [n_rows][2] float32 (8-byte aligned):
@@ -655,16 +656,19 @@ int twell_head_logprob_forward(const twell_head_shape* shape, const void* x, con
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace twell_head_logprob_backward needs (0 for an invalid
- * shape and for no rows): the gradient of a piece of the vocabulary's logits and
- * transposed operands, about 200 MB beside float32 sums of dx. */
+ * shape and for no rows): the gradient of a piece of the vocabulary's logits, about
+ * 200 MB with parts of float32 w (at least 1024 columns), beside float32 sums of dx
+ * in up to 32 slices of the vocabulary (128 with up to 64 rows), a copy of x and its
+ * parts. */
 size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape);
 
 /* The gradients of sum_n dlogp[n] logp[n] from the forward's stats:
  *   dl = scale * dlogp (1[v = target] - exp(z_v) / sum exp z);  dx = dl w,  dw = dl^T x
  * dx [n_rows][d_model] and dw [vocab][d_model] in dtype, written, not added to; sums
- * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w) or
- * with 22 bits and more (float32; dl / dlogp and scale * dlogp * x within 2^-40 of
- * their largest).  n_rows == 0 writes a zero dw. */
+ * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w; as two
+ * bfloat16 parts with up to 64 rows) or, of float32 ones, with 22 bits and more (dl /
+ * dlogp and scale * dlogp * x within 2^-40 of their largest; up to 64 rows: 24
+ * bits).  n_rows == 0 writes a zero dw. */
 int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, const void* w,
                                 const void* targets, const float* stats, const float* dlogp,
                                 void* dx, void* dw, void* workspace, size_t workspace_bytes,
@@ -678,10 +682,11 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
  * which replaces every singular value s of X by a polynomial's iterate: towards 1
  * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
  *  - Sums are float32; X, G and B enter the products with 22 bits and more, elements
- *    far below the matrix's bound with an error of 2^-40 of it.  A bfloat16 M's X is
- *    rounded to 11 bits after each step, an eighth of M's own rounding.  |M|_F is summed
- *    in double.
- *  - M = 0 gives 0; an infinity or NaN in M gives NaN.
+ *    far below the matrix's bound with an error of 2^-40 of it.  With the smaller side
+ *    past 128, a bfloat16 M's X enters X X^T and B X with 11 bits, an eighth of M's own
+ *    rounding.  |M|_F is summed in double.
+ *  - M = 0 gives 0; an infinity or NaN in M gives NaN.  Coefficients under which X, G or B
+ *    may pass 2^100 may give infinities and NaN.
  * Requirements: rows, cols > 0; dtype a twell_dtype (of m and out); 1 <= steps <=
  * TWELL_ORTH_MAX_STEPS; a, b, c and scale finite; eps positive and finite.  Limits,
  * else TWELL_ERR_UNSUPPORTED: rows and cols at most 2^20, the smaller at most 2^16,
@@ -698,7 +703,8 @@ typedef struct twell_orth_shape {
 } twell_orth_shape;
 
 /* Bytes of device workspace twell_orthogonalize needs (0 for an invalid shape): X's
- * parts in both orders, G's and B's, and float32 products. */
+ * parts before and after a step, G's and B's, and float32 products; with the smaller
+ * side up to 128 a float32 X and a float32 G per 128 columns of the longer. */
 size_t twell_orthogonalize_workspace_size(const twell_orth_shape* shape);
 
 /* out [rows][cols] = the orthogonalised m [rows][cols]; out may be m. */
