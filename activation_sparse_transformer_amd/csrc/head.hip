@@ -353,11 +353,10 @@ __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict
 }
 
 // ---------------------------------------------------------------- few rows
-// At most 64: reading w bounds them.  16 x 4096 x 131072 bf16 194 us, of which the product
-// 183 (5.9 TB/s; a plain read reaches 6.9), the statistics of z from the workspace 6 and
-// joining 5.  64 x 128 x 1000 float32 gradient: 31 us, five launches of which none fills the
-// card.  With 65 rows the tiles of many rows are as fast: 1024 x 32768 bf16 28 us and 77 for
-// the gradient.
+// At most 64 (few_rows): reading w bounds them.  16 x 4096 x 131072 bf16 194 us, of which the
+// product 183 (5.9 TB/s; a plain read reaches 6.9), the statistics of z from the workspace 6
+// and joining 5.  64 x 128 x 1000 float32 gradient: 31 us, five launches of which none fills
+// the card.
 // z of 4 columns from v: the slices' sums in their order, times scale.
 struct FewZ {
   const float* sums;  // [slices][n_rows][pitch]
@@ -783,6 +782,17 @@ int piece_of(int vocab, size_t per_column, size_t budget, int64_t n, const Us& u
 
 constexpr int kAmax = 2;  // largest magnitudes: of w, of scale * dlogp * x
 
+// Whether the kernels of few rows take a call.  float32: where w's parts cost more than the
+// products (64 x 1024 x 32768: 53 us forward and 178 for the gradient, 135 and 252 with the
+// kernels of many rows).  bfloat16, whose operands lie ready: forward 16 x 4096 x 131072 195 us
+// and 202, 33 x 1024 x 32768 28 and 27, 64 31 and 28; gradient 16 x 512 x 8000 25 and 31, 16 x
+// 1024 x 32768 57 and 65, 16 x 2048 x 50001 195 and 170, 32 x 1024 x 32768 71 and 68.
+bool few_rows(const HeadArgs& a, int elem_bytes, bool backward) {
+  if (elem_bytes == 4) return a.n_rows <= kFewColumns;
+  if (!backward) return a.n_rows <= 32;
+  return a.n_rows <= 16 && static_cast<int64_t>(a.vocab) * a.d <= 1 << 25;
+}
+
 // The form of the operands; and the stages of a product over k.
 Form form_of(int elem_bytes, int64_t n) {
   return elem_bytes == 2 ? kBf16 : n <= kFewColumns ? kRaw : kHalves;
@@ -1028,7 +1038,7 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
 template <Form F, class Call>
 hipError_t with_form_tile(Tile t, const Call& f) {
   if constexpr (F == kRaw) return with_raw_tile(t, f);
-  else return with_few_tile(t, f);
+  else return f(Bare());  // at most 32 rows
 }
 
 // Few rows: z = x w^T of a piece, in slices of K.
@@ -1118,19 +1128,19 @@ hipError_t few_backward(const HeadArgs& a, const float* stats, const float* dlog
 
 size_t head_forward_bytes(const HeadArgs& a, int elem_bytes) {
   if (a.n_rows == 0) return 0;
-  return a.n_rows <= kFewColumns ? few_plan(a, elem_bytes, false, nullptr).bytes
-                                 : forward_plan(a, elem_bytes, nullptr).bytes;
+  return few_rows(a, elem_bytes, false) ? few_plan(a, elem_bytes, false, nullptr).bytes
+                                        : forward_plan(a, elem_bytes, nullptr).bytes;
 }
 size_t head_backward_bytes(const HeadArgs& a, int elem_bytes) {
   if (a.n_rows == 0) return 0;
-  return a.n_rows <= kFewColumns ? few_plan(a, elem_bytes, true, nullptr).bytes
-                                 : backward_plan(a, elem_bytes, nullptr).bytes;
+  return few_rows(a, elem_bytes, true) ? few_plan(a, elem_bytes, true, nullptr).bytes
+                                       : backward_plan(a, elem_bytes, nullptr).bytes;
 }
 
 hipError_t launch_head_forward(const HeadArgs& a, int elem_bytes, void* ws, float* logp,
                                float* lse, float* stats, hipStream_t s) {
   if (a.n_rows == 0) return hipSuccess;
-  const bool few = a.n_rows <= kFewColumns;
+  const bool few = few_rows(a, elem_bytes, false);
   switch (form_of(elem_bytes, a.n_rows)) {
     case kRaw: return few_forward<kRaw>(a, ws, logp, lse, stats, s);
     case kHalves: return forward<kHalves>(a, ws, logp, lse, stats, s);
@@ -1148,7 +1158,7 @@ hipError_t launch_head_backward(const HeadArgs& a, int elem_bytes, const float* 
                        0, s>>>(static_cast<uint4*>(dw), count);
     return hipGetLastError();
   }
-  const bool few = a.n_rows <= kFewColumns;
+  const bool few = few_rows(a, elem_bytes, true);
   switch (form_of(elem_bytes, a.n_rows)) {
     case kRaw: return few_backward<kRaw>(a, stats, dlogp, ws, dx, dw, s);
     case kHalves: return backward<kHalves>(a, stats, dlogp, ws, dx, dw, s);

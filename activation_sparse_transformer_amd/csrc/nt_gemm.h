@@ -866,8 +866,7 @@ __global__ __launch_bounds__(CF::NT) void product_kernel(Operand A, Operand B, i
 // ---------------------------------------------------------------- host side
 typedef Config<256, 256, 4, 2, 2> Big;
 typedef Config<128, 128, 2, 2, 2> Mid;
-typedef Config<128, 64, 4, 1, 3> Few;   // at most 64 columns
-typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32
+typedef Config<128, 32, 4, 1, 4> Bare;  // at most 32 columns
 // kRaw: two workgroups (with 64 columns) or three a CU, which is worth more than a
 // third stage (9005 x 2376 by 39: 31 us, 42 with one workgroup of three stages)
 typedef Config<128, 64, 4, 1, 2> RawFew;
@@ -878,10 +877,6 @@ inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 inline int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
 
 enum Tile { kBare, kFew, kMid, kBig };
-template <class Call>
-hipError_t with_few_tile(Tile t, const Call& f) {
-  return t == kBare ? f(Bare()) : f(Few());
-}
 template <class Call>
 hipError_t with_raw_tile(Tile t, const Call& f) {
   return t == kBare ? f(RawBare()) : f(RawFew());

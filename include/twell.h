@@ -644,9 +644,9 @@ typedef struct twell_head_shape {
 } twell_head_shape;
 
 /* Bytes of device workspace twell_head_logprob_forward needs (0 for an invalid
- * shape and for no rows): a maximum and a sum per row and 128 columns or more; for up
- * to 64 rows z of a piece of the vocabulary, in slices of d_model (under 100 MB);
- * for more float32 ones parts of x and of a piece of w (128 MB). */
+ * shape and for no rows): a maximum and a sum per row and 128 columns or more; for few
+ * rows (float32 up to 64, bfloat16 up to 32) z of a piece of the vocabulary, in slices
+ * of d_model; for more float32 ones parts of x and of a piece of w (128 MB). */
 size_t twell_head_logprob_workspace_size(const twell_head_shape* shape);
 
 /* logp and lse [n_rows] float32, and stats [n_rows][2] float32 (8-byte aligned):
@@ -658,15 +658,14 @@ int twell_head_logprob_forward(const twell_head_shape* shape, const void* x, con
 /* Bytes of device workspace twell_head_logprob_backward needs (0 for an invalid
  * shape and for no rows): the gradient of a piece of the vocabulary's logits, about
  * 200 MB with parts of float32 w (at least 1024 columns), beside float32 sums of dx
- * in up to 32 slices of the vocabulary (128 with up to 64 rows), a copy of x and its
- * parts. */
+ * in up to 32 slices of the vocabulary (128 for few rows), a copy of x and its parts. */
 size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape);
 
 /* The gradients of sum_n dlogp[n] logp[n] from the forward's stats:
  *   dl = scale * dlogp (1[v = target] - exp(z_v) / sum exp z);  dx = dl w,  dw = dl^T x
  * dx [n_rows][d_model] and dw [vocab][d_model] in dtype, written, not added to; sums
  * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w; as two
- * bfloat16 parts with up to 64 rows) or, of float32 ones, with 22 bits and more (dl /
+ * bfloat16 parts with up to 16 rows and vocab * d_model up to 2^25) or, of float32 ones, with 22 bits and more (dl /
  * dlogp and scale * dlogp * x within 2^-40 of their largest; up to 64 rows: 24
  * bits).  n_rows == 0 writes a zero dw. */
 int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, const void* w,
