@@ -240,7 +240,8 @@ def test_refused_shapes():
     lib = twell.load()
     size = lambda *a: lib.twell_norm_backward_workspace_size(ctypes.byref(twell.NormShape(*a)))
     assert size(0, 64, 1, 1.0, 1e-6) == 0 == size(4, 64, 1, 1.0, 0.0) == size(4, 16392, 1, 1.0, 1.0)
-    assert size(4, 64, 1, 1.0, 1e-6) == 2 * 4 * 64 * 4
+    # a workgroup takes four narrow rows, and writes both sums of their columns
+    assert size(4, 64, 1, 1.0, 1e-6) == 2 * 64 * 4 and size(5, 64, 1, 1.0, 1e-6) == 4 * 64 * 4
     assert lib.twell_norm_forward(None, *(P,) * 8, None) == bad
 
 
@@ -276,7 +277,7 @@ def test_refused_pointers():
         assert grad(**{k: P + 4}) == bad, k
     assert grad(w_pre=None, dw_pre=None, dx=None, d_residual_out=None) == bad
     assert grad(w_pre=None, dw_pre=None) == bad
-    assert grad(size=2 * 4 * 64 * 4 - 1) == twell.TWELL_ERR_WORKSPACE
+    assert grad(size=2 * 64 * 4 - 1) == twell.TWELL_ERR_WORKSPACE
     assert grad(n=0, w_post=None) == bad
 
 
