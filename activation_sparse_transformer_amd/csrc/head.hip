@@ -153,32 +153,40 @@ __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
                                                      const float* __restrict__ dlogp,
                                                      float* __restrict__ undo, float* amax,
                                                      uint16_t* __restrict__ out) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
-  if (row >= a.n_rows) return;
-  const float* src = static_cast<const float*>(a.x) + row * a.d;
-  float m = 0.f;
-  for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
-    float v[8];
-    load_run(src + c, v);
+  __shared__ float largest[4];
+  const int wave = threadIdx.x / kWave;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (lane_id() == 0) largest[wave] = 0.f;
+  if (row < a.n_rows) {
+    const float* src = static_cast<const float*>(a.x) + row * a.d;
+    float m = 0.f;
+    for (int c = lane_id() * 8; c < a.d; c += kWave * 8) {
+      float v[8];
+      load_run(src + c, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
-  }
-  m = wave_max(m);
-  const int e = exponent_for(m);
-  const float f = power_of_two(e);
-  if (lane_id() == 0) {
-    undo[row] = power_of_two(-e);
-    if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
-      atomicMax(reinterpret_cast<int*>(amax),
-                __float_as_int(max_finite(0.f, dlogp[row] * a.scale * m)));
-  }
-  for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
-    float v[8] = {};
-    if (c < a.d) load_run(src + c, v);
+      for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
+    }
+    m = wave_max(m);
+    const int e = exponent_for(m);
+    const float f = power_of_two(e);
+    if (lane_id() == 0) {
+      undo[row] = power_of_two(-e);
+      if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
+        largest[wave] = max_finite(0.f, dlogp[row] * a.scale * m);
+    }
+    for (int c = lane_id() * 8; c < ld; c += kWave * 8) {
+      float v[8] = {};
+      if (c < a.d) load_run(src + c, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= f;
-    put_run<kHalves>(out + row * ld, a.n_rows * ld, c, v);
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      put_run<kHalves>(out + row * ld, a.n_rows * ld, c, v);
+    }
   }
+  if (dlogp == nullptr) return;
+  __syncthreads();  // one atomic for the four rows: they are on one address
+  if (threadIdx.x == 0)
+    atomicMax(reinterpret_cast<int*>(amax),
+              __float_as_int(fmaxf(fmaxf(largest[0], largest[1]), fmaxf(largest[2], largest[3]))));
 }
 
 // dw's x, [parts][n_rows][d], a wave a row: rows without a target are zeros (whatever x
