@@ -101,21 +101,24 @@ __device__ __forceinline__ float wave_max(float m) {
 __global__ void head_clear_kernel(float* amax) { amax[threadIdx.x] = 0.f; }
 
 // *amax = max(*amax, the largest finite magnitude of src): an order-free atomic on the
-// bits of non-negative floats.  4 runs a lane, one workgroup after another.
-constexpr int kAmaxRuns = 4 * 256;
+// bits of non-negative floats.  4 runs a lane at a time; at most kAmaxGroups workgroups, as
+// their atomics are on one address.
+constexpr int kAmaxRuns = 4 * 256, kAmaxGroups = 1024;
 __global__ __launch_bounds__(256) void head_amax_kernel(const float* __restrict__ src,
                                                         int64_t runs, float* amax) {
   __shared__ float lds[4];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kAmaxRuns + threadIdx.x;
-  float v[4][8] = {};
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (i0 + u * 256 < runs) load_run(src + (i0 + u * 256) * 8, v[u]);
   float m = 0.f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAmaxRuns + threadIdx.x; i < runs;
+       i += static_cast<int64_t>(gridDim.x) * kAmaxRuns) {
+    float v[4][8] = {};
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u)
+      if (i + u * 256 < runs) load_run(src + (i + u * 256) * 8, v[u]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max_finite(m, v[u][k]);
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max_finite(m, v[u][k]);
+  }
   m = wave_max(m);
   if (lane_id() == 0) lds[threadIdx.x / kWave] = m;
   __syncthreads();
@@ -127,8 +130,8 @@ __global__ __launch_bounds__(256) void head_amax_kernel(const float* __restrict_
   }
 }
 
-// Bound by memory, with the head_amax pass before: 49999 x 1000 56 us for the largest element
-// (3.6 TB/s) and 72 for the parts (5.5 TB/s), of 2145 that the gradient takes.
+// Bound by memory, with the head_amax pass before: 49999 x 1000 45 us for the largest element
+// (4.5 TB/s) and 72 for the parts (5.5 TB/s), of 2170 that the gradient takes.
 // Halves [2][rows][ld] of a piece of w, src [rows][d], scaled by *amax; columns past d
 // are zeros.
 __global__ __launch_bounds__(256) void head_w_kernel(const float* __restrict__ src, int64_t rows,
@@ -933,7 +936,8 @@ Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* und
   const int ld = static_cast<int>(up64(a.d));
   head_clear_kernel<<<1, kAmax, 0, s>>>(amax);
   const int64_t runs = static_cast<int64_t>(a.vocab) * a.d / 8;
-  head_amax_kernel<<<static_cast<uint32_t>(blocks(runs, kAmaxRuns)), 256, 0, s>>>(
+  head_amax_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(runs, kAmaxRuns), kAmaxGroups)),
+                     256, 0, s>>>(
       static_cast<const float*>(a.w), runs, amax);
   head_x_kernel<<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo, amax + 1,
                                                                    xp);
