@@ -66,7 +66,8 @@ def check(m, steps=5, scale=1.0, got=None):
 @BOTH
 @pytest.mark.parametrize("rows,cols", [
     (1, 1), (1, 7), (5, 1), (3, 3), (16, 40), (64, 64), (65, 63), (33, 500), (100, 257), (500, 33),
-    (128, 512), (127, 1024), (129, 300), (1030, 128), (128, 8192), (8200, 60), (64, 40000), (513, 130), (256, 1000), (700, 300), (1025, 511), (40, 5000), (2100, 70)])
+    (128, 512), (127, 1024), (129, 300), (1030, 128), (128, 8192), (8200, 60), (64, 40000),
+    (513, 130), (256, 1000), (700, 300), (1025, 511), (40, 5000), (2100, 70)])
 def test_matches_oracle(rows, cols, dtype):
     say(f"orthogonalize {dtype} {rows}x{cols}")
     m = make(rows + cols, rows, cols, dtype)
