@@ -21,6 +21,7 @@
 // Both products read w, x and dl as they lie, turning fragments with LDS transpose
 // reads where K runs along a column.
 #include <algorithm>
+#include <cfloat>
 #include <numeric>
 #include <type_traits>
 
@@ -149,12 +150,15 @@ __global__ __launch_bounds__(256) void head_w_kernel(const float* __restrict__ s
   put_run<kHalves>(out + row * ld, rows * ld, c, v);
 }
 
-// Halves [2][rows][ld] of x, a wave a row, scaled by the row's largest element, what undoes
-// it in undo[row]; and, for the gradient (dlogp not null), *amax = the largest of
-// |scale dlogp x| over rows with a target.
+// Halves [2][rows][ld] of x, a wave a row, scaled by the row's largest element; in
+// factor[row], positive and finite, what makes z of its products with w's halves: scale and
+// both powers of two undone.  Where that would be under 2^-126 the row's scale is held back
+// (its parts then carry less of z, 2^-133 at most each product); past float32 it ends at the
+// largest one, so that 0 stays 0.  For the gradient (dlogp not null) also amax[1] = the
+// largest of |scale dlogp x| over rows with a target.  amax[0]: w's.
 __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
                                                      const float* __restrict__ dlogp,
-                                                     float* __restrict__ undo, float* amax,
+                                                     float* __restrict__ factor, float* amax,
                                                      uint16_t* __restrict__ out) {
   __shared__ float largest[4];
   const int wave = threadIdx.x / kWave;
@@ -170,10 +174,12 @@ __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
       for (int k = 0; k < 8; ++k) m = max_finite(m, v[k]);
     }
     m = wave_max(m);
-    const int e = exponent_for(m);
+    const int ew = exponent_for(amax[0]);
+    const int e = min(exponent_for(m), 126 + ilogbf(a.scale) - ew);
     const float f = power_of_two(e);
     if (lane_id() == 0) {
-      undo[row] = power_of_two(-e);
+      factor[row] = static_cast<float>(
+          fmin(ldexp(static_cast<double>(a.scale), -(e + ew)), static_cast<double>(FLT_MAX)));
       if (dlogp != nullptr && has_target(a.targets, a.index_bytes, a.vocab, row))
         largest[wave] = max_finite(0.f, dlogp[row] * a.scale * m);
     }
@@ -188,7 +194,7 @@ __global__ __launch_bounds__(256) void head_x_kernel(HeadArgs a, int ld,
   if (dlogp == nullptr) return;
   __syncthreads();  // one atomic for the four rows: they are on one address
   if (threadIdx.x == 0)
-    atomicMax(reinterpret_cast<int*>(amax),
+    atomicMax(reinterpret_cast<int*>(amax + 1),
               __float_as_int(fmaxf(fmaxf(largest[0], largest[1]), fmaxf(largest[2], largest[3]))));
 }
 
@@ -218,12 +224,11 @@ __global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, const float* _
   }
 }
 
-// What a column of accumulators is multiplied by to be z: scale, and the powers of two
-// of both operands undone.
+// What a column of accumulators is multiplied by to be z: positive, so that the -infinity of
+// a row past the vocabulary's end stays one.
 template <Form F, class Args>
 __device__ __forceinline__ float z_factor(const Args& a, int64_t n) {
-  if constexpr (F == kHalves)
-    return a.scale * (n < a.x.rows ? a.undo[n] : 0.f) * power_of_two(-exponent_for(*a.amax));
+  if constexpr (F == kHalves) return n < a.x.rows ? a.factor[n] : 1.f;
   return a.scale;
 }
 
@@ -236,7 +241,7 @@ struct StatsArgs {
   int v0, vocab;     // whole vocabulary
   int ksteps;
   float scale;
-  const float *amax, *undo;  // halves: of w, and per row of x
+  const float* factor;  // halves: per row of x
   const void* targets;
   int index_bytes;
   float2* parts;     // [tiles][n], this piece's first tile onwards
@@ -455,7 +460,7 @@ struct DlArgs {
   int v0, vocab;
   int ksteps;
   float scale;
-  const float *amax, *undo;  // halves: of w, and per row of x
+  const float* factor;  // halves: per row of x
   const void* targets;
   int index_bytes;
   const float2* stats;
@@ -852,7 +857,7 @@ struct ForwardPlan {
   int piece, tiles;
   Tile tile;
   uint16_t *xp, *wp;
-  float *amax, *undo;
+  float *amax, *factor;
   float2* parts;
   float* target_z;
   size_t bytes;
@@ -874,7 +879,7 @@ ForwardPlan forward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.target_z = c.take<float>(a.n_rows);
   if (f == kHalves) {
     p.amax = c.take<float>(kAmax);
-    p.undo = c.take<float>(a.n_rows);
+    p.factor = c.take<float>(a.n_rows);
     p.xp = c.take<uint16_t>(part_bytes / 2 * a.n_rows);
     p.wp = c.take<uint16_t>(part_bytes / 2 * p.piece);
   }
@@ -897,7 +902,7 @@ struct BackwardPlan {
   int piece;
   Cut dx_cut;
   uint16_t *xp, *wp, *gx, *dl;
-  float *amax, *undo, *sums;
+  float *amax, *factor, *sums;
   size_t bytes;
 };
 BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
@@ -917,7 +922,7 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
   p.sums = c.take<float>(p.dx_cut.slices * n * a.d);
   if (f == kHalves) {
     p.amax = c.take<float>(kAmax);
-    p.undo = c.take<float>(n);
+    p.factor = c.take<float>(n);
     p.xp = c.take<uint16_t>(P * ld * n);
     p.wp = c.take<uint16_t>(P * ld * p.piece);
   }
@@ -929,7 +934,7 @@ BackwardPlan backward_plan(const HeadArgs& a, int elem_bytes, void* ws) {
 // The operand x, in place or as parts in xp; halves: amax of w (and of the gradient's x)
 // on the way.
 template <Form F>
-Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* undo, uint16_t* xp,
+Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* factor, uint16_t* xp,
                   hipStream_t s) {
   const int n = static_cast<int>(a.n_rows), units = F == kRaw ? 2 * a.d : a.d;
   if (F != kHalves) return Operand{static_cast<const uint16_t*>(a.x), 0, units, n, units};
@@ -939,7 +944,7 @@ Operand x_operand(const HeadArgs& a, const float* dlogp, float* amax, float* und
   head_amax_kernel<<<static_cast<uint32_t>(std::min<int64_t>(blocks(runs, kAmaxRuns), kAmaxGroups)),
                      256, 0, s>>>(
       static_cast<const float*>(a.w), runs, amax);
-  head_x_kernel<<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, undo, amax + 1,
+  head_x_kernel<<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, ld, dlogp, factor, amax,
                                                                    xp);
   return Operand{xp, a.n_rows * ld, ld, n, ld};
 }
@@ -972,12 +977,12 @@ hipError_t forward(const HeadArgs& a, void* ws, float* logp, float* lse, float* 
                    hipStream_t s) {
   const ForwardPlan p = forward_plan(a, F == kBf16 ? 2 : 4, ws);
   const int n = static_cast<int>(a.n_rows);
-  const Operand x = x_operand<F>(a, nullptr, p.amax, p.undo, p.xp, s);
+  const Operand x = x_operand<F>(a, nullptr, p.amax, p.factor, p.xp, s);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const Operand w = w_operand<F>(a, v0, rows, p.amax, p.wp, s);
-    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, p.amax,
-                      p.undo, a.targets, a.index_bytes,
+    const StatsArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale,
+                      p.factor, a.targets, a.index_bytes,
                       p.parts + v0 / tile_rows(p.tile) * a.n_rows, p.target_z};
     const hipError_t e = with_wide_tile(p.tile, [&](auto cf) {
       typedef decltype(cf) CF;
@@ -1000,14 +1005,14 @@ hipError_t backward(const HeadArgs& a, const float* stats, const float* dlogp, v
   const int n = static_cast<int>(a.n_rows);
   const float* const amax_w = F == kHalves ? p.amax : nullptr;
   const float* const amax_x = F == kHalves ? p.amax + 1 : nullptr;
-  const Operand x = x_operand<F>(a, dlogp, p.amax, p.undo, p.xp, s);
+  const Operand x = x_operand<F>(a, dlogp, p.amax, p.factor, p.xp, s);
   head_gx_kernel<F><<<static_cast<uint32_t>(blocks(n, 4)), 256, 0, s>>>(a, dlogp, amax_x, p.gx);
   const Operand gx{p.gx, a.n_rows * a.d, a.d, a.d, n};
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
     const int rows = static_cast<int>(std::min<int64_t>(p.piece, a.vocab - v0));
     const int ldv = static_cast<int>(up64(rows));
     const Operand w = w_operand<F>(a, v0, rows, amax_w, p.wp, s);
-    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, amax_w, p.undo,
+    const DlArgs k{w, x, static_cast<int>(v0), a.vocab, stages(F, a.d), a.scale, p.factor,
                    a.targets, a.index_bytes, reinterpret_cast<const float2*>(stats), dlogp, p.dl,
                    ldv};
     hipError_t e = with_wide_tile(dl_cut(a, F, rows).tile, [&](auto cf) {
