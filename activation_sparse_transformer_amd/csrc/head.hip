@@ -224,6 +224,18 @@ __global__ __launch_bounds__(256) void head_gx_kernel(HeadArgs a, const float* _
   }
 }
 
+// z of a sum, rounded before anything is taken from it: a multiply-add with -m would leave
+// m's own rounding, |z| 2^-25, in the exponent, and make e^(z - m) infinite for z past 2^32.
+__device__ __forceinline__ float z_of(float sum, float f) {
+#pragma clang fp contract(off)
+  return sum * f;
+}
+// exp(z - m) of a z formed again: at most 1, also where it was summed in another order than
+// the forward pass's.  A row with a NaN is NaN by its sum.
+__device__ __forceinline__ float exp_again(float z, float m) {
+  return __builtin_amdgcn_exp2f(fminf(z - m, 0.f) * kLog2e);
+}
+
 // What a column of accumulators is multiplied by to be z: positive, so that the -infinity of
 // a row past the vocabulary's end stays one.
 template <Form F, class Args>
@@ -234,8 +246,8 @@ __device__ __forceinline__ float z_factor(const Args& a, int64_t n) {
 
 // ---------------------------------------------------------------- forward
 // Many rows: bound by MFMA and the clocks under it.  4096 x 2048 x 32768 bf16 takes 475 us in
-// all, 1.16 PFLOP/s (a plain library product of 8192^3 reaches 1.17); the statistics are two
-// fused multiply-adds, an exp2 and an add per z, behind the products.
+// all, 1.16 PFLOP/s (a plain library product of 8192^3 reaches 1.17); the statistics are a
+// subtraction, a multiply, an exp2 and an add per z, behind the products.
 struct StatsArgs {
   Operand w, x;      // w: a piece of the vocabulary, from column v0
   int v0, vocab;     // whole vocabulary
@@ -275,15 +287,16 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
         if (!full && row0 + nt::row_of(i, r) >= a.w.rows) acc[i][j][r] = -INFINITY;
         m = fmaxf(m, acc[i][j][r]);
       }
-    m = fmaxf(m, other_half(m)) * f;
-    const float base = m == -INFINITY ? 0.f : m;
+    m = fmaxf(m, other_half(m));
+    // z - max z from the sums' difference: 0 at the largest, never above
+    const float base = m == -INFINITY ? 0.f : m, f2 = fminf(f * kLog2e, FLT_MAX);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -base) * kLog2e);
+      for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * f2);
     s += other_half(s);
+    m = z_of(m, f);
     if (half == 0) joint[wm * CF::BN + col] = make_float2(m, s);
     // the target's z, where this wave's rows hold it
     int64_t t = -1;
@@ -301,7 +314,7 @@ __global__ __launch_bounds__(CF::NT) void head_stats_kernel(StatsArgs a, int m_b
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (rel == nt::row_of(i, r)) z = acc[i][j][r];
-      if (mine) a.target_z[n] = z * f;
+      if (mine) a.target_z[n] = z_of(z, f);
     }
   }
   __syncthreads();
@@ -387,7 +400,8 @@ __device__ __forceinline__ float4 few_z(const FewZ& z, int64_t n_rows, int64_t n
     const float4 q = *reinterpret_cast<const float4*>(z.sums + (s * n_rows + n) * z.pitch + v);
     t = make_float4(t.x + q.x, t.y + q.y, t.z + q.z, t.w + q.w);
   }
-  return make_float4(t.x * z.scale, t.y * z.scale, t.z * z.scale, t.w * z.scale);
+  return make_float4(z_of(t.x, z.scale), z_of(t.y, z.scale), z_of(t.z, z.scale),
+                     z_of(t.w, z.scale));
 }
 
 // {m, s} of kFewChunk columns of a row a workgroup: to parts, or, where one holds the whole
@@ -503,7 +517,7 @@ __global__ __launch_bounds__(CF::NT) void head_dl_kernel(DlArgs a, int m_blocks,
     for (int i = 0; i < CF::FM; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -m) * kLog2e);
+        const float e = exp_again(z_of(acc[i][j][r], f), m);
         acc[i][j][r] = given && (full || row0 + nt::row_of(i, r) < a.w.rows) ? share * e : 0.f;
       }
     const bool mine = t >= 0 && t < CF::WTM && wave_row + t < a.w.rows && ((t >> 2) & 1) == half;
@@ -630,7 +644,7 @@ __global__ __launch_bounds__(256) void head_few_dl_kernel(HeadArgs a, FewZ z,
         const float zs[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          d[k] = share * __builtin_amdgcn_exp2f((zs[k] - st.x) * kLog2e);
+          d[k] = share * exp_again(zs[k], st.x);
           if (v + k == t - z.v0) d[k] += g;
           if (v + k >= z.rows) d[k] = 0.f;
         }
