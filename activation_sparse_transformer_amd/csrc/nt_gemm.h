@@ -756,10 +756,11 @@ __device__ __forceinline__ void split(float v, uint16_t (&part)[parts_of(F)]) {
 }
 
 // The exponent e by which a matrix or row of largest magnitude m is scaled: 2^14 <= m
-// 2^e < 2^15 (at most 100, so that 2^-e is a float32; m = 0 and non-finite m: 0).
+// 2^e < 2^15 (at most 126, so that 2^e and 2^-e are normal numbers; m = 0 and non-finite
+// m: 0).
 __device__ __forceinline__ int exponent_for(float m) {
   const int b = static_cast<int>(__float_as_uint(m) >> 23) & 0xff;
-  return b == 0xff || m == 0.f ? 0 : min(14 + 127 - max(b, 1), 100);
+  return b == 0xff || m == 0.f ? 0 : min(14 + 127 - max(b, 1), 126);
 }
 __device__ __forceinline__ float power_of_two(int e) { return ldexpf(1.f, e); }
 
