@@ -600,9 +600,10 @@ __global__ __launch_bounds__(256) void head_dx_kernel(HeadArgs a, const float* _
   const bool given = has_target(a.targets, a.index_bytes, a.vocab, n);
   if (!given) v = make_float4(0, 0, 0, 0);
   if constexpr (F == kHalves) {
-    const float f = power_of_two(-kDlExponent - exponent_for(*amax));
-    const float g = given ? dlogp[n] * a.scale : 0.f;
-    v = make_float4(v.x * f * g, v.y * f * g, v.z * f * g, v.w * f * g);
+    // in double: neither factor alone need leave v in float32's range
+    const double f = given ? ldexp(static_cast<double>(dlogp[n]) * a.scale,
+                                   -kDlExponent - exponent_for(*amax)) : 0.0;
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
   }
   if constexpr (sizeof(E) == 2)
     *reinterpret_cast<uint2*>(dx + i) = make_uint2(pack_part<kBf16>(v.x, v.y, 0),

@@ -60,3 +60,19 @@ def test_small_operands(n, v, d, w_by, x_by, g_by):
     m["w"] *= 2.0 ** w_by
     m["dlogp"] *= 2.0 ** g_by
     check(m)
+
+
+@pytest.mark.parametrize("n,v,d", [(70, 300, 64), (300, 700, 136)])
+@pytest.mark.parametrize("g_by", [-20, -100, 0])
+def test_weights_up_to_the_largest_number(n, v, d, g_by):
+    """Weights of +-1.5 2^127: dl / g times them passes float32's range where dx does not."""
+    say(f"head largest weights n={n} v={v} d={d} dlogp 2^{g_by}")
+    m = make(n, n, v, d, torch.float32)
+    sign = torch.full((v, 1), -1.0)
+    m["t"] = torch.arange(n) % 50
+    sign[:50] = 1
+    m["w"] = sign * (1.25 + 0.25 * torch.rand((v, d), generator=torch.Generator().manual_seed(1)))
+    m["w"] *= 2.0 ** 127
+    m["x"] = (m["x"] / d ** 0.5).double().mul(2.0 ** -127).float()
+    m["dlogp"] *= 2.0 ** g_by
+    check(m)
