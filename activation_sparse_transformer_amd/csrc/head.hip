@@ -14,7 +14,9 @@
 // is of the size of dx's and dw's own (with few rows, where it costs next to nothing,
 // as two parts).  With float32 ones every operand is two half-precision parts
 // (nt_gemm.h), w scaled by its largest element, x by each row's; dl / g lies in [-1, 1]
-// and is scaled by 2^14, with g taken into dx at the end and into the x of dw.  With few
+// and is scaled by 2^15, with g taken into dx at the end and into the x of dw: a dl / g is
+// within 2^-40, so that a token of p < 2^-18 has fewer than 22 bits of its row of dw, and one
+// of p < 2^-41 in every row none.  With few
 // rows, where reading w is what the call costs, float32 operands and dl stay float32, and
 // z is formed with K cut in slices where the vocabulary alone gives too few workgroups to
 // keep the memory busy, so it goes through the workspace (n_rows of a piece of it).
@@ -43,7 +45,7 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int index_byte
 // v of the lane with the other half's rows of the same column
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
-constexpr int kDlExponent = 14;  // of dl / g in halves
+constexpr int kDlExponent = 15;  // of dl / g in halves
 
 __device__ __forceinline__ bool has_target(const void* targets, int index_bytes, int vocab,
                                            int64_t n) {
@@ -458,7 +460,7 @@ __device__ __forceinline__ uint32_t pack_part(float a, float b, int p) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
   } else {
     _Float16 x = static_cast<_Float16>(a), y = static_cast<_Float16>(b);
-    if (p == 1) {  // what the first part leaves; |a| is at most 2^14, or NaN
+    if (p == 1) {  // what the first part leaves; |a| is at most 2^15, or NaN
       x = static_cast<_Float16>(a == a ? a - static_cast<float>(x) : 0.f);
       y = static_cast<_Float16>(b == b ? b - static_cast<float>(y) : 0.f);
     }

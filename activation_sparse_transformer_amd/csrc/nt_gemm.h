@@ -4,7 +4,7 @@
 //  - kHalves:  two half-precision parts hi + lo of a float32 value times a power of
 //              two that brings the matrix (or row) below 2^15.  Both round to 11 bits,
 //              so |lo| <= 2^-11 |v| and hi + lo is within 2^-23 of v (2^-24 in the
-//              mean), or within 2^-25 (2^-40 of the largest) where lo is subnormal;
+//              mean), or within 2^-25 (2^-39 of the largest) where lo is subnormal;
 //              MFMA keeps subnormal inputs.  Of the four products lo lo, 2^-24 of the
 //              whole in the mean and at most 2^-22, is left out: three products, where
 //              three bfloat16 parts would take six for the same 24 bits and MFMA's own

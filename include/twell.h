@@ -622,9 +622,10 @@ int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
  *    aligned to their elements only.
  *  - z is a float32 sum; maxima, sums and probabilities are float32.  The gradient
  *    forms z again.  float32 x and w enter the products with 24 bits for up to 64
- *    rows; for more with 22 bits and more, elements under 2^-18 of the largest of their
- *    row of x, or of w, with an error of 2^-40 of that largest instead; z is then also off
- *    by d_model 2^-133 at most, which only z under 2^-110 or so notice.
+ *    rows; for more with 22 bits and more, elements under 2^-17 of the largest of their
+ *    row of x, or of w, with an error of 2^-39 of that largest instead (of 2^-151 where
+ *    it is under 2^-112); z is then also off by d_model 2^-133 at most, which only z
+ *    under 2^-110 or so notice.
  *  - A row with a NaN, or an infinity that meets its product, has NaN results; a
  *    float32 infinity in x or w makes every z of its row or column infinite or NaN.
  *    z = -inf has probability 0; a row with nothing else has lse = logp = -inf and a
@@ -665,10 +666,12 @@ size_t twell_head_logprob_backward_workspace_size(const twell_head_shape* shape)
 /* The gradients of sum_n dlogp[n] logp[n] from the forward's stats:
  *   dl = scale * dlogp (1[v = target] - exp(z_v) / sum exp z);  dx = dl w,  dw = dl^T x
  * dx [n_rows][d_model] and dw [vocab][d_model] in dtype, written, not added to; sums
- * run in a fixed order.  dl enters the products in bfloat16 (bfloat16 x and w; as two
- * bfloat16 parts with up to 16 rows and vocab * d_model up to 2^25) or, of float32 ones, with 22 bits and more (dl /
- * dlogp and scale * dlogp * x within 2^-40 of their largest; up to 64 rows: 24
- * bits).  n_rows == 0 writes a zero dw. */
+ * run in a fixed order.  With bfloat16 x and w, dl enters the products in bfloat16, as
+ * two bfloat16 parts with up to 16 rows and vocab * d_model up to 2^25.  With float32 ones
+ * it has 24 bits for up to 64 rows; for more 22 bits and more, dl / (scale dlogp) within
+ * 2^-40 and scale * dlogp * x within 2^-39 of its largest: the row of dw of a token whose
+ * probability is under 2^-18 in every row then carries fewer bits, down to none under
+ * 2^-41.  n_rows == 0 writes a zero dw. */
 int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, const void* w,
                                 const void* targets, const float* stats, const float* dlogp,
                                 void* dx, void* dw, void* workspace, size_t workspace_bytes,
@@ -682,7 +685,7 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
  * which replaces every singular value s of X by a polynomial's iterate: towards 1
  * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
  *  - Sums are float32; X, G and B enter the products with 22 bits and more, elements
- *    far below the matrix's bound with an error of 2^-40 of it.  With the smaller side
+ *    far below the matrix's bound with an error of 2^-38 of it.  With the smaller side
  *    past 128, a bfloat16 M's X enters X X^T and B X with 11 bits, an eighth of M's own
  *    rounding.  |M|_F is summed in double.
  *  - M = 0 gives 0; an infinity or NaN in M gives NaN.  Coefficients under which X, G or B
