@@ -393,8 +393,12 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs a, const float*
     if (is_pre) {
       dw_pre[c + k] = v[k];
     } else {
-      if (dw_post != nullptr) dw_post[c + k] = a.gate != nullptr ? v[k] * a.gate[c + k] : v[k];
-      if (dgate != nullptr) dgate[c + k] = a.w_post != nullptr ? v[k] * a.w_post[c + k] : v[k];
+      // without rows zero, also beside a weight that is infinite or NaN
+      const bool some = groups > 0;
+      if (dw_post != nullptr)
+        dw_post[c + k] = some && a.gate != nullptr ? v[k] * a.gate[c + k] : v[k];
+      if (dgate != nullptr)
+        dgate[c + k] = some && a.w_post != nullptr ? v[k] * a.w_post[c + k] : v[k];
     }
   }
 }
