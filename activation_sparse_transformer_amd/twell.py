@@ -1057,7 +1057,8 @@ def twell_norm_forward(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
         x = norm(residual') * w_pre,   norm(v) = v / sqrt(mean(v^2) + eps)
 
     Without w_post, y is not normalised; without y there is only x; without w_pre, no x.
-    Weights are [d_model] float32.  `out` may hold residual and y themselves."""
+    Weights are [d_model] float32.  `out` may hold residual and y themselves; what a call does not
+    write of it is left alone and not handed back."""
     dev, dt = residual.device, residual.dtype
     n, d = residual.shape
     _need(residual, "residual", dev)
@@ -1079,6 +1080,8 @@ def twell_norm_forward(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
         ctypes.byref(shape), _ptr(residual), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre),
         _ptr(out.residual) if y is not None else None, _ptr(out.x) if w_pre is not None else None,
         _here(dev)), "twell_norm_forward")
+    if y is None or w_pre is None:  # what this call did not write is no result of it
+        return NormOut(residual if y is None else out.residual, None if w_pre is None else out.x)
     return out
 
 
@@ -1133,6 +1136,10 @@ def twell_norm_backward(residual_out: torch.Tensor, y: Optional[torch.Tensor],
         _ptr(d_residual_out), _ptr(dx), _ptr(out.d_residual), given(y, out.dy),
         given(w_post, out.dw_post), given(gate, out.dgate), given(w_pre, out.dw_pre),
         _ptr(workspace), workspace.numel(), _here(dev)), "twell_norm_backward")
+    if y is None or w_post is None or gate is None or w_pre is None:
+        only = lambda w, g: None if w is None else g
+        return NormGrads(out.d_residual, only(y, out.dy), only(w_post, out.dw_post),
+                         only(gate, out.dgate), only(w_pre, out.dw_pre))
     return out
 
 
