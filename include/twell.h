@@ -685,11 +685,12 @@ int twell_head_logprob_backward(const twell_head_shape* shape, const void* x, co
  * which replaces every singular value s of X by a polynomial's iterate: towards 1
  * with a = 3.4445, b = -4.775, c = 2.0315 and 5 steps.
  *  - Sums are float32; X, G and B enter the products with 22 bits and more, elements
- *    far below the matrix's bound with an error of 2^-38 of it.  With the smaller side
+ *    far below the bound of the matrix (1 for the first X, so all of M where |M|_F is far
+ *    below eps) with an error of 2^-38 of it.  With the smaller side
  *    past 128, a bfloat16 M's X enters X X^T and B X with 11 bits, an eighth of M's own
  *    rounding.  |M|_F is summed in double.
  *  - M = 0 gives 0; an infinity or NaN in M gives NaN.  Coefficients under which X, G or B
- *    may pass 2^100 may give infinities and NaN.
+ *    may pass 2^100 may give infinities and NaN; results under 2^-119 may be 0.
  * Requirements: rows, cols > 0; dtype a twell_dtype (of m and out); 1 <= steps <=
  * TWELL_ORTH_MAX_STEPS; a, b, c and scale finite; eps positive and finite.  Limits,
  * else TWELL_ERR_UNSUPPORTED: rows and cols at most 2^20, the smaller at most 2^16,
