@@ -10,9 +10,10 @@
 // stays a part of them.  Per piece, with p = exp(z - m) / s and g = scale * dlogp:
 //   dl[n][v] = g[n] (1[v = target] - p)     from z formed again
 //   dx += dl w,   dw = dl^T x
-// With bfloat16 x and w, dl is held in bfloat16: its rounding, 2^-9 of each element,
-// is of the size of dx's and dw's own (with few rows, where it costs next to nothing,
-// as two parts).  With float32 ones every operand is two half-precision parts
+// With bfloat16 x and w, dl is held in bfloat16: its rounding, at most 2^-8 of each element,
+// is of the size of dx's and dw's own (4096 x 2048 x 32768: 0.0022 from float64 with random
+// dlogp, the results' rounding alone 0.0017; two parts would double the products of dx and dw).
+// With few rows, where it costs next to nothing, it is two parts (few_rows).  With float32 ones every operand is two half-precision parts
 // (nt_gemm.h), w scaled by its largest element, x by each row's; dl / g lies in [-1, 1]
 // and is scaled by 2^15, with g taken into dx at the end and into the x of dw: a dl / g is
 // within 2^-40, so that a token of p < 2^-18 has fewer than 22 bits of its row of dw, and one
@@ -471,6 +472,7 @@ __device__ __forceinline__ uint32_t pack_part(float a, float b, int p) {
 
 // Many rows: z formed again and dl in its place: 4096 x 2048 x 16384 bf16 285 us, 0.96
 // PFLOP/s (the statistics pass 250): the epilogue's exponentials, and dl's 134 MB through LDS.
+// In halves the epilogue of 256 x 256 tiles spills 22 registers (92 bytes a lane).
 struct DlArgs {
   Operand w, x;
   int v0, vocab;

@@ -209,7 +209,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_forward_kernel(NormArg
 // A group walks rows group, group + groups, ... and keeps its columns' sums in
 // registers; a workgroup b's sums[b][d] (S) and sums[gridDim.x + b][d] (dw_pre) are added
 // up by norm_sums_kernel.  8192 x 4096 float32 157 us, 5.1 TB/s; 4096 x 2048 bf16 27 us,
-// 3.7 TB/s: with eight rows a workgroup the latency of a row's loads and sums shows.
+// 3.7 TB/s: with eight rows a workgroup the latency of a row's loads and sums shows.  Past
+// 8192 columns two runs a lane spill (bf16 13 registers, 56 bytes a lane; float32 112, 260
+// bytes): 1024 x 16384 bf16 79 us, float32 205, 2.6 and 2.0 TB/s.
 template <typename E, int G, int V>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(NormArgs a,
                                                                           NormGradPtrs<E> p,
