@@ -540,7 +540,8 @@ __device__ __forceinline__ void mainloop_pipe(const Operand& A, int m0, const Op
   __syncthreads();  // the stages are free for the epilogue
 }
 
-// Three bfloat16 parts of 8 floats.
+// Three bfloat16 parts of 8 floats.  The first ends at the largest bfloat16, as a larger
+// float32 would round to an infinity there.
 __device__ __forceinline__ void split3(const float (&v)[8], i32x4_t (&part)[3]) {
   typedef __attribute__((ext_vector_type(2))) float f32x2_t;
   typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
@@ -549,8 +550,11 @@ __device__ __forceinline__ void split3(const float (&v)[8], i32x4_t (&part)[3]) 
     float a = v[2 * k], b = v[2 * k + 1];
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-      const uint32_t w =
-          __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+      constexpr float kMost = 0x1.fep127f;
+      const f32x2_t in = p > 0 ? f32x2_t{a, b}
+                               : f32x2_t{__builtin_amdgcn_fmed3f(a, -kMost, kMost),
+                                         __builtin_amdgcn_fmed3f(b, -kMost, kMost)};
+      const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(in, bf16x2_t));
       part[p][k] = static_cast<int>(w);
       a -= __uint_as_float(w << 16);
       b -= __uint_as_float(w & 0xffff0000u);

@@ -622,10 +622,11 @@ int twell_norm_backward(const twell_norm_shape* shape, const void* residual_out,
  *    aligned to their elements only.
  *  - z is a float32 sum; maxima, sums and probabilities are float32.  The gradient
  *    forms z again.  float32 x and w enter the products with 24 bits for up to 64
- *    rows; for more with 22 bits and more, elements under 2^-17 of the largest of their
- *    row of x, or of w, with an error of 2^-39 of that largest instead (of 2^-151 where
- *    it is under 2^-112); z is then also off by d_model 2^-133 at most, which only z
- *    under 2^-110 or so notice.
+ *    rows (elements under 2^-108 with an error of 2^-133); for more with 22 bits and
+ *    more, elements under 2^-17 of the largest of their row of x, or of w, with an error of
+ *    2^-39 of that largest instead (of 2^-151 where it is under 2^-112): a w that masks
+ *    tokens by float32's lowest value leaves nothing of the other tokens there.  z is then
+ *    also off by d_model 2^-133 at most, which only z under 2^-110 or so notice.
  *  - A row with a NaN, or an infinity that meets its product, has NaN results; a
  *    float32 infinity in x or w makes every z of its row or column infinite or NaN.
  *    z = -inf has probability 0; a row with nothing else has lse = logp = -inf and a
