@@ -572,8 +572,8 @@ int twell_logprob_backward(const twell_logprob_shape* shape, const void* logits,
  *    gate are NULL, w_pre is given and residual_scale is 1.  Without w_pre
  *    (behind the last block) x is NULL.
  *  - All arithmetic is float32, and r' and x are rounded once each (x is formed
- *    from r' before its rounding).  Rows whose squares pass float32's range
- *    (elements of about 1e19) are not normalised.
+ *    from r' before its rounding).  Rows whose sum of squares passes
+ *    float32's range (elements of 1.8e19 / sqrt(d_model)) are not normalised.
  * Requirements: 0 <= n_rows < 2^31; d_model > 0 and a multiple of 8, at most
  * 16384 (else TWELL_ERR_UNSUPPORTED); dtype a twell_dtype; residual_scale
  * finite; eps positive and finite. */
